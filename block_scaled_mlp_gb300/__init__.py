@@ -27,6 +27,7 @@ __all__ = [
     "mlp_workspace_size", "mlp_ctx_layout", "mlp_fwd", "mlp_bwd", "mlp_fwd_static_scratch", "MlpContext", "ErrorWord",
     "token_group_pad", "token_group_capacity", "gather_rows", "linear_fwd", "linear_bwd", "LinearContext",
     "KERNEL_FAMILIES", "launch_counts", "fp8_amax", "fp8_quantize", "fp8_grouped_mm",
+    "Ckpt8", "ckpt8_save", "ckpt8_load", "swiglu_ckpt8_fwd", "swiglu_ckpt8_bwd", "add_rmsnorm_fwd", "add_rmsnorm_bwd",
 ]
 
 ROW, COL, BOTH = 1, 2, 3
@@ -40,6 +41,7 @@ library_path = os.path.join(_HERE, "libmxmlp.so")
 _lib = None
 
 _V, _I64, _I32, _I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int
+_F = ctypes.c_float
 _SIGS = {
     "mx_version": ([], _I),
     "mx_status_string": ([_I], ctypes.c_char_p),
@@ -73,6 +75,13 @@ _SIGS = {
     "mx_launch_counts": ([ctypes.POINTER(ctypes.c_int64), _I], _I),
     "mx_fp8_amax": ([_V, _I64, _I64, _V, _V], _I),
     "mx_fp8_quantize": ([_V, _I64, _I64, _I64, _V, _I, _V, _V, _V], _I),
+    "mx_add_rmsnorm_fwd": ([_V, _V, _V, _I64, _I64, _F, _V, _V, _V, _I, _I, _I, _V, _V, _V, _V, _V, _V, _V], _I),
+    "mx_add_rmsnorm_bwd_workspace": ([_I64, _I64], ctypes.c_size_t),
+    "mx_add_rmsnorm_bwd": ([_V, _V, _V, _V, _V, _V, _V, _I64, _I64, _V, _V, _V, _V], _I),
+    "mx_ckpt8_save": ([_V, _I64, _I64, _V, _V, _V], _I),
+    "mx_ckpt8_load": ([_V, _V, _I64, _I64, _V, _V], _I),
+    "mx_swiglu_ckpt8_fwd": ([_V, _I64, _I64, _V, _V, _V, _V], _I),
+    "mx_swiglu_ckpt8_bwd": ([_V, _V, _V, _I64, _I64, _V, _V, _V], _I),
     "mx_fp8_grouped_mm": ([_I, _V, _V, _V, _V, _I64, _I64, _I64, _V, _I32, _I32, _V, _V, _V], _I),
 }
 
@@ -123,7 +132,8 @@ def _need(t, dtype, name):
         raise MxError(1, f"{name} must be contiguous")
 
 
-KERNEL_FAMILIES = ("quant", "swiglu_fwd", "swiglu_bwd", "gemm", "gemm_swiglu", "dispatch", "memset")
+KERNEL_FAMILIES = ("quant", "swiglu_fwd", "swiglu_bwd", "gemm", "gemm_swiglu", "dispatch", "memset", "norm",
+                   "ckpt8")
 
 
 def silu_table():
@@ -513,4 +523,148 @@ def linear_bwd(ctx: LinearContext, dout, err: ErrorWord | None = None):
     dw = torch.empty((N, K), dtype=torch.bfloat16, device=dout.device)
     _check(lib().mx_linear_bwd(_ptr(ctx.buf), _ptr(dout), _ptr(w), M, K, N, recipe, _ptr(scratch), _ptr(dx),
                                _ptr(dw), err.ptr() if err else None, _stream()))
+    return dx, dw
+
+
+# ---------------------------------------------------------------- 8-bit activation checkpoints
+
+
+class Ckpt8:
+    """A bf16 matrix kept in 8 bits: codes int8 [rows, cols], scales uint8
+    [rows, cols/32] (one power of two for 32 elements of a row)."""
+
+    def __init__(self, codes, scales):
+        self.codes = codes
+        self.scales = scales
+
+    @classmethod
+    def empty(cls, rows, cols, device):
+        return cls(torch.empty((rows, cols), dtype=torch.int8, device=device),
+                   torch.empty((rows, cols // 32), dtype=torch.uint8, device=device))
+
+    @property
+    def shape(self):
+        return self.codes.shape
+
+    def nbytes(self) -> int:
+        return self.codes.numel() + self.scales.numel()
+
+
+def _need_ckpt(ck, shape, name):
+    if not isinstance(ck, Ckpt8):
+        raise MxError(1, f"{name} must be a Ckpt8")
+    _need(ck.codes, torch.int8, f"{name}.codes")
+    _need(ck.scales, torch.uint8, f"{name}.scales")
+    if tuple(ck.codes.shape) != tuple(shape) or ck.scales.shape != (shape[0], shape[1] // 32):
+        raise MxError(1, f"{name} must be a checkpoint of a {list(shape)} matrix, got {list(ck.codes.shape)}")
+
+
+def _need2d(t, name, shape=None):
+    _need(t, torch.bfloat16, name)
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise MxError(1, f"{name} must be a {'2-d' if shape is None else list(shape)} matrix, got {list(t.shape)}")
+
+
+def ckpt8_save(x):
+    """8-bit checkpoint of a bf16 [rows, cols] matrix (cols % 32 == 0)."""
+    _need2d(x, "x")
+    ck = Ckpt8.empty(x.shape[0], x.shape[1], x.device)
+    _check(lib().mx_ckpt8_save(_ptr(x), x.shape[0], x.shape[1], _ptr(ck.codes), _ptr(ck.scales), _stream()))
+    return ck
+
+
+def ckpt8_load(ck: Ckpt8):
+    """The bf16 matrix that a checkpoint holds."""
+    _need_ckpt(ck, ck.shape if isinstance(ck, Ckpt8) else (0, 0), "ck")
+    x = torch.empty(ck.codes.shape, dtype=torch.bfloat16, device=ck.codes.device)
+    _check(lib().mx_ckpt8_load(_ptr(ck.codes), _ptr(ck.scales), x.shape[0], x.shape[1], _ptr(x), _stream()))
+    return x
+
+
+def swiglu_ckpt8_fwd(h13):
+    """y = silu(g) u [M, h] in bf16 and the 8-bit checkpoint of h13 [M, 2h] = [g | u]."""
+    _need2d(h13, "h13")
+    M, h = h13.shape[0], h13.shape[1] // 2
+    if h13.shape[1] % 64:
+        raise MxError(4, f"h13 must have 2h columns with h a multiple of 32, got {h13.shape[1]}")
+    y = torch.empty((M, h), dtype=torch.bfloat16, device=h13.device)
+    ck = Ckpt8.empty(M, 2 * h, h13.device)
+    _check(lib().mx_swiglu_ckpt8_fwd(_ptr(h13), M, h, _ptr(y), _ptr(ck.codes), _ptr(ck.scales), _stream()))
+    return y, ck
+
+
+def swiglu_ckpt8_bwd(dy, ck: Ckpt8, y=True):
+    """(dh13 [M, 2h], y [M, h]) from dy [M, h] and the checkpoint of h13; y is
+    computed again from the checkpoint (None with y=False)."""
+    _need2d(dy, "dy")
+    M, h = dy.shape
+    _need_ckpt(ck, (M, 2 * h), "ck")
+    dh13 = torch.empty((M, 2 * h), dtype=torch.bfloat16, device=dy.device)
+    out = torch.empty((M, h), dtype=torch.bfloat16, device=dy.device) if y else None
+    _check(lib().mx_swiglu_ckpt8_bwd(_ptr(dy), _ptr(ck.codes), _ptr(ck.scales), M, h, _ptr(dh13), _ptr(out), _stream()))
+    return dh13, out
+
+
+# ---------------------------------------------------------------- residual + RMS norm
+
+
+def add_rmsnorm_fwd(x, w, residual=None, eps=1e-5, y=True, axis=0, layout=SCALE_MMA, scale_mode=SCALE_RCEIL,
+                    ckpt=False):
+    """r = x + residual, y = r rstd w, rstd = (mean(r^2) + eps)^-1/2 over each
+    row of x [M, d].  Returns a dict: r [M, d] bf16 (x itself without a
+    residual), rstd [M] fp32, y [M, d] bf16 (y=True), the MXFP8 codes and
+    scales of y as quantize() names them (axis), ckpt: a Ckpt8 of r
+    (ckpt=True); what was not asked for is None."""
+    _need2d(x, "x")
+    M, d = x.shape
+    _need(w, torch.bfloat16, "w")
+    if w.shape != (d,):
+        raise MxError(1, f"w must be [{d}], got {list(w.shape)}")
+    if residual is not None:
+        _need2d(residual, "residual", (M, d))
+    dev = x.device
+    out = dict(r=x, rstd=torch.empty(M, dtype=torch.float32, device=dev), y=None, q_row=None, s_row=None, q_col=None,
+               s_col=None, ckpt=None)
+    if residual is not None:
+        out["r"] = torch.empty_like(x)
+    if y:
+        out["y"] = torch.empty_like(x)
+    if axis & ROW:
+        out["q_row"] = torch.empty((M, d), dtype=torch.uint8, device=dev)
+        out["s_row"] = _scales(M, d, layout, dev)
+    if axis & COL:
+        out["q_col"] = torch.empty((d, M), dtype=torch.uint8, device=dev)
+        out["s_col"] = _scales(d, M, layout, dev)
+    ck = out["ckpt"] = Ckpt8.empty(M, d, dev) if ckpt else None
+    _check(lib().mx_add_rmsnorm_fwd(_ptr(x), _ptr(residual), _ptr(w), M, d, eps,
+                                    None if residual is None else _ptr(out["r"]), _ptr(out["rstd"]), _ptr(out["y"]), axis,
+                                    layout, scale_mode, _ptr(out["q_row"]), _ptr(out["s_row"]), _ptr(out["q_col"]),
+                                    _ptr(out["s_col"]), _ptr(ck.codes) if ckpt else None,
+                                    _ptr(ck.scales) if ckpt else None, _stream()))
+    return out
+
+
+def add_rmsnorm_bwd(dy, saved, rstd, w, dres=None):
+    """(dx [M, d], dw [d]) of add_rmsnorm_fwd from dy [M, d], the saved r (bf16,
+    or its Ckpt8), rstd and w; dres [M, d] is the gradient that reaches r on
+    the residual path.  dx is the gradient of x and of the residual."""
+    _need2d(dy, "dy")
+    M, d = dy.shape
+    ck = saved if isinstance(saved, Ckpt8) else None
+    if ck is not None:
+        _need_ckpt(ck, (M, d), "saved")
+    else:
+        _need2d(saved, "saved", (M, d))
+    _need(w, torch.bfloat16, "w")
+    _need(rstd, torch.float32, "rstd")
+    if w.shape != (d,) or rstd.shape != (M,):
+        raise MxError(1, f"w must be [{d}] and rstd [{M}], got {list(w.shape)} and {list(rstd.shape)}")
+    if dres is not None:
+        _need2d(dres, "dres", (M, d))
+    dx = torch.empty_like(dy)
+    dw = torch.empty(d, dtype=torch.bfloat16, device=dy.device)
+    ws = torch.empty(max(lib().mx_add_rmsnorm_bwd_workspace(M, d), 16), dtype=torch.uint8, device=dy.device)
+    _check(lib().mx_add_rmsnorm_bwd(_ptr(dy), None if ck else _ptr(saved), _ptr(ck.codes) if ck else None,
+                                    _ptr(ck.scales) if ck else None, _ptr(rstd), _ptr(w), _ptr(dres), M, d, _ptr(dx),
+                                    _ptr(dw), _ptr(ws), _stream()))
     return dx, dw

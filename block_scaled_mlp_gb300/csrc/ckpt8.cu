@@ -1,0 +1,179 @@
+// ckpt8.cu - 8-bit activation checkpoints (format: ckpt8.cuh) by themselves,
+// and SwiGLU with [g | u] kept as one: the forward pass writes y and the
+// checkpoint from one read of h13, the backward pass reads the checkpoint.
+//
+//   y  = g s u,  s = 1 / (1 + e^-g)                 from the unrounded h13
+//   dg = dy u s (1 + g (1 - s)),  du = dy g s,  y' = g s u
+//                                                   from the checkpoint's g, u
+// in fp32, each result rounded once to bf16.
+//
+// All four kernels are bound by HBM (8.06, 10.06 and 3.03 bytes an element
+// against about 30 instructions), so the layout is the plainest that keeps
+// every access full: a lane holds eight consecutive elements (16 bytes of
+// bf16, 8 bytes of codes), four lanes one block, and no shared memory.
+#include "ckpt8.cuh"
+#include "kernels.h"
+
+namespace mx {
+
+namespace {
+
+constexpr int C8_THREADS = 256;
+
+// s = 1 / (1 + e^-g) by the approximate exponential and reciprocal (a few
+// units of 2^-23: far below the bf16 rounding of every result).  e^-g
+// overflows to infinity below g = -88.7 and s is 0 there.
+MX_DEVINL float sigmoid_approx(float g) { return __frcp_rn(1.0f + __expf(-g)); }
+
+__global__ void __launch_bounds__(C8_THREADS)
+    ckpt8_save_kernel(const uint4* __restrict__ x, int64_t n8, uint2* __restrict__ codes, uint8_t* __restrict__ scales) {
+  const int64_t i = (int64_t)blockIdx.x * C8_THREADS + threadIdx.x;
+  const bool in = i < n8;   // whole blocks: four lanes together
+  float v[8];
+  unpack8(in ? ld_once(x + i) : make_uint4(0, 0, 0, 0), v);
+  const uint32_t s = ckpt8_scale(block_amax(v));
+  if (!in) return;
+  codes[i] = ckpt8_encode(v, s);
+  if ((threadIdx.x & 3) == 0) scales[i >> 2] = (uint8_t)s;
+}
+
+__global__ void __launch_bounds__(C8_THREADS)
+    ckpt8_load_kernel(const uint2* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t n8,
+                      uint4* __restrict__ x) {
+  const int64_t i = (int64_t)blockIdx.x * C8_THREADS + threadIdx.x;
+  if (i >= n8) return;
+  float v[8];
+  values8(ld_once(codes + i), pow2_of_byte(scales[i >> 2]), v);
+  x[i] = pack8(v);
+}
+
+struct SwigluCkptParams {
+  const uint4* h13;       // [M, 2h] bf16 (forward)
+  const uint4* dy;        // [M, h] bf16 (backward)
+  uint2* codes;           // [M, 2h]
+  uint8_t* scales;        // [M, 2h/32]
+  uint4* y;               // [M, h] bf16; backward: the recomputed y, or NULL
+  uint4* dh13;            // [M, 2h] bf16 (backward)
+  int64_t n8;             // M * h / 8
+  uint32_t h8;            // h / 8
+};
+
+// Row and 8-element column of vector i of an [M, h] matrix (n8 < 2^32, or the
+// 64-bit division).
+MX_DEVINL void row_col(int64_t i, uint32_t h8, bool narrow, int64_t& row, uint32_t& c) {
+  if (narrow) {
+    row = (uint32_t)i / h8;
+    c = (uint32_t)i - (uint32_t)row * h8;
+  } else {
+    row = i / h8;
+    c = (uint32_t)(i - row * h8);
+  }
+}
+
+__global__ void __launch_bounds__(C8_THREADS) swiglu_ckpt8_fwd_kernel(SwigluCkptParams p) {
+  const int64_t i = (int64_t)blockIdx.x * C8_THREADS + threadIdx.x;
+  const bool in = i < p.n8;
+  int64_t row;
+  uint32_t c;
+  row_col(in ? i : 0, p.h8, p.n8 <= 0xFFFFFFFFll, row, c);
+  const int64_t gi = row * 2 * p.h8 + c, ui = gi + p.h8;
+  float g[8], u[8], y[8];
+  const uint4 z = make_uint4(0, 0, 0, 0);
+  const uint4 gp = in ? ld_once(p.h13 + gi) : z, up = in ? ld_once(p.h13 + ui) : z;
+  unpack8(gp, g);
+  unpack8(up, u);
+  const uint32_t sg = ckpt8_scale(block_amax(g)), su = ckpt8_scale(block_amax(u));
+  if (!in) return;
+  p.codes[gi] = ckpt8_encode(g, sg);
+  p.codes[ui] = ckpt8_encode(u, su);
+  if ((threadIdx.x & 3) == 0) {
+    p.scales[gi >> 2] = (uint8_t)sg;
+    p.scales[ui >> 2] = (uint8_t)su;
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) y[k] = g[k] * sigmoid_approx(g[k]) * u[k];
+  p.y[i] = pack8(y);
+}
+
+__global__ void __launch_bounds__(C8_THREADS) swiglu_ckpt8_bwd_kernel(SwigluCkptParams p) {
+  const int64_t i = (int64_t)blockIdx.x * C8_THREADS + threadIdx.x;
+  if (i >= p.n8) return;
+  int64_t row;
+  uint32_t c;
+  row_col(i, p.h8, p.n8 <= 0xFFFFFFFFll, row, c);
+  const int64_t gi = row * 2 * p.h8 + c, ui = gi + p.h8;
+  const uint4 dp = ld_once(p.dy + i);
+  const uint2 gc = ld_once(p.codes + gi), uc = ld_once(p.codes + ui);
+  const uint32_t sg = p.scales[gi >> 2], su = p.scales[ui >> 2];
+  float g[8], u[8], dy[8], y[8];
+  unpack8(dp, dy);
+  values8(gc, pow2_of_byte(sg), g);
+  values8(uc, pow2_of_byte(su), u);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float s = sigmoid_approx(g[k]);
+    const float a = g[k] * s;
+    const float dg = dy[k] * u[k] * (s + a * (1.0f - s));
+    y[k] = a * u[k];
+    u[k] = dy[k] * a;
+    g[k] = dg;
+  }
+  p.dh13[gi] = pack8(g);
+  p.dh13[ui] = pack8(u);
+  if (p.y) p.y[i] = pack8(y);
+}
+
+int grid_of(int64_t n8, unsigned* grid) {
+  const int64_t b = (n8 + C8_THREADS - 1) / C8_THREADS;
+  if (b > INT32_MAX) return fail(MX_ERR_UNSUPPORTED, "8-bit checkpoint: too many elements");
+  *grid = (unsigned)b;
+  return MX_OK;
+}
+
+}  // namespace
+
+int launch_ckpt8_save(const void* x, int64_t rows, int64_t cols, void* codes, void* scales, cudaStream_t stream) {
+  const int64_t n8 = rows * (cols / 8);
+  unsigned grid;
+  if (int rc = grid_of(n8, &grid)) return rc;
+  count_launch(MX_KERNEL_CKPT8);
+  ckpt8_save_kernel<<<grid, C8_THREADS, 0, stream>>>((const uint4*)x, n8, (uint2*)codes, (uint8_t*)scales);
+  return cuda_status(cudaGetLastError(), "ckpt8_save_kernel launch");
+}
+
+int launch_ckpt8_load(const void* codes, const void* scales, int64_t rows, int64_t cols, void* x, cudaStream_t stream) {
+  const int64_t n8 = rows * (cols / 8);
+  unsigned grid;
+  if (int rc = grid_of(n8, &grid)) return rc;
+  count_launch(MX_KERNEL_CKPT8);
+  ckpt8_load_kernel<<<grid, C8_THREADS, 0, stream>>>((const uint2*)codes, (const uint8_t*)scales, n8, (uint4*)x);
+  return cuda_status(cudaGetLastError(), "ckpt8_load_kernel launch");
+}
+
+int launch_swiglu_ckpt8_fwd(const void* h13, int64_t M, int64_t h, void* y, void* codes, void* scales,
+                            cudaStream_t stream) {
+  SwigluCkptParams p{};
+  p.h13 = (const uint4*)h13; p.y = (uint4*)y; p.codes = (uint2*)codes; p.scales = (uint8_t*)scales;
+  p.n8 = M * (h / 8); p.h8 = (uint32_t)(h / 8);
+  unsigned grid;
+  if (int rc = grid_of(p.n8, &grid)) return rc;
+  count_launch(MX_KERNEL_CKPT8);
+  swiglu_ckpt8_fwd_kernel<<<grid, C8_THREADS, 0, stream>>>(p);
+  return cuda_status(cudaGetLastError(), "swiglu_ckpt8_fwd_kernel launch");
+}
+
+int launch_swiglu_ckpt8_bwd(const void* dy, const void* codes, const void* scales, int64_t M, int64_t h, void* dh13,
+                            void* y, cudaStream_t stream) {
+  SwigluCkptParams p{};
+  p.dy = (const uint4*)dy; p.codes = (uint2*)const_cast<void*>(codes);
+  p.scales = (uint8_t*)const_cast<void*>(scales);
+  p.dh13 = (uint4*)dh13; p.y = (uint4*)y;
+  p.n8 = M * (h / 8); p.h8 = (uint32_t)(h / 8);
+  unsigned grid;
+  if (int rc = grid_of(p.n8, &grid)) return rc;
+  count_launch(MX_KERNEL_CKPT8);
+  swiglu_ckpt8_bwd_kernel<<<grid, C8_THREADS, 0, stream>>>(p);
+  return cuda_status(cudaGetLastError(), "swiglu_ckpt8_bwd_kernel launch");
+}
+
+}  // namespace mx

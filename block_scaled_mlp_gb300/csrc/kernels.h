@@ -123,4 +123,45 @@ int launch_token_group_pad(const int32_t* expert_of, int64_t R, int32_t E, int32
 int launch_gather_rows(const void* x, int64_t rows_in, int64_t cols, const int32_t* src, int64_t rows_out,
                        int32_t div, void* y, int32_t* err, cudaStream_t stream);
 
+// ---------------------------------------------------------------- norm
+constexpr int64_t kNormMaxD = 16384;
+struct NormFwdLaunch {
+  const void* x;          // [M, d] bf16
+  const void* residual;   // [M, d] bf16 or NULL
+  const void* w;          // [d] bf16
+  int64_t M, d;
+  float eps;
+  void* r;                // [M, d] bf16: the sum (with a residual)
+  float* rstd;            // [M]
+  void* y;                // [M, d] bf16 or NULL
+  int layout;
+  void* q_row; void* s_row;   // MXFP8 rows, or NULL
+  void* q_col; void* s_col;   // MXFP8 columns, or NULL
+  void* ck; void* ck_scales;  // 8-bit checkpoint of the sum, or NULL
+  int floor_scale;
+};
+int launch_add_rmsnorm_fwd(const NormFwdLaunch& a, cudaStream_t stream);
+struct NormBwdLaunch {
+  const void* dy;         // [M, d] bf16
+  const void* r;          // [M, d] bf16, or NULL with
+  const void* ck; const void* ck_scales;  // its 8-bit checkpoint
+  const float* rstd;
+  const void* w;
+  const void* dres;       // [M, d] bf16 or NULL
+  int64_t M, d;
+  void* dx;               // [M, d] bf16
+  void* dw;               // [d] bf16
+  void* workspace;        // norm_bwd_ctas(M) * d floats
+};
+int norm_bwd_ctas(int64_t M);
+int launch_add_rmsnorm_bwd(const NormBwdLaunch& a, cudaStream_t stream);
+
+// ---------------------------------------------------------------- 8-bit checkpoints
+int launch_ckpt8_save(const void* x, int64_t rows, int64_t cols, void* codes, void* scales, cudaStream_t stream);
+int launch_ckpt8_load(const void* codes, const void* scales, int64_t rows, int64_t cols, void* x, cudaStream_t stream);
+int launch_swiglu_ckpt8_fwd(const void* h13, int64_t M, int64_t h, void* y, void* codes, void* scales,
+                            cudaStream_t stream);
+int launch_swiglu_ckpt8_bwd(const void* dy, const void* codes, const void* scales, int64_t M, int64_t h, void* dh13,
+                            void* y, cudaStream_t stream);
+
 }  // namespace mx

@@ -1,0 +1,543 @@
+// norm.cu - residual addition and root-mean-square norm with the result in
+// MXFP8 (rows, or rows and columns) and / or bf16, and the backward pass.
+//
+//   r = RN_bf16(x + residual),  n = (sum_j r_j^2 / d + eps)^-1/2,  y = r n w
+//   dr = n (dy w - r n c) + dres,  c = n / d sum_j dy_j w_j r_j
+//   dw = sum over rows of dy r n
+//
+// Sums are fp32; n is kept as an unevaluated pair of fp32 values and r w is
+// exact in fp32 (two bf16 factors), so y is the fp32 value nearest to r w n
+// and is then rounded to E4M3 or to bf16.  With n and y rounded step by step,
+// two to four times as many codes fell on the other side of a tie.  The sum r is what the model carries on in bf16, so the norm is taken of the rounded
+// value, the one that the backward pass has.  All kernels are bound by HBM:
+// each input is read once and each output written once, a row staying in
+// registers or shared memory between its two uses.
+#include "ckpt8.cuh"
+#include "kernels.h"
+#include "tile_quant.cuh"
+
+namespace mx {
+
+namespace {
+
+struct NormFwdParams {
+  const uint4* x;        // [M, d] bf16
+  const uint4* res;      // [M, d] bf16 or NULL
+  const uint4* w;        // [d] bf16
+  uint4* r;              // [M, d] bf16: x + res, or NULL
+  float* rstd;           // [M]
+  uint4* y;              // [M, d] bf16 or NULL
+  uint8_t* q_row;        // [M, d] E4M3 or NULL
+  ScaleDst s_row;
+  uint8_t* q_col;        // [d, M] E4M3 or NULL
+  ScaleDst s_col;
+  uint8_t* ck;           // [M, d] checkpoint codes of r, or NULL
+  uint8_t* ck_s;         // [M, d/32]
+  int64_t M;
+  int32_t d8;            // d / 8
+  float d, eps;
+  uint32_t rceil;
+};
+
+// r of eight elements: the bf16 sum, packed.
+MX_DEVINL uint4 add8(const uint4& a, const uint4& b) {
+  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = f2_to_bf16x2(f2_add(f2_from_bf16x2(x[i]), f2_from_bf16x2(y[i])));
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+MX_DEVINL float sumsq8(const uint4& a) {
+  const uint32_t x[4] = {a.x, a.y, a.z, a.w};
+  f2 s = f2_splat(0.0f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const f2 v = f2_from_bf16x2(x[i]);
+    s = f2_fma(v, v, s);
+  }
+  return s.x + s.y;
+}
+
+MX_DEVINL float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+// Unevaluated sums hi + lo; one that is infinite or NaN stays so.
+MX_DEVINL f2 pair_add(f2 a, f2 b) {
+  const float s = __fadd_rn(a.x, b.x), t = __fsub_rn(s, a.x);
+  const float e = __fadd_rn(__fsub_rn(a.x, __fsub_rn(s, t)), __fsub_rn(b.x, t));  // s + e = a.x + b.x
+  const float l = __fadd_rn(e, __fadd_rn(a.y, b.y)), h = __fadd_rn(s, l);
+  return abs_bits(s) < 0x7F800000u ? f2_pack(h, __fsub_rn(l, __fsub_rn(h, s))) : f2_pack(s, 0.0f);
+}
+template <int FROM>
+MX_DEVINL f2 warp_sum_pair(f2 v) {
+#pragma unroll
+  for (int o = FROM; o > 0; o >>= 1)
+    v = pair_add(v, f2_pack(__shfl_xor_sync(0xFFFFFFFFu, v.x, o), __shfl_xor_sync(0xFFFFFFFFu, v.y, o)));
+  return v;
+}
+
+// (ss / d + eps)^-1/2 as a pair: the rounded root and one Newton step's
+// correction.  A root that is not finite (or zero) stays as it is.
+MX_DEVINL f2 rstd_pair(f2 ss, float d, float eps) {
+  const float q = __fdiv_rn(ss.x, d);
+  const float ql = __fdividef(__fadd_rn(__fmaf_rn(-q, d, ss.x), ss.y), d);
+  const f2 m = pair_add(f2_pack(q, ql), f2_pack(eps, 0.0f));
+  const float n = __frsqrt_rn(m.x), t = __fmul_rn(n, n);
+  float e = __fmaf_rn(-m.x, t, 1.0f);
+  e = __fmaf_rn(-m.x, __fmaf_rn(n, n, -t), e);
+  e = __fmaf_rn(-m.y, t, e);
+  const float lo = __fmul_rn(__fmul_rn(0.5f, n), e);
+  return f2_pack(n, fabsf(lo) < n ? lo : 0.0f);
+}
+
+// y of eight elements, fp32
+MX_DEVINL void norm8(const uint4& r, f2 n, const uint4& w, float (&y)[8]) {
+  float rv[8], wv[8];
+  unpack8(r, rv);
+  unpack8(w, wv);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float rw = __fmul_rn(rv[i], wv[i]);
+    y[i] = __fmaf_rn(rw, n.x, __fmul_rn(rw, n.y));
+  }
+}
+
+// ---- rows: one CTA per row, the row in registers (V vectors of eight a
+// thread).  CTAs past M only clear the scale layout's padding rows.
+template <int V>
+__global__ void __launch_bounds__(512) add_rmsnorm_row_kernel(NormFwdParams p) {
+  const int64_t row = blockIdx.x;
+  const int T = blockDim.x;
+  if (p.q_row && p.s_row.mma) {
+    // zeros where the layout is padded: whole rows past M, columns past d / 32
+    const int S = p.d8 / 4, S4 = (S + 3) & ~3;
+    for (int c = (row < p.M ? S : 0) + threadIdx.x; c < S4; c += T) p.s_row.put(row, c, 0);
+  }
+  if (row >= p.M) return;
+  const int64_t base = row * p.d8;
+  uint4 v[V];
+  float ss = 0;
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    const int c = threadIdx.x + k * T;
+    v[k] = c < p.d8 ? ld_once(p.x + base + c) : make_uint4(0, 0, 0, 0);
+  }
+  if (p.res) {
+    uint4 a[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const int c = threadIdx.x + k * T;
+      a[k] = c < p.d8 ? ld_once(p.res + base + c) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const int c = threadIdx.x + k * T;
+      v[k] = add8(v[k], a[k]);
+      if (c < p.d8) p.r[base + c] = v[k];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < V; ++k) ss += sumsq8(v[k]);
+  __shared__ f2 part[16];
+  const int lane = threadIdx.x & 31;
+  f2 sum = warp_sum_pair<16>(f2_pack(ss, 0.0f));
+  if (lane == 0) part[threadIdx.x >> 5] = sum;
+  __syncthreads();
+  sum = warp_sum_pair<8>((lane & 15) < (T >> 5) ? part[lane & 15] : f2_splat(0.0f));
+  const f2 n = rstd_pair(sum, p.d, p.eps);
+  if (threadIdx.x == 0) p.rstd[row] = n.x + n.y;
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    const int c = threadIdx.x + k * T;
+    const bool in = c < p.d8;
+    if (p.ck) {
+      float f[8];
+      unpack8(v[k], f);
+      const uint32_t s = ckpt8_scale(block_amax(f));
+      if (in) {
+        *reinterpret_cast<uint2*>(p.ck + (base + c) * 8) = ckpt8_encode(f, s);
+        if ((c & 3) == 0) p.ck_s[(base + c) >> 2] = (uint8_t)s;
+      }
+    }
+    float y[8];
+    norm8(v[k], n, in ? __ldg(p.w + c) : make_uint4(0, 0, 0, 0), y);
+    if (p.y && in) p.y[base + c] = pack8(y);
+    if (p.q_row) {
+      const uint32_t s = e8m0_from_amax_f32(block_amax(y), p.rceil);
+      if (in) {
+        *reinterpret_cast<uint2*>(p.q_row + (base + c) * 8) = mx_encode(y, s);
+        if ((c & 3) == 0) p.s_row.put(row, c >> 2, s);
+      }
+    }
+  }
+}
+
+// ---- rows and columns: a cluster of CTAs per 32 rows, each with a slice of
+// the columns (a multiple of 32).  r of the slice stays in shared memory in
+// bf16; the rows' sums of squares are exchanged through distributed shared
+// memory, so one pass over HBM gives both quantizations (a second kernel for
+// the columns would read r again: 10 bytes an element instead of 8).
+constexpr int NC_ROWS = 32;
+constexpr int NC_THREADS = 256;
+constexpr int NC_MAX_CTAS = 8;
+
+size_t nc_smem(int slice8) { return (size_t)NC_ROWS * slice8 * 16; }
+
+__global__ void __launch_bounds__(NC_THREADS) add_rmsnorm_col_kernel(NormFwdParams p, int32_t slice8) {
+  extern __shared__ __align__(16) uint4 tile[];   // [32][slice8]
+  __shared__ __align__(16) f2 part[NC_MAX_CTAS][NC_ROWS];       // sums of squares by CTA and row
+  const int rank = (int)cluster_ctarank();
+  const int ctas = (int)(gridDim.y);
+  const int64_t r0 = (int64_t)blockIdx.x * NC_ROWS;
+  const int c0 = rank * slice8;                                  // first vector of the slice
+  const int n8 = min(slice8, p.d8 - c0);                         // its vectors
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool live = r0 < p.M;  // else: a row block of the scale layout's padding
+
+  if (p.s_col.mma && rank == ctas - 1) {
+    // zeros where the layouts are padded: rows past M, columns past d
+    const int S = p.d8 / 4, first = live ? S : 0, cols = ((S + 3) & ~3) - first;
+    if (p.q_row)
+      for (int i = threadIdx.x; i < cols * NC_ROWS; i += NC_THREADS) p.s_row.put(r0 + i % NC_ROWS, first + i / NC_ROWS, 0);
+    for (int64_t c = (live ? p.d8 * 8 : 0) + threadIdx.x; c < ((p.d8 * 8 + 127) & ~127); c += NC_THREADS)
+      p.s_col.put(c, r0 >> 5, 0);
+  }
+  if (!live) return;  // the whole cluster
+
+  // warp: four rows of the slice
+  float ss[4] = {0, 0, 0, 0};
+  for (int c = lane; c < n8; c += 32) {
+    uint4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = ld_once(p.x + (r0 + warp * 4 + k) * p.d8 + c0 + c);
+    if (p.res) {
+      uint4 a[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) a[k] = ld_once(p.res + (r0 + warp * 4 + k) * p.d8 + c0 + c);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        v[k] = add8(v[k], a[k]);
+        p.r[(r0 + warp * 4 + k) * p.d8 + c0 + c] = v[k];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      tile[(warp * 4 + k) * slice8 + c] = v[k];
+      ss[k] += sumsq8(v[k]);
+    }
+  }
+  f2 sum[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) sum[k] = warp_sum_pair<16>(f2_pack(ss[k], 0.0f));
+  if (lane < ctas) {
+    // lane j: this CTA's sums of the warp's rows to CTA j of the cluster
+    const uint32_t dst = cluster_map(smem_u32(&part[rank][warp * 4]), lane);
+#pragma unroll
+    for (int k = 0; k < 4; k += 2)
+      asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(dst + k * 8), "f"(sum[k].x), "f"(sum[k].y),
+                   "f"(sum[k + 1].x), "f"(sum[k + 1].y)
+                   : "memory");
+  }
+  cluster_sync();  // every CTA's sums are here; the tile is complete too
+  __shared__ f2 s_n[NC_ROWS];
+  if (threadIdx.x < NC_ROWS) {
+    f2 t = part[0][threadIdx.x];
+    for (int j = 1; j < ctas; ++j) t = pair_add(t, part[j][threadIdx.x]);  // the same order in every CTA
+    const f2 n = rstd_pair(t, p.d, p.eps);
+    s_n[threadIdx.x] = n;
+    if (rank == 0) p.rstd[r0 + threadIdx.x] = n.x + n.y;
+  }
+  __syncthreads();
+
+  // rows: each lane eight elements, four lanes a block
+  for (int cb = 0; cb < n8; cb += 32) {
+    const int c = cb + lane;
+    const bool in = c < n8;
+    const uint4 w = in ? __ldg(p.w + c0 + c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int rr = warp * 4 + k;
+      const uint4 v = in ? tile[rr * slice8 + c] : make_uint4(0, 0, 0, 0);
+      const int64_t at = (r0 + rr) * p.d8 + c0 + c;
+      if (p.ck) {
+        float f[8];
+        unpack8(v, f);
+        const uint32_t s = ckpt8_scale(block_amax(f));
+        if (in) {
+          *reinterpret_cast<uint2*>(p.ck + at * 8) = ckpt8_encode(f, s);
+          if ((c & 3) == 0) p.ck_s[at >> 2] = (uint8_t)s;
+        }
+      }
+      float y[8];
+      norm8(v, s_n[rr], w, y);
+      if (p.y && in) p.y[at] = pack8(y);
+      if (p.q_row) {
+        const uint32_t s = e8m0_from_amax_f32(block_amax(y), p.rceil);
+        if (in) {
+          *reinterpret_cast<uint2*>(p.q_row + at * 8) = mx_encode(y, s);
+          if ((c & 3) == 0) p.s_row.put(r0 + rr, (c0 + c) >> 2, s);
+        }
+      }
+    }
+  }
+
+  // columns: each thread two adjacent columns, 32 rows (one block each)
+  const uint32_t* words = reinterpret_cast<const uint32_t*>(tile);
+  const uint32_t* ww = reinterpret_cast<const uint32_t*>(p.w + c0);
+  for (int pc = threadIdx.x; pc < n8 * 4; pc += NC_THREADS) {
+    const f2 w2 = f2_from_bf16x2(__ldg(ww + pc));
+    f2 y[NC_ROWS];
+    uint32_t ma = 0, mb = 0;
+#pragma unroll
+    for (int i = 0; i < NC_ROWS; ++i) {
+      const f2 rw = f2_mul(f2_from_bf16x2(words[i * slice8 * 4 + pc]), w2), n = s_n[i];
+      y[i] = f2_fma(rw, f2_splat(n.x), f2_mul(rw, f2_splat(n.y)));
+      ma = max(ma, abs_bits(y[i].x));
+      mb = max(mb, abs_bits(y[i].y));
+    }
+    const uint32_t sa = e8m0_from_amax_f32(ma, p.rceil), sb = e8m0_from_amax_f32(mb, p.rceil);
+    const f2 inv = f2_pack(inv_pow2(sa == 0xFF ? 127u : sa), inv_pow2(sb == 0xFF ? 127u : sb));
+    uint32_t ca[8], cb[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      f2 t[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) t[k] = f2_mul(y[4 * i + k], inv);
+      ca[i] = sa == 0xFF ? 0x7F7F7F7Fu : cvt_e4m3x2(t[0].x, t[1].x) | (cvt_e4m3x2(t[2].x, t[3].x) << 16);
+      cb[i] = sb == 0xFF ? 0x7F7F7F7Fu : cvt_e4m3x2(t[0].y, t[1].y) | (cvt_e4m3x2(t[2].y, t[3].y) << 16);
+    }
+    const int64_t col = (int64_t)c0 * 8 + 2 * pc;
+    uint8_t* dst = p.q_col + col * p.M + r0;   // 32-byte aligned if q_col is: M and r0 are multiples of 32
+    const bool v8 = ((uintptr_t)p.q_col & 31) == 0;
+    store32_codes(dst, ca, v8);
+    store32_codes(dst + p.M, cb, v8);
+    p.s_col.put(col, r0 >> 5, sa);
+    p.s_col.put(col + 1, r0 >> 5, sb);
+  }
+}
+
+// ---- backward: each CTA takes every G-th row; a thread keeps its columns'
+// weights and weight gradients (fp32) in registers over all of its rows and
+// has the next row's vectors in flight while the current row's sum goes
+// around.  The CTAs' partial weight gradients go to the workspace [G][d] and
+// a second kernel adds them in a fixed order: results do not change from run
+// to run.
+struct NormBwdParams {
+  const uint4* dy;       // [M, d] bf16
+  const uint4* r;        // [M, d] bf16, or
+  const uint2* ck;       // [M, d] checkpoint codes
+  const uint8_t* ck_s;   // [M, d/32]
+  const float* rstd;     // [M]
+  const uint4* w;        // [d]
+  const uint4* dres;     // [M, d] bf16 or NULL
+  uint4* dx;             // [M, d] bf16
+  float* part;           // [G][d]
+  int64_t M;
+  int32_t d8;
+  float inv_d;
+};
+
+template <bool CK> struct Saved;
+template <> struct Saved<false> {
+  uint4 v;
+  MX_DEVINL void load(const NormBwdParams& p, int64_t at, bool in) {
+    v = in ? ld_once(p.r + at) : make_uint4(0, 0, 0, 0);
+  }
+  MX_DEVINL void values(float (&f)[8]) const { unpack8(v, f); }
+};
+template <> struct Saved<true> {
+  uint2 v;
+  uint32_t s;
+  MX_DEVINL void load(const NormBwdParams& p, int64_t at, bool in) {
+    v = in ? ld_once(p.ck + at) : make_uint2(0, 0);
+    s = in ? (uint32_t)p.ck_s[at >> 2] : 0u;
+  }
+  MX_DEVINL void values(float (&f)[8]) const { values8(v, pow2_of_byte(s), f); }
+};
+
+template <int V, int T_MAX, int RES, bool CK>
+__global__ void __launch_bounds__(T_MAX, RES) add_rmsnorm_bwd_kernel(NormBwdParams p) {
+  const int T = blockDim.x, warps = T >> 5;
+  const uint4 z = make_uint4(0, 0, 0, 0);
+  __shared__ float sums[2][16];
+  uint4 w[V], dy[V];
+  Saved<CK> sv[V];
+  float acc[V][8];
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    const int c = threadIdx.x + k * T;
+    w[k] = c < p.d8 ? __ldg(p.w + c) : z;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[k][i] = 0;
+  }
+  auto load = [&](int64_t row, uint4 (&a)[V], Saved<CK> (&b)[V]) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const int c = threadIdx.x + k * T;
+      const bool in = c < p.d8;
+      a[k] = in ? ld_once(p.dy + row * p.d8 + c) : z;
+      b[k].load(p, row * p.d8 + c, in);
+    }
+  };
+  int64_t row = blockIdx.x;
+  if (row < p.M) load(row, dy, sv);
+  int par = 0;
+  for (; row < p.M; row += gridDim.x, par ^= 1) {
+    float dot = 0;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      float a[8], b[8], c[8];
+      unpack8(dy[k], a);
+      unpack8(w[k], b);
+      sv[k].values(c);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) dot = __fmaf_rn(__fmul_rn(a[i], b[i]), c[i], dot);
+    }
+    uint4 ndy[V], dr[V];
+    Saved<CK> nsv[V];
+    const bool more = row + gridDim.x < p.M;
+    if (more) load(row + gridDim.x, ndy, nsv);
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const int c = threadIdx.x + k * T;
+      dr[k] = p.dres && c < p.d8 ? ld_once(p.dres + row * p.d8 + c) : z;
+    }
+    const float n = p.rstd[row];
+    dot = warp_sum(dot);
+    if ((threadIdx.x & 31) == 0) sums[par][threadIdx.x >> 5] = dot;
+    __syncthreads();  // one a row: the next row writes the other buffer
+    dot = 0;
+    for (int i = 0; i < warps; ++i) dot += sums[par][i];
+    const float c1 = n * n * p.inv_d * dot;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const int c = threadIdx.x + k * T;
+      float a[8], b[8], r[8], o[8];
+      unpack8(dy[k], a);
+      unpack8(w[k], b);
+      sv[k].values(r);
+      unpack8(dr[k], o);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        acc[k][i] = __fmaf_rn(a[i], __fmul_rn(r[i], n), acc[k][i]);
+        o[i] = __fmaf_rn(n, __fmaf_rn(-c1, r[i], __fmul_rn(a[i], b[i])), o[i]);
+      }
+      if (c < p.d8) p.dx[row * p.d8 + c] = pack8(o);
+    }
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      dy[k] = ndy[k];
+      sv[k] = nsv[k];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    const int c = threadIdx.x + k * T;
+    if (c >= p.d8) continue;
+    float4* dst = reinterpret_cast<float4*>(p.part + ((int64_t)blockIdx.x * p.d8 + c) * 8);
+    dst[0] = make_float4(acc[k][0], acc[k][1], acc[k][2], acc[k][3]);
+    dst[1] = make_float4(acc[k][4], acc[k][5], acc[k][6], acc[k][7]);
+  }
+}
+
+// dw[c] = sum over g of part[g][c]: 32 columns a block, eight threads a
+// column each with every eighth row of the partials.
+__global__ void __launch_bounds__(256) norm_dw_kernel(const float* __restrict__ part, int32_t G, int32_t d,
+                                                      __nv_bfloat16* __restrict__ dw) {
+  __shared__ float s[8][32];
+  const int c = blockIdx.x * 32 + (threadIdx.x & 31), g0 = threadIdx.x >> 5;
+  float t = 0;
+  if (c < d)
+    for (int g = g0; g < G; g += 8) t += part[(int64_t)g * d + c];
+  s[g0][threadIdx.x & 31] = t;
+  __syncthreads();
+  if (g0 == 0 && c < d) {
+    for (int i = 1; i < 8; ++i) t += s[i][threadIdx.x];
+    dw[c] = __float2bfloat16_rn(t);
+  }
+}
+
+// Vectors of eight a thread holds of a row.
+int vectors_of(int d8) { return d8 <= 256 ? 1 : d8 <= 512 ? 2 : 4; }
+int bwd_vectors_of(int d8) { return d8 <= 256 ? 1 : d8 <= 1024 ? 2 : 4; }
+int threads_of(int d8, int V) { return ((d8 + V - 1) / V + 31) / 32 * 32; }
+
+}  // namespace
+
+int norm_bwd_ctas(int64_t M) { return (int)std::min<int64_t>(M, 2 * (int64_t)num_sms()); }
+
+int launch_add_rmsnorm_fwd(const NormFwdLaunch& a, cudaStream_t stream) {
+  NormFwdParams p{};
+  p.x = (const uint4*)a.x; p.res = (const uint4*)a.residual; p.w = (const uint4*)a.w;
+  p.r = (uint4*)a.r; p.rstd = a.rstd; p.y = (uint4*)a.y;
+  p.M = a.M; p.d8 = (int32_t)(a.d / 8); p.d = (float)a.d; p.eps = a.eps;
+  p.rceil = a.floor_scale ? 0u : 1u;
+  const bool mma = a.layout == MX_SCALE_MMA;
+  const int64_t Sr = a.d / 32, Sc = a.M / 32;
+  p.q_row = (uint8_t*)a.q_row; p.s_row = ScaleDst{(uint8_t*)a.s_row, (Sr + 3) / 4, Sr, mma};
+  p.q_col = (uint8_t*)a.q_col; p.s_col = ScaleDst{(uint8_t*)a.s_col, (Sc + 3) / 4, Sc, mma};
+  p.ck = (uint8_t*)a.ck; p.ck_s = (uint8_t*)a.ck_scales;
+  const int64_t padded = mma && (a.q_row || a.q_col) ? (a.M + 127) / 128 * 128 : a.M;  // rows of the scale layout
+  if (padded > INT32_MAX) return fail(MX_ERR_UNSUPPORTED, "norm: too many rows");
+  cudaError_t e;
+  if (a.q_col) {
+    // slices of at least 32 columns, as many as a portable cluster has CTAs
+    const int slice8 = ((p.d8 + NC_MAX_CTAS - 1) / NC_MAX_CTAS + 3) / 4 * 4;
+    const int ctas = (p.d8 + slice8 - 1) / slice8;
+    const size_t smem = nc_smem(slice8);
+    e = cudaFuncSetAttribute(add_rmsnorm_col_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute");
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(padded / NC_ROWS), (unsigned)ctas);
+    cfg.blockDim = dim3(NC_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1;
+    attr[0].val.clusterDim.y = ctas;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    count_launch(MX_KERNEL_NORM);
+    return cuda_status(cudaLaunchKernelEx(&cfg, add_rmsnorm_col_kernel, p, (int32_t)slice8),
+                       "add_rmsnorm_col_kernel launch");
+  }
+  const int V = vectors_of(p.d8), T = threads_of(p.d8, V);
+  count_launch(MX_KERNEL_NORM);
+  if (V == 1) add_rmsnorm_row_kernel<1><<<(unsigned)padded, T, 0, stream>>>(p);
+  else if (V == 2) add_rmsnorm_row_kernel<2><<<(unsigned)padded, T, 0, stream>>>(p);
+  else add_rmsnorm_row_kernel<4><<<(unsigned)padded, T, 0, stream>>>(p);
+  return cuda_status(cudaGetLastError(), "add_rmsnorm_row_kernel launch");
+}
+
+int launch_add_rmsnorm_bwd(const NormBwdLaunch& a, cudaStream_t stream) {
+  NormBwdParams p{};
+  p.dy = (const uint4*)a.dy; p.r = (const uint4*)a.r; p.ck = (const uint2*)a.ck; p.ck_s = (const uint8_t*)a.ck_scales;
+  p.rstd = a.rstd; p.w = (const uint4*)a.w; p.dres = (const uint4*)a.dres; p.dx = (uint4*)a.dx;
+  p.part = (float*)a.workspace;
+  p.M = a.M; p.d8 = (int32_t)(a.d / 8); p.inv_d = 1.0f / (float)a.d;
+  const int G = norm_bwd_ctas(a.M);
+  const int V = bwd_vectors_of(p.d8), T = threads_of(p.d8, V);
+  count_launch(MX_KERNEL_NORM);
+#define MX_LAUNCH_NB(V_, T_, R_)                                                     \
+  do {                                                                               \
+    if (a.ck) add_rmsnorm_bwd_kernel<V_, T_, R_, true><<<G, T, 0, stream>>>(p);      \
+    else add_rmsnorm_bwd_kernel<V_, T_, R_, false><<<G, T, 0, stream>>>(p);          \
+  } while (0)
+  if (V == 1) MX_LAUNCH_NB(1, 256, 2);
+  else if (V == 2) MX_LAUNCH_NB(2, 512, 1);
+  else MX_LAUNCH_NB(4, 512, 1);
+#undef MX_LAUNCH_NB
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_status(e, "add_rmsnorm_bwd_kernel launch");
+  count_launch(MX_KERNEL_NORM);
+  norm_dw_kernel<<<(unsigned)((a.d + 31) / 32), 256, 0, stream>>>(p.part, G, (int32_t)a.d, (__nv_bfloat16*)a.dw);
+  return cuda_status(cudaGetLastError(), "norm_dw_kernel launch");
+}
+
+}  // namespace mx

@@ -446,6 +446,75 @@ MX_API int mx_fp8_grouped_mm(int mode, const void* aq, const float* amax_a, cons
                              int32_t pad_multiple, void* c, int32_t* err_word, void* stream);
 
 /*
+ * ---- Operators around the MLP in a transformer block (no counterpart on
+ * the pages): the norm in front of it, and activations kept in 8 bits for
+ * the backward pass.  M and rows may be 0 (no rows: nothing is read; weight
+ * gradients are still written, as zeros).
+ *
+ * mx_add_rmsnorm_fwd - residual addition, root-mean-square norm and MXFP8
+ * cast in one pass over the data.
+ *
+ *   r    = RN_bf16(x + residual) (x itself without a residual)
+ *   rstd = (mean(r^2) + eps)^-1/2 per row, y = r * rstd * w, fp32
+ *   x, residual [M, d], w [d]: bf16; residual may be NULL.
+ *   r       [M, d] bf16 out, only with a residual (it may be x or residual).
+ *   rstd    [M] fp32 out.
+ *   y       [M, d] bf16 out, RN of the fp32 y; may be NULL.
+ *   axis    0, MX_ROW, MX_COL or MX_BOTH: MXFP8 codes and scales of y as in
+ *           mx_quantize_mode, rounded once from the fp32 y (not from the bf16 y).
+ *   ck_codes, ck_scales  8-bit checkpoint of r (see mx_ckpt8_save), or NULL.
+ * Requirements: d % 8 == 0, d <= 16384; d % 32 == 0 with codes or a
+ * checkpoint; M % 32 == 0 for MX_COL; 16-byte aligned pointers.
+ */
+MX_API int mx_add_rmsnorm_fwd(const void* x, const void* residual, const void* w, int64_t M, int64_t d, float eps,
+                              void* r, float* rstd, void* y, int axis, int layout, int scale_mode, void* q_row,
+                              void* s_row, void* q_col, void* s_col, void* ck_codes, void* ck_scales, void* stream);
+
+/*
+ * mx_add_rmsnorm_bwd - gradients of the above from the saved r (bf16), or from
+ * its 8-bit checkpoint (r then is what the checkpoint holds):
+ *   dx = rstd * (dy w - r rstd mean(dy w r rstd)) + dres, which is the gradient
+ *        of x and of the residual alike; dw = sum over rows of dy r rstd.
+ *   dy [M, d] bf16, rstd [M] from the forward call, dres [M, d] bf16: gradient
+ *   that reaches r on the residual path, or NULL.  dx [M, d], dw [d]: bf16 out.
+ *   workspace: mx_add_rmsnorm_bwd_workspace(M, d) bytes (partial weight
+ *   gradients, added in a fixed order).
+ */
+MX_API size_t mx_add_rmsnorm_bwd_workspace(int64_t M, int64_t d);
+MX_API int mx_add_rmsnorm_bwd(const void* dy, const void* r, const void* ck_codes, const void* ck_scales,
+                              const float* rstd, const void* w, const void* dres, int64_t M, int64_t d, void* dx,
+                              void* dw, void* workspace, void* stream);
+
+/*
+ * mx_ckpt8_save / mx_ckpt8_load - a bf16 activation in 8 bits and back.
+ *   x [rows, cols] bf16; codes [rows, cols] int8; scales [rows, cols/32] bytes:
+ *   32 elements along a row share 2^e, e the smallest (>= -127) with
+ *   max|x| <= 127 * 2^e, byte e + 127; code = RN(x * 2^-e).  Zero block: byte
+ *   0.  A block with a NaN or an infinity: byte 0xFF, loads as NaN.  A loaded
+ *   value is code * 2^e, exact in bf16.
+ * Requirements: cols % 32 == 0, 16-byte aligned pointers.
+ */
+MX_API int mx_ckpt8_save(const void* x, int64_t rows, int64_t cols, void* codes, void* scales, void* stream);
+MX_API int mx_ckpt8_load(const void* codes, const void* scales, int64_t rows, int64_t cols, void* x, void* stream);
+
+/*
+ * mx_swiglu_ckpt8_fwd / _bwd - SwiGLU whose backward pass works from an 8-bit
+ * checkpoint of h13 = [g | u]: 2.06 h bytes a row are kept instead of the 6 h
+ * of h13 and y in bf16.
+ *   forward   h13 [M, 2h] bf16 -> y = silu(g) u [M, h] bf16 (from the unrounded
+ *             h13), codes [M, 2h], scales [M, 2h/32].
+ *   backward  dy [M, h] bf16 and the checkpoint -> dh13 = [dg | du] [M, 2h]
+ *             bf16; y [M, h] bf16: silu(g) u again from the checkpoint (the operand of
+ *             w2's weight gradient), may be NULL.
+ * fp32 arithmetic, one rounding to bf16 each.
+ * Requirements: h % 32 == 0, 16-byte aligned pointers.
+ */
+MX_API int mx_swiglu_ckpt8_fwd(const void* h13, int64_t M, int64_t h, void* y, void* codes, void* scales,
+                               void* stream);
+MX_API int mx_swiglu_ckpt8_bwd(const void* dy, const void* codes, const void* scales, int64_t M, int64_t h,
+                               void* dh13, void* y, void* stream);
+
+/*
  * Kernel launch counters (observability; no counterpart on the pages).
  * The torchtitan page's GPU suite holds the fused MLP to an op-count
  * contract ("Add MXFP8 fused-MLP overrides in torchtitan", Numerics and
@@ -461,7 +530,9 @@ enum mx_kernel_family {
   MX_KERNEL_GEMM_SWIGLU = 4,  /* gemm_kernel with the fused SwiGLU epilogue (w13 GEMM + y quantization) */
   MX_KERNEL_DISPATCH = 5,     /* token-group padding and row gathers */
   MX_KERNEL_MEMSET = 6,       /* cudaMemsetAsync of scale padding or dispatch maps */
-  MX_KERNEL_FAMILIES = 7
+  MX_KERNEL_NORM = 7,         /* residual + RMS norm kernels, forward and backward */
+  MX_KERNEL_CKPT8 = 8,        /* 8-bit checkpoint kernels, SwiGLU with one among them */
+  MX_KERNEL_FAMILIES = 9
 };
 
 /*
