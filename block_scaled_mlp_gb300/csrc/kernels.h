@@ -164,4 +164,17 @@ int launch_swiglu_ckpt8_fwd(const void* h13, int64_t M, int64_t h, void* y, void
 int launch_swiglu_ckpt8_bwd(const void* dy, const void* codes, const void* scales, int64_t M, int64_t h, void* dh13,
                             void* y, cudaStream_t stream);
 
+// ---------------------------------------------------------------- ragged expert products
+struct RaggedLaunch {
+  int mode;               // mx_ragged_mode
+  const void* a;          // token rows: x [M, K] (FWD) or dout [M, N]
+  const void* b;          // weights [E, N, K], or x [M, K] (WGRAD)
+  int64_t M, N, K;
+  const int32_t* offs;    // [E] group ends
+  int32_t E;
+  void* c;                // [M, N], [M, K] or [E, N, K]
+  int32_t* err;
+};
+int launch_ragged(const RaggedLaunch& g, cudaStream_t stream);
+
 }  // namespace mx

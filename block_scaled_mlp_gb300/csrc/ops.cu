@@ -1,6 +1,7 @@
 // ops.cu - C ABI of the operators around the MLP (include/mxmlp.h): residual
-// addition + RMS norm, 8-bit activation checkpoints, SwiGLU with one.
-// Argument checks only; the kernels are in norm.cu and ckpt8.cu.
+// addition + RMS norm, 8-bit activation checkpoints, SwiGLU with one, ragged
+// expert products.  Argument checks only; the kernels are in norm.cu, ckpt8.cu
+// and ragged.cu.
 #include <math.h>
 
 #include "kernels.h"
@@ -128,6 +129,29 @@ int mx_swiglu_ckpt8_bwd(const void* dy, const void* codes, const void* scales, i
   if (!dy || !codes || !scales || !dh13) return fail(MX_ERR_INVALID_ARG, "null pointer argument");
   if (!all_aligned16(dy, codes, scales, dh13, y)) return fail(MX_ERR_ALIGNMENT, "tensor pointers must be 16-byte aligned");
   return launch_swiglu_ckpt8_bwd(dy, codes, scales, M, h, dh13, y, (cudaStream_t)stream);
+}
+
+int mx_ragged_mm(int mode, const void* a, const void* b, int64_t M_total, int64_t N, int64_t K, const int32_t* offs,
+                 int32_t E, void* c, int32_t* err_word, void* stream) {
+  if (mode < MX_RAGGED_FWD || mode > MX_RAGGED_WGRAD) return fail(MX_ERR_INVALID_ARG, "unknown ragged mode %d", mode);
+  if (M_total < 0 || N <= 0 || K <= 0) return fail(MX_ERR_INVALID_ARG, "need M_total >= 0, N > 0 and K > 0");
+  if (E < 1 || E > 1024) return fail(MX_ERR_INVALID_ARG, "E must be in [1, 1024]");
+  if (N % 8 || K % 8)
+    return fail(MX_ERR_UNSUPPORTED, "N and K must be multiples of 8 (got %lld, %lld)", (long long)N, (long long)K);
+  // coordinates and tile numbers are 32-bit, with room for a tile past the end
+  const int64_t most = INT32_MAX - 1024;
+  if (M_total > most || N > most || K > most) return fail(MX_ERR_UNSUPPORTED, "dimension too large");
+  if (!offs || (M_total > 0 && (!a || !b)) || (!c && (M_total > 0 || mode == MX_RAGGED_WGRAD)))
+    return fail(MX_ERR_INVALID_ARG, "null pointer argument");
+  if (!all_aligned16(a, b, c)) return fail(MX_ERR_ALIGNMENT, "tensor pointers must be 16-byte aligned");
+  if (M_total == 0) {
+    if (mode != MX_RAGGED_WGRAD) return MX_OK;
+    count_launch(MX_KERNEL_MEMSET);
+    return cuda_status(cudaMemsetAsync(c, 0, (size_t)E * N * K * 2, (cudaStream_t)stream), "cudaMemsetAsync");
+  }
+  RaggedLaunch g{};
+  g.mode = mode; g.a = a; g.b = b; g.M = M_total; g.N = N; g.K = K; g.offs = offs; g.E = E; g.c = c; g.err = err_word;
+  return launch_ragged(g, (cudaStream_t)stream);
 }
 
 }  // extern "C"

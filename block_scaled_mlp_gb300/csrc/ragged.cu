@@ -1,0 +1,511 @@
+// ragged.cu - bf16 matrix products grouped by expert with ragged group sizes.
+//
+//   FWD    out[t, n] = sum_k x[t, k] w[e, n, k]       t in group e
+//   DGRAD  dx[t, k]  = sum_n dout[t, n] w[e, n, k]
+//   WGRAD  dw[e, n, k] = sum_{t in e} dout[t, n] x[t, k]
+//
+// on the tcgen05 tensor cores: bf16 operands, fp32 accumulation in TMEM over
+// the whole contraction, one rounding to bf16.  Group ends may be any
+// non-decreasing numbers; nothing is padded in memory.
+//
+// Token groups are ragged, so tokens are the N side of the MMA (any multiple
+// of 32 at run time) and weight features the M side (256 per CTA pair): the
+// last tile of a group costs what its rows cost, and rows of the next group
+// that a tile's load brings along are columns of the accumulator that nobody
+// reads.  The accumulator comes out with features along its lanes; the
+// epilogue turns 32 x 32 blocks in shared memory and writes token rows.
+// In WGRAD both operands contract over tokens and are read where they lie
+// (token-major, the "MN-major" operand form), with no transposed copies; the
+// last partial step of 16 tokens is cleared behind the group's end in shared
+// memory first, in both operands, so that nothing the next group holds (NaN
+// included) enters the sum.
+//
+// One persistent CTA pair per two SMs, roles as in gemm.cu: warp 0 loads
+// (TMA), warp 1 issues MMAs (even CTA), warps 2-9 drain accumulators (two of
+// them, so a tile's stores overlap the next tile's MMAs), warp 10 clears
+// WGRAD tails.
+#include "common.cuh"
+#include "kernels.h"
+
+namespace mx {
+
+namespace {
+
+constexpr int RG_FWD = 0, RG_DGRAD = 1, RG_WGRAD = 2;
+constexpr int RG_EPI = 8;                 // epilogue warps
+constexpr int RG_MAX_E = 1024;
+constexpr int RG_F = 256;                 // features per pair tile
+
+template <int MODE, int BT>
+struct RCfg {
+  static constexpr bool A_MN = MODE != RG_FWD, B_MN = MODE == RG_WGRAD;
+  static constexpr int A_BYTES = 128 * 128;              // 128 features x 64 contraction elements
+  static constexpr int B_BYTES = (BT / 2) * 128;         // this CTA's half of the tile
+  static constexpr int TX = A_BYTES + B_BYTES;
+  static constexpr int STAGES = BT == 256 ? 6 : 11;
+  static constexpr int EPI_BYTES = RG_EPI * 2048;        // one 32 x 32 bf16 block per warp
+  static constexpr int TMEM = 2 * BT;                    // two accumulators
+  static constexpr int THREADS = 64 + RG_EPI * 32 + (MODE == RG_WGRAD ? 32 : 0);
+  static constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | (A_MN ? 1u << 15 : 0u) |
+                                    (B_MN ? 1u << 16 : 0u) | ((uint32_t)(RG_F >> 4) << 24);
+  static constexpr size_t SMEM = (size_t)STAGES * TX + EPI_BYTES + RG_MAX_E * 8 + 512 + 1024;
+  static_assert(BT == 256 || (BT == 32 && MODE != RG_WGRAD), "tile widths");
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+struct RaggedParams {
+  int64_t M;                // token rows
+  int32_t F;                // features on the M side (FWD, WGRAD: N; DGRAD: K)
+  int32_t C;                // contraction length (FWD: K; DGRAD: N)
+  int32_t T;                // WGRAD: columns of the N side (K)
+  int32_t E;
+  const int32_t* offs;
+  uint8_t* out;             // FWD, DGRAD: [M, F] bf16
+  int32_t* err;
+};
+
+struct Unit {
+  int32_t e;
+  int32_t f0;       // first feature
+  int64_t t0;       // first token row (FWD, DGRAD) or N-side column (WGRAD)
+  int32_t tn;       // live rows / columns of the tile
+  int32_t n_eff;    // tn rounded up to the MMA's multiple of 32
+  int32_t num_kb;   // contraction steps of 64
+  int64_t k0;       // WGRAD: first token
+  int32_t tail;     // WGRAD: tokens of the last step (1..64)
+};
+
+template <int MODE, int BT>
+MX_DEVINL Unit unit_of(const RaggedParams& p, const int32_t* ends, const int32_t* unit_end, int32_t u) {
+  Unit r{};
+  const int32_t f_tiles = (p.F + RG_F - 1) / RG_F;
+  if (MODE == RG_WGRAD) {
+    const int32_t t_tiles = (p.T + BT - 1) / BT, per = f_tiles * t_tiles;
+    r.e = u / per;
+    const int32_t v = u - r.e * per;
+    r.f0 = (v % f_tiles) * RG_F;
+    r.t0 = (int64_t)(v / f_tiles) * BT;
+    r.tn = (int32_t)min((int64_t)BT, p.T - r.t0);
+    r.k0 = r.e ? ends[r.e - 1] : 0;
+    const int32_t rows = ends[r.e] - (int32_t)r.k0;
+    r.num_kb = (rows + 63) / 64;
+    r.tail = rows - (r.num_kb - 1) * 64;
+  } else {
+    int lo = 0, hi = p.E - 1;  // first group whose unit_end is > u
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (unit_end[mid] > u) hi = mid; else lo = mid + 1;
+    }
+    r.e = lo;
+    const int32_t v = u - (lo ? unit_end[lo - 1] : 0);
+    const int64_t start = lo ? ends[lo - 1] : 0;
+    const int32_t rows = ends[lo] - (int32_t)start;
+    const int32_t t_tiles = (rows + BT - 1) / BT;
+    int32_t t, f;
+    if (rows <= p.F) {  // the rows are the smaller operand: re-read them, stream the weights once
+      f = v / t_tiles;
+      t = v - f * t_tiles;
+    } else {
+      t = v / f_tiles;
+      f = v - t * f_tiles;
+    }
+    r.f0 = f * RG_F;
+    r.t0 = start + (int64_t)t * BT;
+    r.tn = min(BT, rows - t * BT);
+    r.num_kb = (p.C + 63) / 64;
+    r.tail = 64;
+  }
+  r.n_eff = (r.tn + 31) & ~31;
+  return r;
+}
+
+template <int MODE, int BT>
+__global__ void __launch_bounds__(RCfg<MODE, BT>::THREADS, 1)
+    ragged_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                  const __grid_constant__ CUtensorMap tmC, RaggedParams p) {
+  using C = RCfg<MODE, BT>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = sA + C::STAGES * C::A_BYTES;
+  uint8_t* sEpi = sB + C::STAGES * C::B_BYTES;
+  int32_t* ends = reinterpret_cast<int32_t*>(sEpi + C::EPI_BYTES);
+  int32_t* unit_end = ends + RG_MAX_E;
+  uint64_t* full = reinterpret_cast<uint64_t*>(unit_end + RG_MAX_E);
+  uint64_t* empty = full + C::STAGES;
+  uint64_t* acc_full = empty + C::STAGES;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* done_bar = acc_empty + 2;
+  uint64_t* tail_bar = done_bar + 1;   // one per stage, like full
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(tail_bar + C::STAGES);
+  __shared__ int s_ok, s_units;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_ctarank();
+  const int32_t unit0 = blockIdx.x / 2, ustep = gridDim.x / 2;
+  const int32_t f_tiles = (p.F + RG_F - 1) / RG_F;
+
+  if (threadIdx.x == 0) {
+    // the even CTA's full and acc_empty barriers serve the pair; in WGRAD both
+    // CTAs arrive on full (the loader, or the warp that cleared a tail)
+    for (int s = 0; s < C::STAGES; ++s) { mbar_init(&full[s], MODE == RG_WGRAD ? 2 : 1); mbar_init(&empty[s], 1); }
+    for (int a = 0; a < 2; ++a) { mbar_init(&acc_full[a], 1); mbar_init(&acc_empty[a], 2 * RG_EPI); }
+    for (int s = 0; s < C::STAGES; ++s) mbar_init(&tail_bar[s], 1);
+    mbar_init(done_bar, 1);
+    fence_mbar_init();
+  }
+  if (warp == 2) {
+    // group ends, checked, and the running number of work units
+    int32_t prev = 0, units = 0;
+    bool ok = true;
+    for (int base = 0; base < p.E; base += 32) {
+      const int e = base + lane;
+      const int32_t v = e < p.E ? p.offs[e] : 0x7FFFFFFF;
+      int32_t before = __shfl_up_sync(0xFFFFFFFFu, v, 1);
+      if (lane == 0) before = prev;
+      const bool in = e < p.E;
+      if (in && (v < before || v < 0 || (int64_t)v > p.M)) ok = false;
+      int32_t n = in && ok ? (v - before + BT - 1) / BT * f_tiles : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int32_t m = __shfl_up_sync(0xFFFFFFFFu, n, o);
+        if (lane >= o) n += m;
+      }
+      if (in) {
+        ends[e] = v;
+        unit_end[e] = units + n;
+      }
+      units += __shfl_sync(0xFFFFFFFFu, n, 31);
+      prev = __shfl_sync(0xFFFFFFFFu, v, min(31, p.E - 1 - base));
+    }
+    ok = __all_sync(0xFFFFFFFFu, ok);
+    if (lane == 0) {
+      s_ok = ok;
+      s_units = MODE == RG_WGRAD ? p.E * f_tiles * ((p.T + BT - 1) / BT) : ok ? units : 0;
+      if (!ok && blockIdx.x == 0) record_error(p.err, MX_ERR_BAD_OFFSETS);
+    }
+    __syncwarp();
+    if (!ok && MODE == RG_WGRAD)
+      for (int e = lane; e < p.E; e += 32) ends[e] = 0;  // every group empty: zeros everywhere
+  }
+  if (warp == 1) { tmem_alloc_pair(tmem_holder, C::TMEM); tmem_relinquish_pair(); }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  cluster_sync();  // the peer's barriers exist before any remote arrive or pair copy
+  const uint32_t tmem = *tmem_holder;
+  const int32_t n_units = s_units;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ loads
+    const bool leader = elect_one();
+    if (leader) {
+      prefetch_tmap(&tmA);
+      prefetch_tmap(&tmB);
+    }
+    int stage = 0; uint32_t phase = 0;
+    bool ok = true;
+    for (int32_t u = unit0; u < n_units && ok; u += ustep) {
+      const Unit t = unit_of<MODE, BT>(p, ends, unit_end, u);
+      const int32_t f = t.f0 + rank * 128;
+      const int32_t b0 = (int32_t)(t.t0 + rank * (t.n_eff / 2));
+      for (int kb = 0; kb < t.num_kb; ++kb) {
+        if (!warp_wait(&empty[stage], phase ^ 1, p.err)) { ok = false; break; }
+        if (leader) {
+          uint8_t* dA = sA + stage * C::A_BYTES;
+          uint8_t* dB = sB + stage * C::B_BYTES;
+          const int32_t k = (int32_t)(t.k0 + kb * 64);
+          const bool clear = MODE == RG_WGRAD && kb == t.num_kb - 1 && (t.tail & 15);
+          uint32_t bar;
+          if (clear) {
+            // the tail's bytes complete on this CTA's own barrier; the warp
+            // that clears it arrives on the pair's full barrier
+            mbar_arrive_expect_tx(&tail_bar[stage], C::TX);
+            bar = cluster_map(smem_u32(&tail_bar[stage]), rank);
+          } else {
+            bar = cluster_map(smem_u32(&full[stage]), 0);
+            if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * C::TX);
+            else if (MODE == RG_WGRAD) mbar_arrive_cluster(bar);
+          }
+          if (MODE == RG_FWD) {
+            tma_load_3d_pair(dA, &tmA, k, f, t.e, bar);
+            tma_load_2d_pair(dB, &tmB, k, b0, bar);
+          } else if (MODE == RG_DGRAD) {
+            tma_load_3d_pair(dA, &tmA, f, k, t.e, bar);
+            tma_load_3d_pair(dA + 8192, &tmA, f + 64, k, t.e, bar);
+            tma_load_2d_pair(dB, &tmB, k, b0, bar);
+          } else {
+            tma_load_2d_pair(dA, &tmA, f, k, bar);
+            tma_load_2d_pair(dA + 8192, &tmA, f + 64, k, bar);
+            tma_load_2d_pair(dB, &tmB, b0, k, bar);
+            tma_load_2d_pair(dB + 8192, &tmB, b0 + 64, k, bar);
+          }
+        }
+        __syncwarp();
+        if (++stage == C::STAGES) { stage = 0; phase ^= 1; }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMAs
+    if (rank == 0) {
+      const bool leader = elect_one();
+      // K-major: 8-row atoms 1024 bytes apart, 16 elements = 32 bytes along the row.
+      // MN-major: 64-element columns 8192 bytes apart, 8-row atoms 1024 apart, 16
+      // contraction rows = 2048 bytes.
+      const uint64_t a0 = smem_desc(smem_u32(sA), C::A_MN ? 8192 : 16, 1024, 2);
+      const uint64_t b0 = smem_desc(smem_u32(sB), C::B_MN ? 8192 : 16, 1024, 2);
+      constexpr uint64_t a_step = C::A_MN ? 128 : 2, b_step = C::B_MN ? 128 : 2;
+      int stage = 0; uint32_t phase = 0;
+      int acc = 0; uint32_t acc_phase = 0;
+      bool ok = true;
+      for (int32_t u = unit0; u < n_units && ok; u += ustep) {
+        const Unit t = unit_of<MODE, BT>(p, ends, unit_end, u);
+        if (t.num_kb == 0) continue;
+        if (!warp_wait(&acc_empty[acc], acc_phase ^ 1, p.err)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)(acc * BT);
+        const uint32_t idesc = C::IDESC | ((uint32_t)(t.n_eff >> 3) << 17);
+        for (int kb = 0; kb < t.num_kb; ++kb) {
+          if (!warp_wait(&full[stage], phase, p.err)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t ad = a0 + (uint64_t)((stage * C::A_BYTES) >> 4);
+          const uint64_t bd = b0 + (uint64_t)((stage * C::B_BYTES) >> 4);
+          const int nk = kb == t.num_kb - 1 ? (t.tail + 15) / 16 : 4;
+          if (leader) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (k < nk) mma_bf16_pair(d, ad + k * a_step, bd + k * b_step, idesc, kb > 0 || k > 0);
+            tc_commit_pair_mc(&empty[stage], (uint16_t)0x3);
+          }
+          __syncwarp();
+          if (++stage == C::STAGES) { stage = 0; phase ^= 1; }
+        }
+        if (!ok) break;
+        if (leader) tc_commit_pair_mc(&acc_full[acc], (uint16_t)0x3);
+        __syncwarp();
+        if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+      }
+      if (leader) tc_commit_pair_mc(done_bar, (uint16_t)0x1);
+      __syncwarp();
+      mbar_wait(done_bar, 0, p.err);
+    }
+    __syncwarp();
+  } else if (MODE == RG_WGRAD && warp == 2 + RG_EPI) {
+    // ------------------------------------------------------------ tails
+    int stage = 0; uint32_t phases = 0;  // bit s: the parity that tail_bar[s] completes next
+    for (int32_t u = unit0; u < n_units; u += ustep) {
+      const Unit t = unit_of<MODE, BT>(p, ends, unit_end, u);
+      if (t.num_kb == 0) continue;
+      stage = (stage + t.num_kb - 1) % C::STAGES;  // the last step's stage
+      if (t.tail & 15) {
+        if (!warp_wait(&tail_bar[stage], (phases >> stage) & 1, p.err)) break;
+        phases ^= 1u << stage;
+        // rows tail .. the next multiple of 16 of both operands' 64-column
+        // blocks (the swizzle permutes within a 128-byte row only)
+        const int bytes = (16 - (t.tail & 15)) * 128;
+        for (int b = 0; b < 4; ++b) {
+          uint8_t* at = (b < 2 ? sA + stage * C::A_BYTES + b * 8192 : sB + stage * C::B_BYTES + (b - 2) * 8192) + t.tail * 128;
+          for (int i = lane * 16; i < bytes; i += 512) *reinterpret_cast<uint4*>(at + i) = make_uint4(0, 0, 0, 0);
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (rank == 0) mbar_arrive(&full[stage]);
+          else mbar_arrive_cluster(cluster_map(smem_u32(&full[stage]), 0));
+        }
+      }
+      if (++stage == C::STAGES) stage = 0;
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int ew = warp - 2, q = warp & 3, half = ew >> 2;
+    uint8_t* stg = sEpi + ew * 2048;
+    int acc = 0; uint32_t acc_phase = 0;
+    for (int32_t u = unit0; u < n_units; u += ustep) {
+      const Unit t = unit_of<MODE, BT>(p, ends, unit_end, u);
+      const int32_t f = t.f0 + rank * 128 + q * 32;   // this warp's features
+      if (t.num_kb == 0) {                            // WGRAD: an empty group's zeros
+        if (lane == 0) bulk_wait_read<0>();
+        __syncwarp();
+        uint4* row = reinterpret_cast<uint4*>(stg + lane * 64);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) row[j] = make_uint4(0, 0, 0, 0);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0 && f < p.F) {
+          for (int c = half; c * 32 < t.tn; c += 2)
+            asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                             reinterpret_cast<uint64_t>(&tmC)),
+                         "r"((int32_t)t.t0 + c * 32), "r"(f), "r"(t.e), "r"(smem_u32(stg))
+                         : "memory");
+          bulk_commit();
+        }
+        continue;
+      }
+      if (!warp_wait(&acc_full[acc], acc_phase, p.err)) break;
+      tc_fence_after();
+      const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BT);
+      for (int c = half; c * 32 < t.tn; c += 2) {
+        uint32_t r[32];
+        tmem_ld_32cols(tb + c * 32, r);
+        tmem_ld_wait();
+        if (f >= p.F) continue;
+        if (MODE == RG_WGRAD) {
+          // lane: a row of dw, 32 columns of it
+          if (lane == 0) bulk_wait_read<0>();
+          __syncwarp();
+          uint8_t* row = stg + lane * 64;
+          const int sw = (lane >> 1) & 3;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              w[i] = f2_to_bf16x2(f2_pack(__uint_as_float(r[8 * j + 2 * i]), __uint_as_float(r[8 * j + 2 * i + 1])));
+            *reinterpret_cast<uint4*>(row + ((j ^ sw) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                             reinterpret_cast<uint64_t>(&tmC)),
+                         "r"((int32_t)t.t0 + c * 32), "r"(f), "r"(t.e), "r"(smem_u32(stg))
+                         : "memory");
+            bulk_commit();
+          }
+        } else {
+          // lane: a feature, 32 tokens of it; turned through shared memory
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const uint32_t w = f2_to_bf16x2(f2_pack(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])));
+            *reinterpret_cast<uint16_t*>(stg + (2 * i) * 64 + lane * 2) = (uint16_t)w;
+            *reinterpret_cast<uint16_t*>(stg + (2 * i + 1) * 64 + lane * 2) = (uint16_t)(w >> 16);
+          }
+          __syncwarp();
+          const int32_t col = f + (lane & 3) * 8;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int row = i * 8 + (lane >> 2);
+            const uint4 v = *reinterpret_cast<const uint4*>(stg + row * 64 + (lane & 3) * 16);
+            if (c * 32 + row < t.tn && col < p.F)
+              *reinterpret_cast<uint4*>(p.out + ((t.t0 + c * 32 + row) * p.F + col) * 2) = v;
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (rank != 0) mbar_arrive_cluster(cluster_map(smem_u32(&acc_empty[acc]), 0));
+        else mbar_arrive(&acc_empty[acc]);
+      }
+      if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+    }
+    if (MODE == RG_WGRAD) {
+      if (lane == 0) bulk_wait<0>();
+    } else {
+      // rows past the last group (all rows, if the ends were refused) are zeros
+      const int64_t first = s_ok ? ends[p.E - 1] : 0;
+      uint4* dst = reinterpret_cast<uint4*>(p.out + first * p.F * 2);
+      const int64_t n = (p.M - first) * p.F / 8;
+      for (int64_t i = (int64_t)blockIdx.x * (RG_EPI * 32) + ew * 32 + lane; i < n; i += (int64_t)gridDim.x * (RG_EPI * 32))
+        dst[i] = make_uint4(0, 0, 0, 0);
+    }
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // no pair MMA, copy or remote arrive targets an exited CTA
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, C::TMEM);
+}
+
+template <int MODE, int BT>
+int launch_cfg(const CUtensorMap& tA, const CUtensorMap& tB, const CUtensorMap& tC, const RaggedParams& p, int64_t units,
+               cudaStream_t stream) {
+  using C = RCfg<MODE, BT>;
+  auto k = ragged_kernel<MODE, BT>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+  if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute");
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  static int resident[64] = {0};  // pairs that can be resident at once, by device
+  int dev = 0;
+  cudaGetDevice(&dev);
+  int& nres = resident[dev & 63];
+  if (nres == 0) {
+    cfg.gridDim = dim3(2 * (num_sms() / 2));
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, k, &cfg);
+    if (e != cudaSuccess || n <= 0)
+      return cuda_status(e != cudaSuccess ? e : cudaErrorInvalidConfiguration, "cudaOccupancyMaxActiveClusters");
+    nres = n;
+  }
+  cfg.gridDim = dim3(2 * (unsigned)std::max<int64_t>(1, std::min<int64_t>(units, nres)));
+  count_launch(MX_KERNEL_RAGGED);
+  return cuda_status(cudaLaunchKernelEx(&cfg, k, tA, tB, tC, p), "ragged_kernel launch");
+}
+
+}  // namespace
+
+int launch_ragged(const RaggedLaunch& g, cudaStream_t stream) {
+  const int mode = g.mode;
+  // few rows a group: the weights' bytes count, and a narrow token tile leaves
+  // shared memory to 11 stages of them
+  const bool narrow = mode != MX_RAGGED_WGRAD && g.M <= 32 * (int64_t)g.E;
+  const uint32_t bt = narrow ? 32 : 256;
+  CUtensorMap tA, tB, tC;
+  int rc;
+  const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  auto map2 = [&](CUtensorMap* m, const void* base, int64_t cols, uint32_t rows) {
+    uint64_t dims[2] = {(uint64_t)cols, (uint64_t)g.M};
+    uint64_t strides[1] = {(uint64_t)cols * 2};
+    uint32_t box[2] = {64, rows};
+    return make_tmap(m, bf, 2, const_cast<void*>(base), dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+  };
+  auto map_w = [&](CUtensorMap* m, const void* base, uint32_t cols, uint32_t rows, CUtensorMapSwizzle swz) {
+    uint64_t dims[3] = {(uint64_t)g.K, (uint64_t)g.N, (uint64_t)g.E};
+    uint64_t strides[2] = {(uint64_t)g.K * 2, (uint64_t)g.K * g.N * 2};
+    uint32_t box[3] = {cols, rows, 1};
+    return make_tmap(m, bf, 3, const_cast<void*>(base), dims, strides, box, swz);
+  };
+  RaggedParams p{};
+  p.M = g.M; p.E = g.E; p.offs = g.offs; p.out = (uint8_t*)g.c; p.err = g.err;
+  const int64_t t_units = g.M / bt + g.E;  // at most: every group may end in a part of a tile
+  if (mode == MX_RAGGED_FWD) {
+    p.F = (int32_t)g.N; p.C = (int32_t)g.K;
+    if ((rc = map_w(&tA, g.b, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B)) || (rc = map2(&tB, g.a, g.K, bt / 2))) return rc;
+    const int64_t units = t_units * ((g.N + RG_F - 1) / RG_F);
+    if (units > INT32_MAX) return fail(MX_ERR_UNSUPPORTED, "ragged product: too many tiles");
+    return narrow ? launch_cfg<RG_FWD, 32>(tA, tB, tB, p, units, stream) : launch_cfg<RG_FWD, 256>(tA, tB, tB, p, units, stream);
+  }
+  if (mode == MX_RAGGED_DGRAD) {
+    p.F = (int32_t)g.K; p.C = (int32_t)g.N;
+    if ((rc = map_w(&tA, g.b, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B)) || (rc = map2(&tB, g.a, g.N, bt / 2))) return rc;
+    const int64_t units = t_units * ((g.K + RG_F - 1) / RG_F);
+    if (units > INT32_MAX) return fail(MX_ERR_UNSUPPORTED, "ragged product: too many tiles");
+    return narrow ? launch_cfg<RG_DGRAD, 32>(tA, tB, tB, p, units, stream)
+                  : launch_cfg<RG_DGRAD, 256>(tA, tB, tB, p, units, stream);
+  }
+  p.F = (int32_t)g.N; p.T = (int32_t)g.K;
+  if ((rc = map2(&tA, g.a, g.N, 64)) || (rc = map2(&tB, g.b, g.K, 64)) ||
+      (rc = map_w(&tC, g.c, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)))
+    return rc;
+  const int64_t units = (int64_t)g.E * ((g.N + RG_F - 1) / RG_F) * ((g.K + 255) / 256);
+  if (units > INT32_MAX) return fail(MX_ERR_UNSUPPORTED, "ragged product: too many tiles");
+  return launch_cfg<RG_WGRAD, 256>(tA, tB, tC, p, units, stream);
+}
+
+}  // namespace mx

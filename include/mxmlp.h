@@ -515,6 +515,31 @@ MX_API int mx_swiglu_ckpt8_bwd(const void* dy, const void* codes, const void* sc
                                void* dh13, void* y, void* stream);
 
 /*
+ * mx_ragged_mm - bf16 matrix products grouped by expert, group sizes as the
+ * router left them (no padding, unlike mx_grouped_mm): fp32 accumulation on
+ * the tensor cores, one RN to bf16.
+ *   offs  [E] int32 device array of cumulative group ends: group e owns token
+ *         rows [offs[e-1], offs[e]) (offs[-1] = 0), any non-negative sizes.  Read
+ *         on the device: no host synchronization.
+ *   MX_RAGGED_FWD    a = x [M_total, K], b = w [E, N, K] -> c = out [M_total, N]:
+ *                    out[t] = x[t] . w[e]^T for t in group e.
+ *   MX_RAGGED_DGRAD  a = dout [M_total, N], b = w [E, N, K] -> c = dx [M_total, K]:
+ *                    dx[t] = dout[t] . w[e].
+ *   MX_RAGGED_WGRAD  a = dout [M_total, N], b = x [M_total, K] -> c = dw [E, N, K]:
+ *                    dw[e] = dout[group e]^T . x[group e] (operands read as they
+ *                    lie, no transposed copies).
+ * Rows past offs[E-1] are written as zeros (FWD, DGRAD) and not read (WGRAD);
+ * an empty group's dw[e] is zeros.
+ * Requirements: N, K multiples of 8; 1 <= E <= 1024; 16-byte aligned pointers;
+ * M_total may be 0 (dw is then zeros).  err_word (may be NULL) receives
+ * MX_ERR_BAD_OFFSETS if offs decreases, is negative or passes M_total; the
+ * whole result is then zeros.
+ */
+typedef enum { MX_RAGGED_FWD = 0, MX_RAGGED_DGRAD = 1, MX_RAGGED_WGRAD = 2 } mx_ragged_mode;
+MX_API int mx_ragged_mm(int mode, const void* a, const void* b, int64_t M_total, int64_t N, int64_t K,
+                        const int32_t* offs, int32_t E, void* c, int32_t* err_word, void* stream);
+
+/*
  * Kernel launch counters (observability; no counterpart on the pages).
  * The torchtitan page's GPU suite holds the fused MLP to an op-count
  * contract ("Add MXFP8 fused-MLP overrides in torchtitan", Numerics and
@@ -532,7 +557,8 @@ enum mx_kernel_family {
   MX_KERNEL_MEMSET = 6,       /* cudaMemsetAsync of scale padding or dispatch maps */
   MX_KERNEL_NORM = 7,         /* residual + RMS norm kernels, forward and backward */
   MX_KERNEL_CKPT8 = 8,        /* 8-bit checkpoint kernels, SwiGLU with one among them */
-  MX_KERNEL_FAMILIES = 9
+  MX_KERNEL_RAGGED = 9,       /* ragged expert products */
+  MX_KERNEL_FAMILIES = 10
 };
 
 /*

@@ -61,3 +61,16 @@ def test_checkpoint_refusals(L):
     assert L.mx_swiglu_ckpt8_fwd(P, 4, 64, ODD, P, P, None) == 2
     assert L.mx_swiglu_ckpt8_bwd(P, P, P, 4, 64, None, P, None) == 1 and L.mx_swiglu_ckpt8_bwd(P, P, P, 4, 64, P, ODD, None) == 2
     assert L.mx_swiglu_ckpt8_bwd(P, P, P, -4, 64, P, P, None) == 1
+
+
+def test_ragged_refusals(L):
+    def mm(mode=0, a=P, b=P, M=100, N=64, K=72, offs=P, E=4, c=P):
+        return L.mx_ragged_mm(mode, a, b, M, N, K, offs, E, c, None, None)
+
+    for mode in (0, 1, 2):
+        assert mm(mode, a=None) == 1 and mm(mode, b=None) == 1 and mm(mode, offs=None) == 1 and mm(mode, c=None) == 1
+        assert mm(mode, N=60) == 4 and mm(mode, K=60) == 4 and mm(mode, M=-1) == 1 and mm(mode, N=0) == 1
+        assert mm(mode, E=0) == 1 and mm(mode, E=1025) == 1 and mm(mode, M=1 << 31) == 4
+        assert mm(mode, a=ODD) == 2 and mm(mode, b=ODD) == 2 and mm(mode, c=ODD) == 2
+    assert mm(3) == 1 and mm(-1) == 1
+    assert mm(0, M=0, a=None, b=None) == 0
