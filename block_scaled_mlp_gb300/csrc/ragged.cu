@@ -16,9 +16,9 @@
 // epilogue turns 32 x 32 blocks in shared memory and writes token rows.
 // In WGRAD both operands contract over tokens and are read where they lie
 // (token-major, the "MN-major" operand form), with no transposed copies; the
-// last partial step of 16 tokens is cleared behind the group's end in shared
-// memory first, in both operands, so that nothing the next group holds (NaN
-// included) enters the sum.
+// last partial step of 16 tokens is overwritten with zeros behind the group's
+// end in shared memory first, in both operands, so that nothing the next group
+// holds (NaN included) enters the sum.
 //
 // One persistent CTA pair per two SMs, roles as in gemm.cu: warp 0 loads
 // (TMA), warp 1 issues MMAs (even CTA), warps 2-9 drain accumulators (two of
@@ -48,7 +48,7 @@ struct RCfg {
   static constexpr int THREADS = 64 + RG_EPI * 32 + (MODE == RG_WGRAD ? 32 : 0);
   static constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | (A_MN ? 1u << 15 : 0u) |
                                     (B_MN ? 1u << 16 : 0u) | ((uint32_t)(RG_F >> 4) << 24);
-  static constexpr size_t SMEM = (size_t)STAGES * TX + EPI_BYTES + RG_MAX_E * 8 + 512 + 1024;
+  static constexpr size_t SMEM = (size_t)STAGES * TX + EPI_BYTES + RG_MAX_E * 8 + 512 /*barriers*/ + 1024 /*align*/;
   static_assert(BT == 256 || (BT == 32 && MODE != RG_WGRAD), "tile widths");
   static_assert(SMEM <= 227 * 1024, "shared memory");
 };
@@ -60,8 +60,22 @@ struct RaggedParams {
   int32_t T;                // WGRAD: columns of the N side (K)
   int32_t E;
   const int32_t* offs;
-  uint8_t* out;             // FWD, DGRAD: [M, F] bf16
+  uint8_t* out;             // [M, F] (FWD, DGRAD) or [E, F, T] (WGRAD), bf16
   int32_t* err;
+};
+
+// Arrival in the even CTA for an accumulator that is drained: its values are in
+// registers (tcgen05.wait::ld), nothing else is handed over, so the arrival
+// need not release anything.  With release at cluster scope it waits for the
+// acknowledgement of the tile's global stores (1391 against 1169 us, at that
+// stage, for the weight gradients of 512 rows over 64 experts, 4096 x 7168).
+MX_DEVINL void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// WGRAD: boxes of 1, 2, 4 and 8 rows of 64 elements.
+struct ZeroMaps {
+  CUtensorMap rows[4];
 };
 
 struct Unit {
@@ -72,7 +86,7 @@ struct Unit {
   int32_t n_eff;    // tn rounded up to the MMA's multiple of 32
   int32_t num_kb;   // contraction steps of 64
   int64_t k0;       // WGRAD: first token
-  int32_t tail;     // WGRAD: tokens of the last step (1..64)
+  int32_t tail;     // WGRAD: tokens of the last step (1 to 64)
 };
 
 template <int MODE, int BT>
@@ -109,11 +123,13 @@ MX_DEVINL Unit unit_of(const RaggedParams& p, const int32_t* ends, const int32_t
       t = v / f_tiles;
       f = v - t * f_tiles;
     }
+    // the group's rows shared out evenly over its tiles, in multiples of 32 (a
+    // last tile of a few rows would load as much of the weights as a full one)
+    const int32_t share = ((rows + t_tiles - 1) / t_tiles + 31) & ~31;
     r.f0 = f * RG_F;
-    r.t0 = start + (int64_t)t * BT;
-    r.tn = min(BT, rows - t * BT);
+    r.t0 = start + (int64_t)t * share;
+    r.tn = min(share, rows - t * share);
     r.num_kb = (p.C + 63) / 64;
-    r.tail = 64;
   }
   r.n_eff = (r.tn + 31) & ~31;
   return r;
@@ -122,7 +138,7 @@ MX_DEVINL Unit unit_of(const RaggedParams& p, const int32_t* ends, const int32_t
 template <int MODE, int BT>
 __global__ void __launch_bounds__(RCfg<MODE, BT>::THREADS, 1)
     ragged_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                  const __grid_constant__ CUtensorMap tmC, RaggedParams p) {
+                  const __grid_constant__ ZeroMaps tmZ, RaggedParams p) {
   using C = RCfg<MODE, BT>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -136,7 +152,7 @@ __global__ void __launch_bounds__(RCfg<MODE, BT>::THREADS, 1)
   uint64_t* acc_full = empty + C::STAGES;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* done_bar = acc_empty + 2;
-  uint64_t* tail_bar = done_bar + 1;   // one per stage, like full
+  uint64_t* tail_bar = done_bar + 1;   // WGRAD, by stage: a tail's bytes are here
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(tail_bar + C::STAGES);
   __shared__ int s_ok, s_units;
 
@@ -146,9 +162,8 @@ __global__ void __launch_bounds__(RCfg<MODE, BT>::THREADS, 1)
   const int32_t f_tiles = (p.F + RG_F - 1) / RG_F;
 
   if (threadIdx.x == 0) {
-    // the even CTA's full and acc_empty barriers serve the pair; in WGRAD both
-    // CTAs arrive on full (the loader, or the warp that cleared a tail)
-    for (int s = 0; s < C::STAGES; ++s) { mbar_init(&full[s], MODE == RG_WGRAD ? 2 : 1); mbar_init(&empty[s], 1); }
+    // the even CTA's full and acc_empty barriers serve the pair
+    for (int s = 0; s < C::STAGES; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
     for (int a = 0; a < 2; ++a) { mbar_init(&acc_full[a], 1); mbar_init(&acc_empty[a], 2 * RG_EPI); }
     for (int s = 0; s < C::STAGES; ++s) mbar_init(&tail_bar[s], 1);
     mbar_init(done_bar, 1);
@@ -218,14 +233,13 @@ __global__ void __launch_bounds__(RCfg<MODE, BT>::THREADS, 1)
           const bool clear = MODE == RG_WGRAD && kb == t.num_kb - 1 && (t.tail & 15);
           uint32_t bar;
           if (clear) {
-            // the tail's bytes complete on this CTA's own barrier; the warp
-            // that clears it arrives on the pair's full barrier
+            // the step's bytes complete on this CTA's own barrier, and the
+            // zeros that follow them on the pair's full barrier
             mbar_arrive_expect_tx(&tail_bar[stage], C::TX);
             bar = cluster_map(smem_u32(&tail_bar[stage]), rank);
           } else {
             bar = cluster_map(smem_u32(&full[stage]), 0);
             if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * C::TX);
-            else if (MODE == RG_WGRAD) mbar_arrive_cluster(bar);
           }
           if (MODE == RG_FWD) {
             tma_load_3d_pair(dA, &tmA, k, f, t.e, bar);
@@ -271,7 +285,7 @@ __global__ void __launch_bounds__(RCfg<MODE, BT>::THREADS, 1)
           tc_fence_after();
           const uint64_t ad = a0 + (uint64_t)((stage * C::A_BYTES) >> 4);
           const uint64_t bd = b0 + (uint64_t)((stage * C::B_BYTES) >> 4);
-          const int nk = kb == t.num_kb - 1 ? (t.tail + 15) / 16 : 4;
+          const int nk = MODE == RG_WGRAD && kb == t.num_kb - 1 ? (t.tail + 15) / 16 : 4;
           if (leader) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -293,27 +307,35 @@ __global__ void __launch_bounds__(RCfg<MODE, BT>::THREADS, 1)
     __syncwarp();
   } else if (MODE == RG_WGRAD && warp == 2 + RG_EPI) {
     // ------------------------------------------------------------ tails
+    // Zeros over rows tail .. the next multiple of 16 of both operands' 64-column
+    // blocks, once the step's own bytes are here: TMA loads of rows past the
+    // end of the tensor (8, 4, 2 and 1 of them), which read as zeros and complete on
+    // the pair's full barrier.  Stores from a warp took a fence and, in the odd CTA,
+    // an arrival with release at cluster scope, which waits for the epilogue's global
+    // stores too: 948 against 833 us for 64 experts of 250 rows (4096 x 7168).
+    const bool leader = elect_one();
     int stage = 0; uint32_t phases = 0;  // bit s: the parity that tail_bar[s] completes next
     for (int32_t u = unit0; u < n_units; u += ustep) {
       const Unit t = unit_of<MODE, BT>(p, ends, unit_end, u);
       if (t.num_kb == 0) continue;
       stage = (stage + t.num_kb - 1) % C::STAGES;  // the last step's stage
-      if (t.tail & 15) {
+      const int rows = -t.tail & 15;
+      if (rows) {
         if (!warp_wait(&tail_bar[stage], (phases >> stage) & 1, p.err)) break;
         phases ^= 1u << stage;
-        // rows tail .. the next multiple of 16 of both operands' 64-column
-        // blocks (the swizzle permutes within a 128-byte row only)
-        const int bytes = (16 - (t.tail & 15)) * 128;
-        for (int b = 0; b < 4; ++b) {
-          uint8_t* at = (b < 2 ? sA + stage * C::A_BYTES + b * 8192 : sB + stage * C::B_BYTES + (b - 2) * 8192) + t.tail * 128;
-          for (int i = lane * 16; i < bytes; i += 512) *reinterpret_cast<uint4*>(at + i) = make_uint4(0, 0, 0, 0);
+        if (leader) {
+          const uint32_t bar = cluster_map(smem_u32(&full[stage]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * 4 * rows * 128);
+          for (int b = 0; b < 4; ++b) {
+            uint8_t* at = (b < 2 ? sA + stage * C::A_BYTES + b * 8192 : sB + stage * C::B_BYTES + (b - 2) * 8192) + t.tail * 128;
+            for (int i = 0; i < 4; ++i)
+              if (rows >> i & 1) {
+                tma_load_2d_pair(at, &tmZ.rows[i], 0, (int32_t)p.M, bar);
+                at += 128 << i;
+              }
+          }
         }
-        fence_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          if (rank == 0) mbar_arrive(&full[stage]);
-          else mbar_arrive_cluster(cluster_map(smem_u32(&full[stage]), 0));
-        }
       }
       if (++stage == C::STAGES) stage = 0;
     }
@@ -323,89 +345,95 @@ __global__ void __launch_bounds__(RCfg<MODE, BT>::THREADS, 1)
     const int ew = warp - 2, q = warp & 3, half = ew >> 2;
     uint8_t* stg = sEpi + ew * 2048;
     int acc = 0; uint32_t acc_phase = 0;
+    // WGRAD: row n, column col of the tile, of dw[e]
+    auto dw_at = [&](const Unit& t, int32_t n, int32_t col) {
+      return p.out + (((int64_t)t.e * p.F + n) * p.T + t.t0 + col) * 2;
+    };
     for (int32_t u = unit0; u < n_units; u += ustep) {
       const Unit t = unit_of<MODE, BT>(p, ends, unit_end, u);
       const int32_t f = t.f0 + rank * 128 + q * 32;   // this warp's features
       if (t.num_kb == 0) {                            // WGRAD: an empty group's zeros
-        if (lane == 0) bulk_wait_read<0>();
-        __syncwarp();
-        uint4* row = reinterpret_cast<uint4*>(stg + lane * 64);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) row[j] = make_uint4(0, 0, 0, 0);
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0 && f < p.F) {
-          for (int c = half; c * 32 < t.tn; c += 2)
-            asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
-                             reinterpret_cast<uint64_t>(&tmC)),
-                         "r"((int32_t)t.t0 + c * 32), "r"(f), "r"(t.e), "r"(smem_u32(stg))
-                         : "memory");
-          bulk_commit();
-        }
+        for (int c = half; c * 32 < t.tn; c += 2)
+          for (int i = 0; i < 4; ++i)
+            if (f + i * 8 < p.F && c * 32 + (lane & 3) * 8 < t.tn)
+              *reinterpret_cast<uint4*>(dw_at(t, f + i * 8 + (lane >> 2), c * 32 + (lane & 3) * 8)) = make_uint4(0, 0, 0, 0);
         continue;
       }
       if (!warp_wait(&acc_full[acc], acc_phase, p.err)) break;
       tc_fence_after();
-      const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BT);
-      for (int c = half; c * 32 < t.tn; c += 2) {
-        uint32_t r[32];
-        tmem_ld_32cols(tb + c * 32, r);
-        tmem_ld_wait();
-        if (f >= p.F) continue;
+      // every other block of columns: a short tile keeps both warps of a lane
+      // quarter busy, and the halves of a 128-byte line are written together (a
+      // contiguous half each: 724 against 685 us for a store-bound weight gradient)
+      constexpr int NC = BT == 32 ? 1 : BT / 64, STEP = NC == 1 ? 1 : 2;
+      constexpr int JB = 64;           // columns from a warp's block to its next
+      const int c_first = half * 32;
+      const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BT + c_first);
+      const int qr = lane >> 2, qc = (lane & 3) * 8;  // this lane's row (of 8) and columns in a 32 x 32 block's stores
+      uint8_t* dst = MODE == RG_WGRAD ? dw_at(t, f + qr, c_first + qc)
+                                      : p.out + ((t.t0 + c_first + qr) * p.F + f + qc) * 2;
+      // two blocks at a time: both loads in flight and one wait, and few enough
+      // registers that nothing spills (four at a time spilled 12 to 88 bytes, which
+      // L1, nearly all shared memory here, does not hold: 1.3x the time of a
+      // store-bound weight gradient)
+#pragma unroll 1
+      for (int j0 = 0; j0 < NC; j0 += STEP) {
+      uint32_t r[STEP][32];
+#pragma unroll
+      for (int j = 0; j < STEP; ++j)
+        if (c_first + (j0 + j) * JB < t.tn) tmem_ld_32cols(tb + (j0 + j) * JB, r[j]);
+      tmem_ld_wait();
+      if (j0 + STEP == NC) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (rank != 0) mbar_arrive_cluster_relaxed(cluster_map(smem_u32(&acc_empty[acc]), 0));
+          else mbar_arrive(&acc_empty[acc]);
+        }
+      }
+      if (f >= p.F) continue;
+#pragma unroll
+      for (int j = 0; j < STEP; ++j) {
+        const int c = c_first + (j0 + j) * JB;  // the block's first column of the tile
+        if (c >= t.tn) break;
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          w[i] = f2_to_bf16x2(f2_pack(__uint_as_float(r[j][2 * i]), __uint_as_float(r[j][2 * i + 1])));
+        __syncwarp();
         if (MODE == RG_WGRAD) {
-          // lane: a row of dw, 32 columns of it
-          if (lane == 0) bulk_wait_read<0>();
-          __syncwarp();
-          uint8_t* row = stg + lane * 64;
-          const int sw = (lane >> 1) & 3;
+          // lane: a row of dw, 32 columns of it; through shared memory (16-byte
+          // chunk k of row r at k ^ (r >> 1 & 3)) so that four lanes write one row
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              w[i] = f2_to_bf16x2(f2_pack(__uint_as_float(r[8 * j + 2 * i]), __uint_as_float(r[8 * j + 2 * i + 1])));
-            *reinterpret_cast<uint4*>(row + ((j ^ sw) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
-                             reinterpret_cast<uint64_t>(&tmC)),
-                         "r"((int32_t)t.t0 + c * 32), "r"(f), "r"(t.e), "r"(smem_u32(stg))
-                         : "memory");
-            bulk_commit();
-          }
+          for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<uint4*>(stg + lane * 64 + ((k ^ ((lane >> 1) & 3)) * 16)) =
+                make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
         } else {
           // lane: a feature, 32 tokens of it; turned through shared memory
-          __syncwarp();
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const uint32_t w = f2_to_bf16x2(f2_pack(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])));
-            *reinterpret_cast<uint16_t*>(stg + (2 * i) * 64 + lane * 2) = (uint16_t)w;
-            *reinterpret_cast<uint16_t*>(stg + (2 * i + 1) * 64 + lane * 2) = (uint16_t)(w >> 16);
+            *reinterpret_cast<uint16_t*>(stg + (2 * i) * 64 + lane * 2) = (uint16_t)w[i];
+            *reinterpret_cast<uint16_t*>(stg + (2 * i + 1) * 64 + lane * 2) = (uint16_t)(w[i] >> 16);
           }
-          __syncwarp();
-          const int32_t col = f + (lane & 3) * 8;
+        }
+        __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int row = i * 8 + (lane >> 2);
-            const uint4 v = *reinterpret_cast<const uint4*>(stg + row * 64 + (lane & 3) * 16);
-            if (c * 32 + row < t.tn && col < p.F)
-              *reinterpret_cast<uint4*>(p.out + ((t.t0 + c * 32 + row) * p.F + col) * 2) = v;
+        for (int i = 0; i < 4; ++i) {
+          const int rr = i * 8 + qr;
+          if (MODE == RG_WGRAD) {
+            if (f + i * 8 < p.F && c + qc < t.tn)
+              *reinterpret_cast<uint4*>(dst + ((int64_t)i * 8 * p.T + (j0 + j) * JB) * 2) =
+                  *reinterpret_cast<const uint4*>(stg + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) * 16));
+          } else {
+            if (c + rr < t.tn && f + qc < p.F)
+              *reinterpret_cast<uint4*>(dst + (int64_t)((j0 + j) * JB + i * 8) * p.F * 2) =
+                  *reinterpret_cast<const uint4*>(stg + rr * 64 + (lane & 3) * 16);
           }
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (rank != 0) mbar_arrive_cluster(cluster_map(smem_u32(&acc_empty[acc]), 0));
-        else mbar_arrive(&acc_empty[acc]);
       }
       if (++acc == 2) { acc = 0; acc_phase ^= 1; }
     }
-    if (MODE == RG_WGRAD) {
-      if (lane == 0) bulk_wait<0>();
-    } else {
+    if (MODE != RG_WGRAD) {
       // rows past the last group (all rows, if the ends were refused) are zeros
       const int64_t first = s_ok ? ends[p.E - 1] : 0;
       uint4* dst = reinterpret_cast<uint4*>(p.out + first * p.F * 2);
@@ -424,7 +452,7 @@ __global__ void __launch_bounds__(RCfg<MODE, BT>::THREADS, 1)
 }
 
 template <int MODE, int BT>
-int launch_cfg(const CUtensorMap& tA, const CUtensorMap& tB, const CUtensorMap& tC, const RaggedParams& p, int64_t units,
+int launch_cfg(const CUtensorMap& tA, const CUtensorMap& tB, const ZeroMaps& tZ, const RaggedParams& p, int64_t units,
                cudaStream_t stream) {
   using C = RCfg<MODE, BT>;
   auto k = ragged_kernel<MODE, BT>;
@@ -455,7 +483,7 @@ int launch_cfg(const CUtensorMap& tA, const CUtensorMap& tB, const CUtensorMap& 
   }
   cfg.gridDim = dim3(2 * (unsigned)std::max<int64_t>(1, std::min<int64_t>(units, nres)));
   count_launch(MX_KERNEL_RAGGED);
-  return cuda_status(cudaLaunchKernelEx(&cfg, k, tA, tB, tC, p), "ragged_kernel launch");
+  return cuda_status(cudaLaunchKernelEx(&cfg, k, tA, tB, tZ, p), "ragged_kernel launch");
 }
 
 }  // namespace
@@ -466,46 +494,48 @@ int launch_ragged(const RaggedLaunch& g, cudaStream_t stream) {
   // shared memory to 11 stages of them
   const bool narrow = mode != MX_RAGGED_WGRAD && g.M <= 32 * (int64_t)g.E;
   const uint32_t bt = narrow ? 32 : 256;
-  CUtensorMap tA, tB, tC;
+  CUtensorMap tA, tB;
+  ZeroMaps tZ{};
   int rc;
   const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  auto map2 = [&](CUtensorMap* m, const void* base, int64_t cols, uint32_t rows) {
+  auto map2 = [&](CUtensorMap* m, const void* base, int64_t cols, uint32_t rows,
+                  CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B) {
     uint64_t dims[2] = {(uint64_t)cols, (uint64_t)g.M};
     uint64_t strides[1] = {(uint64_t)cols * 2};
     uint32_t box[2] = {64, rows};
-    return make_tmap(m, bf, 2, const_cast<void*>(base), dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    return make_tmap(m, bf, 2, const_cast<void*>(base), dims, strides, box, swz);
   };
-  auto map_w = [&](CUtensorMap* m, const void* base, uint32_t cols, uint32_t rows, CUtensorMapSwizzle swz) {
+  auto map_w = [&](CUtensorMap* m, uint32_t rows) {
     uint64_t dims[3] = {(uint64_t)g.K, (uint64_t)g.N, (uint64_t)g.E};
     uint64_t strides[2] = {(uint64_t)g.K * 2, (uint64_t)g.K * g.N * 2};
-    uint32_t box[3] = {cols, rows, 1};
-    return make_tmap(m, bf, 3, const_cast<void*>(base), dims, strides, box, swz);
+    uint32_t box[3] = {64, rows, 1};
+    return make_tmap(m, bf, 3, const_cast<void*>(g.b), dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
   };
   RaggedParams p{};
   p.M = g.M; p.E = g.E; p.offs = g.offs; p.out = (uint8_t*)g.c; p.err = g.err;
   const int64_t t_units = g.M / bt + g.E;  // at most: every group may end in a part of a tile
   if (mode == MX_RAGGED_FWD) {
     p.F = (int32_t)g.N; p.C = (int32_t)g.K;
-    if ((rc = map_w(&tA, g.b, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B)) || (rc = map2(&tB, g.a, g.K, bt / 2))) return rc;
+    if ((rc = map_w(&tA, 128)) || (rc = map2(&tB, g.a, g.K, bt / 2))) return rc;
     const int64_t units = t_units * ((g.N + RG_F - 1) / RG_F);
     if (units > INT32_MAX) return fail(MX_ERR_UNSUPPORTED, "ragged product: too many tiles");
-    return narrow ? launch_cfg<RG_FWD, 32>(tA, tB, tB, p, units, stream) : launch_cfg<RG_FWD, 256>(tA, tB, tB, p, units, stream);
+    return narrow ? launch_cfg<RG_FWD, 32>(tA, tB, tZ, p, units, stream) : launch_cfg<RG_FWD, 256>(tA, tB, tZ, p, units, stream);
   }
   if (mode == MX_RAGGED_DGRAD) {
     p.F = (int32_t)g.K; p.C = (int32_t)g.N;
-    if ((rc = map_w(&tA, g.b, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B)) || (rc = map2(&tB, g.a, g.N, bt / 2))) return rc;
+    if ((rc = map_w(&tA, 64)) || (rc = map2(&tB, g.a, g.N, bt / 2))) return rc;
     const int64_t units = t_units * ((g.K + RG_F - 1) / RG_F);
     if (units > INT32_MAX) return fail(MX_ERR_UNSUPPORTED, "ragged product: too many tiles");
-    return narrow ? launch_cfg<RG_DGRAD, 32>(tA, tB, tB, p, units, stream)
-                  : launch_cfg<RG_DGRAD, 256>(tA, tB, tB, p, units, stream);
+    return narrow ? launch_cfg<RG_DGRAD, 32>(tA, tB, tZ, p, units, stream)
+                  : launch_cfg<RG_DGRAD, 256>(tA, tB, tZ, p, units, stream);
   }
   p.F = (int32_t)g.N; p.T = (int32_t)g.K;
-  if ((rc = map2(&tA, g.a, g.N, 64)) || (rc = map2(&tB, g.b, g.K, 64)) ||
-      (rc = map_w(&tC, g.c, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)))
-    return rc;
+  if ((rc = map2(&tA, g.a, g.N, 64)) || (rc = map2(&tB, g.b, g.K, 64))) return rc;
+  for (int i = 0; i < 4; ++i)
+    if ((rc = map2(&tZ.rows[i], g.b, g.K, 1u << i, CU_TENSOR_MAP_SWIZZLE_NONE))) return rc;
   const int64_t units = (int64_t)g.E * ((g.N + RG_F - 1) / RG_F) * ((g.K + 255) / 256);
   if (units > INT32_MAX) return fail(MX_ERR_UNSUPPORTED, "ragged product: too many tiles");
-  return launch_cfg<RG_WGRAD, 256>(tA, tB, tC, p, units, stream);
+  return launch_cfg<RG_WGRAD, 256>(tA, tB, tZ, p, units, stream);
 }
 
 }  // namespace mx
