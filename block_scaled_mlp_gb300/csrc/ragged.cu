@@ -43,14 +43,20 @@ struct RCfg {
   static constexpr int B_BYTES = (BT / 2) * 128;         // this CTA's half of the tile
   static constexpr int TX = A_BYTES + B_BYTES;
   static constexpr int STAGES = BT == 256 ? 6 : 11;
-  static constexpr int EPI_BYTES = RG_EPI * 2048;        // one 32 x 32 bf16 block per warp
+  static constexpr int EPI_WARP = MODE == RG_WGRAD ? 4096 : 2048;  // a warp's 32 x 64 or 32 x 32 bf16 block
+  static constexpr int EPI_BYTES = RG_EPI * EPI_WARP;
+  // Group ends and running unit numbers.  WGRAD needs the ends only, and its
+  // 64-column blocks leave room for 128: with more experts every role reads them
+  // from global memory (620 against 575 us for 64 experts of 8 rows, 4096 x 7168).
+  static constexpr int ENDS = MODE == RG_WGRAD ? 128 : RG_MAX_E;
+  static constexpr int TABLE = ENDS * (MODE == RG_WGRAD ? 4 : 8);
   static constexpr int TMEM = 2 * BT;                    // two accumulators
   static constexpr int THREADS = 64 + RG_EPI * 32 + (MODE == RG_WGRAD ? 32 : 0);
   static constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | (A_MN ? 1u << 15 : 0u) |
                                     (B_MN ? 1u << 16 : 0u) | ((uint32_t)(RG_F >> 4) << 24);
-  static constexpr size_t SMEM = (size_t)STAGES * TX + EPI_BYTES + RG_MAX_E * 8 + 512 /*barriers*/ + 1024 /*align*/;
+  static constexpr size_t SMEM = (size_t)STAGES * TX + EPI_BYTES + TABLE + 512 /*barriers*/ + 1024 /*align*/;
   static_assert(BT == 256 || (BT == 32 && MODE != RG_WGRAD), "tile widths");
-  static_assert(SMEM <= 227 * 1024, "shared memory");
+  static_assert(SMEM + 1024 /*static*/ <= 227 * 1024, "shared memory");
 };
 
 struct RaggedParams {
@@ -100,8 +106,8 @@ MX_DEVINL Unit unit_of(const RaggedParams& p, const int32_t* ends, const int32_t
     r.f0 = (v % f_tiles) * RG_F;
     r.t0 = (int64_t)(v / f_tiles) * BT;
     r.tn = (int32_t)min((int64_t)BT, p.T - r.t0);
-    r.k0 = r.e ? ends[r.e - 1] : 0;
-    const int32_t rows = ends[r.e] - (int32_t)r.k0;
+    r.k0 = r.e && ends ? ends[r.e - 1] : 0;
+    const int32_t rows = ends ? ends[r.e] - (int32_t)r.k0 : 0;
     r.num_kb = (rows + 63) / 64;
     r.tail = rows - (r.num_kb - 1) * 64;
   } else {
@@ -145,9 +151,10 @@ __global__ void __launch_bounds__(RCfg<MODE, BT>::THREADS, 1)
   uint8_t* sA = smem;
   uint8_t* sB = sA + C::STAGES * C::A_BYTES;
   uint8_t* sEpi = sB + C::STAGES * C::B_BYTES;
-  int32_t* ends = reinterpret_cast<int32_t*>(sEpi + C::EPI_BYTES);
-  int32_t* unit_end = ends + RG_MAX_E;
-  uint64_t* full = reinterpret_cast<uint64_t*>(unit_end + RG_MAX_E);
+  int32_t* s_ends = reinterpret_cast<int32_t*>(sEpi + C::EPI_BYTES);
+  int32_t* unit_end = s_ends + C::ENDS;  // not WGRAD
+  const int32_t* ends = s_ends;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sEpi + C::EPI_BYTES + C::TABLE);
   uint64_t* empty = full + C::STAGES;
   uint64_t* acc_full = empty + C::STAGES;
   uint64_t* acc_empty = acc_full + 2;
@@ -186,9 +193,9 @@ __global__ void __launch_bounds__(RCfg<MODE, BT>::THREADS, 1)
         const int32_t m = __shfl_up_sync(0xFFFFFFFFu, n, o);
         if (lane >= o) n += m;
       }
-      if (in) {
-        ends[e] = v;
-        unit_end[e] = units + n;
+      if (in && e < C::ENDS) {
+        s_ends[e] = v;
+        if (MODE != RG_WGRAD) unit_end[e] = units + n;
       }
       units += __shfl_sync(0xFFFFFFFFu, n, 31);
       prev = __shfl_sync(0xFFFFFFFFu, v, min(31, p.E - 1 - base));
@@ -199,9 +206,6 @@ __global__ void __launch_bounds__(RCfg<MODE, BT>::THREADS, 1)
       s_units = MODE == RG_WGRAD ? p.E * f_tiles * ((p.T + BT - 1) / BT) : ok ? units : 0;
       if (!ok && blockIdx.x == 0) record_error(p.err, MX_ERR_BAD_OFFSETS);
     }
-    __syncwarp();
-    if (!ok && MODE == RG_WGRAD)
-      for (int e = lane; e < p.E; e += 32) ends[e] = 0;  // every group empty: zeros everywhere
   }
   if (warp == 1) { tmem_alloc_pair(tmem_holder, C::TMEM); tmem_relinquish_pair(); }
   tc_fence_before();
@@ -210,6 +214,7 @@ __global__ void __launch_bounds__(RCfg<MODE, BT>::THREADS, 1)
   cluster_sync();  // the peer's barriers exist before any remote arrive or pair copy
   const uint32_t tmem = *tmem_holder;
   const int32_t n_units = s_units;
+  if (MODE == RG_WGRAD) ends = !s_ok ? nullptr /* refused: every group empty, zeros */ : p.E <= C::ENDS ? s_ends : p.offs;
 
   if (warp == 0) {
     // ------------------------------------------------------------ loads
@@ -343,7 +348,7 @@ __global__ void __launch_bounds__(RCfg<MODE, BT>::THREADS, 1)
   } else {
     // ------------------------------------------------------------ epilogue
     const int ew = warp - 2, q = warp & 3, half = ew >> 2;
-    uint8_t* stg = sEpi + ew * 2048;
+    uint8_t* stg = sEpi + ew * C::EPI_WARP;
     int acc = 0; uint32_t acc_phase = 0;
     // WGRAD: row n, column col of the tile, of dw[e]
     auto dw_at = [&](const Unit& t, int32_t n, int32_t col) {
@@ -361,16 +366,15 @@ __global__ void __launch_bounds__(RCfg<MODE, BT>::THREADS, 1)
       }
       if (!warp_wait(&acc_full[acc], acc_phase, p.err)) break;
       tc_fence_after();
-      // every other block of columns: a short tile keeps both warps of a lane
-      // quarter busy, and the halves of a 128-byte line are written together (a
-      // contiguous half each: 724 against 685 us for a store-bound weight gradient)
       constexpr int NC = BT == 32 ? 1 : BT / 64, STEP = NC == 1 ? 1 : 2;
-      constexpr int JB = 64;           // columns from a warp's block to its next
-      const int c_first = half * 32;
-      const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BT + c_first);
-      const int qr = lane >> 2, qc = (lane & 3) * 8;  // this lane's row (of 8) and columns in a 32 x 32 block's stores
-      uint8_t* dst = MODE == RG_WGRAD ? dw_at(t, f + qr, c_first + qc)
-                                      : p.out + ((t.t0 + c_first + qr) * p.F + f + qc) * 2;
+      // columns of the warp's block j: pairs of neighbours in WGRAD (whole
+      // 128-byte lines of a row), every other one else, so that a short tile keeps both
+      // warps of a lane quarter busy
+      auto col_of = [half](int j) { return MODE == RG_WGRAD ? (j >> 1) * 128 + half * 64 + (j & 1) * 32 : (2 * j + half) * 32; };
+      const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BT);
+      const int qr = MODE == RG_WGRAD ? lane >> 3 : lane >> 2;            // this lane's row and columns in a block's stores
+      const int qc = MODE == RG_WGRAD ? (lane & 7) * 8 : (lane & 3) * 8;
+      uint8_t* dst = MODE == RG_WGRAD ? dw_at(t, f + qr, qc) : p.out + ((t.t0 + qr) * p.F + f + qc) * 2;
       // two blocks at a time: both loads in flight and one wait, and few enough
       // registers that nothing spills (four at a time spilled 12 to 88 bytes, which
       // L1, nearly all shared memory here, does not hold: 1.3x the time of a
@@ -380,7 +384,7 @@ __global__ void __launch_bounds__(RCfg<MODE, BT>::THREADS, 1)
       uint32_t r[STEP][32];
 #pragma unroll
       for (int j = 0; j < STEP; ++j)
-        if (c_first + (j0 + j) * JB < t.tn) tmem_ld_32cols(tb + (j0 + j) * JB, r[j]);
+        if (col_of(j0 + j) < t.tn) tmem_ld_32cols(tb + col_of(j0 + j), r[j]);
       tmem_ld_wait();
       if (j0 + STEP == NC) {
         tc_fence_before();
@@ -391,41 +395,49 @@ __global__ void __launch_bounds__(RCfg<MODE, BT>::THREADS, 1)
         }
       }
       if (f >= p.F) continue;
-#pragma unroll
-      for (int j = 0; j < STEP; ++j) {
-        const int c = c_first + (j0 + j) * JB;  // the block's first column of the tile
-        if (c >= t.tn) break;
-        uint32_t w[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          w[i] = f2_to_bf16x2(f2_pack(__uint_as_float(r[j][2 * i]), __uint_as_float(r[j][2 * i + 1])));
+      if (MODE == RG_WGRAD) {
+        // lane: a row of dw, 64 columns of it; through shared memory (16-byte
+        // chunk k of row r at k ^ (r & 7)) so that eight lanes write a row's line
+        const int c = col_of(j0);
+        if (c >= t.tn) continue;
         __syncwarp();
-        if (MODE == RG_WGRAD) {
-          // lane: a row of dw, 32 columns of it; through shared memory (16-byte
-          // chunk k of row r at k ^ (r >> 1 & 3)) so that four lanes write one row
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            *reinterpret_cast<uint4*>(stg + lane * 64 + ((k ^ ((lane >> 1) & 3)) * 16)) =
-                make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
-        } else {
+        for (int j = 0; j < STEP; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              w[i] = f2_to_bf16x2(f2_pack(__uint_as_float(r[j][8 * k + 2 * i]), __uint_as_float(r[j][8 * k + 2 * i + 1])));
+            *reinterpret_cast<uint4*>(stg + lane * 128 + (((j * 4 + k) ^ (lane & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int rr = i * 4 + qr;
+          if (f + i * 4 < p.F && c + qc < t.tn)  // F is a multiple of 8
+            *reinterpret_cast<uint4*>(dst + ((int64_t)i * 4 * p.T + c) * 2) =
+                *reinterpret_cast<const uint4*>(stg + rr * 128 + (((lane & 7) ^ (rr & 7)) * 16));
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < STEP; ++j) {
           // lane: a feature, 32 tokens of it; turned through shared memory
+          const int c = col_of(j0 + j);
+          if (c >= t.tn) break;
+          __syncwarp();
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            *reinterpret_cast<uint16_t*>(stg + (2 * i) * 64 + lane * 2) = (uint16_t)w[i];
-            *reinterpret_cast<uint16_t*>(stg + (2 * i + 1) * 64 + lane * 2) = (uint16_t)(w[i] >> 16);
+            const uint32_t w = f2_to_bf16x2(f2_pack(__uint_as_float(r[j][2 * i]), __uint_as_float(r[j][2 * i + 1])));
+            *reinterpret_cast<uint16_t*>(stg + (2 * i) * 64 + lane * 2) = (uint16_t)w;
+            *reinterpret_cast<uint16_t*>(stg + (2 * i + 1) * 64 + lane * 2) = (uint16_t)(w >> 16);
           }
-        }
-        __syncwarp();
+          __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int rr = i * 8 + qr;
-          if (MODE == RG_WGRAD) {
-            if (f + i * 8 < p.F && c + qc < t.tn)
-              *reinterpret_cast<uint4*>(dst + ((int64_t)i * 8 * p.T + (j0 + j) * JB) * 2) =
-                  *reinterpret_cast<const uint4*>(stg + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) * 16));
-          } else {
+          for (int i = 0; i < 4; ++i) {
+            const int rr = i * 8 + qr;
             if (c + rr < t.tn && f + qc < p.F)
-              *reinterpret_cast<uint4*>(dst + (int64_t)((j0 + j) * JB + i * 8) * p.F * 2) =
+              *reinterpret_cast<uint4*>(dst + (int64_t)(c + i * 8) * p.F * 2) =
                   *reinterpret_cast<const uint4*>(stg + rr * 64 + (lane & 3) * 16);
           }
         }
