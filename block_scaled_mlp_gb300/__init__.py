@@ -119,7 +119,7 @@ def _check(rc: int):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream():
@@ -531,11 +531,19 @@ def linear_bwd(ctx: LinearContext, dout, err: ErrorWord | None = None):
 
 
 # ---------------------------------------------------------------- 8-bit activation checkpoints
+#
+# The calls from here on take a few microseconds on the device at their
+# smallest, less than a binding that builds objects for every argument: each
+# tensor is looked at once, and pointers go as plain integers.
+
+_BF16, _U8, _I8 = torch.bfloat16, torch.uint8, torch.int8
 
 
 class Ckpt8:
     """A bf16 matrix kept in 8 bits: codes int8 [rows, cols], scales uint8
     [rows, cols/32] (one power of two for 32 elements of a row)."""
+
+    __slots__ = ("codes", "scales")
 
     def __init__(self, codes, scales):
         self.codes = codes
@@ -543,8 +551,8 @@ class Ckpt8:
 
     @classmethod
     def empty(cls, rows, cols, device):
-        return cls(torch.empty((rows, cols), dtype=torch.int8, device=device),
-                   torch.empty((rows, cols // 32), dtype=torch.uint8, device=device))
+        return cls(torch.empty((rows, cols), dtype=_I8, device=device),
+                   torch.empty((rows, cols // 32), dtype=_U8, device=device))
 
     @property
     def shape(self):
@@ -554,58 +562,65 @@ class Ckpt8:
         return self.codes.numel() + self.scales.numel()
 
 
-def _need_ckpt(ck, shape, name):
+def _need_ckpt(ck, rows, cols, name):
     if not isinstance(ck, Ckpt8):
         raise MxError(1, f"{name} must be a Ckpt8")
-    _need(ck.codes, torch.int8, f"{name}.codes")
-    _need(ck.scales, torch.uint8, f"{name}.scales")
-    if tuple(ck.codes.shape) != tuple(shape) or ck.scales.shape != (shape[0], shape[1] // 32):
-        raise MxError(1, f"{name} must be a checkpoint of a {list(shape)} matrix, got {list(ck.codes.shape)}")
+    _need(ck.codes, _I8, f"{name}.codes")
+    _need(ck.scales, _U8, f"{name}.scales")
+    if ck.codes.shape != (rows, cols) or ck.scales.shape != (rows, cols // 32):
+        raise MxError(1, f"{name} must be a checkpoint of a {[rows, cols]} matrix, got {list(ck.codes.shape)}")
 
 
 def _need2d(t, name, shape=None):
-    _need(t, torch.bfloat16, name)
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
-        raise MxError(1, f"{name} must be a {'2-d' if shape is None else list(shape)} matrix, got {list(t.shape)}")
+    """Checks a contiguous bf16 matrix on the device and returns its shape."""
+    _need(t, _BF16, name)
+    got = t.shape
+    if len(got) != 2 or (shape is not None and got != shape):
+        raise MxError(1, f"{name} must be a {'2-d' if shape is None else list(shape)} matrix, got {list(got)}")
+    return got
 
 
 def ckpt8_save(x):
     """8-bit checkpoint of a bf16 [rows, cols] matrix (cols % 32 == 0)."""
-    _need2d(x, "x")
-    ck = Ckpt8.empty(x.shape[0], x.shape[1], x.device)
-    _check(lib().mx_ckpt8_save(_ptr(x), x.shape[0], x.shape[1], _ptr(ck.codes), _ptr(ck.scales), _stream()))
+    rows, cols = _need2d(x, "x")
+    ck = Ckpt8.empty(rows, cols, x.device)
+    _check(lib().mx_ckpt8_save(x.data_ptr(), rows, cols, ck.codes.data_ptr(), ck.scales.data_ptr(), _stream()))
     return ck
 
 
 def ckpt8_load(ck: Ckpt8):
     """The bf16 matrix that a checkpoint holds."""
-    _need_ckpt(ck, ck.shape if isinstance(ck, Ckpt8) else (0, 0), "ck")
-    x = torch.empty(ck.codes.shape, dtype=torch.bfloat16, device=ck.codes.device)
-    _check(lib().mx_ckpt8_load(_ptr(ck.codes), _ptr(ck.scales), x.shape[0], x.shape[1], _ptr(x), _stream()))
+    if not isinstance(ck, Ckpt8) or ck.codes.dim() != 2:
+        raise MxError(1, "ck must be a Ckpt8")
+    rows, cols = ck.codes.shape
+    _need_ckpt(ck, rows, cols, "ck")
+    x = torch.empty((rows, cols), dtype=_BF16, device=ck.codes.device)
+    _check(lib().mx_ckpt8_load(ck.codes.data_ptr(), ck.scales.data_ptr(), rows, cols, x.data_ptr(), _stream()))
     return x
 
 
 def swiglu_ckpt8_fwd(h13):
     """y = silu(g) u [M, h] in bf16 and the 8-bit checkpoint of h13 [M, 2h] = [g | u]."""
-    _need2d(h13, "h13")
-    M, h = h13.shape[0], h13.shape[1] // 2
-    if h13.shape[1] % 64:
-        raise MxError(4, f"h13 must have 2h columns with h a multiple of 32, got {h13.shape[1]}")
-    y = torch.empty((M, h), dtype=torch.bfloat16, device=h13.device)
-    ck = Ckpt8.empty(M, 2 * h, h13.device)
-    _check(lib().mx_swiglu_ckpt8_fwd(_ptr(h13), M, h, _ptr(y), _ptr(ck.codes), _ptr(ck.scales), _stream()))
+    M, h2 = _need2d(h13, "h13")
+    if h2 % 64:
+        raise MxError(4, f"h13 must have 2h columns with h a multiple of 32, got {h2}")
+    dev = h13.device
+    y = torch.empty((M, h2 // 2), dtype=_BF16, device=dev)
+    ck = Ckpt8.empty(M, h2, dev)
+    _check(lib().mx_swiglu_ckpt8_fwd(h13.data_ptr(), M, h2 // 2, y.data_ptr(), ck.codes.data_ptr(),
+                                     ck.scales.data_ptr(), _stream()))
     return y, ck
 
 
 def swiglu_ckpt8_bwd(dy, ck: Ckpt8, y=True):
     """(dh13 [M, 2h], y [M, h]) from dy [M, h] and the checkpoint of h13; y is
     computed again from the checkpoint (None with y=False)."""
-    _need2d(dy, "dy")
-    M, h = dy.shape
-    _need_ckpt(ck, (M, 2 * h), "ck")
-    dh13 = torch.empty((M, 2 * h), dtype=torch.bfloat16, device=dy.device)
-    out = torch.empty((M, h), dtype=torch.bfloat16, device=dy.device) if y else None
-    _check(lib().mx_swiglu_ckpt8_bwd(_ptr(dy), _ptr(ck.codes), _ptr(ck.scales), M, h, _ptr(dh13), _ptr(out), _stream()))
+    M, h = _need2d(dy, "dy")
+    _need_ckpt(ck, M, 2 * h, "ck")
+    dh13 = torch.empty((M, 2 * h), dtype=_BF16, device=dy.device)
+    out = torch.empty_like(dy) if y else None
+    _check(lib().mx_swiglu_ckpt8_bwd(dy.data_ptr(), ck.codes.data_ptr(), ck.scales.data_ptr(), M, h, dh13.data_ptr(),
+                                     _ptr(out), _stream()))
     return dh13, out
 
 
@@ -619,58 +634,56 @@ def add_rmsnorm_fwd(x, w, residual=None, eps=1e-5, y=True, axis=0, layout=SCALE_
     residual), rstd [M] fp32, y [M, d] bf16 (y=True), the MXFP8 codes and
     scales of y as quantize() names them (axis), ckpt: a Ckpt8 of r
     (ckpt=True); what was not asked for is None."""
-    _need2d(x, "x")
-    M, d = x.shape
-    _need(w, torch.bfloat16, "w")
+    M, d = shape = _need2d(x, "x")
+    _need(w, _BF16, "w")
     if w.shape != (d,):
         raise MxError(1, f"w must be [{d}], got {list(w.shape)}")
-    if residual is not None:
-        _need2d(residual, "residual", (M, d))
     dev = x.device
-    out = dict(r=x, rstd=torch.empty(M, dtype=torch.float32, device=dev), y=None, q_row=None, s_row=None, q_col=None,
-               s_col=None, ckpt=None)
+    r, r_ptr, res_ptr = x, None, None
     if residual is not None:
-        out["r"] = torch.empty_like(x)
-    if y:
-        out["y"] = torch.empty_like(x)
+        _need2d(residual, "residual", shape)
+        r = torch.empty_like(x)
+        r_ptr, res_ptr = r.data_ptr(), residual.data_ptr()
+    rstd = torch.empty(M, dtype=torch.float32, device=dev)
+    out_y = torch.empty_like(x) if y else None
+    q_row = s_row = q_col = s_col = ck = ck_codes = ck_scales = None
     if axis & ROW:
-        out["q_row"] = torch.empty((M, d), dtype=torch.uint8, device=dev)
-        out["s_row"] = _scales(M, d, layout, dev)
+        q_row, s_row = torch.empty((M, d), dtype=_U8, device=dev), _scales(M, d, layout, dev)
     if axis & COL:
-        out["q_col"] = torch.empty((d, M), dtype=torch.uint8, device=dev)
-        out["s_col"] = _scales(d, M, layout, dev)
-    ck = out["ckpt"] = Ckpt8.empty(M, d, dev) if ckpt else None
-    _check(lib().mx_add_rmsnorm_fwd(_ptr(x), _ptr(residual), _ptr(w), M, d, eps,
-                                    None if residual is None else _ptr(out["r"]), _ptr(out["rstd"]), _ptr(out["y"]), axis,
-                                    layout, scale_mode, _ptr(out["q_row"]), _ptr(out["s_row"]), _ptr(out["q_col"]),
-                                    _ptr(out["s_col"]), _ptr(ck.codes) if ckpt else None,
-                                    _ptr(ck.scales) if ckpt else None, _stream()))
-    return out
+        q_col, s_col = torch.empty((d, M), dtype=_U8, device=dev), _scales(d, M, layout, dev)
+    if ckpt:
+        ck = Ckpt8.empty(M, d, dev)
+        ck_codes, ck_scales = ck.codes.data_ptr(), ck.scales.data_ptr()
+    _check(lib().mx_add_rmsnorm_fwd(x.data_ptr(), res_ptr, w.data_ptr(), M, d, eps, r_ptr, rstd.data_ptr(), _ptr(out_y),
+                                    axis, layout, scale_mode, _ptr(q_row), _ptr(s_row), _ptr(q_col), _ptr(s_col),
+                                    ck_codes, ck_scales, _stream()))
+    return dict(r=r, rstd=rstd, y=out_y, q_row=q_row, s_row=s_row, q_col=q_col, s_col=s_col, ckpt=ck)
 
 
 def add_rmsnorm_bwd(dy, saved, rstd, w, dres=None):
     """(dx [M, d], dw [d]) of add_rmsnorm_fwd from dy [M, d], the saved r (bf16,
     or its Ckpt8), rstd and w; dres [M, d] is the gradient that reaches r on
     the residual path.  dx is the gradient of x and of the residual."""
-    _need2d(dy, "dy")
-    M, d = dy.shape
-    ck = saved if isinstance(saved, Ckpt8) else None
-    if ck is not None:
-        _need_ckpt(ck, (M, d), "saved")
+    M, d = shape = _need2d(dy, "dy")
+    r = ck_codes = ck_scales = None
+    if isinstance(saved, Ckpt8):
+        _need_ckpt(saved, M, d, "saved")
+        ck_codes, ck_scales = saved.codes.data_ptr(), saved.scales.data_ptr()
     else:
-        _need2d(saved, "saved", (M, d))
-    _need(w, torch.bfloat16, "w")
+        _need2d(saved, "saved", shape)
+        r = saved.data_ptr()
+    _need(w, _BF16, "w")
     _need(rstd, torch.float32, "rstd")
     if w.shape != (d,) or rstd.shape != (M,):
         raise MxError(1, f"w must be [{d}] and rstd [{M}], got {list(w.shape)} and {list(rstd.shape)}")
     if dres is not None:
-        _need2d(dres, "dres", (M, d))
+        _need2d(dres, "dres", shape)
+    L = lib()
     dx = torch.empty_like(dy)
-    dw = torch.empty(d, dtype=torch.bfloat16, device=dy.device)
-    ws = torch.empty(max(lib().mx_add_rmsnorm_bwd_workspace(M, d), 16), dtype=torch.uint8, device=dy.device)
-    _check(lib().mx_add_rmsnorm_bwd(_ptr(dy), None if ck else _ptr(saved), _ptr(ck.codes) if ck else None,
-                                    _ptr(ck.scales) if ck else None, _ptr(rstd), _ptr(w), _ptr(dres), M, d, _ptr(dx),
-                                    _ptr(dw), _ptr(ws), _stream()))
+    dw = torch.empty_like(w)
+    ws = torch.empty(max(L.mx_add_rmsnorm_bwd_workspace(M, d), 16), dtype=_U8, device=dy.device)
+    _check(L.mx_add_rmsnorm_bwd(dy.data_ptr(), r, ck_codes, ck_scales, rstd.data_ptr(), w.data_ptr(), _ptr(dres), M, d,
+                                dx.data_ptr(), dw.data_ptr(), ws.data_ptr(), _stream()))
     return dx, dw
 
 
@@ -679,8 +692,8 @@ def add_rmsnorm_bwd(dy, saved, rstd, w, dres=None):
 
 def _ragged(mode, a, b, offs, shape, M, N, K, err):
     _need(offs, torch.int32, "offs")
-    c = torch.empty(shape, dtype=torch.bfloat16, device=a.device)
-    _check(lib().mx_ragged_mm(mode, _ptr(a), _ptr(b), M, N, K, _ptr(offs), offs.numel(), _ptr(c),
+    c = torch.empty(shape, dtype=_BF16, device=a.device)
+    _check(lib().mx_ragged_mm(mode, a.data_ptr(), b.data_ptr(), M, N, K, offs.data_ptr(), offs.numel(), c.data_ptr(),
                               err.ptr() if err else None, _stream()))
     return c
 

@@ -29,9 +29,8 @@ __global__ void __launch_bounds__(C8_THREADS)
     ckpt8_save_kernel(const uint4* __restrict__ x, int64_t n8, uint2* __restrict__ codes, uint8_t* __restrict__ scales) {
   const int64_t i = (int64_t)blockIdx.x * C8_THREADS + threadIdx.x;
   const bool in = i < n8;   // whole blocks: four lanes together
-  float v[8];
-  unpack8(in ? ld_once(x + i) : make_uint4(0, 0, 0, 0), v);
-  const uint32_t s = ckpt8_scale(block_amax(v));
+  const uint4 v = in ? ld_once(x + i) : make_uint4(0, 0, 0, 0);
+  const uint32_t s = ckpt8_block_scale(v);
   if (!in) return;
   codes[i] = ckpt8_encode(v, s);
   if ((threadIdx.x & 3) == 0) scales[i >> 2] = (uint8_t)s;
@@ -80,12 +79,12 @@ __global__ void __launch_bounds__(C8_THREADS) swiglu_ckpt8_fwd_kernel(SwigluCkpt
   float g[8], u[8], y[8];
   const uint4 z = make_uint4(0, 0, 0, 0);
   const uint4 gp = in ? ld_once(p.h13 + gi) : z, up = in ? ld_once(p.h13 + ui) : z;
+  const uint32_t sg = ckpt8_block_scale(gp), su = ckpt8_block_scale(up);
+  if (!in) return;
+  p.codes[gi] = ckpt8_encode(gp, sg);
+  p.codes[ui] = ckpt8_encode(up, su);
   unpack8(gp, g);
   unpack8(up, u);
-  const uint32_t sg = ckpt8_scale(block_amax(g)), su = ckpt8_scale(block_amax(u));
-  if (!in) return;
-  p.codes[gi] = ckpt8_encode(g, sg);
-  p.codes[ui] = ckpt8_encode(u, su);
   if ((threadIdx.x & 3) == 0) {
     p.scales[gi >> 2] = (uint8_t)sg;
     p.scales[ui >> 2] = (uint8_t)su;

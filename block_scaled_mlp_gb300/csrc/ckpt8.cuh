@@ -14,24 +14,61 @@
 #pragma once
 
 #include "common.cuh"
+#include "tile_quant.cuh"
 
 namespace mx {
 
-// |x| as bits, so that the integer maximum orders NaN above infinity above
-// every number.
-MX_DEVINL uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+// Products and sums straight from the halves of packed bf16 pairs: the two
+// elements of a times those of b in fp32 (exact), their squares added to c, and
+// the two elements times a power of two plus c (one rounding).
+MX_DEVINL f2 mul_bf16x2(uint32_t a, uint32_t b) {
+  f2 r;
+  asm("{\n .reg .b16 al, ah, bl, bh;\n mov.b32 {al, ah}, %2;\n mov.b32 {bl, bh}, %3;\n"
+      " fma.rn.f32.bf16 %0, al, bl, 0f80000000;\n fma.rn.f32.bf16 %1, ah, bh, 0f80000000;\n}"
+      : "=f"(r.x), "=f"(r.y)
+      : "r"(a), "r"(b));
+  return r;
+}
+MX_DEVINL void sumsq_bf16x2(uint32_t a, f2& c) {
+  asm("{\n .reg .b16 al, ah;\n mov.b32 {al, ah}, %2;\n"
+      " fma.rn.f32.bf16 %0, al, al, %0;\n fma.rn.f32.bf16 %1, ah, ah, %1;\n}"
+      : "+f"(c.x), "+f"(c.y)
+      : "r"(a));
+}
+MX_DEVINL f2 scale_add_bf16x2(uint32_t a, uint16_t pow2, float c) {
+  f2 r;
+  asm("{\n .reg .b16 al, ah;\n mov.b32 {al, ah}, %2;\n"
+      " fma.rn.f32.bf16 %0, al, %3, %4;\n fma.rn.f32.bf16 %1, ah, %3, %4;\n}"
+      : "=f"(r.x), "=f"(r.y)
+      : "r"(a), "h"(pow2), "f"(c));
+  return r;
+}
 
-// Scale byte of a checkpoint block from the fp32 bits of its amax.
+// max(|a|, |b|, |c|); NaN if one is.
+MX_DEVINL float max3_abs(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+MX_DEVINL float max_abs(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
+}
+
+// Scale byte of a checkpoint block from the bf16 bits of its amax (a NaN has
+// the largest exponent field, as infinity does).
 MX_DEVINL uint32_t ckpt8_scale(uint32_t amax) {
-  const uint32_t E = amax >> 23, m = amax & 0x7FFFFFu;
+  const uint32_t E = amax >> 7, m = amax & 0x7Fu;
   if (E == 0xFF) return 0xFF;
-  const int s = (int)E - 6 + (m > 0x7E0000u ? 1 : 0);  // 127 = 1.984375 * 2^6
+  const int s = (int)E - 6 + (m > 0x7Eu ? 1 : 0);  // 127 = 1.984375 * 2^6
   return s < 0 ? 0u : (uint32_t)s;
 }
 
-// E8M0 byte of an MX block from the fp32 bits of its amax (the fp32 form of
+// E8M0 byte of an MX block from its amax (not negative; the fp32 form of
 // e8m0_from_amax_bits: 448 = 1.75 * 2^8).
-MX_DEVINL uint32_t e8m0_from_amax_f32(uint32_t amax, uint32_t rceil) {
+MX_DEVINL uint32_t e8m0_from_amax_f32(float amax_f, uint32_t rceil) {
+  const uint32_t amax = __float_as_uint(amax_f);
   const uint32_t E = amax >> 23, m = amax & 0x7FFFFFu;
   if (E == 0xFF) return 0xFF;
   const int s = (int)E - 8 + ((m > 0x600000u && rceil) ? 1 : 0);
@@ -45,14 +82,23 @@ MX_DEVINL float pow2_of_byte(uint32_t s) {
   return __uint_as_float(s == 0xFF ? 0x7FC00000u : s ? s << 23 : 0x00400000u);
 }
 
-// Four codes RN(x * inv) in one word, element 0 in the lowest byte.  Adding
-// 1.5 * 2^23 rounds the exact product once, to nearest even, into the low
-// bits of the sum.
-MX_DEVINL uint32_t ckpt8_codes4(float a, float b, float c, float d, float inv) {
-  const float big = 12582912.0f;
-  const uint32_t ua = __float_as_uint(__fmaf_rn(a, inv, big)), ub = __float_as_uint(__fmaf_rn(b, inv, big));
-  const uint32_t uc = __float_as_uint(__fmaf_rn(c, inv, big)), ud = __float_as_uint(__fmaf_rn(d, inv, big));
-  return __byte_perm(__byte_perm(ua, ub, 0x0040), __byte_perm(uc, ud, 0x0040), 0x5410);
+// 2^(127 - s) in bf16, for the bytes of finite blocks (0 <= s <= 249).
+MX_DEVINL uint16_t inv_pow2_bf16(uint32_t s) { return (uint16_t)((254u - s) << 7); }
+
+// This lane's eight checkpoint codes RN(x * 2^(127 - s)), element 0 in the
+// lowest byte.  Adding 1.5 * 2^23 rounds the exact product once, to nearest even,
+// into the low bits of the sum.
+MX_DEVINL uint2 ckpt8_encode(const uint4& x, uint32_t s) {
+  if (s == 0xFF) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+  const uint16_t inv = inv_pow2_bf16(s);
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const f2 v = scale_add_bf16x2(w[i], inv, 12582912.0f);
+    h[i] = __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x0040);
+  }
+  return make_uint2(__byte_perm(h[0], h[1], 0x5410), __byte_perm(h[2], h[3], 0x5410));
 }
 
 // Four codes times the block's power of two.  A code's byte with its sign bit
@@ -88,35 +134,41 @@ MX_DEVINL uint4 pack8(const float (&v)[8]) {
   return make_uint4(f2_to_bf16x2(f2_pack(v[0], v[1])), f2_to_bf16x2(f2_pack(v[2], v[3])),
                     f2_to_bf16x2(f2_pack(v[4], v[5])), f2_to_bf16x2(f2_pack(v[6], v[7])));
 }
-
-// amax (as bits) of a 32-element block held by four consecutive lanes, eight
-// elements each.  All 32 lanes take part.
-MX_DEVINL uint32_t block_amax(const float (&v)[8]) {
-  uint32_t m = abs_bits(v[0]);
-#pragma unroll
-  for (int i = 1; i < 8; ++i) m = max(m, abs_bits(v[i]));
-  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-  return max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+MX_DEVINL uint4 pack8(const f2 (&v)[4]) {
+  return make_uint4(f2_to_bf16x2(v[0]), f2_to_bf16x2(v[1]), f2_to_bf16x2(v[2]), f2_to_bf16x2(v[3]));
 }
 
-// This lane's eight checkpoint codes of such a block.
-MX_DEVINL uint2 ckpt8_encode(const float (&v)[8], uint32_t s) {
-  if (s == 0xFF) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-  const float inv = inv_pow2(s);
-  return make_uint2(ckpt8_codes4(v[0], v[1], v[2], v[3], inv), ckpt8_codes4(v[4], v[5], v[6], v[7], inv));
+// Checkpoint scale of a 32-element block held by four consecutive lanes, eight
+// elements each.  All 32 lanes take part.
+MX_DEVINL uint32_t ckpt8_block_scale(const uint4& x) {
+  uint32_t m = maxabs2(maxabs2(x.x, x.y), maxabs2(x.z, x.w));
+  m = maxabs2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+  m = maxabs2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+  return ckpt8_scale(max_halves(m & 0x7FFF7FFFu));
+}
+
+// amax of such a block of fp32 values; NaN if one is.
+MX_DEVINL float block_amax(const f2 (&v)[4]) {
+  float m = max3_abs(v[0].x, v[0].y, v[1].x);
+  m = max3_abs(m, v[1].y, v[2].x);
+  m = max3_abs(m, v[2].y, v[3].x);
+  m = max_abs(m, v[3].y);
+  m = max_abs(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+  return max_abs(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
 }
 
 // This lane's eight E4M3 codes of an MX block (scaling by a power of two is
 // exact, so fp32 values round once; NaN and infinite blocks as in MX).
-MX_DEVINL uint2 mx_encode(const float (&v)[8], uint32_t s) {
+MX_DEVINL uint2 mx_encode(const f2 (&v)[4], uint32_t s) {
   if (s == 0xFF) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-  const float inv = inv_pow2(s);
-  uint32_t w[2];
+  const f2 inv = f2_splat(inv_pow2(s));
+  uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-    w[i] = cvt_e4m3x2(__fmul_rn(v[4 * i], inv), __fmul_rn(v[4 * i + 1], inv)) |
-           (cvt_e4m3x2(__fmul_rn(v[4 * i + 2], inv), __fmul_rn(v[4 * i + 3], inv)) << 16);
-  return make_uint2(w[0], w[1]);
+  for (int i = 0; i < 4; ++i) {
+    const f2 t = f2_mul(v[i], inv);
+    w[i] = cvt_e4m3x2(t.x, t.y);
+  }
+  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
 // Reads of data that is used once, past L1.

@@ -39,24 +39,20 @@ struct NormFwdParams {
   uint32_t rceil;
 };
 
-// r of eight elements: the bf16 sum, packed.
+// r of eight elements: the bf16 sums (rounded once), packed.
 MX_DEVINL uint4 add8(const uint4& a, const uint4& b) {
   const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
   uint32_t o[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = f2_to_bf16x2(f2_add(f2_from_bf16x2(x[i]), f2_from_bf16x2(y[i])));
+  for (int i = 0; i < 4; ++i) asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(x[i]), "r"(y[i]));
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-MX_DEVINL float sumsq8(const uint4& a) {
-  const uint32_t x[4] = {a.x, a.y, a.z, a.w};
-  f2 s = f2_splat(0.0f);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const f2 v = f2_from_bf16x2(x[i]);
-    s = f2_fma(v, v, s);
-  }
-  return s.x + s.y;
+MX_DEVINL void sumsq8(const uint4& a, f2& s) {
+  sumsq_bf16x2(a.x, s);
+  sumsq_bf16x2(a.y, s);
+  sumsq_bf16x2(a.z, s);
+  sumsq_bf16x2(a.w, s);
 }
 
 MX_DEVINL float warp_sum(float v) {
@@ -70,7 +66,7 @@ MX_DEVINL f2 pair_add(f2 a, f2 b) {
   const float s = __fadd_rn(a.x, b.x), t = __fsub_rn(s, a.x);
   const float e = __fadd_rn(__fsub_rn(a.x, __fsub_rn(s, t)), __fsub_rn(b.x, t));  // s + e = a.x + b.x
   const float l = __fadd_rn(e, __fadd_rn(a.y, b.y)), h = __fadd_rn(s, l);
-  return abs_bits(s) < 0x7F800000u ? f2_pack(h, __fsub_rn(l, __fsub_rn(h, s))) : f2_pack(s, 0.0f);
+  return fabsf(s) < __uint_as_float(0x7F800000u) ? f2_pack(h, __fsub_rn(l, __fsub_rn(h, s))) : f2_pack(s, 0.0f);
 }
 template <int FROM>
 MX_DEVINL f2 warp_sum_pair(f2 v) {
@@ -94,16 +90,16 @@ MX_DEVINL f2 rstd_pair(f2 ss, float d, float eps) {
   return f2_pack(n, fabsf(lo) < n ? lo : 0.0f);
 }
 
-// y of eight elements, fp32
-MX_DEVINL void norm8(const uint4& r, f2 n, const uint4& w, float (&y)[8]) {
-  float rv[8], wv[8];
-  unpack8(r, rv);
-  unpack8(w, wv);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float rw = __fmul_rn(rv[i], wv[i]);
-    y[i] = __fmaf_rn(rw, n.x, __fmul_rn(rw, n.y));
-  }
+// y of two and of eight elements, fp32
+MX_DEVINL f2 norm2(uint32_t r, f2 n, uint32_t w) {
+  const f2 rw = mul_bf16x2(r, w);
+  return f2_fma(rw, f2_splat(n.x), f2_mul(rw, f2_splat(n.y)));
+}
+MX_DEVINL void norm8(const uint4& r, f2 n, const uint4& w, f2 (&y)[4]) {
+  y[0] = norm2(r.x, n, w.x);
+  y[1] = norm2(r.y, n, w.y);
+  y[2] = norm2(r.z, n, w.z);
+  y[3] = norm2(r.w, n, w.w);
 }
 
 // ---- rows: one CTA per row, the row in registers (V vectors of eight a
@@ -120,7 +116,7 @@ __global__ void __launch_bounds__(512) add_rmsnorm_row_kernel(NormFwdParams p) {
   if (row >= p.M) return;
   const int64_t base = row * p.d8;
   uint4 v[V];
-  float ss = 0;
+  f2 ss = f2_splat(0.0f);
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     const int c = threadIdx.x + k * T;
@@ -141,10 +137,10 @@ __global__ void __launch_bounds__(512) add_rmsnorm_row_kernel(NormFwdParams p) {
     }
   }
 #pragma unroll
-  for (int k = 0; k < V; ++k) ss += sumsq8(v[k]);
+  for (int k = 0; k < V; ++k) sumsq8(v[k], ss);
   __shared__ f2 part[16];
   const int lane = threadIdx.x & 31;
-  f2 sum = warp_sum_pair<16>(f2_pack(ss, 0.0f));
+  f2 sum = warp_sum_pair<16>(f2_pack(ss.x + ss.y, 0.0f));
   if (lane == 0) part[threadIdx.x >> 5] = sum;
   __syncthreads();
   sum = warp_sum_pair<8>((lane & 15) < (T >> 5) ? part[lane & 15] : f2_splat(0.0f));
@@ -155,15 +151,13 @@ __global__ void __launch_bounds__(512) add_rmsnorm_row_kernel(NormFwdParams p) {
     const int c = threadIdx.x + k * T;
     const bool in = c < p.d8;
     if (p.ck) {
-      float f[8];
-      unpack8(v[k], f);
-      const uint32_t s = ckpt8_scale(block_amax(f));
+      const uint32_t s = ckpt8_block_scale(v[k]);
       if (in) {
-        *reinterpret_cast<uint2*>(p.ck + (base + c) * 8) = ckpt8_encode(f, s);
+        *reinterpret_cast<uint2*>(p.ck + (base + c) * 8) = ckpt8_encode(v[k], s);
         if ((c & 3) == 0) p.ck_s[(base + c) >> 2] = (uint8_t)s;
       }
     }
-    float y[8];
+    f2 y[4];
     norm8(v[k], n, in ? __ldg(p.w + c) : make_uint4(0, 0, 0, 0), y);
     if (p.y && in) p.y[base + c] = pack8(y);
     if (p.q_row) {
@@ -181,15 +175,34 @@ __global__ void __launch_bounds__(512) add_rmsnorm_row_kernel(NormFwdParams p) {
 // bf16; the rows' sums of squares are exchanged through distributed shared
 // memory, so one pass over HBM gives both quantizations (a second kernel for
 // the columns would read r again: 10 bytes an element instead of 8).
+//
+// Row passes: a warp has four rows, a lane eight elements of each, four lanes
+// one block.  Column pass: lanes l and l ^ 16 have rows 0-15 and 16-31 of one
+// column pair (16 rows keep the registers low enough for three CTAs an SM).
+// The tile's 16-byte vectors of rows 16-31 sit at vector index ^ 4, so that the
+// two half-warps of the column pass read different banks.
 constexpr int NC_ROWS = 32;
 constexpr int NC_THREADS = 256;
 constexpr int NC_MAX_CTAS = 8;
 
-size_t nc_smem(int slice8) { return (size_t)NC_ROWS * slice8 * 16; }
+int nc_pitch8(int slice8) { return (slice8 + 7) & ~7; }
+size_t nc_smem(int slice8) { return (size_t)NC_ROWS * nc_pitch8(slice8) * 16; }
 
-__global__ void __launch_bounds__(NC_THREADS) add_rmsnorm_col_kernel(NormFwdParams p, int32_t slice8) {
-  extern __shared__ __align__(16) uint4 tile[];   // [32][slice8]
-  __shared__ __align__(16) f2 part[NC_MAX_CTAS][NC_ROWS];       // sums of squares by CTA and row
+// Scale bytes of row r at columns c, c + step, ...: the first one's address
+// and the distance for eight further columns.
+struct ScaleRow {
+  uint8_t* at;
+  int32_t step8;
+};
+MX_DEVINL ScaleRow scale_row(const ScaleDst& d, int64_t r, int32_t c) {
+  return d.mma ? ScaleRow{d.base + mma_scale_offset(r, c, d.tiles_per_row), 1024} : ScaleRow{d.base + r * d.ld + c, 8};
+}
+
+template <bool RES, bool CK, bool Y, bool ROW>
+__global__ void __launch_bounds__(NC_THREADS, 3) add_rmsnorm_col_kernel(NormFwdParams p, int32_t slice8, int32_t pitch8) {
+  extern __shared__ __align__(16) uint4 tile[];   // [32][pitch8]
+  __shared__ __align__(16) f2 part[NC_MAX_CTAS][NC_ROWS];    // sums of squares by CTA and row
+  __shared__ __align__(16) f2 s_n[NC_ROWS];
   const int rank = (int)cluster_ctarank();
   const int ctas = (int)(gridDim.y);
   const int64_t r0 = (int64_t)blockIdx.x * NC_ROWS;
@@ -201,41 +214,55 @@ __global__ void __launch_bounds__(NC_THREADS) add_rmsnorm_col_kernel(NormFwdPara
   if (p.s_col.mma && rank == ctas - 1) {
     // zeros where the layouts are padded: rows past M, columns past d
     const int S = p.d8 / 4, first = live ? S : 0, cols = ((S + 3) & ~3) - first;
-    if (p.q_row)
+    if (ROW)
       for (int i = threadIdx.x; i < cols * NC_ROWS; i += NC_THREADS) p.s_row.put(r0 + i % NC_ROWS, first + i / NC_ROWS, 0);
     for (int64_t c = (live ? p.d8 * 8 : 0) + threadIdx.x; c < ((p.d8 * 8 + 127) & ~127); c += NC_THREADS)
       p.s_col.put(c, r0 >> 5, 0);
   }
   if (!live) return;  // the whole cluster
 
-  // warp: four rows of the slice
-  float ss[4] = {0, 0, 0, 0};
-  for (int c = lane; c < n8; c += 32) {
+  const int rw = warp * 4;                                       // the warp's first row
+  const int64_t at0 = (r0 + rw) * p.d8 + c0 + lane;              // its first vector
+  uint4* trow = tile + rw * pitch8;
+  const int flip = rw >= 16 ? 4 : 0;
+  const int n8w = (n8 + 31) & ~31;                               // whole warps: the blocks' lanes work together
+  f2 ss[4] = {};
+  for (int cb = 0; cb < n8w; cb += 32) {
+    const int c = cb + lane;
+    const bool in = c < n8;
+    const int64_t at = at0 + cb;
     uint4 v[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = ld_once(p.x + (r0 + warp * 4 + k) * p.d8 + c0 + c);
-    if (p.res) {
+    for (int k = 0; k < 4; ++k) v[k] = in ? ld_once(p.x + at + k * p.d8) : make_uint4(0, 0, 0, 0);
+    if (RES) {
       uint4 a[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) a[k] = ld_once(p.res + (r0 + warp * 4 + k) * p.d8 + c0 + c);
+      for (int k = 0; k < 4; ++k) a[k] = in ? ld_once(p.res + at + k * p.d8) : make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         v[k] = add8(v[k], a[k]);
-        p.r[(r0 + warp * 4 + k) * p.d8 + c0 + c] = v[k];
+        if (in) p.r[at + k * p.d8] = v[k];
       }
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      tile[(warp * 4 + k) * slice8 + c] = v[k];
-      ss[k] += sumsq8(v[k]);
+      sumsq8(v[k], ss[k]);
+      if (in) trow[k * pitch8 + (c ^ flip)] = v[k];
+      if (CK) {
+        const uint32_t s = ckpt8_block_scale(v[k]);
+        if (in) {
+          *reinterpret_cast<uint2*>(p.ck + (at + k * p.d8) * 8) = ckpt8_encode(v[k], s);
+          if ((lane & 3) == 0) p.ck_s[(at + k * p.d8) >> 2] = (uint8_t)s;
+        }
+      }
     }
   }
   f2 sum[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) sum[k] = warp_sum_pair<16>(f2_pack(ss[k], 0.0f));
+  for (int k = 0; k < 4; ++k) sum[k] = warp_sum_pair<16>(f2_pack(ss[k].x + ss[k].y, 0.0f));
   if (lane < ctas) {
     // lane j: this CTA's sums of the warp's rows to CTA j of the cluster
-    const uint32_t dst = cluster_map(smem_u32(&part[rank][warp * 4]), lane);
+    const uint32_t dst = cluster_map(smem_u32(&part[rank][rw]), lane);
 #pragma unroll
     for (int k = 0; k < 4; k += 2)
       asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(dst + k * 8), "f"(sum[k].x), "f"(sum[k].y),
@@ -243,7 +270,6 @@ __global__ void __launch_bounds__(NC_THREADS) add_rmsnorm_col_kernel(NormFwdPara
                    : "memory");
   }
   cluster_sync();  // every CTA's sums are here; the tile is complete too
-  __shared__ f2 s_n[NC_ROWS];
   if (threadIdx.x < NC_ROWS) {
     f2 t = part[0][threadIdx.x];
     for (int j = 1; j < ctas; ++j) t = pair_add(t, part[j][threadIdx.x]);  // the same order in every CTA
@@ -253,70 +279,77 @@ __global__ void __launch_bounds__(NC_THREADS) add_rmsnorm_col_kernel(NormFwdPara
   }
   __syncthreads();
 
-  // rows: each lane eight elements, four lanes a block
-  for (int cb = 0; cb < n8; cb += 32) {
-    const int c = cb + lane;
-    const bool in = c < n8;
-    const uint4 w = in ? __ldg(p.w + c0 + c) : make_uint4(0, 0, 0, 0);
+  // rows
+  if (Y || ROW) {
+    f2 n[4];
+    ScaleRow sr[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int rr = warp * 4 + k;
-      const uint4 v = in ? tile[rr * slice8 + c] : make_uint4(0, 0, 0, 0);
-      const int64_t at = (r0 + rr) * p.d8 + c0 + c;
-      if (p.ck) {
-        float f[8];
-        unpack8(v, f);
-        const uint32_t s = ckpt8_scale(block_amax(f));
-        if (in) {
-          *reinterpret_cast<uint2*>(p.ck + at * 8) = ckpt8_encode(f, s);
-          if ((c & 3) == 0) p.ck_s[at >> 2] = (uint8_t)s;
-        }
-      }
-      float y[8];
-      norm8(v, s_n[rr], w, y);
-      if (p.y && in) p.y[at] = pack8(y);
-      if (p.q_row) {
-        const uint32_t s = e8m0_from_amax_f32(block_amax(y), p.rceil);
-        if (in) {
-          *reinterpret_cast<uint2*>(p.q_row + at * 8) = mx_encode(y, s);
-          if ((c & 3) == 0) p.s_row.put(r0 + rr, (c0 + c) >> 2, s);
+      n[k] = s_n[rw + k];
+      if (ROW) sr[k] = scale_row(p.s_row, r0 + rw + k, (c0 + lane) >> 2);
+    }
+    for (int cb = 0; cb < n8w; cb += 32) {
+      const int c = cb + lane;
+      const bool in = c < n8;
+      const uint4 w = in ? __ldg(p.w + c0 + c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint4 v = in ? trow[k * pitch8 + (c ^ flip)] : make_uint4(0, 0, 0, 0);
+        const int64_t at = at0 + cb + k * p.d8;
+        f2 y[4];
+        norm8(v, n[k], w, y);
+        if (Y && in) p.y[at] = pack8(y);
+        if (ROW) {
+          const uint32_t s = e8m0_from_amax_f32(block_amax(y), p.rceil);
+          if (in) {
+            *reinterpret_cast<uint2*>(p.q_row + at * 8) = mx_encode(y, s);
+            if ((lane & 3) == 0) *sr[k].at = (uint8_t)s;
+          }
+          sr[k].at += sr[k].step8;
         }
       }
     }
   }
 
-  // columns: each thread two adjacent columns, 32 rows (one block each)
-  const uint32_t* words = reinterpret_cast<const uint32_t*>(tile);
+  // columns: 16 pairs a warp at a time
+  const int rh = lane >> 4;
+  const uint32_t* words = reinterpret_cast<const uint32_t*>(tile) + rh * 16 * pitch8 * 4;
   const uint32_t* ww = reinterpret_cast<const uint32_t*>(p.w + c0);
-  for (int pc = threadIdx.x; pc < n8 * 4; pc += NC_THREADS) {
-    const f2 w2 = f2_from_bf16x2(__ldg(ww + pc));
-    f2 y[NC_ROWS];
-    uint32_t ma = 0, mb = 0;
+  const f2* nr = s_n + rh * 16;
+  uint8_t* sc = p.s_col.base + (p.s_col.mma ? ((r0 >> 7) << 9) + ((r0 >> 5) & 3) : r0 >> 5);
+  const bool v8 = ((uintptr_t)p.q_col & 31) == 0;  // rows r0 .. of a column: M and r0 are multiples of 32
+  for (int pb = warp * 16; pb < n8 * 4; pb += NC_THREADS / 2) {
+    const int pc = pb + (lane & 15);                // n8 is a multiple of 4: all 16 pairs exist
+    const uint32_t w = __ldg(ww + pc);
+    const uint32_t* src = words + (pc ^ (rh << 4));
+    f2 y[16];
+    float ma = 0, mb = 0;
 #pragma unroll
-    for (int i = 0; i < NC_ROWS; ++i) {
-      const f2 rw = f2_mul(f2_from_bf16x2(words[i * slice8 * 4 + pc]), w2), n = s_n[i];
-      y[i] = f2_fma(rw, f2_splat(n.x), f2_mul(rw, f2_splat(n.y)));
-      ma = max(ma, abs_bits(y[i].x));
-      mb = max(mb, abs_bits(y[i].y));
+    for (int i = 0; i < 16; i += 2) {
+      const float4 nn = *reinterpret_cast<const float4*>(nr + i);
+      y[i] = norm2(src[i * pitch8 * 4], f2_pack(nn.x, nn.y), w);
+      y[i + 1] = norm2(src[(i + 1) * pitch8 * 4], f2_pack(nn.z, nn.w), w);
+      ma = max3_abs(ma, y[i].x, y[i + 1].x);
+      mb = max3_abs(mb, y[i].y, y[i + 1].y);
     }
+    ma = max_abs(ma, __shfl_xor_sync(0xFFFFFFFFu, ma, 16));
+    mb = max_abs(mb, __shfl_xor_sync(0xFFFFFFFFu, mb, 16));
     const uint32_t sa = e8m0_from_amax_f32(ma, p.rceil), sb = e8m0_from_amax_f32(mb, p.rceil);
     const f2 inv = f2_pack(inv_pow2(sa == 0xFF ? 127u : sa), inv_pow2(sb == 0xFF ? 127u : sb));
-    uint32_t ca[8], cb[8];
+    uint32_t ca[4], cb[4], out[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
       f2 t[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) t[k] = f2_mul(y[4 * i + k], inv);
       ca[i] = sa == 0xFF ? 0x7F7F7F7Fu : cvt_e4m3x2(t[0].x, t[1].x) | (cvt_e4m3x2(t[2].x, t[3].x) << 16);
       cb[i] = sb == 0xFF ? 0x7F7F7F7Fu : cvt_e4m3x2(t[0].y, t[1].y) | (cvt_e4m3x2(t[2].y, t[3].y) << 16);
     }
-    const int64_t col = (int64_t)c0 * 8 + 2 * pc;
-    uint8_t* dst = p.q_col + col * p.M + r0;   // 32-byte aligned if q_col is: M and r0 are multiples of 32
-    const bool v8 = ((uintptr_t)p.q_col & 31) == 0;
-    store32_codes(dst, ca, v8);
-    store32_codes(dst + p.M, cb, v8);
-    p.s_col.put(col, r0 >> 5, sa);
-    p.s_col.put(col + 1, r0 >> 5, sb);
+    col16x2_gather(ca, cb, rh, out);                // lane: all 32 rows of one column
+    const int64_t col = (int64_t)c0 * 8 + 2 * pc + rh;
+    store32_codes(p.q_col + col * p.M + r0, out, v8);
+    sc[p.s_col.mma ? (col >> 7) * p.s_col.tiles_per_row * 512 + (col & 31) * 16 + ((col >> 5) & 3) * 4 : col * p.s_col.ld] =
+        (uint8_t)(rh ? sb : sa);
   }
 }
 
@@ -488,9 +521,8 @@ int launch_add_rmsnorm_fwd(const NormFwdLaunch& a, cudaStream_t stream) {
     // slices of at least 32 columns, as many as a portable cluster has CTAs
     const int slice8 = ((p.d8 + NC_MAX_CTAS - 1) / NC_MAX_CTAS + 3) / 4 * 4;
     const int ctas = (p.d8 + slice8 - 1) / slice8;
+    const int pitch8 = nc_pitch8(slice8);
     const size_t smem = nc_smem(slice8);
-    e = cudaFuncSetAttribute(add_rmsnorm_col_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute");
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(padded / NC_ROWS), (unsigned)ctas);
     cfg.blockDim = dim3(NC_THREADS);
@@ -503,9 +535,18 @@ int launch_add_rmsnorm_fwd(const NormFwdLaunch& a, cudaStream_t stream) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    using Kernel = void (*)(NormFwdParams, int32_t, int32_t);
+    // [residual][checkpoint][bf16 y][row codes]
+#define MX_NC(R, C) {{add_rmsnorm_col_kernel<R, C, false, false>, add_rmsnorm_col_kernel<R, C, false, true>}, \
+                     {add_rmsnorm_col_kernel<R, C, true, false>, add_rmsnorm_col_kernel<R, C, true, true>}}
+    static const Kernel kernels[2][2][2][2] = {{MX_NC(false, false), MX_NC(false, true)},
+                                               {MX_NC(true, false), MX_NC(true, true)}};
+#undef MX_NC
+    const Kernel k = kernels[p.res != nullptr][p.ck != nullptr][p.y != nullptr][p.q_row != nullptr];
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute");
     count_launch(MX_KERNEL_NORM);
-    return cuda_status(cudaLaunchKernelEx(&cfg, add_rmsnorm_col_kernel, p, (int32_t)slice8),
-                       "add_rmsnorm_col_kernel launch");
+    return cuda_status(cudaLaunchKernelEx(&cfg, k, p, (int32_t)slice8, (int32_t)pitch8), "add_rmsnorm_col_kernel launch");
   }
   const int V = vectors_of(p.d8), T = threads_of(p.d8, V);
   count_launch(MX_KERNEL_NORM);
