@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(C8_THREADS)
   const uint4 v = in ? ld_once(x + i) : make_uint4(0, 0, 0, 0);
   const uint32_t s = ckpt8_block_scale(v);
   if (!in) return;
-  codes[i] = ckpt8_encode(v, s);
+  codes[i] = ckpt8_encode(v, inv_pow2_bf16(s));
   if ((threadIdx.x & 3) == 0) scales[i >> 2] = (uint8_t)s;
 }
 
@@ -79,15 +79,15 @@ __global__ void __launch_bounds__(C8_THREADS) swiglu_ckpt8_fwd_kernel(SwigluCkpt
   float g[8], u[8], y[8];
   const uint4 z = make_uint4(0, 0, 0, 0);
   const uint4 gp = in ? ld_once(p.h13 + gi) : z, up = in ? ld_once(p.h13 + ui) : z;
-  const uint32_t sg = ckpt8_block_scale(gp), su = ckpt8_block_scale(up);
+  const uint32_t s2 = ckpt8_block_scales(gp, up), inv2 = inv_pow2_bf16x2(s2);
   if (!in) return;
-  p.codes[gi] = ckpt8_encode(gp, sg);
-  p.codes[ui] = ckpt8_encode(up, su);
+  p.codes[gi] = ckpt8_encode(gp, (uint16_t)inv2);
+  p.codes[ui] = ckpt8_encode(up, (uint16_t)(inv2 >> 16));
   unpack8(gp, g);
   unpack8(up, u);
   if ((threadIdx.x & 3) == 0) {
-    p.scales[gi >> 2] = (uint8_t)sg;
-    p.scales[ui >> 2] = (uint8_t)su;
+    p.scales[gi >> 2] = (uint8_t)s2;
+    p.scales[ui >> 2] = (uint8_t)(s2 >> 16);
   }
 #pragma unroll
   for (int k = 0; k < 8; ++k) y[k] = g[k] * sigmoid_approx(g[k]) * u[k];

@@ -85,12 +85,11 @@ MX_DEVINL float pow2_of_byte(uint32_t s) {
 // 2^(127 - s) in bf16, for the bytes of finite blocks (0 <= s <= 249).
 MX_DEVINL uint16_t inv_pow2_bf16(uint32_t s) { return (uint16_t)((254u - s) << 7); }
 
-// This lane's eight checkpoint codes RN(x * 2^(127 - s)), element 0 in the
-// lowest byte.  Adding 1.5 * 2^23 rounds the exact product once, to nearest even,
-// into the low bits of the sum.
-MX_DEVINL uint2 ckpt8_encode(const uint4& x, uint32_t s) {
-  if (s == 0xFF) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-  const uint16_t inv = inv_pow2_bf16(s);
+// This lane's eight checkpoint codes RN(x * inv), inv a power of two, element
+// 0 in the lowest byte.  Adding 1.5 * 2^23 rounds the exact product once, to
+// nearest even, into the low bits of the sum.  (A NaN or infinite block has
+// inv = -infinity; its codes mean nothing.)
+MX_DEVINL uint2 ckpt8_encode(const uint4& x, uint16_t inv) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   uint32_t h[4];
 #pragma unroll
@@ -138,8 +137,26 @@ MX_DEVINL uint4 pack8(const f2 (&v)[4]) {
   return make_uint4(f2_to_bf16x2(v[0]), f2_to_bf16x2(v[1]), f2_to_bf16x2(v[2]), f2_to_bf16x2(v[3]));
 }
 
-// Checkpoint scale of a 32-element block held by four consecutive lanes, eight
-// elements each.  All 32 lanes take part.
+// Checkpoint scales of two 32-element blocks, each held by four consecutive
+// lanes, eight elements (a, b) each: block a's byte in the low half, b's in the
+// high half.  The bf16 maxima of both travel in one word, and the rule
+// max(((amax + 1) >> 7) - 6, 0) works on both halves at once (the + 1 carries
+// into the exponent exactly for significands above 127/64).  All 32 lanes take part.
+MX_DEVINL uint32_t ckpt8_block_scales(const uint4& a, const uint4& b) {
+  const uint32_t ma = maxabs2(maxabs2(a.x, a.y), maxabs2(a.z, a.w));
+  const uint32_t mb = maxabs2(maxabs2(b.x, b.y), maxabs2(b.z, b.w));
+  uint32_t m = maxabs2(__byte_perm(ma, mb, 0x5410), __byte_perm(ma, mb, 0x7632));
+  m = maxabs2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+  m = maxabs2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2)) & 0x7FFF7FFFu;
+  uint32_t s = __viaddmax_s16x2(((m + 0x00010001u) >> 7) & 0x01FF01FFu, 0xFFFAFFFAu, 0u);
+  const uint32_t bad = (m + 0x00800080u) & 0x80008000u;  // exponent field 255
+  if (bad) s |= (bad >> 15) * 0xFFu;
+  return s;
+}
+// 2^(127 - s) of both blocks, bf16.
+MX_DEVINL uint32_t inv_pow2_bf16x2(uint32_t s2) { return (0x00FE00FEu - (s2 & 0x00FF00FFu)) << 7; }
+
+// The same of one block.
 MX_DEVINL uint32_t ckpt8_block_scale(const uint4& x) {
   uint32_t m = maxabs2(maxabs2(x.x, x.y), maxabs2(x.z, x.w));
   m = maxabs2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
@@ -157,18 +174,39 @@ MX_DEVINL float block_amax(const f2 (&v)[4]) {
   return max_abs(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
 }
 
-// This lane's eight E4M3 codes of an MX block (scaling by a power of two is
-// exact, so fp32 values round once; NaN and infinite blocks as in MX).
+// This lane's eight E4M3 codes of an MX block with scale byte s (scaling by a
+// power of two is exact, so fp32 values round once; a NaN or infinite block
+// has a NaN for its inverse scale and every code 0x7F, as in MX).
 MX_DEVINL uint2 mx_encode(const f2 (&v)[4], uint32_t s) {
-  if (s == 0xFF) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-  const f2 inv = f2_splat(inv_pow2(s));
+  const f2 inv = f2_splat(s == 0xFF ? __uint_as_float(0x7FC00000u) : inv_pow2(s));
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const f2 t = f2_mul(v[i], inv);
     w[i] = cvt_e4m3x2(t.x, t.y);
   }
-  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+  return make_uint2(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410));
+}
+
+// MX scale bytes of two blocks as above (fp32 values): low and high half.  Only
+// max(((bits + up) >> 23) - 8, 0) of the maxima matters, with up = 0x1FFFFF
+// (RCEIL: carries for significands above 1.75) or 0 (FLOOR), and it is
+// monotone, so each lane's own value, 16 bits, is what the lanes exchange.  A
+// lane that holds a NaN or an infinity gives 0x7FFF.
+MX_DEVINL uint32_t mx_block_scales(const f2 (&a)[4], const f2 (&b)[4], uint32_t up) {
+  auto key = [up](const f2 (&v)[4]) {
+    float m = max3_abs(v[0].x, v[0].y, v[1].x);
+    m = max3_abs(m, v[1].y, v[2].x);
+    m = max3_abs(m, v[2].y, v[3].x);
+    const uint32_t bits = __float_as_uint(max_abs(m, v[3].y));
+    return bits >= 0x7F800000u ? 0x7FFFu : (bits + up) >> 23;
+  };
+  uint32_t k = __byte_perm(key(a), key(b), 0x5410);
+  k = __vmaxs2(k, __shfl_xor_sync(0xFFFFFFFFu, k, 1));
+  k = __vmaxs2(k, __shfl_xor_sync(0xFFFFFFFFu, k, 2));
+  uint32_t s = __viaddmax_s16x2(k, 0xFFF8FFF8u, 0u);
+  if (s & 0x7F007F00u) s |= ((s >> 8) & 0x00010001u) * 0xFFu;
+  return s & 0x00FF00FFu;
 }
 
 // Reads of data that is used once, past L1.

@@ -151,9 +151,9 @@ struct NormBwdLaunch {
   int64_t M, d;
   void* dx;               // [M, d] bf16
   void* dw;               // [d] bf16
-  void* workspace;        // norm_bwd_ctas(M) * d floats
+  void* workspace;        // norm_bwd_ctas(M, d) * d floats
 };
-int norm_bwd_ctas(int64_t M);
+int norm_bwd_ctas(int64_t M, int64_t d);
 int launch_add_rmsnorm_bwd(const NormBwdLaunch& a, cudaStream_t stream);
 
 // ---------------------------------------------------------------- 8-bit checkpoints

@@ -70,7 +70,7 @@ int mx_add_rmsnorm_fwd(const void* x, const void* residual, const void* w, int64
 
 size_t mx_add_rmsnorm_bwd_workspace(int64_t M, int64_t d) {
   if (M <= 0 || d <= 0 || d > kNormMaxD) return 0;
-  return (size_t)norm_bwd_ctas(M) * (size_t)d * 4;
+  return (size_t)norm_bwd_ctas(M, d) * (size_t)d * 4;
 }
 
 int mx_add_rmsnorm_bwd(const void* dy, const void* r, const void* ck_codes, const void* ck_scales, const float* rstd,
