@@ -187,8 +187,14 @@ __global__ void __launch_bounds__(512) add_rmsnorm_row_kernel(NormFwdParams p) {
 // two half-warps of the column pass read different banks.
 constexpr int NC_ROWS = 32;
 constexpr int NC_THREADS = 256;
-constexpr int NC_MAX_CTAS = 8;
+constexpr int NC_MAX_CTAS = 16;
+constexpr int NC_CTAS_SM = 3;
 
+
+MX_DEVINL void copy_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+MX_DEVINL void copy_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Scale bytes of row r at columns c, c + step, ...: the first one's address
 // and the distance for eight further columns.
@@ -201,7 +207,7 @@ MX_DEVINL ScaleRow scale_row(const ScaleDst& d, int64_t r, int32_t c) {
 }
 
 template <bool RES, bool CK, bool Y, bool ROW>
-__global__ void __launch_bounds__(NC_THREADS, 3) add_rmsnorm_col_kernel(NormFwdParams p, int32_t slice8) {
+__global__ void __launch_bounds__(NC_THREADS, NC_CTAS_SM) add_rmsnorm_col_kernel(NormFwdParams p, int32_t slice8) {
   extern __shared__ __align__(16) uint4 tile[];   // [32][slice8]
   __shared__ __align__(16) f2 part[NC_MAX_CTAS][NC_ROWS];    // sums of squares by CTA and row
   __shared__ __align__(16) f2 s_n[NC_ROWS];
@@ -227,28 +233,42 @@ __global__ void __launch_bounds__(NC_THREADS, 3) add_rmsnorm_col_kernel(NormFwdP
   const int64_t at0 = (r0 + rw) * p.d8 + c0 + lane;              // its first vector
   uint4* trow = tile + rw * slice8 + (lane ^ (rw >= 16 ? 4 : 0));
   f2 ss[4] = {};
-  // 32 vectors of four rows; IN: all of them exist
-  auto load_rows = [&](int cb, auto all) {
-    const bool in = decltype(all)::value || cb + lane < n8;
+  // x goes to the tile by asynchronous copies, all of them in flight at once;
+  // the residual's vectors are loaded one step ahead
+  const int steps = (n8 + 31) / 32;
+  for (int i = 0; i < steps; ++i)
+    if (i * 32 + lane < n8) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) copy_async16(trow + k * slice8 + i * 32, p.x + at0 + i * 32 + k * p.d8);
+    }
+  uint4 a[4];
+  auto load_res = [&](int cb) {
+    if (RES && cb + lane < n8) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) a[k] = ld_once(p.res + at0 + cb + k * p.d8);
+    }
+  };
+  load_res(0);
+  copy_async_wait_all();  // a lane reads only what it copied itself
+  for (int cb = 0; cb < n8; cb += 32) {
+    const bool in = cb + lane < n8;
     const int64_t at = at0 + cb;
     uint4 v[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = in ? ld_once(p.x + at + k * p.d8) : make_uint4(0, 0, 0, 0);
+    for (int k = 0; k < 4; ++k) v[k] = in ? trow[k * slice8 + cb] : make_uint4(0, 0, 0, 0);
     if (RES) {
-      uint4 a[4];
+      if (in) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) a[k] = in ? ld_once(p.res + at + k * p.d8) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        v[k] = add8(v[k], a[k]);
-        if (in) p.r[at + k * p.d8] = v[k];
+        for (int k = 0; k < 4; ++k) {
+          v[k] = add8(v[k], a[k]);
+          trow[k * slice8 + cb] = v[k];
+          p.r[at + k * p.d8] = v[k];
+        }
       }
+      load_res(cb + 32);
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      sumsq8(v[k], ss[k]);
-      if (in) trow[k * slice8 + cb] = v[k];
-    }
+    for (int k = 0; k < 4; ++k) sumsq8(v[k], ss[k]);
     if (CK) {
 #pragma unroll
       for (int k = 0; k < 4; k += 2) {
@@ -264,10 +284,8 @@ __global__ void __launch_bounds__(NC_THREADS, 3) add_rmsnorm_col_kernel(NormFwdP
         }
       }
     }
-  };
+  }
   const int n8_all = n8 & ~31;
-  for (int cb = 0; cb < n8_all; cb += 32) load_rows(cb, std::true_type{});
-  if (n8_all < n8) load_rows(n8_all, std::false_type{});
   f2 sum[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) sum[k] = warp_sum_pair<16>(f2_pack(ss[k].x + ss[k].y, 0.0f));
@@ -593,9 +611,12 @@ int launch_add_rmsnorm_fwd(const NormFwdLaunch& a, cudaStream_t stream) {
   if (padded > INT32_MAX) return fail(MX_ERR_UNSUPPORTED, "norm: too many rows");
   cudaError_t e;
   if (a.q_col) {
-    // slices of a multiple of 256 columns (whole warps), as many as a portable
-    // cluster has CTAs
-    const int slice8 = ((p.d8 + 31) / 32 + NC_MAX_CTAS - 1) / NC_MAX_CTAS * 32;
+    // Slices of a multiple of 256 columns (whole warps): eight CTAs, sixteen
+    // where slices would pass 1024 columns (their tile then leaves an SM one CTA: 4096 x
+    // 16384, 189 us on eight, 133 on sixteen; 16384 x 7168, 217 on seven, 221 to 253
+    // on fourteen).
+    const int most = p.d8 > 8 * 128 ? 16 : 8;
+    const int slice8 = ((p.d8 + 31) / 32 + most - 1) / most * 32;
     const int ctas = (p.d8 + slice8 - 1) / slice8;
     const size_t smem = (size_t)NC_ROWS * slice8 * 16;
     cudaLaunchConfig_t cfg = {};
@@ -620,6 +641,10 @@ int launch_add_rmsnorm_fwd(const NormFwdLaunch& a, cudaStream_t stream) {
     const Kernel k = kernels[p.res != nullptr][p.ck != nullptr][p.y != nullptr][p.q_row != nullptr];
     e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute");
+    if (ctas > 8) {
+      e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute");
+    }
     count_launch(MX_KERNEL_NORM);
     return cuda_status(cudaLaunchKernelEx(&cfg, k, p, (int32_t)slice8), "add_rmsnorm_col_kernel launch");
   }
