@@ -25,25 +25,38 @@ constexpr int C8_THREADS = 256;
 // overflows to infinity below g = -88.7 and s is 0 there.
 MX_DEVINL float sigmoid_approx(float g) { return __frcp_rn(1.0f + __expf(-g)); }
 
+// A thread has vectors i and i + C8_THREADS of its CTA's 2 * C8_THREADS.
 __global__ void __launch_bounds__(C8_THREADS)
     ckpt8_save_kernel(const uint4* __restrict__ x, int64_t n8, uint2* __restrict__ codes, uint8_t* __restrict__ scales) {
-  const int64_t i = (int64_t)blockIdx.x * C8_THREADS + threadIdx.x;
-  const bool in = i < n8;   // whole blocks: four lanes together
-  const uint4 v = in ? ld_once(x + i) : make_uint4(0, 0, 0, 0);
-  const uint32_t s = ckpt8_block_scale(v);
-  if (!in) return;
-  codes[i] = ckpt8_encode(v, inv_pow2_bf16(s));
-  if ((threadIdx.x & 3) == 0) scales[i >> 2] = (uint8_t)s;
+  const int64_t i = (int64_t)blockIdx.x * (2 * C8_THREADS) + threadIdx.x, j = i + C8_THREADS;
+  const uint4 z = make_uint4(0, 0, 0, 0);
+  const uint4 a = i < n8 ? ld_once(x + i) : z, b = j < n8 ? ld_once(x + j) : z;  // whole blocks: four lanes together
+  const uint32_t s2 = ckpt8_block_scales(a, b), inv2 = inv_pow2_bf16x2(s2);
+  if (i < n8) {
+    codes[i] = ckpt8_encode(a, (uint16_t)inv2);
+    if ((threadIdx.x & 3) == 0) scales[i >> 2] = (uint8_t)s2;
+  }
+  if (j < n8) {
+    codes[j] = ckpt8_encode(b, (uint16_t)(inv2 >> 16));
+    if ((threadIdx.x & 3) == 0) scales[j >> 2] = (uint8_t)(s2 >> 16);
+  }
 }
 
 __global__ void __launch_bounds__(C8_THREADS)
     ckpt8_load_kernel(const uint2* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t n8,
                       uint4* __restrict__ x) {
-  const int64_t i = (int64_t)blockIdx.x * C8_THREADS + threadIdx.x;
+  const int64_t i = (int64_t)blockIdx.x * (2 * C8_THREADS) + threadIdx.x, j = i + C8_THREADS;
   if (i >= n8) return;
+  const bool two = j < n8;
+  const uint2 a = ld_once(codes + i), b = two ? ld_once(codes + j) : make_uint2(0, 0);
+  const uint32_t sa = scales[i >> 2], sb = two ? scales[j >> 2] : 0;
   float v[8];
-  values8(ld_once(codes + i), pow2_of_byte(scales[i >> 2]), v);
+  values8(a, pow2_of_byte(sa), v);
   x[i] = pack8(v);
+  if (two) {
+    values8(b, pow2_of_byte(sb), v);
+    x[j] = pack8(v);
+  }
 }
 
 struct SwigluCkptParams {
@@ -122,8 +135,8 @@ __global__ void __launch_bounds__(C8_THREADS) swiglu_ckpt8_bwd_kernel(SwigluCkpt
   if (p.y) p.y[i] = pack8(y);
 }
 
-int grid_of(int64_t n8, unsigned* grid) {
-  const int64_t b = (n8 + C8_THREADS - 1) / C8_THREADS;
+int grid_of(int64_t n8, int per_thread, unsigned* grid) {
+  const int64_t b = (n8 + per_thread * C8_THREADS - 1) / (per_thread * C8_THREADS);
   if (b > INT32_MAX) return fail(MX_ERR_UNSUPPORTED, "8-bit checkpoint: too many elements");
   *grid = (unsigned)b;
   return MX_OK;
@@ -134,7 +147,7 @@ int grid_of(int64_t n8, unsigned* grid) {
 int launch_ckpt8_save(const void* x, int64_t rows, int64_t cols, void* codes, void* scales, cudaStream_t stream) {
   const int64_t n8 = rows * (cols / 8);
   unsigned grid;
-  if (int rc = grid_of(n8, &grid)) return rc;
+  if (int rc = grid_of(n8, 2, &grid)) return rc;
   count_launch(MX_KERNEL_CKPT8);
   ckpt8_save_kernel<<<grid, C8_THREADS, 0, stream>>>((const uint4*)x, n8, (uint2*)codes, (uint8_t*)scales);
   return cuda_status(cudaGetLastError(), "ckpt8_save_kernel launch");
@@ -143,7 +156,7 @@ int launch_ckpt8_save(const void* x, int64_t rows, int64_t cols, void* codes, vo
 int launch_ckpt8_load(const void* codes, const void* scales, int64_t rows, int64_t cols, void* x, cudaStream_t stream) {
   const int64_t n8 = rows * (cols / 8);
   unsigned grid;
-  if (int rc = grid_of(n8, &grid)) return rc;
+  if (int rc = grid_of(n8, 2, &grid)) return rc;
   count_launch(MX_KERNEL_CKPT8);
   ckpt8_load_kernel<<<grid, C8_THREADS, 0, stream>>>((const uint2*)codes, (const uint8_t*)scales, n8, (uint4*)x);
   return cuda_status(cudaGetLastError(), "ckpt8_load_kernel launch");
@@ -155,7 +168,7 @@ int launch_swiglu_ckpt8_fwd(const void* h13, int64_t M, int64_t h, void* y, void
   p.h13 = (const uint4*)h13; p.y = (uint4*)y; p.codes = (uint2*)codes; p.scales = (uint8_t*)scales;
   p.n8 = M * (h / 8); p.h8 = (uint32_t)(h / 8);
   unsigned grid;
-  if (int rc = grid_of(p.n8, &grid)) return rc;
+  if (int rc = grid_of(p.n8, 1, &grid)) return rc;
   count_launch(MX_KERNEL_CKPT8);
   swiglu_ckpt8_fwd_kernel<<<grid, C8_THREADS, 0, stream>>>(p);
   return cuda_status(cudaGetLastError(), "swiglu_ckpt8_fwd_kernel launch");
@@ -169,7 +182,7 @@ int launch_swiglu_ckpt8_bwd(const void* dy, const void* codes, const void* scale
   p.dh13 = (uint4*)dh13; p.y = (uint4*)y;
   p.n8 = M * (h / 8); p.h8 = (uint32_t)(h / 8);
   unsigned grid;
-  if (int rc = grid_of(p.n8, &grid)) return rc;
+  if (int rc = grid_of(p.n8, 1, &grid)) return rc;
   count_launch(MX_KERNEL_CKPT8);
   swiglu_ckpt8_bwd_kernel<<<grid, C8_THREADS, 0, stream>>>(p);
   return cuda_status(cudaGetLastError(), "swiglu_ckpt8_bwd_kernel launch");

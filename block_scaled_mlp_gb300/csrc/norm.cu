@@ -150,25 +150,41 @@ __global__ void __launch_bounds__(512) add_rmsnorm_row_kernel(NormFwdParams p) {
   sum = warp_sum_pair<8>((lane & 15) < (T >> 5) ? part[lane & 15] : f2_splat(0.0f));
   const f2 n = rstd_pair(sum, p.d, p.eps);
   if (threadIdx.x == 0) p.rstd[row] = n.x + n.y;
+  const uint32_t up = p.rceil ? 0x1FFFFFu : 0u;
+  // two vectors of the row at a time (V = 1: one, and zeros), so that two
+  // blocks share the scales' exchange
 #pragma unroll
-  for (int k = 0; k < V; ++k) {
-    const int c = threadIdx.x + k * T;
-    const bool in = c < p.d8;
+  for (int k = 0; k < V; k += 2) {
+    const int c0 = threadIdx.x + k * T, c1 = c0 + T;
+    const bool in0 = c0 < p.d8, in1 = V > 1 && c1 < p.d8;
+    const uint4 z = make_uint4(0, 0, 0, 0), v0 = v[k], v1 = V > 1 ? v[k + (V > 1)] : z;
     if (p.ck) {
-      const uint32_t s = ckpt8_block_scale(v[k]);
-      if (in) {
-        *reinterpret_cast<uint2*>(p.ck + (base + c) * 8) = ckpt8_encode(v[k], inv_pow2_bf16(s));
-        if ((c & 3) == 0) p.ck_s[(base + c) >> 2] = (uint8_t)s;
+      const uint32_t s2 = ckpt8_block_scales(v0, v1), inv2 = inv_pow2_bf16x2(s2);
+      if (in0) {
+        reinterpret_cast<uint2*>(p.ck)[base + c0] = ckpt8_encode(v0, (uint16_t)inv2);
+        if ((c0 & 3) == 0) p.ck_s[(base + c0) >> 2] = (uint8_t)s2;
+      }
+      if (in1) {
+        reinterpret_cast<uint2*>(p.ck)[base + c1] = ckpt8_encode(v1, (uint16_t)(inv2 >> 16));
+        if ((c1 & 3) == 0) p.ck_s[(base + c1) >> 2] = (uint8_t)(s2 >> 16);
       }
     }
-    f2 y[4];
-    norm8(v[k], n, in ? __ldg(p.w + c) : make_uint4(0, 0, 0, 0), y);
-    if (p.y && in) p.y[base + c] = pack8(y);
+    f2 y0[4], y1[4];
+    norm8(v0, n, in0 ? __ldg(p.w + c0) : z, y0);
+    norm8(v1, n, in1 ? __ldg(p.w + c1) : z, y1);
+    if (p.y) {
+      if (in0) p.y[base + c0] = pack8(y0);
+      if (in1) p.y[base + c1] = pack8(y1);
+    }
     if (p.q_row) {
-      const uint32_t s = e8m0_from_amax_f32(block_amax(y), p.rceil);
-      if (in) {
-        *reinterpret_cast<uint2*>(p.q_row + (base + c) * 8) = mx_encode(y, s);
-        if ((c & 3) == 0) p.s_row.put(row, c >> 2, s);
+      const uint32_t s2 = mx_block_scales(y0, y1, up);
+      if (in0) {
+        reinterpret_cast<uint2*>(p.q_row)[base + c0] = mx_encode(y0, s2 & 0xFF);
+        if ((c0 & 3) == 0) p.s_row.put(row, c0 >> 2, s2 & 0xFF);
+      }
+      if (in1) {
+        reinterpret_cast<uint2*>(p.q_row)[base + c1] = mx_encode(y1, s2 >> 16);
+        if ((c1 & 3) == 0) p.s_row.put(row, c1 >> 2, s2 >> 16);
       }
     }
   }
@@ -563,15 +579,15 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const float* __restrict__
   if (x == 0 && blockIdx.x * 32 + g0 < d) dw[blockIdx.x * 32 + g0] = __float2bfloat16_rn(t);
 }
 
-// Vectors of eight a thread holds of a row.
-int vectors_of(int d8) { return d8 <= 256 ? 1 : d8 <= 512 ? 2 : 4; }
+// Vectors of eight a thread holds of a row.  With rows enough to fill the device, four beyond 512 (16384 x
+// 7168 without a residual: 86 us, 114 with two); with fewer rows than SMs, two up to 1024 (more
+// threads a row: 3.2 against 3.4 us for one row of 7168).
+int vectors_of(int64_t M, int d8) { return d8 <= 256 ? 1 : d8 <= 512 || (d8 <= 1024 && M <= num_sms()) ? 2 : 4; }
 int threads_of(int d8, int V) { return ((d8 + V - 1) / V + 31) / 32 * 32; }
 
-// Backward: vectors and threads; CTAs an SM (NBX_THREADS threads' worth, while two stages of
-// their rows fit); ring stages.
-#ifndef NBX_THREADS
-#define NBX_THREADS 896
-#endif
+// Backward: vectors and threads; CTAs an SM (896 threads' worth, while two stages of
+// their rows fit: with 512 or 1344 the backward pass of 16384 x 7168 from a checkpoint took
+// 235 or 174 us, not 150); ring stages.
 struct NormBwdShape {
   int V, T, ctas, stages, stage_bytes;
 };
@@ -582,7 +598,7 @@ NormBwdShape bwd_shape(int64_t d, bool ck, bool dres) {
   s.T = threads_of(d8, s.V);
   s.stage_bytes = (int)((d * (2 + (ck ? 1 : 2) + (dres ? 2 : 0)) + 127) / 128 * 128);
   const int smem = 220 * 1024;
-  s.ctas = std::max(1, std::min(8, NBX_THREADS / s.T));
+  s.ctas = std::max(1, std::min(8, 896 / s.T));
   while (s.ctas > 1 && (smem / s.ctas - 1024) / s.stage_bytes < 2) --s.ctas;
   s.stages = std::min(NB_MAX_STAGES, (smem / s.ctas - 1024) / s.stage_bytes);
   return s;
@@ -648,7 +664,7 @@ int launch_add_rmsnorm_fwd(const NormFwdLaunch& a, cudaStream_t stream) {
     count_launch(MX_KERNEL_NORM);
     return cuda_status(cudaLaunchKernelEx(&cfg, k, p, (int32_t)slice8), "add_rmsnorm_col_kernel launch");
   }
-  const int V = vectors_of(p.d8), T = threads_of(p.d8, V);
+  const int V = vectors_of(a.M, p.d8), T = threads_of(p.d8, V);
   count_launch(MX_KERNEL_NORM);
   if (V == 1) add_rmsnorm_row_kernel<1><<<(unsigned)padded, T, 0, stream>>>(p);
   else if (V == 2) add_rmsnorm_row_kernel<2><<<(unsigned)padded, T, 0, stream>>>(p);
