@@ -23,7 +23,7 @@ constexpr int C8_THREADS = 256;
 // s = 1 / (1 + e^-g) by the approximate exponential and reciprocal (a few
 // units of 2^-23: far below the bf16 rounding of every result).  e^-g
 // overflows to infinity below g = -88.7 and s is 0 there.
-MX_DEVINL float sigmoid_approx(float g) { return __frcp_rn(1.0f + __expf(-g)); }
+MX_DEVINL float sigmoid_approx(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
 
 // A thread has vectors i and i + C8_THREADS of its CTA's 2 * C8_THREADS.
 __global__ void __launch_bounds__(C8_THREADS)
@@ -82,57 +82,91 @@ MX_DEVINL void row_col(int64_t i, uint32_t h8, bool narrow, int64_t& row, uint32
   }
 }
 
-__global__ void __launch_bounds__(C8_THREADS) swiglu_ckpt8_fwd_kernel(SwigluCkptParams p) {
-  const int64_t i = (int64_t)blockIdx.x * C8_THREADS + threadIdx.x;
-  const bool in = i < p.n8;
+// Both kernels: SW vectors a thread, C8_THREADS apart, all loads before the
+// first use.
+constexpr int SW = 2;
+
+struct SwigluAt {
+  int64_t i;    // vector of the [M, h] matrices; of g and of u in [M, 2h]
+  int64_t gi, ui;
+  bool in;
+};
+MX_DEVINL SwigluAt swiglu_at(const SwigluCkptParams& p, int k) {
+  SwigluAt a;
+  a.i = (int64_t)blockIdx.x * (SW * C8_THREADS) + k * C8_THREADS + threadIdx.x;
+  a.in = a.i < p.n8;
   int64_t row;
   uint32_t c;
-  row_col(in ? i : 0, p.h8, p.n8 <= 0xFFFFFFFFll, row, c);
-  const int64_t gi = row * 2 * p.h8 + c, ui = gi + p.h8;
-  float g[8], u[8], y[8];
-  const uint4 z = make_uint4(0, 0, 0, 0);
-  const uint4 gp = in ? ld_once(p.h13 + gi) : z, up = in ? ld_once(p.h13 + ui) : z;
-  const uint32_t s2 = ckpt8_block_scales(gp, up), inv2 = inv_pow2_bf16x2(s2);
-  if (!in) return;
-  p.codes[gi] = ckpt8_encode(gp, (uint16_t)inv2);
-  p.codes[ui] = ckpt8_encode(up, (uint16_t)(inv2 >> 16));
-  unpack8(gp, g);
-  unpack8(up, u);
-  if ((threadIdx.x & 3) == 0) {
-    p.scales[gi >> 2] = (uint8_t)s2;
-    p.scales[ui >> 2] = (uint8_t)(s2 >> 16);
+  row_col(a.in ? a.i : 0, p.h8, p.n8 <= 0xFFFFFFFFll, row, c);
+  a.gi = row * 2 * p.h8 + c;
+  a.ui = a.gi + p.h8;
+  return a;
+}
+
+__global__ void __launch_bounds__(C8_THREADS) swiglu_ckpt8_fwd_kernel(SwigluCkptParams p) {
+  SwigluAt at[SW];
+  uint4 gp[SW], up[SW];
+#pragma unroll
+  for (int k = 0; k < SW; ++k) {
+    at[k] = swiglu_at(p, k);
+    const uint4 z = make_uint4(0, 0, 0, 0);
+    gp[k] = at[k].in ? ld_once(p.h13 + at[k].gi) : z;
+    up[k] = at[k].in ? ld_once(p.h13 + at[k].ui) : z;
   }
 #pragma unroll
-  for (int k = 0; k < 8; ++k) y[k] = g[k] * sigmoid_approx(g[k]) * u[k];
-  p.y[i] = pack8(y);
+  for (int k = 0; k < SW; ++k) {
+    const uint32_t s2 = ckpt8_block_scales(gp[k], up[k]), inv2 = inv_pow2_bf16x2(s2);
+    if (!at[k].in) continue;
+    p.codes[at[k].gi] = ckpt8_encode(gp[k], (uint16_t)inv2);
+    p.codes[at[k].ui] = ckpt8_encode(up[k], (uint16_t)(inv2 >> 16));
+    if ((threadIdx.x & 3) == 0) {
+      p.scales[at[k].gi >> 2] = (uint8_t)s2;
+      p.scales[at[k].ui >> 2] = (uint8_t)(s2 >> 16);
+    }
+    float g[8], u[8], y[8];
+    unpack8(gp[k], g);
+    unpack8(up[k], u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = g[i] * sigmoid_approx(g[i]) * u[i];
+    p.y[at[k].i] = pack8(y);
+  }
 }
 
 __global__ void __launch_bounds__(C8_THREADS) swiglu_ckpt8_bwd_kernel(SwigluCkptParams p) {
-  const int64_t i = (int64_t)blockIdx.x * C8_THREADS + threadIdx.x;
-  if (i >= p.n8) return;
-  int64_t row;
-  uint32_t c;
-  row_col(i, p.h8, p.n8 <= 0xFFFFFFFFll, row, c);
-  const int64_t gi = row * 2 * p.h8 + c, ui = gi + p.h8;
-  const uint4 dp = ld_once(p.dy + i);
-  const uint2 gc = ld_once(p.codes + gi), uc = ld_once(p.codes + ui);
-  const uint32_t sg = p.scales[gi >> 2], su = p.scales[ui >> 2];
-  float g[8], u[8], dy[8], y[8];
-  unpack8(dp, dy);
-  values8(gc, pow2_of_byte(sg), g);
-  values8(uc, pow2_of_byte(su), u);
+  SwigluAt at[SW];
+  uint4 dp[SW];
+  uint2 gc[SW], uc[SW];
+  uint32_t sg[SW], su[SW];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const float s = sigmoid_approx(g[k]);
-    const float a = g[k] * s;
-    const float dg = dy[k] * u[k] * (s + a * (1.0f - s));
-    y[k] = a * u[k];
-    u[k] = dy[k] * a;
-    g[k] = dg;
+  for (int k = 0; k < SW; ++k) {
+    at[k] = swiglu_at(p, k);
+    if (!at[k].in) continue;
+    dp[k] = ld_once(p.dy + at[k].i);
+    gc[k] = ld_once(p.codes + at[k].gi);
+    uc[k] = ld_once(p.codes + at[k].ui);
+    sg[k] = p.scales[at[k].gi >> 2];
+    su[k] = p.scales[at[k].ui >> 2];
   }
-  p.dh13[gi] = pack8(g);
-  p.dh13[ui] = pack8(u);
-  if (p.y) p.y[i] = pack8(y);
+#pragma unroll
+  for (int k = 0; k < SW; ++k) {
+    if (!at[k].in) continue;
+    float g[8], u[8], dy[8], y[8];
+    unpack8(dp[k], dy);
+    values8(gc[k], pow2_of_byte(sg[k]), g);
+    values8(uc[k], pow2_of_byte(su[k]), u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float s = sigmoid_approx(g[i]);
+      const float a = g[i] * s;
+      const float dg = dy[i] * u[i] * (s + a * (1.0f - s));
+      y[i] = a * u[i];
+      u[i] = dy[i] * a;
+      g[i] = dg;
+    }
+    p.dh13[at[k].gi] = pack8(g);
+    p.dh13[at[k].ui] = pack8(u);
+    if (p.y) p.y[at[k].i] = pack8(y);
+  }
 }
 
 int grid_of(int64_t n8, int per_thread, unsigned* grid) {
@@ -168,7 +202,7 @@ int launch_swiglu_ckpt8_fwd(const void* h13, int64_t M, int64_t h, void* y, void
   p.h13 = (const uint4*)h13; p.y = (uint4*)y; p.codes = (uint2*)codes; p.scales = (uint8_t*)scales;
   p.n8 = M * (h / 8); p.h8 = (uint32_t)(h / 8);
   unsigned grid;
-  if (int rc = grid_of(p.n8, 1, &grid)) return rc;
+  if (int rc = grid_of(p.n8, SW, &grid)) return rc;
   count_launch(MX_KERNEL_CKPT8);
   swiglu_ckpt8_fwd_kernel<<<grid, C8_THREADS, 0, stream>>>(p);
   return cuda_status(cudaGetLastError(), "swiglu_ckpt8_fwd_kernel launch");
@@ -182,7 +216,7 @@ int launch_swiglu_ckpt8_bwd(const void* dy, const void* codes, const void* scale
   p.dh13 = (uint4*)dh13; p.y = (uint4*)y;
   p.n8 = M * (h / 8); p.h8 = (uint32_t)(h / 8);
   unsigned grid;
-  if (int rc = grid_of(p.n8, 1, &grid)) return rc;
+  if (int rc = grid_of(p.n8, SW, &grid)) return rc;
   count_launch(MX_KERNEL_CKPT8);
   swiglu_ckpt8_bwd_kernel<<<grid, C8_THREADS, 0, stream>>>(p);
   return cuda_status(cudaGetLastError(), "swiglu_ckpt8_bwd_kernel launch");
