@@ -354,94 +354,97 @@ __global__ void __launch_bounds__(RCfg<MODE, BT>::THREADS, 1)
     auto dw_at = [&](const Unit& t, int32_t n, int32_t col) {
       return p.out + (((int64_t)t.e * p.F + n) * p.T + t.t0 + col) * 2;
     };
+    constexpr int NC = BT == 32 ? 1 : BT / 64, STEP = NC == 1 ? 1 : 2;
+    // columns of the warp's block j: pairs of neighbours in WGRAD (whole
+    // 128-byte lines of a row), every other one else, so that a short tile keeps both
+    // warps of a lane quarter busy
+    auto col_of = [half](int j) { return MODE == RG_WGRAD ? (j >> 1) * 128 + half * 64 + (j & 1) * 32 : (2 * j + half) * 32; };
+    const int qr = MODE == RG_WGRAD ? lane >> 3 : lane >> 2;            // this lane's row and columns in a block's stores
+    const int qc = MODE == RG_WGRAD ? (lane & 7) * 8 : (lane & 3) * 8;
+    // FWD, DGRAD: a block of 32 tokens from column c of the tile on; a lane has
+    // one feature of all of them: turned through shared memory
+    auto store_tokens = [&](const Unit& t, int32_t f, int c, const uint32_t (&r)[32]) {
+      uint8_t* dst = p.out + ((t.t0 + c + qr) * p.F + f + qc) * 2;
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t v = f2_to_bf16x2(f2_pack(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])));
+        *reinterpret_cast<uint16_t*>(stg + (2 * i) * 64 + lane * 2) = (uint16_t)v;
+        *reinterpret_cast<uint16_t*>(stg + (2 * i + 1) * 64 + lane * 2) = (uint16_t)(v >> 16);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c + i * 8 + qr < t.tn && f + qc < p.F)
+          *reinterpret_cast<uint4*>(dst + (int64_t)(i * 8) * p.F * 2) =
+              *reinterpret_cast<const uint4*>(stg + (i * 8 + qr) * 64 + (lane & 3) * 16);
+    };
     for (int32_t u = unit0; u < n_units; u += ustep) {
       const Unit t = unit_of<MODE, BT>(p, ends, unit_end, u);
       const int32_t f = t.f0 + rank * 128 + q * 32;   // this warp's features
       if (t.num_kb == 0) {                            // WGRAD: an empty group's zeros
         for (int c = half; c * 32 < t.tn; c += 2)
-          for (int i = 0; i < 4; ++i)
-            if (f + i * 8 < p.F && c * 32 + (lane & 3) * 8 < t.tn)
-              *reinterpret_cast<uint4*>(dw_at(t, f + i * 8 + (lane >> 2), c * 32 + (lane & 3) * 8)) = make_uint4(0, 0, 0, 0);
+          for (int j = 0; j < 4; ++j)
+            if (f + j * 8 < p.F && c * 32 + (lane & 3) * 8 < t.tn)
+              *reinterpret_cast<uint4*>(dw_at(t, f + j * 8 + (lane >> 2), c * 32 + (lane & 3) * 8)) = make_uint4(0, 0, 0, 0);
         continue;
       }
       if (!warp_wait(&acc_full[acc], acc_phase, p.err)) break;
       tc_fence_after();
-      constexpr int NC = BT == 32 ? 1 : BT / 64, STEP = NC == 1 ? 1 : 2;
-      // columns of the warp's block j: pairs of neighbours in WGRAD (whole
-      // 128-byte lines of a row), every other one else, so that a short tile keeps both
-      // warps of a lane quarter busy
-      auto col_of = [half](int j) { return MODE == RG_WGRAD ? (j >> 1) * 128 + half * 64 + (j & 1) * 32 : (2 * j + half) * 32; };
       const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BT);
-      const int qr = MODE == RG_WGRAD ? lane >> 3 : lane >> 2;            // this lane's row and columns in a block's stores
-      const int qc = MODE == RG_WGRAD ? (lane & 7) * 8 : (lane & 3) * 8;
-      uint8_t* dst = MODE == RG_WGRAD ? dw_at(t, f + qr, qc) : p.out + ((t.t0 + qr) * p.F + f + qc) * 2;
       // two blocks at a time: both loads in flight and one wait, and few enough
       // registers that nothing spills (four at a time spilled 12 to 88 bytes, which
-      // L1, nearly all shared memory here, does not hold: 1.3x the time of a
-      // store-bound weight gradient)
+      // L1, nearly all shared memory here, does not hold: 1169 against 683 us for
+      // a store-bound weight gradient)
 #pragma unroll 1
       for (int j0 = 0; j0 < NC; j0 += STEP) {
-      uint32_t r[STEP][32];
-#pragma unroll
-      for (int j = 0; j < STEP; ++j)
-        if (col_of(j0 + j) < t.tn) tmem_ld_32cols(tb + col_of(j0 + j), r[j]);
-      tmem_ld_wait();
-      if (j0 + STEP == NC) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (rank != 0) mbar_arrive_cluster_relaxed(cluster_map(smem_u32(&acc_empty[acc]), 0));
-          else mbar_arrive(&acc_empty[acc]);
-        }
-      }
-      if (f >= p.F) continue;
-      if (MODE == RG_WGRAD) {
-        // lane: a row of dw, 64 columns of it; through shared memory (16-byte
-        // chunk k of row r at k ^ (r & 7)) so that eight lanes write a row's line
-        const int c = col_of(j0);
-        if (c >= t.tn) continue;
-        __syncwarp();
+        uint32_t r[STEP][32];
 #pragma unroll
         for (int j = 0; j < STEP; ++j)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              w[i] = f2_to_bf16x2(f2_pack(__uint_as_float(r[j][8 * k + 2 * i]), __uint_as_float(r[j][8 * k + 2 * i + 1])));
-            *reinterpret_cast<uint4*>(stg + lane * 128 + (((j * 4 + k) ^ (lane & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int rr = i * 4 + qr;
-          if (f + i * 4 < p.F && c + qc < t.tn)  // F is a multiple of 8
-            *reinterpret_cast<uint4*>(dst + ((int64_t)i * 4 * p.T + c) * 2) =
-                *reinterpret_cast<const uint4*>(stg + rr * 128 + (((lane & 7) ^ (rr & 7)) * 16));
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < STEP; ++j) {
-          // lane: a feature, 32 tokens of it; turned through shared memory
-          const int c = col_of(j0 + j);
-          if (c >= t.tn) break;
+          if (col_of(j0 + j) < t.tn) tmem_ld_32cols(tb + col_of(j0 + j), r[j]);
+        tmem_ld_wait();
+        if (j0 + STEP == NC) {
+          tc_fence_before();
           __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const uint32_t w = f2_to_bf16x2(f2_pack(__uint_as_float(r[j][2 * i]), __uint_as_float(r[j][2 * i + 1])));
-            *reinterpret_cast<uint16_t*>(stg + (2 * i) * 64 + lane * 2) = (uint16_t)w;
-            *reinterpret_cast<uint16_t*>(stg + (2 * i + 1) * 64 + lane * 2) = (uint16_t)(w >> 16);
-          }
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int rr = i * 8 + qr;
-            if (c + rr < t.tn && f + qc < p.F)
-              *reinterpret_cast<uint4*>(dst + (int64_t)(c + i * 8) * p.F * 2) =
-                  *reinterpret_cast<const uint4*>(stg + rr * 64 + (lane & 3) * 16);
+          if (lane == 0) {
+            if (rank != 0) mbar_arrive_cluster_relaxed(cluster_map(smem_u32(&acc_empty[acc]), 0));
+            else mbar_arrive(&acc_empty[acc]);
           }
         }
-      }
+        if (f >= p.F) continue;
+        if (MODE == RG_WGRAD) {
+          // lane: a row of dw, 64 columns of it; through shared memory (16-byte
+          // chunk k of row r at k ^ (r & 7)) so that eight lanes write a row's line
+          const int c = col_of(j0);
+          if (c >= t.tn) continue;
+          uint8_t* dst = dw_at(t, f + qr, c + qc);
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < STEP; ++j)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t v[4];
+#pragma unroll
+              for (int l = 0; l < 4; ++l)
+                v[l] = f2_to_bf16x2(f2_pack(__uint_as_float(r[j][8 * k + 2 * l]), __uint_as_float(r[j][8 * k + 2 * l + 1])));
+              *reinterpret_cast<uint4*>(stg + lane * 128 + (((j * 4 + k) ^ (lane & 7)) * 16)) = make_uint4(v[0], v[1], v[2], v[3]);
+            }
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int rr = k * 4 + qr;
+            if (f + k * 4 < p.F && c + qc < t.tn)  // F is a multiple of 8
+              *reinterpret_cast<uint4*>(dst + (int64_t)k * 4 * p.T * 2) =
+                  *reinterpret_cast<const uint4*>(stg + rr * 128 + (((lane & 7) ^ (rr & 7)) * 16));
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < STEP; ++j) {
+            const int c = col_of(j0 + j);
+            if (c >= t.tn) break;
+            store_tokens(t, f, c, r[j]);
+          }
+        }
       }
       if (++acc == 2) { acc = 0; acc_phase ^= 1; }
     }

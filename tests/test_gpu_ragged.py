@@ -64,6 +64,12 @@ def test_products(counts, N, K):
     _check(counts, 0, N, K, sum(counts) + N)
 
 
+@pytest.mark.parametrize("counts", [[1], [8, 0, 3], [33, 1], [64, 64, 64], [300, 17], [257, 0, 600, 31]])
+@pytest.mark.parametrize("N,K", [(1032, 2056), (4096, 512), (264, 4096)])
+def test_few_tiles_and_long_contractions(counts, N, K):
+    _check(counts, 3, N, K, sum(counts) + K)
+
+
 @pytest.mark.parametrize("counts,spare,N,K", [([5, 9, 0, 2], 77, 128, 256), ([0, 0], 40, 64, 64), ([700, 20], 1, 512, 320),
                                               ([3] * 40, 5, 136, 200), ([0] * 7, 9, 40, 24)])
 def test_spare_rows_are_zero(counts, spare, N, K):
