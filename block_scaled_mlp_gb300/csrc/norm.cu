@@ -6,9 +6,8 @@
 //   dw = sum over rows of dy r n
 //
 // Sums are fp32; n is kept as an unevaluated pair of fp32 values and r w is
-// exact in fp32 (two bf16 factors), so y is the fp32 value nearest to r w n
-// and is then rounded to E4M3 or to bf16.  With n and y rounded step by step,
-// two to four times as many codes fell on the other side of a tie.  The sum r is what the model carries on in bf16, so the norm is taken of the rounded
+// exact in fp32 (two bf16 factors), and y keeps enough of r w n that the codes
+// and the bf16 values are r w n rounded once (see norm2).  The sum r is what the model carries on in bf16, so the norm is taken of the rounded
 // value, the one that the backward pass has.  All kernels are bound by HBM:
 // each input is read once and each output written once, a row staying in
 // registers or shared memory between its two uses.
@@ -94,10 +93,17 @@ MX_DEVINL f2 rstd_pair(f2 ss, float d, float eps) {
   return f2_pack(n, fabsf(lo) < n ? lo : 0.0f);
 }
 
-// y of two and of eight elements, fp32
+// y of two and of eight elements, fp32, rounded to odd: truncated, and the last
+// bit set (r w n is hardly ever a 24-bit number).  Such a value lies on the same
+// side of every E4M3 and bf16 tie as r w n itself, so the rounding that follows
+// is that of r w n, where an fp32 value to nearest lands on the tie itself once
+// in a million times and goes to the even side (of 117 million codes 69 to 71 differed
+// from the 64-bit result, now 14 to 33, by the last bits of the sums).
+// Zero becomes 2^-149, which rounds to a zero code and a zero bf16.
 MX_DEVINL f2 norm2(uint32_t r, f2 n, uint32_t w) {
   const f2 rw = mul_bf16x2(r, w);
-  return f2_fma(rw, f2_splat(n.x), f2_mul(rw, f2_splat(n.y)));
+  const f2 y = __ffma2_rz(rw, f2_splat(n.x), f2_mul(rw, f2_splat(n.y)));
+  return f2_pack(__uint_as_float(__float_as_uint(y.x) | 1u), __uint_as_float(__float_as_uint(y.y) | 1u));
 }
 MX_DEVINL void norm8(const uint4& r, f2 n, const uint4& w, f2 (&y)[4]) {
   y[0] = norm2(r.x, n, w.x);
