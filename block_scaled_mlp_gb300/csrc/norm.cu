@@ -558,6 +558,7 @@ __global__ void __launch_bounds__(T_MAX, CTAS) add_rmsnorm_bwd_kernel(NormBwdPar
     }
     if (++stage == p.stages) { stage = 0; phase ^= 1; }
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     const int c = threadIdx.x + k * T;
@@ -573,6 +574,7 @@ __global__ void __launch_bounds__(T_MAX, CTAS) add_rmsnorm_bwd_kernel(NormBwdPar
 __global__ void __launch_bounds__(1024) norm_dw_kernel(const float* __restrict__ part, int32_t G, int32_t d,
                                                        __nv_bfloat16* __restrict__ dw) {
   __shared__ float s[32][33];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials of the kernel before
   const int x = threadIdx.x & 31, g0 = threadIdx.x >> 5, c = blockIdx.x * 32 + x;
   float t = 0;
   if (c < d) {
@@ -699,9 +701,21 @@ int launch_add_rmsnorm_bwd(const NormBwdLaunch& a, cudaStream_t stream) {
   k<<<G, s.T, smem, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_status(e, "add_rmsnorm_bwd_kernel launch");
+  // the sums' kernel is launched while the last CTAs still work, and waits for
+  // them on the device (8192 x 4096: 37.1 -> 36.1 us, one row: 5.5 -> 4.9)
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((a.d + 31) / 32));
+  cfg.blockDim = dim3(1024);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   count_launch(MX_KERNEL_NORM);
-  norm_dw_kernel<<<(unsigned)((a.d + 31) / 32), 1024, 0, stream>>>(p.part, G, (int32_t)a.d, (__nv_bfloat16*)a.dw);
-  return cuda_status(cudaGetLastError(), "norm_dw_kernel launch");
+  return cuda_status(cudaLaunchKernelEx(&cfg, norm_dw_kernel, (const float*)p.part, (int32_t)G, (int32_t)a.d,
+                                        (__nv_bfloat16*)a.dw),
+                     "norm_dw_kernel launch");
 }
 
 }  // namespace mx
