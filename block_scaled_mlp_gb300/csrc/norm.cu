@@ -204,13 +204,14 @@ __global__ void __launch_bounds__(512) add_rmsnorm_row_kernel(NormFwdParams p) {
 //
 // Row passes: a warp has four rows, a lane eight elements of each, four lanes
 // one block.  Column pass: lanes l and l ^ 16 have rows 0-15 and 16-31 of one
-// column pair (16 rows keep the registers low enough for three CTAs an SM).
+// column pair (16 rows keep the registers low enough for four CTAs an SM, where the
+// tiles leave room: 8192 x 4096, 60 us against 68 with three).
 // The tile's 16-byte vectors of rows 16-31 sit at vector index ^ 4, so that the
 // two half-warps of the column pass read different banks.
 constexpr int NC_ROWS = 32;
 constexpr int NC_THREADS = 256;
 constexpr int NC_MAX_CTAS = 16;
-constexpr int NC_CTAS_SM = 3;
+constexpr int NC_CTAS_SM = 4;
 
 
 MX_DEVINL void copy_async16(void* dst, const void* src) {
@@ -635,12 +636,16 @@ int launch_add_rmsnorm_fwd(const NormFwdLaunch& a, cudaStream_t stream) {
   if (padded > INT32_MAX) return fail(MX_ERR_UNSUPPORTED, "norm: too many rows");
   cudaError_t e;
   if (a.q_col) {
-    // Slices of a multiple of 256 columns (whole warps): eight CTAs, sixteen
-    // where slices would pass 1024 columns (their tile then leaves an SM one CTA: 4096 x
-    // 16384, 189 us on eight, 133 on sixteen; 16384 x 7168, 217 on seven, 221 to 253
-    // on fourteen).
-    const int most = p.d8 > 8 * 128 ? 16 : 8;
-    const int slice8 = ((p.d8 + 31) / 32 + most - 1) / most * 32;
+    // Slices of a multiple of 256 columns (whole warps).  Enough rows: at least
+    // 512 columns, so that clusters stay small (16384 x 2048: 64 us on four CTAs,
+    // 75 on eight), on up to eight CTAs, sixteen where slices would pass 1024
+    // columns (their tile leaves an SM one CTA: 4096 x 16384, 189 us on eight, 133 on sixteen;
+    // 16384 x 7168, 217 on seven, 214 on ten, 227 on fourteen).  Few rows
+    // (under two 512-column slices an SM): as many CTAs as there can be (32 x 7168: 6.7 us on
+    // fourteen, 9.4 on seven; 1024 x 2048: 7.3 us on eight, 8.5 on four).
+    const bool few = padded / NC_ROWS * ((p.d8 + 63) / 64) <= 2 * (int64_t)num_sms();
+    const int most = few || p.d8 > 8 * 128 ? 16 : 8;
+    const int slice8 = std::max(few ? 32 : 64, ((p.d8 + 31) / 32 + most - 1) / most * 32);
     const int ctas = (p.d8 + slice8 - 1) / slice8;
     const size_t smem = (size_t)NC_ROWS * slice8 * 16;
     cudaLaunchConfig_t cfg = {};
