@@ -529,8 +529,13 @@ __global__ void __launch_bounds__(T_MAX, CTAS) add_rmsnorm_bwd_kernel(NormBwdPar
     float dot = warp_sum(dot2.x + dot2.y);
     if ((threadIdx.x & 31) == 0) sums[par][threadIdx.x >> 5] = dot;
     // the row's barrier (the next row writes the other buffer); a wait that
-    // ran out of its bound ends the kernel for the whole CTA
-    if (!__syncthreads_and(here)) break;
+    // ran out of its bound ends the kernel for the whole CTA, once the rows
+    // still on their way have come (or run out of the bound as well)
+    if (!__syncthreads_and(here)) {
+      for (int k = 1; k < p.stages - 1 && row + (int64_t)k * gridDim.x < p.M; ++k)
+        mbar_wait(&full[(stage + k) % p.stages], stage + k < p.stages ? phase : phase ^ 1, nullptr);
+      break;
+    }
     if (threadIdx.x == 0) {
       // every thread is past the previous row: its stage takes the next one
       const int64_t next = row + (int64_t)(p.stages - 1) * gridDim.x;
