@@ -4,7 +4,7 @@ library ``libmxmlp.so`` (declared in ``include/mxmlp.h``).
 Every function here only marshals arguments: it checks tensor devices and
 dtypes, allocates output tensors with PyTorch (device memory and streams are
 all PyTorch is used for), and calls the C entry point of the same name on the
-current CUDA stream.  There is no other code path: if the library is missing
+current CUDA stream (for the operators around the MLP in compiled code).  There is no other code path: if the library is missing
 the calls raise ``MxError``.
 
 Tensors:
@@ -530,13 +530,27 @@ def linear_bwd(ctx: LinearContext, dout, err: ErrorWord | None = None):
     return dx, dw
 
 
-# ---------------------------------------------------------------- 8-bit activation checkpoints
+# ---------------------------------------------------------------- operators around the MLP
 #
 # The calls from here on take a few microseconds on the device at their
-# smallest, less than a binding that builds objects for every argument: each
-# tensor is looked at once, and pointers go as plain integers.
+# smallest, so their checks, allocations and C calls are compiled
+# (csrc/binding.cpp, _binding.so).
 
-_BF16, _U8, _I8 = torch.bfloat16, torch.uint8, torch.int8
+_ext = None
+
+
+def _fast():
+    """The compiled binding (built in-tree by ``__graft_entry__.build()``)."""
+    global _ext
+    if _ext is None:
+        lib()
+        path = os.path.join(_HERE, "_binding.so")
+        if not os.path.exists(path):
+            raise MxError(-1, f"{path} is not built; run __graft_entry__.build()")
+        from . import _binding as ext
+        ext.set_error(MxError)
+        _ext = ext
+    return _ext
 
 
 class Ckpt8:
@@ -549,11 +563,6 @@ class Ckpt8:
         self.codes = codes
         self.scales = scales
 
-    @classmethod
-    def empty(cls, rows, cols, device):
-        return cls(torch.empty((rows, cols), dtype=_I8, device=device),
-                   torch.empty((rows, cols // 32), dtype=_U8, device=device))
-
     @property
     def shape(self):
         return self.codes.shape
@@ -562,69 +571,32 @@ class Ckpt8:
         return self.codes.numel() + self.scales.numel()
 
 
-def _need_ckpt(ck, rows, cols, name):
+def _parts(ck, name):
     if not isinstance(ck, Ckpt8):
         raise MxError(1, f"{name} must be a Ckpt8")
-    _need(ck.codes, _I8, f"{name}.codes")
-    _need(ck.scales, _U8, f"{name}.scales")
-    if ck.codes.shape != (rows, cols) or ck.scales.shape != (rows, cols // 32):
-        raise MxError(1, f"{name} must be a checkpoint of a {[rows, cols]} matrix, got {list(ck.codes.shape)}")
-
-
-def _need2d(t, name, shape=None):
-    """Checks a contiguous bf16 matrix on the device and returns its shape."""
-    _need(t, _BF16, name)
-    got = t.shape
-    if len(got) != 2 or (shape is not None and got != shape):
-        raise MxError(1, f"{name} must be a {'2-d' if shape is None else list(shape)} matrix, got {list(got)}")
-    return got
+    return ck.codes, ck.scales
 
 
 def ckpt8_save(x):
     """8-bit checkpoint of a bf16 [rows, cols] matrix (cols % 32 == 0)."""
-    rows, cols = _need2d(x, "x")
-    ck = Ckpt8.empty(rows, cols, x.device)
-    _check(lib().mx_ckpt8_save(x.data_ptr(), rows, cols, ck.codes.data_ptr(), ck.scales.data_ptr(), _stream()))
-    return ck
+    return Ckpt8(*(_ext or _fast()).ckpt8_save(x))
 
 
 def ckpt8_load(ck: Ckpt8):
     """The bf16 matrix that a checkpoint holds."""
-    if not isinstance(ck, Ckpt8) or ck.codes.dim() != 2:
-        raise MxError(1, "ck must be a Ckpt8")
-    rows, cols = ck.codes.shape
-    _need_ckpt(ck, rows, cols, "ck")
-    x = torch.empty((rows, cols), dtype=_BF16, device=ck.codes.device)
-    _check(lib().mx_ckpt8_load(ck.codes.data_ptr(), ck.scales.data_ptr(), rows, cols, x.data_ptr(), _stream()))
-    return x
+    return (_ext or _fast()).ckpt8_load(*_parts(ck, "ck"))
 
 
 def swiglu_ckpt8_fwd(h13):
     """y = silu(g) u [M, h] in bf16 and the 8-bit checkpoint of h13 [M, 2h] = [g | u]."""
-    M, h2 = _need2d(h13, "h13")
-    if h2 % 64:
-        raise MxError(4, f"h13 must have 2h columns with h a multiple of 32, got {h2}")
-    dev = h13.device
-    y = torch.empty((M, h2 // 2), dtype=_BF16, device=dev)
-    ck = Ckpt8.empty(M, h2, dev)
-    _check(lib().mx_swiglu_ckpt8_fwd(h13.data_ptr(), M, h2 // 2, y.data_ptr(), ck.codes.data_ptr(),
-                                     ck.scales.data_ptr(), _stream()))
-    return y, ck
+    y, codes, scales = (_ext or _fast()).swiglu_ckpt8_fwd(h13)
+    return y, Ckpt8(codes, scales)
 
 
 def swiglu_ckpt8_bwd(dy, ck: Ckpt8, y=True):
     """(dh13 [M, 2h], y [M, h]) from dy [M, h] and the checkpoint of h13; y is
     computed again from the checkpoint (None with y=False)."""
-    M, h = _need2d(dy, "dy")
-    _need_ckpt(ck, M, 2 * h, "ck")
-    dh13 = torch.empty((M, 2 * h), dtype=_BF16, device=dy.device)
-    out = torch.empty_like(dy) if y else None
-    _check(lib().mx_swiglu_ckpt8_bwd(dy.data_ptr(), ck.codes.data_ptr(), ck.scales.data_ptr(), M, h, dh13.data_ptr(),
-                                     _ptr(out), _stream()))
-    return dh13, out
-
-
-# ---------------------------------------------------------------- residual + RMS norm
+    return (_ext or _fast()).swiglu_ckpt8_bwd(dy, *_parts(ck, "ck"), y)
 
 
 def add_rmsnorm_fwd(x, w, residual=None, eps=1e-5, y=True, axis=0, layout=SCALE_MMA, scale_mode=SCALE_RCEIL,
@@ -634,105 +606,38 @@ def add_rmsnorm_fwd(x, w, residual=None, eps=1e-5, y=True, axis=0, layout=SCALE_
     residual), rstd [M] fp32, y [M, d] bf16 (y=True), the MXFP8 codes and
     scales of y as quantize() names them (axis), ckpt: a Ckpt8 of r
     (ckpt=True); what was not asked for is None."""
-    M, d = shape = _need2d(x, "x")
-    _need(w, _BF16, "w")
-    if w.shape != (d,):
-        raise MxError(1, f"w must be [{d}], got {list(w.shape)}")
-    dev = x.device
-    r, r_ptr, res_ptr = x, None, None
-    if residual is not None:
-        _need2d(residual, "residual", shape)
-        r = torch.empty_like(x)
-        r_ptr, res_ptr = r.data_ptr(), residual.data_ptr()
-    rstd = torch.empty(M, dtype=torch.float32, device=dev)
-    out_y = torch.empty_like(x) if y else None
-    q_row = s_row = q_col = s_col = ck = ck_codes = ck_scales = None
-    if axis & ROW:
-        q_row, s_row = torch.empty((M, d), dtype=_U8, device=dev), _scales(M, d, layout, dev)
-    if axis & COL:
-        q_col, s_col = torch.empty((d, M), dtype=_U8, device=dev), _scales(d, M, layout, dev)
-    if ckpt:
-        ck = Ckpt8.empty(M, d, dev)
-        ck_codes, ck_scales = ck.codes.data_ptr(), ck.scales.data_ptr()
-    _check(lib().mx_add_rmsnorm_fwd(x.data_ptr(), res_ptr, w.data_ptr(), M, d, eps, r_ptr, rstd.data_ptr(), _ptr(out_y),
-                                    axis, layout, scale_mode, _ptr(q_row), _ptr(s_row), _ptr(q_col), _ptr(s_col),
-                                    ck_codes, ck_scales, _stream()))
-    return dict(r=r, rstd=rstd, y=out_y, q_row=q_row, s_row=s_row, q_col=q_col, s_col=s_col, ckpt=ck)
+    r, rstd, out_y, q_row, s_row, q_col, s_col, codes, scales = (_ext or _fast()).add_rmsnorm_fwd(
+        x, w, residual, eps, y, axis, layout, scale_mode, ckpt)
+    return dict(r=x if residual is None else r, rstd=rstd, y=out_y, q_row=q_row, s_row=s_row, q_col=q_col, s_col=s_col,
+                ckpt=Ckpt8(codes, scales) if ckpt else None)
 
 
 def add_rmsnorm_bwd(dy, saved, rstd, w, dres=None):
     """(dx [M, d], dw [d]) of add_rmsnorm_fwd from dy [M, d], the saved r (bf16,
     or its Ckpt8), rstd and w; dres [M, d] is the gradient that reaches r on
     the residual path.  dx is the gradient of x and of the residual."""
-    M, d = shape = _need2d(dy, "dy")
-    r = ck_codes = ck_scales = None
     if isinstance(saved, Ckpt8):
-        _need_ckpt(saved, M, d, "saved")
-        ck_codes, ck_scales = saved.codes.data_ptr(), saved.scales.data_ptr()
-    else:
-        _need2d(saved, "saved", shape)
-        r = saved.data_ptr()
-    _need(w, _BF16, "w")
-    _need(rstd, torch.float32, "rstd")
-    if w.shape != (d,) or rstd.shape != (M,):
-        raise MxError(1, f"w must be [{d}] and rstd [{M}], got {list(w.shape)} and {list(rstd.shape)}")
-    if dres is not None:
-        _need2d(dres, "dres", shape)
-    L = lib()
-    dx = torch.empty_like(dy)
-    dw = torch.empty_like(w)
-    ws = torch.empty(max(L.mx_add_rmsnorm_bwd_workspace(M, d), 16), dtype=_U8, device=dy.device)
-    _check(L.mx_add_rmsnorm_bwd(dy.data_ptr(), r, ck_codes, ck_scales, rstd.data_ptr(), w.data_ptr(), _ptr(dres), M, d,
-                                dx.data_ptr(), dw.data_ptr(), ws.data_ptr(), _stream()))
-    return dx, dw
+        return (_ext or _fast()).add_rmsnorm_bwd(dy, None, saved.codes, saved.scales, rstd, w, dres)
+    return (_ext or _fast()).add_rmsnorm_bwd(dy, saved, None, None, rstd, w, dres)
 
 
-# ---------------------------------------------------------------- ragged expert products
-
-
-def _ragged(mode, a, b, offs, shape, M, N, K, err):
-    _need(offs, torch.int32, "offs")
-    c = torch.empty(shape, dtype=_BF16, device=a.device)
-    _check(lib().mx_ragged_mm(mode, a.data_ptr(), b.data_ptr(), M, N, K, offs.data_ptr(), offs.numel(), c.data_ptr(),
-                              err.ptr() if err else None, _stream()))
-    return c
-
-
-def _need_w(w, offs, name="w"):
-    _need(w, torch.bfloat16, name)
-    if w.dim() != 3 or w.shape[0] != offs.numel():
-        raise MxError(1, f"{name} must be [E, N, K] with E = {offs.numel()}, got {list(w.shape)}")
+def _word(err):
+    return err.t.data_ptr() if err else 0
 
 
 def ragged_mm(x, w, offs, err: ErrorWord | None = None):
     """out [M, N] = x [M, K] . w[e]^T by expert: group e owns rows
     [offs[e-1], offs[e]) (int32 ends on the device, any sizes), w [E, N, K].
     Rows past the last group are zeros."""
-    _need2d(x, "x")
-    _need_w(w, offs)
-    E, N, K = w.shape
-    if x.shape[1] != K:
-        raise MxError(1, f"x must have {K} columns, got {x.shape[1]}")
-    return _ragged(RAGGED_FWD, x, w, offs, (x.shape[0], N), x.shape[0], N, K, err)
+    return (_ext or _fast()).ragged(RAGGED_FWD, x, w, offs, _word(err))
 
 
 def ragged_mm_dgrad(dout, w, offs, err: ErrorWord | None = None):
     """dx [M, K] = dout [M, N] . w[e] by expert: the gradient of ragged_mm's x."""
-    _need2d(dout, "dout")
-    _need_w(w, offs)
-    E, N, K = w.shape
-    if dout.shape[1] != N:
-        raise MxError(1, f"dout must have {N} columns, got {dout.shape[1]}")
-    return _ragged(RAGGED_DGRAD, dout, w, offs, (dout.shape[0], K), dout.shape[0], N, K, err)
+    return (_ext or _fast()).ragged(RAGGED_DGRAD, dout, w, offs, _word(err))
 
 
 def ragged_mm_wgrad(dout, x, offs, err: ErrorWord | None = None):
     """dw [E, N, K], dw[e] = dout[group e]^T . x[group e]: the gradient of
     ragged_mm's w, from the token-major operands as they lie."""
-    _need2d(dout, "dout")
-    _need2d(x, "x")
-    if dout.shape[0] != x.shape[0]:
-        raise MxError(1, f"dout and x must have the same rows, got {dout.shape[0]} and {x.shape[0]}")
-    M, N = dout.shape
-    K = x.shape[1]
-    return _ragged(RAGGED_WGRAD, dout, x, offs, (offs.numel(), N, K), M, N, K, err)
+    return (_ext or _fast()).ragged(RAGGED_WGRAD, dout, x, offs, _word(err))

@@ -3,7 +3,9 @@
 Each .cu file is compiled to an object in parallel, then the objects are
 linked into ``block_scaled_mlp_gb300/libmxmlp.so`` (static CUDA runtime, no
 libcuda link: the driver entry point for tensor maps is looked up at run
-time, so the library also loads on machines without a GPU driver).
+time, so the library also loads on machines without a GPU driver).  Beside it
+``_binding.so``, the Python binding of the operators whose calls are short
+(csrc/binding.cpp, compiled against the installed torch's headers).
 """
 from __future__ import annotations
 
@@ -17,6 +19,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmxmlp.so")
+BINDING = os.path.join(HERE, "_binding.so")
 SOURCES = ["api.cu", "quant.cu", "swiglu.cu", "gemm.cu", "dispatch.cu", "norm.cu", "ckpt8.cu",
            "ragged.cu", "ops.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -39,6 +42,21 @@ def _stale(obj: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _torch_flags():
+    """Compile and link flags of a Python extension on the installed torch."""
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    abi = f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"
+    libs = [f"-L{os.path.join(root, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    return [abi, *("-I" + i for i in inc)], libs
+
+
 def build(verbose: bool = False, force: bool = False, extra_flags=None) -> str:
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
@@ -57,8 +75,22 @@ def build(verbose: bool = False, force: bool = False, extra_flags=None) -> str:
             raise RuntimeError(f"nvcc failed for {src}:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         return o, r.stdout + r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    def run(cmd, what):
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"{what} failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+
+    binding_src, binding_obj = os.path.join(CSRC, "binding.cpp"), os.path.join(BUILD, "binding.o")
+
+    def compile_binding():
+        if force or _stale(binding_obj, [binding_src, headers[-1]]):
+            run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", *_torch_flags()[0], "-c", binding_src, "-o",
+                 binding_obj], "g++ for binding.cpp")
+
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(compile_binding)
         results = list(ex.map(compile_one, SOURCES))
+        binding.result()
     objs = [o for o, _ in results]
     if verbose:
         for _, log in results:
@@ -69,6 +101,9 @@ def build(verbose: bool = False, force: bool = False, extra_flags=None) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    if force or _stale(BINDING, [binding_obj]):
+        run(["g++", "-shared", "-o", BINDING, binding_obj, f"-L{HERE}", "-l:libmxmlp.so", "-Wl,-rpath,$ORIGIN",
+             *_torch_flags()[1]], "link of the binding")
     return LIB
 
 
