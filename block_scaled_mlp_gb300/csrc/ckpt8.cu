@@ -28,6 +28,7 @@ MX_DEVINL float sigmoid_approx(float g) { return __fdividef(1.0f, 1.0f + __expf(
 // A thread has vectors i and i + C8_THREADS of its CTA's 2 * C8_THREADS.
 __global__ void __launch_bounds__(C8_THREADS)
     ckpt8_save_kernel(const uint4* __restrict__ x, int64_t n8, uint2* __restrict__ codes, uint8_t* __restrict__ scales) {
+  pdl_begin();
   const int64_t i = (int64_t)blockIdx.x * (2 * C8_THREADS) + threadIdx.x, j = i + C8_THREADS;
   const uint4 z = make_uint4(0, 0, 0, 0);
   const uint4 a = i < n8 ? ld_once(x + i) : z, b = j < n8 ? ld_once(x + j) : z;  // whole blocks: four lanes together
@@ -45,6 +46,7 @@ __global__ void __launch_bounds__(C8_THREADS)
 __global__ void __launch_bounds__(C8_THREADS)
     ckpt8_load_kernel(const uint2* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t n8,
                       uint4* __restrict__ x) {
+  pdl_begin();
   const int64_t i = (int64_t)blockIdx.x * (2 * C8_THREADS) + threadIdx.x, j = i + C8_THREADS;
   if (i >= n8) return;
   const bool two = j < n8;
@@ -104,6 +106,7 @@ MX_DEVINL SwigluAt swiglu_at(const SwigluCkptParams& p, int k) {
 }
 
 __global__ void __launch_bounds__(C8_THREADS) swiglu_ckpt8_fwd_kernel(SwigluCkptParams p) {
+  pdl_begin();
   SwigluAt at[SW];
   uint4 gp[SW], up[SW];
 #pragma unroll
@@ -133,6 +136,7 @@ __global__ void __launch_bounds__(C8_THREADS) swiglu_ckpt8_fwd_kernel(SwigluCkpt
 }
 
 __global__ void __launch_bounds__(C8_THREADS) swiglu_ckpt8_bwd_kernel(SwigluCkptParams p) {
+  pdl_begin();
   SwigluAt at[SW];
   uint4 dp[SW];
   uint2 gc[SW], uc[SW];
@@ -183,8 +187,9 @@ int launch_ckpt8_save(const void* x, int64_t rows, int64_t cols, void* codes, vo
   unsigned grid;
   if (int rc = grid_of(n8, 2, &grid)) return rc;
   count_launch(MX_KERNEL_CKPT8);
-  ckpt8_save_kernel<<<grid, C8_THREADS, 0, stream>>>((const uint4*)x, n8, (uint2*)codes, (uint8_t*)scales);
-  return cuda_status(cudaGetLastError(), "ckpt8_save_kernel launch");
+  return cuda_status(launch_overlapped(ckpt8_save_kernel, grid, C8_THREADS, 0, stream, 1, (const uint4*)x, n8, (uint2*)codes,
+                                       (uint8_t*)scales),
+                     "ckpt8_save_kernel launch");
 }
 
 int launch_ckpt8_load(const void* codes, const void* scales, int64_t rows, int64_t cols, void* x, cudaStream_t stream) {
@@ -192,8 +197,9 @@ int launch_ckpt8_load(const void* codes, const void* scales, int64_t rows, int64
   unsigned grid;
   if (int rc = grid_of(n8, 2, &grid)) return rc;
   count_launch(MX_KERNEL_CKPT8);
-  ckpt8_load_kernel<<<grid, C8_THREADS, 0, stream>>>((const uint2*)codes, (const uint8_t*)scales, n8, (uint4*)x);
-  return cuda_status(cudaGetLastError(), "ckpt8_load_kernel launch");
+  return cuda_status(launch_overlapped(ckpt8_load_kernel, grid, C8_THREADS, 0, stream, 1, (const uint2*)codes,
+                                       (const uint8_t*)scales, n8, (uint4*)x),
+                     "ckpt8_load_kernel launch");
 }
 
 int launch_swiglu_ckpt8_fwd(const void* h13, int64_t M, int64_t h, void* y, void* codes, void* scales,
@@ -204,8 +210,8 @@ int launch_swiglu_ckpt8_fwd(const void* h13, int64_t M, int64_t h, void* y, void
   unsigned grid;
   if (int rc = grid_of(p.n8, SW, &grid)) return rc;
   count_launch(MX_KERNEL_CKPT8);
-  swiglu_ckpt8_fwd_kernel<<<grid, C8_THREADS, 0, stream>>>(p);
-  return cuda_status(cudaGetLastError(), "swiglu_ckpt8_fwd_kernel launch");
+  return cuda_status(launch_overlapped(swiglu_ckpt8_fwd_kernel, grid, C8_THREADS, 0, stream, 1, p),
+                     "swiglu_ckpt8_fwd_kernel launch");
 }
 
 int launch_swiglu_ckpt8_bwd(const void* dy, const void* codes, const void* scales, int64_t M, int64_t h, void* dh13,
@@ -218,8 +224,8 @@ int launch_swiglu_ckpt8_bwd(const void* dy, const void* codes, const void* scale
   unsigned grid;
   if (int rc = grid_of(p.n8, SW, &grid)) return rc;
   count_launch(MX_KERNEL_CKPT8);
-  swiglu_ckpt8_bwd_kernel<<<grid, C8_THREADS, 0, stream>>>(p);
-  return cuda_status(cudaGetLastError(), "swiglu_ckpt8_bwd_kernel launch");
+  return cuda_status(launch_overlapped(swiglu_ckpt8_bwd_kernel, grid, C8_THREADS, 0, stream, 1, p),
+                     "swiglu_ckpt8_bwd_kernel launch");
 }
 
 }  // namespace mx

@@ -32,6 +32,17 @@ MX_DEVINL uint64_t globaltimer_ns() {
 // MX_ERR_TIMEOUT in the error word and gives up instead of spinning forever.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 
+// Overlap with the neighbours on the stream (for kernels launched by
+// launch_overlapped): the next such kernel may be scheduled from here on, as
+// room allows, and this one waits for the end of the one before.  Nothing that the
+// kernel before writes or reads may be touched earlier.
+MX_DEVINL void pdl_allow_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+MX_DEVINL void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+MX_DEVINL void pdl_begin() {
+  pdl_allow_next();
+  pdl_wait();
+}
+
 MX_DEVINL void record_error(int32_t* err, int32_t code) {
   if (err) atomicOr(err, code);
 }

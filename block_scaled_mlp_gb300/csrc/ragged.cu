@@ -176,6 +176,13 @@ __global__ void __launch_bounds__(RCfg<MODE, BT>::THREADS, 1)
     mbar_init(done_bar, 1);
     fence_mbar_init();
   }
+  if (warp == 1) { tmem_alloc_pair(tmem_holder, C::TMEM); tmem_relinquish_pair(); }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  cluster_sync();  // the peer's barriers exist before any remote arrive or pair copy
+  const uint32_t tmem = *tmem_holder;
+  pdl_begin();     // all of the above overlaps the kernel before
   if (warp == 2) {
     // group ends, checked, and the running number of work units
     int32_t prev = 0, units = 0;
@@ -207,12 +214,7 @@ __global__ void __launch_bounds__(RCfg<MODE, BT>::THREADS, 1)
       if (!ok && blockIdx.x == 0) record_error(p.err, MX_ERR_BAD_OFFSETS);
     }
   }
-  if (warp == 1) { tmem_alloc_pair(tmem_holder, C::TMEM); tmem_relinquish_pair(); }
-  tc_fence_before();
   __syncthreads();
-  tc_fence_after();
-  cluster_sync();  // the peer's barriers exist before any remote arrive or pair copy
-  const uint32_t tmem = *tmem_holder;
   const int32_t n_units = s_units;
   if (MODE == RG_WGRAD) ends = !s_ok ? nullptr /* refused: every group empty, zeros */ : p.E <= C::ENDS ? s_ends : p.offs;
 
@@ -496,9 +498,10 @@ int launch_cfg(const CUtensorMap& tA, const CUtensorMap& tB, const ZeroMaps& tZ,
       return cuda_status(e != cudaSuccess ? e : cudaErrorInvalidConfiguration, "cudaOccupancyMaxActiveClusters");
     nres = n;
   }
-  cfg.gridDim = dim3(2 * (unsigned)std::max<int64_t>(1, std::min<int64_t>(units, nres)));
   count_launch(MX_KERNEL_RAGGED);
-  return cuda_status(cudaLaunchKernelEx(&cfg, k, tA, tB, tZ, p), "ragged_kernel launch");
+  return cuda_status(launch_overlapped(k, 2 * (unsigned)std::max<int64_t>(1, std::min<int64_t>(units, nres)), C::THREADS,
+                                       C::SMEM, stream, 2, tA, tB, tZ, p),
+                     "ragged_kernel launch");
 }
 
 }  // namespace
