@@ -51,13 +51,6 @@ MX_DEVINL uint4 add8(const uint4& a, const uint4& b) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-MX_DEVINL void sumsq8(const uint4& a, f2& s) {
-  sumsq_bf16x2(a.x, s);
-  sumsq_bf16x2(a.y, s);
-  sumsq_bf16x2(a.z, s);
-  sumsq_bf16x2(a.w, s);
-}
-
 MX_DEVINL float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
@@ -70,6 +63,20 @@ MX_DEVINL f2 pair_add(f2 a, f2 b) {
   const float e = __fadd_rn(__fsub_rn(a.x, __fsub_rn(s, t)), __fsub_rn(b.x, t));  // s + e = a.x + b.x
   const float l = __fadd_rn(e, __fadd_rn(a.y, b.y)), h = __fadd_rn(s, l);
   return fabsf(s) < __uint_as_float(0x7F800000u) ? f2_pack(h, __fsub_rn(l, __fsub_rn(h, s))) : f2_pack(s, 0.0f);
+}
+// The squares of eight elements added to a pair: fp32 for four of them at a
+// time (each square is exact), unevaluated from there on, so that the row's sum is off by
+// some 1e-9 and not by the 5e-9 of one fp32 chain a thread.
+MX_DEVINL void squares8(const uint4& a, f2& s) {
+  sumsq_bf16x2(a.x, s);
+  sumsq_bf16x2(a.y, s);
+  sumsq_bf16x2(a.z, s);
+  sumsq_bf16x2(a.w, s);
+}
+MX_DEVINL f2 add_squares8(f2 sum, const uint4& a) {
+  f2 s = f2_splat(0.0f);
+  squares8(a, s);
+  return pair_add(sum, pair_add(f2_pack(s.x, 0.0f), f2_pack(s.y, 0.0f)));
 }
 template <int FROM>
 MX_DEVINL f2 warp_sum_pair(f2 v) {
@@ -97,8 +104,8 @@ MX_DEVINL f2 rstd_pair(f2 ss, float d, float eps) {
 // bit set (r w n is hardly ever a 24-bit number).  Such a value lies on the same
 // side of every E4M3 and bf16 tie as r w n itself, so the rounding that follows
 // is that of r w n, where an fp32 value to nearest lands on the tie itself once
-// in a million times and goes to the even side (of 117 million codes 69 to 71 differed
-// from the 64-bit result, now 14 to 33, by the last bits of the sums).
+// in a million times and goes to the even side: of 117 million codes 69 to 71 then
+// differed from the 64-bit result, and 0 to 6 do with this and the sums above.
 // Zero becomes 2^-149, which rounds to a zero code and a zero bf16.
 MX_DEVINL f2 norm2(uint32_t r, f2 n, uint32_t w) {
   const f2 rw = mul_bf16x2(r, w);
@@ -148,10 +155,15 @@ __global__ void __launch_bounds__(512) add_rmsnorm_row_kernel(NormFwdParams p) {
     }
   }
 #pragma unroll
-  for (int k = 0; k < V; ++k) sumsq8(v[k], ss);
+  for (int k = 0; k < V; ++k) {
+    // without codes no tie hangs on the sum's last bits (8192 x 4096: 28 us, not 30)
+    if (p.q_row) ss = add_squares8(ss, v[k]);
+    else squares8(v[k], ss);
+  }
+  if (!p.q_row) ss = f2_pack(ss.x + ss.y, 0.0f);
   __shared__ f2 part[16];
   const int lane = threadIdx.x & 31;
-  f2 sum = warp_sum_pair<16>(f2_pack(ss.x + ss.y, 0.0f));
+  f2 sum = warp_sum_pair<16>(ss);
   if (lane == 0) part[threadIdx.x >> 5] = sum;
   __syncthreads();
   sum = warp_sum_pair<8>((lane & 15) < (T >> 5) ? part[lane & 15] : f2_splat(0.0f));
@@ -293,7 +305,7 @@ __global__ void __launch_bounds__(NC_THREADS, NC_CTAS_SM) add_rmsnorm_col_kernel
       load_res(cb + 32);
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) sumsq8(v[k], ss[k]);
+    for (int k = 0; k < 4; ++k) ss[k] = add_squares8(ss[k], v[k]);
     if (CK) {
 #pragma unroll
       for (int k = 0; k < 4; k += 2) {
@@ -313,7 +325,7 @@ __global__ void __launch_bounds__(NC_THREADS, NC_CTAS_SM) add_rmsnorm_col_kernel
   const int n8_all = n8 & ~31;
   f2 sum[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) sum[k] = warp_sum_pair<16>(f2_pack(ss[k].x + ss[k].y, 0.0f));
+  for (int k = 0; k < 4; ++k) sum[k] = warp_sum_pair<16>(ss[k]);
   if (lane < ctas) {
     // lane j: this CTA's sums of the warp's rows to CTA j of the cluster
     const uint32_t dst = cluster_map(smem_u32(&part[rank][rw]), lane);
