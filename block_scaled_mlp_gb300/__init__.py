@@ -4,8 +4,9 @@ library ``libmxmlp.so`` (declared in ``include/mxmlp.h``).
 Every function here only marshals arguments: it checks tensor devices and
 dtypes, allocates output tensors with PyTorch (device memory and streams are
 all PyTorch is used for), and calls the C entry point of the same name on the
-current CUDA stream (for the operators around the MLP in compiled code).  There is no other code path: if the library is missing
-the calls raise ``MxError``.
+current CUDA stream (for the operators around the MLP in compiled code).
+There is no other code path: if the library is missing the calls raise
+``MxError``.
 
 Tensors:
   bf16 activations/weights     torch.bfloat16, contiguous, on a CUDA device
@@ -622,7 +623,7 @@ def add_rmsnorm_bwd(dy, saved, rstd, w, dres=None):
 
 
 def _word(err):
-    return err.t.data_ptr() if err else 0
+    return err.t if err else None
 
 
 def ragged_mm(x, w, offs, err: ErrorWord | None = None):

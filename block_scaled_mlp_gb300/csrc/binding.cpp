@@ -2,15 +2,17 @@
 // checkpoints, ragged products) on torch tensors.
 //
 // These calls take 2 to 5 us on the device at their smallest, and a binding in
-// Python took 12 to 20 us for one: a microsecond and a half for each output
-// that it allocated, as much again for its checks and for turning nineteen arguments into C
-// values.  Here a call checks its tensors, allocates its outputs and calls the C entry
-// point of include/mxmlp.h on the tensors' device and its current stream in one go.
-// Refusals raise MxError with the status and text that the C entry gives,
-// allocation failures torch's own error; no C++ exception leaves a function.
+// Python took 12 to 20 us for one: a microsecond and a half for each output that
+// it allocated, as much again for its checks and for turning nineteen arguments
+// into C values.  Here a call checks its tensors, allocates its outputs and calls
+// the C entry point of include/mxmlp.h on the tensors' device and its current
+// stream in one go (4 to 9 us).  Refusals raise MxError with the status and text
+// that the C entry gives, allocation failures torch's own error; no C++ exception
+// leaves a function.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <algorithm>
 #include <string>
 
 #include <ATen/core/Tensor.h>
@@ -90,12 +92,30 @@ at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, const at::Tensor& l
 
 void* ptr(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 
-// The device of a call's tensors, made current, and its current stream.
+// The device of a call's tensors, made current, and its current stream, with
+// the interpreter's lock released: an allocation or a launch may wait for the
+// device, and other threads run meanwhile.  finish() takes the lock back and
+// turns a status into a refusal.
 struct On {
   c10::cuda::CUDAGuard guard;
   void* stream;
+  PyThreadState* thread;  // last: what may throw comes before it
   explicit On(const at::Tensor& t)
-      : guard(t.device()), stream(c10::cuda::getCurrentCUDAStream(t.device().index()).stream()) {}
+      : guard(t.device()), stream(c10::cuda::getCurrentCUDAStream(t.device().index()).stream()),
+        thread(PyEval_SaveThread()) {}
+  void finish(int rc) {
+    lock();
+    check(rc);
+  }
+  ~On() { lock(); }
+  On(const On&) = delete;
+  On& operator=(const On&) = delete;
+
+ private:
+  void lock() {
+    if (thread) PyEval_RestoreThread(thread);
+    thread = nullptr;
+  }
 };
 
 PyObject* wrap(const at::Tensor& t) {
@@ -129,11 +149,26 @@ int64_t integer(PyObject* o) {
   return v;
 }
 
+int small_integer(PyObject* o, const char* name) {
+  const int64_t v = integer(o);
+  if (v < INT32_MIN || v > INT32_MAX) refuse(std::string(name) + " is out of range");
+  return (int)v;
+}
+
+bool truth(PyObject* o, const char* name) {
+  const int t = PyObject_IsTrue(o);
+  if (t < 0) {
+    PyErr_Clear();
+    refuse(std::string(name) + " must be true or false");
+  }
+  return t == 1;
+}
+
 void arguments(Py_ssize_t got, Py_ssize_t want) {
   if (got != want) refuse("wrong number of arguments");
 }
 
-at::Tensor scales(int64_t rows, int64_t cols, int64_t layout, const at::Tensor& like) {
+at::Tensor scales(int64_t rows, int64_t cols, int layout, const at::Tensor& like) {
   const int64_t s = cols / 32;
   return empty({layout == MX_SCALE_MMA ? (rows + 127) / 128 * ((s + 3) / 4) * 512 : rows * s}, at::kByte, like);
 }
@@ -146,7 +181,7 @@ PyObject* py_ckpt8_save(PyObject*, PyObject* const* a, Py_ssize_t n) {
     On on(x);
     const int64_t rows = x.size(0), cols = x.size(1);
     at::Tensor codes = empty({rows, cols}, at::kChar, x), sc = empty({rows, cols / 32}, at::kByte, x);
-    check(mx_ckpt8_save(ptr(x), rows, cols, ptr(codes), ptr(sc), on.stream));
+    on.finish(mx_ckpt8_save(ptr(x), rows, cols, ptr(codes), ptr(sc), on.stream));
     return tuple_of(codes, sc);
   });
 }
@@ -172,7 +207,7 @@ PyObject* py_ckpt8_load(PyObject*, PyObject* const* a, Py_ssize_t n) {
     checkpoint(a[0], a[1], -1, -1, "ck", nullptr, &c, &s);
     On on(*c);
     at::Tensor x = empty(c->sizes(), at::kBFloat16, *c);
-    check(mx_ckpt8_load(ptr(*c), ptr(*s), c->size(0), c->size(1), ptr(x), on.stream));
+    on.finish(mx_ckpt8_load(ptr(*c), ptr(*s), c->size(0), c->size(1), ptr(x), on.stream));
     return wrap(x);
   });
 }
@@ -188,7 +223,7 @@ PyObject* py_swiglu_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     On on(h13);
     at::Tensor y = empty({M, h}, at::kBFloat16, h13), codes = empty({M, h2}, at::kChar, h13);
     at::Tensor sc = empty({M, h2 / 32}, at::kByte, h13);
-    check(mx_swiglu_ckpt8_fwd(ptr(h13), M, h, ptr(y), ptr(codes), ptr(sc), on.stream));
+    on.finish(mx_swiglu_ckpt8_fwd(ptr(h13), M, h, ptr(y), ptr(codes), ptr(sc), on.stream));
     return tuple_of(y, codes, sc);
   });
 }
@@ -201,10 +236,11 @@ PyObject* py_swiglu_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t M = dy.size(0), h = dy.size(1);
     const at::Tensor *c, *s;
     checkpoint(a[1], a[2], M, 2 * h, "ck", &dy, &c, &s);
+    const bool want_y = truth(a[3], "y");
     On on(dy);
     at::Tensor dh13 = empty({M, 2 * h}, at::kBFloat16, dy), y;
-    if (PyObject_IsTrue(a[3]) == 1) y = empty({M, h}, at::kBFloat16, dy);
-    check(mx_swiglu_ckpt8_bwd(ptr(dy), ptr(*c), ptr(*s), M, h, ptr(dh13), ptr(y), on.stream));
+    if (want_y) y = empty({M, h}, at::kBFloat16, dy);
+    on.finish(mx_swiglu_ckpt8_bwd(ptr(dy), ptr(*c), ptr(*s), M, h, ptr(dh13), ptr(y), on.stream));
     return tuple_of(dh13, y);
   });
 }
@@ -223,8 +259,9 @@ PyObject* py_norm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
       PyErr_Clear();
       refuse("eps must be a number");
     }
-    const bool want_y = PyObject_IsTrue(a[4]) == 1, ckpt = PyObject_IsTrue(a[8]) == 1;
-    const int64_t axis = integer(a[5]), layout = integer(a[6]), mode = integer(a[7]);
+    const bool want_y = truth(a[4], "y"), ckpt = truth(a[8], "ckpt");
+    const int axis = small_integer(a[5], "axis"), layout = small_integer(a[6], "layout");
+    const int mode = small_integer(a[7], "scale_mode");
     On on(x);
     at::Tensor r, y, q_row, s_row, q_col, s_col, codes, sc;
     if (residual) r = empty({M, d}, at::kBFloat16, x);
@@ -242,9 +279,9 @@ PyObject* py_norm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
       codes = empty({M, d}, at::kChar, x);
       sc = empty({M, d / 32}, at::kByte, x);
     }
-    check(mx_add_rmsnorm_fwd(ptr(x), residual ? ptr(*residual) : nullptr, ptr(w), M, d, (float)eps, ptr(r),
-                             (float*)ptr(rstd), ptr(y), (int)axis, (int)layout, (int)mode, ptr(q_row), ptr(s_row),
-                             ptr(q_col), ptr(s_col), ptr(codes), ptr(sc), on.stream));
+    on.finish(mx_add_rmsnorm_fwd(ptr(x), residual ? ptr(*residual) : nullptr, ptr(w), M, d, (float)eps, ptr(r),
+                                 (float*)ptr(rstd), ptr(y), axis, layout, mode, ptr(q_row), ptr(s_row),
+                                 ptr(q_col), ptr(s_col), ptr(codes), ptr(sc), on.stream));
     return tuple_of(residual ? r : x, rstd, y, q_row, s_row, q_col, s_col, codes, sc);
   });
 }
@@ -264,21 +301,22 @@ PyObject* py_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     On on(dy);
     at::Tensor dx = empty({M, d}, at::kBFloat16, dy), dw = empty({d}, at::kBFloat16, dy);
     at::Tensor ws = empty({(int64_t)mx_add_rmsnorm_bwd_workspace(M, d) + 16}, at::kByte, dy);
-    check(mx_add_rmsnorm_bwd(ptr(dy), r ? ptr(*r) : nullptr, c ? ptr(*c) : nullptr, s ? ptr(*s) : nullptr,
-                             (const float*)ptr(rstd), ptr(w), dres ? ptr(*dres) : nullptr, M, d, ptr(dx), ptr(dw), ptr(ws),
-                             on.stream));
+    on.finish(mx_add_rmsnorm_bwd(ptr(dy), r ? ptr(*r) : nullptr, c ? ptr(*c) : nullptr, s ? ptr(*s) : nullptr,
+                                 (const float*)ptr(rstd), ptr(w), dres ? ptr(*dres) : nullptr, M, d, ptr(dx), ptr(dw),
+                                 ptr(ws), on.stream));
     return tuple_of(dx, dw);
   });
 }
 
-// ragged(mode, a, b, offs, err) -> c; err: the address of an error word, or 0
+// ragged(mode, a, b, offs, err) -> c; err: an error word's tensor, or None
 PyObject* py_ragged(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&] {
     arguments(n, 5);
-    const int64_t mode = integer(a[0]);
+    const int mode = small_integer(a[0], "mode");
     const at::Tensor& t = matrix(a[1], mode == MX_RAGGED_FWD ? "x" : "dout");
     const at::Tensor& offs = need(a[3], "offs", at::kInt, &t);
-    const int64_t M = t.size(0), E = offs.numel();
+    void* err = a[4] == Py_None ? nullptr : ptr(need(a[4], "err", at::kInt, {1}, &t));
+    const int64_t M = t.size(0), E = std::min<int64_t>(offs.numel(), INT32_MAX);
     int64_t N, K;
     const at::Tensor* b;
     at::Tensor c;
@@ -302,8 +340,8 @@ PyObject* py_ragged(PyObject*, PyObject* const* a, Py_ssize_t n) {
     On on(t);
     if (mode == MX_RAGGED_WGRAD) c = empty({E, N, K}, at::kBFloat16, t);
     else c = empty({M, mode == MX_RAGGED_FWD ? N : K}, at::kBFloat16, t);
-    check(mx_ragged_mm((int)mode, ptr(t), ptr(*b), M, N, K, (const int32_t*)ptr(offs), (int32_t)E, ptr(c),
-                       (int32_t*)(uintptr_t)integer(a[4]), on.stream));
+    on.finish(mx_ragged_mm(mode, ptr(t), ptr(*b), M, N, K, (const int32_t*)ptr(offs), (int32_t)E, ptr(c),
+                           (int32_t*)err, on.stream));
     return wrap(c);
   });
 }

@@ -7,10 +7,11 @@
 //
 // Sums are fp32; n is kept as an unevaluated pair of fp32 values and r w is
 // exact in fp32 (two bf16 factors), and y keeps enough of r w n that the codes
-// and the bf16 values are r w n rounded once (see norm2).  The sum r is what the model carries on in bf16, so the norm is taken of the rounded
-// value, the one that the backward pass has.  All kernels are bound by HBM:
-// each input is read once and each output written once, a row staying in
-// registers or shared memory between its two uses.
+// and the bf16 values are r w n rounded once (see norm2).  The sum r is what
+// the model carries on in bf16, so the norm is taken of the rounded value, the
+// one that the backward pass has.  Each input is read once and each output
+// written once, a row staying in registers or shared memory between its two
+// uses.  Times below are device times on a GB300 whose copy runs at 6.78 TB/s.
 #include "ckpt8.cuh"
 #include "kernels.h"
 #include "tile_quant.cuh"
@@ -65,8 +66,8 @@ MX_DEVINL f2 pair_add(f2 a, f2 b) {
   return fabsf(s) < __uint_as_float(0x7F800000u) ? f2_pack(h, __fsub_rn(l, __fsub_rn(h, s))) : f2_pack(s, 0.0f);
 }
 // The squares of eight elements added to a pair: fp32 for four of them at a
-// time (each square is exact), unevaluated from there on, so that the row's sum is off by
-// some 1e-9 and not by the 5e-9 of one fp32 chain a thread.
+// time (each square is exact), unevaluated from there on, so that the row's sum
+// is off by some 1e-9 and not by the 5e-9 of one fp32 chain a thread.
 MX_DEVINL void squares8(const uint4& a, f2& s) {
   sumsq_bf16x2(a.x, s);
   sumsq_bf16x2(a.y, s);
@@ -104,8 +105,8 @@ MX_DEVINL f2 rstd_pair(f2 ss, float d, float eps) {
 // bit set (r w n is hardly ever a 24-bit number).  Such a value lies on the same
 // side of every E4M3 and bf16 tie as r w n itself, so the rounding that follows
 // is that of r w n, where an fp32 value to nearest lands on the tie itself once
-// in a million times and goes to the even side: of 117 million codes 69 to 71 then
-// differed from the 64-bit result, and 0 to 6 do with this and the sums above.
+// in a million times and goes to the even side: of 117 million codes 69 to 71
+// then differed from the 64-bit result, and 0 to 6 do with this and the sums above.
 // Zero becomes 2^-149, which rounds to a zero code and a zero bf16.
 MX_DEVINL f2 norm2(uint32_t r, f2 n, uint32_t w) {
   const f2 rw = mul_bf16x2(r, w);
@@ -120,7 +121,9 @@ MX_DEVINL void norm8(const uint4& r, f2 n, const uint4& w, f2 (&y)[4]) {
 }
 
 // ---- rows: one CTA per row, the row in registers (V vectors of eight a
-// thread).  CTAs past M only clear the scale layout's padding rows.
+// thread).  CTAs past M only clear the scale layout's padding rows.  Bound by
+// HBM from some hundred rows on: 16384 x 7168 with a residual into row codes and
+// bf16 162 us (6.5 TB/s); below that by the latency of one row (1 x 7168: 3.1 us).
 template <int V>
 __global__ void __launch_bounds__(512) add_rmsnorm_row_kernel(NormFwdParams p) {
   pdl_begin();
@@ -210,22 +213,24 @@ __global__ void __launch_bounds__(512) add_rmsnorm_row_kernel(NormFwdParams p) {
 }
 
 // ---- rows and columns: a cluster of CTAs per 32 rows, each with a slice of
-// the columns.  r of the slice stays in shared memory in
-// bf16; the rows' sums of squares are exchanged through distributed shared
-// memory, so one pass over HBM gives both quantizations (a second kernel for
-// the columns would read r again: 10 bytes an element instead of 8).
+// the columns.  r of the slice stays in shared memory in bf16; the rows' sums of
+// squares are exchanged through distributed shared memory, so one pass over HBM
+// gives both quantizations (a second kernel for the columns would read r again:
+// 10 bytes an element instead of 8).  16384 x 7168 with a residual into both
+// codes and a checkpoint takes 219 us (4.9 TB/s): three or four CTAs an SM do
+// not cover the load, exchange and two quantization phases of one another; the
+// column pass adds 36 us.
 //
 // Row passes: a warp has four rows, a lane eight elements of each, four lanes
 // one block.  Column pass: lanes l and l ^ 16 have rows 0-15 and 16-31 of one
-// column pair (16 rows keep the registers low enough for four CTAs an SM, where the
-// tiles leave room: 8192 x 4096, 60 us against 68 with three).
-// The tile's 16-byte vectors of rows 16-31 sit at vector index ^ 4, so that the
-// two half-warps of the column pass read different banks.
+// column pair (16 rows keep the registers low enough for four CTAs an SM, where
+// the tiles leave room: 8192 x 4096, 60 us against 68 with three).  The tile's
+// 16-byte vectors of rows 16-31 sit at vector index ^ 4, so that the two
+// half-warps of the column pass read different banks.
 constexpr int NC_ROWS = 32;
 constexpr int NC_THREADS = 256;
 constexpr int NC_MAX_CTAS = 16;
 constexpr int NC_CTAS_SM = 4;
-
 
 MX_DEVINL void copy_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
@@ -432,12 +437,13 @@ __global__ void __launch_bounds__(NC_THREADS, NC_CTAS_SM) add_rmsnorm_col_kernel
 // ---- backward: each CTA takes every G-th row.  Bulk copies bring the rows of
 // dy, r (or its codes) and dres into a ring in shared memory, NB_STAGES - 1
 // rows ahead, so that registers hold only the thread's columns of w and of the
-// weight gradient (fp32, over all of the CTA's rows).  A row is read twice from shared
-// memory: for the sum, which takes the row's one barrier, and for dx.  Rows held in
-// registers, with the next row's loads in flight, took 128 of them, one CTA an SM,
-// and 167 us for 16384 x 7168 from a checkpoint against 150 us.  The CTAs' partial
-// weight gradients go to the workspace [G][d] and a second kernel adds them in a
-// fixed order: results do not change from run to run.
+// weight gradient (fp32, over all of the CTA's rows).  A row is read twice from
+// shared memory: for the sum, which takes the row's one barrier, and for dx.
+// Bound by HBM: 16384 x 7168 takes 125 us from a checkpoint (6.6 TB/s) and 141 us
+// from bf16 (6.65 TB/s).  Rows held in registers, with the next row's loads in
+// flight, took 128 of them, one CTA an SM, and 167 us from a checkpoint.  The
+// CTAs' partial weight gradients go to the workspace [G][d] and a second kernel
+// adds them in a fixed order: results do not change from run to run.
 struct NormBwdParams {
   const uint8_t* dy;     // [M, d] bf16
   const uint8_t* r;      // [M, d] bf16, or (CK) its checkpoint codes
@@ -612,15 +618,16 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const float* __restrict__
   if (x == 0 && blockIdx.x * 32 + g0 < d) dw[blockIdx.x * 32 + g0] = __float2bfloat16_rn(t);
 }
 
-// Vectors of eight a thread holds of a row.  With rows enough to fill the device, four beyond 512 (16384 x
-// 7168 without a residual: 86 us, 114 with two); with fewer rows than SMs, two up to 1024 (more
-// threads a row: 3.2 against 3.4 us for one row of 7168).
+// Vectors of eight a thread holds of a row.  With rows enough to fill the
+// device, four beyond 512 (16384 x 7168 without a residual: 86 us, 114 with two);
+// with fewer rows than SMs, two up to 1024 (more threads a row: 3.2 against 3.4
+// us for one row of 7168).
 int vectors_of(int64_t M, int d8) { return d8 <= 256 ? 1 : d8 <= 512 || (d8 <= 1024 && M <= num_sms()) ? 2 : 4; }
 int threads_of(int d8, int V) { return ((d8 + V - 1) / V + 31) / 32 * 32; }
 
-// Backward: vectors and threads; CTAs an SM (896 threads' worth, while two stages of
-// their rows fit: with 512 or 1344 the backward pass of 16384 x 7168 from a checkpoint took
-// 235 or 174 us, not 150); ring stages.
+// Backward: vectors and threads; CTAs an SM (896 threads' worth, while two stages
+// of their rows fit: with 512 or 1344 the backward pass of 16384 x 7168 from a
+// checkpoint took 234 or 174 us, where 896 took 150 then and 125 now); ring stages.
 struct NormBwdShape {
   int V, T, ctas, stages, stage_bytes;
 };
@@ -663,10 +670,11 @@ int launch_add_rmsnorm_fwd(const NormFwdLaunch& a, cudaStream_t stream) {
     // Slices of a multiple of 256 columns (whole warps).  Enough rows: at least
     // 512 columns, so that clusters stay small (16384 x 2048: 64 us on four CTAs,
     // 75 on eight), on up to eight CTAs, sixteen where slices would pass 1024
-    // columns (their tile leaves an SM one CTA: 4096 x 16384, 189 us on eight, 133 on sixteen;
-    // 16384 x 7168, 217 on seven, 214 on ten, 227 on fourteen).  Few rows
-    // (under two 512-column slices an SM): as many CTAs as there can be (32 x 7168: 6.7 us on
-    // fourteen, 9.4 on seven; 1024 x 2048: 7.3 us on eight, 8.5 on four).
+    // columns (their tile leaves an SM one CTA: 4096 x 16384, 189 us on eight,
+    // 133 on sixteen; 16384 x 7168, 217 on seven, 214 on ten, 227 on fourteen).
+    // Few rows (under two 512-column slices an SM): as many CTAs as there can be
+    // (32 x 7168: 6.7 us on fourteen, 9.4 on seven; 1024 x 2048: 7.3 us on eight,
+    // 8.5 on four).
     const bool few = padded / NC_ROWS * ((p.d8 + 63) / 64) <= 2 * (int64_t)num_sms();
     const int most = few || p.d8 > 8 * 128 ? 16 : 8;
     const int slice8 = std::max(few ? 32 : 64, ((p.d8 + 31) / 32 + most - 1) / most * 32);
