@@ -65,26 +65,53 @@ MX_DEVINL f2 pair_add(f2 a, f2 b) {
   const float l = __fadd_rn(e, __fadd_rn(a.y, b.y)), h = __fadd_rn(s, l);
   return fabsf(s) < __uint_as_float(0x7F800000u) ? f2_pack(h, __fsub_rn(l, __fsub_rn(h, s))) : f2_pack(s, 0.0f);
 }
-// The squares of eight elements added to a pair: fp32 for four of them at a
-// time (each square is exact), unevaluated from there on, so that the row's sum
-// is off by some 1e-9 and not by the 5e-9 of one fp32 chain a thread.
 MX_DEVINL void squares8(const uint4& a, f2& s) {
   sumsq_bf16x2(a.x, s);
   sumsq_bf16x2(a.y, s);
   sumsq_bf16x2(a.z, s);
   sumsq_bf16x2(a.w, s);
 }
-MX_DEVINL f2 add_squares8(f2 sum, const uint4& a) {
-  f2 s = f2_splat(0.0f);
-  squares8(a, s);
-  return pair_add(sum, pair_add(f2_pack(s.x, 0.0f), f2_pack(s.y, 0.0f)));
+
+// Sums of squares as hi + lo: the squares are exact, up to eight are added in
+// fp32, and from there on each addition's rounding error goes to lo, so that a
+// row's sum is off by some 1e-9 and not by the 5e-9 of one fp32 chain a thread.
+// hi alone says whether a sum is finite (lo is then NaN); settle() before use.
+// Two sums at once, and one of hi + lo with another.
+MX_DEVINL f2 f2_sub(f2 a, f2 b) { return f2_fma(b, f2_splat(-1.0f), a); }
+MX_DEVINL void sum_add2(f2& hi, f2& lo, f2 v) {
+  const f2 s = f2_add(hi, v), t = f2_sub(s, hi);
+  lo = f2_add(lo, f2_add(f2_sub(hi, f2_sub(s, t)), f2_sub(v, t)));
+  hi = s;
 }
+MX_DEVINL void sum_add(f2& a, f2 b) {
+  const float s = __fadd_rn(a.x, b.x), t = __fsub_rn(s, a.x);
+  const float e = __fadd_rn(__fsub_rn(a.x, __fsub_rn(s, t)), __fsub_rn(b.x, t));
+  a = f2_pack(s, __fadd_rn(__fadd_rn(a.y, b.y), e));
+}
+MX_DEVINL f2 settle(f2 a) { return pair_add(f2_pack(a.x, 0.0f), f2_pack(0.0f, a.y)); }
 template <int FROM>
-MX_DEVINL f2 warp_sum_pair(f2 v) {
+MX_DEVINL f2 warp_sum_add(f2 v) {
 #pragma unroll
   for (int o = FROM; o > 0; o >>= 1)
-    v = pair_add(v, f2_pack(__shfl_xor_sync(0xFFFFFFFFu, v.x, o), __shfl_xor_sync(0xFFFFFFFFu, v.y, o)));
+    sum_add(v, f2_pack(__shfl_xor_sync(0xFFFFFFFFu, v.x, o), __shfl_xor_sync(0xFFFFFFFFu, v.y, o)));
   return v;
+}
+// The warp's sums of four rows (two a pair), row lane / 8 in each lane: a lane
+// hands on the rows of the other half, so 12 exchanges and not 40.
+MX_DEVINL f2 warp_sum_rows(const f2 (&hi)[2], const f2 (&lo)[2]) {
+  const int lane = threadIdx.x & 31;
+  const bool up = lane & 16;
+  f2 h = up ? hi[1] : hi[0], l = up ? lo[1] : lo[0];
+  const f2 sh = up ? hi[0] : hi[1], sl = up ? lo[0] : lo[1];
+  auto other = [](f2 v, int o) {
+    return f2_pack(__shfl_xor_sync(0xFFFFFFFFu, v.x, o), __shfl_xor_sync(0xFFFFFFFFu, v.y, o));
+  };
+  sum_add2(h, l, other(sh, 16));
+  l = f2_add(l, other(sl, 16));
+  const bool second = lane & 8;
+  f2 v = second ? f2_pack(h.y, l.y) : f2_pack(h.x, l.x);
+  sum_add(v, other(second ? f2_pack(h.x, l.x) : f2_pack(h.y, l.y), 8));
+  return warp_sum_add<4>(v);
 }
 
 // (ss / d + eps)^-1/2 as a pair: the rounded root and one Newton step's
@@ -107,7 +134,9 @@ MX_DEVINL f2 rstd_pair(f2 ss, float d, float eps) {
 // is that of r w n, where an fp32 value to nearest lands on the tie itself once
 // in a million times and goes to the even side: of 117 million codes 69 to 71
 // then differed from the 64-bit result, and 0 to 6 do with this and the sums above.
-// Zero becomes 2^-149, which rounds to a zero code and a zero bf16.
+// Zero becomes 2^-149, which rounds to a zero code and a zero bf16.  Where r w
+// passes fp32 (|w| >= 2^64; from |r| = 2^64 on n is zero) y is NaN; multiplying
+// r n by w for such weights cost 2.5% of every call.
 MX_DEVINL f2 norm2(uint32_t r, f2 n, uint32_t w) {
   const f2 rw = mul_bf16x2(r, w);
   const f2 y = __ffma2_rz(rw, f2_splat(n.x), f2_mul(rw, f2_splat(n.y)));
@@ -137,7 +166,7 @@ __global__ void __launch_bounds__(512) add_rmsnorm_row_kernel(NormFwdParams p) {
   if (row >= p.M) return;
   const int64_t base = row * p.d8;
   uint4 v[V];
-  f2 ss = f2_splat(0.0f);
+  f2 ss = f2_splat(0.0f), ss_lo = ss;
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     const int c = threadIdx.x + k * T;
@@ -159,17 +188,18 @@ __global__ void __launch_bounds__(512) add_rmsnorm_row_kernel(NormFwdParams p) {
   }
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    // without codes no tie hangs on the sum's last bits (8192 x 4096: 28 us, not 30)
-    if (p.q_row) ss = add_squares8(ss, v[k]);
-    else squares8(v[k], ss);
+    f2 sq = f2_splat(0.0f);
+    squares8(v[k], sq);
+    sum_add2(ss, ss_lo, sq);
   }
-  if (!p.q_row) ss = f2_pack(ss.x + ss.y, 0.0f);
   __shared__ f2 part[16];
   const int lane = threadIdx.x & 31;
-  f2 sum = warp_sum_pair<16>(ss);
+  f2 sum = f2_pack(ss.x, ss_lo.x);
+  sum_add(sum, f2_pack(ss.y, ss_lo.y));
+  sum = warp_sum_add<16>(sum);
   if (lane == 0) part[threadIdx.x >> 5] = sum;
   __syncthreads();
-  sum = warp_sum_pair<8>((lane & 15) < (T >> 5) ? part[lane & 15] : f2_splat(0.0f));
+  sum = settle(warp_sum_add<8>((lane & 15) < (T >> 5) ? part[lane & 15] : f2_splat(0.0f)));
   const f2 n = rstd_pair(sum, p.d, p.eps);
   if (threadIdx.x == 0) p.rstd[row] = n.x + n.y;
   const uint32_t up = p.rceil ? 0x1FFFFFu : 0u;
@@ -274,7 +304,7 @@ __global__ void __launch_bounds__(NC_THREADS, NC_CTAS_SM) add_rmsnorm_col_kernel
   const int rw = warp * 4;                                       // the warp's first row
   const int64_t at0 = (r0 + rw) * p.d8 + c0 + lane;              // its first vector
   uint4* trow = tile + rw * slice8 + (lane ^ (rw >= 16 ? 4 : 0));
-  f2 ss[4] = {};
+  f2 ss[2] = {}, ss_lo[2] = {};
   // x goes to the tile by asynchronous copies, all of them in flight at once;
   // the residual's vectors are loaded one step ahead
   const int steps = (n8 + 31) / 32;
@@ -310,7 +340,12 @@ __global__ void __launch_bounds__(NC_THREADS, NC_CTAS_SM) add_rmsnorm_col_kernel
       load_res(cb + 32);
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) ss[k] = add_squares8(ss[k], v[k]);
+    for (int k = 0; k < 2; ++k) {
+      f2 a2 = f2_splat(0.0f), b2 = a2;
+      squares8(v[2 * k], a2);
+      squares8(v[2 * k + 1], b2);
+      sum_add2(ss[k], ss_lo[k], f2_pack(a2.x + a2.y, b2.x + b2.y));
+    }
     if (CK) {
 #pragma unroll
       for (int k = 0; k < 4; k += 2) {
@@ -328,23 +363,17 @@ __global__ void __launch_bounds__(NC_THREADS, NC_CTAS_SM) add_rmsnorm_col_kernel
     }
   }
   const int n8_all = n8 & ~31;
-  f2 sum[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) sum[k] = warp_sum_pair<16>(ss[k]);
-  if (lane < ctas) {
-    // lane j: this CTA's sums of the warp's rows to CTA j of the cluster
-    const uint32_t dst = cluster_map(smem_u32(&part[rank][rw]), lane);
-#pragma unroll
-    for (int k = 0; k < 4; k += 2)
-      asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(dst + k * 8), "f"(sum[k].x), "f"(sum[k].y),
-                   "f"(sum[k + 1].x), "f"(sum[k + 1].y)
-                   : "memory");
-  }
+  const f2 sum = warp_sum_rows(ss, ss_lo);
+  // lane: this CTA's sum of row lane / 8 of the warp to CTAs lane % 8 and + 8 of the cluster
+  for (int j = lane & 7; j < ctas; j += 8)
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(cluster_map(smem_u32(&part[rank][rw + (lane >> 3)]), j)),
+                 "f"(sum.x), "f"(sum.y)
+                 : "memory");
   cluster_sync();  // every CTA's sums are here; the tile is complete too
   if (threadIdx.x < NC_ROWS) {
     f2 t = part[0][threadIdx.x];
-    for (int j = 1; j < ctas; ++j) t = pair_add(t, part[j][threadIdx.x]);  // the same order in every CTA
-    const f2 n = rstd_pair(t, p.d, p.eps);
+    for (int j = 1; j < ctas; ++j) sum_add(t, part[j][threadIdx.x]);  // the same order in every CTA
+    const f2 n = rstd_pair(settle(t), p.d, p.eps);
     s_n[threadIdx.x] = n;
     if (rank == 0) p.rstd[r0 + threadIdx.x] = n.x + n.y;
   }
@@ -526,6 +555,7 @@ __global__ void __launch_bounds__(T_MAX, CTAS) add_rmsnorm_bwd_kernel(NormBwdPar
       if (CK && c < p.d8) s_next[k] = p.ck_s[row * (p.d8 >> 2) + (c >> 2)];
     }
   };
+  bool lost = false;
   if (blockIdx.x < p.M) fetch(blockIdx.x);
   for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x, par ^= 1) {
     const uint8_t* in = ring + stage * p.stage_bytes;
@@ -553,10 +583,12 @@ __global__ void __launch_bounds__(T_MAX, CTAS) add_rmsnorm_bwd_kernel(NormBwdPar
     if ((threadIdx.x & 31) == 0) sums[par][threadIdx.x >> 5] = dot;
     // the row's barrier (the next row writes the other buffer); a wait that
     // ran out of its bound ends the kernel for the whole CTA, once the rows
-    // still on their way have come (or run out of the bound as well)
+    // still on their way have come (or run out of the bound as well), and makes
+    // dw NaN
     if (!__syncthreads_and(here)) {
       for (int k = 1; k < p.stages - 1 && row + (int64_t)k * gridDim.x < p.M; ++k)
         mbar_wait(&full[(stage + k) % p.stages], stage + k < p.stages ? phase : phase ^ 1, nullptr);
+      lost = true;
       break;
     }
     if (threadIdx.x == 0) {
@@ -595,6 +627,7 @@ __global__ void __launch_bounds__(T_MAX, CTAS) add_rmsnorm_bwd_kernel(NormBwdPar
     const int c = threadIdx.x + k * T;
     if (c >= p.d8) continue;
     float4* dst = reinterpret_cast<float4*>(p.part + ((int64_t)blockIdx.x * p.d8 + c) * 8);
+    if (lost) acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = f2_splat(__int_as_float(0x7FC00000));
     dst[0] = make_float4(acc[k][0].x, acc[k][0].y, acc[k][1].x, acc[k][1].y);
     dst[1] = make_float4(acc[k][2].x, acc[k][2].y, acc[k][3].x, acc[k][3].y);
   }

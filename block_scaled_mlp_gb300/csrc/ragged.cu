@@ -547,14 +547,14 @@ int launch_ragged(const RaggedLaunch& g, cudaStream_t stream) {
     p.F = (int32_t)g.N; p.C = (int32_t)g.K;
     if ((rc = map_w(&tA, 128)) || (rc = map2(&tB, g.a, g.K, bt / 2))) return rc;
     const int64_t units = t_units * ((g.N + RG_F - 1) / RG_F);
-    if (units > INT32_MAX) return fail(MX_ERR_UNSUPPORTED, "ragged product: too many tiles");
+    if (units > INT32_MAX - 1024) return fail(MX_ERR_UNSUPPORTED, "ragged product: too many tiles");
     return narrow ? launch_cfg<RG_FWD, 32>(tA, tB, tZ, p, units, stream) : launch_cfg<RG_FWD, 256>(tA, tB, tZ, p, units, stream);
   }
   if (mode == MX_RAGGED_DGRAD) {
     p.F = (int32_t)g.K; p.C = (int32_t)g.N;
     if ((rc = map_w(&tA, 64)) || (rc = map2(&tB, g.a, g.N, bt / 2))) return rc;
     const int64_t units = t_units * ((g.K + RG_F - 1) / RG_F);
-    if (units > INT32_MAX) return fail(MX_ERR_UNSUPPORTED, "ragged product: too many tiles");
+    if (units > INT32_MAX - 1024) return fail(MX_ERR_UNSUPPORTED, "ragged product: too many tiles");
     return narrow ? launch_cfg<RG_DGRAD, 32>(tA, tB, tZ, p, units, stream)
                   : launch_cfg<RG_DGRAD, 256>(tA, tB, tZ, p, units, stream);
   }
@@ -563,7 +563,7 @@ int launch_ragged(const RaggedLaunch& g, cudaStream_t stream) {
   for (int i = 0; i < 4; ++i)
     if ((rc = map2(&tZ.rows[i], g.b, g.K, 1u << i, CU_TENSOR_MAP_SWIZZLE_NONE))) return rc;
   const int64_t units = (int64_t)g.E * ((g.N + RG_F - 1) / RG_F) * ((g.K + 255) / 256);
-  if (units > INT32_MAX) return fail(MX_ERR_UNSUPPORTED, "ragged product: too many tiles");
+  if (units > INT32_MAX - 1024) return fail(MX_ERR_UNSUPPORTED, "ragged product: too many tiles");
   return launch_cfg<RG_WGRAD, 256>(tA, tB, tZ, p, units, stream);
 }
 
