@@ -149,19 +149,22 @@ MX_DEVINL void norm8(const uint4& r, f2 n, const uint4& w, f2 (&y)[4]) {
   y[3] = norm2(r.w, n, w.w);
 }
 
-// ---- rows: one CTA per row, the row in registers (V vectors of eight a
-// thread).  CTAs past M only clear the scale layout's padding rows.  Bound by
-// HBM from some hundred rows on: 16384 x 7168 with a residual into row codes and
-// bf16 162 us (6.5 TB/s); below that by the latency of one row (1 x 7168: 3.1 us).
-template <int V>
+// ---- rows: one CTA per row, or (WARP) one warp, ROW_WARPS of them a CTA; the
+// row in registers, V vectors of eight a thread.  Rows past M only clear the
+// scale layout's padding rows.  Bound by HBM from some hundred rows on: 16384 x
+// 7168 with a residual into row codes and bf16 158 us (6.7 TB/s), 8192 x 4096 into
+// bf16 22.5 us (6.0 TB/s); below that by the latency of one row (1 x 7168: 3.0 us).
+constexpr int ROW_WARPS = 4;
+template <int V, bool WARP>
 __global__ void __launch_bounds__(512) add_rmsnorm_row_kernel(NormFwdParams p) {
   pdl_begin();
-  const int64_t row = blockIdx.x;
-  const int T = blockDim.x;
+  const int lane = threadIdx.x & 31;
+  const int T = WARP ? 32 : blockDim.x, t = WARP ? lane : threadIdx.x;
+  const int64_t row = WARP ? (int64_t)blockIdx.x * ROW_WARPS + (threadIdx.x >> 5) : blockIdx.x;
   if (p.q_row && p.s_row.mma) {
-    // zeros where the layout is padded: whole rows past M, columns past d / 32
+    // zeros where the layout is padded (to 128 rows): whole rows past M, columns past d / 32
     const int S = p.d8 / 4, S4 = (S + 3) & ~3;
-    for (int c = (row < p.M ? S : 0) + threadIdx.x; c < S4; c += T) p.s_row.put(row, c, 0);
+    for (int c = (row < p.M ? S : 0) + t; c < S4; c += T) p.s_row.put(row, c, 0);
   }
   if (row >= p.M) return;
   const int64_t base = row * p.d8;
@@ -169,19 +172,19 @@ __global__ void __launch_bounds__(512) add_rmsnorm_row_kernel(NormFwdParams p) {
   f2 ss = f2_splat(0.0f), ss_lo = ss;
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    const int c = threadIdx.x + k * T;
+    const int c = t + k * T;
     v[k] = c < p.d8 ? ld_once(p.x + base + c) : make_uint4(0, 0, 0, 0);
   }
   if (p.res) {
     uint4 a[V];
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      const int c = threadIdx.x + k * T;
+      const int c = t + k * T;
       a[k] = c < p.d8 ? ld_once(p.res + base + c) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      const int c = threadIdx.x + k * T;
+      const int c = t + k * T;
       v[k] = add8(v[k], a[k]);
       if (c < p.d8) p.r[base + c] = v[k];
     }
@@ -192,22 +195,24 @@ __global__ void __launch_bounds__(512) add_rmsnorm_row_kernel(NormFwdParams p) {
     squares8(v[k], sq);
     sum_add2(ss, ss_lo, sq);
   }
-  __shared__ f2 part[16];
-  const int lane = threadIdx.x & 31;
   f2 sum = f2_pack(ss.x, ss_lo.x);
   sum_add(sum, f2_pack(ss.y, ss_lo.y));
   sum = warp_sum_add<16>(sum);
-  if (lane == 0) part[threadIdx.x >> 5] = sum;
-  __syncthreads();
-  sum = settle(warp_sum_add<8>((lane & 15) < (T >> 5) ? part[lane & 15] : f2_splat(0.0f)));
+  if (!WARP) {
+    __shared__ f2 part[16];
+    if (lane == 0) part[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    sum = warp_sum_add<8>((lane & 15) < (T >> 5) ? part[lane & 15] : f2_splat(0.0f));
+  }
+  sum = settle(sum);
   const f2 n = rstd_pair(sum, p.d, p.eps);
-  if (threadIdx.x == 0) p.rstd[row] = n.x + n.y;
+  if (t == 0) p.rstd[row] = n.x + n.y;
   const uint32_t up = p.rceil ? 0x1FFFFFu : 0u;
   // two vectors of the row at a time (V = 1: one, and zeros), so that two
   // blocks share the scales' exchange
 #pragma unroll
   for (int k = 0; k < V; k += 2) {
-    const int c0 = threadIdx.x + k * T, c1 = c0 + T;
+    const int c0 = t + k * T, c1 = c0 + T;
     const bool in0 = c0 < p.d8, in1 = V > 1 && c1 < p.d8;
     const uint4 z = make_uint4(0, 0, 0, 0), v0 = v[k], v1 = V > 1 ? v[k + (V > 1)] : z;
     if (p.ck) {
@@ -651,11 +656,28 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const float* __restrict__
   if (x == 0 && blockIdx.x * 32 + g0 < d) dw[blockIdx.x * 32 + g0] = __float2bfloat16_rn(t);
 }
 
-// Vectors of eight a thread holds of a row.  With rows enough to fill the
-// device, four beyond 512 (16384 x 7168 without a residual: 86 us, 114 with two);
-// with fewer rows than SMs, two up to 1024 (more threads a row: 3.2 against 3.4
-// us for one row of 7168).
-int vectors_of(int64_t M, int d8) { return d8 <= 256 ? 1 : d8 <= 512 || (d8 <= 1024 && M <= num_sms()) ? 2 : 4; }
+// How a row is held: vectors of eight a thread, and by a warp or a CTA.
+//   Few rows (two an SM or fewer): many threads a row (1 x 7168: 3.2 against 3.4
+// us with two vectors against four; 152 x 1024: 1.8 against 2.1 with one and two).
+//   Else as many loads in flight as the registers allow, which is four vectors,
+// or two of x and two of the residual: without one, 8192 x 4096 takes 22.5 us with
+// four and 27.0 with two, 16384 x 7168 75.9 and 92.3; with one 48.0 and 49.1, 158
+// and 162; 16384 x 2048 47 with two, 58 with one.  Past 8192 columns a CTA's 512
+// threads need four (without a residual 128 us; 131 with eight), or take eight
+// (with one: 184 us for 8192 x 16384; 198 with four).
+//   Up to 512 columns, and to 1024 without a residual, a warp has a row: CTAs of
+// one row cannot start faster (65536 x 512: 23 us, 66 with them; 32768 x 1024
+// without a residual 22 against 33, with one 48 against 47).
+struct RowShape {
+  int V;
+  bool warp;
+};
+RowShape row_shape(int64_t M, int d8, bool res) {
+  if (M <= 2 * (int64_t)num_sms()) return {d8 <= 256 ? 1 : d8 <= 1024 ? 2 : 4, false};
+  if (d8 <= 64) return {2, true};
+  if (d8 <= 128 && !res) return {4, true};
+  return {d8 > 1024 ? (res ? 8 : 4) : res ? 2 : 4, false};
+}
 int threads_of(int d8, int V) { return ((d8 + V - 1) / V + 31) / 32 * 32; }
 
 // Backward: vectors and threads; CTAs an SM (896 threads' worth, while two stages
@@ -732,10 +754,18 @@ int launch_add_rmsnorm_fwd(const NormFwdLaunch& a, cudaStream_t stream) {
                                          dim3(1, (unsigned)ctas), p, (int32_t)slice8),
                        "add_rmsnorm_col_kernel launch");
   }
-  const int V = vectors_of(a.M, p.d8), T = threads_of(p.d8, V);
+  const RowShape sh = row_shape(a.M, p.d8, p.res != nullptr);
   count_launch(MX_KERNEL_NORM);
-  auto k = V == 1 ? add_rmsnorm_row_kernel<1> : V == 2 ? add_rmsnorm_row_kernel<2> : add_rmsnorm_row_kernel<4>;
-  return cuda_status(launch_overlapped(k, (unsigned)padded, T, 0, stream, 1, p), "add_rmsnorm_row_kernel launch");
+  if (sh.warp)
+    return cuda_status(launch_overlapped(sh.V == 2 ? add_rmsnorm_row_kernel<2, true> : add_rmsnorm_row_kernel<4, true>,
+                                         (unsigned)((padded + ROW_WARPS - 1) / ROW_WARPS), ROW_WARPS * 32, 0, stream, 1, p),
+                       "add_rmsnorm_row_kernel launch");
+  auto k = sh.V == 1   ? add_rmsnorm_row_kernel<1, false>
+           : sh.V == 2 ? add_rmsnorm_row_kernel<2, false>
+           : sh.V == 4 ? add_rmsnorm_row_kernel<4, false>
+                       : add_rmsnorm_row_kernel<8, false>;
+  return cuda_status(launch_overlapped(k, (unsigned)padded, threads_of(p.d8, sh.V), 0, stream, 1, p),
+                     "add_rmsnorm_row_kernel launch");
 }
 
 int launch_add_rmsnorm_bwd(const NormBwdLaunch& a, cudaStream_t stream) {

@@ -89,6 +89,37 @@ def test_forward(M, d, residual, axis, layout, floor):
     assert torch.equal(ref64.f64(mx.ckpt8_load(f["ckpt"])), ref64.int8_values(r.double()))
 
 
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("d,axis", [(8, 0), (32, 1), (200, 0), (256, 1), (512, 1), (520, 0), (544, 1), (1024, 1), (1032, 0),
+                                    (1056, 1), (2080, 1), (4096, 1), (8192, 1), (8200, 0), (8224, 1), (16384, 1)])
+def test_forward_of_many_rows(d, axis, residual):
+    """More rows than two an SM: the forms that hold a row in a warp and in a CTA.  Padding reads zero in buffers
+    that held something else."""
+    M = 2 * 160 + 11
+    x, res, w = _inputs(M, d, residual, 5 + d)
+    P = lambda t: None if t is None else ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    r = x if res is None else (x.float() + res.float()).to(torch.bfloat16)
+    xc, wc, rc = x.cuda(), w.cuda(), None if res is None else res.cuda()
+    out_r, out_y, rstd = torch.empty_like(xc), torch.empty_like(xc), torch.empty(M, device="cuda")
+    q = torch.full((M, d), 0xAB, dtype=torch.uint8, device="cuda")
+    s = torch.full((mx.mma_scale_bytes(M, d) if axis else 1,), 0xAB, dtype=torch.uint8, device="cuda")
+    ck, cs = torch.empty((M, d), dtype=torch.int8, device="cuda"), torch.empty((M, d // 32), dtype=torch.uint8, device="cuda")
+    st = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    assert mx.lib().mx_add_rmsnorm_fwd(P(xc), P(rc), P(wc), M, d, EPS, P(out_r) if residual else None, P(rstd), P(out_y), axis,
+                                       1, 0, P(q) if axis else None, P(s) if axis else None, None, None,
+                                       P(ck) if axis else None, P(cs) if axis else None, st) == 0
+    y, n = ref64.rmsnorm(r.double(), w.double(), EPS)
+    if residual:
+        assert torch.equal(out_r.cpu(), r)
+    assert torch.all((ref64.f64(rstd) - n).abs() <= n * EY)
+    assert torch.all((ref64.f64(out_y) - y).abs() <= y.abs() * (2.0 ** -8 + EY))
+    if axis:
+        s2, pad = ref64.untile(s, M, d // 32)
+        assert not pad.any()
+        _check_codes(q, s2, y)
+        assert torch.equal(ref64.f64(mx.ckpt8_load(mx.Ckpt8(ck, cs))), ref64.int8_values(r.double()))
+
+
 @pytest.mark.parametrize("M,d", [(1, 8), (7, 40), (3, 1000), (2, 16376)])
 def test_forward_widths_without_codes(M, d):
     x, res, w = _inputs(M, d, True, d)
