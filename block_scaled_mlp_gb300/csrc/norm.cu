@@ -680,20 +680,24 @@ RowShape row_shape(int64_t M, int d8, bool res) {
 }
 int threads_of(int d8, int V) { return ((d8 + V - 1) / V + 31) / 32 * 32; }
 
-// Backward: vectors and threads; CTAs an SM (896 threads' worth, while two stages
-// of their rows fit: with 512 or 1344 the backward pass of 16384 x 7168 from a
-// checkpoint took 234 or 174 us, where 896 took 150 then and 125 now); ring stages.
+// Backward: vectors and threads, CTAs an SM, ring stages.  Four vectors a thread:
+// few warps meet at a row's barrier, and several rows are under way.  512 threads
+// an SM from a checkpoint (with a residual gradient, against 896 threads with two
+// vectors: 8192 x 8192 77 us and 104, 16384 x 5120 94 and 103), 384 from bf16, whose
+// rows need fewer instructions and fill the ring sooner (16384 x 8192 153 us, 158
+// with 512; 16384 x 5120 without a residual gradient 77 and 87).  Up to 512 columns
+// a warp has a row, 24 of them an SM (65536 x 512: 51 us, 56 with 16).
 struct NormBwdShape {
   int V, T, ctas, stages, stage_bytes;
 };
 NormBwdShape bwd_shape(int64_t d, bool ck, bool dres) {
   NormBwdShape s;
   const int d8 = (int)(d / 8);
-  s.V = d8 <= 256 ? 1 : d8 <= 1024 ? 2 : 4;
+  s.V = d8 <= 32 ? 1 : d8 <= 64 ? 2 : 4;
   s.T = threads_of(d8, s.V);
   s.stage_bytes = (int)((d * (2 + (ck ? 1 : 2) + (dres ? 2 : 0)) + 127) / 128 * 128);
   const int smem = 220 * 1024;
-  s.ctas = std::max(1, std::min(8, 896 / s.T));
+  s.ctas = std::max(1, s.V < 4 ? 24 : (ck ? 512 : 384) / s.T);
   while (s.ctas > 1 && (smem / s.ctas - 1024) / s.stage_bytes < 2) --s.ctas;
   s.stages = std::min(NB_MAX_STAGES, (smem / s.ctas - 1024) / s.stage_bytes);
   return s;
@@ -701,11 +705,15 @@ NormBwdShape bwd_shape(int64_t d, bool ck, bool dres) {
 
 }  // namespace
 
+// CTAs of the backward pass: each with two rows at least, beyond two an SM (1200 x
+// 1024: 6.2 us, 8.0 with a row each, whose partial gradients outweigh it).
+int bwd_grid(int64_t M, int ctas_sm) {
+  const int64_t sms = num_sms();
+  return (int)std::min(std::min(M, ctas_sm * sms), std::max(2 * sms, M / 2));
+}
 // Rows of partial weight gradients, whatever is kept of r and with or without
 // a residual gradient.
-int norm_bwd_ctas(int64_t M, int64_t d) {
-  return (int)std::min<int64_t>(M, (int64_t)bwd_shape(d, true, false).ctas * num_sms());
-}
+int norm_bwd_ctas(int64_t M, int64_t d) { return bwd_grid(M, bwd_shape(d, true, false).ctas); }
 
 int launch_add_rmsnorm_fwd(const NormFwdLaunch& a, cudaStream_t stream) {
   NormFwdParams p{};
@@ -776,11 +784,11 @@ int launch_add_rmsnorm_bwd(const NormBwdLaunch& a, cudaStream_t stream) {
   p.part = (float*)a.workspace;
   p.M = a.M; p.d8 = (int32_t)(a.d / 8); p.inv_d = 1.0f / (float)a.d;
   p.stages = s.stages; p.stage_bytes = s.stage_bytes;
-  const int G = (int)std::min<int64_t>(a.M, (int64_t)s.ctas * num_sms());
+  const int G = bwd_grid(a.M, s.ctas);
   const size_t smem = (size_t)s.stages * s.stage_bytes;
   using Kernel = void (*)(NormBwdParams);
 #define MX_NB(V, T, C) {add_rmsnorm_bwd_kernel<V, T, C, false>, add_rmsnorm_bwd_kernel<V, T, C, true>}
-  static const Kernel kernels[3][2] = {MX_NB(1, 256, 3), MX_NB(2, 512, 2), MX_NB(4, 512, 1)};
+  static const Kernel kernels[3][2] = {MX_NB(1, 32, 24), MX_NB(2, 32, 24), MX_NB(4, 512, 1)};
 #undef MX_NB
   const Kernel k = kernels[s.V == 1 ? 0 : s.V == 2 ? 1 : 2][a.ck != nullptr];
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
