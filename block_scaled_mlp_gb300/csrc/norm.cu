@@ -473,8 +473,8 @@ __global__ void __launch_bounds__(NC_THREADS, NC_CTAS_SM) add_rmsnorm_col_kernel
 // rows ahead, so that registers hold only the thread's columns of w and of the
 // weight gradient (fp32, over all of the CTA's rows).  A row is read twice from
 // shared memory: for the sum, which takes the row's one barrier, and for dx.
-// Bound by HBM: 16384 x 7168 takes 125 us from a checkpoint (6.6 TB/s) and 141 us
-// from bf16 (6.65 TB/s).  Rows held in registers, with the next row's loads in
+// Bound by HBM: 16384 x 7168 takes 126 us from a checkpoint (6.6 TB/s) and 137 us
+// from bf16 (6.9 TB/s).  Rows held in registers, with the next row's loads in
 // flight, took 128 of them, one CTA an SM, and 167 us from a checkpoint.  The
 // CTAs' partial weight gradients go to the workspace [G][d] and a second kernel
 // adds them in a fixed order: results do not change from run to run.
