@@ -20,6 +20,10 @@
 // end in shared memory first, in both operands, so that nothing the next group
 // holds (NaN included) enters the sum.
 //
+// Where tiles are fewer than pairs, the pairs of a cluster share a tile's
+// contraction (S of them); the first pair adds the others' fp32 sums, sent
+// through distributed shared memory, in order.
+//
 // One persistent CTA pair per two SMs, roles as in gemm.cu: warp 0 loads
 // (TMA), warp 1 issues MMAs (even CTA), warps 2-9 drain accumulators (two of
 // them, so a tile's stores overlap the next tile's MMAs), warp 10 clears
@@ -44,13 +48,13 @@ constexpr int RG_EPI = 8;                 // epilogue warps
 constexpr int RG_MAX_E = 1024;
 constexpr int RG_F = 256;                 // features per pair tile
 
-template <int MODE, int BT>
+// BT: columns of a token tile; S: CTA pairs that share a tile's contraction.
+template <int MODE, int BT, int S>
 struct RCfg {
   static constexpr bool A_MN = MODE != RG_FWD, B_MN = MODE == RG_WGRAD;
   static constexpr int A_BYTES = 128 * 128;              // 128 features x 64 contraction elements
   static constexpr int B_BYTES = (BT / 2) * 128;         // this CTA's half of the tile
   static constexpr int TX = A_BYTES + B_BYTES;
-  static constexpr int STAGES = BT == 256 ? 6 : 11;
   static constexpr int EPI_WARP = MODE == RG_WGRAD ? 4096 : 2048;  // a warp's 32 x 64 or 32 x 32 bf16 block
   static constexpr int EPI_BYTES = RG_EPI * EPI_WARP;
   // Group ends and running unit numbers.  WGRAD needs the ends only, and its
@@ -58,12 +62,16 @@ struct RCfg {
   // from global memory (620 against 575 us for 64 experts of 8 rows, 4096 x 7168).
   static constexpr int ENDS = MODE == RG_WGRAD ? 128 : RG_MAX_E;
   static constexpr int TABLE = ENDS * (MODE == RG_WGRAD ? 4 : 8);
+  static constexpr int PART = BT * 128 * 4;              // one CTA's accumulator
+  static constexpr int PARTS = (S - 1) * PART;           // in a tile's first pair: the other pairs'
   static constexpr int TMEM = 2 * BT;                    // two accumulators
   static constexpr int THREADS = 64 + RG_EPI * 32 + (MODE == RG_WGRAD ? 32 : 0);
   static constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | (A_MN ? 1u << 15 : 0u) |
                                     (B_MN ? 1u << 16 : 0u) | ((uint32_t)(RG_F >> 4) << 24);
-  static constexpr size_t SMEM = (size_t)STAGES * TX + EPI_BYTES + TABLE + 512 /*barriers*/ + 1024 /*align*/;
-  static_assert(BT == 256 || (BT == 32 && MODE != RG_WGRAD), "tile widths");
+  static constexpr int STAGES = (226 * 1024 - EPI_BYTES - PARTS - TABLE - 1536) / TX;
+  static constexpr size_t SMEM = (size_t)STAGES * TX + EPI_BYTES + PARTS + TABLE + 512 /*barriers*/ + 1024 /*align*/;
+  static_assert((BT == 256 && S == 1) || (BT <= 64 && MODE != RG_WGRAD), "tile widths");
+  static_assert(S == 1 || S == 2 || S == 4, "at most eight CTAs a cluster");
   static_assert(SMEM + 1024 /*static*/ <= 227 * 1024, "shared memory");
 };
 
@@ -91,6 +99,25 @@ MX_DEVINL void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
 struct ZeroMaps {
   CUtensorMap rows[4];
 };
+
+// Bounded wait for arrivals from other CTAs of the cluster, whose writes it makes visible.
+MX_DEVINL bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, int32_t* err) {
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      record_error(err, MX_ERR_TIMEOUT);
+      return false;
+    }
+  }
+}
 
 struct Unit {
   int32_t e;
@@ -149,31 +176,35 @@ MX_DEVINL Unit unit_of(const RaggedParams& p, const int32_t* ends, const int32_t
   return r;
 }
 
-template <int MODE, int BT>
-__global__ void __launch_bounds__(RCfg<MODE, BT>::THREADS, 1)
+template <int MODE, int BT, int S>
+__global__ void __launch_bounds__(RCfg<MODE, BT, S>::THREADS, 1)
     ragged_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                   const __grid_constant__ ZeroMaps tmZ, RaggedParams p) {
-  using C = RCfg<MODE, BT>;
+  using C = RCfg<MODE, BT, S>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
   uint8_t* sB = sA + C::STAGES * C::A_BYTES;
   uint8_t* sEpi = sB + C::STAGES * C::B_BYTES;
-  int32_t* s_ends = reinterpret_cast<int32_t*>(sEpi + C::EPI_BYTES);
+  uint8_t* sParts = sEpi + C::EPI_BYTES;
+  int32_t* s_ends = reinterpret_cast<int32_t*>(sParts + C::PARTS);
   int32_t* unit_end = s_ends + C::ENDS;  // not WGRAD
   const int32_t* ends = s_ends;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sEpi + C::EPI_BYTES + C::TABLE);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sParts + C::PARTS + C::TABLE);
   uint64_t* empty = full + C::STAGES;
   uint64_t* acc_full = empty + C::STAGES;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* done_bar = acc_empty + 2;
   uint64_t* tail_bar = done_bar + 1;   // WGRAD, by stage: a tail's bytes are here
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(tail_bar + C::STAGES);
+  uint64_t* parts_bar = tail_bar + C::STAGES;  // S > 1, by epilogue warp: the other pairs' sums are here
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(parts_bar + RG_EPI);
   __shared__ int s_ok, s_units;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = (int)cluster_ctarank();
-  const int32_t unit0 = blockIdx.x / 2, ustep = gridDim.x / 2;
+  const int crank = (int)cluster_ctarank();
+  const int rank = crank & 1, lead = crank & ~1;   // of the pair; its even CTA
+  const int part = crank >> 1;                     // the pair's share of the contraction
+  const int32_t unit0 = blockIdx.x / (2 * S), ustep = gridDim.x / (2 * S);
   const int32_t f_tiles = (p.F + RG_F - 1) / RG_F;
 
   if (threadIdx.x == 0) {
@@ -182,6 +213,7 @@ __global__ void __launch_bounds__(RCfg<MODE, BT>::THREADS, 1)
     for (int a = 0; a < 2; ++a) { mbar_init(&acc_full[a], 1); mbar_init(&acc_empty[a], 2 * RG_EPI); }
     for (int s = 0; s < C::STAGES; ++s) mbar_init(&tail_bar[s], 1);
     mbar_init(done_bar, 1);
+    for (int w = 0; w < RG_EPI; ++w) mbar_init(&parts_bar[w], S > 1 ? 32 * (S - 1) : 1);
     fence_mbar_init();
   }
   if (warp == 1) { tmem_alloc_pair(tmem_holder, C::TMEM); tmem_relinquish_pair(); }
@@ -239,7 +271,8 @@ __global__ void __launch_bounds__(RCfg<MODE, BT>::THREADS, 1)
       const Unit t = unit_of<MODE, BT>(p, ends, unit_end, u);
       const int32_t f = t.f0 + rank * 128;
       const int32_t b0 = (int32_t)(t.t0 + rank * (t.n_eff / 2));
-      for (int kb = 0; kb < t.num_kb; ++kb) {
+      const int kb0 = t.num_kb * part / S, kb1 = t.num_kb * (part + 1) / S;
+      for (int kb = kb0; kb < kb1; ++kb) {
         if (!warp_wait(&empty[stage], phase ^ 1, p.err)) { ok = false; break; }
         if (leader) {
           uint8_t* dA = sA + stage * C::A_BYTES;
@@ -251,9 +284,9 @@ __global__ void __launch_bounds__(RCfg<MODE, BT>::THREADS, 1)
             // the step's bytes complete on this CTA's own barrier, and the
             // zeros that follow them on the pair's full barrier
             mbar_arrive_expect_tx(&tail_bar[stage], C::TX);
-            bar = cluster_map(smem_u32(&tail_bar[stage]), rank);
+            bar = cluster_map(smem_u32(&tail_bar[stage]), crank);
           } else {
-            bar = cluster_map(smem_u32(&full[stage]), 0);
+            bar = cluster_map(smem_u32(&full[stage]), lead);
             if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * C::TX);
           }
           if (MODE == RG_FWD) {
@@ -295,7 +328,8 @@ __global__ void __launch_bounds__(RCfg<MODE, BT>::THREADS, 1)
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(acc * BT);
         const uint32_t idesc = C::IDESC | ((uint32_t)(t.n_eff >> 3) << 17);
-        for (int kb = 0; kb < t.num_kb; ++kb) {
+        const int kb0 = t.num_kb * part / S, kb1 = t.num_kb * (part + 1) / S;
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!warp_wait(&full[stage], phase, p.err)) { ok = false; break; }
           tc_fence_after();
           const uint64_t ad = a0 + (uint64_t)((stage * C::A_BYTES) >> 4);
@@ -304,18 +338,18 @@ __global__ void __launch_bounds__(RCfg<MODE, BT>::THREADS, 1)
           if (leader) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              if (k < nk) mma_bf16_pair(d, ad + k * a_step, bd + k * b_step, idesc, kb > 0 || k > 0);
-            tc_commit_pair_mc(&empty[stage], (uint16_t)0x3);
+              if (k < nk) mma_bf16_pair(d, ad + k * a_step, bd + k * b_step, idesc, kb > kb0 || k > 0);
+            tc_commit_pair_mc(&empty[stage], (uint16_t)(0x3 << lead));
           }
           __syncwarp();
           if (++stage == C::STAGES) { stage = 0; phase ^= 1; }
         }
         if (!ok) break;
-        if (leader) tc_commit_pair_mc(&acc_full[acc], (uint16_t)0x3);
+        if (leader) tc_commit_pair_mc(&acc_full[acc], (uint16_t)(0x3 << lead));
         __syncwarp();
         if (++acc == 2) { acc = 0; acc_phase ^= 1; }
       }
-      if (leader) tc_commit_pair_mc(done_bar, (uint16_t)0x1);
+      if (leader) tc_commit_pair_mc(done_bar, (uint16_t)(0x1 << lead));
       __syncwarp();
       mbar_wait(done_bar, 0, p.err);
     }
@@ -339,7 +373,7 @@ __global__ void __launch_bounds__(RCfg<MODE, BT>::THREADS, 1)
         if (!warp_wait(&tail_bar[stage], (phases >> stage) & 1, p.err)) break;
         phases ^= 1u << stage;
         if (leader) {
-          const uint32_t bar = cluster_map(smem_u32(&full[stage]), 0);
+          const uint32_t bar = cluster_map(smem_u32(&full[stage]), lead);
           if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * 4 * rows * 128);
           for (int b = 0; b < 4; ++b) {
             uint8_t* at = (b < 2 ? sA + stage * C::A_BYTES + b * 8192 : sB + stage * C::B_BYTES + (b - 2) * 8192) + t.tail * 128;
@@ -364,7 +398,7 @@ __global__ void __launch_bounds__(RCfg<MODE, BT>::THREADS, 1)
     auto dw_at = [&](const Unit& t, int32_t n, int32_t col) {
       return p.out + (((int64_t)t.e * p.F + n) * p.T + t.t0 + col) * 2;
     };
-    constexpr int NC = BT == 32 ? 1 : BT / 64, STEP = NC == 1 ? 1 : 2;
+    constexpr int NC = BT <= 64 ? 1 : BT / 64, STEP = NC == 1 ? 1 : 2;
     // columns of the warp's block j: pairs of neighbours in WGRAD (whole
     // 128-byte lines of a row), every other one else, so that a short tile keeps both
     // warps of a lane quarter busy
@@ -417,11 +451,37 @@ __global__ void __launch_bounds__(RCfg<MODE, BT>::THREADS, 1)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
-            if (rank != 0) mbar_arrive_cluster_relaxed(cluster_map(smem_u32(&acc_empty[acc]), 0));
+            if (rank != 0) mbar_arrive_cluster_relaxed(cluster_map(smem_u32(&acc_empty[acc]), lead));
             else mbar_arrive(&acc_empty[acc]);
           }
         }
         if (f >= p.F) continue;
+        if (S > 1 && col_of(0) < t.tn) {
+          // the other pairs' sums of this block to the first pair, which adds them in order
+          const uint32_t at = (uint32_t)(ew * 32 + lane) * 16;   // 8 vectors of 4 tokens, 4 KB apart
+          constexpr int V_STEP = RG_EPI * 512 / (BT == 32 ? 2 : 1);
+          if (part) {
+            const uint32_t dst = cluster_map(smem_u32(sParts), rank) + (part - 1) * C::PART + at;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + i * V_STEP), "r"(r[0][4 * i]),
+                           "r"(r[0][4 * i + 1]), "r"(r[0][4 * i + 2]), "r"(r[0][4 * i + 3])
+                           : "memory");
+            mbar_arrive_cluster(cluster_map(smem_u32(&parts_bar[ew]), rank));
+            continue;
+          }
+          if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&parts_bar[ew], 0, p.err))) break;
+#pragma unroll
+          for (int o = 0; o < S - 1; ++o)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 v = *reinterpret_cast<const float4*>(sParts + o * C::PART + at + i * V_STEP);
+              r[0][4 * i] = __float_as_uint(__uint_as_float(r[0][4 * i]) + v.x);
+              r[0][4 * i + 1] = __float_as_uint(__uint_as_float(r[0][4 * i + 1]) + v.y);
+              r[0][4 * i + 2] = __float_as_uint(__uint_as_float(r[0][4 * i + 2]) + v.z);
+              r[0][4 * i + 3] = __float_as_uint(__uint_as_float(r[0][4 * i + 3]) + v.w);
+            }
+        }
         if (MODE == RG_WGRAD) {
           // lane: a row of dw, 64 columns of it; through shared memory (16-byte
           // chunk k of row r at k ^ (r & 7)) so that eight lanes write a row's line
@@ -476,53 +536,110 @@ __global__ void __launch_bounds__(RCfg<MODE, BT>::THREADS, 1)
   if (warp == 1) tmem_dealloc_pair(tmem, C::TMEM);
 }
 
-template <int MODE, int BT>
+// Clusters that can be resident at once, by device.
+template <int MODE, int BT, int S>
+int resident_clusters(int* n) {
+  using C = RCfg<MODE, BT, S>;
+  static int resident[64] = {0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_status(e, "cudaGetDevice");
+  int& r = resident[dev & 63];
+  if (r == 0) {
+    auto k = ragged_kernel<MODE, BT, S>;
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+    if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute");
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * S * (num_sms() / (2 * S)));
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2 * S;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int m = 0;
+    e = cudaOccupancyMaxActiveClusters(&m, k, &cfg);
+    if (e != cudaSuccess || m <= 0)
+      return cuda_status(e != cudaSuccess ? e : cudaErrorInvalidConfiguration, "cudaOccupancyMaxActiveClusters");
+    r = m;
+  }
+  *n = r;
+  return MX_OK;
+}
+
+template <int MODE, int BT, int S>
 int launch_cfg(const CUtensorMap& tA, const CUtensorMap& tB, const ZeroMaps& tZ, const RaggedParams& p, int64_t units,
                cudaStream_t stream) {
-  using C = RCfg<MODE, BT>;
-  auto k = ragged_kernel<MODE, BT>;
+  using C = RCfg<MODE, BT, S>;
+  auto k = ragged_kernel<MODE, BT, S>;
+  int nres = 0;
+  if (int rc = resident_clusters<MODE, BT, S>(&nres)) return rc;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
   if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute");
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(C::THREADS);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  static int resident[64] = {0};  // pairs that can be resident at once, by device
-  int dev = 0;
-  cudaGetDevice(&dev);
-  int& nres = resident[dev & 63];
-  if (nres == 0) {
-    cfg.gridDim = dim3(2 * (num_sms() / 2));
-    int n = 0;
-    e = cudaOccupancyMaxActiveClusters(&n, k, &cfg);
-    if (e != cudaSuccess || n <= 0)
-      return cuda_status(e != cudaSuccess ? e : cudaErrorInvalidConfiguration, "cudaOccupancyMaxActiveClusters");
-    nres = n;
-  }
+  // S > 1: a cluster has one tile at most (its buffer for the other pairs' sums is written once)
+  const int64_t clusters = std::max<int64_t>(1, S > 1 ? units : std::min<int64_t>(units, nres));
   count_launch(MX_KERNEL_RAGGED);
-  return cuda_status(launch_overlapped(k, 2 * (unsigned)std::max<int64_t>(1, std::min<int64_t>(units, nres)), C::THREADS,
-                                       C::SMEM, stream, 2, tA, tB, tZ, p),
+  return cuda_status(launch_overlapped(k, (unsigned)(2 * S * clusters), C::THREADS, C::SMEM, stream, 2 * S, tA, tB, tZ, p),
                      "ragged_kernel launch");
+}
+
+
+// Tiles of bt token rows, at most: any group that has rows may end in a part of one.
+int64_t tile_bound(const RaggedLaunch& g, const RaggedParams& p, int bt) {
+  const int64_t groups = std::min<int64_t>(g.E, g.M);
+  return (g.M + groups * (bt - 1)) / bt * ((p.F + RG_F - 1) / RG_F);
+}
+
+// Token rows to a tile and pairs to a tile's contraction (FWD, DGRAD).
+//   Few tiles: an SM takes in some 110 GB/s, so a long contraction is shared by
+// the pairs of a cluster, in one wave of clusters (8 rows of one group, us without,
+// with two and with four pairs: 512 x 7168 21.3, 13.3, 9.4; 2048 x 4096 13.9, 9.9,
+// 7.9; 1024 x 1024 6.0, 5.8, 5.7; 200 rows of 1024 x 1024 6.2, 6.5 with two; 100 rows
+// of 4096 x 4096 15.3, 12.6 with two and tiles of 64 rows).
+//   At most 32 rows a group, or narrow tiles in one wave: the weights' bytes
+// count, and a narrow tile leaves shared memory to 11 stages of them.  Forward /
+// input gradient in us, 32 wide against 256: 30 rows over 16 of 1024 x 2048, 11 / 12
+// against 19 / 15; 500 of one 1024 x 1024 6.8 / 6.8 against 9.9 / 9.9; 32 a group (512,
+// 16 of 2048 x 4096) 49 / 45 against 48 / 46; 64 a group 53 / 55 against 49 / 47.
+struct TokenShape {
+  int bt, pairs;
+};
+template <int MODE>
+int token_shape(const RaggedLaunch& g, const RaggedParams& p, TokenShape* s) {
+  int n1 = 0, n2 = 0, n4 = 0, rc;
+  if ((rc = resident_clusters<MODE, 32, 1>(&n1)) || (rc = resident_clusters<MODE, 64, 2>(&n2)) ||
+      (rc = resident_clusters<MODE, 64, 4>(&n4)))
+    return rc;
+  const int64_t t32 = tile_bound(g, p, 32), t64 = tile_bound(g, p, 64);
+  if (p.C >= 1024 && t32 <= n4) *s = TokenShape{32, 4};
+  else if (p.C >= 1024 && t64 <= n4) *s = TokenShape{64, 4};
+  else if (p.C >= 1536 && t32 <= n2) *s = TokenShape{32, 2};
+  else if (p.C >= 1536 && t64 <= n2) *s = TokenShape{64, 2};
+  else *s = TokenShape{g.M <= 32 * (int64_t)g.E || t32 <= n1 ? 32 : 256, 1};
+  return MX_OK;
+}
+
+template <int MODE>
+int launch_tokens(const CUtensorMap& tA, const CUtensorMap& tB, const RaggedParams& p, TokenShape s, int64_t units,
+                  cudaStream_t stream) {
+  const ZeroMaps none{};
+  if (s.bt == 32)
+    return s.pairs == 1   ? launch_cfg<MODE, 32, 1>(tA, tB, none, p, units, stream)
+           : s.pairs == 2 ? launch_cfg<MODE, 32, 2>(tA, tB, none, p, units, stream)
+                          : launch_cfg<MODE, 32, 4>(tA, tB, none, p, units, stream);
+  if (s.bt == 64)
+    return s.pairs == 2 ? launch_cfg<MODE, 64, 2>(tA, tB, none, p, units, stream)
+                        : launch_cfg<MODE, 64, 4>(tA, tB, none, p, units, stream);
+  return launch_cfg<MODE, 256, 1>(tA, tB, none, p, units, stream);
 }
 
 }  // namespace
 
 int launch_ragged(const RaggedLaunch& g, cudaStream_t stream) {
   const int mode = g.mode;
-  // At most 32 rows a group: the weights' bytes count, and a narrow token tile
-  // leaves shared memory to 11 stages of them.  Forward / input gradient in us,
-  // 32 wide against 256: 4 rows of one 4096 x 7168, 22 / 15 against 28 / 23; 30 rows
-  // over 16 of 1024 x 2048, 11 / 12 against 19 / 15; 32 a group (512, 16 of 2048 x
-  // 4096) 49 / 45 against 48 / 46; 64 a group 53 / 55 against 49 / 47.
-  const bool narrow = mode != MX_RAGGED_WGRAD && g.M <= 32 * (int64_t)g.E;
-  const uint32_t bt = narrow ? 32 : 256;
   CUtensorMap tA, tB;
   ZeroMaps tZ{};
   int rc;
@@ -542,21 +659,16 @@ int launch_ragged(const RaggedLaunch& g, cudaStream_t stream) {
   };
   RaggedParams p{};
   p.M = g.M; p.E = g.E; p.offs = g.offs; p.out = (uint8_t*)g.c; p.err = g.err;
-  const int64_t t_units = g.M / bt + g.E;  // at most: every group may end in a part of a tile
-  if (mode == MX_RAGGED_FWD) {
-    p.F = (int32_t)g.N; p.C = (int32_t)g.K;
-    if ((rc = map_w(&tA, 128)) || (rc = map2(&tB, g.a, g.K, bt / 2))) return rc;
-    const int64_t units = t_units * ((g.N + RG_F - 1) / RG_F);
+  if (mode != MX_RAGGED_WGRAD) {
+    const bool fwd = mode == MX_RAGGED_FWD;
+    p.F = (int32_t)(fwd ? g.N : g.K);
+    p.C = (int32_t)(fwd ? g.K : g.N);
+    TokenShape s;
+    if ((rc = fwd ? token_shape<RG_FWD>(g, p, &s) : token_shape<RG_DGRAD>(g, p, &s))) return rc;
+    const int64_t units = tile_bound(g, p, s.bt);
     if (units > INT32_MAX - 1024) return fail(MX_ERR_UNSUPPORTED, "ragged product: too many tiles");
-    return narrow ? launch_cfg<RG_FWD, 32>(tA, tB, tZ, p, units, stream) : launch_cfg<RG_FWD, 256>(tA, tB, tZ, p, units, stream);
-  }
-  if (mode == MX_RAGGED_DGRAD) {
-    p.F = (int32_t)g.K; p.C = (int32_t)g.N;
-    if ((rc = map_w(&tA, 64)) || (rc = map2(&tB, g.a, g.N, bt / 2))) return rc;
-    const int64_t units = t_units * ((g.K + RG_F - 1) / RG_F);
-    if (units > INT32_MAX - 1024) return fail(MX_ERR_UNSUPPORTED, "ragged product: too many tiles");
-    return narrow ? launch_cfg<RG_DGRAD, 32>(tA, tB, tZ, p, units, stream)
-                  : launch_cfg<RG_DGRAD, 256>(tA, tB, tZ, p, units, stream);
+    if ((rc = map_w(&tA, fwd ? 128 : 64)) || (rc = map2(&tB, g.a, p.C, s.bt / 2))) return rc;
+    return fwd ? launch_tokens<RG_FWD>(tA, tB, p, s, units, stream) : launch_tokens<RG_DGRAD>(tA, tB, p, s, units, stream);
   }
   p.F = (int32_t)g.N; p.T = (int32_t)g.K;
   if ((rc = map2(&tA, g.a, g.N, 64)) || (rc = map2(&tB, g.b, g.K, 64))) return rc;
@@ -564,7 +676,7 @@ int launch_ragged(const RaggedLaunch& g, cudaStream_t stream) {
     if ((rc = map2(&tZ.rows[i], g.b, g.K, 1u << i, CU_TENSOR_MAP_SWIZZLE_NONE))) return rc;
   const int64_t units = (int64_t)g.E * ((g.N + RG_F - 1) / RG_F) * ((g.K + 255) / 256);
   if (units > INT32_MAX - 1024) return fail(MX_ERR_UNSUPPORTED, "ragged product: too many tiles");
-  return launch_cfg<RG_WGRAD, 256>(tA, tB, tZ, p, units, stream);
+  return launch_cfg<RG_WGRAD, 256, 1>(tA, tB, tZ, p, units, stream);
 }
 
 }  // namespace mx

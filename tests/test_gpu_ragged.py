@@ -70,6 +70,30 @@ def test_few_tiles_and_long_contractions(counts, N, K):
     _check(counts, 3, N, K, sum(counts) + K)
 
 
+@pytest.mark.parametrize("counts,N,K", [([8], 512, 7168), ([8], 7168, 512), ([31, 2], 1000, 1032), ([100], 1024, 4096),
+                                        ([60, 3], 2048, 1600), ([64], 2304, 1544), ([65, 64, 1], 1800, 2048),
+                                        ([0, 3, 0, 1, 0], 1288, 3000), ([33, 31], 264, 1024)])
+@pytest.mark.parametrize("spare", [0, 40])
+def test_contractions_shared_by_pairs(counts, N, K, spare):
+    """Few tiles: two and four pairs a tile, tiles of 32 and of 64 rows; other groups' and spare rows hold NaN."""
+    out, dx, _ = _check(counts, spare, N, K, sum(counts) + N)
+    n = sum(counts)
+    assert not out[n:].any() and not dx[n:].any()
+    x, dout, w, offs = (t.cuda() for t in _case(counts, spare, N, K, sum(counts) + N))
+    last = max(e for e, c in enumerate(counts) if c)
+    start = sum(counts[:last])
+    x[:start], dout[:start], x[n:], dout[n:] = (float("nan"),) * 4
+    out2, dx2 = mx.ragged_mm(x, w, offs), mx.ragged_mm_dgrad(dout, w, offs)
+    assert torch.equal(out2[start:n].cpu(), out[start:n].cpu()) and torch.equal(dx2[start:n].cpu(), dx[start:n].cpu())
+    assert not out2[n:].any() and not dx2[n:].any()
+    err = mx.ErrorWord()
+    bad = offs.clone()
+    bad[-1] = -1
+    assert not mx.ragged_mm(x, w, bad, err).any() and not mx.ragged_mm_dgrad(dout, w, bad, err).any()
+    with pytest.raises(mx.MxError):
+        err.check()
+
+
 @pytest.mark.parametrize("counts,spare,N,K", [([5, 9, 0, 2], 77, 128, 256), ([0, 0], 40, 64, 64), ([700, 20], 1, 512, 320),
                                               ([3] * 40, 5, 136, 200), ([0] * 7, 9, 40, 24)])
 def test_spare_rows_are_zero(counts, spare, N, K):
