@@ -70,8 +70,9 @@ struct RCfg {
                                     (B_MN ? 1u << 16 : 0u) | ((uint32_t)(RG_F >> 4) << 24);
   static constexpr int STAGES = (226 * 1024 - EPI_BYTES - PARTS - TABLE - 1536) / TX;
   static constexpr size_t SMEM = (size_t)STAGES * TX + EPI_BYTES + PARTS + TABLE + 512 /*barriers*/ + 1024 /*align*/;
-  static_assert((BT == 256 && S == 1) || (BT <= 64 && MODE != RG_WGRAD), "tile widths");
+  static_assert(BT == 256 ? S == 1 : MODE != RG_WGRAD && (BT == 128 ? S == 1 : BT == 64 || BT == 32), "tile widths");
   static_assert(S == 1 || S == 2 || S == 4, "at most eight CTAs a cluster");
+  static_assert(STAGES >= 4, "shared memory");
   static_assert(SMEM + 1024 /*static*/ <= 227 * 1024, "shared memory");
 };
 
@@ -457,8 +458,9 @@ __global__ void __launch_bounds__(RCfg<MODE, BT, S>::THREADS, 1)
         }
         if (f >= p.F) continue;
         if (S > 1 && col_of(0) < t.tn) {
-          // the other pairs' sums of this block to the first pair, which adds them in order
-          const uint32_t at = (uint32_t)(ew * 32 + lane) * 16;   // 8 vectors of 4 tokens, 4 KB apart
+          // the other pairs' sums of this block to the first pair, which adds them in order:
+          // 8 vectors of 4 tokens a lane
+          const uint32_t at = (uint32_t)(ew * 32 + lane) * 16;
           constexpr int V_STEP = RG_EPI * 512 / (BT == 32 ? 2 : 1);
           if (part) {
             const uint32_t dst = cluster_map(smem_u32(sParts), rank) + (part - 1) * C::PART + at;
@@ -599,11 +601,13 @@ int64_t tile_bound(const RaggedLaunch& g, const RaggedParams& p, int bt) {
 // with two and with four pairs: 512 x 7168 21.3, 13.3, 9.4; 2048 x 4096 13.9, 9.9,
 // 7.9; 1024 x 1024 6.0, 5.8, 5.7; 200 rows of 1024 x 1024 6.2, 6.5 with two; 100 rows
 // of 4096 x 4096 15.3, 12.6 with two and tiles of 64 rows).
-//   At most 32 rows a group, or narrow tiles in one wave: the weights' bytes
-// count, and a narrow tile leaves shared memory to 11 stages of them.  Forward /
-// input gradient in us, 32 wide against 256: 30 rows over 16 of 1024 x 2048, 11 / 12
-// against 19 / 15; 500 of one 1024 x 1024 6.8 / 6.8 against 9.9 / 9.9; 32 a group (512,
-// 16 of 2048 x 4096) 49 / 45 against 48 / 46; 64 a group 53 / 55 against 49 / 47.
+//   At most 16 rows a group, or in one wave: 32 rows a tile.  The weights' bytes
+// count, and a narrow tile leaves shared memory to 11 stages of them.  At most 64 a
+// group, or in one wave: 128; else 256.  Forward, us, with 32 / 128 / 256: 30 rows over
+// 16 of 1024 x 2048 11 / - / 19; 400 over 43 of 1176 x 1176 23.1 / 24.3 / 28.8; 256 over 8
+// of 2048 x 2048 19.4 / 15.4 / 16.0; 343 over 8 of 4744 x 2248 40.8 / 32.7 / 37.4; 4096
+// over 64 of 2048 x 2048 108 / 87.5 / 90.8; 800 over 8 of them 27 / 20.7 / 17.6; 500 of one
+// 1024 x 1024 6.8 / - / 9.9; 1000 of one 1024 x 4096 25 / 15.4 / 23.1.
 struct TokenShape {
   int bt, pairs;
 };
@@ -613,12 +617,14 @@ int token_shape(const RaggedLaunch& g, const RaggedParams& p, TokenShape* s) {
   if ((rc = resident_clusters<MODE, 32, 1>(&n1)) || (rc = resident_clusters<MODE, 64, 2>(&n2)) ||
       (rc = resident_clusters<MODE, 64, 4>(&n4)))
     return rc;
-  const int64_t t32 = tile_bound(g, p, 32), t64 = tile_bound(g, p, 64);
+  const int64_t t32 = tile_bound(g, p, 32), t64 = tile_bound(g, p, 64), t128 = tile_bound(g, p, 128);
   if (p.C >= 1024 && t32 <= n4) *s = TokenShape{32, 4};
   else if (p.C >= 1024 && t64 <= n4) *s = TokenShape{64, 4};
   else if (p.C >= 1536 && t32 <= n2) *s = TokenShape{32, 2};
   else if (p.C >= 1536 && t64 <= n2) *s = TokenShape{64, 2};
-  else *s = TokenShape{g.M <= 32 * (int64_t)g.E || t32 <= n1 ? 32 : 256, 1};
+  else if (g.M <= 16 * (int64_t)g.E || t32 <= n1) *s = TokenShape{32, 1};
+  else if (g.M <= 64 * (int64_t)g.E || t128 <= n1) *s = TokenShape{128, 1};
+  else *s = TokenShape{256, 1};
   return MX_OK;
 }
 
@@ -633,6 +639,8 @@ int launch_tokens(const CUtensorMap& tA, const CUtensorMap& tB, const RaggedPara
   if (s.bt == 64)
     return s.pairs == 2 ? launch_cfg<MODE, 64, 2>(tA, tB, none, p, units, stream)
                         : launch_cfg<MODE, 64, 4>(tA, tB, none, p, units, stream);
+  if (s.bt == 128)
+    return launch_cfg<MODE, 128, 1>(tA, tB, none, p, units, stream);
   return launch_cfg<MODE, 256, 1>(tA, tB, none, p, units, stream);
 }
 

@@ -70,6 +70,13 @@ def test_few_tiles_and_long_contractions(counts, N, K):
     _check(counts, 3, N, K, sum(counts) + K)
 
 
+@pytest.mark.parametrize("counts", [[128], [129, 31], [40, 64, 0, 90], [127, 1, 128, 0, 7], [600, 3], [1000]])
+@pytest.mark.parametrize("N,K", [(1032, 264), (200, 2056), (4104, 512)])
+def test_tiles_of_128_rows(counts, N, K):
+    out, dx, _ = _check(counts, 5, N, K, sum(counts) + N)
+    assert not out[-5:].any() and not dx[-5:].any()
+
+
 @pytest.mark.parametrize("counts,N,K", [([8], 512, 7168), ([8], 7168, 512), ([31, 2], 1000, 1032), ([100], 1024, 4096),
                                         ([60, 3], 2048, 1600), ([64], 2304, 1544), ([65, 64, 1], 1800, 2048),
                                         ([0, 3, 0, 1, 0], 1288, 3000), ([33, 31], 264, 1024)])
