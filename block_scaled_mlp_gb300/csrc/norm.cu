@@ -252,9 +252,9 @@ __global__ void __launch_bounds__(512) add_rmsnorm_row_kernel(NormFwdParams p) {
 // squares are exchanged through distributed shared memory, so one pass over HBM
 // gives both quantizations (a second kernel for the columns would read r again:
 // 10 bytes an element instead of 8).  16384 x 7168 with a residual into both
-// codes and a checkpoint takes 219 us (4.9 TB/s): three or four CTAs an SM do
-// not cover the load, exchange and two quantization phases of one another; the
-// column pass adds 36 us.
+// codes and a checkpoint takes 211 us (5.1 TB/s), without either 128 us (3.7 TB/s), of
+// which the loads and sums take 44 by themselves: 24 to 32 warps an SM do not
+// cover the loads, the exchange and the two quantizations of one another.
 //
 // Row passes: a warp has four rows, a lane eight elements of each, four lanes
 // one block.  Column pass: lanes l and l ^ 16 have rows 0-15 and 16-31 of one
@@ -731,15 +731,14 @@ int launch_add_rmsnorm_fwd(const NormFwdLaunch& a, cudaStream_t stream) {
   cudaError_t e;
   if (a.q_col) {
     // Slices of a multiple of 256 columns (whole warps).  Enough rows: at least
-    // 512 columns, so that clusters stay small (16384 x 2048: 64 us on four CTAs,
-    // 75 on eight), on up to eight CTAs, sixteen where slices would pass 1024
-    // columns (their tile leaves an SM one CTA: 4096 x 16384, 189 us on eight,
-    // 133 on sixteen; 16384 x 7168, 217 on seven, 214 on ten, 227 on fourteen).
-    // Few rows (under two 512-column slices an SM): as many CTAs as there can be
-    // (32 x 7168: 6.7 us on fourteen, 9.4 on seven; 1024 x 2048: 7.3 us on eight,
-    // 8.5 on four).
+    // 512 columns, so that clusters stay small (16384 x 2048: 63 us on four CTAs,
+    // 72 on eight), on up to eleven CTAs, whose tiles of 768 columns leave an SM four
+    // of them (16384 x 7168: 212 us on ten, 219 on seven; 16384 x 8192: 240 on eleven,
+    // 248 on eight), sixteen where slices would pass that (8192 x 16384).  Few rows
+    // (under two 512-column slices an SM): as many CTAs as there can be (32 x 7168:
+    // 6.7 us on fourteen, 9.4 on seven; 1024 x 2048: 7.3 us on eight, 8.5 on four).
     const bool few = padded / NC_ROWS * ((p.d8 + 63) / 64) <= 2 * (int64_t)num_sms();
-    const int most = few || p.d8 > 8 * 128 ? 16 : 8;
+    const int most = few || p.d8 > 11 * 96 ? 16 : 11;
     const int slice8 = std::max(few ? 32 : 64, ((p.d8 + 31) / 32 + most - 1) / most * 32);
     const int ctas = (p.d8 + slice8 - 1) / slice8;
     const size_t smem = (size_t)NC_ROWS * slice8 * 16;
