@@ -56,15 +56,6 @@ MX_DEVINL float max_abs(float a, float b) {
   return r;
 }
 
-// Scale byte of a checkpoint block from the bf16 bits of its amax (a NaN has
-// the largest exponent field, as infinity does).
-MX_DEVINL uint32_t ckpt8_scale(uint32_t amax) {
-  const uint32_t E = amax >> 7, m = amax & 0x7Fu;
-  if (E == 0xFF) return 0xFF;
-  const int s = (int)E - 6 + (m > 0x7Eu ? 1 : 0);  // 127 = 1.984375 * 2^6
-  return s < 0 ? 0u : (uint32_t)s;
-}
-
 // E8M0 byte of an MX block from its amax (not negative; the fp32 form of
 // e8m0_from_amax_bits: 448 = 1.75 * 2^8).
 MX_DEVINL uint32_t e8m0_from_amax_f32(float amax_f, uint32_t rceil) {
@@ -81,9 +72,6 @@ MX_DEVINL float inv_pow2(uint32_t s) { return __uint_as_float((254u - s) << 23);
 MX_DEVINL float pow2_of_byte(uint32_t s) {
   return __uint_as_float(s == 0xFF ? 0x7FC00000u : s ? s << 23 : 0x00400000u);
 }
-
-// 2^(127 - s) in bf16, for the bytes of finite blocks (0 <= s <= 249).
-MX_DEVINL uint16_t inv_pow2_bf16(uint32_t s) { return (uint16_t)((254u - s) << 7); }
 
 // This lane's eight checkpoint codes RN(x * inv), inv a power of two, element
 // 0 in the lowest byte.  Adding 1.5 * 2^23 rounds the exact product once, to
@@ -155,24 +143,6 @@ MX_DEVINL uint32_t ckpt8_block_scales(const uint4& a, const uint4& b) {
 }
 // 2^(127 - s) of both blocks, bf16.
 MX_DEVINL uint32_t inv_pow2_bf16x2(uint32_t s2) { return (0x00FE00FEu - (s2 & 0x00FF00FFu)) << 7; }
-
-// The same of one block.
-MX_DEVINL uint32_t ckpt8_block_scale(const uint4& x) {
-  uint32_t m = maxabs2(maxabs2(x.x, x.y), maxabs2(x.z, x.w));
-  m = maxabs2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-  m = maxabs2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-  return ckpt8_scale(max_halves(m & 0x7FFF7FFFu));
-}
-
-// amax of such a block of fp32 values; NaN if one is.
-MX_DEVINL float block_amax(const f2 (&v)[4]) {
-  float m = max3_abs(v[0].x, v[0].y, v[1].x);
-  m = max3_abs(m, v[1].y, v[2].x);
-  m = max3_abs(m, v[2].y, v[3].x);
-  m = max_abs(m, v[3].y);
-  m = max_abs(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-  return max_abs(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-}
 
 // This lane's eight E4M3 codes of an MX block with scale byte s (scaling by a
 // power of two is exact, so fp32 values round once; a NaN or infinite block
