@@ -155,7 +155,7 @@ MX_DEVINL uint2 mx_encode(const f2 (&v)[4], uint32_t s) {
     const f2 t = f2_mul(v[i], inv);
     w[i] = cvt_e4m3x2(t.x, t.y);
   }
-  return make_uint2(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410));
+  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));  // the shift is part of the conversion
 }
 
 // MX scale bytes of two blocks as above (fp32 values): low and high half.  Only
