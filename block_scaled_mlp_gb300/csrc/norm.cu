@@ -252,9 +252,10 @@ __global__ void __launch_bounds__(512) add_rmsnorm_row_kernel(NormFwdParams p) {
 // squares are exchanged through distributed shared memory, so one pass over HBM
 // gives both quantizations (a second kernel for the columns would read r again:
 // 10 bytes an element instead of 8).  16384 x 7168 with a residual into both
-// codes and a checkpoint takes 211 us (5.1 TB/s), without either 128 us (3.7 TB/s), of
-// which the loads and sums take 44 by themselves: 24 to 32 warps an SM do not
-// cover the loads, the exchange and the two quantizations of one another.
+// codes and a checkpoint takes 199 us (5.4 TB/s), without either 126 us (3.8 TB/s), of
+// which the loads and sums take 44 by themselves, either quantization some 40: 32
+// warps an SM do not cover the loads, the exchange and the quantizations of one
+// another.
 //
 // Row passes: a warp has four rows, a lane eight elements of each, four lanes
 // one block.  Column pass: lanes l and l ^ 16 have rows 0-15 and 16-31 of one
@@ -270,6 +271,7 @@ constexpr int NC_CTAS_SM = 4;
 MX_DEVINL void copy_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
+MX_DEVINL void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 MX_DEVINL void copy_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Scale bytes of row r at columns c, c + step, ...: the first one's address
@@ -311,7 +313,9 @@ __global__ void __launch_bounds__(NC_THREADS, NC_CTAS_SM) add_rmsnorm_col_kernel
   uint4* trow = tile + rw * slice8 + (lane ^ (rw >= 16 ? 4 : 0));
   f2 ss[2] = {}, ss_lo[2] = {};
   // x goes to the tile by asynchronous copies, all of them in flight at once;
-  // the residual's vectors are loaded one step ahead
+  // the residual's vectors are loaded one step ahead, from L2 after the first
+  // step (16384 x 7168 with a checkpoint: 199 us, 211 without the prefetch, 207 with
+  // it before the copies of x)
   const int steps = (n8 + 31) / 32;
   for (int i = 0; i < steps; ++i)
     if (i * 32 + lane < n8) {
@@ -326,6 +330,11 @@ __global__ void __launch_bounds__(NC_THREADS, NC_CTAS_SM) add_rmsnorm_col_kernel
     }
   };
   load_res(0);
+  if (RES && (lane & 7) == 0)  // a lane a 128-byte line
+    for (int cb = 32; cb + lane < n8; cb += 32) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) prefetch_l2(p.res + at0 + cb + k * p.d8);
+    }
   copy_async_wait_all();  // a lane reads only what it copied itself
   for (int cb = 0; cb < n8; cb += 32) {
     const bool in = cb + lane < n8;
@@ -733,8 +742,8 @@ int launch_add_rmsnorm_fwd(const NormFwdLaunch& a, cudaStream_t stream) {
     // Slices of a multiple of 256 columns (whole warps).  Enough rows: at least
     // 512 columns, so that clusters stay small (16384 x 2048: 63 us on four CTAs,
     // 72 on eight), on up to eleven CTAs, whose tiles of 768 columns leave an SM four
-    // of them (16384 x 7168: 212 us on ten, 219 on seven; 16384 x 8192: 240 on eleven,
-    // 248 on eight), sixteen where slices would pass that (8192 x 16384).  Few rows
+    // of them (before the residual's prefetch, 16384 x 7168: 212 us on ten, 219 on
+    // seven; 16384 x 8192: 240 on eleven, 248 on eight), sixteen where slices would pass that (8192 x 16384).  Few rows
     // (under two 512-column slices an SM): as many CTAs as there can be (32 x 7168:
     // 6.7 us on fourteen, 9.4 on seven; 1024 x 2048: 7.3 us on eight, 8.5 on four).
     const bool few = padded / NC_ROWS * ((p.d8 + 63) / 64) <= 2 * (int64_t)num_sms();
