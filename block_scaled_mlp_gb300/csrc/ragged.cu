@@ -538,11 +538,11 @@ __global__ void __launch_bounds__(RCfg<MODE, BT, S>::THREADS, 1)
   if (warp == 1) tmem_dealloc_pair(tmem, C::TMEM);
 }
 
-// Clusters that can be resident at once, by device.
+// Clusters that can be resident at once (none, if no part of the device holds one), by device.
 template <int MODE, int BT, int S>
 int resident_clusters(int* n) {
   using C = RCfg<MODE, BT, S>;
-  static int resident[64] = {0};
+  static int resident[64] = {0};  // the number + 1, once known
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_status(e, "cudaGetDevice");
@@ -564,11 +564,10 @@ int resident_clusters(int* n) {
     cfg.numAttrs = 1;
     int m = 0;
     e = cudaOccupancyMaxActiveClusters(&m, k, &cfg);
-    if (e != cudaSuccess || m <= 0)
-      return cuda_status(e != cudaSuccess ? e : cudaErrorInvalidConfiguration, "cudaOccupancyMaxActiveClusters");
-    r = m;
+    if (e != cudaSuccess) return cuda_status(e, "cudaOccupancyMaxActiveClusters");
+    r = m + 1;
   }
-  *n = r;
+  *n = r - 1;
   return MX_OK;
 }
 
@@ -579,6 +578,7 @@ int launch_cfg(const CUtensorMap& tA, const CUtensorMap& tB, const ZeroMaps& tZ,
   auto k = ragged_kernel<MODE, BT, S>;
   int nres = 0;
   if (int rc = resident_clusters<MODE, BT, S>(&nres)) return rc;
+  if (nres <= 0) return cuda_status(cudaErrorInvalidConfiguration, "cudaOccupancyMaxActiveClusters");
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
   if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute");
   // S > 1: a cluster has one tile at most (its buffer for the other pairs' sums is written once)
