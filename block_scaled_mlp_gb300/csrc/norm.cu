@@ -647,22 +647,34 @@ __global__ void __launch_bounds__(T_MAX, CTAS) add_rmsnorm_bwd_kernel(NormBwdPar
   }
 }
 
-// dw[c] = sum over g of part[g][c]: 32 columns a block, 32 threads a column with
-// every 32nd row of the partials each, then their sums in order.
-__global__ void __launch_bounds__(1024) norm_dw_kernel(const float* __restrict__ part, int32_t G, int32_t d,
-                                                       __nv_bfloat16* __restrict__ dw) {
-  __shared__ float s[32][33];
+// dw[c] = sum over g of part[g][c]: C columns a block, R threads a column with every
+// R-th row of the partials each, then their sums in order.  Bound by latency (2 of the
+// 35 us of 8192 x 4096): few columns a block where a row has too few for all SMs
+// (65536 x 512: 36 us in all with 8, 42 with 32), many for few partials (600 x 1536:
+// 5.8 us with 32, 6.9 with 8; 300 x 7168 6.5 and 9.0).
+constexpr int NB_SUM_THREADS = 1024;
+template <int C>
+__global__ void __launch_bounds__(NB_SUM_THREADS) norm_dw_kernel(const float* __restrict__ part, int32_t G, int32_t d,
+                                                                 __nv_bfloat16* __restrict__ dw) {
+  constexpr int R = NB_SUM_THREADS / C;
+  static_assert(C <= NB_SUM_THREADS / 32, "a warp a column");
+  __shared__ float s[C][R + 1];
   pdl_begin();  // the partials of the kernel before
-  const int x = threadIdx.x & 31, g0 = threadIdx.x >> 5, c = blockIdx.x * 32 + x;
+  const int x = threadIdx.x % C, g0 = threadIdx.x / C, c = blockIdx.x * C + x;
   float t = 0;
   if (c < d) {
-#pragma unroll 8
-    for (int g = g0; g < G; g += 32) t += part[(int64_t)g * d + c];
+#pragma unroll 4
+    for (int g = g0; g < G; g += R) t += part[(int64_t)g * d + c];
   }
-  s[g0][x] = t;
+  s[x][g0] = t;
   __syncthreads();
-  t = warp_sum(s[x][g0]);  // warp: a column
-  if (x == 0 && blockIdx.x * 32 + g0 < d) dw[blockIdx.x * 32 + g0] = __float2bfloat16_rn(t);
+  const int col = threadIdx.x >> 5, lane = threadIdx.x & 31;  // warp: a column
+  if (col >= C) return;
+  t = 0;
+#pragma unroll
+  for (int i = lane; i < R; i += 32) t += s[col][i];
+  t = warp_sum(t);
+  if (lane == 0 && blockIdx.x * C + col < d) dw[blockIdx.x * C + col] = __float2bfloat16_rn(t);
 }
 
 // How a row is held: vectors of eight a thread, and by a warp or a CTA.
@@ -695,7 +707,8 @@ int threads_of(int d8, int V) { return ((d8 + V - 1) / V + 31) / 32 * 32; }
 // vectors: 8192 x 8192 77 us and 104, 16384 x 5120 94 and 103), 384 from bf16, whose
 // rows need fewer instructions and fill the ring sooner (16384 x 8192 153 us, 158
 // with 512; 16384 x 5120 without a residual gradient 77 and 87).  Up to 512 columns
-// a warp has a row, 24 of them an SM (65536 x 512: 51 us, 56 with 16).
+// a warp has a row, 24 of them an SM (65536 x 512: 42 us; 51 and 56 with 24 and 16
+// before the sum of its partials was spread over more blocks).
 struct NormBwdShape {
   int V, T, ctas, stages, stage_bytes;
 };
@@ -715,7 +728,7 @@ NormBwdShape bwd_shape(int64_t d, bool ck, bool dres) {
 }  // namespace
 
 // CTAs of the backward pass: each with two rows at least, beyond two an SM (1200 x
-// 1024: 6.2 us, 8.0 with a row each, whose partial gradients outweigh it).
+// 1024: 7.2 us, 8.0 with a row each, whose partial gradients outweigh it).
 int bwd_grid(int64_t M, int ctas_sm) {
   const int64_t sms = num_sms();
   return (int)std::min(std::min(M, ctas_sm * sms), std::max(2 * sms, M / 2));
@@ -805,7 +818,10 @@ int launch_add_rmsnorm_bwd(const NormBwdLaunch& a, cudaStream_t stream) {
   e = launch_overlapped(k, G, s.T, smem, stream, 1, p);
   if (e != cudaSuccess) return cuda_status(e, "add_rmsnorm_bwd_kernel launch");
   count_launch(MX_KERNEL_NORM);
-  return cuda_status(launch_overlapped(norm_dw_kernel, (unsigned)((a.d + 31) / 32), 1024, 0, stream, 1, (const float*)p.part,
+  // columns a block of the sum: 32 for few partials or where that gives every SM a block
+  const int C = G <= 2 * num_sms() || a.d >= 32 * num_sms() ? 32 : a.d >= 16 * num_sms() ? 16 : 8;
+  auto sum = C == 32 ? norm_dw_kernel<32> : C == 16 ? norm_dw_kernel<16> : norm_dw_kernel<8>;
+  return cuda_status(launch_overlapped(sum, (unsigned)((a.d + C - 1) / C), NB_SUM_THREADS, 0, stream, 1, (const float*)p.part,
                                        (int32_t)G, (int32_t)a.d, (__nv_bfloat16*)a.dw),
                      "norm_dw_kernel launch");
 }
