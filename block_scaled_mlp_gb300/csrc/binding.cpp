@@ -6,7 +6,7 @@
 // it allocated, as much again for its checks and for turning nineteen arguments
 // into C values.  Here a call checks its tensors, allocates its outputs and calls
 // the C entry point of include/mxmlp.h on the tensors' device and its current
-// stream in one go (4 to 9 us).  Refusals raise MxError with the status and text
+// stream in one go (4 to 7 us).  Refusals raise MxError with the status and text
 // that the C entry gives, allocation failures torch's own error; no C++ exception
 // leaves a function.
 #define PY_SSIZE_T_CLEAN
@@ -16,7 +16,7 @@
 #include <string>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -86,8 +86,10 @@ const at::Tensor& matrix(PyObject* o, const char* name, const at::Tensor* first 
   return t;
 }
 
+// From the caching allocator without the dispatcher's rounds (1.2 us an output with
+// them, 0.8 without).
 at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, const at::Tensor& like) {
-  return at::empty(shape, at::TensorOptions().dtype(type).device(like.device()));
+  return at::Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
 }
 
 void* ptr(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
