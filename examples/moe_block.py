@@ -8,6 +8,8 @@ for its weight gradient).  The routed experts run in bf16 on the groups as the r
 For the backward pass r and both experts' [g | u] are kept in 8 bits; n and the activations are computed again from them.
 
     python examples/moe_block.py [--tokens 8192 --d 2048 --h 1024 --experts 32 --topk 4 --steps 20]
+
+tokens, d and h are multiples of 128 (the MXFP8 products); the routed groups have any sizes.
 """
 import argparse
 import os
