@@ -164,6 +164,12 @@ MX_DEVINL void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// The same barrier in two halves that only wait for one another: after cluster_wait()
+// every CTA of the cluster has started, so its shared memory may be written (not
+// before: CTAs of a cluster being placed together does not promise it).
+MX_DEVINL void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+MX_DEVINL void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 // Address of the same shared variable in CTA `rank` of the cluster.
 MX_DEVINL uint32_t cluster_map(uint32_t saddr, uint32_t rank) {
   uint32_t r;

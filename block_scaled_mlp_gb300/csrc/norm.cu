@@ -307,6 +307,8 @@ __global__ void __launch_bounds__(NC_THREADS, NC_CTAS_SM) add_rmsnorm_col_kernel
       p.s_col.put(c, r0 >> 5, 0);
   }
   if (!live) return;  // the whole cluster
+  __syncwarp();
+  cluster_arrive();   // waited for before the first store into another CTA, behind the loads
 
   const int rw = warp * 4;                                       // the warp's first row
   const int64_t at0 = (r0 + rw) * p.d8 + c0 + lane;              // its first vector
@@ -378,11 +380,14 @@ __global__ void __launch_bounds__(NC_THREADS, NC_CTAS_SM) add_rmsnorm_col_kernel
   }
   const int n8_all = n8 & ~31;
   const f2 sum = warp_sum_rows(ss, ss_lo);
+  __syncwarp();
+  cluster_wait();  // the other CTAs have started
   // lane: this CTA's sum of row lane / 8 of the warp to CTAs lane % 8 and + 8 of the cluster
   for (int j = lane & 7; j < ctas; j += 8)
     asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(cluster_map(smem_u32(&part[rank][rw + (lane >> 3)]), j)),
                  "f"(sum.x), "f"(sum.y)
                  : "memory");
+  __syncwarp();
   cluster_sync();  // every CTA's sums are here; the tile is complete too
   if (threadIdx.x < NC_ROWS) {
     f2 t = part[0][threadIdx.x];
