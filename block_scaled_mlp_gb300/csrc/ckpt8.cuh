@@ -76,7 +76,7 @@ MX_DEVINL float pow2_of_byte(uint32_t s) {
 // This lane's eight checkpoint codes RN(x * inv), inv a power of two, element
 // 0 in the lowest byte.  Adding 1.5 * 2^23 rounds the exact product once, to
 // nearest even, into the low bits of the sum.  (A NaN or infinite block has
-// inv = -infinity; its codes mean nothing.)
+// inv = infinity; its codes mean nothing.)
 MX_DEVINL uint2 ckpt8_encode(const uint4& x, uint16_t inv) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   uint32_t h[4];
@@ -141,8 +141,10 @@ MX_DEVINL uint32_t ckpt8_block_scales(const uint4& a, const uint4& b) {
   if (bad) s |= (bad >> 15) * 0xFFu;
   return s;
 }
-// 2^(127 - s) of both blocks, bf16.
-MX_DEVINL uint32_t inv_pow2_bf16x2(uint32_t s2) { return (0x00FE00FEu - (s2 & 0x00FF00FFu)) << 7; }
+// 2^(127 - s) of both blocks, bf16 (+infinity for 0xFF).  Each half is 0x1FE - s,
+// 0xFF or more, so that no half borrows from the other, and 0x1FF or less, so that
+// none shifts into the other; the sign bit that this leaves is cleared.
+MX_DEVINL uint32_t inv_pow2_bf16x2(uint32_t s2) { return ((0x01FE01FEu - s2) << 7) & 0x7FFF7FFFu; }
 
 // This lane's eight E4M3 codes of an MX block with scale byte s (scaling by a
 // power of two is exact, so fp32 values round once; a NaN or infinite block
