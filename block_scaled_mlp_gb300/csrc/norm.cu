@@ -16,6 +16,8 @@
 #include "kernels.h"
 #include "tile_quant.cuh"
 
+#include <string.h>
+
 #include <type_traits>
 
 namespace mx {
@@ -114,9 +116,17 @@ MX_DEVINL f2 warp_sum_rows(const f2 (&hi)[2], const f2 (&lo)[2]) {
   return warp_sum_add<4>(v);
 }
 
-// (ss / d + eps)^-1/2 as a pair: the rounded root and one Newton step's
-// correction.  A root that is not finite (or zero) stays as it is.
-MX_DEVINL f2 rstd_pair(f2 ss, float d, float eps) {
+// n = (ss / d + eps)^-1/2 as a pair for norm2: the rounded root and one Newton
+// step's correction.  A root that is not finite (or zero) stays as it is.  rstd: n in
+// fp32.
+//   EXACT: where m = ss / d + eps is the square of a number a of 12 bits or less (rows
+// of one magnitude, say), y = r w / a may be an exact number.  The last bit of n's
+// correction (2^-47 of n) says so to norm2: clear where it may, set elsewhere.  In such
+// a row n is raised by 2^-38 of itself, past the pair's own error (some 2^-46): an
+// exact y comes out of norm2's truncation whole, and any other stays on its side of
+// every tie (a tie T of nine bits differs from r w / a by 1 / (T a), 2^-21, or more).
+template <bool EXACT>
+MX_DEVINL f2 rstd_pair(f2 ss, float d, float eps, float& rstd) {
   const float q = __fdiv_rn(ss.x, d);
   const float ql = __fdividef(__fadd_rn(__fmaf_rn(-q, d, ss.x), ss.y), d);
   const f2 m = pair_add(f2_pack(q, ql), f2_pack(eps, 0.0f));
@@ -124,29 +134,55 @@ MX_DEVINL f2 rstd_pair(f2 ss, float d, float eps) {
   float e = __fmaf_rn(-m.x, t, 1.0f);
   e = __fmaf_rn(-m.x, __fmaf_rn(n, n, -t), e);
   e = __fmaf_rn(-m.y, t, e);
-  const float lo = __fmul_rn(__fmul_rn(0.5f, n), e);
-  return f2_pack(n, fabsf(lo) < n ? lo : 0.0f);
+  float lo = __fmul_rn(__fmul_rn(0.5f, n), e);
+  const bool valid = fabsf(lo) < n;
+  if (!valid) lo = 0.0f;
+  rstd = n + lo;
+  if (EXACT && valid) {
+    const float a = __uint_as_float((__float_as_uint(__fmul_rn(m.x, n)) + 0x800u) & ~0xFFFu);  // 12 bits of the root
+    const bool square = m.y == 0.0f && __fmaf_rn(a, a, -m.x) == 0.0f;
+    lo = __uint_as_float(square ? __float_as_uint(__fmaf_rn(n, 0x1p-38f, lo)) & ~1u : __float_as_uint(lo) | 1u);
+  }
+  return f2_pack(n, lo);
 }
 
 // y of two and of eight elements, fp32, rounded to odd: truncated, and the last
-// bit set (r w n is hardly ever a 24-bit number).  Such a value lies on the same
-// side of every E4M3 and bf16 tie as r w n itself, so the rounding that follows
-// is that of r w n, where an fp32 value to nearest lands on the tie itself once
-// in a million times and goes to the even side: of 117 million codes 69 to 71
-// then differed from the 64-bit result, and 0 to 6 do with this and the sums above.
+// bit set (EXACT: unless y may be an exact number, see above).  Such a value lies on
+// the same side of every E4M3 and bf16 tie as r w n itself, so the rounding that
+// follows is that of r w n, where an fp32 value to nearest lands on the tie itself
+// once in a million times and goes to the even side: of 117 million codes 64 to 75
+// then differed from the 64-bit result, and 2 to 5 do with this and the sums above.
+//   EXACT goes by eps alone (short_number): with an eps of many bits no row's m is a
+// short square, unless the row makes up for eps bit by bit.  Asking every element's
+// row costs up to 5% of the two-axis kernel (registers) and 1 to 3% of the others.
 // Zero becomes 2^-149, which rounds to a zero code and a zero bf16.  Where r w
 // passes fp32 (|w| >= 2^64; from |r| = 2^64 on n is zero) y is NaN; multiplying
 // r n by w for such weights cost 2.5% of every call.
+template <bool EXACT>
+MX_DEVINL float to_odd(float y, f2 n) {
+  uint32_t v = __float_as_uint(y) | 1u;
+  if (EXACT)  // y | (n.y & 1) in one instruction
+    asm("lop3.b32 %0, %1, %2, 1, 0xF8;" : "=r"(v) : "r"(__float_as_uint(y)), "r"(__float_as_uint(n.y)));
+  return __uint_as_float(v);
+}
+template <bool EXACT>
 MX_DEVINL f2 norm2(uint32_t r, f2 n, uint32_t w) {
   const f2 rw = mul_bf16x2(r, w);
   const f2 y = __ffma2_rz(rw, f2_splat(n.x), f2_mul(rw, f2_splat(n.y)));
-  return f2_pack(__uint_as_float(__float_as_uint(y.x) | 1u), __uint_as_float(__float_as_uint(y.y) | 1u));
+  return f2_pack(to_odd<EXACT>(y.x, n), to_odd<EXACT>(y.y, n));
 }
+template <bool EXACT>
 MX_DEVINL void norm8(const uint4& r, f2 n, const uint4& w, f2 (&y)[4]) {
-  y[0] = norm2(r.x, n, w.x);
-  y[1] = norm2(r.y, n, w.y);
-  y[2] = norm2(r.z, n, w.z);
-  y[3] = norm2(r.w, n, w.w);
+  y[0] = norm2<EXACT>(r.x, n, w.x);
+  y[1] = norm2<EXACT>(r.y, n, w.y);
+  y[2] = norm2<EXACT>(r.z, n, w.z);
+  y[3] = norm2<EXACT>(r.w, n, w.w);
+}
+// Whether eps has 12 significant bits or less (0, a power of two).
+bool short_number(float eps) {
+  uint32_t bits;
+  memcpy(&bits, &eps, 4);
+  return (bits & 0xFFFu) == 0;
 }
 
 // ---- rows: one CTA per row, or (WARP) one warp, ROW_WARPS of them a CTA; the
@@ -155,7 +191,7 @@ MX_DEVINL void norm8(const uint4& r, f2 n, const uint4& w, f2 (&y)[4]) {
 // 7168 with a residual into row codes and bf16 158 us (6.7 TB/s), 8192 x 4096 into
 // bf16 22.5 us (6.0 TB/s); below that by the latency of one row (1 x 7168: 3.0 us).
 constexpr int ROW_WARPS = 4;
-template <int V, bool WARP>
+template <int V, bool WARP, bool EXACT>
 __global__ void __launch_bounds__(512) add_rmsnorm_row_kernel(NormFwdParams p) {
   pdl_begin();
   const int lane = threadIdx.x & 31;
@@ -205,8 +241,9 @@ __global__ void __launch_bounds__(512) add_rmsnorm_row_kernel(NormFwdParams p) {
     sum = warp_sum_add<8>((lane & 15) < (T >> 5) ? part[lane & 15] : f2_splat(0.0f));
   }
   sum = settle(sum);
-  const f2 n = rstd_pair(sum, p.d, p.eps);
-  if (t == 0) p.rstd[row] = n.x + n.y;
+  float rstd;
+  const f2 n = rstd_pair<EXACT>(sum, p.d, p.eps, rstd);
+  if (t == 0) p.rstd[row] = rstd;
   const uint32_t up = p.rceil ? 0x1FFFFFu : 0u;
   // two vectors of the row at a time (V = 1: one, and zeros), so that two
   // blocks share the scales' exchange
@@ -227,8 +264,8 @@ __global__ void __launch_bounds__(512) add_rmsnorm_row_kernel(NormFwdParams p) {
       }
     }
     f2 y0[4], y1[4];
-    norm8(v0, n, in0 ? __ldg(p.w + c0) : z, y0);
-    norm8(v1, n, in1 ? __ldg(p.w + c1) : z, y1);
+    norm8<EXACT>(v0, n, in0 ? __ldg(p.w + c0) : z, y0);
+    norm8<EXACT>(v1, n, in1 ? __ldg(p.w + c1) : z, y1);
     if (p.y) {
       if (in0) p.y[base + c0] = pack8(y0);
       if (in1) p.y[base + c1] = pack8(y1);
@@ -284,7 +321,7 @@ MX_DEVINL ScaleRow scale_row(const ScaleDst& d, int64_t r, int32_t c) {
   return d.mma ? ScaleRow{d.base + mma_scale_offset(r, c, d.tiles_per_row), 1024} : ScaleRow{d.base + r * d.ld + c, 8};
 }
 
-template <bool RES, bool CK, bool Y, bool ROW>
+template <bool RES, bool CK, bool Y, bool ROW, bool EXACT>
 __global__ void __launch_bounds__(NC_THREADS, NC_CTAS_SM) add_rmsnorm_col_kernel(NormFwdParams p, int32_t slice8) {
   extern __shared__ __align__(16) uint4 tile[];   // [32][slice8]
   __shared__ __align__(16) f2 part[NC_MAX_CTAS][NC_ROWS];    // sums of squares by CTA and row
@@ -392,9 +429,9 @@ __global__ void __launch_bounds__(NC_THREADS, NC_CTAS_SM) add_rmsnorm_col_kernel
   if (threadIdx.x < NC_ROWS) {
     f2 t = part[0][threadIdx.x];
     for (int j = 1; j < ctas; ++j) sum_add(t, part[j][threadIdx.x]);  // the same order in every CTA
-    const f2 n = rstd_pair(settle(t), p.d, p.eps);
-    s_n[threadIdx.x] = n;
-    if (rank == 0) p.rstd[r0 + threadIdx.x] = n.x + n.y;
+    float rstd;
+    s_n[threadIdx.x] = rstd_pair<EXACT>(settle(t), p.d, p.eps, rstd);
+    if (rank == 0) p.rstd[r0 + threadIdx.x] = rstd;
   }
   __syncthreads();
 
@@ -414,8 +451,8 @@ __global__ void __launch_bounds__(NC_THREADS, NC_CTAS_SM) add_rmsnorm_col_kernel
 #pragma unroll
       for (int k = 0; k < 4; k += 2) {
         f2 y0[4], y1[4];
-        norm8(in ? trow[k * slice8 + cb] : z, n[k], w, y0);
-        norm8(in ? trow[(k + 1) * slice8 + cb] : z, n[k + 1], w, y1);
+        norm8<EXACT>(in ? trow[k * slice8 + cb] : z, n[k], w, y0);
+        norm8<EXACT>(in ? trow[(k + 1) * slice8 + cb] : z, n[k + 1], w, y1);
         const int64_t e0 = at0 + cb + k * p.d8, e1 = e0 + p.d8;
         if (Y && in) {
           p.y[e0] = pack8(y0);
@@ -456,8 +493,8 @@ __global__ void __launch_bounds__(NC_THREADS, NC_CTAS_SM) add_rmsnorm_col_kernel
 #pragma unroll
     for (int i = 0; i < 16; i += 2) {
       const float4 nn = *reinterpret_cast<const float4*>(nr + i);
-      y[i] = norm2(src[i * slice8 * 4], f2_pack(nn.x, nn.y), w);
-      y[i + 1] = norm2(src[(i + 1) * slice8 * 4], f2_pack(nn.z, nn.w), w);
+      y[i] = norm2<EXACT>(src[i * slice8 * 4], f2_pack(nn.x, nn.y), w);
+      y[i + 1] = norm2<EXACT>(src[(i + 1) * slice8 * 4], f2_pack(nn.z, nn.w), w);
       ma = max3_abs(ma, y[i].x, y[i + 1].x);
       mb = max3_abs(mb, y[i].y, y[i + 1].y);
     }
@@ -770,13 +807,14 @@ int launch_add_rmsnorm_fwd(const NormFwdLaunch& a, cudaStream_t stream) {
     const int ctas = (p.d8 + slice8 - 1) / slice8;
     const size_t smem = (size_t)NC_ROWS * slice8 * 16;
     using Kernel = void (*)(NormFwdParams, int32_t);
-    // [residual][checkpoint][bf16 y][row codes]
-#define MX_NC(R, C) {{add_rmsnorm_col_kernel<R, C, false, false>, add_rmsnorm_col_kernel<R, C, false, true>}, \
-                     {add_rmsnorm_col_kernel<R, C, true, false>, add_rmsnorm_col_kernel<R, C, true, true>}}
-    static const Kernel kernels[2][2][2][2] = {{MX_NC(false, false), MX_NC(false, true)},
-                                               {MX_NC(true, false), MX_NC(true, true)}};
+    // [exact][residual][checkpoint][bf16 y][row codes]
+#define MX_NC(R, C, X) {{add_rmsnorm_col_kernel<R, C, false, false, X>, add_rmsnorm_col_kernel<R, C, false, true, X>}, \
+                        {add_rmsnorm_col_kernel<R, C, true, false, X>, add_rmsnorm_col_kernel<R, C, true, true, X>}}
+    static const Kernel kernels[2][2][2][2][2] = {
+        {{MX_NC(false, false, false), MX_NC(false, true, false)}, {MX_NC(true, false, false), MX_NC(true, true, false)}},
+        {{MX_NC(false, false, true), MX_NC(false, true, true)}, {MX_NC(true, false, true), MX_NC(true, true, true)}}};
 #undef MX_NC
-    const Kernel k = kernels[p.res != nullptr][p.ck != nullptr][p.y != nullptr][p.q_row != nullptr];
+    const Kernel k = kernels[short_number(p.eps)][p.res != nullptr][p.ck != nullptr][p.y != nullptr][p.q_row != nullptr];
     e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute");
     if (ctas > 8) {
@@ -790,16 +828,16 @@ int launch_add_rmsnorm_fwd(const NormFwdLaunch& a, cudaStream_t stream) {
   }
   const RowShape sh = row_shape(a.M, p.d8, p.res != nullptr);
   count_launch(MX_KERNEL_NORM);
-  if (sh.warp)
-    return cuda_status(launch_overlapped(sh.V == 2 ? add_rmsnorm_row_kernel<2, true> : add_rmsnorm_row_kernel<4, true>,
-                                         (unsigned)((padded + ROW_WARPS - 1) / ROW_WARPS), ROW_WARPS * 32, 0, stream, 1, p),
-                       "add_rmsnorm_row_kernel launch");
-  auto k = sh.V == 1   ? add_rmsnorm_row_kernel<1, false>
-           : sh.V == 2 ? add_rmsnorm_row_kernel<2, false>
-           : sh.V == 4 ? add_rmsnorm_row_kernel<4, false>
-                       : add_rmsnorm_row_kernel<8, false>;
-  return cuda_status(launch_overlapped(k, (unsigned)padded, threads_of(p.d8, sh.V), 0, stream, 1, p),
-                     "add_rmsnorm_row_kernel launch");
+  using Kernel = void (*)(NormFwdParams);
+  // [exact]: a row a warp, V = 2 and 4; a row a CTA, V = 1, 2, 4 and 8
+#define MX_NR(X) {add_rmsnorm_row_kernel<2, true, X>, add_rmsnorm_row_kernel<4, true, X>, add_rmsnorm_row_kernel<1, false, X>, \
+                  add_rmsnorm_row_kernel<2, false, X>, add_rmsnorm_row_kernel<4, false, X>, add_rmsnorm_row_kernel<8, false, X>}
+  static const Kernel kernels[2][6] = {MX_NR(false), MX_NR(true)};
+#undef MX_NR
+  const Kernel k = kernels[short_number(p.eps)][sh.warp ? sh.V / 4 : sh.V == 1 ? 2 : sh.V == 2 ? 3 : sh.V == 4 ? 4 : 5];
+  const int64_t grid = sh.warp ? (padded + ROW_WARPS - 1) / ROW_WARPS : padded;
+  const int threads = sh.warp ? ROW_WARPS * 32 : threads_of(p.d8, sh.V);
+  return cuda_status(launch_overlapped(k, (unsigned)grid, threads, 0, stream, 1, p), "add_rmsnorm_row_kernel launch");
 }
 
 int launch_add_rmsnorm_bwd(const NormBwdLaunch& a, cudaStream_t stream) {
