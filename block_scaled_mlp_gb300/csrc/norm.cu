@@ -24,7 +24,8 @@ namespace mx {
 
 namespace {
 
-constexpr int NB_MAX_STAGES = 6;   // backward: rows in a CTA's ring, at most
+constexpr int NB_MAX_STAGES = 6;          // backward: rows in a CTA's ring, at most
+constexpr int NB_MAX_SMEM = 220 * 1024;   // of all rings of an SM; every call's limit (see NC_MAX_SMEM)
 
 struct NormFwdParams {
   const uint4* x;        // [M, d] bf16
@@ -304,6 +305,9 @@ constexpr int NC_ROWS = 32;
 constexpr int NC_THREADS = 256;
 constexpr int NC_MAX_CTAS = 16;
 constexpr int NC_CTAS_SM = 4;
+// Shared memory of the widest slice.  The kernels' limit is this for every call: it is
+// the function's, not the launch's, and another thread may launch with another width.
+constexpr int NC_MAX_SMEM = NC_ROWS * (int)(kNormMaxD / NC_MAX_CTAS) * 2;
 
 MX_DEVINL void copy_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
@@ -760,7 +764,7 @@ NormBwdShape bwd_shape(int64_t d, bool ck, bool dres) {
   s.V = d8 <= 32 ? 1 : d8 <= 64 ? 2 : 4;
   s.T = threads_of(d8, s.V);
   s.stage_bytes = (int)((d * (2 + (ck ? 1 : 2) + (dres ? 2 : 0)) + 127) / 128 * 128);
-  const int smem = 220 * 1024;
+  const int smem = NB_MAX_SMEM;
   s.ctas = std::max(1, s.V < 4 ? 24 : (ck ? 512 : 384) / s.T);
   while (s.ctas > 1 && (smem / s.ctas - 1024) / s.stage_bytes < 2) --s.ctas;
   s.stages = std::min(NB_MAX_STAGES, (smem / s.ctas - 1024) / s.stage_bytes);
@@ -815,7 +819,7 @@ int launch_add_rmsnorm_fwd(const NormFwdLaunch& a, cudaStream_t stream) {
         {{MX_NC(false, false, true), MX_NC(false, true, true)}, {MX_NC(true, false, true), MX_NC(true, true, true)}}};
 #undef MX_NC
     const Kernel k = kernels[short_number(p.eps)][p.res != nullptr][p.ck != nullptr][p.y != nullptr][p.q_row != nullptr];
-    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, NC_MAX_SMEM);
     if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute");
     if (ctas > 8) {
       e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -855,7 +859,7 @@ int launch_add_rmsnorm_bwd(const NormBwdLaunch& a, cudaStream_t stream) {
   static const Kernel kernels[3][2] = {MX_NB(1, 32, 24), MX_NB(2, 32, 24), MX_NB(4, 512, 1)};
 #undef MX_NB
   const Kernel k = kernels[s.V == 1 ? 0 : s.V == 2 ? 1 : 2][a.ck != nullptr];
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, NB_MAX_SMEM);
   if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute");
   count_launch(MX_KERNEL_NORM);
   e = launch_overlapped(k, G, s.T, smem, stream, 1, p);
