@@ -658,7 +658,8 @@ __global__ void __launch_bounds__(T_MAX, CTAS) add_rmsnorm_bwd_kernel(NormBwdPar
     }
     dot = 0;
     for (int i = 0; i < warps; ++i) dot += sums[par][i];
-    const f2 n2 = f2_splat(n), c2 = f2_splat(-n * n * p.inv_d * dot);
+    // n dot first, which has the size of dy w: n^2 passes fp32 where |r| < 2^-64
+    const f2 n2 = f2_splat(n), c2 = f2_splat(-(n * dot * p.inv_d * n));
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       const int c = threadIdx.x + k * T;

@@ -1,0 +1,29 @@
+"""Where the norm's fp32 range ends, and that it does not end earlier."""
+import pytest
+import torch
+
+import block_scaled_mlp_gb300 as mx
+from tests import ref64
+
+pytestmark = pytest.mark.gpu
+
+
+def _bf16(shape, seed, std=1.0):
+    return (torch.randn(shape, generator=torch.Generator().manual_seed(seed), dtype=torch.float64) * std).to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("ckpt", [False, True])
+@pytest.mark.parametrize("e", [-66, -40, 40, 56])
+@pytest.mark.parametrize("M,d", [(3, 256), (5, 544), (400, 2080)])
+def test_backward_of_small_and_large_rows(M, d, e, ckpt):
+    """rstd's square may pass fp32, dx does not.  Tolerances as in test_gpu_norm: 2^-8 of a result (its bf16 rounding),
+    2^-18 of the magnitudes in a sum, and rstd's own rounding."""
+    r, w, dy = _bf16((M, d), M + d, 2.0 ** e), _bf16(d, 3), _bf16((M, d), 5)
+    n = 1 / torch.sqrt((r.double() ** 2).mean(1))
+    kept = mx.ckpt8_save(r.cuda()) if ckpt else r.cuda()
+    dx, dw = mx.add_rmsnorm_bwd(dy.cuda(), kept, n.float().cuda(), w.cuda())
+    at = ref64.int8_values(r.double()) if ckpt else r.double()
+    gx, gw, mag, mw = ref64.rmsnorm_bwd(dy.double(), at, n, w.double())
+    assert torch.isfinite(dx).all() and torch.isfinite(dw).all()
+    assert torch.all((ref64.f64(dx) - gx).abs() <= gx.abs() * 2.0 ** -8 + mag * 2.0 ** -18)
+    assert torch.all((ref64.f64(dw) - gw).abs() <= gw.abs() * 2.0 ** -8 + mw * 2.0 ** -18)
