@@ -27,3 +27,18 @@ def test_backward_of_small_and_large_rows(M, d, e, ckpt):
     assert torch.isfinite(dx).all() and torch.isfinite(dw).all()
     assert torch.all((ref64.f64(dx) - gx).abs() <= gx.abs() * 2.0 ** -8 + mag * 2.0 ** -18)
     assert torch.all((ref64.f64(dw) - gw).abs() <= gw.abs() * 2.0 ** -8 + mw * 2.0 ** -18)
+
+
+@pytest.mark.parametrize("axis", [0, 3])
+@pytest.mark.parametrize("d", [256, 2080, 8192, 16384])
+def test_statistic_of_a_row_with_one_large_value(d, axis):
+    """One square of 2^24 beside ones: an fp32 sum drops each one that it adds to it.  The kernel adds at most eight
+    squares in fp32 (four roundings of 2^-24 of the sum, halved by the root), the rest with its errors carried; rstd is
+    rounded once (2^-24)."""
+    M = 64
+    x = torch.ones((M, d), dtype=torch.bfloat16)
+    at = torch.randint(0, d, (M,), generator=torch.Generator().manual_seed(d))
+    x[torch.arange(M), at] = 4096.0
+    f = mx.add_rmsnorm_fwd(x.cuda(), torch.ones(d, dtype=torch.bfloat16).cuda(), eps=1e-5, axis=axis)
+    n = ref64.rmsnorm(x.double(), torch.ones(d).double(), float(torch.tensor(1e-5)))[1]
+    assert torch.all((ref64.f64(f["rstd"]) - n).abs() <= n * (2 + 1 + 0.1) * 2.0 ** -24)
