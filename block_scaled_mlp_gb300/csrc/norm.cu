@@ -158,9 +158,9 @@ MX_DEVINL f2 rstd_pair(f2 ss, float d, float eps, float& rstd) {
 //   EXACT goes by eps alone (short_number): with an eps of many bits no row's m is a
 // short square, unless the row makes up for eps bit by bit.  Asking every element's
 // row costs up to 5% of the two-axis kernel (registers) and 1 to 3% of the others.
-// Zero becomes 2^-149, which rounds to a zero code and a zero bf16.  Where r w
-// passes fp32 (|w| >= 2^64; from |r| = 2^64 on n is zero) y is NaN; multiplying
-// r n by w for such weights cost 2.5% of every call.
+// Zero becomes 2^-149, which rounds to a zero code and a zero bf16.  Where |r w|
+// passes fp32 y is NaN; multiplying r n by w for such weights cost 2.5% of every
+// call.  (Where a row's sum of squares passes it, n is zero, and y with it.)
 template <bool EXACT>
 MX_DEVINL float to_odd(float y, f2 n) {
   uint32_t v = __float_as_uint(y) | 1u;

@@ -456,8 +456,9 @@ MX_API int mx_fp8_grouped_mm(int mode, const void* aq, const float* amax_a, cons
  *
  *   r    = RN_bf16(x + residual) (x itself without a residual)
  *   rstd = (mean(r^2) + eps)^-1/2 per row, y = r * rstd * w, fp32
- *   x, residual [M, d], w [d]: bf16; residual may be NULL.  r^2 and r w are
- *   fp32: a row with |r| >= 2^64 has rstd 0, and y is NaN where |w| >= 2^64.
+ *   x, residual [M, d], w [d]: bf16; residual may be NULL.  A row's sum of r^2 and
+ *   the products r w are fp32: where the sum passes it (2^128; every |r| at 2^57 is
+ *   enough for d = 16384) rstd and y are 0, and y is NaN where |r w| does.
  *   r       [M, d] bf16 out, only with a residual (it may be x or residual).
  *   rstd    [M] fp32 out.
  *   y       [M, d] bf16 out, RN of the fp32 y; may be NULL.

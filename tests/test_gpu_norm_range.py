@@ -42,3 +42,41 @@ def test_statistic_of_a_row_with_one_large_value(d, axis):
     f = mx.add_rmsnorm_fwd(x.cuda(), torch.ones(d, dtype=torch.bfloat16).cuda(), eps=1e-5, axis=axis)
     n = ref64.rmsnorm(x.double(), torch.ones(d).double(), float(torch.tensor(1e-5)))[1]
     assert torch.all((ref64.f64(f["rstd"]) - n).abs() <= n * (2 + 1 + 0.1) * 2.0 ** -24)
+
+
+@pytest.mark.parametrize("axis", [1, 3])
+@pytest.mark.parametrize("d", [64, 1024, 16384])
+def test_sum_of_squares_past_fp32(d, axis):
+    """sum r^2 = 2^128: rstd and every result are zero; half of it: the norm."""
+    M = 32
+    over = torch.full((M, d), 2.0 ** 60, dtype=torch.bfloat16)
+    over[:, 0] = 2.0 ** 64
+    w = torch.ones(d, dtype=torch.bfloat16)
+    f = mx.add_rmsnorm_fwd(over.cuda(), w.cuda(), axis=axis, layout=mx.SCALE_LINEAR)
+    assert not f["rstd"].any() and not f["y"].any() and not f["q_row"].any() and not f["s_row"].any()
+    under = torch.full((M, d), 2.0 ** 56, dtype=torch.bfloat16)
+    f = mx.add_rmsnorm_fwd(under.cuda(), w.cuda(), axis=axis, layout=mx.SCALE_LINEAR)
+    assert torch.all(f["rstd"] == 2.0 ** -56) and torch.all(f["y"] == 1)
+    if d == 16384:                                            # sum r^2 = 2^128 with every |r| = 2^57
+        f = mx.add_rmsnorm_fwd((under * 2).cuda(), w.cuda(), axis=axis, layout=mx.SCALE_LINEAR)
+        assert not f["rstd"].any() and not f["y"].any()
+
+
+@pytest.mark.parametrize("axis", [0, 1, 3])
+def test_weights_past_the_product(axis):
+    """|r w| < 2^128 is in range, whatever w is; from there on y is NaN, in that element alone."""
+    M, d = 32, 256
+    x = torch.ones((M, d), dtype=torch.bfloat16)
+    x[:, 7] = 2.0
+    w = torch.full((d,), 2.0 ** 100, dtype=torch.bfloat16)
+    w[7] = 2.0 ** 127
+    w[9] = 2.0 ** 127
+    f = mx.add_rmsnorm_fwd(x.cuda(), w.cuda(), axis=axis, layout=mx.SCALE_LINEAR)
+    y = (x.double() * w.double()) / torch.sqrt((x.double() ** 2).mean(1, keepdim=True) + 1e-5)
+    got = ref64.f64(f["y"])
+    assert torch.isnan(got[:, 7]).all()
+    keep = torch.arange(d) != 7
+    assert torch.all((got - y).abs()[:, keep] <= y[:, keep] * (2.0 ** -8 + 2.5e-6))
+    if axis:
+        s = f["s_row"].view(M, d // 32)
+        assert torch.all(s[:, 0] == 255) and not (s[:, 1:] == 255).any()
