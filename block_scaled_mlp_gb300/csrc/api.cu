@@ -18,7 +18,7 @@ namespace {
 thread_local char g_msg[512] = "";
 std::once_flag g_encode_once;
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
-int g_sms[64] = {0};
+std::atomic<int> g_sms[64];  // 0: not asked yet
 std::atomic<long long> g_launches[MX_KERNEL_FAMILIES];
 }  // namespace
 
@@ -42,12 +42,12 @@ int cuda_status(cudaError_t e, const char* what) {
 int num_sms() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
-  if (g_sms[dev] == 0) {
-    int n = 0;
+  int n = g_sms[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
-    g_sms[dev] = n;
+    g_sms[dev].store(n, std::memory_order_relaxed);
   }
-  return g_sms[dev];
+  return n;
 }
 
 namespace {

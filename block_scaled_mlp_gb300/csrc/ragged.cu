@@ -36,6 +36,8 @@
 // partial tiles bring 32 KB a step and CTA from L2 for little work, and the last
 // wave is not full: 4096 rows over 16 experts, 5120 x 8192, 281 / 272 / 317 us,
 // 1.1 to 1.3 PFLOP/s and 4.2 to 4.9 TB/s of weights.
+#include <atomic>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -542,11 +544,11 @@ __global__ void __launch_bounds__(RCfg<MODE, BT, S>::THREADS, 1)
 template <int MODE, int BT, int S>
 int resident_clusters(int* n) {
   using C = RCfg<MODE, BT, S>;
-  static int resident[64] = {0};  // the number + 1, once known
+  static std::atomic<int> resident[64];  // the number + 1, once known; any thread may be the one that asks
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_status(e, "cudaGetDevice");
-  int& r = resident[dev & 63];
+  int r = resident[dev & 63].load(std::memory_order_relaxed);
   if (r == 0) {
     auto k = ragged_kernel<MODE, BT, S>;
     e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
@@ -566,6 +568,7 @@ int resident_clusters(int* n) {
     e = cudaOccupancyMaxActiveClusters(&m, k, &cfg);
     if (e != cudaSuccess) return cuda_status(e, "cudaOccupancyMaxActiveClusters");
     r = m + 1;
+    resident[dev & 63].store(r, std::memory_order_relaxed);
   }
   *n = r - 1;
   return MX_OK;

@@ -21,9 +21,9 @@ def _flat(v):
 
 
 def _together(calls, rounds):
-    want = [_flat(c()) for c in calls]
+    """The calls at once, before any of them ran alone."""
     torch.cuda.synchronize()
-    failed, differ, old = [], [], sys.getswitchinterval()
+    failed, got, old = [], [None] * len(calls), sys.getswitchinterval()
     sys.setswitchinterval(1e-5)
 
     def work(i):
@@ -31,13 +31,11 @@ def _together(calls, rounds):
         with torch.cuda.stream(s):
             for _ in range(rounds):
                 try:
-                    got = _flat(calls[i]())
+                    got[i] = _flat(calls[i]())
                 except Exception as e:  # noqa: BLE001
                     failed.append((i, str(e)))
                     return
             s.synchronize()
-            if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
-                differ.append(i)
 
     threads = [threading.Thread(target=work, args=(i,)) for i in range(len(calls))]
     try:
@@ -47,7 +45,9 @@ def _together(calls, rounds):
             t.join()
     finally:
         sys.setswitchinterval(old)
-    assert not failed and not differ, (failed, differ)
+    assert not failed, failed
+    for call, mine in zip(calls, got):
+        assert all(torch.equal(a, b) for a, b in zip(mine, _flat(call())))
 
 
 def _bf16(shape, seed):
@@ -71,3 +71,13 @@ def test_norm_backward_of_two_widths(ckpt):
         kept = f["ckpt"] if ckpt else x
         calls.append(lambda w=w, dy=dy, kept=kept, n=f["rstd"]: mx.add_rmsnorm_bwd(dy, kept, n, w))
     _together(calls, 2000)
+
+
+def test_ragged_products_of_several_shapes():
+    """Several tile shapes, each of which asks the device once how many of its clusters it holds."""
+    calls = []
+    for i, (counts, N, K) in enumerate([([8], 512, 7168), ([100], 1024, 4096), ([300, 17], 264, 328), ([40] * 30, 1032, 264)]):
+        offs = torch.tensor(counts, dtype=torch.int32).cumsum(0).to(torch.int32).cuda()
+        x, w = _bf16((sum(counts), K), i), _bf16((len(counts), N, K), i + 5)
+        calls.append(lambda x=x, w=w, offs=offs: mx.ragged_mm(x, w, offs))
+    _together(calls, 300)
