@@ -75,6 +75,7 @@ _SIGS = {
     "mx_gather_rows": ([_V, _I64, _I64, _V, _I64, _I32, _V, _V, _V], _I),
     "mx_selftest_wait_timeout": ([_V, _V], _I),
     "mx_selftest_silu_table": ([_V, _V], _I),
+    "mx_selftest_norm_clusters": ([_I], _I),
     "mx_launch_counts": ([ctypes.POINTER(ctypes.c_int64), _I], _I),
     "mx_fp8_amax": ([_V, _I64, _I64, _V, _V], _I),
     "mx_fp8_quantize": ([_V, _I64, _I64, _I64, _V, _I, _V, _V, _V], _I),

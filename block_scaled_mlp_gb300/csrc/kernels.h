@@ -164,6 +164,7 @@ struct NormFwdLaunch {
   int floor_scale;
 };
 int launch_add_rmsnorm_fwd(const NormFwdLaunch& a, cudaStream_t stream);
+void set_norm_cluster_limit(int most);
 struct NormBwdLaunch {
   const void* dy;         // [M, d] bf16
   const void* r;          // [M, d] bf16, or NULL with

@@ -18,6 +18,7 @@
 
 #include <string.h>
 
+#include <atomic>
 #include <type_traits>
 
 namespace mx {
@@ -307,9 +308,10 @@ constexpr int NC_ROWS = 32;
 constexpr int NC_THREADS = 256;
 constexpr int NC_MAX_CTAS = 16;
 constexpr int NC_CTAS_SM = 4;
+constexpr int NC_PORTABLE_CTAS = 8;  // a cluster that every device holds
 // Shared memory of the widest slice.  The kernels' limit is this for every call: it is
 // the function's, not the launch's, and another thread may launch with another width.
-constexpr int NC_MAX_SMEM = NC_ROWS * (int)(kNormMaxD / NC_MAX_CTAS) * 2;
+constexpr int NC_MAX_SMEM = NC_ROWS * (int)(kNormMaxD / NC_PORTABLE_CTAS) * 2;
 
 MX_DEVINL void copy_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
@@ -774,7 +776,59 @@ NormBwdShape bwd_shape(int64_t d, bool ck, bool dres) {
   return s;
 }
 
+// Two-axis kernels by [exact][residual][checkpoint][bf16 y][row codes].
+using ColKernel = void (*)(NormFwdParams, int32_t);
+#define MX_NC(R, C, X) {{add_rmsnorm_col_kernel<R, C, false, false, X>, add_rmsnorm_col_kernel<R, C, false, true, X>}, \
+                        {add_rmsnorm_col_kernel<R, C, true, false, X>, add_rmsnorm_col_kernel<R, C, true, true, X>}}
+const ColKernel col_kernels[2][2][2][2][2] = {
+    {{MX_NC(false, false, false), MX_NC(false, true, false)}, {MX_NC(true, false, false), MX_NC(true, true, false)}},
+    {{MX_NC(false, false, true), MX_NC(false, true, true)}, {MX_NC(true, false, true), MX_NC(true, true, true)}}};
+#undef MX_NC
+
+int col_attributes(ColKernel k) {
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, NC_MAX_SMEM);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  return cuda_status(e, "cudaFuncSetAttribute");
+}
+
+// CTAs of a cluster, at most: sixteen, or eight where no part of the device (a slice of
+// one, say) holds sixteen.  The kernels differ in nothing that counts for it, so one
+// is asked about, once a device.
+std::atomic<int> g_col_limit;  // mx_selftest_norm_clusters
+int col_cluster_limit(int* most) {
+  static std::atomic<int> held[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_status(e, "cudaGetDevice");
+  int n = held[dev & 63].load(std::memory_order_relaxed);
+  if (n == 0) {
+    const ColKernel k = col_kernels[0][1][1][1][1];
+    if (int rc = col_attributes(k)) return rc;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1, NC_MAX_CTAS);
+    cfg.blockDim = dim3(NC_THREADS);
+    cfg.dynamicSmemBytes = NC_ROWS * (kNormMaxD / NC_MAX_CTAS) * 2;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1;
+    attr[0].val.clusterDim.y = NC_MAX_CTAS;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int m = 0;
+    e = cudaOccupancyMaxActiveClusters(&m, k, &cfg);
+    if (e != cudaSuccess) return cuda_status(e, "cudaOccupancyMaxActiveClusters");
+    n = m > 0 ? NC_MAX_CTAS : NC_PORTABLE_CTAS;
+    held[dev & 63].store(n, std::memory_order_relaxed);
+  }
+  const int limit = g_col_limit.load(std::memory_order_relaxed);
+  *most = limit ? std::min(limit, n) : n;
+  return MX_OK;
+}
+
 }  // namespace
+
+void set_norm_cluster_limit(int most) { g_col_limit.store(most, std::memory_order_relaxed); }
 
 // CTAs of the backward pass: each with two rows at least, beyond two an SM (1200 x
 // 1024: 7.2 us, 8.0 with a row each, whose partial gradients outweigh it).
@@ -799,7 +853,6 @@ int launch_add_rmsnorm_fwd(const NormFwdLaunch& a, cudaStream_t stream) {
   p.ck = (uint8_t*)a.ck; p.ck_s = (uint8_t*)a.ck_scales;
   const int64_t padded = mma && (a.q_row || a.q_col) ? (a.M + 127) / 128 * 128 : a.M;  // rows of the scale layout
   if (padded > INT32_MAX) return fail(MX_ERR_UNSUPPORTED, "norm: too many rows");
-  cudaError_t e;
   if (a.q_col) {
     // Slices of a multiple of 256 columns (whole warps).  Enough rows: at least
     // 512 columns, so that clusters stay small (16384 x 2048: 63 us on four CTAs,
@@ -809,25 +862,15 @@ int launch_add_rmsnorm_fwd(const NormFwdLaunch& a, cudaStream_t stream) {
     // (under two 512-column slices an SM): as many CTAs as there can be (32 x 7168:
     // 6.7 us on fourteen, 9.4 on seven; 1024 x 2048: 7.3 us on eight, 8.5 on four).
     const bool few = padded / NC_ROWS * ((p.d8 + 63) / 64) <= 2 * (int64_t)num_sms();
-    const int most = few || p.d8 > 11 * 96 ? 16 : 11;
+    int limit;
+    if (int rc = col_cluster_limit(&limit)) return rc;
+    const int most = std::min(limit, few || p.d8 > 11 * 96 ? NC_MAX_CTAS : 11);
     const int slice8 = std::max(few ? 32 : 64, ((p.d8 + 31) / 32 + most - 1) / most * 32);
     const int ctas = (p.d8 + slice8 - 1) / slice8;
     const size_t smem = (size_t)NC_ROWS * slice8 * 16;
-    using Kernel = void (*)(NormFwdParams, int32_t);
-    // [exact][residual][checkpoint][bf16 y][row codes]
-#define MX_NC(R, C, X) {{add_rmsnorm_col_kernel<R, C, false, false, X>, add_rmsnorm_col_kernel<R, C, false, true, X>}, \
-                        {add_rmsnorm_col_kernel<R, C, true, false, X>, add_rmsnorm_col_kernel<R, C, true, true, X>}}
-    static const Kernel kernels[2][2][2][2][2] = {
-        {{MX_NC(false, false, false), MX_NC(false, true, false)}, {MX_NC(true, false, false), MX_NC(true, true, false)}},
-        {{MX_NC(false, false, true), MX_NC(false, true, true)}, {MX_NC(true, false, true), MX_NC(true, true, true)}}};
-#undef MX_NC
-    const Kernel k = kernels[short_number(p.eps)][p.res != nullptr][p.ck != nullptr][p.y != nullptr][p.q_row != nullptr];
-    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, NC_MAX_SMEM);
-    if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute");
-    if (ctas > 8) {
-      e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-      if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute");
-    }
+    const ColKernel k =
+        col_kernels[short_number(p.eps)][p.res != nullptr][p.ck != nullptr][p.y != nullptr][p.q_row != nullptr];
+    if (int rc = col_attributes(k)) return rc;
     count_launch(MX_KERNEL_NORM);
     return cuda_status(launch_overlapped(k, dim3((unsigned)(padded / NC_ROWS), (unsigned)ctas), NC_THREADS, smem, stream,
                                          dim3(1, (unsigned)ctas), p, (int32_t)slice8),

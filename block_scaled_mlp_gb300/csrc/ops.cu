@@ -68,6 +68,12 @@ int mx_add_rmsnorm_fwd(const void* x, const void* residual, const void* w, int64
   return launch_add_rmsnorm_fwd(a, (cudaStream_t)stream);
 }
 
+int mx_selftest_norm_clusters(int most) {
+  if (most != 0 && most != 8) return fail(MX_ERR_INVALID_ARG, "most must be 0 or 8");
+  set_norm_cluster_limit(most);
+  return MX_OK;
+}
+
 size_t mx_add_rmsnorm_bwd_workspace(int64_t M, int64_t d) {
   if (M <= 0 || d <= 0 || d > kNormMaxD) return 0;
   return (size_t)norm_bwd_ctas(M, d) * (size_t)d * 4;

@@ -595,6 +595,13 @@ MX_API int mx_selftest_wait_timeout(int32_t* err_word, void* stream);
  */
 MX_API int mx_selftest_silu_table(uint16_t* dst, void* stream);
 
+/*
+ * mx_selftest_norm_clusters - test entry: later calls of mx_add_rmsnorm_fwd with
+ * column codes use clusters of at most `most` CTAs, as on a device that holds
+ * no larger ones (8), or what the device holds (0, as it is from the start).
+ */
+MX_API int mx_selftest_norm_clusters(int most);
+
 #ifdef __cplusplus
 }
 #endif

@@ -49,3 +49,28 @@ def test_sum_may_replace_an_input_with_codes(M, d, axis):
         assert torch.equal(r, want["r"])
         assert all(torch.equal(new[k], want[k]) for k in new if new[k] is not None)
         assert torch.equal(ck.codes, want["ckpt"].codes) and torch.equal(ck.scales, want["ckpt"].scales)
+
+
+@pytest.fixture
+def small_clusters():
+    """As on a device that holds no cluster of more than eight CTAs."""
+    assert mx.lib().mx_selftest_norm_clusters(8) == 0
+    yield
+    assert mx.lib().mx_selftest_norm_clusters(0) == 0
+
+
+@pytest.mark.parametrize("M,d", [(32, 32), (32, 2304), (64, 7168), (32, 8224), (32, 16384), (4096, 8192), (2048, 12320)])
+def test_clusters_of_eight(M, d, small_clusters):
+    x, res, w = _inputs(M, d, True, M + d)
+    f = mx.add_rmsnorm_fwd(x.cuda(), w.cuda(), res.cuda(), eps=EPS, axis=mx.BOTH, layout=mx.SCALE_LINEAR, ckpt=True)
+    r = (x.float() + res.float()).to(torch.bfloat16)
+    y, n = ref64.rmsnorm(r.double(), w.double(), EPS)
+    assert torch.equal(f["r"].cpu(), r)
+    assert torch.all((ref64.f64(f["rstd"]) - n).abs() <= n * EY)
+    _check_codes(f["q_row"], f["s_row"].view(M, d // 32), y)
+    _check_codes(f["q_col"], f["s_col"].view(d, M // 32), y.t().contiguous())
+    assert torch.equal(ref64.f64(mx.ckpt8_load(f["ckpt"])), ref64.int8_values(r.double()))
+
+
+def test_refuses_other_cluster_limits():
+    assert mx.lib().mx_selftest_norm_clusters(3) == 1 and mx.lib().mx_selftest_norm_clusters(-1) == 1
