@@ -5,7 +5,9 @@ linked into ``block_scaled_mlp_gb300/libmxmlp.so`` (static CUDA runtime, no
 libcuda link: the driver entry point for tensor maps is looked up at run
 time, so the library also loads on machines without a GPU driver).  Beside it
 ``_binding.so``, the Python binding of the operators whose calls are short
-(csrc/binding.cpp, compiled against the installed torch's headers).
+(csrc/binding.cpp, compiled against the installed torch's headers, and again
+when another torch is installed).  Where that does not compile the library is
+built all the same, with a warning; the calls that need the binding then raise.
 """
 from __future__ import annotations
 
@@ -57,6 +59,13 @@ def _torch_flags():
     return [abi, *("-I" + i for i in inc)], libs
 
 
+def _torch_key() -> str:
+    """What a compiled binding depends on besides its sources."""
+    import torch
+
+    return f"{sys.implementation.cache_tag} torch {torch.__version__} {os.path.dirname(torch.__file__)}"
+
+
 def build(verbose: bool = False, force: bool = False, extra_flags=None) -> str:
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
@@ -81,16 +90,21 @@ def build(verbose: bool = False, force: bool = False, extra_flags=None) -> str:
             raise RuntimeError(f"{what} failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
 
     binding_src, binding_obj = os.path.join(CSRC, "binding.cpp"), os.path.join(BUILD, "binding.o")
+    key_file, key = os.path.join(BUILD, "binding.key"), _torch_key()
 
     def compile_binding():
-        if force or _stale(binding_obj, [binding_src, headers[-1]]):
+        old = open(key_file).read() if os.path.exists(key_file) else None
+        if force or old != key or _stale(binding_obj, [binding_src, headers[-1]]):
+            if os.path.exists(key_file):
+                os.remove(key_file)
             run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", *_torch_flags()[0], "-c", binding_src, "-o",
                  binding_obj], "g++ for binding.cpp")
+            with open(key_file, "w") as f:
+                f.write(key)
 
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         binding = ex.submit(compile_binding)
         results = list(ex.map(compile_one, SOURCES))
-        binding.result()
     objs = [o for o, _ in results]
     if verbose:
         for _, log in results:
@@ -101,9 +115,15 @@ def build(verbose: bool = False, force: bool = False, extra_flags=None) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
-    if force or _stale(BINDING, [binding_obj]):
-        run(["g++", "-shared", "-o", BINDING, binding_obj, f"-L{HERE}", "-l:libmxmlp.so", "-Wl,-rpath,$ORIGIN",
-             *_torch_flags()[1]], "link of the binding")
+    try:
+        binding.result()
+        if force or _stale(BINDING, [binding_obj]):
+            run(["g++", "-shared", "-o", BINDING, binding_obj, f"-L{HERE}", "-l:libmxmlp.so", "-Wl,-rpath,$ORIGIN",
+                 *_torch_flags()[1]], "link of the binding")
+    except (RuntimeError, OSError) as e:
+        if os.path.exists(BINDING):  # one of other sources or another torch
+            os.remove(BINDING)
+        print(f"warning: {BINDING} is not built, the operators around the MLP will raise\n{e}", file=sys.stderr)
     return LIB
 
 
