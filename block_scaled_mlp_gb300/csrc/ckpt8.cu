@@ -26,9 +26,12 @@ namespace {
 
 constexpr int C8_THREADS = 256;
 
-// s = 1 / (1 + e^-g) by the approximate exponential and reciprocal (a few
-// units of 2^-23: far below the bf16 rounding of every result).  e^-g
-// overflows to infinity below g = -88.7 and s is 0 there.
+// s = 1 / (1 + e^-g) by the approximate exponential and division.  CUDA's bounds for
+// them are 2 + 1.173 |g| units in the last place and two units: s is off by some 5
+// units of 2^-23 near g = 0, 30 at g = -20 and 110 at -87, 1.3e-5 of itself, where a
+// bf16 result is rounded by 2^-9.  For 8192 x 14336, forward and backward, it takes
+// 140 and 183 us; with expf, to one unit, 145 and 194, with an IEEE division besides
+// 160 and 236.  Below g = -87.3 the denominator passes 2^126 and s is 0 (1e-38).
 MX_DEVINL float sigmoid_approx(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
 
 // A thread has vectors i and i + C8_THREADS of its CTA's 2 * C8_THREADS.
