@@ -12,8 +12,8 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
-#include <algorithm>
 #include <string>
+#include <utility>
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
@@ -318,7 +318,8 @@ PyObject* py_ragged(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor& t = matrix(a[1], mode == MX_RAGGED_FWD ? "x" : "dout");
     const at::Tensor& offs = need(a[3], "offs", at::kInt, &t);
     void* err = a[4] == Py_None ? nullptr : ptr(need(a[4], "err", at::kInt, {1}, &t));
-    const int64_t M = t.size(0), E = std::min<int64_t>(offs.numel(), INT32_MAX);
+    const int64_t M = t.size(0), E = offs.numel();
+    if (E < 1 || E > 1024) refuse("E must be in [1, 1024], got " + std::to_string(E));  // before dw is allocated
     int64_t N, K;
     const at::Tensor* b;
     at::Tensor c;
