@@ -30,6 +30,8 @@ __all__ = [
     "KERNEL_FAMILIES", "launch_counts", "fp8_amax", "fp8_quantize", "fp8_grouped_mm",
     "Ckpt8", "ckpt8_save", "ckpt8_load", "swiglu_ckpt8_fwd", "swiglu_ckpt8_bwd", "add_rmsnorm_fwd", "add_rmsnorm_bwd",
     "ragged_mm", "ragged_mm_dgrad", "ragged_mm_wgrad",
+    "SCORE_SOFTMAX", "SCORE_SIGMOID", "moe_route", "moe_route_bwd", "token_group", "moe_combine", "moe_combine_bwd",
+    "Fp8Block", "Fp8BlockWeight", "fp8_block_quantize", "fp8_block_quantize_weight", "fp8_block_mm", "fp8_block_mm_dgrad",
 ]
 
 ROW, COL, BOTH = 1, 2, 3
@@ -38,6 +40,7 @@ RECIPE_RCEIL, RECIPE_RCEIL_WGRAD_HP, RECIPE_FLOOR, RECIPE_FLOOR_WGRAD_HP = 0, 1,
 SCALE_RCEIL, SCALE_FLOOR = 0, 1
 GROUP_M, GROUP_K = 0, 1
 RAGGED_FWD, RAGGED_DGRAD, RAGGED_WGRAD = 0, 1, 2
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_HERE, "libmxmlp.so")
@@ -87,6 +90,15 @@ _SIGS = {
     "mx_swiglu_ckpt8_fwd": ([_V, _I64, _I64, _V, _V, _V, _V], _I),
     "mx_swiglu_ckpt8_bwd": ([_V, _V, _V, _I64, _I64, _V, _V, _V], _I),
     "mx_ragged_mm": ([_I, _V, _V, _I64, _I64, _I64, _V, _I32, _V, _V, _V], _I),
+    "mx_moe_route": ([_V, _I, _I64, _I32, _I32, _I, _V, _I32, _I32, _I, _F, _V, _V, _V], _I),
+    "mx_moe_route_bwd": ([_V, _V, _I, _V, _I64, _I32, _I32, _I, _I, _F, _V, _V, _V], _I),
+    "mx_token_group_workspace": ([_I64, _I32], ctypes.c_size_t),
+    "mx_token_group": ([_V, _I64, _I32, _V, _V, _V, _V, _V, _V], _I),
+    "mx_moe_combine": ([_V, _I64, _I64, _V, _I64, _I32, _V, _V, _V, _V, _V], _I),
+    "mx_moe_combine_bwd": ([_V, _V, _I64, _I64, _V, _V, _I64, _I32, _V, _V, _V, _V, _V], _I),
+    "mx_fp8_block_quantize": ([_V, _I64, _I64, _V, _I64, _I32, _V, _V, _V, _V], _I),
+    "mx_fp8_block_quantize_weight": ([_V, _I64, _I64, _I64, _V, _V, _V, _V], _I),
+    "mx_fp8_block_mm": ([_I, _V, _V, _V, _V, _I64, _I64, _I64, _V, _I32, _V, _V, _V], _I),
     "mx_fp8_grouped_mm": ([_I, _V, _V, _V, _V, _I64, _I64, _I64, _V, _I32, _I32, _V, _V, _V], _I),
 }
 
@@ -139,7 +151,7 @@ def _need(t, dtype, name):
 
 
 KERNEL_FAMILIES = ("quant", "swiglu_fwd", "swiglu_bwd", "gemm", "gemm_swiglu", "dispatch", "memset", "norm",
-                   "ckpt8", "ragged")
+                   "ckpt8", "ragged", "route", "fp8_block")
 
 
 def silu_table():
@@ -643,3 +655,108 @@ def ragged_mm_wgrad(dout, x, offs, err: ErrorWord | None = None):
     """dw [E, N, K], dw[e] = dout[group e]^T . x[group e]: the gradient of
     ragged_mm's w, from the token-major operands as they lie."""
     return (_ext or _fast()).ragged(RAGGED_WGRAD, dout, x, offs, _word(err))
+
+
+# ---------------------------------------------------------------- routing
+
+
+def moe_route(logits, k, score=SCORE_SOFTMAX, bias=None, groups=1, top_groups=1, renorm=True, scale=1.0):
+    """(ids [T, k] int32, weights [T, k] fp32): the k experts of each token and their weights, from a router's logits
+    [T, E] (bf16 or fp32).
+
+    Scores are the softmax or the sigmoid of the logits; bias [E] fp32 is added to choose experts and does not enter
+    the weights.  With groups > 1 the top_groups groups of E / groups neighbours whose two best experts are worth most
+    are taken first.  ids go from the best expert down, equal ones by number, decided in double precision.
+    weights = scale * score, renormalised over the k (renorm) or not."""
+    return (_ext or _fast()).moe_route(logits, k, score, bias, groups, top_groups, renorm, scale)
+
+
+def moe_route_bwd(dweights, logits, ids, score=SCORE_SOFTMAX, renorm=True, scale=1.0, err: ErrorWord | None = None):
+    """dlogits [T, E] (the logits' type) from dweights [T, k] fp32 and moe_route's ids and arguments."""
+    return (_ext or _fast()).moe_route_bwd(dweights, logits, ids, score, renorm, scale, _word(err))
+
+
+def token_group(expert_of, E: int, err: ErrorWord | None = None):
+    """Routed rows grouped by expert without padding, as ragged_mm and fp8_block_mm take them: (offs [E] group ends,
+    row_dst [R], row_src [R]), int32 on the device, from R expert numbers (int32, any shape).  Rows of a group keep
+    their order.  token_group_pad gives the padded layout of grouped_mm."""
+    return (_ext or _fast()).token_group(expert_of, E, _word(err))
+
+
+def moe_combine(rows, row_dst, weights=None, k: int | None = None, add=None, err: ErrorWord | None = None):
+    """out [T, d] = add + the sum of each token's k rows times weights [T, k] fp32 (ones without; then k is needed):
+    rows [n, d] bf16 where row_dst [T * k] says, add [T, d] bf16 or None.  Negative row_dst: no row."""
+    return (_ext or _fast()).moe_combine(rows, row_dst, weights, k, add, _word(err))
+
+
+def moe_combine_bwd(dout, rows, row_dst, row_src, weights, err: ErrorWord | None = None):
+    """(drows [n, d] bf16, dweights [T, k] fp32) of moe_combine from dout [T, d]; rows that hold no routed row
+    (row_src < 0) get zeros.  The gradient of add is dout."""
+    return (_ext or _fast()).moe_combine_bwd(dout, rows, row_dst, row_src, weights, _word(err))
+
+
+# ---------------------------------------------------------------- FP8 with a scale for 128 elements
+
+
+class Fp8Block:
+    """Token rows in E4M3: codes uint8 [rows, cols], scales fp32 [ceil(cols / 128), rows] (one for 128 neighbours of a
+    row; value = code * scale)."""
+
+    __slots__ = ("codes", "scales")
+
+    def __init__(self, codes, scales):
+        self.codes = codes
+        self.scales = scales
+
+    @property
+    def shape(self):
+        return self.codes.shape
+
+
+class Fp8BlockWeight:
+    """A weight in E4M3: codes uint8 [(E,) N, K], codes_t [(E,) K, N] (the same, transposed, for the input gradient; or
+    None), scales fp32 [(E,) ceil(N / 128), ceil(K / 128)] (one for each 128 x 128 block)."""
+
+    __slots__ = ("codes", "codes_t", "scales")
+
+    def __init__(self, codes, codes_t, scales):
+        self.codes = codes
+        self.codes_t = codes_t
+        self.scales = scales
+
+    @property
+    def shape(self):
+        return self.codes.shape
+
+
+def fp8_block_quantize(x, src=None, div: int = 1, err: ErrorWord | None = None):
+    """Fp8Block of a bf16 [rows, cols] matrix (cols % 16 == 0); with src (int32) of the rows x[src[i] // div], zero
+    rows for src[i] < 0, as gather_rows gives them."""
+    return Fp8Block(*(_ext or _fast()).fp8_block_quantize(x, src, div, _word(err)))
+
+
+def fp8_block_quantize_weight(w, transposed=True):
+    """Fp8BlockWeight of a bf16 [(E,) N, K] weight (N, K % 16 == 0); transposed=False: for the forward product alone."""
+    return Fp8BlockWeight(*(_ext or _fast()).fp8_block_quantize_weight(w, transposed))
+
+
+def _kind(t, kind, name):
+    if not isinstance(t, kind):
+        raise MxError(1, f"{name} must be a {kind.__name__}")
+    return t
+
+
+def fp8_block_mm(x: Fp8Block, w: Fp8BlockWeight, offs=None, err: ErrorWord | None = None):
+    """out [M, N] bf16 = x [M, K] . w^T, dense (w [N, K]) or by expert (w [E, N, K], offs as in ragged_mm; rows past
+    the last group are zeros)."""
+    _kind(x, Fp8Block, "x"), _kind(w, Fp8BlockWeight, "w")
+    return (_ext or _fast()).fp8_block_mm(RAGGED_FWD, x.codes, x.scales, w.codes, w.scales, offs, _word(err))
+
+
+def fp8_block_mm_dgrad(dout: Fp8Block, w: Fp8BlockWeight, offs=None, err: ErrorWord | None = None):
+    """dx [M, K] bf16 = dout [M, N] . w: the gradient of fp8_block_mm's x.  That of w contracts over tokens and stays in
+    bf16 (ragged_mm_wgrad, bf16_wgrad)."""
+    _kind(dout, Fp8Block, "dout"), _kind(w, Fp8BlockWeight, "w")
+    if w.codes_t is None:
+        raise MxError(1, "w holds no transposed codes")
+    return (_ext or _fast()).fp8_block_mm(RAGGED_DGRAD, dout.codes, dout.scales, w.codes_t, w.scales, offs, _word(err))

@@ -1,5 +1,5 @@
 // binding.cpp - Python binding of the operators around the MLP (norm, 8-bit
-// checkpoints, ragged products) on torch tensors.
+// checkpoints, ragged products, routing, FP8 with 128-blocks) on torch tensors.
 //
 // These calls take 2 to 5 us on the device at their smallest, and a binding in
 // Python took 12 to 20 us for one: a microsecond and a half for each output that
@@ -349,6 +349,225 @@ PyObject* py_ragged(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// A router's logits: a matrix of bf16 or fp32.
+const at::Tensor& logits_of(PyObject* o, const at::Tensor* first = nullptr) {
+  const bool wide = THPVariable_Check(o) && THPVariable_Unpack(o).scalar_type() == at::kFloat;
+  const at::Tensor& t = need(o, "logits", wide ? at::kFloat : at::kBFloat16, first);
+  if (t.dim() != 2) refuse("logits must be a matrix, got " + shape_text(t.sizes()));
+  return t;
+}
+
+int float_type(const at::Tensor& t) { return t.scalar_type() == at::kFloat ? MX_FP32 : MX_BF16; }
+
+float number(PyObject* o, const char* name) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) {
+    PyErr_Clear();
+    refuse(std::string(name) + " must be a number");
+  }
+  return (float)v;
+}
+
+int32_t* error_word(PyObject* o, const at::Tensor& first) {
+  return o == Py_None ? nullptr : (int32_t*)ptr(need(o, "err", at::kInt, {1}, &first));
+}
+
+// Experts of a matrix of logits, as the C entries take them.
+int32_t experts_of(const at::Tensor& logits) {
+  const int64_t E = logits.size(1);
+  if (E < 1 || E > 1024) refuse("E must be in [1, 1024], got " + std::to_string(E));
+  return (int32_t)E;
+}
+
+// Refused before an output of that width is allocated.
+int32_t top_k(PyObject* o, int64_t E) {
+  const int k = small_integer(o, "k");
+  if (k < 1 || k > 32 || k > E) refuse("k must be in [1, 32] and at most E, got " + std::to_string(k));
+  return k;
+}
+
+// moe_route(logits, k, score, bias, groups, top_groups, renorm, scale) -> (ids, weights)
+PyObject* py_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&] {
+    arguments(n, 8);
+    const at::Tensor& l = logits_of(a[0]);
+    const int64_t T = l.size(0);
+    const int32_t E = experts_of(l), k = top_k(a[1], E);
+    const int score = small_integer(a[2], "score"), groups = small_integer(a[4], "groups");
+    const at::Tensor* bias = a[3] == Py_None ? nullptr : &need(a[3], "bias", at::kFloat, {(int64_t)E}, &l);
+    const int top = small_integer(a[5], "top_groups");
+    const bool renorm = truth(a[6], "renorm");
+    const float scale = number(a[7], "scale");
+    On on(l);
+    at::Tensor ids = empty({T, k}, at::kInt, l), w = empty({T, k}, at::kFloat, l);
+    on.finish(mx_moe_route(ptr(l), float_type(l), T, E, k, score, bias ? (const float*)ptr(*bias) : nullptr, groups, top, renorm,
+                           scale, (int32_t*)ptr(ids), (float*)ptr(w), on.stream));
+    return tuple_of(ids, w);
+  });
+}
+
+// moe_route_bwd(dweights, logits, ids, score, renorm, scale, err) -> dlogits
+PyObject* py_route_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&] {
+    arguments(n, 7);
+    const at::Tensor& l = logits_of(a[1]);
+    const int64_t T = l.size(0);
+    const int32_t E = experts_of(l);
+    const at::Tensor& dw = need(a[0], "dweights", at::kFloat, &l);
+    if (dw.dim() != 2 || dw.size(0) != T) refuse("dweights must be [" + std::to_string(T) + ", k], got " + shape_text(dw.sizes()));
+    const int64_t k = dw.size(1);
+    if (k < 1 || k > 32) refuse("k must be in [1, 32], got " + std::to_string(k));
+    const at::Tensor& ids = need(a[2], "ids", at::kInt, dw.sizes(), &l);
+    const int score = small_integer(a[3], "score");
+    const bool renorm = truth(a[4], "renorm");
+    const float scale = number(a[5], "scale");
+    int32_t* err = error_word(a[6], l);
+    On on(l);
+    at::Tensor d = empty(l.sizes(), l.scalar_type(), l);
+    on.finish(mx_moe_route_bwd((const float*)ptr(dw), ptr(l), float_type(l), (const int32_t*)ptr(ids), T, E, (int32_t)k, score,
+                               renorm, scale, ptr(d), err, on.stream));
+    return wrap(d);
+  });
+}
+
+// token_group(expert_of, E, err) -> (offs, row_dst, row_src)
+PyObject* py_token_group(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&] {
+    arguments(n, 3);
+    const at::Tensor& ids = need(a[0], "expert_of", at::kInt);
+    const int E = small_integer(a[1], "E");
+    if (E < 1 || E > 1024) refuse("E must be in [1, 1024], got " + std::to_string(E));
+    int32_t* err = error_word(a[2], ids);
+    const int64_t R = ids.numel();
+    On on(ids);
+    at::Tensor offs = empty({E}, at::kInt, ids), dst = empty({R}, at::kInt, ids), src = empty({R}, at::kInt, ids);
+    at::Tensor ws = empty({(int64_t)mx_token_group_workspace(R, E) + 16}, at::kByte, ids);
+    on.finish(mx_token_group((const int32_t*)ptr(ids), R, E, (int32_t*)ptr(offs), (int32_t*)ptr(dst), (int32_t*)ptr(src), ptr(ws),
+                             err, on.stream));
+    return tuple_of(offs, dst, src);
+  });
+}
+
+// moe_combine(rows, row_dst, weights, k, add, err) -> out; weights or k, and add, may be None
+PyObject* py_combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&] {
+    arguments(n, 6);
+    const at::Tensor& rows = matrix(a[0], "rows");
+    const at::Tensor& dst = need(a[1], "row_dst", at::kInt, &rows);
+    const at::Tensor* w = a[2] == Py_None ? nullptr : &need(a[2], "weights", at::kFloat, &rows);
+    if (w && w->dim() != 2) refuse("weights must be [T, k], got " + shape_text(w->sizes()));
+    if (!w && a[3] == Py_None) refuse("k is needed without weights");
+    const int64_t k = a[3] == Py_None ? w->size(1) : small_integer(a[3], "k");
+    if (k < 1 || k > 32) refuse("k must be in [1, 32], got " + std::to_string(k));
+    if (dst.numel() % k) refuse("row_dst must hold k numbers a token, got " + std::to_string(dst.numel()));
+    const int64_t T = dst.numel() / k, d = rows.size(1);
+    if (w) need(a[2], "weights", at::kFloat, {T, k}, &rows);
+    const at::Tensor* add = a[4] == Py_None ? nullptr : &need(a[4], "add", at::kBFloat16, {T, d}, &rows);
+    int32_t* err = error_word(a[5], rows);
+    On on(rows);
+    at::Tensor out = empty({T, d}, at::kBFloat16, rows);
+    on.finish(mx_moe_combine(ptr(rows), rows.size(0), d, (const int32_t*)ptr(dst), T, (int32_t)k, w ? (const float*)ptr(*w) : nullptr,
+                             add ? ptr(*add) : nullptr, ptr(out), err, on.stream));
+    return wrap(out);
+  });
+}
+
+// moe_combine_bwd(dout, rows, row_dst, row_src, weights, err) -> (drows, dweights)
+PyObject* py_combine_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&] {
+    arguments(n, 6);
+    const at::Tensor& dout = matrix(a[0], "dout");
+    const int64_t T = dout.size(0), d = dout.size(1);
+    const at::Tensor& rows = matrix(a[1], "rows", &dout);
+    if (rows.size(1) != d) refuse("rows must have " + std::to_string(d) + " columns, got " + shape_text(rows.sizes()));
+    const at::Tensor& w = need(a[4], "weights", at::kFloat, &dout);
+    if (w.dim() != 2 || w.size(0) != T) refuse("weights must be [" + std::to_string(T) + ", k], got " + shape_text(w.sizes()));
+    const int64_t k = w.size(1);
+    const at::Tensor& dst = need(a[2], "row_dst", at::kInt, &dout);
+    if (dst.numel() != T * k) refuse("row_dst must hold " + std::to_string(T * k) + " numbers, got " + std::to_string(dst.numel()));
+    const at::Tensor& src = need(a[3], "row_src", at::kInt, {rows.size(0)}, &dout);
+    if (k < 1 || k > 32) refuse("k must be in [1, 32], got " + std::to_string(k));
+    int32_t* err = error_word(a[5], dout);
+    On on(dout);
+    at::Tensor drows = empty(rows.sizes(), at::kBFloat16, dout), dw = empty({T, k}, at::kFloat, dout);
+    on.finish(mx_moe_combine_bwd(ptr(dout), ptr(rows), rows.size(0), d, (const int32_t*)ptr(dst), (const int32_t*)ptr(src), T,
+                                 (int32_t)k, (const float*)ptr(w), ptr(drows), (float*)ptr(dw), err, on.stream));
+    return tuple_of(drows, dw);
+  });
+}
+
+// fp8_block_quantize(x, src, div, err) -> (codes, scales); src may be None
+PyObject* py_fp8_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&] {
+    arguments(n, 4);
+    const at::Tensor& x = matrix(a[0], "x");
+    const at::Tensor* src = a[1] == Py_None ? nullptr : &need(a[1], "src", at::kInt, &x);
+    const int div = small_integer(a[2], "div");
+    int32_t* err = error_word(a[3], x);
+    const int64_t rows = src ? src->numel() : x.size(0), cols = x.size(1);
+    On on(x);
+    at::Tensor codes = empty({rows, cols}, at::kByte, x), sc = empty({(cols + 127) / 128, rows}, at::kFloat, x);
+    on.finish(mx_fp8_block_quantize(ptr(x), x.size(0), cols, src ? (const int32_t*)ptr(*src) : nullptr, rows, div, ptr(codes),
+                                    (float*)ptr(sc), err, on.stream));
+    return tuple_of(codes, sc);
+  });
+}
+
+// fp8_block_quantize_weight(w, transposed) -> (codes, codes_t or None, scales)
+PyObject* py_fp8_weight(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&] {
+    arguments(n, 2);
+    const at::Tensor& w = need(a[0], "w", at::kBFloat16);
+    if (w.dim() != 2 && w.dim() != 3) refuse("w must be [N, K] or [E, N, K], got " + shape_text(w.sizes()));
+    const bool transposed = truth(a[1], "transposed"), batch = w.dim() == 3;
+    const int64_t E = batch ? w.size(0) : 1, N = w.size(-2), K = w.size(-1), nb = (N + 127) / 128, kb = (K + 127) / 128;
+    On on(w);
+    at::Tensor codes = empty(w.sizes(), at::kByte, w), codes_t, sc;
+    if (batch) {
+      if (transposed) codes_t = empty({E, K, N}, at::kByte, w);
+      sc = empty({E, nb, kb}, at::kFloat, w);
+    } else {
+      if (transposed) codes_t = empty({K, N}, at::kByte, w);
+      sc = empty({nb, kb}, at::kFloat, w);
+    }
+    on.finish(mx_fp8_block_quantize_weight(ptr(w), E, N, K, ptr(codes), ptr(codes_t), (float*)ptr(sc), on.stream));
+    return tuple_of(codes, codes_t, sc);
+  });
+}
+
+// fp8_block_mm(mode, codes, scales, w_codes, w_scales, offs, err) -> c; w_codes: the transposed ones for the input gradient; offs
+// may be None: dense
+PyObject* py_fp8_mm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&] {
+    arguments(n, 7);
+    const int mode = small_integer(a[0], "mode");
+    const bool fwd = mode == MX_RAGGED_FWD;
+    const char* name = fwd ? "x" : "dout";
+    const at::Tensor& t = need(a[1], name, at::kByte);
+    if (t.dim() != 2) refuse(std::string(name) + " must hold a matrix, got " + shape_text(t.sizes()));
+    const int64_t M = t.size(0), C = t.size(1);
+    const at::Tensor& st = need(a[2], "the scales of the rows", at::kFloat, {(C + 127) / 128, M}, &t);
+    const at::Tensor& w = need(a[3], "w", at::kByte, &t);
+    const at::Tensor* offs = a[5] == Py_None ? nullptr : &need(a[5], "offs", at::kInt, &t);
+    const int64_t E = offs ? offs->numel() : 1;
+    if (E < 1 || E > 1024) refuse("E must be in [1, 1024], got " + std::to_string(E));
+    if ((w.dim() != 3 || w.size(0) != E) && (offs || w.dim() != 2))
+      refuse("w must hold " + std::string(offs ? "[" + std::to_string(E) + ", N, K]" : "[N, K] or [1, N, K]") + ", got codes " +
+             shape_text(w.sizes()));
+    const int64_t F = w.size(-2);
+    if (w.size(-1) != C) refuse(std::string(name) + " must have " + std::to_string(w.size(-1)) + " columns, got " + std::to_string(C));
+    const int64_t N = fwd ? F : C, K = fwd ? C : F, nb = (N + 127) / 128, kb = (K + 127) / 128;
+    const at::Tensor& sw = w.dim() == 3 ? need(a[4], "the scales of w", at::kFloat, {E, nb, kb}, &t)
+                                        : need(a[4], "the scales of w", at::kFloat, {nb, kb}, &t);
+    int32_t* err = error_word(a[6], t);
+    On on(t);
+    at::Tensor c = empty({M, F}, at::kBFloat16, t);
+    on.finish(mx_fp8_block_mm(mode, ptr(t), (const float*)ptr(st), ptr(w), (const float*)ptr(sw), M, N, K,
+                              offs ? (const int32_t*)ptr(*offs) : nullptr, (int32_t)E, ptr(c), err, on.stream));
+    return wrap(c);
+  });
+}
+
 // set_error(MxError)
 PyObject* py_set_error(PyObject*, PyObject* cls) {
   Py_XDECREF(g_error);
@@ -366,6 +585,14 @@ PyMethodDef g_methods[] = {{"set_error", py_set_error, METH_O, nullptr},
                            {"add_rmsnorm_fwd", MX_FAST(py_norm_fwd)},
                            {"add_rmsnorm_bwd", MX_FAST(py_norm_bwd)},
                            {"ragged", MX_FAST(py_ragged)},
+                           {"moe_route", MX_FAST(py_route)},
+                           {"moe_route_bwd", MX_FAST(py_route_bwd)},
+                           {"token_group", MX_FAST(py_token_group)},
+                           {"moe_combine", MX_FAST(py_combine)},
+                           {"moe_combine_bwd", MX_FAST(py_combine_bwd)},
+                           {"fp8_block_quantize", MX_FAST(py_fp8_rows)},
+                           {"fp8_block_quantize_weight", MX_FAST(py_fp8_weight)},
+                           {"fp8_block_mm", MX_FAST(py_fp8_mm)},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

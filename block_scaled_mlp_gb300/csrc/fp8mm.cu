@@ -1,0 +1,462 @@
+// fp8mm.cu - matrix products of E4M3 operands with one fp32 scale for 128 contraction elements of a token row and for
+// 128 x 128 of a weight, dense or grouped by expert.
+//
+//   FWD    out[t, n] = sum_b sx[b, t] sw[e, n / 128, b] sum_{k in block b} x[t, k] w[e, n, k]
+//   DGRAD  dx[t, k]  = sum_b sd[b, t] sw[e, b, k / 128] sum_{n in block b} dout[t, n] w[e, n, k]
+//
+// (DGRAD reads the transposed codes, so both are one kernel: features F, contraction C.)  The inner sums are tensor core
+// products (tcgen05, kind::f8f6f4) of 128 elements, each into an accumulator of its own in TMEM; the epilogue warps
+// bring it out, multiply it by its scales in fp32 and add it to sums in registers.  One rounding to bf16 at the end.
+//
+// Tokens are the N side of the MMA (any multiple of 32 at run time) and features the M side (256 per CTA pair), as in
+// ragged.cu: a group's last tile costs what its rows cost, and a CTA's 128 features are one block of the weight's
+// scales, so that a K block's scale of a token is one number for the CTA: a warp forms sx sw ahead of the epilogue.
+#include <atomic>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace mx {
+
+namespace {
+
+constexpr int FM_EPI = 8;                 // epilogue warps
+constexpr int FM_MAX_E = 1024;
+constexpr int FM_F = 256;                 // features per pair tile
+constexpr int FM_THREADS = 128 + FM_EPI * 32;
+constexpr int FM_REGS = 168;              // a thread at launch; 56 + 2 * 224 = 3 * 168 after the split
+
+// BT: columns of a token tile.
+template <int BT>
+struct FCfg {
+  static constexpr int A_BYTES = 128 * 128;              // 128 features x 128 contraction elements
+  static constexpr int B_BYTES = (BT / 2) * 128;         // this CTA's half of the tile
+  static constexpr int TX = A_BYTES + B_BYTES;
+  static constexpr int EPI_BYTES = FM_EPI * 2048;        // a warp's 32 x 32 bf16 block
+  static constexpr int TABLE = FM_MAX_E * 8;             // group ends and running unit numbers
+  static constexpr int SLOTS = 8;                        // K blocks whose scales are ready
+  static constexpr int SC_BYTES = SLOTS * BT * 4;
+  static constexpr int BUFS = BT == 256 ? 2 : 4;         // accumulators
+  static constexpr int TMEM = BUFS * BT;
+  static constexpr uint32_t IDESC = (1u << 4) | ((uint32_t)(FM_F >> 4) << 24);
+  static constexpr int STAGES = (226 * 1024 - EPI_BYTES - SC_BYTES - TABLE - 1536) / TX;
+  static constexpr size_t SMEM = (size_t)STAGES * TX + EPI_BYTES + SC_BYTES + TABLE + 512 /*barriers*/ + 1024 /*align*/;
+  static_assert(BT == 256 || BT == 128 || BT == 32, "tile widths");
+  static_assert((2 * STAGES + 2 * BUFS + 2 * SLOTS + 2) * 8 <= 512, "barriers");
+  static_assert(SMEM + 1024 /*static*/ <= 227 * 1024, "shared memory");
+};
+
+struct MmParams {
+  int64_t M;                // token rows
+  int32_t F, C;             // features, contraction length
+  int32_t E;
+  const int32_t* offs;      // NULL: one group of all rows
+  const float* st;          // [ceil(C / 128), M]
+  const float* sw;          // of expert e, feature block f, contraction block c: sw[e * sw_e + f * sw_f + c * sw_c]
+  int64_t sw_e, sw_f, sw_c;
+  uint8_t* out;             // [M, F] bf16
+  int32_t* err;
+};
+
+MX_DEVINL void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+template <int R>
+MX_DEVINL void regs_give() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R>
+MX_DEVINL void regs_take() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
+
+// tcgen05.wait::ld that the loaded registers pass through: no use of them moves ahead of it.
+MX_DEVINL void tmem_ld_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
+struct Unit {
+  int32_t e;
+  int32_t f0;       // first feature
+  int64_t t0;       // first token row
+  int32_t tn;       // live rows of the tile
+  int32_t n_eff;    // tn rounded up to the MMA's multiple of 32
+};
+
+template <int BT>
+MX_DEVINL Unit unit_of(const MmParams& p, const int32_t* ends, const int32_t* unit_end, int32_t u) {
+  Unit r;
+  const int32_t f_tiles = (p.F + FM_F - 1) / FM_F;
+  int lo = 0, hi = p.E - 1;  // first group whose unit_end is > u
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (unit_end[mid] > u) hi = mid; else lo = mid + 1;
+  }
+  r.e = lo;
+  const int32_t v = u - (lo ? unit_end[lo - 1] : 0);
+  const int32_t start = lo ? ends[lo - 1] : 0, rows = ends[lo] - start;
+  const int32_t t_tiles = (rows + BT - 1) / BT;
+  int32_t t, f;
+  if (rows <= p.F) {  // the rows are the smaller operand: re-read them, stream the weights once
+    f = v / t_tiles;
+    t = v - f * t_tiles;
+  } else {
+    t = v / f_tiles;
+    f = v - t * f_tiles;
+  }
+  // the group's rows shared out evenly over its tiles, in multiples of 32
+  const int32_t share = ((rows + t_tiles - 1) / t_tiles + 31) & ~31;
+  r.f0 = f * FM_F;
+  r.t0 = (int64_t)start + (int64_t)t * share;
+  r.tn = min(share, rows - t * share);
+  r.n_eff = (r.tn + 31) & ~31;
+  return r;
+}
+
+template <int BT>
+__global__ void __launch_bounds__(FM_THREADS, 1)
+    fp8_block_mm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, MmParams p) {
+  using C = FCfg<BT>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = sA + C::STAGES * C::A_BYTES;
+  uint8_t* sEpi = sB + C::STAGES * C::B_BYTES;
+  float* sScale = reinterpret_cast<float*>(sEpi + C::EPI_BYTES);
+  int32_t* ends = reinterpret_cast<int32_t*>(sEpi + C::EPI_BYTES + C::SC_BYTES);
+  int32_t* unit_end = ends + FM_MAX_E;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sEpi + C::EPI_BYTES + C::SC_BYTES + C::TABLE);
+  uint64_t* empty = full + C::STAGES;
+  uint64_t* acc_full = empty + C::STAGES;
+  uint64_t* acc_empty = acc_full + C::BUFS;
+  uint64_t* sc_full = acc_empty + C::BUFS;
+  uint64_t* sc_empty = sc_full + C::SLOTS;
+  uint64_t* done_bar = sc_empty + C::SLOTS;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done_bar + 1);
+  __shared__ int s_ok, s_units;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_ctarank();
+  const int32_t unit0 = blockIdx.x / 2, ustep = gridDim.x / 2;
+  const int32_t f_tiles = (p.F + FM_F - 1) / FM_F;
+  const int32_t num_kb = (p.C + 127) / 128;
+
+  if (threadIdx.x == 0) {
+    // the even CTA's full and acc_empty barriers serve the pair
+    for (int s = 0; s < C::STAGES; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+    for (int a = 0; a < C::BUFS; ++a) { mbar_init(&acc_full[a], 1); mbar_init(&acc_empty[a], 2 * FM_EPI); }
+    for (int s = 0; s < C::SLOTS; ++s) { mbar_init(&sc_full[s], 32); mbar_init(&sc_empty[s], FM_EPI); }
+    mbar_init(done_bar, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) { tmem_alloc_pair(tmem_holder, C::TMEM); tmem_relinquish_pair(); }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  cluster_sync();  // the peer's barriers exist before any remote arrive or pair copy
+  const uint32_t tmem = *tmem_holder;
+  pdl_begin();     // all of the above overlaps the kernel before
+  if (warp == 2) {
+    // group ends, checked, and the running number of work units
+    int32_t prev = 0, units = 0;
+    bool ok = true;
+    for (int base = 0; base < p.E; base += 32) {
+      const int e = base + lane;
+      const int32_t v = e >= p.E ? 0x7FFFFFFF : p.offs ? p.offs[e] : (int32_t)p.M;
+      int32_t before = __shfl_up_sync(0xFFFFFFFFu, v, 1);
+      if (lane == 0) before = prev;
+      const bool in = e < p.E;
+      if (in && (v < before || v < 0 || (int64_t)v > p.M)) ok = false;
+      int32_t n = in && ok ? (v - before + BT - 1) / BT * f_tiles : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int32_t m = __shfl_up_sync(0xFFFFFFFFu, n, o);
+        if (lane >= o) n += m;
+      }
+      if (in) {
+        ends[e] = v;
+        unit_end[e] = units + n;
+      }
+      units += __shfl_sync(0xFFFFFFFFu, n, 31);
+      prev = __shfl_sync(0xFFFFFFFFu, v, min(31, p.E - 1 - base));
+    }
+    ok = __all_sync(0xFFFFFFFFu, ok);
+    if (lane == 0) {
+      s_ok = ok;
+      s_units = ok ? units : 0;
+      if (!ok && blockIdx.x == 0) record_error(p.err, MX_ERR_BAD_OFFSETS);
+    }
+  }
+  __syncthreads();
+  const int32_t n_units = s_units;
+
+  if (warp < 4) {
+  regs_give<56>();
+  if (warp == 0) {
+    // ------------------------------------------------------------ loads
+    const bool leader = elect_one();
+    if (leader) {
+      prefetch_tmap(&tmA);
+      prefetch_tmap(&tmB);
+    }
+    int stage = 0; uint32_t phase = 0;
+    bool ok = true;
+    for (int32_t u = unit0; u < n_units && ok; u += ustep) {
+      const Unit t = unit_of<BT>(p, ends, unit_end, u);
+      const int32_t f = t.f0 + rank * 128;
+      const int32_t b0 = (int32_t)(t.t0 + rank * (t.n_eff / 2));
+      for (int kb = 0; kb < num_kb; ++kb) {
+        if (!warp_wait(&empty[stage], phase ^ 1, p.err)) { ok = false; break; }
+        if (leader) {
+          const uint32_t bar = cluster_map(smem_u32(&full[stage]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * C::TX);
+          tma_load_3d_pair(sA + stage * C::A_BYTES, &tmA, kb * 128, f, t.e, bar);
+          tma_load_2d_pair(sB + stage * C::B_BYTES, &tmB, kb * 128, b0, bar);
+        }
+        __syncwarp();
+        if (++stage == C::STAGES) { stage = 0; phase ^= 1; }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMAs
+    if (rank == 0) {
+      const bool leader = elect_one();
+      // K-major: 8-row atoms 1024 bytes apart, 32 elements = 32 bytes along the row
+      const uint64_t a0 = smem_desc(smem_u32(sA), 16, 1024, 2);
+      const uint64_t b0 = smem_desc(smem_u32(sB), 16, 1024, 2);
+      int stage = 0; uint32_t phase = 0;
+      int buf = 0; uint32_t buf_phase = 0;
+      bool ok = true;
+      for (int32_t u = unit0; u < n_units && ok; u += ustep) {
+        const Unit t = unit_of<BT>(p, ends, unit_end, u);
+        const uint32_t idesc = C::IDESC | ((uint32_t)(t.n_eff >> 3) << 17);
+        for (int kb = 0; kb < num_kb; ++kb) {
+          if (!warp_wait(&acc_empty[buf], buf_phase ^ 1, p.err)) { ok = false; break; }
+          if (!warp_wait(&full[stage], phase, p.err)) { ok = false; break; }
+          tc_fence_after();
+          if (leader) {
+            const uint32_t d = tmem + (uint32_t)(buf * BT);
+            const uint64_t ad = a0 + (uint64_t)((stage * C::A_BYTES) >> 4);
+            const uint64_t bd = b0 + (uint64_t)((stage * C::B_BYTES) >> 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma_f8_pair(d, ad + k * 2, bd + k * 2, idesc, k > 0);
+            tc_commit_pair_mc(&empty[stage], 0x3);
+            tc_commit_pair_mc(&acc_full[buf], 0x3);
+          }
+          __syncwarp();
+          if (++stage == C::STAGES) { stage = 0; phase ^= 1; }
+          if (++buf == C::BUFS) { buf = 0; buf_phase ^= 1; }
+        }
+      }
+      if (leader) tc_commit_pair_mc(done_bar, 0x1);
+      __syncwarp();
+      mbar_wait(done_bar, 0, p.err);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ scales
+    // every other K block of a warp's: those of the tile's tokens times the one of the CTA's features
+    constexpr int PER = BT / 32;
+    int slot = warp - 2; uint32_t phase = 0;
+    bool ok = true;
+    int32_t kb0 = warp - 2;  // K blocks are numbered through all units
+    for (int32_t u = unit0; u < n_units && ok; u += ustep) {
+      const Unit t = unit_of<BT>(p, ends, unit_end, u);
+      const int32_t f = t.f0 + rank * 128;
+      const float* w = p.sw + t.e * p.sw_e + (f >> 7) * p.sw_f;
+      int kb = kb0;
+      for (; kb < num_kb; kb += 2) {
+        const float sw = f < p.F ? w[kb * p.sw_c] : 0.0f;
+        float s[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const int64_t at = t.t0 + lane + 32 * i;
+          s[i] = lane + 32 * i < t.tn && at < p.M ? p.st[kb * p.M + at] * sw : 0.0f;
+        }
+        if (!warp_wait(&sc_empty[slot], phase ^ 1, p.err)) { ok = false; break; }
+        float* dst = sScale + slot * BT;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) dst[lane + 32 * i] = s[i];
+        mbar_arrive(&sc_full[slot]);
+        slot += 2;
+        if (slot >= C::SLOTS) { slot -= C::SLOTS; phase ^= 1; }
+      }
+      kb0 = kb - num_kb;
+    }
+    __syncwarp();
+  }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    regs_take<224>();
+    const int ew = warp - 4, q = warp & 3, half = ew >> 2;
+    uint8_t* stg = sEpi + ew * 2048;
+    constexpr int NC = BT <= 64 ? 1 : BT / 64;   // blocks of 32 columns a warp
+    auto col_of = [half](int j) { return (2 * j + half) * 32; };
+    const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16);
+    const int qr = lane >> 2, qc = (lane & 3) * 8;
+    int buf = 0; uint32_t buf_phase = 0;
+    int slot = 0; uint32_t sc_phase = 0;
+    bool ok = true;
+    for (int32_t u = unit0; u < n_units && ok; u += ustep) {
+      const Unit t = unit_of<BT>(p, ends, unit_end, u);
+      const int32_t f = t.f0 + rank * 128 + q * 32;   // this warp's features
+      f2 acc[NC][16];
+#pragma unroll
+      for (int j = 0; j < NC; ++j)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[j][i] = f2_splat(0.0f);
+      for (int kb = 0; kb < num_kb; ++kb) {
+        if (!warp_wait(&sc_full[slot], sc_phase, p.err) || !warp_wait(&acc_full[buf], buf_phase, p.err)) { ok = false; break; }
+        tc_fence_after();
+        const float* sc = sScale + slot * BT;
+        const uint32_t at = tb + (uint32_t)(buf * BT);
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+          const int c = col_of(j);
+          if (c < t.tn) {
+            uint32_t r[32];
+            tmem_ld_32cols(at + c, r);
+            tmem_ld_wait(r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 s = *reinterpret_cast<const float4*>(sc + c + 4 * i);
+              acc[j][2 * i] = f2_fma(f2_pack(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1])), f2_pack(s.x, s.y), acc[j][2 * i]);
+              acc[j][2 * i + 1] = f2_fma(f2_pack(__uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3])), f2_pack(s.z, s.w), acc[j][2 * i + 1]);
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sc_empty[slot]);
+          if (rank != 0) mbar_arrive_cluster_relaxed(cluster_map(smem_u32(&acc_empty[buf]), 0));
+          else mbar_arrive(&acc_empty[buf]);
+        }
+        if (++buf == C::BUFS) { buf = 0; buf_phase ^= 1; }
+        if (++slot == C::SLOTS) { slot = 0; sc_phase ^= 1; }
+      }
+      if (!ok || f >= p.F) continue;
+      // a block of 32 tokens; a lane has one feature of all of them: turned through shared memory
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+        const int c = col_of(j);
+        if (c < t.tn) {
+          uint8_t* dst = p.out + ((t.t0 + c + qr) * p.F + f + qc) * 2;
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const uint32_t v = f2_to_bf16x2(acc[j][i]);
+            *reinterpret_cast<uint16_t*>(stg + (2 * i) * 64 + lane * 2) = (uint16_t)v;
+            *reinterpret_cast<uint16_t*>(stg + (2 * i + 1) * 64 + lane * 2) = (uint16_t)(v >> 16);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (c + i * 8 + qr < t.tn && f + qc < p.F)
+              *reinterpret_cast<uint4*>(dst + (int64_t)(i * 8) * p.F * 2) =
+                  *reinterpret_cast<const uint4*>(stg + (i * 8 + qr) * 64 + (lane & 3) * 16);
+        }
+      }
+    }
+    // rows past the last group (all rows, if the ends were refused) are zeros
+    const int64_t first = s_ok ? ends[p.E - 1] : 0;
+    uint4* dst = reinterpret_cast<uint4*>(p.out + first * p.F * 2);
+    const int64_t n = (p.M - first) * p.F / 8;
+    for (int64_t i = (int64_t)blockIdx.x * (FM_EPI * 32) + ew * 32 + lane; i < n; i += (int64_t)gridDim.x * (FM_EPI * 32))
+      dst[i] = make_uint4(0, 0, 0, 0);
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // no pair MMA, copy or remote arrive targets an exited CTA
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, C::TMEM);
+}
+
+// Pairs that can be resident at once, by device; the kernel's register split needs the registers it was written for.
+template <int BT>
+int resident_pairs(int* n) {
+  using C = FCfg<BT>;
+  static std::atomic<int> resident[64];  // the number + 1, once known; any thread may be the one that asks
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_status(e, "cudaGetDevice");
+  int r = resident[dev & 63].load(std::memory_order_relaxed);
+  if (r == 0) {
+    auto k = fp8_block_mm_kernel<BT>;
+    cudaFuncAttributes a{};
+    if ((e = cudaFuncGetAttributes(&a, k)) != cudaSuccess) return cuda_status(e, "cudaFuncGetAttributes");
+    if (a.numRegs != FM_REGS)
+      return fail(MX_ERR_UNSUPPORTED, "fp8_block_mm_kernel was built with %d registers a thread, not %d", a.numRegs, FM_REGS);
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+    if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute");
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (num_sms() / 2));
+    cfg.blockDim = dim3(FM_THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int m = 0;
+    if ((e = cudaOccupancyMaxActiveClusters(&m, k, &cfg)) != cudaSuccess) return cuda_status(e, "cudaOccupancyMaxActiveClusters");
+    r = m + 1;
+    resident[dev & 63].store(r, std::memory_order_relaxed);
+  }
+  *n = r - 1;
+  return *n > 0 ? MX_OK : cuda_status(cudaErrorInvalidConfiguration, "cudaOccupancyMaxActiveClusters");
+}
+
+// Tiles of bt token rows, at most: any group that has rows may end in a part of one.
+int64_t tile_bound(const MmParams& p, int bt) {
+  const int64_t groups = std::min<int64_t>(p.E, p.M);
+  return (p.M + groups * (bt - 1)) / bt * ((p.F + FM_F - 1) / FM_F);
+}
+
+template <int BT>
+int launch_cfg(const CUtensorMap& tA, const CUtensorMap& tB, const MmParams& p, cudaStream_t stream) {
+  using C = FCfg<BT>;
+  const int64_t units = tile_bound(p, BT);
+  if (units > INT32_MAX - 1024) return fail(MX_ERR_UNSUPPORTED, "FP8 product: too many tiles");
+  int nres = 0;
+  if (int rc = resident_pairs<BT>(&nres)) return rc;
+  auto k = fp8_block_mm_kernel<BT>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+  if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute");
+  const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(units, nres));
+  count_launch(MX_KERNEL_FP8_BLOCK);
+  return cuda_status(launch_overlapped(k, (unsigned)(2 * pairs), FM_THREADS, C::SMEM, stream, 2, tA, tB, p),
+                     "fp8_block_mm_kernel launch");
+}
+
+}  // namespace
+
+int launch_fp8_block_mm(const Fp8MmLaunch& g, cudaStream_t stream) {
+  const bool fwd = g.mode == MX_RAGGED_FWD;
+  MmParams p{};
+  p.M = g.M; p.E = g.offs ? g.E : 1; p.offs = g.offs; p.out = (uint8_t*)g.c; p.err = g.err;
+  p.F = (int32_t)(fwd ? g.N : g.K);
+  p.C = (int32_t)(fwd ? g.K : g.N);
+  const int64_t nb = (g.N + 127) / 128, kb = (g.K + 127) / 128;
+  p.st = g.sa; p.sw = g.sw; p.sw_e = nb * kb; p.sw_f = fwd ? kb : 1; p.sw_c = fwd ? 1 : kb;
+  const int bt = p.M <= 16 * (int64_t)p.E ? 32 : p.M <= 64 * (int64_t)p.E ? 128 : 256;
+  CUtensorMap tA, tB;
+  uint64_t da[3] = {(uint64_t)p.C, (uint64_t)p.F, (uint64_t)p.E}, sa[2] = {(uint64_t)p.C, (uint64_t)p.C * p.F};
+  uint32_t ba[3] = {128, 128, 1};
+  uint64_t db[2] = {(uint64_t)p.C, (uint64_t)p.M}, sb[1] = {(uint64_t)p.C};
+  uint32_t bb[2] = {128, (uint32_t)bt / 2};
+  int rc = make_tmap(&tA, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(g.w), da, sa, ba, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (!rc) rc = make_tmap(&tB, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(g.a), db, sb, bb, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (rc) return rc;
+  return bt == 32 ? launch_cfg<32>(tA, tB, p, stream) : bt == 128 ? launch_cfg<128>(tA, tB, p, stream) : launch_cfg<256>(tA, tB, p, stream);
+}
+
+}  // namespace mx

@@ -201,4 +201,72 @@ struct RaggedLaunch {
 };
 int launch_ragged(const RaggedLaunch& g, cudaStream_t stream);
 
+// ---------------------------------------------------------------- routing (route.cu)
+struct RouteLaunch {
+  const void* logits;     // [T, E] bf16, or fp32 (wide)
+  int wide;
+  const float* bias;      // [E] or NULL
+  int64_t T;
+  int32_t E, k, groups, top_groups;
+  int score, renorm;
+  float scale;
+  int32_t* ids;           // [T, k]
+  float* weights;         // [T, k]
+};
+int launch_moe_route(const RouteLaunch& a, cudaStream_t stream);
+struct RouteBwdLaunch {
+  const float* dweights;  // [T, k]
+  const void* logits;
+  int wide;
+  const int32_t* ids;
+  int64_t T;
+  int32_t E, k;
+  int score, renorm;
+  float scale;
+  void* dlogits;          // [T, E], as logits
+  int32_t* err;
+};
+int launch_moe_route_bwd(const RouteBwdLaunch& a, cudaStream_t stream);
+size_t token_group_workspace(int64_t R, int32_t E);
+int launch_token_group(const int32_t* expert_of, int64_t R, int32_t E, int32_t* offs, int32_t* row_dst, int32_t* row_src,
+                       void* workspace, int32_t* err, cudaStream_t stream);
+
+// ---------------------------------------------------------------- rows back to tokens (combine.cu)
+struct CombineLaunch {
+  const void* rows;       // [n_rows, d] bf16
+  int64_t n_rows, d;
+  const int32_t* row_dst; // [T k]
+  const int32_t* row_src; // [n_rows] (backward)
+  int64_t T;
+  int32_t k;
+  const float* weights;   // [T, k]; forward: or NULL
+  const void* add;        // [T, d] or NULL (forward)
+  void* out;              // [T, d] (forward)
+  const void* dout;       // [T, d] (backward)
+  void* drows;            // [n_rows, d] (backward)
+  float* dweights;        // [T, k] (backward)
+  int32_t* err;
+};
+int launch_moe_combine(const CombineLaunch& a, cudaStream_t stream);
+int launch_moe_combine_bwd(const CombineLaunch& a, cudaStream_t stream);
+
+// ---------------------------------------------------------------- FP8 with 128-blocks (fp8block.cu, fp8mm.cu)
+int launch_fp8_block_rows(const void* x, int64_t rows_in, int64_t cols, const int32_t* src, int64_t rows, int32_t div, void* codes,
+                          float* scales, int32_t* err, cudaStream_t stream);
+int launch_fp8_block_weight(const void* w, int64_t E, int64_t N, int64_t K, void* codes, void* codes_t, float* scales,
+                            cudaStream_t stream);
+struct Fp8MmLaunch {
+  int mode;               // MX_RAGGED_FWD or MX_RAGGED_DGRAD
+  const void* a;          // token codes: [M, K] (FWD) or [M, N]
+  const float* sa;        // their scales [ceil(K or N / 128), M]
+  const void* w;          // weight codes [E, N, K] (FWD) or [E, K, N]
+  const float* sw;        // [E, ceil(N / 128), ceil(K / 128)]
+  int64_t M, N, K;
+  const int32_t* offs;    // [E] group ends, or NULL: dense
+  int32_t E;
+  void* c;                // [M, N] or [M, K] bf16
+  int32_t* err;
+};
+int launch_fp8_block_mm(const Fp8MmLaunch& g, cudaStream_t stream);
+
 }  // namespace mx

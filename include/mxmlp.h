@@ -542,6 +542,134 @@ MX_API int mx_ragged_mm(int mode, const void* a, const void* b, int64_t M_total,
                         const int32_t* offs, int32_t E, void* c, int32_t* err_word, void* stream);
 
 /*
+ * ---- The layer around the experts' products (no counterpart on the pages):
+ * a router, the routed rows grouped without padding, and the experts' rows
+ * back to tokens.
+ *
+ * mx_moe_route - a router's logits to expert numbers and weights.
+ *
+ *   s = softmax of a token's E logits, or 1 / (1 + e^-logit) of each (score);
+ *       a logit of -inf: s = 0
+ *   c = s + bias, in double precision; a logit of -inf: c = -inf
+ *   A group of E / groups neighbouring experts is worth its two largest c
+ *   added (its one, if it has one); the top_groups most valuable are taken,
+ *   equal ones by number.  ids = the k largest c of the groups taken, larger
+ *   ones first, equal ones by number (without a bias: the k largest logits).
+ *   weights = scale * s, or with renorm scale * s / (sum of the k s + 1e-20);
+ *   fp32, within 2^-18.
+ *   logits    [T, E], bf16 (MX_BF16) or fp32 (MX_FP32).
+ *   bias      [E] fp32, or NULL.  It decides ids and does not enter weights.
+ *   ids, weights  [T, k] int32 and fp32 out.
+ * A token with a NaN among its logits or c, or under softmax with an infinite
+ * logit, has ids 0 to k - 1 and NaN weights.
+ * Requirements: 1 <= E <= 1024, 1 <= groups <= 32, E % groups == 0,
+ * 1 <= top_groups <= groups, 1 <= k <= 32, k <= top_groups * E / groups, scale finite.
+ */
+typedef enum { MX_SCORE_SOFTMAX = 0, MX_SCORE_SIGMOID = 1 } mx_score;
+typedef enum { MX_BF16 = 0, MX_FP32 = 1 } mx_float_type;
+MX_API int mx_moe_route(const void* logits, int logits_type, int64_t T, int32_t E, int32_t k, int score, const float* bias,
+                        int32_t groups, int32_t top_groups, int renorm, float scale, int32_t* ids, float* weights,
+                        void* stream);
+
+/*
+ * mx_moe_route_bwd - gradient of the logits from that of the weights
+ * (dweights [T, k] fp32), with the ids as they are: the scores are computed
+ * again from the logits.  dlogits [T, E] out, the logits' type, fp32
+ * arithmetic and one rounding.  With an id named twice both gradients count.
+ * err_word (may be NULL) receives MX_ERR_BAD_OFFSETS for an id outside
+ * [0, E); that id adds nothing.
+ */
+MX_API int mx_moe_route_bwd(const float* dweights, const void* logits, int logits_type, const int32_t* ids, int64_t T,
+                            int32_t E, int32_t k, int score, int renorm, float scale, void* dlogits, int32_t* err_word,
+                            void* stream);
+
+/*
+ * mx_token_group - routed rows grouped by expert without padding, the layout
+ * that mx_ragged_mm takes (mx_token_group_pad is the padded one).
+ *   expert_of [R] int32 device array: expert of each routed row.
+ *   offs      [E] int32 out: cumulative ends of the groups.
+ *   row_dst   [R] int32 out: row of routed row r; a group's rows keep their order.
+ *   row_src   [R] int32 out: routed row that row i holds.
+ *   workspace mx_token_group_workspace(R, E) bytes.
+ * An expert number outside [0, E) is reported in err_word (may be NULL,
+ * MX_ERR_BAD_OFFSETS): that row is not placed, row_dst -1, and as many rows
+ * behind the last group have row_src -1.
+ * Requirements: 1 <= E <= 1024, R < 2^31.
+ */
+MX_API size_t mx_token_group_workspace(int64_t R, int32_t E);
+MX_API int mx_token_group(const int32_t* expert_of, int64_t R, int32_t E, int32_t* offs, int32_t* row_dst, int32_t* row_src,
+                          void* workspace, int32_t* err_word, void* stream);
+
+/*
+ * mx_moe_combine - the rows of a token's k experts weighted and summed:
+ *   out[t] = add[t] + sum_j weights[t, j] rows[row_dst[t k + j]]
+ * in fp32 (add first, then j in order), one rounding to bf16.
+ *   rows    [n_rows, d] bf16.   row_dst [T k] int32 (of either layout).
+ *   weights [T, k] fp32, or NULL: ones (the gradient of mx_gather_rows).
+ *   add     [T, d] bf16 (a shared expert's output), or NULL.   out [T, d] bf16.
+ * A negative row_dst adds nothing; one past n_rows adds nothing either and
+ * sets MX_ERR_BAD_OFFSETS in err_word (may be NULL).
+ *
+ * mx_moe_combine_bwd - its gradients from dout [T, d] bf16:
+ *   drows[row_dst[t k + j]] = weights[t, j] dout[t]   [n_rows, d] bf16 out
+ *   dweights[t, j] = dout[t] . rows[row_dst[t k + j]] [T, k] fp32 out
+ *   row_src [n_rows] int32 of the same layout: rows with a negative one hold
+ *   no routed row and get zeros.  (The gradient of add is dout.)
+ * Requirements: d % 8 == 0, 1 <= k <= 32, 16-byte aligned rows, add, out,
+ * dout and drows; no two entries of row_dst alike (drows).
+ */
+MX_API int mx_moe_combine(const void* rows, int64_t n_rows, int64_t d, const int32_t* row_dst, int64_t T, int32_t k,
+                          const float* weights, const void* add, void* out, int32_t* err_word, void* stream);
+MX_API int mx_moe_combine_bwd(const void* dout, const void* rows, int64_t n_rows, int64_t d, const int32_t* row_dst,
+                              const int32_t* row_src, int64_t T, int32_t k, const float* weights, void* drows,
+                              float* dweights, int32_t* err_word, void* stream);
+
+/*
+ * ---- FP8 with a scale for 128 elements (no counterpart on the pages):
+ * E4M3 codes, one fp32 scale for 128 neighbours of a token row and for each
+ * 128 x 128 block of a weight (the last ones may be smaller).
+ *   m = max |x| of the block, 2^-100 at least; scale = RN(m / 448);
+ *   code = RN_e4m3(448 x / m), rounded once; value = code * scale.
+ * A block that holds a NaN or an infinity has a NaN scale and codes 0x7F.
+ *
+ * mx_fp8_block_quantize - codes of token rows, gathered on the way or not:
+ *   x [rows_in, cols] bf16.  src NULL: row i from x[i] (rows == rows_in); else
+ *   src [rows] int32, row i from x[src[i] / div], zeros for a negative src and
+ *   for one past rows_in (which err_word, may be NULL, receives as
+ *   MX_ERR_BAD_OFFSETS), as mx_gather_rows has it.
+ *   codes [rows, cols]; scales [ceil(cols / 128), rows] fp32: a block's scales
+ *   of neighbouring rows lie side by side.
+ * mx_fp8_block_quantize_weight - codes of w [E, N, K] bf16 as it lies and,
+ *   with codes_t, transposed for the input gradient (the scales are the same):
+ *   codes [E, N, K], codes_t [E, K, N] or NULL,
+ *   scales [E, ceil(N / 128), ceil(K / 128)] fp32.
+ * Requirements: cols, N and K multiples of 16, 16-byte aligned pointers.
+ */
+MX_API int mx_fp8_block_quantize(const void* x, int64_t rows_in, int64_t cols, const int32_t* src, int64_t rows,
+                                 int32_t div, void* codes, float* scales, int32_t* err_word, void* stream);
+MX_API int mx_fp8_block_quantize_weight(const void* w, int64_t E, int64_t N, int64_t K, void* codes, void* codes_t,
+                                        float* scales, void* stream);
+
+/*
+ * mx_fp8_block_mm - products of such operands, dense or grouped by expert:
+ * exact products and tensor core sums over a block of 128, times both scales in
+ * fp32, sums over the blocks in fp32, one rounding to bf16.
+ *   MX_RAGGED_FWD    a [M_total, K], sa [ceil(K / 128), M_total], w = codes [E, N, K]
+ *                    -> c = out [M_total, N] = x . w[e]^T
+ *   MX_RAGGED_DGRAD  a [M_total, N], sa [ceil(N / 128), M_total], w = codes_t [E, K, N]
+ *                    -> c = dx [M_total, K] = dout . w[e]
+ *   sw   [E, ceil(N / 128), ceil(K / 128)] either way.
+ *   offs [E] group ends as in mx_ragged_mm (any sizes, rows past the last group
+ *        are zeros); NULL: dense, E = 1.
+ * A product of two scales has to be in fp32's range (2^-126 to 2^128).
+ * Weight gradients contract over tokens and stay in bf16 (mx_ragged_mm).
+ * Requirements: N, K multiples of 16; 1 <= E <= 1024; 16-byte aligned a, w
+ * and c; M_total may be 0.  err_word as in mx_ragged_mm.
+ */
+MX_API int mx_fp8_block_mm(int mode, const void* a, const float* sa, const void* w, const float* sw, int64_t M_total,
+                           int64_t N, int64_t K, const int32_t* offs, int32_t E, void* c, int32_t* err_word, void* stream);
+
+/*
  * Kernel launch counters (observability; no counterpart on the pages).
  * The torchtitan page's GPU suite holds the fused MLP to an op-count
  * contract ("Add MXFP8 fused-MLP overrides in torchtitan", Numerics and
@@ -555,12 +683,14 @@ enum mx_kernel_family {
   MX_KERNEL_SWIGLU_BWD = 2,   /* swiglu_bwd_kernel: SwiGLU backward + MX quantization of dh13 */
   MX_KERNEL_GEMM = 3,         /* gemm_kernel: MXFP8 or bf16 GEMM (dense, M- or K-grouped) */
   MX_KERNEL_GEMM_SWIGLU = 4,  /* gemm_kernel with the fused SwiGLU epilogue (w13 GEMM + y quantization) */
-  MX_KERNEL_DISPATCH = 5,     /* token-group padding and row gathers */
+  MX_KERNEL_DISPATCH = 5,     /* token grouping and padding, row gathers, rows back to tokens */
   MX_KERNEL_MEMSET = 6,       /* cudaMemsetAsync of scale padding or dispatch maps */
   MX_KERNEL_NORM = 7,         /* residual + RMS norm kernels, forward and backward */
   MX_KERNEL_CKPT8 = 8,        /* 8-bit checkpoint kernels, SwiGLU with one among them */
   MX_KERNEL_RAGGED = 9,       /* ragged expert products */
-  MX_KERNEL_FAMILIES = 10
+  MX_KERNEL_ROUTE = 10,       /* routers, forward and backward */
+  MX_KERNEL_FP8_BLOCK = 11,   /* FP8 with 128-blocks: casts and products */
+  MX_KERNEL_FAMILIES = 12
 };
 
 /*
