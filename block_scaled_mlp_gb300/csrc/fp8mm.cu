@@ -36,12 +36,12 @@ struct FCfg {
   static constexpr int TABLE = FM_MAX_E * 8;             // group ends and running unit numbers
   static constexpr int SLOTS = 8;                        // K blocks whose scales are ready
   static constexpr int SC_BYTES = SLOTS * BT * 4;
-  static constexpr int BUFS = BT == 256 ? 2 : 4;         // accumulators
+  static constexpr int BUFS = 4;                         // accumulators
   static constexpr int TMEM = BUFS * BT;
   static constexpr uint32_t IDESC = (1u << 4) | ((uint32_t)(FM_F >> 4) << 24);
   static constexpr int STAGES = (226 * 1024 - EPI_BYTES - SC_BYTES - TABLE - 1536) / TX;
   static constexpr size_t SMEM = (size_t)STAGES * TX + EPI_BYTES + SC_BYTES + TABLE + 512 /*barriers*/ + 1024 /*align*/;
-  static_assert(BT == 256 || BT == 128 || BT == 32, "tile widths");
+  static_assert(BT == 128 || BT == 32, "tile widths");
   static_assert((2 * STAGES + 2 * BUFS + 2 * SLOTS + 2) * 8 <= 512, "barriers");
   static_assert(SMEM + 1024 /*static*/ <= 227 * 1024, "shared memory");
 };
@@ -107,8 +107,8 @@ MX_DEVINL Unit unit_of(const MmParams& p, const int32_t* ends, const int32_t* un
     t = v / f_tiles;
     f = v - t * f_tiles;
   }
-  // the group's rows shared out evenly over its tiles, in multiples of 32
-  const int32_t share = ((rows + t_tiles - 1) / t_tiles + 31) & ~31;
+  // narrow tiles: the group's rows shared out evenly, in multiples of 32
+  const int32_t share = BT == 256 ? BT : ((rows + t_tiles - 1) / t_tiles + 31) & ~31;
   r.f0 = f * FM_F;
   r.t0 = (int64_t)start + (int64_t)t * share;
   r.tn = min(share, rows - t * share);
@@ -116,9 +116,69 @@ MX_DEVINL Unit unit_of(const MmParams& p, const int32_t* ends, const int32_t* un
   return r;
 }
 
+// By one warp: group ends, checked, and the running number of work units.
+template <int BT>
+MX_DEVINL void read_ends(const MmParams& p, int32_t* ends, int32_t* unit_end, int* s_ok, int* s_units) {
+  const int lane = threadIdx.x & 31;
+  const int32_t f_tiles = (p.F + FM_F - 1) / FM_F;
+  int32_t prev = 0, units = 0;
+  bool ok = true;
+  for (int base = 0; base < p.E; base += 32) {
+    const int e = base + lane;
+    const int32_t v = e >= p.E ? 0x7FFFFFFF : p.offs ? p.offs[e] : (int32_t)p.M;
+    int32_t before = __shfl_up_sync(0xFFFFFFFFu, v, 1);
+    if (lane == 0) before = prev;
+    const bool in = e < p.E;
+    if (in && (v < before || v < 0 || (int64_t)v > p.M)) ok = false;
+    int32_t n = in && ok ? (v - before + BT - 1) / BT * f_tiles : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t m = __shfl_up_sync(0xFFFFFFFFu, n, o);
+      if (lane >= o) n += m;
+    }
+    if (in) {
+      ends[e] = v;
+      unit_end[e] = units + n;
+    }
+    units += __shfl_sync(0xFFFFFFFFu, n, 31);
+    prev = __shfl_sync(0xFFFFFFFFu, v, min(31, p.E - 1 - base));
+  }
+  ok = __all_sync(0xFFFFFFFFu, ok);
+  if (lane == 0) {
+    *s_ok = ok;
+    *s_units = ok ? units : 0;
+    if (!ok && blockIdx.x == 0) record_error(p.err, MX_ERR_BAD_OFFSETS);
+  }
+}
+
+// By the epilogue's threads: rows past the last group (all rows, if the ends were refused) are zeros.
+MX_DEVINL void zero_spare_rows(const MmParams& p, int64_t first, int thread) {
+  uint4* dst = reinterpret_cast<uint4*>(p.out + first * p.F * 2);
+  const int64_t n = (p.M - first) * p.F / 8;
+  for (int64_t i = (int64_t)blockIdx.x * (FM_EPI * 32) + thread; i < n; i += (int64_t)gridDim.x * (FM_EPI * 32))
+    dst[i] = make_uint4(0, 0, 0, 0);
+}
+
+// 16 values in bf16 with one 32-byte store, or two of 16 bytes where the output is not on 32 bytes.
+MX_DEVINL void store_32b(uint8_t* dst, const f2* v) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = f2_to_bf16x2(v[i]);
+  if ((reinterpret_cast<uintptr_t>(dst) & 31) == 0) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+// ---------------------------------------------------------------- tokens on the N side
+
 template <int BT>
 __global__ void __launch_bounds__(FM_THREADS, 1)
-    fp8_block_mm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, MmParams p) {
+    fp8_mm_narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, MmParams p) {
   using C = FCfg<BT>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -141,7 +201,6 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_ctarank();
   const int32_t unit0 = blockIdx.x / 2, ustep = gridDim.x / 2;
-  const int32_t f_tiles = (p.F + FM_F - 1) / FM_F;
   const int32_t num_kb = (p.C + 127) / 128;
 
   if (threadIdx.x == 0) {
@@ -159,136 +218,106 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
   cluster_sync();  // the peer's barriers exist before any remote arrive or pair copy
   const uint32_t tmem = *tmem_holder;
   pdl_begin();     // all of the above overlaps the kernel before
-  if (warp == 2) {
-    // group ends, checked, and the running number of work units
-    int32_t prev = 0, units = 0;
-    bool ok = true;
-    for (int base = 0; base < p.E; base += 32) {
-      const int e = base + lane;
-      const int32_t v = e >= p.E ? 0x7FFFFFFF : p.offs ? p.offs[e] : (int32_t)p.M;
-      int32_t before = __shfl_up_sync(0xFFFFFFFFu, v, 1);
-      if (lane == 0) before = prev;
-      const bool in = e < p.E;
-      if (in && (v < before || v < 0 || (int64_t)v > p.M)) ok = false;
-      int32_t n = in && ok ? (v - before + BT - 1) / BT * f_tiles : 0;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int32_t m = __shfl_up_sync(0xFFFFFFFFu, n, o);
-        if (lane >= o) n += m;
-      }
-      if (in) {
-        ends[e] = v;
-        unit_end[e] = units + n;
-      }
-      units += __shfl_sync(0xFFFFFFFFu, n, 31);
-      prev = __shfl_sync(0xFFFFFFFFu, v, min(31, p.E - 1 - base));
-    }
-    ok = __all_sync(0xFFFFFFFFu, ok);
-    if (lane == 0) {
-      s_ok = ok;
-      s_units = ok ? units : 0;
-      if (!ok && blockIdx.x == 0) record_error(p.err, MX_ERR_BAD_OFFSETS);
-    }
-  }
+  if (warp == 2) read_ends<BT>(p, ends, unit_end, &s_ok, &s_units);
   __syncthreads();
   const int32_t n_units = s_units;
 
   if (warp < 4) {
-  regs_give<56>();
-  if (warp == 0) {
-    // ------------------------------------------------------------ loads
-    const bool leader = elect_one();
-    if (leader) {
-      prefetch_tmap(&tmA);
-      prefetch_tmap(&tmB);
-    }
-    int stage = 0; uint32_t phase = 0;
-    bool ok = true;
-    for (int32_t u = unit0; u < n_units && ok; u += ustep) {
-      const Unit t = unit_of<BT>(p, ends, unit_end, u);
-      const int32_t f = t.f0 + rank * 128;
-      const int32_t b0 = (int32_t)(t.t0 + rank * (t.n_eff / 2));
-      for (int kb = 0; kb < num_kb; ++kb) {
-        if (!warp_wait(&empty[stage], phase ^ 1, p.err)) { ok = false; break; }
-        if (leader) {
-          const uint32_t bar = cluster_map(smem_u32(&full[stage]), 0);
-          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * C::TX);
-          tma_load_3d_pair(sA + stage * C::A_BYTES, &tmA, kb * 128, f, t.e, bar);
-          tma_load_2d_pair(sB + stage * C::B_BYTES, &tmB, kb * 128, b0, bar);
-        }
-        __syncwarp();
-        if (++stage == C::STAGES) { stage = 0; phase ^= 1; }
-      }
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMAs
-    if (rank == 0) {
+    regs_give<56>();
+    if (warp == 0) {
+      // ------------------------------------------------------------ loads
       const bool leader = elect_one();
-      // K-major: 8-row atoms 1024 bytes apart, 32 elements = 32 bytes along the row
-      const uint64_t a0 = smem_desc(smem_u32(sA), 16, 1024, 2);
-      const uint64_t b0 = smem_desc(smem_u32(sB), 16, 1024, 2);
+      if (leader) {
+        prefetch_tmap(&tmA);
+        prefetch_tmap(&tmB);
+      }
       int stage = 0; uint32_t phase = 0;
-      int buf = 0; uint32_t buf_phase = 0;
       bool ok = true;
       for (int32_t u = unit0; u < n_units && ok; u += ustep) {
         const Unit t = unit_of<BT>(p, ends, unit_end, u);
-        const uint32_t idesc = C::IDESC | ((uint32_t)(t.n_eff >> 3) << 17);
+        const int32_t f = t.f0 + rank * 128;
+        const int32_t b0 = (int32_t)(t.t0 + rank * (t.n_eff / 2));
         for (int kb = 0; kb < num_kb; ++kb) {
-          if (!warp_wait(&acc_empty[buf], buf_phase ^ 1, p.err)) { ok = false; break; }
-          if (!warp_wait(&full[stage], phase, p.err)) { ok = false; break; }
-          tc_fence_after();
+          if (!warp_wait(&empty[stage], phase ^ 1, p.err)) { ok = false; break; }
           if (leader) {
-            const uint32_t d = tmem + (uint32_t)(buf * BT);
-            const uint64_t ad = a0 + (uint64_t)((stage * C::A_BYTES) >> 4);
-            const uint64_t bd = b0 + (uint64_t)((stage * C::B_BYTES) >> 4);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mma_f8_pair(d, ad + k * 2, bd + k * 2, idesc, k > 0);
-            tc_commit_pair_mc(&empty[stage], 0x3);
-            tc_commit_pair_mc(&acc_full[buf], 0x3);
+            const uint32_t bar = cluster_map(smem_u32(&full[stage]), 0);
+            if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * C::TX);
+            tma_load_3d_pair(sA + stage * C::A_BYTES, &tmA, kb * 128, f, t.e, bar);
+            tma_load_2d_pair(sB + stage * C::B_BYTES, &tmB, kb * 128, b0, bar);
           }
           __syncwarp();
           if (++stage == C::STAGES) { stage = 0; phase ^= 1; }
-          if (++buf == C::BUFS) { buf = 0; buf_phase ^= 1; }
         }
       }
-      if (leader) tc_commit_pair_mc(done_bar, 0x1);
       __syncwarp();
-      mbar_wait(done_bar, 0, p.err);
-    }
-    __syncwarp();
-  } else {
-    // ------------------------------------------------------------ scales
-    // every other K block of a warp's: those of the tile's tokens times the one of the CTA's features
-    constexpr int PER = BT / 32;
-    int slot = warp - 2; uint32_t phase = 0;
-    bool ok = true;
-    int32_t kb0 = warp - 2;  // K blocks are numbered through all units
-    for (int32_t u = unit0; u < n_units && ok; u += ustep) {
-      const Unit t = unit_of<BT>(p, ends, unit_end, u);
-      const int32_t f = t.f0 + rank * 128;
-      const float* w = p.sw + t.e * p.sw_e + (f >> 7) * p.sw_f;
-      int kb = kb0;
-      for (; kb < num_kb; kb += 2) {
-        const float sw = f < p.F ? w[kb * p.sw_c] : 0.0f;
-        float s[PER];
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ MMAs
+      if (rank == 0) {
+        const bool leader = elect_one();
+        // K-major: 8-row atoms 1024 bytes apart, 32 elements = 32 bytes along the row
+        const uint64_t a0 = smem_desc(smem_u32(sA), 16, 1024, 2);
+        const uint64_t b0 = smem_desc(smem_u32(sB), 16, 1024, 2);
+        int stage = 0; uint32_t phase = 0;
+        int buf = 0; uint32_t buf_phase = 0;
+        bool ok = true;
+        for (int32_t u = unit0; u < n_units && ok; u += ustep) {
+          const Unit t = unit_of<BT>(p, ends, unit_end, u);
+          const uint32_t idesc = C::IDESC | ((uint32_t)(t.n_eff >> 3) << 17);
+          for (int kb = 0; kb < num_kb; ++kb) {
+            if (!warp_wait(&acc_empty[buf], buf_phase ^ 1, p.err)) { ok = false; break; }
+            if (!warp_wait(&full[stage], phase, p.err)) { ok = false; break; }
+            tc_fence_after();
+            if (leader) {
+              const uint32_t d = tmem + (uint32_t)(buf * BT);
+              const uint64_t ad = a0 + (uint64_t)((stage * C::A_BYTES) >> 4);
+              const uint64_t bd = b0 + (uint64_t)((stage * C::B_BYTES) >> 4);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          const int64_t at = t.t0 + lane + 32 * i;
-          s[i] = lane + 32 * i < t.tn && at < p.M ? p.st[kb * p.M + at] * sw : 0.0f;
+              for (int k = 0; k < 4; ++k) mma_f8_pair(d, ad + k * 2, bd + k * 2, idesc, k > 0);
+              tc_commit_pair_mc(&empty[stage], 0x3);
+              tc_commit_pair_mc(&acc_full[buf], 0x3);
+            }
+            __syncwarp();
+            if (++stage == C::STAGES) { stage = 0; phase ^= 1; }
+            if (++buf == C::BUFS) { buf = 0; buf_phase ^= 1; }
+          }
         }
-        if (!warp_wait(&sc_empty[slot], phase ^ 1, p.err)) { ok = false; break; }
-        float* dst = sScale + slot * BT;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) dst[lane + 32 * i] = s[i];
-        mbar_arrive(&sc_full[slot]);
-        slot += 2;
-        if (slot >= C::SLOTS) { slot -= C::SLOTS; phase ^= 1; }
+        if (leader) tc_commit_pair_mc(done_bar, 0x1);
+        __syncwarp();
+        mbar_wait(done_bar, 0, p.err);
       }
-      kb0 = kb - num_kb;
+      __syncwarp();
+    } else {
+      // ------------------------------------------------------------ scales
+      // every other K block of a warp's: those of the tile's tokens times the one of the CTA's features
+      constexpr int PER = BT / 32;
+      int slot = warp - 2; uint32_t phase = 0;
+      bool ok = true;
+      int32_t kb0 = warp - 2;  // K blocks are numbered through all units
+      for (int32_t u = unit0; u < n_units && ok; u += ustep) {
+        const Unit t = unit_of<BT>(p, ends, unit_end, u);
+        const int32_t f = t.f0 + rank * 128;
+        const float* w = p.sw + t.e * p.sw_e + (f >> 7) * p.sw_f;
+        int kb = kb0;
+        for (; kb < num_kb; kb += 2) {
+          const float sw = f < p.F ? w[kb * p.sw_c] : 0.0f;
+          float s[PER];
+#pragma unroll
+          for (int i = 0; i < PER; ++i) {
+            const int64_t at = t.t0 + lane + 32 * i;
+            s[i] = lane + 32 * i < t.tn && at < p.M ? p.st[kb * p.M + at] * sw : 0.0f;
+          }
+          if (!warp_wait(&sc_empty[slot], phase ^ 1, p.err)) { ok = false; break; }
+          float* dst = sScale + slot * BT;
+#pragma unroll
+          for (int i = 0; i < PER; ++i) dst[lane + 32 * i] = s[i];
+          mbar_arrive(&sc_full[slot]);
+          slot += 2;
+          if (slot >= C::SLOTS) { slot -= C::SLOTS; phase ^= 1; }
+        }
+        kb0 = kb - num_kb;
+      }
+      __syncwarp();
     }
-    __syncwarp();
-  }
   } else {
     // ------------------------------------------------------------ epilogue
     regs_take<224>();
@@ -362,12 +391,7 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
         }
       }
     }
-    // rows past the last group (all rows, if the ends were refused) are zeros
-    const int64_t first = s_ok ? ends[p.E - 1] : 0;
-    uint4* dst = reinterpret_cast<uint4*>(p.out + first * p.F * 2);
-    const int64_t n = (p.M - first) * p.F / 8;
-    for (int64_t i = (int64_t)blockIdx.x * (FM_EPI * 32) + ew * 32 + lane; i < n; i += (int64_t)gridDim.x * (FM_EPI * 32))
-      dst[i] = make_uint4(0, 0, 0, 0);
+    zero_spare_rows(p, s_ok ? ends[p.E - 1] : 0, ew * 32 + lane);
     __syncwarp();
   }
 
@@ -378,27 +402,250 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
   if (warp == 1) tmem_dealloc_pair(tmem, C::TMEM);
 }
 
-// Pairs that can be resident at once, by device; the kernel's register split needs the registers it was written for.
-template <int BT>
-int resident_pairs(int* n) {
-  using C = FCfg<BT>;
+// ---------------------------------------------------------------- tokens on the M side
+
+// 128 tokens and 256 features a CTA, 256 tokens a pair.
+struct WCfg {
+  static constexpr int A_BYTES = 128 * 128;              // 128 tokens x 128 contraction elements
+  static constexpr int B_BYTES = 128 * 128;              // this CTA's half of the tile's features
+  static constexpr int TX = A_BYTES + B_BYTES;
+  static constexpr int TABLE = FM_MAX_E * 8;
+  static constexpr int SLOTS = 8;
+  static constexpr int SC_BYTES = SLOTS * 256 * 4;       // 128 tokens x 2 feature blocks
+  static constexpr int TMEM = 512;                       // two accumulators of 256 columns
+  static constexpr uint32_t IDESC = (1u << 4) | ((256u >> 3) << 17) | ((256u >> 4) << 24);
+  static constexpr int STAGES = (226 * 1024 - SC_BYTES - TABLE - 1536) / TX;
+  static constexpr size_t SMEM = (size_t)STAGES * TX + SC_BYTES + TABLE + 512 /*barriers*/ + 1024 /*align*/;
+  static_assert((2 * STAGES + 4 + 2 * SLOTS + 2) * 8 <= 512, "barriers");
+  static_assert(SMEM + 1024 /*static*/ <= 227 * 1024, "shared memory");
+};
+
+__global__ void __launch_bounds__(FM_THREADS, 1)
+    fp8_mm_wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, MmParams p) {
+  using C = WCfg;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = sA + C::STAGES * C::A_BYTES;
+  float* sScale = reinterpret_cast<float*>(sB + C::STAGES * C::B_BYTES);
+  int32_t* ends = reinterpret_cast<int32_t*>(sScale + C::SLOTS * 256);
+  int32_t* unit_end = ends + FM_MAX_E;
+  uint64_t* full = reinterpret_cast<uint64_t*>(unit_end + FM_MAX_E);
+  uint64_t* empty = full + C::STAGES;
+  uint64_t* acc_full = empty + C::STAGES;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* sc_full = acc_empty + 2;
+  uint64_t* sc_empty = sc_full + C::SLOTS;
+  uint64_t* done_bar = sc_empty + C::SLOTS;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done_bar + 1);
+  __shared__ int s_ok, s_units;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_ctarank();
+  const int32_t unit0 = blockIdx.x / 2, ustep = gridDim.x / 2;
+  const int32_t num_kb = (p.C + 127) / 128;
+
+  if (threadIdx.x == 0) {
+    // the even CTA's full and acc_empty barriers serve the pair
+    for (int s = 0; s < C::STAGES; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+    for (int a = 0; a < 2; ++a) { mbar_init(&acc_full[a], 1); mbar_init(&acc_empty[a], 2 * FM_EPI); }
+    for (int s = 0; s < C::SLOTS; ++s) { mbar_init(&sc_full[s], 32); mbar_init(&sc_empty[s], FM_EPI); }
+    mbar_init(done_bar, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) { tmem_alloc_pair(tmem_holder, C::TMEM); tmem_relinquish_pair(); }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  cluster_sync();  // the peer's barriers exist before any remote arrive or pair copy
+  const uint32_t tmem = *tmem_holder;
+  pdl_begin();     // all of the above overlaps the kernel before
+  if (warp == 2) read_ends<256>(p, ends, unit_end, &s_ok, &s_units);
+  __syncthreads();
+  const int32_t n_units = s_units;
+
+  if (warp < 4) {
+    regs_give<56>();
+    if (warp == 0) {
+      // ---------------------------------------------------------- loads
+      const bool leader = elect_one();
+      if (leader) {
+        prefetch_tmap(&tmA);
+        prefetch_tmap(&tmB);
+      }
+      int stage = 0; uint32_t phase = 0;
+      bool ok = true;
+      for (int32_t u = unit0; u < n_units && ok; u += ustep) {
+        const Unit t = unit_of<256>(p, ends, unit_end, u);
+        const int32_t row = (int32_t)t.t0 + rank * 128, f = t.f0 + rank * 128;
+        for (int kb = 0; kb < num_kb; ++kb) {
+          if (!warp_wait(&empty[stage], phase ^ 1, p.err)) { ok = false; break; }
+          if (leader) {
+            const uint32_t bar = cluster_map(smem_u32(&full[stage]), 0);
+            if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * C::TX);
+            tma_load_2d_pair(sA + stage * C::A_BYTES, &tmA, kb * 128, row, bar);
+            tma_load_3d_pair(sB + stage * C::B_BYTES, &tmB, kb * 128, f, t.e, bar);
+          }
+          __syncwarp();
+          if (++stage == C::STAGES) { stage = 0; phase ^= 1; }
+        }
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      // ---------------------------------------------------------- MMAs
+      if (rank == 0) {
+        const bool leader = elect_one();
+        const uint64_t a0 = smem_desc(smem_u32(sA), 16, 1024, 2);
+        const uint64_t b0 = smem_desc(smem_u32(sB), 16, 1024, 2);
+        int stage = 0; uint32_t phase = 0;
+        int buf = 0; uint32_t buf_phase = 0;
+        bool ok = true;
+        for (int32_t u = unit0; u < n_units && ok; u += ustep) {
+          for (int kb = 0; kb < num_kb; ++kb) {
+            if (!warp_wait(&acc_empty[buf], buf_phase ^ 1, p.err)) { ok = false; break; }
+            if (!warp_wait(&full[stage], phase, p.err)) { ok = false; break; }
+            tc_fence_after();
+            if (leader) {
+              const uint32_t d = tmem + (uint32_t)(buf * 256);
+              const uint64_t ad = a0 + (uint64_t)((stage * C::A_BYTES) >> 4);
+              const uint64_t bd = b0 + (uint64_t)((stage * C::B_BYTES) >> 4);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) mma_f8_pair(d, ad + k * 2, bd + k * 2, C::IDESC, k > 0);
+              tc_commit_pair_mc(&empty[stage], 0x3);
+              tc_commit_pair_mc(&acc_full[buf], 0x3);
+            }
+            __syncwarp();
+            if (++stage == C::STAGES) { stage = 0; phase ^= 1; }
+            if (++buf == 2) { buf = 0; buf_phase ^= 1; }
+          }
+        }
+        if (leader) tc_commit_pair_mc(done_bar, 0x1);
+        __syncwarp();
+        mbar_wait(done_bar, 0, p.err);
+      }
+      __syncwarp();
+    } else {
+      // ---------------------------------------------------------- scales
+      // every other K block of a warp's: those of the CTA's 128 tokens times each of the tile's two feature blocks'
+      int slot = warp - 2; uint32_t phase = 0;
+      bool ok = true;
+      int32_t kb = warp - 2;  // K blocks are numbered through all units
+      for (int32_t u = unit0; u < n_units && ok; u += ustep) {
+        const Unit t = unit_of<256>(p, ends, unit_end, u);
+        const float* w0 = p.sw + t.e * p.sw_e + (t.f0 >> 7) * p.sw_f;
+        const bool two = t.f0 + 128 < p.F;
+        const int live = min(128, t.tn - rank * 128);
+        for (; kb < num_kb; kb += 2) {
+          const float sw0 = w0[kb * p.sw_c], sw1 = two ? w0[kb * p.sw_c + p.sw_f] : 0.0f;
+          float s[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            s[i] = lane + 32 * i < live ? p.st[kb * p.M + t.t0 + rank * 128 + lane + 32 * i] : 0.0f;
+          if (!warp_wait(&sc_empty[slot], phase ^ 1, p.err)) { ok = false; break; }
+          float* dst = sScale + slot * 256;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            dst[lane + 32 * i] = s[i] * sw0;
+            dst[128 + lane + 32 * i] = s[i] * sw1;
+          }
+          mbar_arrive(&sc_full[slot]);
+          slot += 2;
+          if (slot >= C::SLOTS) { slot -= C::SLOTS; phase ^= 1; }
+        }
+        kb -= num_kb;
+      }
+      __syncwarp();
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    regs_take<224>();
+    const int ew = warp - 4, q = warp & 3, half = ew >> 2;
+    const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * 128);
+    const float* my_scale = sScale + half * 128 + q * 32 + lane;
+    int buf = 0; uint32_t buf_phase = 0;
+    int slot = 0; uint32_t sc_phase = 0;
+    bool ok = true;
+    for (int32_t u = unit0; u < n_units && ok; u += ustep) {
+      const Unit t = unit_of<256>(p, ends, unit_end, u);
+      const int32_t r = rank * 128 + q * 32 + lane;   // this lane's row of the tile
+      f2 acc[4][16];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[j][i] = f2_splat(0.0f);
+      for (int kb = 0; kb < num_kb; ++kb) {
+        if (!warp_wait(&sc_full[slot], sc_phase, p.err)) { ok = false; break; }
+        const f2 s = f2_splat(my_scale[slot * 256]);
+        if (!warp_wait(&acc_full[buf], buf_phase, p.err)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t at = tb + (uint32_t)(buf * 256);
+        // a block is loaded while the one before it is added
+        uint32_t v[2][32];
+        tmem_ld_32cols(at, v[0]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          tmem_ld_wait(v[j & 1]);
+          if (j < 3) tmem_ld_32cols(at + (j + 1) * 32, v[(j + 1) & 1]);
+          else {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&sc_empty[slot]);
+              if (rank != 0) mbar_arrive_cluster_relaxed(cluster_map(smem_u32(&acc_empty[buf]), 0));
+              else mbar_arrive(&acc_empty[buf]);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            acc[j][i] = f2_fma(f2_pack(__uint_as_float(v[j & 1][2 * i]), __uint_as_float(v[j & 1][2 * i + 1])), s, acc[j][i]);
+        }
+        if (++buf == 2) { buf = 0; buf_phase ^= 1; }
+        if (++slot == C::SLOTS) { slot = 0; sc_phase ^= 1; }
+      }
+      if (!ok) break;
+      if (r < t.tn) {
+        const int32_t f = t.f0 + half * 128;
+        uint8_t* dst = p.out + ((t.t0 + r) * p.F + f) * 2;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)   // 16 columns: F is a multiple of 16, rows are 32-byte aligned
+            if (f + j * 32 + i * 16 < p.F) store_32b(dst + j * 64 + i * 32, &acc[j][i * 8]);
+      }
+    }
+    zero_spare_rows(p, s_ok ? ends[p.E - 1] : 0, ew * 32 + lane);
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // no pair MMA, copy or remote arrive targets an exited CTA
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, C::TMEM);
+}
+
+using Kernel = void (*)(CUtensorMap, CUtensorMap, MmParams);
+
+// Pairs of a kernel that can be resident at once, by device (KIND tells the kernels apart); its register split needs
+// the registers that it was written for.
+template <int KIND>
+int resident_pairs(Kernel k, size_t smem, int* n) {
   static std::atomic<int> resident[64];  // the number + 1, once known; any thread may be the one that asks
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_status(e, "cudaGetDevice");
   int r = resident[dev & 63].load(std::memory_order_relaxed);
   if (r == 0) {
-    auto k = fp8_block_mm_kernel<BT>;
     cudaFuncAttributes a{};
     if ((e = cudaFuncGetAttributes(&a, k)) != cudaSuccess) return cuda_status(e, "cudaFuncGetAttributes");
     if (a.numRegs != FM_REGS)
-      return fail(MX_ERR_UNSUPPORTED, "fp8_block_mm_kernel was built with %d registers a thread, not %d", a.numRegs, FM_REGS);
-    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
-    if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute");
+      return fail(MX_ERR_UNSUPPORTED, "the FP8 product was built with %d registers a thread, not %d", a.numRegs, FM_REGS);
+    if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
+      return cuda_status(e, "cudaFuncSetAttribute");
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (num_sms() / 2));
     cfg.blockDim = dim3(FM_THREADS);
-    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.dynamicSmemBytes = smem;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
@@ -421,20 +668,17 @@ int64_t tile_bound(const MmParams& p, int bt) {
   return (p.M + groups * (bt - 1)) / bt * ((p.F + FM_F - 1) / FM_F);
 }
 
-template <int BT>
-int launch_cfg(const CUtensorMap& tA, const CUtensorMap& tB, const MmParams& p, cudaStream_t stream) {
-  using C = FCfg<BT>;
-  const int64_t units = tile_bound(p, BT);
+template <int KIND>
+int launch_cfg(Kernel k, size_t smem, int bt, const CUtensorMap& tA, const CUtensorMap& tB, const MmParams& p, cudaStream_t stream) {
+  const int64_t units = tile_bound(p, bt);
   if (units > INT32_MAX - 1024) return fail(MX_ERR_UNSUPPORTED, "FP8 product: too many tiles");
   int nres = 0;
-  if (int rc = resident_pairs<BT>(&nres)) return rc;
-  auto k = fp8_block_mm_kernel<BT>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+  if (int rc = resident_pairs<KIND>(k, smem, &nres)) return rc;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute");
   const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(units, nres));
   count_launch(MX_KERNEL_FP8_BLOCK);
-  return cuda_status(launch_overlapped(k, (unsigned)(2 * pairs), FM_THREADS, C::SMEM, stream, 2, tA, tB, p),
-                     "fp8_block_mm_kernel launch");
+  return cuda_status(launch_overlapped(k, (unsigned)(2 * pairs), FM_THREADS, smem, stream, 2, tA, tB, p), "FP8 product launch");
 }
 
 }  // namespace
@@ -447,16 +691,19 @@ int launch_fp8_block_mm(const Fp8MmLaunch& g, cudaStream_t stream) {
   p.C = (int32_t)(fwd ? g.K : g.N);
   const int64_t nb = (g.N + 127) / 128, kb = (g.K + 127) / 128;
   p.st = g.sa; p.sw = g.sw; p.sw_e = nb * kb; p.sw_f = fwd ? kb : 1; p.sw_c = fwd ? 1 : kb;
-  const int bt = p.M <= 16 * (int64_t)p.E ? 32 : p.M <= 64 * (int64_t)p.E ? 128 : 256;
-  CUtensorMap tA, tB;
-  uint64_t da[3] = {(uint64_t)p.C, (uint64_t)p.F, (uint64_t)p.E}, sa[2] = {(uint64_t)p.C, (uint64_t)p.C * p.F};
-  uint32_t ba[3] = {128, 128, 1};
-  uint64_t db[2] = {(uint64_t)p.C, (uint64_t)p.M}, sb[1] = {(uint64_t)p.C};
-  uint32_t bb[2] = {128, (uint32_t)bt / 2};
-  int rc = make_tmap(&tA, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(g.w), da, sa, ba, CU_TENSOR_MAP_SWIZZLE_128B);
-  if (!rc) rc = make_tmap(&tB, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(g.a), db, sb, bb, CU_TENSOR_MAP_SWIZZLE_128B);
+  const bool wide = p.M > 64 * (int64_t)p.E;
+  const int bt = wide ? 256 : p.M <= 16 * (int64_t)p.E ? 32 : 128;
+  CUtensorMap w, a;
+  uint64_t dw[3] = {(uint64_t)p.C, (uint64_t)p.F, (uint64_t)p.E}, sw[2] = {(uint64_t)p.C, (uint64_t)p.C * p.F};
+  uint32_t bw[3] = {128, 128, 1};
+  uint64_t da[2] = {(uint64_t)p.C, (uint64_t)p.M}, sa[1] = {(uint64_t)p.C};
+  uint32_t ba[2] = {128, (uint32_t)bt / 2};
+  int rc = make_tmap(&w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(g.w), dw, sw, bw, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (!rc) rc = make_tmap(&a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(g.a), da, sa, ba, CU_TENSOR_MAP_SWIZZLE_128B);
   if (rc) return rc;
-  return bt == 32 ? launch_cfg<32>(tA, tB, p, stream) : bt == 128 ? launch_cfg<128>(tA, tB, p, stream) : launch_cfg<256>(tA, tB, p, stream);
+  if (wide) return launch_cfg<256>(fp8_mm_wide_kernel, WCfg::SMEM, 256, a, w, p, stream);
+  return bt == 32 ? launch_cfg<32>(fp8_mm_narrow_kernel<32>, FCfg<32>::SMEM, 32, w, a, p, stream)
+                  : launch_cfg<128>(fp8_mm_narrow_kernel<128>, FCfg<128>::SMEM, 128, w, a, p, stream);
 }
 
 }  // namespace mx
