@@ -62,6 +62,33 @@ MX_DEVINL void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// warp_wait and mbar_arrive by the barrier's shared memory address.
+MX_DEVINL bool warp_wait_at(uint32_t bar, uint32_t parity, int32_t* err) {
+  uint32_t ok;
+  auto try_wait = [&] {
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+  };
+  bool done = try_wait();
+  if (!done) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!(done = try_wait()))
+      if (globaltimer_ns() - t0 > kWaitLimitNs) {
+        record_error(err, MX_ERR_TIMEOUT);
+        break;
+      }
+  }
+  return __all_sync(0xFFFFFFFFu, done);
+}
+MX_DEVINL void mbar_arrive_at(uint32_t bar) {
+  asm volatile("{\n .reg .b64 st;\n mbarrier.arrive.shared::cta.b64 st, [%0];\n}" ::"r"(bar) : "memory");
+}
+
 template <int R>
 MX_DEVINL void regs_give() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R>
@@ -198,7 +225,9 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done_bar + 1);
   __shared__ int s_ok, s_units;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // by way of a shuffle the compiler knows it to be one number for the warp: without, the roles spill (24 bytes, read back
+  // in their loops)
+  const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = (int)cluster_ctarank();
   const int32_t unit0 = blockIdx.x / 2, ustep = gridDim.x / 2;
   const int32_t num_kb = (p.C + 127) / 128;
@@ -410,13 +439,13 @@ struct WCfg {
   static constexpr int B_BYTES = 128 * 128;              // this CTA's half of the tile's features
   static constexpr int TX = A_BYTES + B_BYTES;
   static constexpr int TABLE = FM_MAX_E * 8;
-  static constexpr int SLOTS = 8;
-  static constexpr int SC_BYTES = SLOTS * 256 * 4;       // 128 tokens x 2 feature blocks
+  static constexpr int SC_KB = 4;                        // K blocks whose scales are handed over together
+  static constexpr int SC_BYTES = 2 * SC_KB * 256 * 4;   // two such lots: 128 tokens x 2 feature blocks each
   static constexpr int TMEM = 512;                       // two accumulators of 256 columns
   static constexpr uint32_t IDESC = (1u << 4) | ((256u >> 3) << 17) | ((256u >> 4) << 24);
   static constexpr int STAGES = (226 * 1024 - SC_BYTES - TABLE - 1536) / TX;
   static constexpr size_t SMEM = (size_t)STAGES * TX + SC_BYTES + TABLE + 512 /*barriers*/ + 1024 /*align*/;
-  static_assert((2 * STAGES + 4 + 2 * SLOTS + 2) * 8 <= 512, "barriers");
+  static_assert((2 * STAGES + 4 + 4 + 2) * 8 <= 512, "barriers");
   static_assert(SMEM + 1024 /*static*/ <= 227 * 1024, "shared memory");
 };
 
@@ -428,19 +457,21 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
   uint8_t* sA = smem;
   uint8_t* sB = sA + C::STAGES * C::A_BYTES;
   float* sScale = reinterpret_cast<float*>(sB + C::STAGES * C::B_BYTES);
-  int32_t* ends = reinterpret_cast<int32_t*>(sScale + C::SLOTS * 256);
+  int32_t* ends = reinterpret_cast<int32_t*>(sScale + 2 * C::SC_KB * 256);
   int32_t* unit_end = ends + FM_MAX_E;
   uint64_t* full = reinterpret_cast<uint64_t*>(unit_end + FM_MAX_E);
   uint64_t* empty = full + C::STAGES;
   uint64_t* acc_full = empty + C::STAGES;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* sc_full = acc_empty + 2;
-  uint64_t* sc_empty = sc_full + C::SLOTS;
-  uint64_t* done_bar = sc_empty + C::SLOTS;
+  uint64_t* sc_empty = sc_full + 2;
+  uint64_t* done_bar = sc_empty + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done_bar + 1);
   __shared__ int s_ok, s_units;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // by way of a shuffle the compiler knows it to be one number for the warp: without, the roles spill (24 bytes, read back
+  // in their loops)
+  const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = (int)cluster_ctarank();
   const int32_t unit0 = blockIdx.x / 2, ustep = gridDim.x / 2;
   const int32_t num_kb = (p.C + 127) / 128;
@@ -449,7 +480,7 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
     // the even CTA's full and acc_empty barriers serve the pair
     for (int s = 0; s < C::STAGES; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
     for (int a = 0; a < 2; ++a) { mbar_init(&acc_full[a], 1); mbar_init(&acc_empty[a], 2 * FM_EPI); }
-    for (int s = 0; s < C::SLOTS; ++s) { mbar_init(&sc_full[s], 32); mbar_init(&sc_empty[s], FM_EPI); }
+    for (int s = 0; s < 2; ++s) { mbar_init(&sc_full[s], 32); mbar_init(&sc_empty[s], FM_EPI); }
     mbar_init(done_bar, 1);
     fence_mbar_init();
   }
@@ -526,94 +557,116 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
       __syncwarp();
     } else {
       // ---------------------------------------------------------- scales
-      // every other K block of a warp's: those of the CTA's 128 tokens times each of the tile's two feature blocks'
-      int slot = warp - 2; uint32_t phase = 0;
+      // every other lot of K blocks of a warp's: those of the CTA's 128 tokens times each of the tile's two feature blocks'
+      uint32_t phase = 0;
       bool ok = true;
-      int32_t kb = warp - 2;  // K blocks are numbered through all units
+      int lot = warp - 2;  // lots are numbered through all units
+      const int lots = (num_kb + C::SC_KB - 1) / C::SC_KB;
+      float* const dst = sScale + lot * C::SC_KB * 256 + lane;
+      uint64_t* const my_full = &sc_full[lot];
+      uint64_t* const my_empty = &sc_empty[lot];
       for (int32_t u = unit0; u < n_units && ok; u += ustep) {
         const Unit t = unit_of<256>(p, ends, unit_end, u);
-        const float* w0 = p.sw + t.e * p.sw_e + (t.f0 >> 7) * p.sw_f;
+        const float* w = p.sw + t.e * p.sw_e + (t.f0 >> 7) * p.sw_f;
         const bool two = t.f0 + 128 < p.F;
         const int live = min(128, t.tn - rank * 128);
-        for (; kb < num_kb; kb += 2) {
-          const float sw0 = w0[kb * p.sw_c], sw1 = two ? w0[kb * p.sw_c + p.sw_f] : 0.0f;
-          float s[4];
+        const float* st = p.st + t.t0 + rank * 128 + lane;
+        for (; lot < lots; lot += 2) {
+          float s[C::SC_KB][4], sw[C::SC_KB][2];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            s[i] = lane + 32 * i < live ? p.st[kb * p.M + t.t0 + rank * 128 + lane + 32 * i] : 0.0f;
-          if (!warp_wait(&sc_empty[slot], phase ^ 1, p.err)) { ok = false; break; }
-          float* dst = sScale + slot * 256;
+          for (int b = 0; b < C::SC_KB; ++b) {
+            const int kb = lot * C::SC_KB + b;
+            const bool in = kb < num_kb;
+            sw[b][0] = in ? w[kb * p.sw_c] : 0.0f;
+            sw[b][1] = in && two ? w[kb * p.sw_c + p.sw_f] : 0.0f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            dst[lane + 32 * i] = s[i] * sw0;
-            dst[128 + lane + 32 * i] = s[i] * sw1;
+            for (int i = 0; i < 4; ++i) s[b][i] = in && lane + 32 * i < live ? st[kb * p.M + 32 * i] : 0.0f;
           }
-          mbar_arrive(&sc_full[slot]);
-          slot += 2;
-          if (slot >= C::SLOTS) { slot -= C::SLOTS; phase ^= 1; }
+          if (!warp_wait(my_empty, phase ^ 1, p.err)) { ok = false; break; }
+#pragma unroll
+          for (int b = 0; b < C::SC_KB; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              dst[b * 256 + 32 * i] = s[b][i] * sw[b][0];
+              dst[b * 256 + 128 + 32 * i] = s[b][i] * sw[b][1];
+            }
+          mbar_arrive(my_full);
+          phase ^= 1;
         }
-        kb -= num_kb;
+        lot -= lots;
       }
       __syncwarp();
     }
   } else {
     // ------------------------------------------------------------ epilogue
     regs_take<224>();
-    const int ew = warp - 4, q = warp & 3, half = ew >> 2;
-    const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * 128);
-    const float* my_scale = sScale + half * 128 + q * 32 + lane;
-    int buf = 0; uint32_t buf_phase = 0;
-    int slot = 0; uint32_t sc_phase = 0;
+    // Registers are what is short (128 sums, 64 values on their way): barriers by their addresses, phases from one count
+    // of K blocks, and the unit is worked out again for the stores.
+    const uint32_t tb = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)((warp - 4) >> 2) * 128;
+    const uint32_t bars = smem_u32(acc_full);                                  // acc_full, acc_empty, sc_full, sc_empty
+    const uint32_t give = cluster_map(bars + 16, 0);                           // the even CTA's acc_empty
+    const uint32_t scales = smem_u32(sScale) + (((warp - 4) >> 2) * 128 + (warp & 3) * 32 + lane) * 4;
+    uint32_t g = 0, lots = 0;   // K blocks and lots of scales so far
     bool ok = true;
     for (int32_t u = unit0; u < n_units && ok; u += ustep) {
-      const Unit t = unit_of<256>(p, ends, unit_end, u);
-      const int32_t r = rank * 128 + q * 32 + lane;   // this lane's row of the tile
       f2 acc[4][16];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[j][i] = f2_splat(0.0f);
+      // one load from TMEM is always on its way: a block of 32 columns is loaded while the one before it is added, the
+      // first of the next K block while the last of this one is
+      uint32_t v[2][32];
+      ok = warp_wait_at(bars + (g & 1) * 8, (g >> 1) & 1, p.err);
+      tc_fence_after();
+      tmem_ld_32cols(tb + (g & 1) * 256, v[0]);
       for (int kb = 0; kb < num_kb; ++kb) {
-        if (!warp_wait(&sc_full[slot], sc_phase, p.err)) { ok = false; break; }
-        const f2 s = f2_splat(my_scale[slot * 256]);
-        if (!warp_wait(&acc_full[buf], buf_phase, p.err)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t at = tb + (uint32_t)(buf * 256);
-        // a block is loaded while the one before it is added
-        uint32_t v[2][32];
-        tmem_ld_32cols(at, v[0]);
+        const uint32_t lot = lots & 1;
+        if (ok && (kb & (C::SC_KB - 1)) == 0) ok = warp_wait_at(bars + 32 + lot * 8, (lots >> 1) & 1, p.err);
+        if (!ok) break;
+        f2 s;
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(s.x) : "r"(scales + (lot * C::SC_KB + (kb & (C::SC_KB - 1))) * 1024));
+        s.y = s.x;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           tmem_ld_wait(v[j & 1]);
-          if (j < 3) tmem_ld_32cols(at + (j + 1) * 32, v[(j + 1) & 1]);
-          else {
+          if (j < 3) {
+            tmem_ld_32cols(tb + (g & 1) * 256 + (j + 1) * 32, v[(j + 1) & 1]);
+          } else {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(&sc_empty[slot]);
-              if (rank != 0) mbar_arrive_cluster_relaxed(cluster_map(smem_u32(&acc_empty[buf]), 0));
-              else mbar_arrive(&acc_empty[buf]);
+            if (lane == 0) mbar_arrive_cluster_relaxed(give + (g & 1) * 8);
+            ++g;
+            if (kb + 1 < num_kb) {
+              ok = warp_wait_at(bars + (g & 1) * 8, (g >> 1) & 1, p.err);
+              tc_fence_after();
+              tmem_ld_32cols(tb + (g & 1) * 256, v[0]);
             }
           }
 #pragma unroll
           for (int i = 0; i < 16; ++i)
             acc[j][i] = f2_fma(f2_pack(__uint_as_float(v[j & 1][2 * i]), __uint_as_float(v[j & 1][2 * i + 1])), s, acc[j][i]);
         }
-        if (++buf == 2) { buf = 0; buf_phase ^= 1; }
-        if (++slot == C::SLOTS) { slot = 0; sc_phase ^= 1; }
+        if ((kb & (C::SC_KB - 1)) == C::SC_KB - 1 || kb == num_kb - 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive_at(bars + 48 + lot * 8);
+          ++lots;
+        }
       }
       if (!ok) break;
+      const Unit t = unit_of<256>(p, ends, unit_end, u);
+      const int32_t r = rank * 128 + (warp & 3) * 32 + lane;   // this lane's row of the tile
       if (r < t.tn) {
-        const int32_t f = t.f0 + half * 128;
+        const int32_t f = t.f0 + ((warp - 4) >> 2) * 128;
         uint8_t* dst = p.out + ((t.t0 + r) * p.F + f) * 2;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)   // 16 columns: F is a multiple of 16, rows are 32-byte aligned
+          for (int i = 0; i < 2; ++i)   // 16 columns: F is a multiple of 16
             if (f + j * 32 + i * 16 < p.F) store_32b(dst + j * 64 + i * 32, &acc[j][i * 8]);
       }
     }
-    zero_spare_rows(p, s_ok ? ends[p.E - 1] : 0, ew * 32 + lane);
+    zero_spare_rows(p, s_ok ? ends[p.E - 1] : 0, (warp - 4) * 32 + lane);
     __syncwarp();
   }
 
