@@ -12,6 +12,7 @@
 // ragged.cu: a group's last tile costs what its rows cost, and a CTA's 128 features are one block of the weight's
 // scales, so that a K block's scale of a token is one number for the CTA: a warp forms sx sw ahead of the epilogue.
 #include <atomic>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -63,21 +64,23 @@ MX_DEVINL void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
 }
 
 // warp_wait and mbar_arrive by the barrier's shared memory address.
-MX_DEVINL bool warp_wait_at(uint32_t bar, uint32_t parity, int32_t* err) {
+MX_DEVINL bool mbar_try_wait_at(uint32_t bar, uint32_t parity) {
   uint32_t ok;
-  auto try_wait = [&] {
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-  };
-  bool done = try_wait();
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// `done`: an earlier try's outcome.
+MX_DEVINL bool warp_wait_at(uint32_t bar, uint32_t parity, int32_t* err, bool done = false) {
+  if (__all_sync(0xFFFFFFFFu, done)) return true;
+  done = mbar_try_wait_at(bar, parity);
   if (!done) {
     const uint64_t t0 = globaltimer_ns();
-    while (!(done = try_wait()))
+    while (!(done = mbar_try_wait_at(bar, parity)))
       if (globaltimer_ns() - t0 > kWaitLimitNs) {
         record_error(err, MX_ERR_TIMEOUT);
         break;
@@ -441,11 +444,12 @@ struct WCfg {
   static constexpr int TABLE = FM_MAX_E * 8;
   static constexpr int SC_KB = 4;                        // K blocks whose scales are handed over together
   static constexpr int SC_BYTES = 2 * SC_KB * 256 * 4;   // two such lots: 128 tokens x 2 feature blocks each
-  static constexpr int TMEM = 512;                       // two accumulators of 256 columns
-  static constexpr uint32_t IDESC = (1u << 4) | ((256u >> 3) << 17) | ((256u >> 4) << 24);
+  static constexpr int BUFS = 4;                         // accumulators of 128 columns, two for either feature block
+  static constexpr int TMEM = BUFS * 128;
+  static constexpr uint32_t IDESC = (1u << 4) | ((128u >> 3) << 17) | ((256u >> 4) << 24);
   static constexpr int STAGES = (226 * 1024 - SC_BYTES - TABLE - 1536) / TX;
   static constexpr size_t SMEM = (size_t)STAGES * TX + SC_BYTES + TABLE + 512 /*barriers*/ + 1024 /*align*/;
-  static_assert((2 * STAGES + 4 + 4 + 2) * 8 <= 512, "barriers");
+  static_assert((2 * STAGES + 2 * BUFS + 4 + 2) * 8 <= 512, "barriers");
   static_assert(SMEM + 1024 /*static*/ <= 227 * 1024, "shared memory");
 };
 
@@ -462,8 +466,8 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(unit_end + FM_MAX_E);
   uint64_t* empty = full + C::STAGES;
   uint64_t* acc_full = empty + C::STAGES;
-  uint64_t* acc_empty = acc_full + 2;
-  uint64_t* sc_full = acc_empty + 2;
+  uint64_t* acc_empty = acc_full + C::BUFS;
+  uint64_t* sc_full = acc_empty + C::BUFS;
   uint64_t* sc_empty = sc_full + 2;
   uint64_t* done_bar = sc_empty + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done_bar + 1);
@@ -479,7 +483,7 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
   if (threadIdx.x == 0) {
     // the even CTA's full and acc_empty barriers serve the pair
     for (int s = 0; s < C::STAGES; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
-    for (int a = 0; a < 2; ++a) { mbar_init(&acc_full[a], 1); mbar_init(&acc_empty[a], 2 * FM_EPI); }
+    for (int a = 0; a < C::BUFS; ++a) { mbar_init(&acc_full[a], 1); mbar_init(&acc_empty[a], FM_EPI); }
     for (int s = 0; s < 2; ++s) { mbar_init(&sc_full[s], 32); mbar_init(&sc_empty[s], FM_EPI); }
     mbar_init(done_bar, 1);
     fence_mbar_init();
@@ -508,14 +512,16 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
       bool ok = true;
       for (int32_t u = unit0; u < n_units && ok; u += ustep) {
         const Unit t = unit_of<256>(p, ends, unit_end, u);
-        const int32_t row = (int32_t)t.t0 + rank * 128, f = t.f0 + rank * 128;
+        const int32_t row = (int32_t)t.t0 + rank * 128, f = t.f0 + rank * 64;
         for (int kb = 0; kb < num_kb; ++kb) {
           if (!warp_wait(&empty[stage], phase ^ 1, p.err)) { ok = false; break; }
           if (leader) {
             const uint32_t bar = cluster_map(smem_u32(&full[stage]), 0);
             if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * C::TX);
             tma_load_2d_pair(sA + stage * C::A_BYTES, &tmA, kb * 128, row, bar);
+            // 64 of either block's 128 features: the MMA's N side is both CTAs' rows
             tma_load_3d_pair(sB + stage * C::B_BYTES, &tmB, kb * 128, f, t.e, bar);
+            tma_load_3d_pair(sB + stage * C::B_BYTES + 8192, &tmB, kb * 128, f + 128, t.e, bar);
           }
           __syncwarp();
           if (++stage == C::STAGES) { stage = 0; phase ^= 1; }
@@ -529,25 +535,31 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
         const uint64_t a0 = smem_desc(smem_u32(sA), 16, 1024, 2);
         const uint64_t b0 = smem_desc(smem_u32(sB), 16, 1024, 2);
         int stage = 0; uint32_t phase = 0;
-        int buf = 0; uint32_t buf_phase = 0;
+        uint32_t phases = 0;  // bit b: of accumulator b of either feature block
         bool ok = true;
         for (int32_t u = unit0; u < n_units && ok; u += ustep) {
           for (int kb = 0; kb < num_kb; ++kb) {
-            if (!warp_wait(&acc_empty[buf], buf_phase ^ 1, p.err)) { ok = false; break; }
+            const int buf = kb & 1;  // each tile begins with accumulator 0
             if (!warp_wait(&full[stage], phase, p.err)) { ok = false; break; }
-            tc_fence_after();
-            if (leader) {
-              const uint32_t d = tmem + (uint32_t)(buf * 256);
-              const uint64_t ad = a0 + (uint64_t)((stage * C::A_BYTES) >> 4);
-              const uint64_t bd = b0 + (uint64_t)((stage * C::B_BYTES) >> 4);
+            const uint64_t ad = a0 + (uint64_t)((stage * C::A_BYTES) >> 4);
+            const uint64_t bd = b0 + (uint64_t)((stage * C::B_BYTES) >> 4);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) mma_f8_pair(d, ad + k * 2, bd + k * 2, C::IDESC, k > 0);
-              tc_commit_pair_mc(&empty[stage], 0x3);
-              tc_commit_pair_mc(&acc_full[buf], 0x3);
+            for (int half = 0; half < 2; ++half) {   // feature blocks
+              if (ok) ok = warp_wait(&acc_empty[half * 2 + buf], ~(phases >> buf) & 1, p.err);
+              if (!ok) break;
+              tc_fence_after();
+              if (leader) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  mma_f8_pair(tmem + (uint32_t)((half * 2 + buf) * 128), ad + k * 2, bd + half * 512 + k * 2, C::IDESC, k > 0);
+                if (half == 1) tc_commit_pair_mc(&empty[stage], 0x3);
+                tc_commit_pair_mc(&acc_full[half * 2 + buf], 0x3);
+              }
+              __syncwarp();
             }
-            __syncwarp();
+            phases ^= 1u << buf;
+            if (!ok) break;
             if (++stage == C::STAGES) { stage = 0; phase ^= 1; }
-            if (++buf == 2) { buf = 0; buf_phase ^= 1; }
           }
         }
         if (leader) tc_commit_pair_mc(done_bar, 0x1);
@@ -600,13 +612,16 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
   } else {
     // ------------------------------------------------------------ epilogue
     regs_take<224>();
-    // Registers are what is short (128 sums, 64 values on their way): barriers by their addresses, phases from one count
-    // of K blocks, and the unit is worked out again for the stores.
-    const uint32_t tb = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)((warp - 4) >> 2) * 128;
-    const uint32_t bars = smem_u32(acc_full);                                  // acc_full, acc_empty, sc_full, sc_empty
-    const uint32_t give = cluster_map(bars + 16, 0);                           // the even CTA's acc_empty
-    const uint32_t scales = smem_u32(sScale) + (((warp - 4) >> 2) * 128 + (warp & 3) * 32 + lane) * 4;
-    uint32_t g = 0, lots = 0;   // K blocks and lots of scales so far
+    // A warp has 32 tokens and one feature block, the other warp of its scheduler the other: their MMAs come one after the
+    // other, so one adds while the other waits or loads (both on either block's half: 376 us against ...).
+    // Registers are what is short (128 sums, 64 values on their way): barriers by their addresses, and the unit is worked out again for the stores.
+    const uint32_t half = (uint32_t)(warp - 4) >> 2;
+    const uint32_t tb = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * 256;
+    const uint32_t bars = smem_u32(acc_full) + half * 16;                      // acc_full, acc_empty, sc_full, sc_empty
+    const uint32_t give = cluster_map(bars + C::BUFS * 8, 0);                  // the even CTA's acc_empty
+    const uint32_t sc_bars = smem_u32(sc_full);
+    const uint32_t scales = smem_u32(sScale) + (half * 128 + (warp & 3) * 32 + lane) * 4;
+    uint32_t ph0 = 0, ph1 = 0, lots = 0;   // phases of the accumulators; lots of scales so far
     bool ok = true;
     for (int32_t u = unit0; u < n_units && ok; u += ustep) {
       f2 acc[4][16];
@@ -617,47 +632,55 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
       // one load from TMEM is always on its way: a block of 32 columns is loaded while the one before it is added, the
       // first of the next K block while the last of this one is
       uint32_t v[2][32];
-      ok = warp_wait_at(bars + (g & 1) * 8, (g >> 1) & 1, p.err);
+      ok = warp_wait_at(bars, ph0, p.err);
       tc_fence_after();
-      tmem_ld_32cols(tb + (g & 1) * 256, v[0]);
-      for (int kb = 0; kb < num_kb; ++kb) {
+      tmem_ld_32cols(tb, v[0]);
+      // K block kb, in accumulator BUF
+      auto step = [&](auto buf_c, int kb) {
+        constexpr int BUF = decltype(buf_c)::value;
         const uint32_t lot = lots & 1;
-        if (ok && (kb & (C::SC_KB - 1)) == 0) ok = warp_wait_at(bars + 32 + lot * 8, (lots >> 1) & 1, p.err);
-        if (!ok) break;
+        if (ok && (kb & (C::SC_KB - 1)) == 0) ok = warp_wait_at(sc_bars + lot * 8, (lots >> 1) & 1, p.err);
         f2 s;
         asm volatile("ld.shared.f32 %0, [%1];" : "=f"(s.x) : "r"(scales + (lot * C::SC_KB + (kb & (C::SC_KB - 1))) * 1024));
         s.y = s.x;
+        const bool more = kb + 1 < num_kb;
+        bool ready = false;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
+          if (j == 3) ready = mbar_try_wait_at(bars + (BUF ^ 1) * 8, BUF ? ph0 : ph1);
           tmem_ld_wait(v[j & 1]);
           if (j < 3) {
-            tmem_ld_32cols(tb + (g & 1) * 256 + (j + 1) * 32, v[(j + 1) & 1]);
+            tmem_ld_32cols(tb + BUF * 128 + (j + 1) * 32, v[(j + 1) & 1]);
           } else {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster_relaxed(give + (g & 1) * 8);
-            ++g;
-            if (kb + 1 < num_kb) {
-              ok = warp_wait_at(bars + (g & 1) * 8, (g >> 1) & 1, p.err);
+            if (lane == 0) mbar_arrive_cluster_relaxed(give + BUF * 8);
+            if (BUF) ph1 ^= 1; else ph0 ^= 1;
+            if (more) {
+              if (ok) ok = warp_wait_at(bars + (BUF ^ 1) * 8, BUF ? ph0 : ph1, p.err, ready);
               tc_fence_after();
-              tmem_ld_32cols(tb + (g & 1) * 256, v[0]);
+              tmem_ld_32cols(tb + (BUF ^ 1) * 128, v[0]);
             }
           }
 #pragma unroll
           for (int i = 0; i < 16; ++i)
             acc[j][i] = f2_fma(f2_pack(__uint_as_float(v[j & 1][2 * i]), __uint_as_float(v[j & 1][2 * i + 1])), s, acc[j][i]);
         }
-        if ((kb & (C::SC_KB - 1)) == C::SC_KB - 1 || kb == num_kb - 1) {
+        if ((kb & (C::SC_KB - 1)) == C::SC_KB - 1 || !more) {
           __syncwarp();
-          if (lane == 0) mbar_arrive_at(bars + 48 + lot * 8);
+          if (lane == 0) mbar_arrive_at(sc_bars + 16 + lot * 8);
           ++lots;
         }
+      };
+      for (int kb = 0; kb < num_kb && ok; kb += 2) {
+        step(std::integral_constant<int, 0>{}, kb);
+        if (kb + 1 < num_kb && ok) step(std::integral_constant<int, 1>{}, kb + 1);
       }
       if (!ok) break;
       const Unit t = unit_of<256>(p, ends, unit_end, u);
       const int32_t r = rank * 128 + (warp & 3) * 32 + lane;   // this lane's row of the tile
       if (r < t.tn) {
-        const int32_t f = t.f0 + ((warp - 4) >> 2) * 128;
+        const int32_t f = t.f0 + (int32_t)half * 128;
         uint8_t* dst = p.out + ((t.t0 + r) * p.F + f) * 2;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -748,7 +771,7 @@ int launch_fp8_block_mm(const Fp8MmLaunch& g, cudaStream_t stream) {
   const int bt = wide ? 256 : p.M <= 16 * (int64_t)p.E ? 32 : 128;
   CUtensorMap w, a;
   uint64_t dw[3] = {(uint64_t)p.C, (uint64_t)p.F, (uint64_t)p.E}, sw[2] = {(uint64_t)p.C, (uint64_t)p.C * p.F};
-  uint32_t bw[3] = {128, 128, 1};
+  uint32_t bw[3] = {128, wide ? 64u : 128u, 1};
   uint64_t da[2] = {(uint64_t)p.C, (uint64_t)p.M}, sa[1] = {(uint64_t)p.C};
   uint32_t ba[2] = {128, (uint32_t)bt / 2};
   int rc = make_tmap(&w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(g.w), dw, sw, bw, CU_TENSOR_MAP_SWIZZLE_128B);
