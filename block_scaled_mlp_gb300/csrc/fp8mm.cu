@@ -92,6 +92,16 @@ MX_DEVINL void mbar_arrive_at(uint32_t bar) {
   asm volatile("{\n .reg .b64 st;\n mbarrier.arrive.shared::cta.b64 st, [%0];\n}" ::"r"(bar) : "memory");
 }
 
+// acc += (a, b) s, where it stands: as a volatile statement it stays behind the TMEM load that was issued before it (left
+// to the compiler's order, 356 against 342 us).
+MX_DEVINL void fma_here(f2& acc, uint32_t a, uint32_t b, float s) {
+  asm volatile(
+      "{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %4};\n mov.b64 z, {%0, %1};\n"
+      " fma.rn.f32x2 z, x, y, z;\n mov.b64 {%0, %1}, z;\n}"
+      : "+f"(acc.x), "+f"(acc.y)
+      : "r"(a), "r"(b), "f"(s));
+}
+
 template <int R>
 MX_DEVINL void regs_give() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R>
@@ -442,14 +452,12 @@ struct WCfg {
   static constexpr int B_BYTES = 128 * 128;              // this CTA's half of the tile's features
   static constexpr int TX = A_BYTES + B_BYTES;
   static constexpr int TABLE = FM_MAX_E * 8;
-  static constexpr int SC_KB = 4;                        // K blocks whose scales are handed over together
-  static constexpr int SC_BYTES = 2 * SC_KB * 256 * 4;   // two such lots: 128 tokens x 2 feature blocks each
   static constexpr int BUFS = 4;                         // accumulators of 128 columns, two for either feature block
   static constexpr int TMEM = BUFS * 128;
   static constexpr uint32_t IDESC = (1u << 4) | ((128u >> 3) << 17) | ((256u >> 4) << 24);
-  static constexpr int STAGES = (226 * 1024 - SC_BYTES - TABLE - 1536) / TX;
-  static constexpr size_t SMEM = (size_t)STAGES * TX + SC_BYTES + TABLE + 512 /*barriers*/ + 1024 /*align*/;
-  static_assert((2 * STAGES + 2 * BUFS + 4 + 2) * 8 <= 512, "barriers");
+  static constexpr int STAGES = (226 * 1024 - TABLE - 1536) / TX;
+  static constexpr size_t SMEM = (size_t)STAGES * TX + TABLE + 512 /*barriers*/ + 1024 /*align*/;
+  static_assert((2 * STAGES + 2 * BUFS + 2) * 8 <= 512, "barriers");
   static_assert(SMEM + 1024 /*static*/ <= 227 * 1024, "shared memory");
 };
 
@@ -460,16 +468,13 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
   uint8_t* sB = sA + C::STAGES * C::A_BYTES;
-  float* sScale = reinterpret_cast<float*>(sB + C::STAGES * C::B_BYTES);
-  int32_t* ends = reinterpret_cast<int32_t*>(sScale + 2 * C::SC_KB * 256);
+  int32_t* ends = reinterpret_cast<int32_t*>(sB + C::STAGES * C::B_BYTES);
   int32_t* unit_end = ends + FM_MAX_E;
   uint64_t* full = reinterpret_cast<uint64_t*>(unit_end + FM_MAX_E);
   uint64_t* empty = full + C::STAGES;
   uint64_t* acc_full = empty + C::STAGES;
   uint64_t* acc_empty = acc_full + C::BUFS;
-  uint64_t* sc_full = acc_empty + C::BUFS;
-  uint64_t* sc_empty = sc_full + 2;
-  uint64_t* done_bar = sc_empty + 2;
+  uint64_t* done_bar = acc_empty + C::BUFS;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done_bar + 1);
   __shared__ int s_ok, s_units;
 
@@ -484,7 +489,6 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
     // the even CTA's full and acc_empty barriers serve the pair
     for (int s = 0; s < C::STAGES; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
     for (int a = 0; a < C::BUFS; ++a) { mbar_init(&acc_full[a], 1); mbar_init(&acc_empty[a], FM_EPI); }
-    for (int s = 0; s < 2; ++s) { mbar_init(&sc_full[s], 32); mbar_init(&sc_empty[s], FM_EPI); }
     mbar_init(done_bar, 1);
     fence_mbar_init();
   }
@@ -567,47 +571,6 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
         mbar_wait(done_bar, 0, p.err);
       }
       __syncwarp();
-    } else {
-      // ---------------------------------------------------------- scales
-      // every other lot of K blocks of a warp's: those of the CTA's 128 tokens times each of the tile's two feature blocks'
-      uint32_t phase = 0;
-      bool ok = true;
-      int lot = warp - 2;  // lots are numbered through all units
-      const int lots = (num_kb + C::SC_KB - 1) / C::SC_KB;
-      float* const dst = sScale + lot * C::SC_KB * 256 + lane;
-      uint64_t* const my_full = &sc_full[lot];
-      uint64_t* const my_empty = &sc_empty[lot];
-      for (int32_t u = unit0; u < n_units && ok; u += ustep) {
-        const Unit t = unit_of<256>(p, ends, unit_end, u);
-        const float* w = p.sw + t.e * p.sw_e + (t.f0 >> 7) * p.sw_f;
-        const bool two = t.f0 + 128 < p.F;
-        const int live = min(128, t.tn - rank * 128);
-        const float* st = p.st + t.t0 + rank * 128 + lane;
-        for (; lot < lots; lot += 2) {
-          float s[C::SC_KB][4], sw[C::SC_KB][2];
-#pragma unroll
-          for (int b = 0; b < C::SC_KB; ++b) {
-            const int kb = lot * C::SC_KB + b;
-            const bool in = kb < num_kb;
-            sw[b][0] = in ? w[kb * p.sw_c] : 0.0f;
-            sw[b][1] = in && two ? w[kb * p.sw_c + p.sw_f] : 0.0f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[b][i] = in && lane + 32 * i < live ? st[kb * p.M + 32 * i] : 0.0f;
-          }
-          if (!warp_wait(my_empty, phase ^ 1, p.err)) { ok = false; break; }
-#pragma unroll
-          for (int b = 0; b < C::SC_KB; ++b)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              dst[b * 256 + 32 * i] = s[b][i] * sw[b][0];
-              dst[b * 256 + 128 + 32 * i] = s[b][i] * sw[b][1];
-            }
-          mbar_arrive(my_full);
-          phase ^= 1;
-        }
-        lot -= lots;
-      }
-      __syncwarp();
     }
   } else {
     // ------------------------------------------------------------ epilogue
@@ -617,12 +580,27 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
     // Registers are what is short (128 sums, 64 values on their way): barriers by their addresses, and the unit is worked out again for the stores.
     const uint32_t half = (uint32_t)(warp - 4) >> 2;
     const uint32_t tb = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * 256;
-    const uint32_t bars = smem_u32(acc_full) + half * 16;                      // acc_full, acc_empty, sc_full, sc_empty
+    const uint32_t bars = smem_u32(acc_full) + half * 16;                      // acc_full, acc_empty
     const uint32_t give = cluster_map(bars + C::BUFS * 8, 0);                  // the even CTA's acc_empty
-    const uint32_t sc_bars = smem_u32(sc_full);
-    const uint32_t scales = smem_u32(sScale) + (half * 128 + (warp & 3) * 32 + lane) * 4;
-    uint32_t ph0 = 0, ph1 = 0, lots = 0;   // phases of the accumulators; lots of scales so far
+    uint32_t ph0 = 0, ph1 = 0;   // phases of the accumulators
     bool ok = true;
+    // scales of this lane's token and of the warp's features, two K blocks ahead
+    const float *st = nullptr, *sw = nullptr;
+    int ahead = 0;
+    float st0 = 0.0f, sw0 = 0.0f, st1 = 0.0f, sw1 = 0.0f;
+    auto scales_of = [&](int32_t u) {
+      const Unit t = unit_of<256>(p, ends, unit_end, u);
+      const int32_t r = rank * 128 + (warp & 3) * 32 + lane;
+      st = p.st + t.t0 + min(r, t.tn - 1);
+      sw = p.sw + t.e * p.sw_e + min((t.f0 >> 7) + (int32_t)half, (p.F - 1) >> 7) * p.sw_f;
+      st0 = st1 = *st, sw0 = sw1 = *sw;
+      if (num_kb > 1) {
+        st += p.M, sw += p.sw_c;
+        st1 = *st, sw1 = *sw;
+      }
+      ahead = num_kb - 2;
+    };
+    if (unit0 < n_units) scales_of(unit0);
     for (int32_t u = unit0; u < n_units && ok; u += ustep) {
       f2 acc[4][16];
 #pragma unroll
@@ -638,11 +616,12 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
       // K block kb, in accumulator BUF
       auto step = [&](auto buf_c, int kb) {
         constexpr int BUF = decltype(buf_c)::value;
-        const uint32_t lot = lots & 1;
-        if (ok && (kb & (C::SC_KB - 1)) == 0) ok = warp_wait_at(sc_bars + lot * 8, (lots >> 1) & 1, p.err);
-        f2 s;
-        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(s.x) : "r"(scales + (lot * C::SC_KB + (kb & (C::SC_KB - 1))) * 1024));
-        s.y = s.x;
+        const float s = BUF ? st1 * sw1 : st0 * sw0;
+        if (--ahead >= 0) {  // into the same registers: a copy would wait for the load
+          st += p.M, sw += p.sw_c;
+          if (BUF) st1 = __ldg(st), sw1 = __ldg(sw);
+          else st0 = __ldg(st), sw0 = __ldg(sw);
+        }
         const bool more = kb + 1 < num_kb;
         bool ready = false;
 #pragma unroll
@@ -663,13 +642,7 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
             }
           }
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            acc[j][i] = f2_fma(f2_pack(__uint_as_float(v[j & 1][2 * i]), __uint_as_float(v[j & 1][2 * i + 1])), s, acc[j][i]);
-        }
-        if ((kb & (C::SC_KB - 1)) == C::SC_KB - 1 || !more) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive_at(sc_bars + 16 + lot * 8);
-          ++lots;
+          for (int i = 0; i < 16; ++i) fma_here(acc[j][i], v[j & 1][2 * i], v[j & 1][2 * i + 1], s);
         }
       };
       for (int kb = 0; kb < num_kb && ok; kb += 2) {
@@ -677,6 +650,7 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
         if (kb + 1 < num_kb && ok) step(std::integral_constant<int, 1>{}, kb + 1);
       }
       if (!ok) break;
+      if (u + ustep < n_units) scales_of(u + ustep);   // while this tile is stored
       const Unit t = unit_of<256>(p, ends, unit_end, u);
       const int32_t r = rank * 128 + (warp & 3) * 32 + lane;   // this lane's row of the tile
       if (r < t.tn) {
