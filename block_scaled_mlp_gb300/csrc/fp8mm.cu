@@ -452,11 +452,13 @@ struct WCfg {
   static constexpr int B_BYTES = 128 * 128;              // this CTA's half of the tile's features
   static constexpr int TX = A_BYTES + B_BYTES;
   static constexpr int TABLE = FM_MAX_E * 8;
+  static constexpr int SLOTS = 4;                        // K blocks whose scales are at hand
+  static constexpr int SC_BYTES = SLOTS * 256 * 4;       // 128 tokens x 2 feature blocks each
   static constexpr int BUFS = 4;                         // accumulators of 128 columns, two for either feature block
   static constexpr int TMEM = BUFS * 128;
   static constexpr uint32_t IDESC = (1u << 4) | ((128u >> 3) << 17) | ((256u >> 4) << 24);
-  static constexpr int STAGES = (226 * 1024 - TABLE - 1536) / TX;
-  static constexpr size_t SMEM = (size_t)STAGES * TX + TABLE + 512 /*barriers*/ + 1024 /*align*/;
+  static constexpr int STAGES = (226 * 1024 - SC_BYTES - TABLE - 1536) / TX;
+  static constexpr size_t SMEM = (size_t)STAGES * TX + SC_BYTES + TABLE + 512 /*barriers*/ + 1024 /*align*/;
   static_assert((2 * STAGES + 2 * BUFS + 2) * 8 <= 512, "barriers");
   static_assert(SMEM + 1024 /*static*/ <= 227 * 1024, "shared memory");
 };
@@ -468,7 +470,8 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
   uint8_t* sB = sA + C::STAGES * C::A_BYTES;
-  int32_t* ends = reinterpret_cast<int32_t*>(sB + C::STAGES * C::B_BYTES);
+  float* sScale = reinterpret_cast<float*>(sB + C::STAGES * C::B_BYTES);
+  int32_t* ends = reinterpret_cast<int32_t*>(sScale + C::SLOTS * 256);
   int32_t* unit_end = ends + FM_MAX_E;
   uint64_t* full = reinterpret_cast<uint64_t*>(unit_end + FM_MAX_E);
   uint64_t* empty = full + C::STAGES;
@@ -488,7 +491,7 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
   if (threadIdx.x == 0) {
     // the even CTA's full and acc_empty barriers serve the pair
     for (int s = 0; s < C::STAGES; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
-    for (int a = 0; a < C::BUFS; ++a) { mbar_init(&acc_full[a], 1); mbar_init(&acc_empty[a], FM_EPI); }
+    for (int a = 0; a < C::BUFS; ++a) { mbar_init(&acc_full[a], 2); mbar_init(&acc_empty[a], FM_EPI); }
     mbar_init(done_bar, 1);
     fence_mbar_init();
   }
@@ -571,6 +574,53 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
         mbar_wait(done_bar, 0, p.err);
       }
       __syncwarp();
+    } else {
+      // ---------------------------------------------------------- scales
+      // A warp for either feature block: the scales of the CTA's 128 tokens times the block's, loaded four K blocks ahead.
+      // They are part of what an accumulator's acc_full stands for, so the epilogue waits once for both (a barrier of their
+      // own cost it 30 us of 340).  A slot is free when the accumulator's last product is done: its MMA waited for the
+      // epilogue to be through with the one before, four K blocks ago at most.
+      const int half = warp - 2;
+      int32_t next_u = unit0, next_kb = 0;
+      const float *st = nullptr, *sw = nullptr;
+      int live = 0;
+      float s[4][4], f[4];
+      auto load = [&](int i) {
+        if (next_u >= n_units) return;
+        if (next_kb == 0) {
+          const Unit t = unit_of<256>(p, ends, unit_end, next_u);
+          st = p.st + t.t0 + rank * 128 + lane;
+          sw = p.sw + t.e * p.sw_e + min((t.f0 >> 7) + half, (p.F - 1) >> 7) * p.sw_f;
+          live = t.tn - rank * 128;
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s[i][c] = lane + 32 * c < live ? __ldg(st + 32 * c) : 0.0f;
+        f[i] = __ldg(sw);
+        st += p.M, sw += p.sw_c;
+        if (++next_kb == num_kb) { next_kb = 0; next_u += ustep; }
+      };
+      float* dst = sScale + half * 128 + lane;
+      int32_t u = unit0, kb = 0;
+      uint32_t phases = 0;  // bit b: of the block's accumulator b
+      bool ok = true;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) load(i);
+      while (u < n_units && ok) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (u >= n_units || !ok) break;
+          const int buf = kb & 1;
+          ok = warp_wait(&acc_full[half * 2 + buf], ~(phases >> buf) & 1, p.err);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) dst[i * 256 + 32 * c] = s[i][c] * f[i];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acc_full[half * 2 + buf]);
+          phases ^= 1u << buf;
+          load(i);
+          if (++kb == num_kb) { kb = 0; u += ustep; }
+        }
+      }
+      __syncwarp();
     }
   } else {
     // ------------------------------------------------------------ epilogue
@@ -584,23 +634,8 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
     const uint32_t give = cluster_map(bars + C::BUFS * 8, 0);                  // the even CTA's acc_empty
     uint32_t ph0 = 0, ph1 = 0;   // phases of the accumulators
     bool ok = true;
-    // scales of this lane's token and of the warp's features, two K blocks ahead
-    const float *st = nullptr, *sw = nullptr;
-    int ahead = 0;
-    float st0 = 0.0f, sw0 = 0.0f, st1 = 0.0f, sw1 = 0.0f;
-    auto scales_of = [&](int32_t u) {
-      const Unit t = unit_of<256>(p, ends, unit_end, u);
-      const int32_t r = rank * 128 + (warp & 3) * 32 + lane;
-      st = p.st + t.t0 + min(r, t.tn - 1);
-      sw = p.sw + t.e * p.sw_e + min((t.f0 >> 7) + (int32_t)half, (p.F - 1) >> 7) * p.sw_f;
-      st0 = st1 = *st, sw0 = sw1 = *sw;
-      if (num_kb > 1) {
-        st += p.M, sw += p.sw_c;
-        st1 = *st, sw1 = *sw;
-      }
-      ahead = num_kb - 2;
-    };
-    if (unit0 < n_units) scales_of(unit0);
+    const uint32_t scales = smem_u32(sScale) + (half * 128 + (warp & 3) * 32 + lane) * 4;
+    uint32_t slot = 0;
     for (int32_t u = unit0; u < n_units && ok; u += ustep) {
       f2 acc[4][16];
 #pragma unroll
@@ -616,12 +651,9 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
       // K block kb, in accumulator BUF
       auto step = [&](auto buf_c, int kb) {
         constexpr int BUF = decltype(buf_c)::value;
-        const float s = BUF ? st1 * sw1 : st0 * sw0;
-        if (--ahead >= 0) {  // into the same registers: a copy would wait for the load
-          st += p.M, sw += p.sw_c;
-          if (BUF) st1 = __ldg(st), sw1 = __ldg(sw);
-          else st0 = __ldg(st), sw0 = __ldg(sw);
-        }
+        float s;
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(s) : "r"(scales + slot * 1024));
+        slot = (slot + 1) & (C::SLOTS - 1);
         const bool more = kb + 1 < num_kb;
         bool ready = false;
 #pragma unroll
@@ -650,7 +682,6 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
         if (kb + 1 < num_kb && ok) step(std::integral_constant<int, 1>{}, kb + 1);
       }
       if (!ok) break;
-      if (u + ustep < n_units) scales_of(u + ustep);   // while this tile is stored
       const Unit t = unit_of<256>(p, ends, unit_end, u);
       const int32_t r = rank * 128 + (warp & 3) * 32 + lane;   // this lane's row of the tile
       if (r < t.tn) {
