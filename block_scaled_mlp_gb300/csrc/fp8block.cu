@@ -41,10 +41,16 @@ MX_DEVINL BlockScale block_scale(uint32_t amax_bits) {
   b.ok = amax_bits < 0x7F80u;
   const float m = fmaxf(__uint_as_float(amax_bits << 16), FB_LEAST);
   b.scale = b.ok ? __fdiv_rn(m, 448.0f) : __uint_as_float(0x7FC00000u);
-  const float r = __fdiv_rn(448.0f, m);
-  b.hi = __uint_as_float(__float_as_uint(r) & 0xFFFFFF00u);
-  // the rest of the quotient: 448 - hi m is exact (an fma), m is not subnormal
-  b.lo = __fdiv_rn(fmaf(-b.hi, m, 448.0f), m);
+  // 448 / m by its fraction f in [1, 2): an approximate reciprocal c, hi = 448 c cut off at 16 bits, the rest (448 - hi f) c;
+  // 448 - hi f is exact in an fma, so hi + lo is within 2^-37 of the quotient.  Then both times 2^-e.
+  const uint32_t u = __float_as_uint(m), E = u >> 23;
+  const float f = __uint_as_float((u & 0x007FFFFFu) | 0x3F800000u);
+  float c;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(c) : "f"(f));
+  const float hi = __uint_as_float(__float_as_uint(448.0f * c) & 0xFFFFFF00u), lo = fmaf(-hi, f, 448.0f) * c;
+  const float p = __uint_as_float(E < 254 ? (254 - E) << 23 : 0x00400000u);
+  b.hi = hi * p;
+  b.lo = lo * p;
   return b;
 }
 
@@ -59,45 +65,112 @@ MX_DEVINL uint2 codes8(uint4 v, const BlockScale& s) {
 }
 
 struct RowsParams {
-  const uint4* x;         // [rows_in, cols] bf16
+  const uint8_t* x;       // [rows_in, cols] bf16
   int64_t rows_in;
   const int32_t* src;     // [rows] or NULL
   int64_t rows;
   int32_t div;
-  uint32_t c8;            // cols / 8
-  uint2* codes;           // [rows, cols]
-  float* scales;          // [ceil(cols / 128), rows]
+  int32_t cols;
+  int32_t blocks;         // of a row
+  int32_t share;          // blocks of a row that a warp takes
+  int32_t splits;         // warps that share eight rows
+  uint8_t* codes;         // [rows, cols]
+  float* scales;          // [blocks, rows]
   int32_t* err;
 };
 
 constexpr int FR_THREADS = 256;
+constexpr int FR_DEEP = 2;  // blocks of a row on their way
 
-// 16 lanes have a block.
+// 32 elements of a row: two loads of 32 bytes, or four of 16 where rows are not on 32 bytes.
+struct Quarter {
+  uint32_t w[16];
+};
+template <bool WIDE>
+MX_DEVINL Quarter load_quarter(const uint8_t* x, int left) {  // left: elements up to the row's end
+  Quarter q;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t* w = q.w + h * 8;
+    if (left >= (h + 1) * 16) {   // cols is a multiple of 16
+      if (WIDE) {
+        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                     : "l"(x + h * 32));
+      } else {
+        const uint4 a = __ldg(reinterpret_cast<const uint4*>(x + h * 32)), b = __ldg(reinterpret_cast<const uint4*>(x + h * 32 + 16));
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = 0;
+    }
+  }
+  return q;
+}
+
+// A warp has eight rows, four lanes each, and goes along their blocks: 32 elements a lane, so a block's largest takes two
+// exchanges, the scales of eight rows leave as one sector, and a row's src is read once.
+template <bool WIDE>
 __global__ void __launch_bounds__(FR_THREADS) fp8_block_rows_kernel(RowsParams p) {
   pdl_begin();
-  const uint32_t blocks = (p.c8 + 15) / 16;
-  const int64_t n = p.rows * blocks, g = ((int64_t)blockIdx.x * FR_THREADS + threadIdx.x) >> 4;
-  if (((int64_t)blockIdx.x * FR_THREADS + (threadIdx.x & ~31)) >> 4 >= n) return;  // whole warps: the lanes talk
-  const int sub = threadIdx.x & 15;
-  const int64_t row = g / blocks;
-  const uint32_t b = (uint32_t)(g - row * blocks), c = b * 16 + sub;
-  const bool in = g < n && c < p.c8;
+  const int lane = threadIdx.x & 31, sub = lane & 3;
+  const int64_t w = (int64_t)blockIdx.x * (FR_THREADS / 32) + (threadIdx.x >> 5);
+  const int64_t group = w / p.splits;
+  const int32_t b0 = (int32_t)(w - group * p.splits) * p.share, b1 = min(p.blocks, b0 + p.share);
+  const int64_t row = group * 8 + (lane >> 2);
+  if (group * 8 >= p.rows) return;  // whole warps: the lanes talk
+  const bool live = row < p.rows;
   int64_t from = row;
-  if (p.src && g < n) {
+  if (p.src && live) {
     const int32_t s = p.src[row];
     from = s < 0 ? -1 : s / p.div;
     if (from >= p.rows_in) {
-      if (sub == 0) record_error(p.err, MX_ERR_BAD_OFFSETS);
+      if (sub == 0 && b0 == 0) record_error(p.err, MX_ERR_BAD_OFFSETS);
       from = -1;
     }
   }
-  const uint4 v = in && from >= 0 ? __ldg(p.x + from * p.c8 + c) : make_uint4(0, 0, 0, 0);
-  uint32_t m = amax8(v);
+  const bool read = live && from >= 0;
+  const int c0 = b0 * 128 + sub * 32;   // this lane's columns of the first block
+  const uint8_t* x = p.x + (read ? from * p.cols + c0 : 0) * 2;
+  uint8_t* codes = p.codes + row * p.cols + c0;
+  float* scales = p.scales + b0 * p.rows + row;
+  Quarter v[FR_DEEP];
 #pragma unroll
-  for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  const BlockScale s = block_scale(m);
-  if (in) p.codes[row * p.c8 + c] = codes8(v, s);
-  if (sub == 0 && g < n) p.scales[b * p.rows + row] = s.scale;
+  for (int i = 0; i < FR_DEEP; ++i)
+    v[i] = load_quarter<WIDE>(x + i * 256, read && b0 + i < b1 ? p.cols - c0 - i * 128 : 0);
+  for (int32_t b = b0; b < b1; b += FR_DEEP) {
+#pragma unroll
+    for (int i = 0; i < FR_DEEP; ++i) {
+      if (b + i >= b1) break;
+      const int left = p.cols - (b + i) * 128 - sub * 32;
+      const Quarter q = v[i];
+      v[i] = load_quarter<WIDE>(x + (b + i + FR_DEEP - b0) * 256, read && b + i + FR_DEEP < b1 ? left - FR_DEEP * 128 : 0);
+      uint32_t m = q.w[0];
+#pragma unroll
+      for (int j = 1; j < 16; ++j) m = max_abs_bf16x2(m, q.w[j]);
+      m &= 0x7FFF7FFFu;
+      m = max(m & 0xFFFFu, m >> 16);  // magnitudes are ordered as whole numbers are, NaN above all
+      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+      const BlockScale s = block_scale(m);
+      uint32_t c[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) c[j] = s.ok ? codes4(q.w[2 * j], q.w[2 * j + 1], s) : 0x7F7F7F7Fu;
+      if (live) {
+        uint8_t* dst = codes + (b + i - b0) * 128;
+        if (WIDE && left >= 32) {
+          asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(c[0]), "r"(c[1]), "r"(c[2]),
+                       "r"(c[3]), "r"(c[4]), "r"(c[5]), "r"(c[6]), "r"(c[7])
+                       : "memory");
+        } else {
+          if (left >= 16) reinterpret_cast<uint4*>(dst)[0] = make_uint4(c[0], c[1], c[2], c[3]);
+          if (left >= 32) reinterpret_cast<uint4*>(dst)[1] = make_uint4(c[4], c[5], c[6], c[7]);
+        }
+        if (sub == 0) scales[(b + i - b0) * p.rows] = s.scale;
+      }
+    }
+  }
 }
 
 struct WeightParams {
@@ -166,12 +239,19 @@ __global__ void __launch_bounds__(FW_THREADS) fp8_block_weight_kernel(WeightPara
 int launch_fp8_block_rows(const void* x, int64_t rows_in, int64_t cols, const int32_t* src, int64_t rows, int32_t div, void* codes,
                           float* scales, int32_t* err, cudaStream_t stream) {
   RowsParams p{};
-  p.x = (const uint4*)x; p.rows_in = rows_in; p.src = src; p.rows = rows; p.div = div; p.c8 = (uint32_t)(cols / 8);
-  p.codes = (uint2*)codes; p.scales = scales; p.err = err;
-  const int64_t n = rows * ((cols + 127) / 128);
+  p.x = (const uint8_t*)x; p.rows_in = rows_in; p.src = src; p.rows = rows; p.div = div; p.cols = (int32_t)cols;
+  p.blocks = (int32_t)((cols + 127) / 128);
+  p.codes = (uint8_t*)codes; p.scales = scales; p.err = err;
+  // few rows: their blocks shared out until each SM has 32 warps
+  const int64_t groups = (rows + 7) / 8, want = 32 * (int64_t)num_sms();
+  p.splits = (int32_t)std::min<int64_t>(p.blocks, (want + groups - 1) / groups);
+  p.share = (p.blocks + p.splits - 1) / p.splits;
+  p.splits = (p.blocks + p.share - 1) / p.share;
+  const bool wide = cols % 32 == 0 && ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(codes)) & 31) == 0;
+  const int64_t n = groups * p.splits;
   count_launch(MX_KERNEL_FP8_BLOCK);
-  return cuda_status(launch_overlapped(fp8_block_rows_kernel, (unsigned)((n + FR_THREADS / 16 - 1) / (FR_THREADS / 16)), FR_THREADS,
-                                       0, stream, 1, p),
+  return cuda_status(launch_overlapped(wide ? fp8_block_rows_kernel<true> : fp8_block_rows_kernel<false>,
+                                       (unsigned)((n + FR_THREADS / 32 - 1) / (FR_THREADS / 32)), FR_THREADS, 0, stream, 1, p),
                      "fp8_block_rows_kernel launch");
 }
 
