@@ -9,17 +9,27 @@
 //
 // The order is that of c in double precision: an expert that a rounding of fp32 puts ahead of another would
 // make the result depend on how the scores are computed.  It is found from fp32 scores whose errors are
-// bounded: a warp has a token, finds the k + 1 largest c, and where two neighbours among them (or the
-// groups at the border) are closer than the bounds of both allow, and are not equal by their inputs, it
-// orders the token's experts again in double precision.  Without a bias and groups the logits themselves
-// are the order and there is nothing to bound.
+// bounded.  Where two neighbours among the k largest are closer than the bounds of both allow, and not equal by their
+// inputs, these k are ordered again by scores of 44 bits (pairs of fp32 values); where that holds for the k-th and one
+// behind it, or for groups at the border, all experts of the token are (route_closely), and where 44 bits leave it open
+// too, in double precision (route_exactly; its fp64 instructions take a warp some 15 us).  Without a bias and groups the
+// logits themselves are the order and there is nothing to bound.
 //
-// Bounds of fp32 scores.  expf is off by 1 ulp (2^-23), l - max is rounded by 2^-24 |l - max|, which is at
-// most 2^-24 (-ln s); sums of E terms in a tree of V + 5 levels by 2^-24 each, and with the exponentials'
-// own errors (their mean |l - max| is at most ln E) by less than 2^-18; it scales all scores of a token
-// alike, so two scores' difference by that much of itself.  Underflow ends at 2^-126.
+// Bounds of fp32 scores.  Sigmoid: expf is off by 2^-23 of itself, which moves s by 2^-23 s (1 - s), 1 + t and the
+// reciprocal by 2^-24 s each: 2^-23 s (2 - s) together.  Softmax: l - max is rounded by 2^-24 |l - max| besides, at most
+// 2^-24 (-ln s) of s, and a sum of E terms, with the terms' own errors, is off by (V + 14) 2^-24: that scales all scores
+// of a token alike, so it moves the difference of two by that much of itself.  c is rounded by 2^-24.  Underflow ends at
+// 2^-126.
+//
+// A warp has a token and a lane V neighbouring experts.  What bounds the kernels is a launch's and a few loads' latency
+// and, from some thousand tokens on, instructions: about 20 for each of the k rounds that find the next largest c (eight
+// lanes a token and four tokens a warp take as many, and were slower: 2.8 against 2.0 us for 8 tokens).
+// ROUTE_MEASURED
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
+#include "swiglu_math.cuh"
 
 namespace mx {
 
@@ -28,17 +38,64 @@ namespace {
 constexpr uint32_t FULL = 0xFFFFFFFFu;
 constexpr int ROUTE_WARPS = 4;
 
-template <bool WIDE>
-MX_DEVINL float logit(const void* row, int e) {
+MX_DEVINL float bf16_value(uint32_t bits) { return __uint_as_float(bits << 16); }
+
+MX_DEVINL float logit(const void* row, bool wide, int e) {
   // + 0: -0 and 0 are one value
-  return WIDE ? reinterpret_cast<const float*>(row)[e] + 0.0f
-              : __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[e] << 16) + 0.0f;
+  return wide ? reinterpret_cast<const float*>(row)[e] + 0.0f : bf16_value(reinterpret_cast<const uint16_t*>(row)[e]) + 0.0f;
+}
+
+// V neighbouring values from the first on: in vectors of up to 16 bytes where rows lie on them.
+template <int V>
+MX_DEVINL void load_values(const void* row, bool wide, bool vec, int first, int E, float none, float (&l)[V]) {
+  if (vec && first < E) {  // E is a multiple of V
+    if (wide) {
+      const float* p = reinterpret_cast<const float*>(row) + first;
+      if constexpr (V >= 4) {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) {
+          const float4 v = __ldg(reinterpret_cast<const float4*>(p) + i);
+          l[4 * i] = v.x, l[4 * i + 1] = v.y, l[4 * i + 2] = v.z, l[4 * i + 3] = v.w;
+        }
+      } else if constexpr (V == 2) {
+        const float2 v = __ldg(reinterpret_cast<const float2*>(p));
+        l[0] = v.x, l[1] = v.y;
+      } else {
+        l[0] = __ldg(p);
+      }
+    } else {
+      const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + first;
+      if constexpr (V >= 8) {
+#pragma unroll
+        for (int i = 0; i < V / 8; ++i) {
+          const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) l[8 * i + 2 * j] = bf16_value(w[j]), l[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+        }
+      } else if constexpr (V >= 2) {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+          const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+          l[2 * i] = bf16_value(w), l[2 * i + 1] = __uint_as_float(w & 0xFFFF0000u);
+        }
+      } else {
+        l[0] = bf16_value(__ldg(p));
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      l[i] = first + i >= E ? none : wide ? __ldg(reinterpret_cast<const float*>(row) + first + i) : bf16_value(__ldg(reinterpret_cast<const uint16_t*>(row) + first + i));
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) l[i] += 0.0f;
 }
 
 // Larger floats have larger keys; 0 is below all of them (NaN does not occur).
 MX_DEVINL uint32_t key_of(float f) {
   const uint32_t u = __float_as_uint(f);
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 MX_DEVINL float of_key(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k); }
 
@@ -59,31 +116,12 @@ struct RouteParams {
   const float* bias;      // [E] or NULL
   int64_t T;
   int32_t E, k, groups, top_groups;
-  int renorm;
+  int wide, sigmoid, renorm;
+  int vec, vec_bias;      // rows of logits, and bias, can be read in vectors
   float scale;
   int32_t* ids;           // [T, k]
   float* weights;         // [T, k]
 };
-
-// The groups taken, as bits, from the values that lane g has for group g; *sure: no other
-// choice is within `off` of it.
-template <class T>
-MX_DEVINL uint32_t take_groups(T value, int groups, int top, T off, bool* sure) {
-  const int lane = threadIdx.x & 31;
-  int rank = 0;
-  for (int g = 0; g < groups; ++g) {
-    const T v = __shfl_sync(FULL, value, g);
-    if (v > value || (v == value && g < lane)) ++rank;
-  }
-  const uint32_t taken = __ballot_sync(FULL, lane < groups && rank < top);
-  const uint32_t last = __ballot_sync(FULL, lane < groups && rank == top - 1);
-  const uint32_t next = __ballot_sync(FULL, lane < groups && rank == top);
-  if (next) {
-    const T a = __shfl_sync(FULL, value, __ffs(last) - 1), b = __shfl_sync(FULL, value, __ffs(next) - 1);
-    *sure = a - b > off || (a == b && isinf(a));
-  }
-  return taken;
-}
 
 // The two largest of a group's values, added.
 template <class T>
@@ -99,16 +137,27 @@ MX_DEVINL T group_value(const T* c, int size, int first) {
   return size > 1 ? a + b : a;
 }
 
+// Rank of `value` among the values that lanes 0, step, ... of the warp have; `mine` is its own place there.
+template <class T>
+MX_DEVINL int rank_of(T value, int mine, int n, int step) {
+  int rank = 0;
+  for (int g = 0; g < n; ++g) {
+    const T v = __shfl_sync(FULL, value, g * step);
+    if (v > value || (v == value && g < mine)) ++rank;
+  }
+  return rank;
+}
+
 // A token's experts in double precision, by one warp: lane j returns the j-th.
-template <bool WIDE, bool SIGMOID>
 __device__ __noinline__ int route_exactly(const RouteParams& p, const void* row, double* c) {
   const int lane = threadIdx.x & 31;
   const int E = p.E, n = (E + 31) / 32;
+  const bool wide = p.wide;
   __syncwarp();
   double most = -INFINITY, z = 0;
   for (int i = 0; i < n; ++i) {
     const int e = lane + 32 * i;
-    if (e < E) most = fmax(most, (double)logit<WIDE>(row, e));
+    if (e < E) most = fmax(most, (double)logit(row, wide, e));
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) most = fmax(most, __shfl_xor_sync(FULL, most, o));
@@ -116,27 +165,27 @@ __device__ __noinline__ int route_exactly(const RouteParams& p, const void* row,
   for (int i = 0; i < n; ++i) {
     const int e = lane + 32 * i;
     if (e >= E) continue;
-    const double l = logit<WIDE>(row, e);
-    const double v = SIGMOID ? 1 / (1 + exp(-l)) : exp(l - most);
-    c[e] = v;
+    const double l = logit(row, wide, e);
+    const double v = exp(p.sigmoid ? -l : l - most);
+    c[e] = p.sigmoid ? 1 / (1 + v) : v;
     z += v;
   }
   z = warp_sum(z);
   for (int i = 0; i < n; ++i) {
     const int e = lane + 32 * i;
     if (e >= E) continue;
-    double v = SIGMOID ? c[e] : z > 0 ? c[e] / z : 0.0;
+    double v = p.sigmoid ? c[e] : z > 0 ? c[e] / z : 0.0;
     if (p.bias) v += (double)p.bias[e];
-    if (logit<WIDE>(row, e) == -INFINITY) v = -INFINITY;
+    if (logit(row, wide, e) == -INFINITY) v = -INFINITY;
     c[e] = v;
   }
   __syncwarp();
   uint32_t taken = 0;  // bit i: expert lane + 32 i is chosen, or of no group that is
   if (p.groups > 1) {
     const int size = E / p.groups;
-    bool sure = true;
     const double v = lane < p.groups ? group_value(c + lane * size, size, lane % size) : 0.0;
-    const uint32_t in = take_groups(v, p.groups, p.top_groups, 0.0, &sure);
+    const int rank = rank_of(v, lane, p.groups, 1);  // by all lanes: they exchange values
+    const uint32_t in = __ballot_sync(FULL, lane < p.groups && rank < p.top_groups);
     for (int i = 0; i < n; ++i) {
       const int e = lane + 32 * i;
       if (e < E && !(in >> (e / size) & 1)) taken |= 1u << i;
@@ -146,7 +195,7 @@ __device__ __noinline__ int route_exactly(const RouteParams& p, const void* row,
     __syncwarp();
     for (int i = 0; i < n; ++i) {
       const int e = lane + 32 * i;
-      if (e < E) c[e] = logit<WIDE>(row, e);
+      if (e < E) c[e] = logit(row, wide, e);
     }
   }
   int mine = 0;
@@ -170,9 +219,216 @@ __device__ __noinline__ int route_exactly(const RouteParams& p, const void* row,
   return mine;
 }
 
-// A warp has a token; lane i experts i V to i V + V - 1.
+// ---- scores of 44 bits
+using swiglu_math::ff;
+
+MX_DEVINL bool ff_more(ff a, ff b) { return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo); }
+MX_DEVINL float ff_minus(ff a, ff b) { return (a.hi - b.hi) + (a.lo - b.lo); }  // a little off: bounds have room
+MX_DEVINL ff ff_shfl(ff v, int lane) { return ff{__shfl_sync(FULL, v.hi, lane), __shfl_sync(FULL, v.lo, lane)}; }
+MX_DEVINL ff ff_shfl_xor(ff v, int o) { return ff{__shfl_xor_sync(FULL, v.hi, o), __shfl_xor_sync(FULL, v.lo, o)}; }
+
+// swiglu_math::ff_exp and ff_rcp (|x| <= 64; relative error below 2^-43) in few instructions: a warp that comes here finds
+// none of them in its instruction cache, and fetching them is what it waits for.
+__constant__ float2 kFfTaylor[7] = {{1.0f, 0.0f}, {1.0f, 0.0f}, {0.5f, 0.0f}, {0x1.555556p-3f, -0x1.555556p-28f},
+                                    {0x1.555556p-5f, -0x1.555556p-30f}, {0x1.111112p-7f, -0x1.dddddep-32f},
+                                    {0x1.6c16c2p-10f, -0x1.27d27ep-35f}};
+__device__ __noinline__ ff ff_exp_small(float x) {
+  using namespace swiglu_math;
+  constexpr float L1 = 0x1.62e4p-1f, L2 = 0x1.7f7d1cp-20f, L3 = 0x1.ef357ap-45f;
+  const float n = rintf(__fmul_rn(x, 0x1.715476p+0f));
+  ff r = two_sum(x, -__fmul_rn(n, L1));  // exact
+  const float p2 = __fmul_rn(n, L2);
+  r = ff_add(r, ff{-p2, -__fmaf_rn(n, L2, -p2)});
+  r = ff_add_f(r, -__fmul_rn(n, L3));
+  float tail = 0x1.ae6456p-26f;
+  tail = __fmaf_rn(tail, r.hi, 0x1.27e4fcp-22f);
+  tail = __fmaf_rn(tail, r.hi, 0x1.71de3ap-19f);
+  tail = __fmaf_rn(tail, r.hi, 0x1.a01a02p-16f);
+  tail = __fmaf_rn(tail, r.hi, 0x1.a01a02p-13f);
+  ff acc{tail, 0.0f};
+#pragma unroll 1
+  for (int k = 6; k >= 0; --k) acc = ff_add(ff_mul(acc, r), ff{kFfTaylor[k].x, kFfTaylor[k].y});
+  const float two_n = __uint_as_float((uint32_t)((int)n + 127) << 23);
+  return {__fmul_rn(acc.hi, two_n), __fmul_rn(acc.lo, two_n)};
+}
+MX_DEVINL ff ff_rcp_small(ff x) {  // one Newton step on an approximate reciprocal
+  const float q = swiglu_math::rcp_approx(x.hi);
+  return swiglu_math::fast_two_sum(q, __fmul_rn(q, __fmaf_rn(-x.lo, q, __fmaf_rn(-x.hi, q, 1.0f))));
+}
+
+// e^(l - most) for |l - most| <= 64: of the difference's nearest fp32 value and the rest
+MX_DEVINL ff ff_exp_difference(float l, float most) {
+  const ff d = swiglu_math::two_sum(l, -most);
+  return swiglu_math::ff_mul(ff_exp_small(d.hi), ff{1.0f, fmaf(0.5f * d.lo, d.lo, d.lo)});
+}
+// Scores within 2^-42 of themselves; |l| (sigmoid) or |l - most| up to 64.  inv: 1 / sum (softmax).
+MX_DEVINL ff ff_score(bool sigmoid, float l, float most, ff inv) {
+  if (sigmoid) return ff_rcp_small(swiglu_math::ff_add_f(ff_exp_small(-l), 1.0f));
+  return swiglu_math::ff_mul(ff_exp_difference(l, most), inv);
+}
+MX_DEVINL bool ff_in_range(bool sigmoid, float l, float most) { return fabsf(sigmoid ? l : l - most) <= 64.0f; }
+// 1 / sum of a token's e^(l - most), by the warp; terms beyond the range are less than 2^-92 of it.
+__device__ __noinline__ ff ff_inverse_sum(const void* row, bool wide, int E, float most) {
+  ff z{0.0f, 0.0f};
+#pragma unroll 1
+  for (int e = threadIdx.x & 31; e < E; e += 32) {
+    const float l = logit(row, wide, e);
+    if (l - most >= -64.0f) z = swiglu_math::ff_add(z, ff_exp_difference(l, most));
+  }
+#pragma unroll 1
+  for (int o = 16; o; o >>= 1) z = swiglu_math::ff_add(z, ff_shfl_xor(z, o));
+  return ff_rcp_small(z);
+}
+
+// A token's experts by scores of 44 bits, by one warp: lane j returns the j-th.  *sure: no difference that decides is
+// within what they are off by (2^-40 with room), or the inputs are equal.
+__device__ __noinline__ int route_closely(const RouteParams& p, const void* row, float most, double* buf, bool* sure) {
+  const int lane = threadIdx.x & 31;
+  const int E = p.E, n = (E + 31) / 32;
+  const bool wide = p.wide, sigmoid = p.sigmoid;
+  float2* c = reinterpret_cast<float2*>(buf);
+  ff inv{1.0f, 0.0f};
+  if (!sigmoid) inv = ff_inverse_sum(row, wide, E, most);
+  bool ok = true;
+  __syncwarp();
+  float size_of_c = 0.0f;
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) {
+    const int e = lane + 32 * i;
+    if (e >= E) continue;
+    const float l = logit(row, wide, e);
+    ff v{-INFINITY, 0.0f};
+    if (l != -INFINITY) {
+      ok = ok && ff_in_range(sigmoid, l, most);
+      v = ff_score(sigmoid, l, most, inv);
+      if (p.bias) v = swiglu_math::ff_add_f(v, p.bias[e]);
+      if (isinf(p.bias ? p.bias[e] : 0.0f)) v = ff{p.bias[e], 0.0f};
+      if (!isinf(v.hi)) size_of_c = fmaxf(size_of_c, fabsf(v.hi));
+    }
+    c[e] = make_float2(v.hi, v.lo);
+  }
+  const float off = 0x1p-39f * (1.0f + warp_max(size_of_c));
+  __syncwarp();
+  uint32_t taken = 0;  // bit i: expert lane + 32 i is chosen, or of no group that is
+  if (p.groups > 1) {
+    const int size = E / p.groups;
+    ff a{-INFINITY, 0.0f}, b{-INFINITY, 0.0f};
+    int ea = lane * size, eb = ea;
+    if (lane < p.groups)
+#pragma unroll 1
+      for (int i = 0; i < size; ++i) {
+        const float2 f = c[lane * size + i];
+        const ff v{f.x, f.y};
+        if (ff_more(v, a)) { b = a; eb = ea; a = v; ea = lane * size + i; }
+        else if (i && ff_more(v, b)) { b = v; eb = lane * size + i; }
+      }
+    ff value = size == 1 || isinf(a.hi) ? a : isinf(b.hi) ? b : swiglu_math::ff_add(a, b);
+    int rank = 0;
+#pragma unroll 1
+    for (int g = 0; g < p.groups; ++g) {
+      const ff v = ff_shfl(value, g);
+      if (ff_more(v, value) || (v.hi == value.hi && v.lo == value.lo && g < lane)) ++rank;
+    }
+    const uint32_t in = __ballot_sync(FULL, lane < p.groups && rank < p.top_groups);
+    // the last group taken and the first that is not: apart, or both of the same two values
+    const int last = __ffs(__ballot_sync(FULL, lane < p.groups && rank == p.top_groups - 1)) - 1;
+    const int next = __ffs(__ballot_sync(FULL, lane < p.groups && rank == p.top_groups)) - 1;
+    if (next >= 0) {
+      const ff va = ff_shfl(value, last), vb = ff_shfl(value, next);
+      const float apart = ff_minus(va, vb);
+      if (!(apart > 2 * off) && !(va.hi == vb.hi && isinf(va.hi))) {  // equal by their two experts' inputs, or open
+        const int a1 = __shfl_sync(FULL, ea, last), a2 = __shfl_sync(FULL, eb, last);
+        const int b1 = __shfl_sync(FULL, ea, next), b2 = __shfl_sync(FULL, eb, next);
+        auto alike = [&](int x, int y) { return logit(row, wide, x) == logit(row, wide, y) && (!p.bias || p.bias[x] == p.bias[y]); };
+        ok = ok && alike(a1, b1) && (size == 1 || alike(a2, b2));
+      }
+    }
+  #pragma unroll 1
+  for (int i = 0; i < n; ++i) {
+      const int e = lane + 32 * i;
+      if (e < E && !(in >> (e / size) & 1)) taken |= 1u << i;
+    }
+  }
+  if (!p.bias) {  // the logits' own order
+    __syncwarp();
+  #pragma unroll 1
+  for (int i = 0; i < n; ++i) {
+      const int e = lane + 32 * i;
+      if (e < E) c[e] = make_float2(logit(row, wide, e), 0.0f);
+    }
+  }
+  int mine = 0;
+  ff last{0.0f, 0.0f};
+  float last_l = 0.0f, last_b = 0.0f;
+#pragma unroll 1
+  for (int j = 0; j < p.k; ++j) {
+    ff v{-INFINITY, 0.0f};
+    int at = INT32_MAX;
+  #pragma unroll 1
+  for (int i = 0; i < n; ++i) {
+      const int e = lane + 32 * i;
+      if (e >= E || (taken >> i & 1)) continue;
+      const ff w{c[e].x, c[e].y};
+      if (at == INT32_MAX || ff_more(w, v)) { v = w; at = e; }
+    }
+#pragma unroll 1
+    for (int o = 16; o; o >>= 1) {
+      const ff w = ff_shfl_xor(v, o);
+      const int b = __shfl_xor_sync(FULL, at, o);
+      if (b != INT32_MAX && (at == INT32_MAX || ff_more(w, v) || (w.hi == v.hi && w.lo == v.lo && b < at))) { v = w; at = b; }
+    }
+    if (lane == j) mine = at;
+    if ((at & 31) == lane) taken |= 1u << (at >> 5);
+    if (p.bias) {
+      const float l = logit(row, wide, at), b = p.bias[at];
+      if (j && !(ff_minus(last, v) > off) && !(l == last_l && b == last_b) && !(isinf(v.hi) && v.hi == last.hi)) ok = false;
+      last = v, last_l = l, last_b = b;
+    }
+  }
+  if (p.bias)
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {  // against all that are left
+      const int e = lane + 32 * i;
+      if (e >= E || (taken >> i & 1)) continue;
+      const ff w{c[e].x, c[e].y};
+      if (!(ff_minus(last, w) > off) && !(logit(row, wide, e) == last_l && p.bias[e] == last_b) && !(isinf(w.hi) && w.hi == last.hi))
+        ok = false;
+    }
+  *sure = __all_sync(FULL, ok);
+  __syncwarp();
+  return mine;
+}
+
+// The k experts that lanes 0 to k - 1 have (numbers and logits) in order by scores of 44 bits: each lane's place.  *sure as
+// in route_closely.
+__device__ __noinline__ int order_closely(const RouteParams& p, const void* row, float most, int id, float x, bool* sure) {
+  const bool has = (int)(threadIdx.x & 31) < p.k, sigmoid = p.sigmoid;
+  ff inv{1.0f, 0.0f}, c{-INFINITY, 0.0f};
+  if (!sigmoid) inv = ff_inverse_sum(row, p.wide, p.E, most);
+  bool fine = true;
+  const float b = has ? p.bias[id] : 0.0f;
+  if (has && x != -INFINITY) {
+    fine = ff_in_range(sigmoid, x, most);
+    c = ff_score(sigmoid, x, most, inv);
+    c = isinf(b) ? ff{b, 0.0f} : swiglu_math::ff_add_f(c, b);
+  }
+  int place = 0;
+#pragma unroll 1
+  for (int j = 0; j < p.k; ++j) {
+    const ff v = ff_shfl(c, j);
+    const int e = __shfl_sync(FULL, id, j);
+    const float xj = __shfl_sync(FULL, x, j), bj = __shfl_sync(FULL, b, j);
+    const bool same = (xj == x && bj == b) || (v.hi == c.hi && isinf(v.hi));
+    if (same ? e < id : ff_more(v, c)) ++place;
+    if (has && !same && !(fabsf(ff_minus(v, c)) > 0x1p-39f * (1.0f + fabsf(c.hi)))) fine = false;
+  }
+  *sure = __all_sync(FULL, fine);
+  return place;
+}
+
+// Lane i has experts i V to i V + V - 1.
 template <int V, bool WIDE, bool SIGMOID>
-__global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(RouteParams p) {
+__global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __grid_constant__ RouteParams p) {
   extern __shared__ double s_c[];
   pdl_begin();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -180,19 +436,19 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(RouteParams
   if (t >= p.T) return;
   double* const buf = s_c + (size_t)warp * p.E;
   const int E = p.E, k = p.k, first = lane * V;
-  const void* row = reinterpret_cast<const uint8_t*>(p.logits) + (size_t)t * E * (WIDE ? 4 : 2);
+  constexpr bool sigmoid = SIGMOID, wide = WIDE;
+  const void* row = reinterpret_cast<const uint8_t*>(p.logits) + (size_t)t * E * (wide ? 4 : 2);
   float l[V];
+  load_values<V>(row, wide, p.vec, first, E, -INFINITY, l);
   bool bad = false;
   float most = -INFINITY;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    l[i] = first + i < E ? logit<WIDE>(row, first + i) : -INFINITY;
-    bad |= l[i] != l[i] || (!SIGMOID && l[i] == INFINITY);
+    bad |= l[i] != l[i] || (!sigmoid && l[i] == INFINITY);
     most = fmaxf(most, l[i]);
   }
   float inv = 1.0f;
-  const bool need_scores = p.bias || p.groups > 1;
-  if (!SIGMOID) {
+  if (!sigmoid) {
     most = warp_max(most);
     if (most == -INFINITY) most = 0.0f;
     float z = 0.0f;
@@ -201,96 +457,179 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(RouteParams
     z = warp_sum(z);
     inv = z > 0.0f ? 1.0f / z : 0.0f;
   }
-  auto score = [&](float x) { return SIGMOID ? 1.0f / (1.0f + expf(-x)) : expf(x - most) * inv; };
+  auto score = [&](float x) { return sigmoid ? __frcp_rn(1.0f + expf(-x)) : expf(x - most) * inv; };
   uint32_t key[V];
-  float c[V];
+  bool sure_groups = true, sure = true;   // of the groups, of the set of k
+  if (p.bias || p.groups > 1) {
+    float c[V], b[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    c[i] = l[i];
-    if (need_scores) {
-      const float s = score(l[i]);
-      float b = 0.0f;
-      if (p.bias && first + i < E) b = p.bias[first + i];
-      bad |= b != b;
-      c[i] = l[i] == -INFINITY ? -INFINITY : s + b;
-      bad |= c[i] != c[i];
-    }
-    key[i] = first + i < E ? key_of(p.bias ? c[i] : l[i]) : 0;
-  }
-  if (__any_sync(FULL, bad)) {  // no order: the first k, and weights that say so
-    if (lane < k) {
-      p.ids[t * k + lane] = lane;
-      p.weights[t * k + lane] = __uint_as_float(0x7FC00000u);
-    }
-    return;
-  }
-  bool sure = true;
-  if (p.groups > 1) {
-    const int size = E / p.groups;
-    float* cf = reinterpret_cast<float*>(buf);
+    for (int i = 0; i < V; ++i) b[i] = 0.0f;
+    if (p.bias) load_values<V>(p.bias, true, p.vec_bias, first, E, 0.0f, b);
     float largest = 0.0f;
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (first + i < E) {
-        cf[first + i] = c[i];
-        if (c[i] != -INFINITY) largest = fmaxf(largest, fabsf(c[i]));
-      }
-    __syncwarp();
-    const float v = lane < p.groups ? group_value(cf + lane * size, size, lane % size) : 0.0f;
-    // a score is off by 2^-18 of the largest at most, a sum of two by twice that; c and the sum are rounded
-    const float off = 0x1p-16f * (SIGMOID ? 1.0f : inv) + 0x1p-20f * warp_max(largest);
-    const uint32_t in = take_groups(v, p.groups, p.top_groups, off, &sure);
+    for (int i = 0; i < V; ++i) {
+      bad |= b[i] != b[i];
+      c[i] = l[i] == -INFINITY ? -INFINITY : score(l[i]) + b[i];
+      bad |= c[i] != c[i];
+      if (c[i] != -INFINITY) largest = fmaxf(largest, fabsf(c[i]));
+      key[i] = first + i >= E ? 0 : key_of(p.bias ? c[i] : l[i]);
+    }
+    if (p.groups > 1) {
+      // a score is off by 2^-23 (sigmoid), or by (V + 22) 2^-24 of the largest there is (softmax), a sum of two by twice that;
+      // c and the sum are rounded
+      const float off = (sigmoid ? 0x1.1p-21f : (V + 22) * 0x1p-22f * inv) + 0x1p-21f * warp_max(largest);
+      const int size = E / p.groups, step = size / V;
+      float value;
+      int mine, rank;
+      bool have = true;
+      if (size % V == 0 && (step & (step - 1)) == 0) {  // a group has lanes of its own, a power of two of them
+        float a = -INFINITY, d = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (first + i < E && !(in >> ((first + i) / size) & 1)) key[i] = 0;
+        for (int i = 0; i < V; ++i) {
+          d = fmaxf(d, fminf(a, c[i]));
+          a = fmaxf(a, c[i]);
+        }
+        for (int o = 1; o < step; o <<= 1) {
+          const float a2 = __shfl_xor_sync(FULL, a, o), d2 = __shfl_xor_sync(FULL, d, o);
+          d = fmaxf(fmaxf(d, d2), fminf(a, a2));
+          a = fmaxf(a, a2);
+        }
+        value = size > 1 ? a + d : a;
+        mine = lane / step;
+        have = mine < p.groups;
+        rank = rank_of(value, mine, p.groups, step);
+        if (have && rank >= p.top_groups) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) key[i] = 0;
+        }
+      } else {  // through shared memory: lane g has group g
+        float* cf = reinterpret_cast<float*>(buf);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (first + i < E) cf[first + i] = c[i];
+        __syncwarp();
+        have = lane < p.groups;
+        mine = lane;
+        value = have ? group_value(cf + lane * size, size, lane % size) : 0.0f;
+        rank = rank_of(value, mine, p.groups, 1);
+        const uint32_t in = __ballot_sync(FULL, have && rank < p.top_groups);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (first + i < E && !(in >> ((first + i) / size) & 1)) key[i] = 0;
+      }
+      bad |= have && value != value;
+      // the last group taken and the first that is not
+      const uint32_t at_last = __ballot_sync(FULL, have && rank == p.top_groups - 1);
+      const uint32_t at_next = __ballot_sync(FULL, have && rank == p.top_groups);
+      if (at_next) {
+        const float a = __shfl_sync(FULL, value, __ffs(at_last) - 1), d = __shfl_sync(FULL, value, __ffs(at_next) - 1);
+        sure_groups = a - d > off || (a == d && isinf(a));
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = first + i >= E ? 0 : key_of(l[i]);
   }
-  // the k largest, and the one behind them
+  // the k largest, and with a bias the one behind them
   uint32_t best = 0;
   int at = 0;
   auto find = [&] {
     best = key[0];
-    at = 0;
+    at = first;
 #pragma unroll
     for (int i = 1; i < V; ++i)
-      if (key[i] > best) { best = key[i]; at = i; }
+      if (key[i] > best) { best = key[i]; at = first + i; }
   };
   find();
-  uint32_t mine = 0, next = 0;  // keys of the lane's expert and of the one behind it
-  int id = 0, next_id = 0;
-  for (int j = 0; j <= k; ++j) {
+  uint32_t mine = 0, behind = 0;  // key of the lane's expert; of the one behind the last
+  int id = 0;
+  auto round = [&](int& e) {
     const uint32_t top = __reduce_max_sync(FULL, best);
-    const int owner = __ffs(__ballot_sync(FULL, best == top)) - 1;  // of equal ones the lowest lane has the lowest numbers
-    const int e = __shfl_sync(FULL, first + at, owner);
+    e = __shfl_sync(FULL, at, __ffs(__ballot_sync(FULL, best == top)) - 1);  // of equal ones the lowest lane has the lowest numbers
+    return top;
+  };
+  for (int j = 0; j < k; ++j) {
+    int e;
+    const uint32_t top = round(e);
     if (lane == j) { mine = top; id = e; }
-    if (lane == j - 1) { next = top; next_id = e; }
-    if (lane == owner) {
+    if (e == at) {  // numbers are one lane's each
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (i == at) key[i] = 0;
+        if (first + i == at) key[i] = 0;
       find();
     }
   }
-  float x = lane < k ? logit<WIDE>(row, id) : 0.0f;
-  float s = lane < k ? score(x) : 0.0f;
-  if (p.bias && lane < k && next) {
-    const float x2 = logit<WIDE>(row, next_id), s2 = score(x2);
-    const float c1 = of_key(mine), c2 = of_key(next);
-    const bool equal = (x == x2 && p.bias[id] == p.bias[next_id]) || (c1 == c2 && isinf(c1));
-    const float u1 = fmaxf(s, 0x1p-126f), u2 = fmaxf(s2, 0x1p-126f);
-    float off = (u1 + u2) * 0x1p-21f + 0x1p-23f * (fabsf(c1) + fabsf(c2));
-    if (!SIGMOID) off += 0x1p-18f * fabsf(s - s2) - 0x1p-23f * (u1 * __logf(u1) + u2 * __logf(u2));
-    if (!equal && !(c1 - c2 > off)) sure = false;
+  const bool has = lane < k;
+  float x = has ? logit(row, wide, id) : 0.0f;
+  float s = has ? score(x) : 0.0f;
+  bool ordered = true;  // within the k
+  float border = 0.0f;  // how far off the difference of the k-th and another may be
+  if (p.bias) {
+    int e;
+    behind = round(e);
+    const float b = has ? p.bias[id] : 0.0f, c1 = of_key(mine);
+    const float x2 = __shfl_down_sync(FULL, x, 1), s2 = __shfl_down_sync(FULL, s, 1), b2 = __shfl_down_sync(FULL, b, 1);
+    const uint32_t next = __shfl_down_sync(FULL, mine, 1);
+    const float u1 = fmaxf(s, 0x1p-126f), own = sigmoid ? 0x1p-23f * u1 * (2.01f - u1) : 0x1.7p-22f * u1 - 0x1p-23f * u1 * __logf(u1);
+    const float own2 = __shfl_down_sync(FULL, own, 1);
+    if (lane < k - 1) {
+      const float c2 = of_key(next), rounding = 0x1.01p-24f * (fabsf(c1) + fabsf(c2));
+      const bool equal = (x == x2 && b == b2) || (c1 == c2 && isinf(c1));
+      const float off = own + own2 + rounding + (sigmoid ? 0.0f : (V + 14) * 0x1p-24f * fabsf(s - s2));
+      ordered = equal || c1 - c2 > off;
+    } else if (lane == k - 1 && behind) {  // against any that was not chosen: a score of the largest there is
+      const float c2 = of_key(behind);
+      border = own + (sigmoid ? 0x1.1p-23f : (V + 22) * 0x1p-24f * inv) + 0x1p-22f * fabsf(c1) + 0x1p-23f * fabsf(c2) + 0x1p-125f;
+      sure = c1 - c2 > border || (c1 == c2 && isinf(c1));
+    }
   }
-  if (!__all_sync(FULL, sure)) {
-    id = route_exactly<WIDE, SIGMOID>(p, row, buf);
-    x = lane < k ? logit<WIDE>(row, id) : 0.0f;
-    s = lane < k ? score(x) : 0.0f;
+  int place = lane;
+  const bool spoilt = __any_sync(FULL, bad);
+  bool again = __any_sync(FULL, !sure || !sure_groups);
+  if (again && !spoilt) {
+    // Equal by their inputs?  Then numbers decide, as they did: all logits (no bias), or all experts as near to the k-th
+    // as their scores are off.
+    if (!p.bias) {
+      float least = INFINITY, high = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (first + i < E) least = fminf(least, l[i]), high = fmaxf(high, l[i]);
+      again = warp_max(high) != -warp_max(-least);
+    } else if (__all_sync(FULL, sure_groups)) {
+      const float xk = __shfl_sync(FULL, x, k - 1), ck = of_key(__shfl_sync(FULL, mine, k - 1));
+      const float bk = p.bias[__shfl_sync(FULL, id, k - 1)], off = __shfl_sync(FULL, border, k - 1);
+      bool equal = true;
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (key[i] && !(ck - of_key(key[i]) > off)) equal = equal && l[i] == xk && p.bias[first + i] == bk;
+      again = !__all_sync(FULL, equal);
+    }
+  }
+  if (again && !spoilt) {
+    bool close_enough;
+    id = route_closely(p, row, most, buf, &close_enough);
+    if (!close_enough) id = route_exactly(p, row, buf);
+    x = has ? logit(row, wide, id) : 0.0f;
+    s = has ? score(x) : 0.0f;
+  } else if (!__all_sync(FULL, ordered) && !spoilt) {
+    bool fine;
+    place = order_closely(p, row, most, id, x, &fine);
+    if (!fine) {
+      id = route_exactly(p, row, buf);
+      place = lane;
+      x = has ? logit(row, wide, id) : 0.0f;
+      s = has ? score(x) : 0.0f;
+    }
   }
   const float total = p.renorm ? warp_sum(s) + 1e-20f : 1.0f;
-  if (lane < k) {
-    p.ids[t * k + lane] = id;
-    p.weights[t * k + lane] = p.scale * (s / total);
+  if (!has) return;
+  float w = p.scale * (s / total);
+  if (spoilt) {  // no order: the first k, and weights that say so
+    id = place = lane;
+    w = __uint_as_float(0x7FC00000u);
   }
+  p.ids[t * k + place] = id;
+  p.weights[t * k + place] = w;
 }
 
 struct RouteBwdParams {
@@ -299,7 +638,8 @@ struct RouteBwdParams {
   const int32_t* ids;     // [T, k]
   int64_t T;
   int32_t E, k;
-  int renorm;
+  int wide, sigmoid, renorm;
+  int vec;                // rows of logits and dlogits can be read and written in vectors
   float scale;
   void* dlogits;          // [T, E], the logits' type
   int32_t* err;
@@ -315,15 +655,16 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_bwd_kernel(RouteBw
   const int64_t t = (int64_t)blockIdx.x * ROUTE_WARPS + warp;
   if (t >= p.T) return;
   const int E = p.E, k = p.k, first = lane * V;
-  const void* row = reinterpret_cast<const uint8_t*>(p.logits) + (size_t)t * E * (WIDE ? 4 : 2);
+  constexpr bool sigmoid = SIGMOID, wide = WIDE;
+  const void* row = reinterpret_cast<const uint8_t*>(p.logits) + (size_t)t * E * (wide ? 4 : 2);
+  int id = lane < k ? p.ids[t * k + lane] : -1;
+  const float dw = lane < k ? p.dweights[t * k + lane] : 0.0f;
   float l[V];
+  load_values<V>(row, wide, p.vec, first, E, -INFINITY, l);
   float most = -INFINITY, z = 0.0f, inv = 1.0f;
+  if (!sigmoid) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    l[i] = first + i < E ? logit<WIDE>(row, first + i) : -INFINITY;
-    most = fmaxf(most, l[i]);
-  }
-  if (!SIGMOID) {
+    for (int i = 0; i < V; ++i) most = fmaxf(most, l[i]);
     most = warp_max(most);
     if (most == -INFINITY) most = 0.0f;
 #pragma unroll
@@ -331,14 +672,12 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_bwd_kernel(RouteBw
     z = warp_sum(z);
     inv = z != 0.0f ? 1.0f / z : 0.0f;
   }
-  int id = lane < k ? p.ids[t * k + lane] : -1;
-  const float dw = lane < k ? p.dweights[t * k + lane] : 0.0f;
   if (lane < k && (id < 0 || id >= E)) {
     record_error(p.err, MX_ERR_BAD_OFFSETS);
     id = -1;
   }
-  const float x = id >= 0 ? logit<WIDE>(row, id) : 0.0f;
-  const float s = id < 0 ? 0.0f : SIGMOID ? 1.0f / (1.0f + expf(-x)) : expf(x - most) * inv;
+  const float x = id >= 0 ? logit(row, wide, id) : 0.0f;
+  const float s = id < 0 ? 0.0f : sigmoid ? 1.0f / (1.0f + expf(-x)) : expf(x - most) * inv;
   float ds = p.scale * dw, back = 0.0f;  // back: sum ds s
   const float dot = warp_sum(id >= 0 ? dw * s : 0.0f);
   if (p.renorm) {
@@ -352,26 +691,70 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_bwd_kernel(RouteBw
 #pragma unroll
   for (int i = 0; i < V; ++i) out[i] = 0.0f;
   for (int j = 0; j < k; ++j) {
-    const int e = __shfl_sync(FULL, id, j);
+    const int e = __shfl_sync(FULL, id, j) - first;
     const float v = __shfl_sync(FULL, ds, j);
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (e == first + i) out[i] += v;
+      if (e == i) out[i] += v;
   }
-  uint8_t* dst = reinterpret_cast<uint8_t*>(p.dlogits) + (size_t)t * E * (WIDE ? 4 : 2);
+  if (first >= E) return;
+  uint8_t* dst = reinterpret_cast<uint8_t*>(p.dlogits) + (size_t)t * E * (wide ? 4 : 2);
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    if (first + i >= E) break;
-    float d;
-    if (SIGMOID) {
+    if (sigmoid) {
       const float q = expf(-fabsf(l[i]));  // s (1 - s) = q / (1 + q)^2
-      d = out[i] == 0.0f ? 0.0f : out[i] * (q / ((1.0f + q) * (1.0f + q)));
+      out[i] = out[i] == 0.0f ? 0.0f : out[i] * (q / ((1.0f + q) * (1.0f + q)));
     } else {
-      d = expf(l[i] - most) * inv * (out[i] - back);
+      out[i] = expf(l[i] - most) * inv * (out[i] - back);
     }
-    if (WIDE) reinterpret_cast<float*>(dst)[first + i] = d;
-    else reinterpret_cast<uint16_t*>(dst)[first + i] = (uint16_t)f32_to_bf16_bits(d);
   }
+  if (p.vec && wide && V >= 4) {
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i)
+      reinterpret_cast<float4*>(dst)[first / 4 + i] = make_float4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]);
+  } else if (p.vec && !wide && V >= 8) {
+#pragma unroll
+    for (int i = 0; i < V / 8; ++i)
+      reinterpret_cast<uint4*>(dst)[first / 8 + i] =
+          make_uint4(f2_to_bf16x2(f2_pack(out[8 * i], out[8 * i + 1])), f2_to_bf16x2(f2_pack(out[8 * i + 2], out[8 * i + 3])),
+                     f2_to_bf16x2(f2_pack(out[8 * i + 4], out[8 * i + 5])), f2_to_bf16x2(f2_pack(out[8 * i + 6], out[8 * i + 7])));
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (first + i >= E) break;
+      if (wide) reinterpret_cast<float*>(dst)[first + i] = out[i];
+      else reinterpret_cast<uint16_t*>(dst)[first + i] = (uint16_t)f32_to_bf16_bits(out[i]);
+    }
+  }
+}
+
+// f(width, wide, sigmoid) for the kernel of these.
+template <class F>
+cudaError_t for_kernel(int v, bool wide, bool sigmoid, F&& f) {
+  auto kinds = [&](auto w) {
+    using Yes = std::true_type;
+    using No = std::false_type;
+    return wide ? (sigmoid ? f(w, Yes{}, Yes{}) : f(w, Yes{}, No{})) : (sigmoid ? f(w, No{}, Yes{}) : f(w, No{}, No{}));
+  };
+  switch (v) {
+    case 1: return kinds(std::integral_constant<int, 1>{});
+    case 2: return kinds(std::integral_constant<int, 2>{});
+    case 4: return kinds(std::integral_constant<int, 4>{});
+    case 8: return kinds(std::integral_constant<int, 8>{});
+    case 16: return kinds(std::integral_constant<int, 16>{});
+    default: return kinds(std::integral_constant<int, 32>{});
+  }
+}
+int route_width(int E) {
+  int v = 1;
+  while (32 * v < E) v *= 2;
+  return v;
+}
+
+// Rows of E values of `size` bytes can be read V at a time, in vectors of 16 bytes at most.
+bool in_vectors(const void* p, int E, int size, int v) {
+  const int bytes = std::min(16, v * size);
+  return E % v == 0 && (int64_t)E * size % bytes == 0 && reinterpret_cast<uintptr_t>(p) % bytes == 0;
 }
 
 // ---------------------------------------------------------------- grouping
@@ -408,50 +791,79 @@ __global__ void __launch_bounds__(TG_WARPS * 32)
   for (int e = threadIdx.x; e < E; e += blockDim.x) counts[(int64_t)blockIdx.x * E + e] = hist[e];
 }
 
-// Each CTA adds up the chunks before its own and all of them, and places its rows: a row's place is its group's start,
-// plus the group's rows in chunks before, in warps before, in earlier steps of the warp and in lower lanes.
-__global__ void __launch_bounds__(TG_WARPS * 32)
+// A row's place is its group's start, plus the group's rows in chunks before, in warps before, in earlier steps of the
+// warp and in lower lanes.  Each CTA adds up the counts of the chunks before its own and of all; alone it needs none.
+// ITER: steps of a warp's 32 rows, kept in registers; 0: any number, walked twice.
+template <int WARPS, int ITER>
+__global__ void __launch_bounds__(WARPS * 32)
     token_group_place_kernel(const int32_t* __restrict__ expert_of, int64_t R, int32_t E, int64_t chunk,
                              const int32_t* __restrict__ counts, int32_t* __restrict__ offs,
                              int32_t* __restrict__ row_dst, int32_t* __restrict__ row_src, int32_t* err) {
   extern __shared__ int32_t sm[];
-  int32_t* next = sm;              // [TG_WARPS][E]
-  int32_t* total = sm + TG_WARPS * E;  // [E], then the groups' ends
-  __shared__ int32_t warp_total[TG_WARPS];
+  int32_t* next = sm;                  // [WARPS][E]
+  int32_t* total = sm + WARPS * E;     // [E], then the groups' ends
+  int32_t* before = total + E;         // [E]
+  __shared__ int32_t warp_total[WARPS];
   pdl_begin();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n_chunks = gridDim.x, mine = blockIdx.x;
-  const int64_t c0 = mine * chunk, c1 = min(R, c0 + chunk), share = chunk / TG_WARPS;
+  const int64_t c0 = mine * chunk, c1 = min(R, c0 + chunk), share = chunk / WARPS;
   const int64_t w0 = min(c1, c0 + warp * share), w1 = min(c1, w0 + share);
   int32_t* h = next + warp * E;
-  for (int e = tid; e < TG_WARPS * E; e += blockDim.x) next[e] = 0;
+  int32_t ex[ITER + 1], pos[ITER + 1];
+#pragma unroll
+  for (int i = 0; i < ITER; ++i) {
+    const int64_t r = w0 + i * 32 + lane;
+    ex[i] = r < w1 ? expert_of[r] : -1;
+  }
+  for (int e = tid; e < (WARPS + 2) * E; e += WARPS * 32) sm[e] = 0;
   __syncthreads();
-  walk(expert_of, w0, w1, E, [&](int64_t, int32_t e, unsigned peers) {
-    if (e >= 0 && lane == __ffs(peers) - 1) h[e] += __popc(peers);
-    __syncwarp();
-  });
-  __syncthreads();
-  for (int e = tid; e < E; e += blockDim.x) {
-    int32_t before = 0, all = 0;
-    if (n_chunks > 1) {
-      for (int c = 0; c < n_chunks; ++c) {
+  if (n_chunks > 1) {
+    // threads side by side take experts, and as many threads as there are for each share the chunks
+    const int parts = max(1, WARPS * 32 / E);
+    for (int i = tid; i < parts * E; i += WARPS * 32) {
+      const int e = i % E;
+      int32_t all = 0, b = 0;
+#pragma unroll 8
+      for (int c = i / E; c < n_chunks; c += parts) {
         const int32_t n = counts[(int64_t)c * E + e];
         all += n;
-        if (c < mine) before += n;
+        b += c < mine ? n : 0;
       }
-    } else {
-      for (int w = 0; w < TG_WARPS; ++w) all += next[w * E + e];
+      atomicAdd(&total[e], all);
+      atomicAdd(&before[e], b);
     }
-    total[e] = all;
-    for (int w = 0; w < TG_WARPS; ++w) {
+  }
+  if (ITER) {
+#pragma unroll
+    for (int i = 0; i < ITER; ++i) {
+      if (ex[i] >= E) ex[i] = -1;
+      const unsigned peers = __match_any_sync(FULL, ex[i] >= 0 ? ex[i] : -1 - lane);
+      pos[i] = ex[i] >= 0 ? h[ex[i]] + __popc(peers & ((1u << lane) - 1u)) : 0;
+      __syncwarp();
+      if (ex[i] >= 0 && lane == __ffs(peers) - 1) h[ex[i]] += __popc(peers);
+      __syncwarp();
+    }
+  } else {
+    walk(expert_of, w0, w1, E, [&](int64_t, int32_t e, unsigned peers) {
+      if (e >= 0 && lane == __ffs(peers) - 1) h[e] += __popc(peers);
+      __syncwarp();
+    });
+  }
+  __syncthreads();
+  for (int e = tid; e < E; e += WARPS * 32) {
+    int32_t run = before[e];
+#pragma unroll 8
+    for (int w = 0; w < WARPS; ++w) {
       const int32_t n = next[w * E + e];
-      next[w * E + e] = before;
-      before += n;
+      next[w * E + e] = run;
+      run += n;
     }
+    if (n_chunks == 1) total[e] = run;
   }
   __syncthreads();
   // ends of the groups: each thread adds up neighbours, then the threads before it
-  const int per = (E + blockDim.x - 1) / blockDim.x, e0 = tid * per;
+  const int per = (E + WARPS * 32 - 1) / (WARPS * 32), e0 = tid * per;
   int32_t sum = 0;
   for (int i = 0; i < per && e0 + i < E; ++i) sum += total[e0 + i];
   int32_t run = sum;
@@ -466,7 +878,7 @@ __global__ void __launch_bounds__(TG_WARPS * 32)
   for (int w = 0; w < warp; ++w) run += warp_total[w];
   for (int i = 0; i < per && e0 + i < E; ++i) {
     const int32_t n = total[e0 + i];
-    for (int w = 0; w < TG_WARPS; ++w) next[w * E + e0 + i] += run;
+    before[e0 + i] = run;   // now the group's start
     run += n;
     total[e0 + i] = run;
     if (mine == 0) offs[e0 + i] = run;
@@ -474,74 +886,58 @@ __global__ void __launch_bounds__(TG_WARPS * 32)
   __syncthreads();
   const int32_t placed = total[E - 1];
   bool bad = false;
-  walk(expert_of, w0, w1, E, [&](int64_t r, int32_t e, unsigned peers) {
-    const int32_t pos = e >= 0 ? h[e] + __popc(peers & ((1u << lane) - 1u)) : -1;
-    __syncwarp();
-    if (e >= 0 && lane == __ffs(peers) - 1) h[e] += __popc(peers);
-    __syncwarp();
-    if (r < w1) {
-      row_dst[r] = pos;
-      if (e >= 0) row_src[pos] = (int32_t)r;
-      else bad = true;
-      if (r >= placed) row_src[r] = -1;
+  auto put = [&](int64_t r, int32_t e, int32_t at) {
+    row_dst[r] = at;
+    if (e >= 0) row_src[at] = (int32_t)r;
+    else bad = true;
+    if (r >= placed) row_src[r] = -1;
+  };
+  if (ITER) {
+#pragma unroll
+    for (int i = 0; i < ITER; ++i) {
+      const int64_t r = w0 + i * 32 + lane;
+      if (r < w1) put(r, ex[i], ex[i] >= 0 ? before[ex[i]] + h[ex[i]] + pos[i] : -1);
     }
-  });
+  } else {
+    walk(expert_of, w0, w1, E, [&](int64_t r, int32_t e, unsigned peers) {
+      const int32_t at = e >= 0 ? before[e] + h[e] + __popc(peers & ((1u << lane) - 1u)) : -1;
+      __syncwarp();
+      if (e >= 0 && lane == __ffs(peers) - 1) h[e] += __popc(peers);
+      __syncwarp();
+      if (r < w1) put(r, e, at);
+    });
+  }
   if (__any_sync(FULL, bad) && lane == 0) record_error(err, MX_ERR_BAD_OFFSETS);
-}
-
-int64_t group_chunk(int64_t R) {
-  const int64_t most = 2 * (int64_t)num_sms();
-  const int64_t c = std::max<int64_t>(1024, (R + most - 1) / most);
-  return (c + 32 * TG_WARPS - 1) / (32 * TG_WARPS) * (32 * TG_WARPS);
-}
-
-template <int V, bool WIDE>
-cudaError_t route_v(const RouteLaunch& a, cudaStream_t stream) {
-  RouteParams p{};
-  p.logits = a.logits; p.bias = a.bias; p.T = a.T; p.E = a.E; p.k = a.k; p.groups = a.groups; p.top_groups = a.top_groups;
-  p.renorm = a.renorm; p.scale = a.scale; p.ids = a.ids; p.weights = a.weights;
-  const size_t smem = (size_t)ROUTE_WARPS * a.E * 8;
-  const unsigned grid = (unsigned)((a.T + ROUTE_WARPS - 1) / ROUTE_WARPS);
-  auto kern = a.score == MX_SCORE_SIGMOID ? moe_route_kernel<V, WIDE, true> : moe_route_kernel<V, WIDE, false>;
-  return launch_overlapped(kern, grid, ROUTE_WARPS * 32, smem, stream, 1, p);
-}
-
-template <int V, bool WIDE>
-cudaError_t route_bwd_v(const RouteBwdLaunch& a, cudaStream_t stream) {
-  RouteBwdParams p{};
-  p.dweights = a.dweights; p.logits = a.logits; p.ids = a.ids; p.T = a.T; p.E = a.E; p.k = a.k; p.renorm = a.renorm;
-  p.scale = a.scale; p.dlogits = a.dlogits; p.err = a.err;
-  const unsigned grid = (unsigned)((a.T + ROUTE_WARPS - 1) / ROUTE_WARPS);
-  auto kern = a.score == MX_SCORE_SIGMOID ? moe_route_bwd_kernel<V, WIDE, true> : moe_route_bwd_kernel<V, WIDE, false>;
-  return launch_overlapped(kern, grid, ROUTE_WARPS * 32, 0, stream, 1, p);
 }
 
 }  // namespace
 
 int launch_moe_route(const RouteLaunch& a, cudaStream_t stream) {
+  const int v = route_width(a.E);
+  RouteParams p{};
+  p.logits = a.logits; p.bias = a.bias; p.T = a.T; p.E = a.E; p.k = a.k; p.groups = a.groups; p.top_groups = a.top_groups;
+  p.wide = a.wide; p.sigmoid = a.score == MX_SCORE_SIGMOID; p.renorm = a.renorm; p.scale = a.scale; p.ids = a.ids;
+  p.weights = a.weights;
+  p.vec = in_vectors(a.logits, a.E, a.wide ? 4 : 2, v);
+  p.vec_bias = in_vectors(a.bias, a.E, 4, v);
   count_launch(MX_KERNEL_ROUTE);
-  auto go = [&](auto f16, auto f32) { return a.wide ? f32(a, stream) : f16(a, stream); };
-  cudaError_t e;
-  if (a.E <= 32) e = go(route_v<1, false>, route_v<1, true>);
-  else if (a.E <= 64) e = go(route_v<2, false>, route_v<2, true>);
-  else if (a.E <= 128) e = go(route_v<4, false>, route_v<4, true>);
-  else if (a.E <= 256) e = go(route_v<8, false>, route_v<8, true>);
-  else if (a.E <= 512) e = go(route_v<16, false>, route_v<16, true>);
-  else e = go(route_v<32, false>, route_v<32, true>);
-  return cuda_status(e, "moe_route_kernel launch");
+  return cuda_status(for_kernel(v, a.wide, p.sigmoid, [&](auto w, auto wide, auto sigmoid) {
+    return launch_overlapped(moe_route_kernel<decltype(w)::value, decltype(wide)::value, decltype(sigmoid)::value>, (unsigned)((a.T + ROUTE_WARPS - 1) / ROUTE_WARPS),
+                             ROUTE_WARPS * 32, (size_t)ROUTE_WARPS * a.E * 8, stream, 1, p);
+  }), "moe_route_kernel launch");
 }
 
 int launch_moe_route_bwd(const RouteBwdLaunch& a, cudaStream_t stream) {
+  const int v = route_width(a.E);
+  RouteBwdParams p{};
+  p.dweights = a.dweights; p.logits = a.logits; p.ids = a.ids; p.T = a.T; p.E = a.E; p.k = a.k; p.wide = a.wide;
+  p.sigmoid = a.score == MX_SCORE_SIGMOID; p.renorm = a.renorm; p.scale = a.scale; p.dlogits = a.dlogits; p.err = a.err;
+  p.vec = in_vectors(a.logits, a.E, a.wide ? 4 : 2, v) && in_vectors(a.dlogits, a.E, a.wide ? 4 : 2, v);
   count_launch(MX_KERNEL_ROUTE);
-  auto go = [&](auto f16, auto f32) { return a.wide ? f32(a, stream) : f16(a, stream); };
-  cudaError_t e;
-  if (a.E <= 32) e = go(route_bwd_v<1, false>, route_bwd_v<1, true>);
-  else if (a.E <= 64) e = go(route_bwd_v<2, false>, route_bwd_v<2, true>);
-  else if (a.E <= 128) e = go(route_bwd_v<4, false>, route_bwd_v<4, true>);
-  else if (a.E <= 256) e = go(route_bwd_v<8, false>, route_bwd_v<8, true>);
-  else if (a.E <= 512) e = go(route_bwd_v<16, false>, route_bwd_v<16, true>);
-  else e = go(route_bwd_v<32, false>, route_bwd_v<32, true>);
-  return cuda_status(e, "moe_route_bwd_kernel launch");
+  return cuda_status(for_kernel(v, a.wide, p.sigmoid, [&](auto w, auto wide, auto sigmoid) {
+    return launch_overlapped(moe_route_bwd_kernel<decltype(w)::value, decltype(wide)::value, decltype(sigmoid)::value>, (unsigned)((a.T + ROUTE_WARPS - 1) / ROUTE_WARPS),
+                             ROUTE_WARPS * 32, 0, stream, 1, p);
+  }), "moe_route_bwd_kernel launch");
 }
 
 size_t token_group_workspace(int64_t R, int32_t E) {
@@ -551,19 +947,32 @@ size_t token_group_workspace(int64_t R, int32_t E) {
 
 int launch_token_group(const int32_t* expert_of, int64_t R, int32_t E, int32_t* offs, int32_t* row_dst, int32_t* row_src,
                        void* workspace, int32_t* err, cudaStream_t stream) {
-  const int64_t chunk = group_chunk(R);
-  const unsigned grid = (unsigned)((R + chunk - 1) / chunk);
   int32_t* counts = reinterpret_cast<int32_t*>(workspace);
-  cudaError_t e;
+  auto place = [&](auto k, unsigned grid, int warps, int64_t chunk) {
+    count_launch(MX_KERNEL_DISPATCH);
+    return cuda_status(launch_overlapped(k, grid, warps * 32, (size_t)(warps + 2) * E * 4, stream, 1, expert_of, R, E, chunk,
+                                         (const int32_t*)counts, offs, row_dst, row_src, err),
+                       "token_group_place_kernel launch");
+  };
+  // up to 8192 rows one large CTA, if its warps' counts fit 48 KB; else the chunks are counted first
+  if (R <= 8192 && E <= 352) {
+    if (R <= 1024) return place(token_group_place_kernel<32, 1>, 1, 32, 1024);
+    if (R <= 2048) return place(token_group_place_kernel<32, 2>, 1, 32, 2048);
+    if (R <= 4096) return place(token_group_place_kernel<32, 4>, 1, 32, 4096);
+    return place(token_group_place_kernel<32, 8>, 1, 32, 8192);
+  }
+  // chunks of 1024 rows while each SM has two of them at most, larger ones else: a CTA reads every chunk's counts
+  const int64_t most = 2 * (int64_t)num_sms();
+  const int64_t chunk = std::max<int64_t>(1024, ((R + most - 1) / most + 255) / 256 * 256);
+  const unsigned grid = (unsigned)((R + chunk - 1) / chunk);
   if (grid > 1) {
     count_launch(MX_KERNEL_DISPATCH);
-    e = launch_overlapped(token_group_count_kernel, grid, TG_WARPS * 32, (size_t)E * 4, stream, 1, expert_of, R, E, chunk, counts);
+    const cudaError_t e = launch_overlapped(token_group_count_kernel, grid, TG_WARPS * 32, (size_t)E * 4, stream, 1, expert_of, R, E,
+                                            chunk, counts);
     if (e != cudaSuccess) return cuda_status(e, "token_group_count_kernel launch");
   }
-  count_launch(MX_KERNEL_DISPATCH);
-  e = launch_overlapped(token_group_place_kernel, grid, TG_WARPS * 32, (size_t)(TG_WARPS + 1) * E * 4, stream, 1, expert_of, R,
-                        E, chunk, (const int32_t*)counts, offs, row_dst, row_src, err);
-  return cuda_status(e, "token_group_place_kernel launch");
+  return chunk == 1024 ? place(token_group_place_kernel<TG_WARPS, 4>, grid, TG_WARPS, chunk)
+                       : place(token_group_place_kernel<TG_WARPS, 0>, grid, TG_WARPS, chunk);
 }
 
 }  // namespace mx
