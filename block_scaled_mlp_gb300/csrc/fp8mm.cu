@@ -4,13 +4,22 @@
 //   FWD    out[t, n] = sum_b sx[b, t] sw[e, n / 128, b] sum_{k in block b} x[t, k] w[e, n, k]
 //   DGRAD  dx[t, k]  = sum_b sd[b, t] sw[e, b, k / 128] sum_{n in block b} dout[t, n] w[e, n, k]
 //
-// (DGRAD reads the transposed codes, so both are one kernel: features F, contraction C.)  The inner sums are tensor core
+// (DGRAD reads the transposed codes, so both are one product: features F, contraction C.)  The inner sums are tensor core
 // products (tcgen05, kind::f8f6f4) of 128 elements, each into an accumulator of its own in TMEM; the epilogue warps
 // bring it out, multiply it by its scales in fp32 and add it to sums in registers.  One rounding to bf16 at the end.
 //
-// Tokens are the N side of the MMA (any multiple of 32 at run time) and features the M side (256 per CTA pair), as in
-// ragged.cu: a group's last tile costs what its rows cost, and a CTA's 128 features are one block of the weight's
-// scales, so that a K block's scale of a token is one number for the CTA: a warp forms sx sw ahead of the epilogue.
+// What that bounds: an accumulator of 128 x 256 is 128 KB to be read and 32768 FMAs to be done in the 512 cycles that its
+// MMAs take, and its columns are free for the next but one only when both CTAs of a pair have read them.  So there are
+// two kernels.
+//   Many rows a group: tokens on the M side, so that a lane of the epilogue has one token and a K block's scale is
+// one number for it (with tokens on the N side a scale a column comes from shared memory, which the MMAs' operands
+// fill already: 715 against 413 us for 8192 x 4096 x 14336 at the first build of both).  CTA pairs, 256 x 256.
+//   Few rows: tokens on the N side (any multiple of 32 at run time), features on the M side, so that a group's last tile
+// costs what its rows cost; one CTA a tile, or several that share its contraction.
+//
+// On a GB300 (twice the bf16 library rate: 3.9 PFLOP/s; copies 6.78 TB/s): 8192 x 4096 x 14336 310 us (3.1 PFLOP/s; 2.65 in
+// long runs, by the power limit), 131072 rows over 64 experts of 4096 x 7168 both ways 6.15 ms (2.5 PFLOP/s); 64 rows over 64
+// of them, 31 hit, 147 us (6.2 TB/s of weights); 8 rows of 4096 x 7168 9.8 us.
 #include <atomic>
 #include <type_traits>
 
@@ -23,27 +32,30 @@ namespace {
 
 constexpr int FM_EPI = 8;                 // epilogue warps
 constexpr int FM_MAX_E = 1024;
-constexpr int FM_F = 256;                 // features per pair tile
 constexpr int FM_THREADS = 128 + FM_EPI * 32;
 constexpr int FM_REGS = 168;              // a thread at launch; 56 + 2 * 224 = 3 * 168 after the split
 
-// BT: columns of a token tile.
-template <int BT>
+// A CTA has 128 features; BT: columns of a token tile; S: CTAs that share a tile's contraction.
+template <int BT, int S>
 struct FCfg {
   static constexpr int A_BYTES = 128 * 128;              // 128 features x 128 contraction elements
-  static constexpr int B_BYTES = (BT / 2) * 128;         // this CTA's half of the tile
+  static constexpr int B_BYTES = BT * 128;
   static constexpr int TX = A_BYTES + B_BYTES;
   static constexpr int EPI_BYTES = FM_EPI * 2048;        // a warp's 32 x 32 bf16 block
   static constexpr int TABLE = FM_MAX_E * 8;             // group ends and running unit numbers
   static constexpr int SLOTS = 8;                        // K blocks whose scales are ready
   static constexpr int SC_BYTES = SLOTS * BT * 4;
+  static constexpr int PART = BT * 128 * 4;              // one CTA's sums
+  static constexpr int PARTS = (S - 1) * PART;           // in a tile's first CTA: the others'
   static constexpr int BUFS = 4;                         // accumulators
   static constexpr int TMEM = BUFS * BT;
-  static constexpr uint32_t IDESC = (1u << 4) | ((uint32_t)(FM_F >> 4) << 24);
-  static constexpr int STAGES = (226 * 1024 - EPI_BYTES - SC_BYTES - TABLE - 1536) / TX;
-  static constexpr size_t SMEM = (size_t)STAGES * TX + EPI_BYTES + SC_BYTES + TABLE + 512 /*barriers*/ + 1024 /*align*/;
-  static_assert(BT == 128 || BT == 32, "tile widths");
-  static_assert((2 * STAGES + 2 * BUFS + 2 * SLOTS + 2) * 8 <= 512, "barriers");
+  static constexpr uint32_t IDESC = (1u << 4) | ((128u >> 4) << 24);
+  static constexpr int STAGES = (226 * 1024 - EPI_BYTES - SC_BYTES - PARTS - TABLE - 1536) / TX;
+  static constexpr size_t SMEM = (size_t)STAGES * TX + EPI_BYTES + SC_BYTES + PARTS + TABLE + 512 /*barriers*/ + 1024 /*align*/;
+  static_assert(BT == 128 || BT == 64 || BT == 32, "tile widths");
+  static_assert(S == 1 || S == 2 || S == 4, "CTAs of a cluster");
+  static_assert(STAGES >= 3, "shared memory");
+  static_assert((2 * STAGES + 2 * BUFS + 2 * SLOTS + 2 + FM_EPI) * 8 <= 512, "barriers");
   static_assert(SMEM + 1024 /*static*/ <= 227 * 1024, "shared memory");
 };
 
@@ -63,7 +75,7 @@ MX_DEVINL void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
-// warp_wait and mbar_arrive by the barrier's shared memory address.
+// warp_wait by the barrier's shared memory address.
 MX_DEVINL bool mbar_try_wait_at(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -88,9 +100,6 @@ MX_DEVINL bool warp_wait_at(uint32_t bar, uint32_t parity, int32_t* err, bool do
   }
   return __all_sync(0xFFFFFFFFu, done);
 }
-MX_DEVINL void mbar_arrive_at(uint32_t bar) {
-  asm volatile("{\n .reg .b64 st;\n mbarrier.arrive.shared::cta.b64 st, [%0];\n}" ::"r"(bar) : "memory");
-}
 
 // acc += (a, b) s, where it stands: as a volatile statement it stays behind the TMEM load that was issued before it (left
 // to the compiler's order, 356 against 342 us).
@@ -100,6 +109,25 @@ MX_DEVINL void fma_here(f2& acc, uint32_t a, uint32_t b, float s) {
       " fma.rn.f32x2 z, x, y, z;\n mov.b64 {%0, %1}, z;\n}"
       : "+f"(acc.x), "+f"(acc.y)
       : "r"(a), "r"(b), "f"(s));
+}
+
+// Bounded wait for arrivals from other CTAs of the cluster, whose writes it makes visible.
+MX_DEVINL bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, int32_t* err) {
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      record_error(err, MX_ERR_TIMEOUT);
+      return false;
+    }
+  }
 }
 
 template <int R>
@@ -126,10 +154,11 @@ struct Unit {
   int32_t n_eff;    // tn rounded up to the MMA's multiple of 32
 };
 
-template <int BT>
+// Tiles of BT token rows and FT features.
+template <int BT, int FT>
 MX_DEVINL Unit unit_of(const MmParams& p, const int32_t* ends, const int32_t* unit_end, int32_t u) {
   Unit r;
-  const int32_t f_tiles = (p.F + FM_F - 1) / FM_F;
+  const int32_t f_tiles = (p.F + FT - 1) / FT;
   int lo = 0, hi = p.E - 1;  // first group whose unit_end is > u
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
@@ -149,7 +178,7 @@ MX_DEVINL Unit unit_of(const MmParams& p, const int32_t* ends, const int32_t* un
   }
   // narrow tiles: the group's rows shared out evenly, in multiples of 32
   const int32_t share = BT == 256 ? BT : ((rows + t_tiles - 1) / t_tiles + 31) & ~31;
-  r.f0 = f * FM_F;
+  r.f0 = f * FT;
   r.t0 = (int64_t)start + (int64_t)t * share;
   r.tn = min(share, rows - t * share);
   r.n_eff = (r.tn + 31) & ~31;
@@ -157,10 +186,10 @@ MX_DEVINL Unit unit_of(const MmParams& p, const int32_t* ends, const int32_t* un
 }
 
 // By one warp: group ends, checked, and the running number of work units.
-template <int BT>
+template <int BT, int FT>
 MX_DEVINL void read_ends(const MmParams& p, int32_t* ends, int32_t* unit_end, int* s_ok, int* s_units) {
   const int lane = threadIdx.x & 31;
-  const int32_t f_tiles = (p.F + FM_F - 1) / FM_F;
+  const int32_t f_tiles = (p.F + FT - 1) / FT;
   int32_t prev = 0, units = 0;
   bool ok = true;
   for (int base = 0; base < p.E; base += 32) {
@@ -216,51 +245,53 @@ MX_DEVINL void store_32b(uint8_t* dst, const f2* v) {
 
 // ---------------------------------------------------------------- tokens on the N side
 
-template <int BT>
+template <int BT, int S>
 __global__ void __launch_bounds__(FM_THREADS, 1)
     fp8_mm_narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, MmParams p) {
-  using C = FCfg<BT>;
+  using C = FCfg<BT, S>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
   uint8_t* sB = sA + C::STAGES * C::A_BYTES;
   uint8_t* sEpi = sB + C::STAGES * C::B_BYTES;
   float* sScale = reinterpret_cast<float*>(sEpi + C::EPI_BYTES);
-  int32_t* ends = reinterpret_cast<int32_t*>(sEpi + C::EPI_BYTES + C::SC_BYTES);
+  uint8_t* sParts = sEpi + C::EPI_BYTES + C::SC_BYTES;
+  int32_t* ends = reinterpret_cast<int32_t*>(sParts + C::PARTS);
   int32_t* unit_end = ends + FM_MAX_E;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sEpi + C::EPI_BYTES + C::SC_BYTES + C::TABLE);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sParts + C::PARTS + C::TABLE);
   uint64_t* empty = full + C::STAGES;
   uint64_t* acc_full = empty + C::STAGES;
   uint64_t* acc_empty = acc_full + C::BUFS;
   uint64_t* sc_full = acc_empty + C::BUFS;
   uint64_t* sc_empty = sc_full + C::SLOTS;
-  uint64_t* done_bar = sc_empty + C::SLOTS;
+  uint64_t* parts_bar = sc_empty + C::SLOTS;   // S > 1, by epilogue warp: the other pairs' sums are here
+  uint64_t* done_bar = parts_bar + FM_EPI;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done_bar + 1);
   __shared__ int s_ok, s_units;
 
   // by way of a shuffle the compiler knows it to be one number for the warp: without, the roles spill (24 bytes, read back
   // in their loops)
   const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int rank = (int)cluster_ctarank();
-  const int32_t unit0 = blockIdx.x / 2, ustep = gridDim.x / 2;
-  const int32_t num_kb = (p.C + 127) / 128;
+  const int part = S > 1 ? (int)cluster_ctarank() : 0;   // this CTA's share of the contraction
+  const int32_t unit0 = blockIdx.x / S, ustep = gridDim.x / S;
+  const int32_t kb0 = (p.C + 127) / 128 * part / S, num_kb = (p.C + 127) / 128 * (part + 1) / S - kb0;   // this CTA's K blocks
 
   if (threadIdx.x == 0) {
-    // the even CTA's full and acc_empty barriers serve the pair
     for (int s = 0; s < C::STAGES; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
-    for (int a = 0; a < C::BUFS; ++a) { mbar_init(&acc_full[a], 1); mbar_init(&acc_empty[a], 2 * FM_EPI); }
+    for (int a = 0; a < C::BUFS; ++a) { mbar_init(&acc_full[a], 1); mbar_init(&acc_empty[a], FM_EPI); }
     for (int s = 0; s < C::SLOTS; ++s) { mbar_init(&sc_full[s], 32); mbar_init(&sc_empty[s], FM_EPI); }
+    for (int e = 0; e < FM_EPI; ++e) mbar_init(&parts_bar[e], S > 1 ? 32 * (S - 1) : 1);
     mbar_init(done_bar, 1);
     fence_mbar_init();
   }
-  if (warp == 1) { tmem_alloc_pair(tmem_holder, C::TMEM); tmem_relinquish_pair(); }
+  if (warp == 1) { tmem_alloc(tmem_holder, C::TMEM); tmem_relinquish(); }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  cluster_sync();  // the peer's barriers exist before any remote arrive or pair copy
+  if (S > 1) cluster_sync();  // the others' barriers exist before any remote arrive
   const uint32_t tmem = *tmem_holder;
   pdl_begin();     // all of the above overlaps the kernel before
-  if (warp == 2) read_ends<BT>(p, ends, unit_end, &s_ok, &s_units);
+  if (warp == 2) read_ends<BT, 128>(p, ends, unit_end, &s_ok, &s_units);
   __syncthreads();
   const int32_t n_units = s_units;
 
@@ -276,16 +307,13 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
       int stage = 0; uint32_t phase = 0;
       bool ok = true;
       for (int32_t u = unit0; u < n_units && ok; u += ustep) {
-        const Unit t = unit_of<BT>(p, ends, unit_end, u);
-        const int32_t f = t.f0 + rank * 128;
-        const int32_t b0 = (int32_t)(t.t0 + rank * (t.n_eff / 2));
+        const Unit t = unit_of<BT, 128>(p, ends, unit_end, u);
         for (int kb = 0; kb < num_kb; ++kb) {
           if (!warp_wait(&empty[stage], phase ^ 1, p.err)) { ok = false; break; }
           if (leader) {
-            const uint32_t bar = cluster_map(smem_u32(&full[stage]), 0);
-            if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * C::TX);
-            tma_load_3d_pair(sA + stage * C::A_BYTES, &tmA, kb * 128, f, t.e, bar);
-            tma_load_2d_pair(sB + stage * C::B_BYTES, &tmB, kb * 128, b0, bar);
+            mbar_arrive_expect_tx(&full[stage], C::TX);
+            tma_load_3d(sA + stage * C::A_BYTES, &tmA, (kb0 + kb) * 128, t.f0, t.e, &full[stage]);
+            tma_load_2d(sB + stage * C::B_BYTES, &tmB, (kb0 + kb) * 128, (int32_t)t.t0, &full[stage]);
           }
           __syncwarp();
           if (++stage == C::STAGES) { stage = 0; phase ^= 1; }
@@ -294,69 +322,85 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
       __syncwarp();
     } else if (warp == 1) {
       // ------------------------------------------------------------ MMAs
-      if (rank == 0) {
-        const bool leader = elect_one();
-        // K-major: 8-row atoms 1024 bytes apart, 32 elements = 32 bytes along the row
-        const uint64_t a0 = smem_desc(smem_u32(sA), 16, 1024, 2);
-        const uint64_t b0 = smem_desc(smem_u32(sB), 16, 1024, 2);
-        int stage = 0; uint32_t phase = 0;
-        int buf = 0; uint32_t buf_phase = 0;
-        bool ok = true;
-        for (int32_t u = unit0; u < n_units && ok; u += ustep) {
-          const Unit t = unit_of<BT>(p, ends, unit_end, u);
-          const uint32_t idesc = C::IDESC | ((uint32_t)(t.n_eff >> 3) << 17);
-          for (int kb = 0; kb < num_kb; ++kb) {
-            if (!warp_wait(&acc_empty[buf], buf_phase ^ 1, p.err)) { ok = false; break; }
-            if (!warp_wait(&full[stage], phase, p.err)) { ok = false; break; }
-            tc_fence_after();
-            if (leader) {
-              const uint32_t d = tmem + (uint32_t)(buf * BT);
-              const uint64_t ad = a0 + (uint64_t)((stage * C::A_BYTES) >> 4);
-              const uint64_t bd = b0 + (uint64_t)((stage * C::B_BYTES) >> 4);
+      const bool leader = elect_one();
+      // K-major: 8-row atoms 1024 bytes apart, 32 elements = 32 bytes along the row
+      const uint64_t a0 = smem_desc(smem_u32(sA), 16, 1024, 2);
+      const uint64_t b0 = smem_desc(smem_u32(sB), 16, 1024, 2);
+      int stage = 0; uint32_t phase = 0;
+      int buf = 0; uint32_t buf_phase = 0;
+      bool ok = true;
+      for (int32_t u = unit0; u < n_units && ok; u += ustep) {
+        const Unit t = unit_of<BT, 128>(p, ends, unit_end, u);
+        const uint32_t idesc = C::IDESC | ((uint32_t)(t.n_eff >> 3) << 17);
+        for (int kb = 0; kb < num_kb; ++kb) {
+          if (!warp_wait(&acc_empty[buf], buf_phase ^ 1, p.err)) { ok = false; break; }
+          if (!warp_wait(&full[stage], phase, p.err)) { ok = false; break; }
+          tc_fence_after();
+          if (leader) {
+            const uint32_t d = tmem + (uint32_t)(buf * BT);
+            const uint64_t ad = a0 + (uint64_t)((stage * C::A_BYTES) >> 4);
+            const uint64_t bd = b0 + (uint64_t)((stage * C::B_BYTES) >> 4);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) mma_f8_pair(d, ad + k * 2, bd + k * 2, idesc, k > 0);
-              tc_commit_pair_mc(&empty[stage], 0x3);
-              tc_commit_pair_mc(&acc_full[buf], 0x3);
-            }
-            __syncwarp();
-            if (++stage == C::STAGES) { stage = 0; phase ^= 1; }
-            if (++buf == C::BUFS) { buf = 0; buf_phase ^= 1; }
+            for (int k = 0; k < 4; ++k) mma_f8(d, ad + k * 2, bd + k * 2, idesc, k > 0);
+            tc_commit(&empty[stage]);
+            tc_commit(&acc_full[buf]);
           }
+          __syncwarp();
+          if (++stage == C::STAGES) { stage = 0; phase ^= 1; }
+          if (++buf == C::BUFS) { buf = 0; buf_phase ^= 1; }
         }
-        if (leader) tc_commit_pair_mc(done_bar, 0x1);
-        __syncwarp();
-        mbar_wait(done_bar, 0, p.err);
       }
+      if (leader) tc_commit(done_bar);
+      __syncwarp();
+      mbar_wait(done_bar, 0, p.err);
       __syncwarp();
     } else {
       // ------------------------------------------------------------ scales
-      // every other K block of a warp's: those of the tile's tokens times the one of the CTA's features
+      // Every other K block of a warp's: those of the tile's tokens times the one of the CTA's features, loaded four turns
+      // ahead.
       constexpr int PER = BT / 32;
+      int32_t next_u = unit0, next_kb = warp - 2;  // K blocks are numbered through all units
+      bool fresh = true;
+      const float *st = nullptr, *w = nullptr;
+      int live = 0;
+      float s[4][PER], f[4];
+      bool have[4];
+      auto load = [&](int i) {
+        while (next_kb >= num_kb && next_u < n_units) { next_kb -= num_kb; next_u += ustep; fresh = true; }
+        have[i] = next_u < n_units;
+        if (!have[i]) return;
+        if (fresh) {
+          const Unit t = unit_of<BT, 128>(p, ends, unit_end, next_u);
+          st = p.st + (kb0 + next_kb) * p.M + t.t0 + lane;
+          w = p.sw + t.e * p.sw_e + (t.f0 >> 7) * p.sw_f + (kb0 + next_kb) * p.sw_c;
+          live = t.tn - lane;
+          fresh = false;
+        }
+#pragma unroll
+        for (int c = 0; c < PER; ++c) s[i][c] = 32 * c < live ? __ldg(st + 32 * c) : 0.0f;
+        f[i] = __ldg(w);
+        st += 2 * p.M, w += 2 * p.sw_c;
+        next_kb += 2;
+      };
       int slot = warp - 2; uint32_t phase = 0;
-      bool ok = true;
-      int32_t kb0 = warp - 2;  // K blocks are numbered through all units
-      for (int32_t u = unit0; u < n_units && ok; u += ustep) {
-        const Unit t = unit_of<BT>(p, ends, unit_end, u);
-        const int32_t f = t.f0 + rank * 128;
-        const float* w = p.sw + t.e * p.sw_e + (f >> 7) * p.sw_f;
-        int kb = kb0;
-        for (; kb < num_kb; kb += 2) {
-          const float sw = f < p.F ? w[kb * p.sw_c] : 0.0f;
-          float s[PER];
+      bool ok = num_kb > 0;
+      if (ok) {
 #pragma unroll
-          for (int i = 0; i < PER; ++i) {
-            const int64_t at = t.t0 + lane + 32 * i;
-            s[i] = lane + 32 * i < t.tn && at < p.M ? p.st[kb * p.M + at] * sw : 0.0f;
-          }
+        for (int i = 0; i < 4; ++i) load(i);
+      }
+      while (ok) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (!ok || !have[i]) { ok = false; break; }
           if (!warp_wait(&sc_empty[slot], phase ^ 1, p.err)) { ok = false; break; }
-          float* dst = sScale + slot * BT;
+          float* dst = sScale + slot * BT + lane;
 #pragma unroll
-          for (int i = 0; i < PER; ++i) dst[lane + 32 * i] = s[i];
+          for (int c = 0; c < PER; ++c) dst[32 * c] = s[i][c] * f[i];
           mbar_arrive(&sc_full[slot]);
           slot += 2;
           if (slot >= C::SLOTS) { slot -= C::SLOTS; phase ^= 1; }
+          load(i);
         }
-        kb0 = kb - num_kb;
       }
       __syncwarp();
     }
@@ -373,8 +417,8 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
     int slot = 0; uint32_t sc_phase = 0;
     bool ok = true;
     for (int32_t u = unit0; u < n_units && ok; u += ustep) {
-      const Unit t = unit_of<BT>(p, ends, unit_end, u);
-      const int32_t f = t.f0 + rank * 128 + q * 32;   // this warp's features
+      const Unit t = unit_of<BT, 128>(p, ends, unit_end, u);
+      const int32_t f = t.f0 + q * 32;   // this warp's features
       f2 acc[NC][16];
 #pragma unroll
       for (int j = 0; j < NC; ++j)
@@ -404,13 +448,43 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&sc_empty[slot]);
-          if (rank != 0) mbar_arrive_cluster_relaxed(cluster_map(smem_u32(&acc_empty[buf]), 0));
-          else mbar_arrive(&acc_empty[buf]);
+          mbar_arrive(&acc_empty[buf]);
         }
         if (++buf == C::BUFS) { buf = 0; buf_phase ^= 1; }
         if (++slot == C::SLOTS) { slot = 0; sc_phase ^= 1; }
       }
       if (!ok || f >= p.F) continue;
+      if constexpr (S > 1) if (col_of(0) < t.tn) {
+        // the other CTAs' sums to the first, which adds them in order: 8 vectors of 4 tokens a lane and block of columns
+        const uint32_t at = (uint32_t)((BT == 32 ? q : ew) * 32 + lane) * 16;
+        constexpr int V_STEP = (BT == 32 ? 4 : 8) * 512;
+        if (part) {
+          const uint32_t dst = cluster_map(smem_u32(sParts), 0) + (part - 1) * C::PART + at;
+#pragma unroll
+          for (int j = 0; j < NC; ++j)
+            if (col_of(j) < t.tn)
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (j * 8 + i) * V_STEP),
+                             "f"(acc[j][2 * i].x), "f"(acc[j][2 * i].y), "f"(acc[j][2 * i + 1].x), "f"(acc[j][2 * i + 1].y)
+                             : "memory");
+          mbar_arrive_cluster(cluster_map(smem_u32(&parts_bar[ew]), 0));
+          continue;
+        }
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&parts_bar[ew], 0, p.err));
+        if (!ok) break;
+#pragma unroll 1
+        for (int o = 0; o < S - 1; ++o)
+#pragma unroll
+          for (int j = 0; j < NC; ++j)
+            if (col_of(j) < t.tn)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float4 v = *reinterpret_cast<const float4*>(sParts + o * C::PART + at + (j * 8 + i) * V_STEP);
+                acc[j][2 * i] = f2_add(acc[j][2 * i], f2_pack(v.x, v.y));
+                acc[j][2 * i + 1] = f2_add(acc[j][2 * i + 1], f2_pack(v.z, v.w));
+              }
+      }
       // a block of 32 tokens; a lane has one feature of all of them: turned through shared memory
 #pragma unroll
       for (int j = 0; j < NC; ++j) {
@@ -439,9 +513,9 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
 
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // no pair MMA, copy or remote arrive targets an exited CTA
+  if (S > 1) cluster_sync();  // no store or arrive from another CTA targets an exited one
   tc_fence_after();
-  if (warp == 1) tmem_dealloc_pair(tmem, C::TMEM);
+  if (warp == 1) tmem_dealloc(tmem, C::TMEM);
 }
 
 // ---------------------------------------------------------------- tokens on the M side
@@ -502,7 +576,7 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
   cluster_sync();  // the peer's barriers exist before any remote arrive or pair copy
   const uint32_t tmem = *tmem_holder;
   pdl_begin();     // all of the above overlaps the kernel before
-  if (warp == 2) read_ends<256>(p, ends, unit_end, &s_ok, &s_units);
+  if (warp == 2) read_ends<256, 256>(p, ends, unit_end, &s_ok, &s_units);
   __syncthreads();
   const int32_t n_units = s_units;
 
@@ -518,7 +592,7 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
       int stage = 0; uint32_t phase = 0;
       bool ok = true;
       for (int32_t u = unit0; u < n_units && ok; u += ustep) {
-        const Unit t = unit_of<256>(p, ends, unit_end, u);
+        const Unit t = unit_of<256, 256>(p, ends, unit_end, u);
         const int32_t row = (int32_t)t.t0 + rank * 128, f = t.f0 + rank * 64;
         for (int kb = 0; kb < num_kb; ++kb) {
           if (!warp_wait(&empty[stage], phase ^ 1, p.err)) { ok = false; break; }
@@ -588,7 +662,7 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
       auto load = [&](int i) {
         if (next_u >= n_units) return;
         if (next_kb == 0) {
-          const Unit t = unit_of<256>(p, ends, unit_end, next_u);
+          const Unit t = unit_of<256, 256>(p, ends, unit_end, next_u);
           st = p.st + t.t0 + rank * 128 + lane;
           sw = p.sw + t.e * p.sw_e + min((t.f0 >> 7) + half, (p.F - 1) >> 7) * p.sw_f;
           live = t.tn - rank * 128;
@@ -682,7 +756,7 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
         if (kb + 1 < num_kb && ok) step(std::integral_constant<int, 1>{}, kb + 1);
       }
       if (!ok) break;
-      const Unit t = unit_of<256>(p, ends, unit_end, u);
+      const Unit t = unit_of<256, 256>(p, ends, unit_end, u);
       const int32_t r = rank * 128 + (warp & 3) * 32 + lane;   // this lane's row of the tile
       if (r < t.tn) {
         const int32_t f = t.f0 + (int32_t)half * 128;
@@ -707,10 +781,10 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
 
 using Kernel = void (*)(CUtensorMap, CUtensorMap, MmParams);
 
-// Pairs of a kernel that can be resident at once, by device (KIND tells the kernels apart); its register split needs
-// the registers that it was written for.
+// Clusters of a kernel that can be resident at once (none, if no part of the device holds one), by device; KIND tells the
+// kernels apart.  A kernel's register split needs the registers that it was written for.
 template <int KIND>
-int resident_pairs(Kernel k, size_t smem, int* n) {
+int resident_clusters(Kernel k, size_t smem, int ctas, int* n) {
   static std::atomic<int> resident[64];  // the number + 1, once known; any thread may be the one that asks
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -724,12 +798,12 @@ int resident_pairs(Kernel k, size_t smem, int* n) {
     if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
       return cuda_status(e, "cudaFuncSetAttribute");
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * (num_sms() / 2));
+    cfg.gridDim = dim3(ctas * (num_sms() / ctas));
     cfg.blockDim = dim3(FM_THREADS);
     cfg.dynamicSmemBytes = smem;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.x = ctas;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
@@ -740,26 +814,59 @@ int resident_pairs(Kernel k, size_t smem, int* n) {
     resident[dev & 63].store(r, std::memory_order_relaxed);
   }
   *n = r - 1;
-  return *n > 0 ? MX_OK : cuda_status(cudaErrorInvalidConfiguration, "cudaOccupancyMaxActiveClusters");
+  return MX_OK;
 }
 
 // Tiles of bt token rows, at most: any group that has rows may end in a part of one.
 int64_t tile_bound(const MmParams& p, int bt) {
-  const int64_t groups = std::min<int64_t>(p.E, p.M);
-  return (p.M + groups * (bt - 1)) / bt * ((p.F + FM_F - 1) / FM_F);
+  const int64_t groups = std::min<int64_t>(p.E, p.M), ft = bt == 256 ? 256 : 128;
+  return (p.M + groups * (bt - 1)) / bt * ((p.F + ft - 1) / ft);
 }
 
+// KIND tells the kernels apart; ctas: of a cluster.  whole: a cluster has one tile at most (S > 1: its buffer for the
+// other pairs' sums is written once).
 template <int KIND>
-int launch_cfg(Kernel k, size_t smem, int bt, const CUtensorMap& tA, const CUtensorMap& tB, const MmParams& p, cudaStream_t stream) {
+int launch_cfg(Kernel k, size_t smem, int bt, int ctas, bool whole, const CUtensorMap& tA, const CUtensorMap& tB, const MmParams& p,
+               cudaStream_t stream) {
   const int64_t units = tile_bound(p, bt);
-  if (units > INT32_MAX - 1024) return fail(MX_ERR_UNSUPPORTED, "FP8 product: too many tiles");
+  if (units > INT32_MAX / 8) return fail(MX_ERR_UNSUPPORTED, "FP8 product: too many tiles");
   int nres = 0;
-  if (int rc = resident_pairs<KIND>(k, smem, &nres)) return rc;
+  if (int rc = resident_clusters<KIND>(k, smem, ctas, &nres)) return rc;
+  if (nres <= 0) return cuda_status(cudaErrorInvalidConfiguration, "cudaOccupancyMaxActiveClusters");
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute");
-  const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(units, nres));
+  const int64_t clusters = std::max<int64_t>(1, whole ? units : std::min<int64_t>(units, nres));
   count_launch(MX_KERNEL_FP8_BLOCK);
-  return cuda_status(launch_overlapped(k, (unsigned)(2 * pairs), FM_THREADS, smem, stream, 2, tA, tB, p), "FP8 product launch");
+  return cuda_status(launch_overlapped(k, (unsigned)(ctas * clusters), FM_THREADS, smem, stream, ctas, tA, tB, p), "FP8 product launch");
+}
+
+// Token rows to a tile (256: tokens on the M side, CTA pairs) and CTAs to a tile's contraction.
+//   Few tiles: an SM takes in some 110 GB/s, so a long contraction is shared by the CTAs of a cluster, in one wave (8 rows of
+// one group, us with one, two and four CTAs: 4096 x 7168 18.2, 12.4, 9.8; 512 x 7168 17.4, 11.3, 8.2; 7168 x 2048 7.5, 7.3
+// and, in two waves, 12.5; 1024 x 1024 5.1, 5.4, 5.3; 128 rows of 4096 x 7168 by 64 19.8, 14.0).
+//   Small tiles while they are one wave or the weights' bytes count, large ones where the tensor cores or the rows' bytes do.
+// us with 32 / 64 / 128 / 256: 512 rows of one 1024 x 1024 5.7 / 5.9 / 7.6 / 11.7; 1000 of one 1024 x 4096 - / 13.0 / 18.3 /
+// 19.0; 2048 of one 2048 x 2048 - / - / 20.2 / 15.8; 64 over 64 of 4096 x 7168 147 / 147 / 151 / 166; 1024 over 64 of 2048 x
+// 2048 47.5 / 46.0 / 47.0 / 56.6; 256 over 8 of it 14.0 / 12.2 / 11.2 / 16.0; 800 over 8 23.7 / 15.2 / 15.7 / 17.0; 2041 over
+// 16 of 1424 x 1008 21.0 / 15.4 / 14.2 / 18.4; 3000 over 64 of 4096 x 2048 139 / 103 / 99 / 111; 6000 over 64 of it 235 / 151 /
+// 134 / 121; 4096 over 16 of 5120 x 8192 626 / 356 / 303 / 191.
+struct TokenShape {
+  int bt, share;
+};
+int token_shape(const MmParams& p, TokenShape* s) {
+  int n2 = 0, n4 = 0, rc;
+  if ((rc = resident_clusters<642>(fp8_mm_narrow_kernel<64, 2>, FCfg<64, 2>::SMEM, 2, &n2)) ||
+      (rc = resident_clusters<324>(fp8_mm_narrow_kernel<32, 4>, FCfg<32, 4>::SMEM, 4, &n4)))
+    return rc;
+  const int64_t t32 = tile_bound(p, 32), t64 = tile_bound(p, 64), t128 = tile_bound(p, 128), n1 = num_sms();
+  if (p.C >= 2048 && t32 <= n4) *s = TokenShape{32, 4};
+  else if (p.C >= 2048 && t32 <= n2) *s = TokenShape{32, 2};
+  else if (p.C >= 2048 && t64 <= n2) *s = TokenShape{64, 2};
+  else if (t32 <= n1 || p.M <= 16 * (int64_t)p.E) *s = TokenShape{32, 1};
+  else if (t64 <= n1 || p.M <= 24 * (int64_t)p.E) *s = TokenShape{64, 1};
+  else if (p.M <= 64 * (int64_t)p.E || (p.M <= 256 * (int64_t)p.E && t128 <= 3 * n1)) *s = TokenShape{128, 1};
+  else *s = TokenShape{256, 1};
+  return MX_OK;
 }
 
 }  // namespace
@@ -772,19 +879,25 @@ int launch_fp8_block_mm(const Fp8MmLaunch& g, cudaStream_t stream) {
   p.C = (int32_t)(fwd ? g.K : g.N);
   const int64_t nb = (g.N + 127) / 128, kb = (g.K + 127) / 128;
   p.st = g.sa; p.sw = g.sw; p.sw_e = nb * kb; p.sw_f = fwd ? kb : 1; p.sw_c = fwd ? 1 : kb;
-  const bool wide = p.M > 64 * (int64_t)p.E;
-  const int bt = wide ? 256 : p.M <= 16 * (int64_t)p.E ? 32 : 128;
+  TokenShape s{};
+  int rc = token_shape(p, &s);
+  if (rc) return rc;
+  const bool wide = s.bt == 256;
   CUtensorMap w, a;
   uint64_t dw[3] = {(uint64_t)p.C, (uint64_t)p.F, (uint64_t)p.E}, sw[2] = {(uint64_t)p.C, (uint64_t)p.C * p.F};
   uint32_t bw[3] = {128, wide ? 64u : 128u, 1};
   uint64_t da[2] = {(uint64_t)p.C, (uint64_t)p.M}, sa[1] = {(uint64_t)p.C};
-  uint32_t ba[2] = {128, (uint32_t)bt / 2};
-  int rc = make_tmap(&w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(g.w), dw, sw, bw, CU_TENSOR_MAP_SWIZZLE_128B);
+  uint32_t ba[2] = {128, wide ? 128u : (uint32_t)s.bt};
+  rc = make_tmap(&w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(g.w), dw, sw, bw, CU_TENSOR_MAP_SWIZZLE_128B);
   if (!rc) rc = make_tmap(&a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(g.a), da, sa, ba, CU_TENSOR_MAP_SWIZZLE_128B);
   if (rc) return rc;
-  if (wide) return launch_cfg<256>(fp8_mm_wide_kernel, WCfg::SMEM, 256, a, w, p, stream);
-  return bt == 32 ? launch_cfg<32>(fp8_mm_narrow_kernel<32>, FCfg<32>::SMEM, 32, w, a, p, stream)
-                  : launch_cfg<128>(fp8_mm_narrow_kernel<128>, FCfg<128>::SMEM, 128, w, a, p, stream);
+  if (wide) return launch_cfg<2561>(fp8_mm_wide_kernel, WCfg::SMEM, 256, 2, false, a, w, p, stream);
+#define MX_NARROW(BT, S)                                                                                            \
+  if (s.bt == BT && s.share == S)                                                                                   \
+    return launch_cfg<BT * 10 + S>(fp8_mm_narrow_kernel<BT, S>, FCfg<BT, S>::SMEM, BT, S, S > 1, w, a, p, stream);
+  MX_NARROW(32, 1) MX_NARROW(32, 2) MX_NARROW(32, 4) MX_NARROW(64, 1) MX_NARROW(64, 2) MX_NARROW(128, 1)
+#undef MX_NARROW
+  return fail(MX_ERR_UNSUPPORTED, "FP8 product: no kernel for the shape");
 }
 
 }  // namespace mx
