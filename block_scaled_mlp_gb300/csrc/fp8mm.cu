@@ -33,7 +33,7 @@ namespace {
 constexpr int FM_EPI = 8;                 // epilogue warps
 constexpr int FM_MAX_E = 1024;
 constexpr int FM_THREADS = 128 + FM_EPI * 32;
-constexpr int FM_REGS = 168;              // a thread at launch; 56 + 2 * 224 = 3 * 168 after the split
+constexpr int FM_REGS = 168;              // a thread at launch; after the split 88 + 2 * 208 or 56 + 2 * 224 = 3 * 168
 
 // A CTA has 128 features; BT: columns of a token tile; S: CTAs that share a tile's contraction.
 template <int BT, int S>
@@ -43,11 +43,10 @@ struct FCfg {
   static constexpr int TX = A_BYTES + B_BYTES;
   static constexpr int EPI_BYTES = FM_EPI * 2048;        // a warp's 32 x 32 bf16 block
   static constexpr int TABLE = FM_MAX_E * 8;             // group ends and running unit numbers
-  static constexpr int SLOTS = 8;                        // K blocks whose scales are ready
-  static constexpr int SC_BYTES = SLOTS * BT * 4;
   static constexpr int PART = BT * 128 * 4;              // one CTA's sums
   static constexpr int PARTS = (S - 1) * PART;           // in a tile's first CTA: the others'
-  static constexpr int BUFS = 4;                         // accumulators
+  static constexpr int BUFS = 4;                         // accumulators, and the scales of their K blocks
+  static constexpr int SC_BYTES = BUFS * BT * 4;
   static constexpr int TMEM = BUFS * BT;
   static constexpr uint32_t IDESC = (1u << 4) | ((128u >> 4) << 24);
   static constexpr int STAGES = (226 * 1024 - EPI_BYTES - SC_BYTES - PARTS - TABLE - 1536) / TX;
@@ -55,7 +54,7 @@ struct FCfg {
   static_assert(BT == 128 || BT == 64 || BT == 32, "tile widths");
   static_assert(S == 1 || S == 2 || S == 4, "CTAs of a cluster");
   static_assert(STAGES >= 3, "shared memory");
-  static_assert((2 * STAGES + 2 * BUFS + 2 * SLOTS + 2 + FM_EPI) * 8 <= 512, "barriers");
+  static_assert((2 * STAGES + 2 * BUFS + 2 + FM_EPI) * 8 <= 512, "barriers");
   static_assert(SMEM + 1024 /*static*/ <= 227 * 1024, "shared memory");
 };
 
@@ -101,14 +100,14 @@ MX_DEVINL bool warp_wait_at(uint32_t bar, uint32_t parity, int32_t* err, bool do
   return __all_sync(0xFFFFFFFFu, done);
 }
 
-// acc += (a, b) s, where it stands: as a volatile statement it stays behind the TMEM load that was issued before it (left
-// to the compiler's order, 356 against 342 us).
-MX_DEVINL void fma_here(f2& acc, uint32_t a, uint32_t b, float s) {
+// acc += (a s, b t), where it stands: as a volatile statement it stays behind the TMEM load that was issued before it (left
+// to the compiler's order, 356 against 342 us for 8192 x 4096 x 14336).
+MX_DEVINL void fma_here(f2& acc, uint32_t a, uint32_t b, float s, float t) {
   asm volatile(
-      "{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %4};\n mov.b64 z, {%0, %1};\n"
+      "{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%0, %1};\n"
       " fma.rn.f32x2 z, x, y, z;\n mov.b64 {%0, %1}, z;\n}"
       : "+f"(acc.x), "+f"(acc.y)
-      : "r"(a), "r"(b), "f"(s));
+      : "r"(a), "r"(b), "f"(s), "f"(t));
 }
 
 // Bounded wait for arrivals from other CTAs of the cluster, whose writes it makes visible.
@@ -262,9 +261,7 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
   uint64_t* empty = full + C::STAGES;
   uint64_t* acc_full = empty + C::STAGES;
   uint64_t* acc_empty = acc_full + C::BUFS;
-  uint64_t* sc_full = acc_empty + C::BUFS;
-  uint64_t* sc_empty = sc_full + C::SLOTS;
-  uint64_t* parts_bar = sc_empty + C::SLOTS;   // S > 1, by epilogue warp: the other pairs' sums are here
+  uint64_t* parts_bar = acc_empty + C::BUFS;   // S > 1, by epilogue warp: the other pairs' sums are here
   uint64_t* done_bar = parts_bar + FM_EPI;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done_bar + 1);
   __shared__ int s_ok, s_units;
@@ -278,8 +275,7 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
-    for (int a = 0; a < C::BUFS; ++a) { mbar_init(&acc_full[a], 1); mbar_init(&acc_empty[a], FM_EPI); }
-    for (int s = 0; s < C::SLOTS; ++s) { mbar_init(&sc_full[s], 32); mbar_init(&sc_empty[s], FM_EPI); }
+    for (int a = 0; a < C::BUFS; ++a) { mbar_init(&acc_full[a], 2); mbar_init(&acc_empty[a], FM_EPI); }
     for (int e = 0; e < FM_EPI; ++e) mbar_init(&parts_bar[e], S > 1 ? 32 * (S - 1) : 1);
     mbar_init(done_bar, 1);
     fence_mbar_init();
@@ -296,7 +292,7 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
   const int32_t n_units = s_units;
 
   if (warp < 4) {
-    regs_give<56>();
+    regs_give<88>();
     if (warp == 0) {
       // ------------------------------------------------------------ loads
       const bool leader = elect_one();
@@ -357,7 +353,7 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
     } else {
       // ------------------------------------------------------------ scales
       // Every other K block of a warp's: those of the tile's tokens times the one of the CTA's features, loaded four turns
-      // ahead.
+      // ahead.  They are part of what an accumulator's acc_full stands for, and their place is free when it is.
       constexpr int PER = BT / 32;
       int32_t next_u = unit0, next_kb = warp - 2;  // K blocks are numbered through all units
       bool fresh = true;
@@ -382,7 +378,7 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
         st += 2 * p.M, w += 2 * p.sw_c;
         next_kb += 2;
       };
-      int slot = warp - 2; uint32_t phase = 0;
+      int buf = warp - 2; uint32_t phase = 0;
       bool ok = num_kb > 0;
       if (ok) {
 #pragma unroll
@@ -392,13 +388,14 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (!ok || !have[i]) { ok = false; break; }
-          if (!warp_wait(&sc_empty[slot], phase ^ 1, p.err)) { ok = false; break; }
-          float* dst = sScale + slot * BT + lane;
+          if (!warp_wait(&acc_empty[buf], phase ^ 1, p.err)) { ok = false; break; }
+          float* dst = sScale + buf * BT + lane;
 #pragma unroll
           for (int c = 0; c < PER; ++c) dst[32 * c] = s[i][c] * f[i];
-          mbar_arrive(&sc_full[slot]);
-          slot += 2;
-          if (slot >= C::SLOTS) { slot -= C::SLOTS; phase ^= 1; }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acc_full[buf]);
+          buf += 2;
+          if (buf >= C::BUFS) { buf -= C::BUFS; phase ^= 1; }
           load(i);
         }
       }
@@ -406,15 +403,15 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    regs_take<224>();
+    regs_take<208>();
     const int ew = warp - 4, q = warp & 3, half = ew >> 2;
     uint8_t* stg = sEpi + ew * 2048;
     constexpr int NC = BT <= 64 ? 1 : BT / 64;   // blocks of 32 columns a warp
     auto col_of = [half](int j) { return (2 * j + half) * 32; };
     const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16);
     const int qr = lane >> 2, qc = (lane & 3) * 8;
+    const uint32_t full_at = smem_u32(acc_full), scales = smem_u32(sScale);
     int buf = 0; uint32_t buf_phase = 0;
-    int slot = 0; uint32_t sc_phase = 0;
     bool ok = true;
     for (int32_t u = unit0; u < n_units && ok; u += ustep) {
       const Unit t = unit_of<BT, 128>(p, ends, unit_end, u);
@@ -425,33 +422,32 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[j][i] = f2_splat(0.0f);
       for (int kb = 0; kb < num_kb; ++kb) {
-        if (!warp_wait(&sc_full[slot], sc_phase, p.err) || !warp_wait(&acc_full[buf], buf_phase, p.err)) { ok = false; break; }
+        ok = warp_wait_at(full_at + buf * 8, buf_phase, p.err);
+        if (!ok) break;
         tc_fence_after();
-        const float* sc = sScale + slot * BT;
-        const uint32_t at = tb + (uint32_t)(buf * BT);
+        const uint32_t at = tb + (uint32_t)(buf * BT), sc = scales + buf * (BT * 4);
+        // a block of 32 columns is loaded while the one before it is added
+        uint32_t v[2][32];
+        if (col_of(0) < t.tn) tmem_ld_32cols(at + col_of(0), v[0]);
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
-          const int c = col_of(j);
-          if (c < t.tn) {
-            uint32_t r[32];
-            tmem_ld_32cols(at + c, r);
-            tmem_ld_wait(r);
+          const bool here = col_of(j) < t.tn;
+          if (here) tmem_ld_wait(v[j & 1]);
+          if (j + 1 < NC && col_of(j + 1) < t.tn) tmem_ld_32cols(at + col_of(j + 1), v[(j + 1) & 1]);
+          if (here) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const float4 s = *reinterpret_cast<const float4*>(sc + c + 4 * i);
-              acc[j][2 * i] = f2_fma(f2_pack(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1])), f2_pack(s.x, s.y), acc[j][2 * i]);
-              acc[j][2 * i + 1] = f2_fma(f2_pack(__uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3])), f2_pack(s.z, s.w), acc[j][2 * i + 1]);
+              float4 m;
+              asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(m.x), "=f"(m.y), "=f"(m.z), "=f"(m.w) : "r"(sc + (col_of(j) + 4 * i) * 4));
+              fma_here(acc[j][2 * i], v[j & 1][4 * i], v[j & 1][4 * i + 1], m.x, m.y);
+              fma_here(acc[j][2 * i + 1], v[j & 1][4 * i + 2], v[j & 1][4 * i + 3], m.z, m.w);
             }
           }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&sc_empty[slot]);
-          mbar_arrive(&acc_empty[buf]);
-        }
+        if (lane == 0) mbar_arrive(&acc_empty[buf]);
         if (++buf == C::BUFS) { buf = 0; buf_phase ^= 1; }
-        if (++slot == C::SLOTS) { slot = 0; sc_phase ^= 1; }
       }
       if (!ok || f >= p.F) continue;
       if constexpr (S > 1) if (col_of(0) < t.tn) {
@@ -748,7 +744,7 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
             }
           }
 #pragma unroll
-          for (int i = 0; i < 16; ++i) fma_here(acc[j][i], v[j & 1][2 * i], v[j & 1][2 * i + 1], s);
+          for (int i = 0; i < 16; ++i) fma_here(acc[j][i], v[j & 1][2 * i], v[j & 1][2 * i + 1], s, s);
         }
       };
       for (int kb = 0; kb < num_kb && ok; kb += 2) {
