@@ -441,7 +441,8 @@ PyObject* py_token_group(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t R = ids.numel();
     On on(ids);
     at::Tensor offs = empty({E}, at::kInt, ids), dst = empty({R}, at::kInt, ids), src = empty({R}, at::kInt, ids);
-    at::Tensor ws = empty({(int64_t)mx_token_group_workspace(R, E) + 16}, at::kByte, ids);
+    at::Tensor ws;
+    if (const int64_t bytes = (int64_t)mx_token_group_workspace(R, E)) ws = empty({bytes}, at::kByte, ids);
     on.finish(mx_token_group((const int32_t*)ptr(ids), R, E, (int32_t*)ptr(offs), (int32_t*)ptr(dst), (int32_t*)ptr(src), ptr(ws),
                              err, on.stream));
     return tuple_of(offs, dst, src);

@@ -233,10 +233,10 @@ int mx_token_group(const int32_t* expert_of, int64_t R, int32_t E, int32_t* offs
   if (R < 0) return fail(MX_ERR_INVALID_ARG, "R must not be negative");
   if (E < 1 || E > 1024) return fail(MX_ERR_INVALID_ARG, "E must be in [1, 1024]");
   if (R > kMaxRows) return fail(MX_ERR_UNSUPPORTED, "too many rows");
-  if (!offs || (R > 0 && (!expert_of || !row_dst || !row_src || !workspace)))
+  if (!offs || (R > 0 && (!expert_of || !row_dst || !row_src || (!workspace && token_group_workspace(R, E)))))
     return fail(MX_ERR_INVALID_ARG, "null pointer argument");
-  if (!aligned_to(4, expert_of, offs, row_dst, row_src, workspace))
-    return fail(MX_ERR_ALIGNMENT, "token group: pointers must be aligned to 4 bytes");
+  if (!aligned_to(4, expert_of, offs, row_dst, row_src) || !all_aligned16(workspace))
+    return fail(MX_ERR_ALIGNMENT, "token group: pointers must be aligned to 4 bytes, the workspace to 16");
   if (R == 0) {
     count_launch(MX_KERNEL_MEMSET);
     return cuda_status(cudaMemsetAsync(offs, 0, (size_t)E * 4, (cudaStream_t)stream), "cudaMemsetAsync");

@@ -820,7 +820,24 @@ __global__ void __launch_bounds__(WARPS * 32)
   __syncthreads();
   if (n_chunks > 1) {
     // threads side by side take experts, and as many threads as there are for each share the chunks
-    const int parts = max(1, WARPS * 32 / E);
+    if (E % 4 == 0) {  // four at a time
+      const int e4 = E / 4, parts4 = max(1, WARPS * 32 / e4);
+      for (int i = tid; i < parts4 * e4; i += WARPS * 32) {
+        const int q = i % e4;
+        int4 all = make_int4(0, 0, 0, 0), b = all;
+#pragma unroll 8
+        for (int c = i / e4; c < n_chunks; c += parts4) {
+          const int4 n = __ldg(reinterpret_cast<const int4*>(counts + (int64_t)c * E) + q);
+          all.x += n.x, all.y += n.y, all.z += n.z, all.w += n.w;
+          if (c < mine) b.x += n.x, b.y += n.y, b.z += n.z, b.w += n.w;
+        }
+        atomicAdd(&total[4 * q], all.x), atomicAdd(&total[4 * q + 1], all.y), atomicAdd(&total[4 * q + 2], all.z);
+        atomicAdd(&total[4 * q + 3], all.w);
+        atomicAdd(&before[4 * q], b.x), atomicAdd(&before[4 * q + 1], b.y), atomicAdd(&before[4 * q + 2], b.z);
+        atomicAdd(&before[4 * q + 3], b.w);
+      }
+    }
+    const int parts = E % 4 ? max(1, WARPS * 32 / E) : 0;
     for (int i = tid; i < parts * E; i += WARPS * 32) {
       const int e = i % E;
       int32_t all = 0, b = 0;
@@ -940,9 +957,14 @@ int launch_moe_route_bwd(const RouteBwdLaunch& a, cudaStream_t stream) {
   }), "moe_route_bwd_kernel launch");
 }
 
+namespace {
+// Up to 8192 rows one large CTA does it all, if its warps' counts fit 48 KB; 1024 rows one small one.
+bool one_cta(int64_t R, int32_t E) { return R <= 1024 || (R <= 8192 && E <= 352); }
+}  // namespace
+
 size_t token_group_workspace(int64_t R, int32_t E) {
   // for any number of SMs: a chunk has 1024 rows at least
-  return (size_t)((R + 1023) / 1024) * (size_t)E * 4;
+  return one_cta(R, E) ? 0 : (size_t)((R + 1023) / 1024) * (size_t)E * 4;
 }
 
 int launch_token_group(const int32_t* expert_of, int64_t R, int32_t E, int32_t* offs, int32_t* row_dst, int32_t* row_src,
@@ -954,8 +976,7 @@ int launch_token_group(const int32_t* expert_of, int64_t R, int32_t E, int32_t* 
                                          (const int32_t*)counts, offs, row_dst, row_src, err),
                        "token_group_place_kernel launch");
   };
-  // up to 8192 rows one large CTA, if its warps' counts fit 48 KB; else the chunks are counted first
-  if (R <= 8192 && E <= 352) {
+  if (one_cta(R, E) && E <= 352) {
     if (R <= 1024) return place(token_group_place_kernel<32, 1>, 1, 32, 1024);
     if (R <= 2048) return place(token_group_place_kernel<32, 2>, 1, 32, 2048);
     if (R <= 4096) return place(token_group_place_kernel<32, 4>, 1, 32, 4096);
@@ -965,7 +986,7 @@ int launch_token_group(const int32_t* expert_of, int64_t R, int32_t E, int32_t* 
   const int64_t most = 2 * (int64_t)num_sms();
   const int64_t chunk = std::max<int64_t>(1024, ((R + most - 1) / most + 255) / 256 * 256);
   const unsigned grid = (unsigned)((R + chunk - 1) / chunk);
-  if (grid > 1) {
+  if (grid > 1) {  // the chunks are counted first
     count_launch(MX_KERNEL_DISPATCH);
     const cudaError_t e = launch_overlapped(token_group_count_kernel, grid, TG_WARPS * 32, (size_t)E * 4, stream, 1, expert_of, R, E,
                                             chunk, counts);

@@ -590,7 +590,8 @@ MX_API int mx_moe_route_bwd(const float* dweights, const void* logits, int logit
  *   offs      [E] int32 out: cumulative ends of the groups.
  *   row_dst   [R] int32 out: row of routed row r; a group's rows keep their order.
  *   row_src   [R] int32 out: routed row that row i holds.
- *   workspace mx_token_group_workspace(R, E) bytes.
+ *   workspace mx_token_group_workspace(R, E) bytes, 16-byte aligned; NULL where
+ *             that is 0 (few rows).
  * An expert number outside [0, E) is reported in err_word (may be NULL,
  * MX_ERR_BAD_OFFSETS): that row is not placed, row_dst -1, and as many rows
  * behind the last group have row_src -1.

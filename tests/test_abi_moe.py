@@ -44,12 +44,13 @@ def test_route_backward_refusals(L):
 
 
 def test_token_group_refusals(L):
-    def group(ids=P, R=10, E=4, offs=P, dst=P, src=P, ws=P):
+    def group(ids=P, R=9000, E=4, offs=P, dst=P, src=P, ws=P):
         return L.mx_token_group(ids, R, E, offs, dst, src, ws, None, None)
 
     assert group(ids=None) == 1 and group(offs=None) == 1 and group(dst=None) == 1 and group(src=None) == 1 and group(ws=None) == 1
-    assert group(R=-1) == 1 and group(E=0) == 1 and group(E=1025) == 1 and group(R=1 << 31) == 4 and group(dst=BYTE) == 2
-    assert L.mx_token_group_workspace(0, 4) == 0 and L.mx_token_group_workspace(1025, 4) == 2 * 4 * 4
+    assert group(R=-1) == 1 and group(E=0) == 1 and group(E=1025) == 1 and group(R=1 << 31) == 4 and group(dst=BYTE) == 2 and group(ws=ODD) == 2
+    assert L.mx_token_group_workspace(0, 4) == 0 and L.mx_token_group_workspace(8192, 352) == 0      # one CTA
+    assert L.mx_token_group_workspace(8193, 4) == 9 * 4 * 4 and L.mx_token_group_workspace(1025, 353) == 2 * 353 * 4
     assert L.mx_token_group_workspace(10, 0) == 0 and L.mx_token_group_workspace(1 << 32, 4) == 0
 
 
