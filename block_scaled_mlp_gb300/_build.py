@@ -77,7 +77,7 @@ def build(verbose: bool = False, force: bool = False, extra_flags=None) -> str:
         s = os.path.join(CSRC, src)
         o = os.path.join(BUILD, src.replace(".cu", ".o"))
         if not force and not _stale(o, [s] + headers):
-            return o, ""
+            return o, None
         cmd = [nvcc, *ARCH, *FLAGS, *extra, "-c", s, "-o", o]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
@@ -101,6 +101,8 @@ def build(verbose: bool = False, force: bool = False, extra_flags=None) -> str:
                  binding_obj], "g++ for binding.cpp")
             with open(key_file, "w") as f:
                 f.write(key)
+            return True
+        return False
 
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         binding = ex.submit(compile_binding)
@@ -108,16 +110,16 @@ def build(verbose: bool = False, force: bool = False, extra_flags=None) -> str:
     objs = [o for o, _ in results]
     if verbose:
         for _, log in results:
-            if log.strip():
+            if log and log.strip():
                 print(log, file=sys.stderr)
-    if force or _stale(LIB, objs):
+    # what was compiled is linked again, even where file times are too coarse to show it
+    if force or any(log is not None for _, log in results) or _stale(LIB, objs):
         cmd = [nvcc, *ARCH, "-shared", "-Xcompiler", "-fPIC", "-o", LIB, *objs]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     try:
-        binding.result()
-        if force or _stale(BINDING, [binding_obj]):
+        if binding.result() or force or _stale(BINDING, [binding_obj]):
             run(["g++", "-shared", "-o", BINDING, binding_obj, f"-L{HERE}", "-l:libmxmlp.so", "-Wl,-rpath,$ORIGIN",
                  *_torch_flags()[1]], "link of the binding")
     except (RuntimeError, OSError) as e:
