@@ -399,10 +399,10 @@ __device__ __noinline__ int route_closely(const RouteParams& p, const void* row,
   return mine;
 }
 
-// The k experts that lanes 0 to k - 1 have (numbers and logits) in order by scores of 44 bits: each lane's place.  *sure as
+// The n experts that lanes 0 to n - 1 have (numbers and logits) in order by scores of 44 bits: each lane's place.  *sure as
 // in route_closely.
-__device__ __noinline__ int order_closely(const RouteParams& p, const void* row, float most, int id, float x, bool* sure) {
-  const bool has = (int)(threadIdx.x & 31) < p.k, sigmoid = p.sigmoid;
+__device__ __noinline__ int order_closely(const RouteParams& p, const void* row, float most, int n, int id, float x, bool* sure) {
+  const bool has = (int)(threadIdx.x & 31) < n, sigmoid = p.sigmoid;
   ff inv{1.0f, 0.0f}, c{-INFINITY, 0.0f};
   if (!sigmoid) inv = ff_inverse_sum(row, p.wide, p.E, most);
   bool fine = true;
@@ -414,7 +414,7 @@ __device__ __noinline__ int order_closely(const RouteParams& p, const void* row,
   }
   int place = 0;
 #pragma unroll 1
-  for (int j = 0; j < p.k; ++j) {
+  for (int j = 0; j < n; ++j) {
     const ff v = ff_shfl(c, j);
     const int e = __shfl_sync(FULL, id, j);
     const float xj = __shfl_sync(FULL, x, j), bj = __shfl_sync(FULL, b, j);
@@ -542,7 +542,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __gri
   };
   find();
   uint32_t mine = 0, behind = 0;  // key of the lane's expert; of the one behind the last
-  int id = 0;
+  int id = 0, behind_e = 0;
   auto round = [&](int& e) {
     const uint32_t top = __reduce_max_sync(FULL, best);
     e = __shfl_sync(FULL, at, __ffs(__ballot_sync(FULL, best == top)) - 1);  // of equal ones the lowest lane has the lowest numbers
@@ -565,8 +565,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __gri
   bool ordered = true;  // within the k
   float border = 0.0f;  // how far off the difference of the k-th and another may be
   if (p.bias) {
-    int e;
-    behind = round(e);
+    behind = round(behind_e);
     const float b = has ? p.bias[id] : 0.0f, c1 = of_key(mine);
     const float x2 = __shfl_down_sync(FULL, x, 1), s2 = __shfl_down_sync(FULL, s, 1), b2 = __shfl_down_sync(FULL, b, 1);
     const uint32_t next = __shfl_down_sync(FULL, mine, 1);
@@ -586,6 +585,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __gri
   int place = lane;
   const bool spoilt = __any_sync(FULL, bad);
   bool again = __any_sync(FULL, !sure || !sure_groups);
+  bool contest = false;
   if (again && !spoilt) {
     // Equal by their inputs?  Then numbers decide, as they did: all logits (no bias), or all experts as near to the k-th
     // as their scores are off.
@@ -599,30 +599,42 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __gri
       const float xk = __shfl_sync(FULL, x, k - 1), ck = of_key(__shfl_sync(FULL, mine, k - 1));
       const float bk = p.bias[__shfl_sync(FULL, id, k - 1)], off = __shfl_sync(FULL, border, k - 1);
       bool equal = true;
+      int near = 0;
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (key[i] && !(ck - of_key(key[i]) > off)) equal = equal && l[i] == xk && p.bias[first + i] == bk;
+        if (key[i] && !(ck - of_key(key[i]) > off)) {
+          equal = equal && l[i] == xk && p.bias[first + i] == bk;
+          ++near;
+        }
       again = !__all_sync(FULL, equal);
+      // one expert alone behind the k-th is put in order with the k
+      contest = again && k < 32 && warp_sum(near) == 1;
     }
+  }
+  bool chosen = has;
+  if (!spoilt && (contest || (!again && !__all_sync(FULL, ordered)))) {
+    if (contest && lane == k) {
+      id = behind_e;
+      x = logit(row, wide, id);
+      s = score(x);
+    }
+    bool fine;
+    place = order_closely(p, row, most, contest ? k + 1 : k, id, x, &fine);
+    chosen = lane < (contest ? k + 1 : k) && place < k;
+    again = !fine;
+    contest = false;
   }
   if (again && !spoilt) {
-    bool close_enough;
-    id = route_closely(p, row, most, buf, &close_enough);
-    if (!close_enough) id = route_exactly(p, row, buf);
+    bool fine;
+    id = route_closely(p, row, most, buf, &fine);
+    if (!fine) id = route_exactly(p, row, buf);
+    chosen = has;
+    place = lane;
     x = has ? logit(row, wide, id) : 0.0f;
     s = has ? score(x) : 0.0f;
-  } else if (!__all_sync(FULL, ordered) && !spoilt) {
-    bool fine;
-    place = order_closely(p, row, most, id, x, &fine);
-    if (!fine) {
-      id = route_exactly(p, row, buf);
-      place = lane;
-      x = has ? logit(row, wide, id) : 0.0f;
-      s = has ? score(x) : 0.0f;
-    }
   }
-  const float total = p.renorm ? warp_sum(s) + 1e-20f : 1.0f;
-  if (!has) return;
+  const float total = p.renorm ? warp_sum(chosen ? s : 0.0f) + 1e-20f : 1.0f;
+  if (!chosen) return;
   float w = p.scale * (s / total);
   if (spoilt) {  // no order: the first k, and weights that say so
     id = place = lane;
