@@ -691,7 +691,8 @@ def moe_combine(rows, row_dst, weights=None, k: int | None = None, add=None, err
 
 def moe_combine_bwd(dout, rows, row_dst, row_src, weights, err: ErrorWord | None = None):
     """(drows [n, d] bf16, dweights [T, k] fp32) of moe_combine from dout [T, d]; rows that hold no routed row
-    (row_src < 0) get zeros.  The gradient of add is dout."""
+    (row_src < 0) get zeros.  The gradient of add is dout.  Two entries of row_dst alike, or maps that are not each other's
+    inverse, are reported in err: the row gets the gradient of the routed row that its row_src names, or zeros."""
     return (_ext or _fast()).moe_combine_bwd(dout, rows, row_dst, row_src, weights, _word(err))
 
 

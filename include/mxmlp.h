@@ -616,8 +616,11 @@ MX_API int mx_token_group(const int32_t* expert_of, int64_t R, int32_t E, int32_
  *   dweights[t, j] = dout[t] . rows[row_dst[t k + j]] [T, k] fp32 out
  *   row_src [n_rows] int32 of the same layout: rows with a negative one hold
  *   no routed row and get zeros.  (The gradient of add is dout.)
+ * The two maps are each other's inverse: a row whose routed row is not placed
+ * there gets zeros, an entry of row_dst whose row holds another routed row (or
+ * that is past n_rows) writes none; either sets MX_ERR_BAD_OFFSETS in err_word.
  * Requirements: d % 8 == 0, 1 <= k <= 32, 16-byte aligned rows, add, out,
- * dout and drows; no two entries of row_dst alike (drows).
+ * dout and drows.
  */
 MX_API int mx_moe_combine(const void* rows, int64_t n_rows, int64_t d, const int32_t* row_dst, int64_t T, int32_t k,
                           const float* weights, const void* add, void* out, int32_t* err_word, void* stream);

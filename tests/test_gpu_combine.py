@@ -74,6 +74,30 @@ def test_rows_that_were_not_placed():
         assert err.value() == 8 and torch.isfinite(again).all()
 
 
+@pytest.mark.parametrize("T", [40, 700])
+def test_maps_that_are_not_inverse(T):
+    """A row that two routed rows name gets the gradient of the one that it holds, one that none names gets zeros; both are
+    reported, and each row is written once."""
+    k, d = 4, 136
+    rows, dst, src, w, _, dout = _case(T, k, d, 7)
+    clean, dw0 = mx.moe_combine_bwd(dout, rows, dst, src, w)
+    two = dst.clone()
+    lost = int(two[5])
+    two[5] = two[9]  # routed rows 5 and 9 name one row; the row that held 5 is named by none
+    err = mx.ErrorWord()
+    drows, dw = mx.moe_combine_bwd(dout, rows, two, src, w, err=err)
+    assert err.value() == 8
+    want = clean.clone()
+    want[lost] = 0
+    assert torch.equal(drows, want)
+    assert torch.equal(dw.view(-1)[6:], dw0.view(-1)[6:])
+    far = src.clone()
+    far[lost] = T * k  # a routed row that there is not
+    err = mx.ErrorWord()
+    drows, _ = mx.moe_combine_bwd(dout, rows, dst, far, w, err=err)
+    assert err.value() == 8 and torch.equal(drows, want)
+
+
 def test_sum_is_the_gradient_of_the_gather():
     """<gather(x), r> = <x, combine(r)> with weights of one, to the outputs' bf16 rounding."""
     T, k, d = 50, 3, 256
