@@ -696,8 +696,9 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
     // ------------------------------------------------------------ epilogue
     regs_take<224>();
     // A warp has 32 tokens and one feature block, the other warp of its scheduler the other: their MMAs come one after the
-    // other, so one adds while the other waits or loads (both on either block's half: 376 us against ...).
-    // Registers are what is short (128 sums, 64 values on their way): barriers by their addresses, and the unit is worked out again for the stores.
+    // other, so one adds while the other waits or loads (both warps on half of either block: 377 us against 364 for 8192 x
+    // 4096 x 14336).  Registers are what is short (128 sums, 64 values on their way): barriers by their addresses, and the
+    // unit is worked out again for the stores.
     const uint32_t half = (uint32_t)(warp - 4) >> 2;
     const uint32_t tb = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * 256;
     const uint32_t bars = smem_u32(acc_full) + half * 16;                      // acc_full, acc_empty
