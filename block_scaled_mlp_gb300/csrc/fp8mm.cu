@@ -156,27 +156,28 @@ struct Unit {
 // Tiles of BT token rows and FT features.
 template <int BT, int FT>
 MX_DEVINL Unit unit_of(const MmParams& p, const int32_t* ends, const int32_t* unit_end, int32_t u) {
+  // u's group: as many as end before u, by blocks of 32 and within one (a warp calls this together)
+  const int lane = threadIdx.x & 31;
+  const int32_t b = 32 * __popc(__ballot_sync(0xFFFFFFFFu, 32 * lane + 31 < p.E && unit_end[min(32 * lane + 31, p.E - 1)] <= u));
+  const int lo = b + __popc(__ballot_sync(0xFFFFFFFFu, b + lane < p.E && unit_end[min(b + lane, p.E - 1)] <= u));
   Unit r;
-  const int32_t f_tiles = (p.F + FT - 1) / FT;
-  int lo = 0, hi = p.E - 1;  // first group whose unit_end is > u
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (unit_end[mid] > u) hi = mid; else lo = mid + 1;
-  }
   r.e = lo;
-  const int32_t v = u - (lo ? unit_end[lo - 1] : 0);
+  const uint32_t f_tiles = (uint32_t)(p.F + FT - 1) / FT;
+  const uint32_t v = u - (lo ? unit_end[lo - 1] : 0);
   const int32_t start = lo ? ends[lo - 1] : 0, rows = ends[lo] - start;
-  const int32_t t_tiles = (rows + BT - 1) / BT;
-  int32_t t, f;
-  if (rows <= p.F) {  // the rows are the smaller operand: re-read them, stream the weights once
-    f = v / t_tiles;
-    t = v - f * t_tiles;
-  } else {
-    t = v / f_tiles;
-    f = v - t * f_tiles;
+  const uint32_t t_tiles = (uint32_t)(rows + BT - 1) / BT;
+  int32_t t = 0, f = v, share = BT;
+  if (t_tiles > 1) {
+    if (rows <= p.F) {  // the rows are the smaller operand: re-read them, stream the weights once
+      f = v / t_tiles;
+      t = v - f * t_tiles;
+    } else {
+      t = v / f_tiles;
+      f = v - t * f_tiles;
+    }
   }
   // narrow tiles: the group's rows shared out evenly, in multiples of 32
-  const int32_t share = BT == 256 ? BT : ((rows + t_tiles - 1) / t_tiles + 31) & ~31;
+  if (BT < 256) share = (((t_tiles > 1 ? (uint32_t)(rows + t_tiles - 1) / t_tiles : rows) + 31) & ~31);
   r.f0 = f * FT;
   r.t0 = (int64_t)start + (int64_t)t * share;
   r.tn = min(share, rows - t * share);
@@ -184,16 +185,21 @@ MX_DEVINL Unit unit_of(const MmParams& p, const int32_t* ends, const int32_t* un
   return r;
 }
 
-// By one warp: group ends, checked, and the running number of work units.
+// By all threads: group ends as they lie.
+MX_DEVINL void load_ends(const MmParams& p, int32_t* ends) {
+  for (int e = threadIdx.x; e < p.E; e += FM_THREADS) ends[e] = p.offs ? __ldg(p.offs + e) : (int32_t)p.M;
+}
+
+// By one warp: group ends checked, and the running number of work units.
 template <int BT, int FT>
-MX_DEVINL void read_ends(const MmParams& p, int32_t* ends, int32_t* unit_end, int* s_ok, int* s_units) {
+MX_DEVINL void read_ends(const MmParams& p, const int32_t* ends, int32_t* unit_end, int* s_ok, int* s_units) {
   const int lane = threadIdx.x & 31;
   const int32_t f_tiles = (p.F + FT - 1) / FT;
   int32_t prev = 0, units = 0;
   bool ok = true;
   for (int base = 0; base < p.E; base += 32) {
     const int e = base + lane;
-    const int32_t v = e >= p.E ? 0x7FFFFFFF : p.offs ? p.offs[e] : (int32_t)p.M;
+    const int32_t v = e >= p.E ? 0x7FFFFFFF : ends[e];
     int32_t before = __shfl_up_sync(0xFFFFFFFFu, v, 1);
     if (lane == 0) before = prev;
     const bool in = e < p.E;
@@ -204,10 +210,7 @@ MX_DEVINL void read_ends(const MmParams& p, int32_t* ends, int32_t* unit_end, in
       const int32_t m = __shfl_up_sync(0xFFFFFFFFu, n, o);
       if (lane >= o) n += m;
     }
-    if (in) {
-      ends[e] = v;
-      unit_end[e] = units + n;
-    }
+    if (in) unit_end[e] = units + n;
     units += __shfl_sync(0xFFFFFFFFu, n, 31);
     prev = __shfl_sync(0xFFFFFFFFu, v, min(31, p.E - 1 - base));
   }
@@ -225,21 +228,6 @@ MX_DEVINL void zero_spare_rows(const MmParams& p, int64_t first, int thread) {
   const int64_t n = (p.M - first) * p.F / 8;
   for (int64_t i = (int64_t)blockIdx.x * (FM_EPI * 32) + thread; i < n; i += (int64_t)gridDim.x * (FM_EPI * 32))
     dst[i] = make_uint4(0, 0, 0, 0);
-}
-
-// 16 values in bf16 with one 32-byte store, or two of 16 bytes where the output is not on 32 bytes.
-MX_DEVINL void store_32b(uint8_t* dst, const f2* v) {
-  uint32_t w[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = f2_to_bf16x2(v[i]);
-  if ((reinterpret_cast<uintptr_t>(dst) & 31) == 0) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
-                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-  } else {
-    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-  }
 }
 
 // ---------------------------------------------------------------- tokens on the N side
@@ -287,6 +275,8 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
   if (S > 1) cluster_sync();  // the others' barriers exist before any remote arrive
   const uint32_t tmem = *tmem_holder;
   pdl_begin();     // all of the above overlaps the kernel before
+  load_ends(p, ends);
+  __syncthreads();
   if (warp == 2) read_ends<BT, 128>(p, ends, unit_end, &s_ok, &s_units);
   __syncthreads();
   const int32_t n_units = s_units;
@@ -524,11 +514,14 @@ struct WCfg {
   static constexpr int TABLE = FM_MAX_E * 8;
   static constexpr int SLOTS = 4;                        // K blocks whose scales are at hand
   static constexpr int SC_BYTES = SLOTS * 256 * 4;       // 128 tokens x 2 feature blocks each
+  static constexpr int EPI_BYTES = FM_EPI * 2048;        // a warp's 32 x 32 bf16 block
+  static constexpr int TILES = 16;                       // tiles that the epilogue is told of by the scales' warps
+  static constexpr int TILE_BYTES = TILES * 2 * 16;
   static constexpr int BUFS = 4;                         // accumulators of 128 columns, two for either feature block
   static constexpr int TMEM = BUFS * 128;
   static constexpr uint32_t IDESC = (1u << 4) | ((128u >> 3) << 17) | ((256u >> 4) << 24);
-  static constexpr int STAGES = (226 * 1024 - SC_BYTES - TABLE - 1536) / TX;
-  static constexpr size_t SMEM = (size_t)STAGES * TX + SC_BYTES + TABLE + 512 /*barriers*/ + 1024 /*align*/;
+  static constexpr int STAGES = (226 * 1024 - EPI_BYTES - SC_BYTES - TILE_BYTES - TABLE - 1536) / TX;
+  static constexpr size_t SMEM = (size_t)STAGES * TX + EPI_BYTES + SC_BYTES + TILE_BYTES + TABLE + 512 /*barriers*/ + 1024 /*align*/;
   static_assert((2 * STAGES + 2 * BUFS + 2) * 8 <= 512, "barriers");
   static_assert(SMEM + 1024 /*static*/ <= 227 * 1024, "shared memory");
 };
@@ -540,8 +533,10 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
   uint8_t* sB = sA + C::STAGES * C::A_BYTES;
-  float* sScale = reinterpret_cast<float*>(sB + C::STAGES * C::B_BYTES);
-  int32_t* ends = reinterpret_cast<int32_t*>(sScale + C::SLOTS * 256);
+  uint8_t* sEpi = sB + C::STAGES * C::B_BYTES;
+  float* sScale = reinterpret_cast<float*>(sEpi + C::EPI_BYTES);
+  int4* sTile = reinterpret_cast<int4*>(sScale + C::SLOTS * 256);
+  int32_t* ends = reinterpret_cast<int32_t*>(sTile + C::TILES * 2);
   int32_t* unit_end = ends + FM_MAX_E;
   uint64_t* full = reinterpret_cast<uint64_t*>(unit_end + FM_MAX_E);
   uint64_t* empty = full + C::STAGES;
@@ -572,6 +567,8 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
   cluster_sync();  // the peer's barriers exist before any remote arrive or pair copy
   const uint32_t tmem = *tmem_holder;
   pdl_begin();     // all of the above overlaps the kernel before
+  load_ends(p, ends);
+  __syncthreads();
   if (warp == 2) read_ends<256, 256>(p, ends, unit_end, &s_ok, &s_units);
   __syncthreads();
   const int32_t n_units = s_units;
@@ -653,7 +650,7 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
       const int half = warp - 2;
       int32_t next_u = unit0, next_kb = 0;
       const float *st = nullptr, *sw = nullptr;
-      int live = 0;
+      int live = 0, tile = 0;
       float s[4][4], f[4];
       auto load = [&](int i) {
         if (next_u >= n_units) return;
@@ -662,6 +659,8 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
           st = p.st + t.t0 + rank * 128 + lane;
           sw = p.sw + t.e * p.sw_e + min((t.f0 >> 7) + half, (p.F - 1) >> 7) * p.sw_f;
           live = t.tn - rank * 128;
+          if (lane == 0) sTile[half * C::TILES + tile] = make_int4((int32_t)t.t0 + rank * 128, live, t.f0, 0);
+          tile = (tile + 1) & (C::TILES - 1);
         }
 #pragma unroll
         for (int c = 0; c < 4; ++c) s[i][c] = lane + 32 * c < live ? __ldg(st + 32 * c) : 0.0f;
@@ -707,6 +706,8 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
     bool ok = true;
     const uint32_t scales = smem_u32(sScale) + (half * 128 + (warp & 3) * 32 + lane) * 4;
     uint32_t slot = 0;
+    uint8_t* stg = sEpi + (warp - 4) * 2048;
+    int tile = 0;
     for (int32_t u = unit0; u < n_units && ok; u += ustep) {
       f2 acc[4][16];
 #pragma unroll
@@ -729,7 +730,7 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
         bool ready = false;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          if (j == 3) ready = mbar_try_wait_at(bars + (BUF ^ 1) * 8, BUF ? ph0 : ph1);
+          if (j == 3 && more) ready = mbar_try_wait_at(bars + (BUF ^ 1) * 8, BUF ? ph0 : ph1);
           tmem_ld_wait(v[j & 1]);
           if (j < 3) {
             tmem_ld_32cols(tb + BUF * 128 + (j + 1) * 32, v[(j + 1) & 1]);
@@ -753,16 +754,31 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
         if (kb + 1 < num_kb && ok) step(std::integral_constant<int, 1>{}, kb + 1);
       }
       if (!ok) break;
-      const Unit t = unit_of<256, 256>(p, ends, unit_end, u);
-      const int32_t r = rank * 128 + (warp & 3) * 32 + lane;   // this lane's row of the tile
-      if (r < t.tn) {
-        const int32_t f = t.f0 + (int32_t)half * 128;
-        uint8_t* dst = p.out + ((t.t0 + r) * p.F + f) * 2;
+      // 32 columns at a time through shared memory (chunks of 16 bytes, in an order that meets no bank twice): a store has
+      // 64 bytes of each of eight rows (lanes that store 32 bytes of their own rows: 2900 cycles a tile).  The tile is known
+      // from the scales' warp, which worked it out ahead (here some 1000 cycles that no MMA runs beside).
+      const int4 t = sTile[half * C::TILES + tile];   // first row, live rows, first feature
+      tile = (tile + 1) & (C::TILES - 1);
+      const int32_t r0 = (warp & 3) * 32, f = t.z + (int32_t)half * 128 + (lane & 3) * 8;
+      uint8_t* dst = p.out + ((int64_t)(t.x + r0 + (lane >> 2)) * p.F + f) * 2;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < 4; ++j) {
+        __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 2; ++i)   // 16 columns: F is a multiple of 16
-            if (f + j * 32 + i * 16 < p.F) store_32b(dst + j * 64 + i * 32, &acc[j][i * 8]);
+        for (int i = 0; i < 4; ++i) {
+          uint32_t w[4];
+#pragma unroll
+          for (int m = 0; m < 4; ++m) w[m] = f2_to_bf16x2(acc[j][4 * i + m]);
+          *reinterpret_cast<uint4*>(stg + lane * 64 + (i ^ ((lane >> 1) & 3)) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = i * 8 + (lane >> 2);
+          if (r0 + r < t.y && f + j * 32 < p.F)
+            *reinterpret_cast<uint4*>(dst + (int64_t)(i * 8) * p.F * 2 + j * 64) =
+                *reinterpret_cast<const uint4*>(stg + r * 64 + ((lane & 3) ^ ((r >> 1) & 3)) * 16);
+        }
       }
     }
     zero_spare_rows(p, s_ok ? ends[p.E - 1] : 0, (warp - 4) * 32 + lane);
