@@ -514,7 +514,8 @@ struct WCfg {
   static constexpr int TABLE = FM_MAX_E * 8;
   static constexpr int SLOTS = 4;                        // K blocks whose scales are at hand
   static constexpr int SC_BYTES = SLOTS * 256 * 4;       // 128 tokens x 2 feature blocks each
-  static constexpr int EPI_BYTES = FM_EPI * 2048;        // a warp's 32 x 32 bf16 block
+  static constexpr int OUTS = 3;                         // 32 x 32 bf16 blocks of a warp on their way out
+  static constexpr int EPI_BYTES = FM_EPI * OUTS * 2048;
   static constexpr int TILES = 16;                       // tiles that the epilogue is told of by the scales' warps
   static constexpr int TILE_BYTES = TILES * 2 * 16;
   static constexpr int BUFS = 4;                         // accumulators of 128 columns, two for either feature block
@@ -527,7 +528,8 @@ struct WCfg {
 };
 
 __global__ void __launch_bounds__(FM_THREADS, 1)
-    fp8_mm_wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, MmParams p) {
+    fp8_mm_wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                       const __grid_constant__ CUtensorMap tmC, MmParams p) {
   using C = WCfg;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -706,7 +708,8 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
     bool ok = true;
     const uint32_t scales = smem_u32(sScale) + (half * 128 + (warp & 3) * 32 + lane) * 4;
     uint32_t slot = 0;
-    uint8_t* stg = sEpi + (warp - 4) * 2048;
+    uint8_t* const stg0 = sEpi + (warp - 4) * (C::OUTS * 2048);
+    uint8_t* stg = stg0;
     int tile = 0;
     for (int32_t u = unit0; u < n_units && ok; u += ustep) {
       f2 acc[4][16];
@@ -754,15 +757,18 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
         if (kb + 1 < num_kb && ok) step(std::integral_constant<int, 1>{}, kb + 1);
       }
       if (!ok) break;
-      // 32 columns at a time through shared memory (chunks of 16 bytes, in an order that meets no bank twice): a store has
-      // 64 bytes of each of eight rows (lanes that store 32 bytes of their own rows: 2900 cycles a tile).  The tile is known
-      // from the scales' warp, which worked it out ahead (here some 1000 cycles that no MMA runs beside).
+      // 32 columns at a time through shared memory (chunks of 16 bytes, in the order of TMA's 64-byte swizzle, which meets no
+      // bank twice), from where TMA takes blocks of 32 live rows.  An SM writes some 20 bytes a cycle, so a tile takes it
+      // 3300 cycles, which the warps need not wait for (32768 rows over 16 of 5120 x 2048: 264 against 274 us with a block a
+      // warp on its way and a stage more for the loads).  The tile is known from the scales' warp, which worked it out ahead
+      // (here some 1000 cycles that no MMA runs beside).
       const int4 t = sTile[half * C::TILES + tile];   // first row, live rows, first feature
       tile = (tile + 1) & (C::TILES - 1);
-      const int32_t r0 = (warp & 3) * 32, f = t.z + (int32_t)half * 128 + (lane & 3) * 8;
-      uint8_t* dst = p.out + ((int64_t)(t.x + r0 + (lane >> 2)) * p.F + f) * 2;
+      const int32_t r0 = (warp & 3) * 32, f = t.z + (int32_t)half * 128;
+      const bool whole = r0 + 32 <= t.y;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
+        if (lane == 0) bulk_wait_read<C::OUTS - 1>();
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -771,16 +777,25 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
           for (int m = 0; m < 4; ++m) w[m] = f2_to_bf16x2(acc[j][4 * i + m]);
           *reinterpret_cast<uint4*>(stg + lane * 64 + (i ^ ((lane >> 1) & 3)) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
         }
+        if (whole) fence_async_smem();
         __syncwarp();
+        if (whole) {
+          if (lane == 0 && f + j * 32 < p.F) tma_store_2d(&tmC, stg, f + j * 32, t.x + r0);
+        } else {
+          const int32_t c = f + j * 32 + (lane & 3) * 8;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = i * 8 + (lane >> 2);
-          if (r0 + r < t.y && f + j * 32 < p.F)
-            *reinterpret_cast<uint4*>(dst + (int64_t)(i * 8) * p.F * 2 + j * 64) =
-                *reinterpret_cast<const uint4*>(stg + r * 64 + ((lane & 3) ^ ((r >> 1) & 3)) * 16);
+          for (int i = 0; i < 4; ++i) {
+            const int r = i * 8 + (lane >> 2);
+            if (r0 + r < t.y && c < p.F)
+              *reinterpret_cast<uint4*>(p.out + ((int64_t)(t.x + r0 + r) * p.F + c) * 2) =
+                  *reinterpret_cast<const uint4*>(stg + r * 64 + ((lane & 3) ^ ((r >> 1) & 3)) * 16);
+          }
         }
+        if (lane == 0) bulk_commit();
+        stg = stg == stg0 + (C::OUTS - 1) * 2048 ? stg0 : stg + 2048;
       }
     }
+    if (lane == 0) bulk_wait<0>();
     zero_spare_rows(p, s_ok ? ends[p.E - 1] : 0, (warp - 4) * 32 + lane);
     __syncwarp();
   }
@@ -792,11 +807,10 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
   if (warp == 1) tmem_dealloc_pair(tmem, C::TMEM);
 }
 
-using Kernel = void (*)(CUtensorMap, CUtensorMap, MmParams);
 
 // Clusters of a kernel that can be resident at once (none, if no part of the device holds one), by device; KIND tells the
 // kernels apart.  A kernel's register split needs the registers that it was written for.
-template <int KIND>
+template <int KIND, class Kernel>
 int resident_clusters(Kernel k, size_t smem, int ctas, int* n) {
   static std::atomic<int> resident[64];  // the number + 1, once known; any thread may be the one that asks
   int dev = 0;
@@ -837,10 +851,9 @@ int64_t tile_bound(const MmParams& p, int bt) {
 }
 
 // KIND tells the kernels apart; ctas: of a cluster.  whole: a cluster has one tile at most (S > 1: its buffer for the
-// other pairs' sums is written once).
-template <int KIND>
-int launch_cfg(Kernel k, size_t smem, int bt, int ctas, bool whole, const CUtensorMap& tA, const CUtensorMap& tB, const MmParams& p,
-               cudaStream_t stream) {
+// other pairs' sums is written once).  args: the kernel's.
+template <int KIND, class... A>
+int launch_cfg(void (*k)(A...), size_t smem, int bt, int ctas, bool whole, const MmParams& p, cudaStream_t stream, const A&... args) {
   const int64_t units = tile_bound(p, bt);
   if (units > INT32_MAX / 8) return fail(MX_ERR_UNSUPPORTED, "FP8 product: too many tiles");
   int nres = 0;
@@ -850,7 +863,7 @@ int launch_cfg(Kernel k, size_t smem, int bt, int ctas, bool whole, const CUtens
   if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute");
   const int64_t clusters = std::max<int64_t>(1, whole ? units : std::min<int64_t>(units, nres));
   count_launch(MX_KERNEL_FP8_BLOCK);
-  return cuda_status(launch_overlapped(k, (unsigned)(ctas * clusters), FM_THREADS, smem, stream, ctas, tA, tB, p), "FP8 product launch");
+  return cuda_status(launch_overlapped(k, (unsigned)(ctas * clusters), FM_THREADS, smem, stream, ctas, args...), "FP8 product launch");
 }
 
 // Token rows to a tile (256: tokens on the M side, CTA pairs) and CTAs to a tile's contraction.
@@ -904,10 +917,17 @@ int launch_fp8_block_mm(const Fp8MmLaunch& g, cudaStream_t stream) {
   rc = make_tmap(&w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(g.w), dw, sw, bw, CU_TENSOR_MAP_SWIZZLE_128B);
   if (!rc) rc = make_tmap(&a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(g.a), da, sa, ba, CU_TENSOR_MAP_SWIZZLE_128B);
   if (rc) return rc;
-  if (wide) return launch_cfg<2561>(fp8_mm_wide_kernel, WCfg::SMEM, 256, 2, false, a, w, p, stream);
+  if (wide) {
+    CUtensorMap c;
+    uint64_t dc[2] = {(uint64_t)p.F, (uint64_t)p.M}, sc[1] = {(uint64_t)p.F * 2};
+    uint32_t bc[2] = {32, 32};
+    rc = make_tmap(&c, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.c, dc, sc, bc, CU_TENSOR_MAP_SWIZZLE_64B);
+    if (rc) return rc;
+    return launch_cfg<2561>(fp8_mm_wide_kernel, WCfg::SMEM, 256, 2, false, p, stream, a, w, c, p);
+  }
 #define MX_NARROW(BT, S)                                                                                            \
   if (s.bt == BT && s.share == S)                                                                                   \
-    return launch_cfg<BT * 10 + S>(fp8_mm_narrow_kernel<BT, S>, FCfg<BT, S>::SMEM, BT, S, S > 1, w, a, p, stream);
+    return launch_cfg<BT * 10 + S>(fp8_mm_narrow_kernel<BT, S>, FCfg<BT, S>::SMEM, BT, S, S > 1, p, stream, w, a, p);
   MX_NARROW(32, 1) MX_NARROW(32, 2) MX_NARROW(32, 4) MX_NARROW(64, 1) MX_NARROW(64, 2) MX_NARROW(128, 1)
 #undef MX_NARROW
   return fail(MX_ERR_UNSUPPORTED, "FP8 product: no kernel for the shape");
