@@ -17,9 +17,9 @@
 //   Few rows: tokens on the N side (any multiple of 32 at run time), features on the M side, so that a group's last tile
 // costs what its rows cost; one CTA a tile, or several that share its contraction.
 //
-// On a GB300 (twice the bf16 library rate: 3.9 PFLOP/s; copies 6.78 TB/s): 8192 x 4096 x 14336 310 us (3.1 PFLOP/s; 2.65 in
-// long runs, by the power limit), 131072 rows over 64 experts of 4096 x 7168 both ways 6.15 ms (2.5 PFLOP/s); 64 rows over 64
-// of them, 31 hit, 147 us (6.2 TB/s of weights); 8 rows of 4096 x 7168 9.8 us.
+// On a GB300 (twice the bf16 library rate: 3.9 PFLOP/s; copies 6.78 TB/s): 8192 x 4096 x 14336 309 us (3.1 PFLOP/s; 2.7 in
+// long runs, by the power limit), 131072 rows over 64 experts of 4096 x 7168 both ways 5.95 ms (2.6 PFLOP/s); 64 rows over 64
+// of them, 31 hit, 141 us (6.5 TB/s of weights); 8 rows of 4096 x 7168 9.4 us; 800 rows over 8 of 2048 x 2048 12.5 us.
 #include <atomic>
 #include <type_traits>
 
@@ -51,7 +51,7 @@ struct FCfg {
   static constexpr uint32_t IDESC = (1u << 4) | ((128u >> 4) << 24);
   static constexpr int STAGES = (226 * 1024 - EPI_BYTES - SC_BYTES - PARTS - TABLE - 1536) / TX;
   static constexpr size_t SMEM = (size_t)STAGES * TX + EPI_BYTES + SC_BYTES + PARTS + TABLE + 512 /*barriers*/ + 1024 /*align*/;
-  static_assert(BT == 128 || BT == 64 || BT == 32, "tile widths");
+  static_assert(BT == 64 || BT == 32, "tile widths");
   static_assert(S == 1 || S == 2 || S == 4, "CTAs of a cluster");
   static_assert(STAGES >= 3, "shared memory");
   static_assert((2 * STAGES + 2 * BUFS + 2 + FM_EPI) * 8 <= 512, "barriers");
@@ -396,8 +396,7 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
     regs_take<208>();
     const int ew = warp - 4, q = warp & 3, half = ew >> 2;
     uint8_t* stg = sEpi + ew * 2048;
-    constexpr int NC = BT <= 64 ? 1 : BT / 64;   // blocks of 32 columns a warp
-    auto col_of = [half](int j) { return (2 * j + half) * 32; };
+    const int c = half * 32;                     // this warp's columns (BT = 32: half of the warps have none)
     const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16);
     const int qr = lane >> 2, qc = (lane & 3) * 8;
     const uint32_t full_at = smem_u32(acc_full), scales = smem_u32(sScale);
@@ -406,32 +405,25 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
     for (int32_t u = unit0; u < n_units && ok; u += ustep) {
       const Unit t = unit_of<BT, 128>(p, ends, unit_end, u);
       const int32_t f = t.f0 + q * 32;   // this warp's features
-      f2 acc[NC][16];
+      const bool here = c < t.tn;
+      f2 acc[16];
 #pragma unroll
-      for (int j = 0; j < NC; ++j)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[j][i] = f2_splat(0.0f);
+      for (int i = 0; i < 16; ++i) acc[i] = f2_splat(0.0f);
       for (int kb = 0; kb < num_kb; ++kb) {
         ok = warp_wait_at(full_at + buf * 8, buf_phase, p.err);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t at = tb + (uint32_t)(buf * BT), sc = scales + buf * (BT * 4);
-        // a block of 32 columns is loaded while the one before it is added
-        uint32_t v[2][32];
-        if (col_of(0) < t.tn) tmem_ld_32cols(at + col_of(0), v[0]);
+        if (here) {
+          const uint32_t sc = scales + (buf * BT + c) * 4;
+          uint32_t v[32];
+          tmem_ld_32cols(tb + (uint32_t)(buf * BT + c), v);
+          tmem_ld_wait(v);
 #pragma unroll
-        for (int j = 0; j < NC; ++j) {
-          const bool here = col_of(j) < t.tn;
-          if (here) tmem_ld_wait(v[j & 1]);
-          if (j + 1 < NC && col_of(j + 1) < t.tn) tmem_ld_32cols(at + col_of(j + 1), v[(j + 1) & 1]);
-          if (here) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              float4 m;
-              asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(m.x), "=f"(m.y), "=f"(m.z), "=f"(m.w) : "r"(sc + (col_of(j) + 4 * i) * 4));
-              fma_here(acc[j][2 * i], v[j & 1][4 * i], v[j & 1][4 * i + 1], m.x, m.y);
-              fma_here(acc[j][2 * i + 1], v[j & 1][4 * i + 2], v[j & 1][4 * i + 3], m.z, m.w);
-            }
+          for (int i = 0; i < 8; ++i) {
+            float4 m;
+            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(m.x), "=f"(m.y), "=f"(m.z), "=f"(m.w) : "r"(sc + i * 16));
+            fma_here(acc[2 * i], v[4 * i], v[4 * i + 1], m.x, m.y);
+            fma_here(acc[2 * i + 1], v[4 * i + 2], v[4 * i + 3], m.z, m.w);
           }
         }
         tc_fence_before();
@@ -439,21 +431,18 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
         if (lane == 0) mbar_arrive(&acc_empty[buf]);
         if (++buf == C::BUFS) { buf = 0; buf_phase ^= 1; }
       }
-      if (!ok || f >= p.F) continue;
-      if constexpr (S > 1) if (col_of(0) < t.tn) {
-        // the other CTAs' sums to the first, which adds them in order: 8 vectors of 4 tokens a lane and block of columns
+      if (!ok || f >= p.F || !here) continue;
+      if constexpr (S > 1) {
+        // the other CTAs' sums to the first, which adds them in order: 8 vectors of 4 tokens a lane
         const uint32_t at = (uint32_t)((BT == 32 ? q : ew) * 32 + lane) * 16;
         constexpr int V_STEP = (BT == 32 ? 4 : 8) * 512;
         if (part) {
           const uint32_t dst = cluster_map(smem_u32(sParts), 0) + (part - 1) * C::PART + at;
 #pragma unroll
-          for (int j = 0; j < NC; ++j)
-            if (col_of(j) < t.tn)
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (j * 8 + i) * V_STEP),
-                             "f"(acc[j][2 * i].x), "f"(acc[j][2 * i].y), "f"(acc[j][2 * i + 1].x), "f"(acc[j][2 * i + 1].y)
-                             : "memory");
+          for (int i = 0; i < 8; ++i)
+            asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(dst + i * V_STEP), "f"(acc[2 * i].x),
+                         "f"(acc[2 * i].y), "f"(acc[2 * i + 1].x), "f"(acc[2 * i + 1].y)
+                         : "memory");
           mbar_arrive_cluster(cluster_map(smem_u32(&parts_bar[ew]), 0));
           continue;
         }
@@ -462,36 +451,27 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
 #pragma unroll 1
         for (int o = 0; o < S - 1; ++o)
 #pragma unroll
-          for (int j = 0; j < NC; ++j)
-            if (col_of(j) < t.tn)
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float4 v = *reinterpret_cast<const float4*>(sParts + o * C::PART + at + (j * 8 + i) * V_STEP);
-                acc[j][2 * i] = f2_add(acc[j][2 * i], f2_pack(v.x, v.y));
-                acc[j][2 * i + 1] = f2_add(acc[j][2 * i + 1], f2_pack(v.z, v.w));
-              }
-      }
-      // a block of 32 tokens; a lane has one feature of all of them: turned through shared memory
-#pragma unroll
-      for (int j = 0; j < NC; ++j) {
-        const int c = col_of(j);
-        if (c < t.tn) {
-          uint8_t* dst = p.out + ((t.t0 + c + qr) * p.F + f + qc) * 2;
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const uint32_t v = f2_to_bf16x2(acc[j][i]);
-            *reinterpret_cast<uint16_t*>(stg + (2 * i) * 64 + lane * 2) = (uint16_t)v;
-            *reinterpret_cast<uint16_t*>(stg + (2 * i + 1) * 64 + lane * 2) = (uint16_t)(v >> 16);
+          for (int i = 0; i < 8; ++i) {
+            const float4 v = *reinterpret_cast<const float4*>(sParts + o * C::PART + at + i * V_STEP);
+            acc[2 * i] = f2_add(acc[2 * i], f2_pack(v.x, v.y));
+            acc[2 * i + 1] = f2_add(acc[2 * i + 1], f2_pack(v.z, v.w));
           }
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (c + i * 8 + qr < t.tn && f + qc < p.F)
-              *reinterpret_cast<uint4*>(dst + (int64_t)(i * 8) * p.F * 2) =
-                  *reinterpret_cast<const uint4*>(stg + (i * 8 + qr) * 64 + (lane & 3) * 16);
-        }
       }
+      // a lane has one feature of all 32 tokens: turned through shared memory
+      uint8_t* dst = p.out + ((t.t0 + c + qr) * p.F + f + qc) * 2;
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t v = f2_to_bf16x2(acc[i]);
+        *reinterpret_cast<uint16_t*>(stg + (2 * i) * 64 + lane * 2) = (uint16_t)v;
+        *reinterpret_cast<uint16_t*>(stg + (2 * i + 1) * 64 + lane * 2) = (uint16_t)(v >> 16);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c + i * 8 + qr < t.tn && f + qc < p.F)
+          *reinterpret_cast<uint4*>(dst + (int64_t)(i * 8) * p.F * 2) =
+              *reinterpret_cast<const uint4*>(stg + (i * 8 + qr) * 64 + (lane & 3) * 16);
     }
     zero_spare_rows(p, s_ok ? ends[p.E - 1] : 0, ew * 32 + lane);
     __syncwarp();
@@ -871,11 +851,11 @@ int launch_cfg(void (*k)(A...), size_t smem, int bt, int ctas, bool whole, const
 // one group, us with one, two and four CTAs: 4096 x 7168 18.2, 12.4, 9.8; 512 x 7168 17.4, 11.3, 8.2; 7168 x 2048 7.5, 7.3
 // and, in two waves, 12.5; 1024 x 1024 5.1, 5.4, 5.3; 128 rows of 4096 x 7168 by 64 19.8, 14.0).
 //   Small tiles while they are one wave or the weights' bytes count, large ones where the tensor cores or the rows' bytes do.
-// us with 32 / 64 / 128 / 256: 512 rows of one 1024 x 1024 5.7 / 5.9 / 7.6 / 11.7; 1000 of one 1024 x 4096 - / 13.0 / 18.3 /
-// 19.0; 2048 of one 2048 x 2048 - / - / 20.2 / 15.8; 64 over 64 of 4096 x 7168 147 / 147 / 151 / 166; 1024 over 64 of 2048 x
-// 2048 47.5 / 46.0 / 47.0 / 56.6; 256 over 8 of it 14.0 / 12.2 / 11.2 / 16.0; 800 over 8 23.7 / 15.2 / 15.7 / 17.0; 2041 over
-// 16 of 1424 x 1008 21.0 / 15.4 / 14.2 / 18.4; 3000 over 64 of 4096 x 2048 139 / 103 / 99 / 111; 6000 over 64 of it 235 / 151 /
-// 134 / 121; 4096 over 16 of 5120 x 8192 626 / 356 / 303 / 191.
+// us with 32 / 64 / 256 (128 of the first kind was ahead for groups of 96 rows only, by 3 to 6%): 512 rows of one 1024 x 1024
+// 5.5 / 5.7 / 7.8; 1000 of one 1024 x 4096 - / 11.5 / 15.3; 2048 of one 2048 x 2048 - / - / 12.0; 64 over 64 of 4096 x 7168
+// 146 / 144 / 163; 1024 over 64 of 2048 x 2048 45.1 / 43.8 / 51.9; 256 over 8 of it 12.0 / 10.7 / 11.6; 800 over 8 19.7 / 13.3 /
+// 12.4; 2041 over 16 of 1424 x 1008 18.1 / 13.5 / 13.8, of 1008 x 1424 16.7 / 13.9 / 10.9; 1000 over 16 of 5120 x 8192 161 / 122 /
+// 129; 4096 over 16 499 / 288 / 193; 3000 over 64 of 4096 x 2048 111 / 92 / 108; 6000 over 64 184 / 122 / 115.
 struct TokenShape {
   int bt, share;
 };
@@ -884,13 +864,12 @@ int token_shape(const MmParams& p, TokenShape* s) {
   if ((rc = resident_clusters<642>(fp8_mm_narrow_kernel<64, 2>, FCfg<64, 2>::SMEM, 2, &n2)) ||
       (rc = resident_clusters<324>(fp8_mm_narrow_kernel<32, 4>, FCfg<32, 4>::SMEM, 4, &n4)))
     return rc;
-  const int64_t t32 = tile_bound(p, 32), t64 = tile_bound(p, 64), t128 = tile_bound(p, 128), n1 = num_sms();
+  const int64_t t32 = tile_bound(p, 32), t64 = tile_bound(p, 64), n1 = num_sms();
   if (p.C >= 2048 && t32 <= n4) *s = TokenShape{32, 4};
   else if (p.C >= 2048 && t32 <= n2) *s = TokenShape{32, 2};
   else if (p.C >= 2048 && t64 <= n2) *s = TokenShape{64, 2};
-  else if (t32 <= n1 || p.M <= 16 * (int64_t)p.E) *s = TokenShape{32, 1};
-  else if (t64 <= n1 || p.M <= 24 * (int64_t)p.E) *s = TokenShape{64, 1};
-  else if (p.M <= 64 * (int64_t)p.E || (p.M <= 256 * (int64_t)p.E && t128 <= 3 * n1)) *s = TokenShape{128, 1};
+  else if (t32 <= n1) *s = TokenShape{32, 1};
+  else if (t64 <= n1 || p.M <= 64 * (int64_t)p.E) *s = TokenShape{64, 1};
   else *s = TokenShape{256, 1};
   return MX_OK;
 }
@@ -928,7 +907,7 @@ int launch_fp8_block_mm(const Fp8MmLaunch& g, cudaStream_t stream) {
 #define MX_NARROW(BT, S)                                                                                            \
   if (s.bt == BT && s.share == S)                                                                                   \
     return launch_cfg<BT * 10 + S>(fp8_mm_narrow_kernel<BT, S>, FCfg<BT, S>::SMEM, BT, S, S > 1, p, stream, w, a, p);
-  MX_NARROW(32, 1) MX_NARROW(32, 2) MX_NARROW(32, 4) MX_NARROW(64, 1) MX_NARROW(64, 2) MX_NARROW(128, 1)
+  MX_NARROW(32, 1) MX_NARROW(32, 2) MX_NARROW(32, 4) MX_NARROW(64, 1) MX_NARROW(64, 2)
 #undef MX_NARROW
   return fail(MX_ERR_UNSUPPORTED, "FP8 product: no kernel for the shape");
 }
