@@ -196,6 +196,17 @@ def test_long_contractions(counts, N, K):
     _check(counts, 3, N, K, sum(counts) + K)
 
 
+# More than 64 rows a group and more small tiles than SMs: tiles of 256 x 256, in one or several waves, of an even and odd
+# number of K blocks, the last features and rows of each in all places.
+@pytest.mark.parametrize("counts,spare", [([300, 1, 0, 700, 31], 7), ([129, 0, 255, 256, 257, 640, 33, 31], 0), ([1000, 1500, 500], 45),
+                                          ([2000], 0)])
+@pytest.mark.parametrize("N,K", [(1424, 48), (1424, 272), (2064, 400), (2304, 640), (272, 1424), (1552, 16), (400, 2064)])
+def test_large_tiles(counts, spare, N, K):
+    out, dx = _check(counts, spare, N, K, sum(counts) + N + K)
+    again = _check(counts, spare, N, K, sum(counts) + N + K)
+    assert torch.equal(out, again[0]) and torch.equal(dx, again[1])
+
+
 @pytest.mark.parametrize("counts,spare", [([5, 9, 0, 2], 77), ([0, 0], 40), ([700, 20], 1), ([3] * 40, 5), ([0] * 7, 9)])
 def test_spare_rows_are_zero(counts, spare):
     _check(counts, spare, 144, 208, 3)
@@ -230,9 +241,10 @@ def test_scales_of_very_different_size():
     _close(mx.fp8_block_mm(q, w), X @ W.t(), X.abs() @ W.abs().t(), K)
 
 
-@pytest.mark.parametrize("counts", [[40, 23, 50], [200, 300, 90], [3, 5, 2]])
-def test_other_groups_and_spare_rows_do_not_leak(counts):
-    x, dout, w, offs = _case(counts, 30, 272, 336, 5)
+@pytest.mark.parametrize("counts,N,K", [([40, 23, 50], 272, 336), ([200, 300, 90], 272, 336), ([3, 5, 2], 272, 336),
+                                        ([700, 500, 290], 1424, 336), ([700, 500, 290], 336, 1424)])
+def test_other_groups_and_spare_rows_do_not_leak(counts, N, K):
+    x, dout, w, offs = _case(counts, 30, N, K, 5)
     clean = mx.fp8_block_mm(x, w, offs), mx.fp8_block_mm_dgrad(dout, w, offs)
     a, b = offs[0].item(), offs[1].item()
     for t in (x, dout):
