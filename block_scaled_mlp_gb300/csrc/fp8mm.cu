@@ -74,6 +74,14 @@ MX_DEVINL void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// Four values into another CTA of the cluster, counted by a barrier there: the sender waits for nothing (stores and an arrival
+// that releases them take it 2000 cycles).
+MX_DEVINL void st_async_4(uint32_t dst, f2 a, f2 b, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(dst), "f"(a.x),
+               "f"(a.y), "f"(b.x), "f"(b.y), "r"(bar)
+               : "memory");
+}
+
 // warp_wait by the barrier's shared memory address.
 MX_DEVINL bool mbar_try_wait_at(uint32_t bar, uint32_t parity) {
   uint32_t ok;
@@ -187,7 +195,15 @@ MX_DEVINL Unit unit_of(const MmParams& p, const int32_t* ends, const int32_t* un
 
 // By all threads: group ends as they lie.
 MX_DEVINL void load_ends(const MmParams& p, int32_t* ends) {
-  for (int e = threadIdx.x; e < p.E; e += FM_THREADS) ends[e] = p.offs ? __ldg(p.offs + e) : (int32_t)p.M;
+  for (int e = threadIdx.x; e < p.E; e += FM_THREADS) ends[e] = __ldg(p.offs + e);
+}
+
+// By one thread, without group ends: one group of all rows.
+template <int BT, int FT>
+MX_DEVINL void one_group(const MmParams& p, int32_t* ends, int32_t* unit_end, int* s_ok, int* s_units) {
+  ends[0] = (int32_t)p.M;
+  *s_units = unit_end[0] = (int32_t)((p.M + BT - 1) / BT) * ((p.F + FT - 1) / FT);
+  *s_ok = 1;
 }
 
 // By one warp: group ends checked, and the running number of work units.
@@ -264,21 +280,26 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
     for (int a = 0; a < C::BUFS; ++a) { mbar_init(&acc_full[a], 2); mbar_init(&acc_empty[a], FM_EPI); }
-    for (int e = 0; e < FM_EPI; ++e) mbar_init(&parts_bar[e], S > 1 ? 32 * (S - 1) : 1);
+    for (int e = 0; e < FM_EPI; ++e) mbar_init(&parts_bar[e], 1);
     mbar_init(done_bar, 1);
     fence_mbar_init();
   }
+  if (threadIdx.x == 96 && !p.offs) one_group<BT, 128>(p, ends, unit_end, &s_ok, &s_units);
   if (warp == 1) { tmem_alloc(tmem_holder, C::TMEM); tmem_relinquish(); }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (S > 1) cluster_sync();  // the others' barriers exist before any remote arrive
   const uint32_t tmem = *tmem_holder;
-  pdl_begin();     // all of the above overlaps the kernel before
-  load_ends(p, ends);
-  __syncthreads();
-  if (warp == 2) read_ends<BT, 128>(p, ends, unit_end, &s_ok, &s_units);
-  __syncthreads();
+  if (p.offs) {
+    pdl_begin();     // all of the above overlaps the kernel before
+    load_ends(p, ends);
+    __syncthreads();
+    if (warp == 2) read_ends<BT, 128>(p, ends, unit_end, &s_ok, &s_units);
+    __syncthreads();
+  } else {
+    pdl_allow_next();   // the warps that load and store wait, when they have worked out where
+  }
   const int32_t n_units = s_units;
 
   if (warp < 4) {
@@ -294,6 +315,7 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
       bool ok = true;
       for (int32_t u = unit0; u < n_units && ok; u += ustep) {
         const Unit t = unit_of<BT, 128>(p, ends, unit_end, u);
+        if (!p.offs && u == unit0) pdl_wait();
         for (int kb = 0; kb < num_kb; ++kb) {
           if (!warp_wait(&empty[stage], phase ^ 1, p.err)) { ok = false; break; }
           if (leader) {
@@ -361,6 +383,7 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
           w = p.sw + t.e * p.sw_e + (t.f0 >> 7) * p.sw_f + (kb0 + next_kb) * p.sw_c;
           live = t.tn - lane;
           fresh = false;
+          if (!p.offs && next_u == unit0) pdl_wait();
         }
 #pragma unroll
         for (int c = 0; c < PER; ++c) s[i][c] = 32 * c < live ? __ldg(st + 32 * c) : 0.0f;
@@ -395,6 +418,7 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
     // ------------------------------------------------------------ epilogue
     regs_take<208>();
     const int ew = warp - 4, q = warp & 3, half = ew >> 2;
+    if (!p.offs) pdl_wait();
     uint8_t* stg = sEpi + ew * 2048;
     const int c = half * 32;                     // this warp's columns (BT = 32: half of the warps have none)
     const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16);
@@ -438,16 +462,18 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
         constexpr int V_STEP = (BT == 32 ? 4 : 8) * 512;
         if (part) {
           const uint32_t dst = cluster_map(smem_u32(sParts), 0) + (part - 1) * C::PART + at;
+          const uint32_t bar = cluster_map(smem_u32(&parts_bar[ew]), 0);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(dst + i * V_STEP), "f"(acc[2 * i].x),
-                         "f"(acc[2 * i].y), "f"(acc[2 * i + 1].x), "f"(acc[2 * i + 1].y)
-                         : "memory");
-          mbar_arrive_cluster(cluster_map(smem_u32(&parts_bar[ew]), 0));
+          for (int i = 0; i < 8; ++i) st_async_4(dst + i * V_STEP, acc[2 * i], acc[2 * i + 1], bar);
           continue;
         }
+        if (lane == 0) mbar_arrive_expect_tx(&parts_bar[ew], (S - 1) * 32 * 128);
+        __syncwarp();
         ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&parts_bar[ew], 0, p.err));
-        if (!ok) break;
+        if (!ok) {
+          mbar_wait_cluster(&parts_bar[ew], 0, p.err);   // once more for what may still come, before this CTA leaves
+          break;
+        }
 #pragma unroll 1
         for (int o = 0; o < S - 1; ++o)
 #pragma unroll
@@ -542,17 +568,22 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
     mbar_init(done_bar, 1);
     fence_mbar_init();
   }
+  if (threadIdx.x == 96 && !p.offs) one_group<256, 256>(p, ends, unit_end, &s_ok, &s_units);
   if (warp == 1) { tmem_alloc_pair(tmem_holder, C::TMEM); tmem_relinquish_pair(); }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   cluster_sync();  // the peer's barriers exist before any remote arrive or pair copy
   const uint32_t tmem = *tmem_holder;
-  pdl_begin();     // all of the above overlaps the kernel before
-  load_ends(p, ends);
-  __syncthreads();
-  if (warp == 2) read_ends<256, 256>(p, ends, unit_end, &s_ok, &s_units);
-  __syncthreads();
+  if (p.offs) {
+    pdl_begin();     // all of the above overlaps the kernel before
+    load_ends(p, ends);
+    __syncthreads();
+    if (warp == 2) read_ends<256, 256>(p, ends, unit_end, &s_ok, &s_units);
+    __syncthreads();
+  } else {
+    pdl_allow_next();   // the warps that load and store wait, when they have worked out where
+  }
   const int32_t n_units = s_units;
 
   if (warp < 4) {
@@ -569,6 +600,7 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
       for (int32_t u = unit0; u < n_units && ok; u += ustep) {
         const Unit t = unit_of<256, 256>(p, ends, unit_end, u);
         const int32_t row = (int32_t)t.t0 + rank * 128, f = t.f0 + rank * 64;
+        if (!p.offs && u == unit0) pdl_wait();
         for (int kb = 0; kb < num_kb; ++kb) {
           if (!warp_wait(&empty[stage], phase ^ 1, p.err)) { ok = false; break; }
           if (leader) {
@@ -643,6 +675,7 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
           live = t.tn - rank * 128;
           if (lane == 0) sTile[half * C::TILES + tile] = make_int4((int32_t)t.t0 + rank * 128, live, t.f0, 0);
           tile = (tile + 1) & (C::TILES - 1);
+          if (!p.offs && next_u == unit0) pdl_wait();
         }
 #pragma unroll
         for (int c = 0; c < 4; ++c) s[i][c] = lane + 32 * c < live ? __ldg(st + 32 * c) : 0.0f;
@@ -681,6 +714,7 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
     // 4096 x 14336).  Registers are what is short (128 sums, 64 values on their way): barriers by their addresses, and the
     // unit is worked out again for the stores.
     const uint32_t half = (uint32_t)(warp - 4) >> 2;
+    if (!p.offs) pdl_wait();
     const uint32_t tb = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * 256;
     const uint32_t bars = smem_u32(acc_full) + half * 16;                      // acc_full, acc_empty
     const uint32_t give = cluster_map(bars + C::BUFS * 8, 0);                  // the even CTA's acc_empty
