@@ -19,7 +19,7 @@
 //
 // On a GB300 (twice the bf16 library rate: 3.9 PFLOP/s; copies 6.78 TB/s): 8192 x 4096 x 14336 309 us (3.1 PFLOP/s; 2.7 in
 // long runs, by the power limit), 131072 rows over 64 experts of 4096 x 7168 both ways 5.95 ms (2.6 PFLOP/s); 64 rows over 64
-// of them, 31 hit, 141 us (6.5 TB/s of weights); 8 rows of 4096 x 7168 9.4 us; 800 rows over 8 of 2048 x 2048 12.5 us.
+// of them, 31 hit, 144 us (6.3 TB/s of weights); 8 rows of 4096 x 7168 8.3 us (9.4 from HBM); 800 rows over 8 of 2048 x 2048 12.5 us.
 #include <atomic>
 #include <type_traits>
 
@@ -881,15 +881,15 @@ int launch_cfg(void (*k)(A...), size_t smem, int bt, int ctas, bool whole, const
 }
 
 // Token rows to a tile (256: tokens on the M side, CTA pairs) and CTAs to a tile's contraction.
-//   Few tiles: an SM takes in some 110 GB/s, so a long contraction is shared by the CTAs of a cluster, in one wave (8 rows of
-// one group, us with one, two and four CTAs: 4096 x 7168 18.2, 12.4, 9.8; 512 x 7168 17.4, 11.3, 8.2; 7168 x 2048 7.5, 7.3
-// and, in two waves, 12.5; 1024 x 1024 5.1, 5.4, 5.3; 128 rows of 4096 x 7168 by 64 19.8, 14.0).
+//   Few tiles: an SM takes in some 50 bytes a cycle, so a long contraction is shared by the CTAs of a cluster, in one wave (8
+// rows of one group, us with one, two and four CTAs: 4096 x 7168 14.5, 9.7, 8.3; 512 x 7168 14.0, 9.0, 6.6; 7168 x 2048 5.9,
+// 5.7; 1024 x 1024 4.1, 4.0, 4.2; 128 rows of 4096 x 7168 by 64 16.0, 11.7).
 //   Small tiles while they are one wave or the weights' bytes count, large ones where the tensor cores or the rows' bytes do.
 // us with 32 / 64 / 256 (128 of the first kind was ahead for groups of 96 rows only, by 3 to 6%): 512 rows of one 1024 x 1024
-// 5.5 / 5.7 / 7.8; 1000 of one 1024 x 4096 - / 11.5 / 15.3; 2048 of one 2048 x 2048 - / - / 12.0; 64 over 64 of 4096 x 7168
-// 146 / 144 / 163; 1024 over 64 of 2048 x 2048 45.1 / 43.8 / 51.9; 256 over 8 of it 12.0 / 10.7 / 11.6; 800 over 8 19.7 / 13.3 /
-// 12.4; 2041 over 16 of 1424 x 1008 18.1 / 13.5 / 13.8, of 1008 x 1424 16.7 / 13.9 / 10.9; 1000 over 16 of 5120 x 8192 161 / 122 /
-// 129; 4096 over 16 499 / 288 / 193; 3000 over 64 of 4096 x 2048 111 / 92 / 108; 6000 over 64 184 / 122 / 115.
+// 4.7 / 4.7 / 6.4; 1000 of one 1024 x 4096 - / 10.5 / 13.6; 2048 of one 2048 x 2048 - / - / 10.3; 64 over 64 of 4096 x 7168
+// 146 / 144 / 166; 1024 over 64 of 2048 x 2048 45.3 / 43.7 / 54.8; 256 over 8 of it 12.2 / 10.7 / 11.5; 800 over 8 19.7 / 13.5 /
+// 12.4; 2041 over 16 of 1424 x 1008 18.2 / 13.8 / 13.9, of 1008 x 1424 16.7 / 13.8 / 10.9; 1000 over 16 of 5120 x 8192 162 / 123 /
+// 129; 4096 over 16 500 / 288 / 187; 3000 over 64 of 4096 x 2048 111 / 92 / 108; 6000 over 64 183 / 122 / 115.
 struct TokenShape {
   int bt, share;
 };
