@@ -219,7 +219,7 @@ def test_many_experts():
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 16, 16), (1, 512, 1024), (31, 272, 144), (64, 1024, 2048), (200, 128, 128), (513, 384, 656),
-                                   (2048, 1024, 512)])
+                                   (2048, 1024, 512), (12001, 16, 144), (144, 12016, 48), (10000, 48, 272)])
 def test_dense_products(M, N, K):
     x, dout, w, offs = _case([M], 0, N, K, M + N)
     out, dx = mx.fp8_block_mm(x, w, offs), mx.fp8_block_mm_dgrad(dout, w, offs)
