@@ -94,6 +94,19 @@ def test_equal_scores_go_by_number(score, E, groups, top):
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E,groups,top", [(64, 8, 4), (256, 8, 4), (96, 12, 3), (30, 5, 2), (1024, 32, 7), (16, 16, 5)])
+def test_equal_logits_with_biases_of_few_steps(score, dtype, E, groups, top):
+    """Padding tokens: their groups' values are sums of biases, which are alike often, exactly or to within a rounding."""
+    l = torch.zeros((6, E), dtype=dtype, device="cuda")
+    l[4:] = _logits(2, E, 3, dtype)
+    for seed in range(12):
+        g = torch.Generator().manual_seed(seed)
+        steps = torch.randint(-3, 4, (E,), generator=g) if seed % 2 else torch.round(torch.randn(E, generator=g) * 20)
+        _check(l, min(5, E // groups * top), score=score, bias=(steps.float() * 1e-3).cuda(), groups=groups, top_groups=top)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_close_scores_are_ordered_in_double_precision(score, dtype):
     """A bias that undoes the scores to within fp32's rounding: c differs by less than fp32 scores are exact to."""
     E = 96
