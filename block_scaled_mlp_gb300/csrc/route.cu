@@ -10,10 +10,10 @@
 // The order is that of c in double precision: an expert that a rounding of fp32 puts ahead of another would
 // make the result depend on how the scores are computed.  It is found from fp32 scores whose errors are
 // bounded.  Where two neighbours among the k largest are closer than the bounds of both allow, and not equal by their
-// inputs, these k are ordered again by scores of 44 bits (pairs of fp32 values); where that holds for the k-th and one
-// behind it, or for groups at the border, all experts of the token are (route_closely), and where 44 bits leave it open
-// too, in double precision (route_exactly; its fp64 instructions take a warp some 15 us).  Without a bias and groups the
-// logits themselves are the order and there is nothing to bound.
+// inputs, these k are ordered again by scores of 44 bits (pairs of fp32 values); where that holds for groups at the border,
+// the experts of these groups are (groups_closely), for the k-th and more than one behind it, those of all groups taken
+// (route_closely), and where 44 bits leave it open too, all in double precision (route_exactly; its fp64 instructions take
+// a warp some 15 us).  Without a bias and groups the logits themselves are the order and there is nothing to bound.
 //
 // Bounds of fp32 scores.  Sigmoid: expf is off by 2^-23 of itself, which moves s by 2^-23 s (1 - s), 1 + t and the
 // reciprocal by 2^-24 s each: 2^-23 s (2 - s) together.  Softmax: l - max is rounded by 2^-24 |l - max| besides, at most
@@ -25,8 +25,8 @@
 // and, from some thousand tokens on, instructions: about 20 for each of the k rounds that find the next largest c (eight
 // lanes a token and four tokens a warp take as many, and were slower: 2.8 against 2.0 us for 8 tokens).
 // On a GB300 (back to back in a graph; a launch that does nothing takes 1.5 us): 8 tokens of 64 experts, top 8, 2.3 us, their
-// grouping 2.9, backward 1.8; 16384 tokens 7.4 us, with a bias 9.8, with 8 groups besides 12.9, a token in doubt among the
-// last 2 to 3 us more; grouping their rows 7.3; backward 4.5 (sigmoid) and 5.6 (softmax).  Their bytes are 2.4 us.
+// grouping 2.9, backward 1.9; 16384 tokens 7.6 us, with a bias 10.5, with 8 groups besides 13.4 (256 experts: 29), tokens in
+// doubt 2 to 5 us more; grouping their rows 7.3; backward 4.5 (sigmoid) and 5.6 (softmax).  Their bytes are 2.4 us.
 #include <type_traits>
 
 #include "common.cuh"
@@ -288,11 +288,13 @@ __device__ __noinline__ ff ff_inverse_sum(const void* row, bool wide, int E, flo
   return ff_rcp_small(z);
 }
 
-// A token's experts by scores of 44 bits, by one warp: lane j returns the j-th.  *sure: no difference that decides is
+// A token's experts (with a bias) by scores of 44 bits, by one warp: lane j returns the j-th.  Bit g of groups_in: group g
+// is taken.  *sure: no difference that decides is
 // within what they are off by (2^-40 with room), or the inputs are equal.
-__device__ __noinline__ int route_closely(const RouteParams& p, const void* row, float most, double* buf, bool* sure) {
+__device__ __noinline__ int route_closely(const RouteParams& p, const void* row, float most, uint32_t groups_in, double* buf,
+                                          bool* sure) {
   const int lane = threadIdx.x & 31;
-  const int E = p.E, n = (E + 31) / 32;
+  const int E = p.E, n = (E + 31) / 32, group_size = E / p.groups;
   const bool wide = p.wide, sigmoid = p.sigmoid;
   float2* c = reinterpret_cast<float2*>(buf);
   ff inv{1.0f, 0.0f};
@@ -300,71 +302,27 @@ __device__ __noinline__ int route_closely(const RouteParams& p, const void* row,
   bool ok = true;
   __syncwarp();
   float size_of_c = 0.0f;
+  uint32_t taken = 0;  // bit i: expert lane + 32 i is chosen, or of no group that is
 #pragma unroll 1
   for (int i = 0; i < n; ++i) {
     const int e = lane + 32 * i;
     if (e >= E) continue;
-    const float l = logit(row, wide, e);
+    if (!(groups_in >> (e / group_size) & 1)) {
+      taken |= 1u << i;
+      continue;
+    }
+    const float l = logit(row, wide, e), b = p.bias[e];
     ff v{-INFINITY, 0.0f};
     if (l != -INFINITY) {
       ok = ok && ff_in_range(sigmoid, l, most);
       v = ff_score(sigmoid, l, most, inv);
-      if (p.bias) v = swiglu_math::ff_add_f(v, p.bias[e]);
-      if (isinf(p.bias ? p.bias[e] : 0.0f)) v = ff{p.bias[e], 0.0f};
+      v = isinf(b) ? ff{b, 0.0f} : swiglu_math::ff_add_f(v, b);
       if (!isinf(v.hi)) size_of_c = fmaxf(size_of_c, fabsf(v.hi));
     }
     c[e] = make_float2(v.hi, v.lo);
   }
   const float off = 0x1p-39f * (1.0f + warp_max(size_of_c));
   __syncwarp();
-  uint32_t taken = 0;  // bit i: expert lane + 32 i is chosen, or of no group that is
-  if (p.groups > 1) {
-    const int size = E / p.groups;
-    ff a{-INFINITY, 0.0f}, b{-INFINITY, 0.0f};
-    int ea = lane * size, eb = ea;
-    if (lane < p.groups)
-#pragma unroll 1
-      for (int i = 0; i < size; ++i) {
-        const float2 f = c[lane * size + i];
-        const ff v{f.x, f.y};
-        if (ff_more(v, a)) { b = a; eb = ea; a = v; ea = lane * size + i; }
-        else if (i && ff_more(v, b)) { b = v; eb = lane * size + i; }
-      }
-    ff value = size == 1 || isinf(a.hi) ? a : isinf(b.hi) ? b : swiglu_math::ff_add(a, b);
-    int rank = 0;
-#pragma unroll 1
-    for (int g = 0; g < p.groups; ++g) {
-      const ff v = ff_shfl(value, g);
-      if (ff_more(v, value) || (v.hi == value.hi && v.lo == value.lo && g < lane)) ++rank;
-    }
-    const uint32_t in = __ballot_sync(FULL, lane < p.groups && rank < p.top_groups);
-    // the last group taken and the first that is not: apart, or both of the same two values
-    const int last = __ffs(__ballot_sync(FULL, lane < p.groups && rank == p.top_groups - 1)) - 1;
-    const int next = __ffs(__ballot_sync(FULL, lane < p.groups && rank == p.top_groups)) - 1;
-    if (next >= 0) {
-      const ff va = ff_shfl(value, last), vb = ff_shfl(value, next);
-      const float apart = ff_minus(va, vb);
-      if (!(apart > 2 * off) && !(va.hi == vb.hi && isinf(va.hi))) {  // equal by their two experts' inputs, or open
-        const int a1 = __shfl_sync(FULL, ea, last), a2 = __shfl_sync(FULL, eb, last);
-        const int b1 = __shfl_sync(FULL, ea, next), b2 = __shfl_sync(FULL, eb, next);
-        auto alike = [&](int x, int y) { return logit(row, wide, x) == logit(row, wide, y) && (!p.bias || p.bias[x] == p.bias[y]); };
-        ok = ok && alike(a1, b1) && (size == 1 || alike(a2, b2));
-      }
-    }
-#pragma unroll 1
-    for (int i = 0; i < n; ++i) {
-      const int e = lane + 32 * i;
-      if (e < E && !(in >> (e / size) & 1)) taken |= 1u << i;
-    }
-  }
-  if (!p.bias) {  // the logits' own order
-    __syncwarp();
-#pragma unroll 1
-    for (int i = 0; i < n; ++i) {
-      const int e = lane + 32 * i;
-      if (e < E) c[e] = make_float2(logit(row, wide, e), 0.0f);
-    }
-  }
   int mine = 0;
   ff last{0.0f, 0.0f};
   float last_l = 0.0f, last_b = 0.0f;
@@ -387,24 +345,94 @@ __device__ __noinline__ int route_closely(const RouteParams& p, const void* row,
     }
     if (lane == j) mine = at;
     if ((at & 31) == lane) taken |= 1u << (at >> 5);
-    if (p.bias) {
-      const float l = logit(row, wide, at), b = p.bias[at];
-      if (j && !(ff_minus(last, v) > off) && !(l == last_l && b == last_b) && !(isinf(v.hi) && v.hi == last.hi)) ok = false;
-      last = v, last_l = l, last_b = b;
-    }
+    const float l = logit(row, wide, at), b = p.bias[at];
+    if (j && !(ff_minus(last, v) > off) && !(l == last_l && b == last_b) && !(isinf(v.hi) && v.hi == last.hi)) ok = false;
+    last = v, last_l = l, last_b = b;
   }
-  if (p.bias)
 #pragma unroll 1
-    for (int i = 0; i < n; ++i) {  // against all that are left
-      const int e = lane + 32 * i;
-      if (e >= E || (taken >> i & 1)) continue;
-      const ff w{c[e].x, c[e].y};
-      if (!(ff_minus(last, w) > off) && !(logit(row, wide, e) == last_l && p.bias[e] == last_b) && !(isinf(w.hi) && w.hi == last.hi))
-        ok = false;
-    }
+  for (int i = 0; i < n; ++i) {  // against all that are left
+    const int e = lane + 32 * i;
+    if (e >= E || (taken >> i & 1)) continue;
+    const ff w{c[e].x, c[e].y};
+    if (!(ff_minus(last, w) > off) && !(logit(row, wide, e) == last_l && p.bias[e] == last_b) && !(isinf(w.hi) && w.hi == last.hi))
+      ok = false;
+  }
   *sure = __all_sync(FULL, ok);
   __syncwarp();
   return mine;
+}
+
+// The `slots` most valuable of the groups in `open` (lane g has group g), by scores of 44 bits.  *sure as in route_closely.
+__device__ __noinline__ uint32_t groups_closely(const RouteParams& p, const void* row, float most, uint32_t open, int slots, double* buf,
+                                                bool* sure) {
+  const int lane = threadIdx.x & 31, size = p.E / p.groups, n = __popc(open) * size;
+  const bool wide = p.wide, sigmoid = p.sigmoid;
+  float2* c = reinterpret_cast<float2*>(buf);
+  ff inv{1.0f, 0.0f};
+  if (!sigmoid) inv = ff_inverse_sum(row, wide, p.E, most);
+  bool ok = true;
+  float size_of_c = 0.0f;
+  __syncwarp();
+#pragma unroll 1
+  for (int i = lane; i < n; i += 32) {
+    uint32_t rest = open;
+#pragma unroll 1
+    for (int g = i / size; g; --g) rest &= rest - 1;
+    const int e = (__ffs(rest) - 1) * size + i % size;
+    const float l = logit(row, wide, e), b = p.bias ? p.bias[e] : 0.0f;
+    ff v{-INFINITY, 0.0f};
+    if (l != -INFINITY) {
+      ok = ok && ff_in_range(sigmoid, l, most);
+      v = ff_score(sigmoid, l, most, inv);
+      v = isinf(b) ? ff{b, 0.0f} : p.bias ? swiglu_math::ff_add_f(v, b) : v;
+      if (!isinf(v.hi)) size_of_c = fmaxf(size_of_c, fabsf(v.hi));
+    }
+    c[e] = make_float2(v.hi, v.lo);
+  }
+  const float off = 0x1p-39f * (1.0f + warp_max(size_of_c));
+  __syncwarp();
+  const bool mine = open >> lane & 1;
+  ff a{-INFINITY, 0.0f}, b{-INFINITY, 0.0f};
+  int ea = lane * size, eb = ea;
+  if (mine)
+#pragma unroll 1
+    for (int i = 0; i < size; ++i) {
+      const float2 f = c[lane * size + i];
+      const ff v{f.x, f.y};
+      if (ff_more(v, a)) { b = a; eb = ea; a = v; ea = lane * size + i; }
+      else if (i && ff_more(v, b)) { b = v; eb = lane * size + i; }
+    }
+  const ff value = size == 1 || isinf(a.hi) ? a : isinf(b.hi) ? b : swiglu_math::ff_add(a, b);
+  int rank = 0;
+#pragma unroll 1
+  for (uint32_t rest = open; rest; rest &= rest - 1) {
+    const int g = __ffs(rest) - 1;
+    const ff v = ff_shfl(value, g);
+    if (ff_more(v, value) || (v.hi == value.hi && v.lo == value.lo && g < lane)) ++rank;
+  }
+  const uint32_t in = __ballot_sync(FULL, mine && rank < slots);
+  // the last group taken and the first that is not: apart, or both of the same two values
+  const int last = __ffs(__ballot_sync(FULL, mine && rank == slots - 1)) - 1;
+  const int next = __ffs(__ballot_sync(FULL, mine && rank == slots)) - 1;
+  if (last >= 0 && next >= 0) {
+    const ff va = ff_shfl(value, last), vb = ff_shfl(value, next);
+    if (!(ff_minus(va, vb) > 2 * off) && !(va.hi == vb.hi && isinf(va.hi))) {
+      // Open, unless all that are as near have the same two experts' inputs, which no third comes near to.
+      const int a1 = __shfl_sync(FULL, ea, last), a2 = __shfl_sync(FULL, eb, last);
+      auto alike = [&](int x, int y) { return logit(row, wide, x) == logit(row, wide, y) && (!p.bias || p.bias[x] == p.bias[y]); };
+      if (mine && !(fabsf(ff_minus(value, va)) > 2 * off)) {
+        ok = ok && alike(ea, a1) && (size == 1 || alike(eb, a2));
+#pragma unroll 1
+        for (int i = 0; i < size; ++i) {
+          const int e = lane * size + i;
+          if (e != ea && e != eb && !(ff_minus(b, ff{c[e].x, c[e].y}) > off) && !alike(e, eb)) ok = false;
+        }
+      }
+    }
+  }
+  *sure = __all_sync(FULL, ok);
+  __syncwarp();
+  return in;
 }
 
 // The n experts that lanes 0 to n - 1 have (numbers and logits) in order by scores of 44 bits: each lane's place.  *sure as
@@ -468,6 +496,13 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __gri
   auto score = [&](float x) { return sigmoid ? __frcp_rn(1.0f + expf(-x)) : expf(x - most) * inv; };
   uint32_t key[V];
   bool sure_groups = true, sure = true;   // of the groups, of the set of k
+  auto all_equal = [&](const float (&x)[V]) {
+    float least = INFINITY, high = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (first + i < E) least = fminf(least, x[i]), high = fmaxf(high, x[i]);
+    return warp_max(high) == -warp_max(-least);
+  };
   if (p.bias || p.groups > 1) {
     float c[V], b[V];
 #pragma unroll
@@ -488,7 +523,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __gri
       const float off = (sigmoid ? 0x1.1p-21f : (V + 22) * 0x1p-22f * inv) + 0x1p-21f * warp_max(largest);
       const int size = E / p.groups, step = size / V;
       float value;
-      int mine, rank;
+      int mine, rank, width = 1;  // width: lanes from one group to the next
       bool have = true;
       if (size % V == 0 && (step & (step - 1)) == 0) {  // a group has lanes of its own, a power of two of them
         float a = -INFINITY, d = -INFINITY;
@@ -504,6 +539,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __gri
         }
         value = size > 1 ? a + d : a;
         mine = lane / step;
+        width = step;
         have = mine < p.groups;
         rank = rank_of(value, mine, p.groups, step);
         if (have && rank >= p.top_groups) {
@@ -532,6 +568,20 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __gri
       if (at_next) {
         const float a = __shfl_sync(FULL, value, __ffs(at_last) - 1), d = __shfl_sync(FULL, value, __ffs(at_next) - 1);
         sure_groups = a - d > off || (a == d && isinf(a));
+        if (!sure_groups && !__any_sync(FULL, bad)) {
+          if (!all_equal(l)) {
+            // those well above the first that is not taken are in, those well below the last that is are out
+            const float v = __shfl_sync(FULL, value, lane < p.groups ? lane * width : 0);
+            const uint32_t in = __ballot_sync(FULL, lane < p.groups && v - d > off);
+            const uint32_t open = __ballot_sync(FULL, lane < p.groups && !(v - d > off) && !(a - v > off));
+            const uint32_t taken = in | groups_closely(p, row, most, open, p.top_groups - __popc(in), buf, &sure_groups);
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+              key[i] = first + i < E && (taken >> ((first + i) / size) & 1) ? key_of(p.bias ? c[i] : l[i]) : 0;
+          } else if (!p.bias) {
+            sure_groups = true;  // numbers decide, as they did
+          }
+        }
       }
     }
   } else {
@@ -594,30 +644,21 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __gri
   const bool spoilt = __any_sync(FULL, bad);
   bool again = __any_sync(FULL, !sure || !sure_groups);
   bool contest = false;
-  if (again && !spoilt) {
-    // Equal by their inputs?  Then numbers decide, as they did: all logits (no bias), or all experts as near to the k-th
-    // as their scores are off.
-    if (!p.bias) {
-      float least = INFINITY, high = -INFINITY;
+  if (again && !spoilt && sure_groups) {
+    // Equal by their inputs, all experts as near to the k-th as their scores are off?  Then numbers decide, as they did.
+    const float xk = __shfl_sync(FULL, x, k - 1), ck = of_key(__shfl_sync(FULL, mine, k - 1));
+    const float bk = p.bias[__shfl_sync(FULL, id, k - 1)], off = __shfl_sync(FULL, border, k - 1);
+    bool equal = true;
+    int near = 0;
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (first + i < E) least = fminf(least, l[i]), high = fmaxf(high, l[i]);
-      again = warp_max(high) != -warp_max(-least);
-    } else if (__all_sync(FULL, sure_groups)) {
-      const float xk = __shfl_sync(FULL, x, k - 1), ck = of_key(__shfl_sync(FULL, mine, k - 1));
-      const float bk = p.bias[__shfl_sync(FULL, id, k - 1)], off = __shfl_sync(FULL, border, k - 1);
-      bool equal = true;
-      int near = 0;
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (key[i] && !(ck - of_key(key[i]) > off)) {
-          equal = equal && l[i] == xk && p.bias[first + i] == bk;
-          ++near;
-        }
-      again = !__all_sync(FULL, equal);
-      // one expert alone behind the k-th is put in order with the k
-      contest = again && k < 32 && warp_sum(near) == 1;
-    }
+    for (int i = 0; i < V; ++i)
+      if (key[i] && !(ck - of_key(key[i]) > off)) {
+        equal = equal && l[i] == xk && p.bias[first + i] == bk;
+        ++near;
+      }
+    again = !__all_sync(FULL, equal);
+    // one expert alone behind the k-th is put in order with the k
+    contest = again && k < 32 && warp_sum(near) == 1;
   }
   bool chosen = has;
   if (!spoilt && (contest || (!again && !__all_sync(FULL, ordered)))) {
@@ -633,14 +674,17 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __gri
     contest = false;
   }
   if (again && !spoilt) {
-    float least = INFINITY, high = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (first + i < E) least = fminf(least, l[i]), high = fmaxf(high, l[i]);
     // a token of equal logits (padding) is in doubt by its biases alone: sums that are alike to the last of 44 bits as well
-    const bool flat = warp_max(high) == -warp_max(-least);
+    const bool flat = all_equal(l);
     bool fine = false;
-    if (!flat) id = route_closely(p, row, most, buf, &fine);
+    if (!flat && sure_groups) {
+      const int size = E / p.groups;   // a group was taken if an expert of it is chosen or could have been
+      uint32_t in = has ? 1u << id / size : 0;
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (key[i]) in |= 1u << (first + i) / size;
+      id = route_closely(p, row, most, __reduce_or_sync(FULL, in), buf, &fine);
+    }
     if (!fine) id = route_exactly(p, row, flat, buf);
     chosen = has;
     place = lane;
