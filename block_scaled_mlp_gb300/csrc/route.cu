@@ -732,7 +732,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_bwd_kernel(RouteBw
   const void* row = reinterpret_cast<const uint8_t*>(p.logits) + (size_t)t * E * (wide ? 4 : 2);
   float* const buf = s_row[warp];
   int id = lane < k ? p.ids[t * k + lane] : -1;
-  const float dw = lane < k ? p.dweights[t * k + lane] : 0.0f;
+  float dw = lane < k ? p.dweights[t * k + lane] : 0.0f;
   float l[V];
   float most = -INFINITY, inv = 1.0f;
   if (!sigmoid) load_values<V>(row, wide, p.vec, first, E, -INFINITY, l);
@@ -755,18 +755,23 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_bwd_kernel(RouteBw
   if (lane < k && (id < 0 || id >= E)) {
     record_error(p.err, MX_ERR_BAD_OFFSETS);
     id = -1;
+    dw = 0.0f;
   }
   const float x = id >= 0 ? logit(row, wide, id) : 0.0f;
   const float q = expf(sigmoid ? -fabsf(x) : x - most), r = sigmoid ? 1.0f / (1.0f + q) : 0.0f;
   const float s = id < 0 ? 0.0f : !sigmoid ? q * inv : x >= 0.0f ? r : q * r;
   float ds = p.scale * dw, back = 0.0f;  // back: sum ds s
-  const float dot = warp_sum(id >= 0 ? dw * s : 0.0f);
   if (p.renorm) {
-    const float over = 1.0f / (warp_sum(s) + 1e-20f);
-    ds = p.scale * (dw - dot * over) * over;
-    back = p.scale * (dot * over) * (1e-20f * over);
+    // From dw less that of the largest score, so that gradients which are alike leave nothing (k = 1: an exact 0):
+    // dw - dot / t = d - (sum d s) / t + top (t - sum s) / t
+    const uint32_t bits = __float_as_uint(s);  // s >= 0
+    const float top = __shfl_sync(FULL, dw, __ffs(__ballot_sync(FULL, bits == __reduce_max_sync(FULL, bits))) - 1);
+    const float d = dw - top, dot = warp_sum(d * s), sum = warp_sum(s);
+    const float t = sum + 1e-20f, over = 1.0f / t, rest = (t - sum) * over;
+    ds = p.scale * ((d - dot * over) + top * rest) * over;
+    back = p.scale * ((dot + top * sum) * over) * rest;
   } else {
-    back = p.scale * dot;
+    back = p.scale * warp_sum(dw * s);
   }
   float mine = sigmoid ? ds * (q * r) * r : ds;   // s (1 - s) = q r r
   if (sigmoid && q == 0.0f) mine = 0.0f;          // a score of 0 or 1 (a logit of -inf: whatever ds is)

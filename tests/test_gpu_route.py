@@ -229,6 +229,18 @@ def test_gradient_against_differences(score, renorm):
         assert abs(num - (dl * v).sum()) <= 1e-5 * (np.abs(dl * v).sum() + 1)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,E,k", [(1, 24, 1), (300, 24, 1), (65, 256, 8), (9, 7, 3)])
+def test_weights_that_cannot_change_have_no_gradient(dtype, score, T, E, k):
+    """Renormalised weights of one expert are constant, and alike gradients of several add up to that of a constant: 0, and
+    no rounding's rest (the 1e-20 in the sum is below fp32's rounding of it)."""
+    l = _logits(T, E, T, dtype)
+    ids, _ = mx.moe_route(l, k, score=SCORES[score])
+    dw = torch.randn((T, 1), generator=torch.Generator().manual_seed(5)).expand(T, k).contiguous().cuda()
+    assert not mx.moe_route_bwd(dw, l, ids, score=SCORES[score], scale=2.5).any()
+
+
 def test_gradient_reports_bad_ids():
     l = _logits(6, 10, 1)
     ids = torch.tensor([[0, 1]] * 6, dtype=torch.int32, device="cuda")
