@@ -298,7 +298,9 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
     if (warp == 2) read_ends<BT, 128>(p, ends, unit_end, &s_ok, &s_units);
     __syncthreads();
   } else {
-    pdl_allow_next();   // the warps that load and store wait, when they have worked out where
+    // The warps that load and store wait, when they have worked out where: at every tile, as a role's first is not always the
+    // CTA's (the second scale warp has none in a tile of one K block); behind the first a wait returns at once.
+    pdl_allow_next();
   }
   const int32_t n_units = s_units;
 
@@ -315,7 +317,7 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
       bool ok = true;
       for (int32_t u = unit0; u < n_units && ok; u += ustep) {
         const Unit t = unit_of<BT, 128>(p, ends, unit_end, u);
-        if (!p.offs && u == unit0) pdl_wait();
+        if (!p.offs) pdl_wait();
         for (int kb = 0; kb < num_kb; ++kb) {
           if (!warp_wait(&empty[stage], phase ^ 1, p.err)) { ok = false; break; }
           if (leader) {
@@ -383,7 +385,7 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
           w = p.sw + t.e * p.sw_e + (t.f0 >> 7) * p.sw_f + (kb0 + next_kb) * p.sw_c;
           live = t.tn - lane;
           fresh = false;
-          if (!p.offs && next_u == unit0) pdl_wait();
+          if (!p.offs) pdl_wait();
         }
 #pragma unroll
         for (int c = 0; c < PER; ++c) s[i][c] = 32 * c < live ? __ldg(st + 32 * c) : 0.0f;
@@ -582,7 +584,7 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
     if (warp == 2) read_ends<256, 256>(p, ends, unit_end, &s_ok, &s_units);
     __syncthreads();
   } else {
-    pdl_allow_next();   // the warps that load and store wait, when they have worked out where
+    pdl_allow_next();   // as above: the warps that load and store wait
   }
   const int32_t n_units = s_units;
 
@@ -600,7 +602,7 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
       for (int32_t u = unit0; u < n_units && ok; u += ustep) {
         const Unit t = unit_of<256, 256>(p, ends, unit_end, u);
         const int32_t row = (int32_t)t.t0 + rank * 128, f = t.f0 + rank * 64;
-        if (!p.offs && u == unit0) pdl_wait();
+        if (!p.offs) pdl_wait();
         for (int kb = 0; kb < num_kb; ++kb) {
           if (!warp_wait(&empty[stage], phase ^ 1, p.err)) { ok = false; break; }
           if (leader) {
@@ -675,7 +677,7 @@ __global__ void __launch_bounds__(FM_THREADS, 1)
           live = t.tn - rank * 128;
           if (lane == 0) sTile[half * C::TILES + tile] = make_int4((int32_t)t.t0 + rank * 128, live, t.f0, 0);
           tile = (tile + 1) & (C::TILES - 1);
-          if (!p.offs && next_u == unit0) pdl_wait();
+          if (!p.offs) pdl_wait();
         }
 #pragma unroll
         for (int c = 0; c < 4; ++c) s[i][c] = lane + 32 * c < live ? __ldg(st + 32 * c) : 0.0f;
