@@ -10,10 +10,11 @@
 // The order is that of c in double precision: an expert that a rounding of fp32 puts ahead of another would
 // make the result depend on how the scores are computed.  It is found from fp32 scores whose errors are
 // bounded.  Where two neighbours among the k largest are closer than the bounds of both allow, and not equal by their
-// inputs, these k are ordered again by scores of 44 bits (pairs of fp32 values); where that holds for groups at the border,
-// the experts of these groups are (groups_closely), for the k-th and more than one behind it, those of all groups taken
-// (route_closely), and where 44 bits leave it open too, all in double precision (route_exactly; its fp64 instructions take
-// a warp some 15 us).  Without a bias and groups the logits themselves are the order and there is nothing to bound.
+// inputs, these k are ordered again by scores of 44 bits (pairs of fp32 values), with the one behind them where that one alone
+// is as close to the k-th as any error allows; where that holds for groups at the border, the experts of these groups are
+// (groups_closely), for the k-th and more than one behind it (and not all so close are equal by their inputs, those before
+// it among them), those of all groups taken (route_closely), and where 44 bits leave it open too, all in double precision
+// (route_exactly; its fp64 instructions take a warp some 15 us).  Without a bias and groups the logits themselves are the order and there is nothing to bound.
 //
 // Bounds of fp32 scores.  Sigmoid: expf is off by 2^-23 of itself, which moves s by 2^-23 s (1 - s), 1 + t and the
 // reciprocal by 2^-24 s each: 2^-23 s (2 - s) together.  Softmax: l - max is rounded by 2^-24 |l - max| besides, at most
@@ -621,7 +622,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __gri
   float x = has ? logit(row, wide, id) : 0.0f;
   float s = has ? score(x) : 0.0f;
   bool ordered = true;  // within the k
-  float border = 0.0f;  // how far off the difference of the k-th and another may be
+  float border = 0.0f;  // how far off the difference of one of the k and another may be
   if (p.bias) {
     behind = round(behind_e);
     const float b = has ? p.bias[id] : 0.0f, c1 = of_key(mine);
@@ -629,6 +630,8 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __gri
     const uint32_t next = __shfl_down_sync(FULL, mine, 1);
     const float u1 = fmaxf(s, 0x1p-126f), own = sigmoid ? 0x1p-23f * u1 * (2.01f - u1) : 0x1.7p-22f * u1 - 0x1p-23f * u1 * __logf(u1);
     const float own2 = __shfl_down_sync(FULL, own, 1);
+    // the least of the k may be another than the k-th, and off by more than it
+    const float own_most = __uint_as_float(__reduce_max_sync(FULL, has ? __float_as_uint(own) : 0u));
     if (lane < k - 1) {
       const float c2 = of_key(next), rounding = 0x1.01p-24f * (fabsf(c1) + fabsf(c2));
       const bool equal = (x == x2 && b == b2) || (c1 == c2 && isinf(c1));
@@ -636,7 +639,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __gri
       ordered = equal || c1 - c2 > off;
     } else if (lane == k - 1 && behind) {  // against any that was not chosen: a score of the largest there is
       const float c2 = of_key(behind);
-      border = own + (sigmoid ? 0x1.1p-23f : (V + 22) * 0x1p-24f * inv) + 0x1p-22f * fabsf(c1) + 0x1p-23f * fabsf(c2) + 0x1p-125f;
+      border = own_most + (sigmoid ? 0x1.1p-23f : (V + 22) * 0x1p-24f * inv) + 0x1p-22f * fabsf(c1) + 0x1p-23f * fabsf(c2) + 0x1p-125f;
       sure = c1 - c2 > border || (c1 == c2 && isinf(c1));
     }
   }
@@ -645,10 +648,11 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __gri
   bool again = __any_sync(FULL, !sure || !sure_groups);
   bool contest = false;
   if (again && !spoilt && sure_groups) {
-    // Equal by their inputs, all experts as near to the k-th as their scores are off?  Then numbers decide, as they did.
+    // Equal by their inputs, all experts as near to the k-th as their scores are off, chosen or not?  Then numbers decide, as
+    // they did: the others of the k are above these, those that are left below.
     const float xk = __shfl_sync(FULL, x, k - 1), ck = of_key(__shfl_sync(FULL, mine, k - 1));
     const float bk = p.bias[__shfl_sync(FULL, id, k - 1)], off = __shfl_sync(FULL, border, k - 1);
-    bool equal = true;
+    bool equal = !has || of_key(mine) - ck > off || (x == xk && p.bias[id] == bk);
     int near = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -657,7 +661,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __gri
         ++near;
       }
     again = !__all_sync(FULL, equal);
-    // one expert alone behind the k-th is put in order with the k
+    // one expert alone behind the k-th is put in order with the k (any other is below all of them)
     contest = again && k < 32 && warp_sum(near) == 1;
   }
   bool chosen = has;

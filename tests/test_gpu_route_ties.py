@@ -1,0 +1,91 @@
+"""Routing where ties and near-ties meet: experts that are equal by their inputs at the border of the k, with others before
+them that fp32 cannot tell from them.  The numbers are those of c in double precision, equal ones by number."""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_route import _check, _scores
+
+pytestmark = pytest.mark.gpu
+
+SCORES = ["softmax", "sigmoid"]
+
+
+def _next(x, n=1):
+    """The fp32 value n steps above x."""
+    x = np.float32(x)
+    for _ in range(n):
+        x = np.nextafter(x, np.float32(np.inf))
+    return x
+
+
+def _on_gpu(bias):
+    return torch.from_numpy(np.asarray(bias, np.float32)).cuda()
+
+
+@pytest.mark.parametrize("score", SCORES)
+@pytest.mark.parametrize("low,high", [(0.0, 2.0 ** -30), (0.003, _next(0.003)), (0.003, _next(0.003, 3)), (-0.25, _next(-0.25))])
+@pytest.mark.parametrize("E,others", [(3, 0), (3, 5), (5, 0), (8, 56), (33, 200), (40, 0)])
+def test_twins_behind_a_nearly_equal_one(score, low, high, E, others):
+    """Expert 0 is worth a little less than all others of the first E, which are twins: the first k of those are chosen."""
+    bias = _on_gpu([low] + [high] * (E - 1) + [-10.0] * others)
+    l = torch.zeros((3, E + others), device="cuda")
+    l[1] = 1.5
+    for k in {1, 2, E // 2, min(E - 1, 32)}:
+        ids, _ = _check(l, k, score=score, bias=bias)
+        assert ids[0].tolist() == list(range(1, k + 1))
+    ids, _ = _check(l, 2, score=score, bias=bias.flip(0).contiguous())      # the lesser one has the highest number
+    assert ids[0].tolist() == [others, others + 1]
+
+
+@pytest.mark.parametrize("score", SCORES)
+@pytest.mark.parametrize("k", [2, 5, 8])
+def test_several_levels_of_twins(score, k):
+    """Levels one step apart, which fp32 sums cannot tell from one another, each with several experts."""
+    for seed in range(60):
+        g = np.random.default_rng(seed)
+        E = int(g.integers(k + 1, 70))
+        steps = g.integers(0, 4, E)
+        bias = _on_gpu([_next(2e-3, int(n)) for n in steps])
+        _check(torch.zeros((2, E), device="cuda"), k, score=score, bias=bias)
+
+
+@pytest.mark.parametrize("score", SCORES)
+@pytest.mark.parametrize("groups,top", [(1, 1), (8, 4)])
+def test_biases_that_have_walked(score, groups, top):
+    """Balance biases after many steps of +-1e-3 in fp32: sums of one value that went other ways differ in their last bits.  A
+    padding token has equal logits."""
+    for seed in range(300):
+        g = np.random.default_rng(seed)
+        bias = np.zeros(64, np.float32)
+        for _ in range(int(g.integers(20, 400))):
+            bias += np.float32(1e-3) * np.sign(g.normal(size=64)).astype(np.float32)
+        _check(torch.zeros((1, 64), device="cuda"), 8, score=score, bias=_on_gpu(bias), groups=groups, top_groups=top)
+
+
+@pytest.mark.parametrize("score", SCORES)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("groups,top", [(1, 1), (6, 3)])
+def test_twins_of_several_logits(score, dtype, groups, top):
+    """A few logits, each with the bias that brings its score to 0.7 to within some of the bias's steps: nearly all experts
+    are as near as fp32 can tell, and many are twins."""
+    for seed in range(80):
+        g = np.random.default_rng(seed)
+        l = torch.from_numpy(g.integers(-2, 3, (1, 48)).astype(np.float32) / 2).to(dtype)
+        s = _scores(l.double().numpy(), score)[0]
+        bias = [_next(0.7 - v, int(n)) for v, n in zip(s, g.integers(0, 3, 48))]
+        _check(l.cuda(), int(g.integers(1, 13)), score=score, bias=_on_gpu(bias), groups=groups, top_groups=top)
+
+
+@pytest.mark.parametrize("score", SCORES)
+def test_one_large_score_among_small_ones(score):
+    """Scores near one with biases near minus one beside scores near nothing: the one's fp32 value is off by far more than the
+    others' are."""
+    for seed in range(40):
+        g = np.random.default_rng(seed)
+        l = torch.from_numpy(np.r_[g.normal() + 9, g.normal(size=15) * 3 - 30].astype(np.float32))[None]
+        s = _scores(l.double().numpy(), score)[0]
+        bias = np.zeros(16, np.float32)
+        bias[0] = -s[0]
+        bias[1:] = s[0] + np.float64(bias[0]) + g.integers(-3, 4, 15) * 2.0 ** -26
+        _check(l.cuda(), 4, score=score, bias=_on_gpu(bias))
