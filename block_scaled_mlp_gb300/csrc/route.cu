@@ -512,9 +512,8 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __gri
     float largest = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      bad |= b[i] != b[i];
       c[i] = l[i] == -INFINITY ? -INFINITY : score(l[i]) + b[i];
-      bad |= c[i] != c[i];
+      bad |= c[i] != c[i];  // a NaN among biases, but not of an expert that is masked
       if (c[i] != -INFINITY) largest = fmaxf(largest, fabsf(c[i]));
       key[i] = first + i >= E ? 0 : key_of(p.bias ? c[i] : l[i]);
     }

@@ -560,8 +560,9 @@ MX_API int mx_ragged_mm(int mode, const void* a, const void* b, int64_t M_total,
  *   logits    [T, E], bf16 (MX_BF16) or fp32 (MX_FP32).
  *   bias      [E] fp32, or NULL.  It decides ids and does not enter weights.
  *   ids, weights  [T, k] int32 and fp32 out.
- * A token with a NaN among its logits, c or its groups' values, or under softmax
- * with an infinite logit, has ids 0 to k - 1 and NaN weights.
+ * A token with a NaN among its logits, c or (where groups are chosen) its groups'
+ * values, or under softmax with a logit of +inf, has ids 0 to k - 1 and NaN weights.
+ * A bias does not matter where the logit is -inf.
  * Requirements: 1 <= E <= 1024, 1 <= groups <= 32, E % groups == 0,
  * 1 <= top_groups <= groups, 1 <= k <= 32, k <= top_groups * E / groups, scale finite.
  */

@@ -4,7 +4,8 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_route import _check, _scores
+import block_scaled_mlp_gb300 as mx
+from test_gpu_route import _check, _logits, _scores
 
 pytestmark = pytest.mark.gpu
 
@@ -89,3 +90,19 @@ def test_one_large_score_among_small_ones(score):
         bias[0] = -s[0]
         bias[1:] = s[0] + np.float64(bias[0]) + g.integers(-3, 4, 15) * 2.0 ** -26
         _check(l.cuda(), 4, score=score, bias=_on_gpu(bias))
+
+
+@pytest.mark.parametrize("score", SCORES)
+@pytest.mark.parametrize("groups,top", [(1, 1), (6, 3)])
+def test_a_bias_of_a_masked_expert_does_not_matter(score, groups, top):
+    """c of a logit of -inf is -inf, whatever the bias: a NaN there spoils the tokens that may choose the expert alone."""
+    E = 48
+    l = _logits(20, E, 3)
+    bias = torch.from_numpy(np.random.default_rng(1).normal(size=E).astype(np.float32)).cuda() * 0.1
+    bias[5] = bias[30] = float("nan")
+    l[:12, 5] = -float("inf")
+    l[:12, 30] = -float("inf")
+    ids, w = _check(l[:12].contiguous(), 6, score=score, bias=bias, groups=groups, top_groups=top)
+    got = mx.moe_route(l, 6, score=SCORES.index(score), bias=bias, groups=groups, top_groups=top)
+    assert torch.equal(got[0][:12], ids) and torch.equal(got[1][:12], w)
+    assert torch.isnan(got[1][12:]).all() and (got[0][12:] == torch.arange(6, device="cuda")).all()
