@@ -494,6 +494,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __gri
     z = warp_sum(z);
     inv = z > 0.0f ? 1.0f / z : 0.0f;
   }
+  // what choosing needs: its bounds have room for the difference's rounding and for underflow
   auto score = [&](float x) { return sigmoid ? __frcp_rn(1.0f + expf(-x)) : expf(x - most) * inv; };
   uint32_t key[V];
   bool sure_groups = true, sure = true;   // of the groups, of the set of k
@@ -617,9 +618,17 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __gri
       find();
     }
   }
+  // A score for its weight: e^-x does not overflow (below -88 it is e^x to within 2^-126 of itself), and what rounding
+  // l - max leaves off, up to 2^-18 where they are 64 apart, is made up for (the rest is a number while the difference is).
+  auto score_of = [&](float x) {
+    if (sigmoid) return x < -88.0f ? expf(x) : __frcp_rn(1.0f + expf(-x));
+    const swiglu_math::ff d = swiglu_math::two_sum(x, -most);
+    const float e = expf(d.hi);
+    return d.hi > -120.0f ? fmaf(e, d.lo, e) * inv : 0.0f;
+  };
   const bool has = lane < k;
   float x = has ? logit(row, wide, id) : 0.0f;
-  float s = has ? score(x) : 0.0f;
+  float s = has ? score_of(x) : 0.0f;
   bool ordered = true;  // within the k
   float border = 0.0f;  // how far off the difference of one of the k and another may be
   if (p.bias) {
@@ -668,7 +677,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __gri
     if (contest && lane == k) {
       id = behind_e;
       x = logit(row, wide, id);
-      s = score(x);
+      s = score_of(x);
     }
     bool fine;
     place = order_closely(p, row, most, contest ? k + 1 : k, id, x, &fine);
@@ -692,7 +701,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __gri
     chosen = has;
     place = lane;
     x = has ? logit(row, wide, id) : 0.0f;
-    s = has ? score(x) : 0.0f;
+    s = has ? score_of(x) : 0.0f;
   }
   const float total = p.renorm ? warp_sum(chosen ? s : 0.0f) + 1e-20f : 1.0f;
   if (!chosen) return;
