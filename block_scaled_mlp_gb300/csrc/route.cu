@@ -644,11 +644,11 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __gri
       const float c2 = of_key(next), rounding = 0x1.01p-24f * (fabsf(c1) + fabsf(c2));
       const bool equal = (x == x2 && b == b2) || (c1 == c2 && isinf(c1));
       const float off = own + own2 + rounding + (sigmoid ? 0.0f : (V + 14) * 0x1p-24f * fabsf(s - s2));
-      ordered = equal || c1 - c2 > off;
+      ordered = equal || c1 - c2 > off || c1 - c2 == INFINITY;  // (off is infinite with either)
     } else if (lane == k - 1 && behind) {  // against any that was not chosen: a score of the largest there is
       const float c2 = of_key(behind);
       border = own_most + (sigmoid ? 0x1.1p-23f : (V + 22) * 0x1p-24f * inv) + 0x1p-22f * fabsf(c1) + 0x1p-23f * fabsf(c2) + 0x1p-125f;
-      sure = c1 - c2 > border || (c1 == c2 && isinf(c1));
+      sure = c1 - c2 > border || c1 - c2 == INFINITY || (c1 == c2 && isinf(c1));  // else border is finite
     }
   }
   int place = lane;

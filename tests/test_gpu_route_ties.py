@@ -106,3 +106,24 @@ def test_a_bias_of_a_masked_expert_does_not_matter(score, groups, top):
     got = mx.moe_route(l, 6, score=SCORES.index(score), bias=bias, groups=groups, top_groups=top)
     assert torch.equal(got[0][:12], ids) and torch.equal(got[1][:12], w)
     assert torch.isnan(got[1][12:]).all() and (got[0][12:] == torch.arange(6, device="cuda")).all()
+
+
+@pytest.mark.parametrize("score", SCORES)
+@pytest.mark.parametrize("k", [1, 4, 8])
+def test_infinite_sums_at_the_border(score, k):
+    """Masked experts right behind the k-th, fewer than k left, and biases of plus and minus infinity."""
+    E, inf = 40, float("inf")
+    for left in (k - 1, k, k + 1):
+        l = torch.full((30, E), -inf)
+        v = _logits(30, E, left).cpu()
+        for t in range(30):
+            at = torch.randperm(E, generator=torch.Generator().manual_seed(t))[:left]
+            l[t, at] = v[t, at]
+        bias = torch.from_numpy(np.random.default_rng(k).integers(-2, 3, E).astype(np.float32)).cuda() * 0.125
+        _check(l.cuda(), k, score=score, bias=bias)
+        _check(l.cuda(), k, score=score, bias=bias, groups=8, top_groups=4)
+    l = _logits(30, E, 77)
+    for seed in range(12):
+        g = np.random.default_rng(seed)
+        bias = g.choice([0.0, 0.25, inf, -inf], E, p=[0.4, 0.4, 0.1, 0.1] if seed % 2 else [0.05, 0.05, 0.1, 0.8])
+        _check(l, k, score=score, bias=_on_gpu(bias))
