@@ -1080,11 +1080,12 @@ int launch_moe_route_bwd(const RouteBwdLaunch& a, cudaStream_t stream) {
 namespace {
 // Up to 8192 rows one large CTA does it all, if its warps' counts fit 48 KB; 1024 rows one small one.
 bool one_cta(int64_t R, int32_t E) { return R <= 1024 || (R <= 8192 && E <= 352); }
+constexpr int64_t TG_MOST_CHUNKS = 512;  // on a device of any size: two for each SM of 256
 }  // namespace
 
 size_t token_group_workspace(int64_t R, int32_t E) {
   // for any number of SMs: a chunk has 1024 rows at least
-  return one_cta(R, E) ? 0 : (size_t)((R + 1023) / 1024) * (size_t)E * 4;
+  return one_cta(R, E) ? 0 : (size_t)std::min<int64_t>((R + 1023) / 1024, TG_MOST_CHUNKS) * (size_t)E * 4;
 }
 
 int launch_token_group(const int32_t* expert_of, int64_t R, int32_t E, int32_t* offs, int32_t* row_dst, int32_t* row_src,
@@ -1103,7 +1104,7 @@ int launch_token_group(const int32_t* expert_of, int64_t R, int32_t E, int32_t* 
     return place(token_group_place_kernel<32, 8>, 1, 32, 8192);
   }
   // chunks of 1024 rows while each SM has two of them at most, larger ones else: a CTA reads every chunk's counts
-  const int64_t most = 2 * (int64_t)num_sms();
+  const int64_t most = std::min<int64_t>(2 * (int64_t)num_sms(), TG_MOST_CHUNKS);
   const int64_t chunk = std::max<int64_t>(1024, ((R + most - 1) / most + 255) / 256 * 256);
   const unsigned grid = (unsigned)((R + chunk - 1) / chunk);
   if (grid > 1) {  // the chunks are counted first
