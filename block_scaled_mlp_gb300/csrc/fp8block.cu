@@ -190,7 +190,7 @@ constexpr int FW_THREADS = 256;
 // shared memory in rows of 132 bytes, so that neither the words of a row nor the bytes of a column meet in one bank often.
 __global__ void __launch_bounds__(FW_THREADS) fp8_block_weight_kernel(WeightParams p) {
   __shared__ uint32_t part[FW_THREADS / 32];
-  __shared__ uint8_t tile[128][132];
+  __shared__ uint32_t tile[128][33];   // written as words (which it lies on by its type), read as bytes
   pdl_begin();
   const int tid = threadIdx.x, cv = tid & 15, r0 = tid >> 4;
   const int64_t e = blockIdx.z, n0 = (int64_t)blockIdx.y * 128, k0 = (int64_t)blockIdx.x * 128;
@@ -217,14 +217,15 @@ __global__ void __launch_bounds__(FW_THREADS) fp8_block_weight_kernel(WeightPara
     const uint2 q = codes8(v[i], s);
     if (in_k && n < p.N) p.codes[(e * p.N + n) * k8 + k0 / 8 + cv] = q;
     if (p.codes_t) {
-      *reinterpret_cast<uint32_t*>(&tile[r0 + i * 16][cv * 8]) = q.x;
-      *reinterpret_cast<uint32_t*>(&tile[r0 + i * 16][cv * 8 + 4]) = q.y;
+      tile[r0 + i * 16][cv * 2] = q.x;
+      tile[r0 + i * 16][cv * 2 + 1] = q.y;
     }
   }
   if (!p.codes_t) return;
   __syncthreads();
   // 16 codes of a column a thread: 8 threads a column, 32 columns a step (N is a multiple of 16)
   const int nv = tid & 7;
+  const uint8_t* bytes = reinterpret_cast<const uint8_t*>(tile[nv * 16]);
 #pragma unroll 1
   for (int i = 0; i < 4; ++i) {
     const int col = (tid >> 3) + i * 32;
@@ -232,8 +233,8 @@ __global__ void __launch_bounds__(FW_THREADS) fp8_block_weight_kernel(WeightPara
     uint32_t q[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      q[j] = tile[nv * 16 + j * 4][col] | tile[nv * 16 + j * 4 + 1][col] << 8 | tile[nv * 16 + j * 4 + 2][col] << 16 |
-             (uint32_t)tile[nv * 16 + j * 4 + 3][col] << 24;
+      q[j] = bytes[j * 4 * 132 + col] | bytes[(j * 4 + 1) * 132 + col] << 8 | bytes[(j * 4 + 2) * 132 + col] << 16 |
+             (uint32_t)bytes[(j * 4 + 3) * 132 + col] << 24;
     *reinterpret_cast<uint4*>(p.codes_t + (e * p.K + k0 + col) * p.N + n0 + nv * 16) = make_uint4(q[0], q[1], q[2], q[3]);
   }
 }
