@@ -174,7 +174,7 @@ MX_DEVINL Unit unit_of(const MmParams& p, const int32_t* ends, const int32_t* un
   const uint32_t v = u - (lo ? unit_end[lo - 1] : 0);
   const int32_t start = lo ? ends[lo - 1] : 0, rows = ends[lo] - start;
   const uint32_t t_tiles = (uint32_t)(rows + BT - 1) / BT;
-  int32_t t = 0, f = v, share = BT;
+  int32_t t = 0, f = v;
   if (t_tiles > 1) {
     if (rows <= p.F) {  // the rows are the smaller operand: re-read them, stream the weights once
       f = v / t_tiles;
@@ -184,11 +184,9 @@ MX_DEVINL Unit unit_of(const MmParams& p, const int32_t* ends, const int32_t* un
       f = v - t * f_tiles;
     }
   }
-  // narrow tiles: the group's rows shared out evenly, in multiples of 32
-  if (BT < 256) share = (((t_tiles > 1 ? (uint32_t)(rows + t_tiles - 1) / t_tiles : rows) + 31) & ~31);
   r.f0 = f * FT;
-  r.t0 = (int64_t)start + (int64_t)t * share;
-  r.tn = min(share, rows - t * share);
+  r.t0 = (int64_t)start + (int64_t)t * BT;
+  r.tn = min(BT, rows - t * BT);
   r.n_eff = (r.tn + 31) & ~31;
   return r;
 }
