@@ -322,6 +322,12 @@ __device__ __noinline__ int route_closely(const RouteParams& p, const void* row,
     }
     c[e] = make_float2(v.hi, v.lo);
   }
+  if (!__all_sync(FULL, ok)) {
+    // A logit that these scores are not made for: its score may be NaN, of which lanes that exchange values find no common
+    // largest; each would cross out its own until there is none left.
+    *sure = false;
+    return 0;
+  }
   const float off = 0x1p-39f * (1.0f + warp_max(size_of_c));
   __syncwarp();
   int mine = 0;

@@ -127,3 +127,21 @@ def test_infinite_sums_at_the_border(score, k):
         g = np.random.default_rng(seed)
         bias = g.choice([0.0, 0.25, inf, -inf], E, p=[0.4, 0.4, 0.1, 0.1] if seed % 2 else [0.05, 0.05, 0.1, 0.8])
         _check(l, k, score=score, bias=_on_gpu(bias))
+
+
+@pytest.mark.parametrize("score", SCORES)
+@pytest.mark.parametrize("far", [88.4, 88.7, 89.0, 95.0, 140.0, 1e4])
+def test_doubts_with_logits_beyond_the_range_of_44_bits(score, far):
+    """All experts of the groups that are taken are chosen, two of them are closer than fp32 can tell, and one has a logit
+    that scores of 44 bits are not made for."""
+    for groups, top, size in ((8, 3, 2), (31, 2, 3), (1, 1, 5), (4, 1, 9)):
+        E = groups * size
+        l = torch.full((4, E), -30.0)
+        l[:, :size * top] = 2.0 if score == "softmax" else 1.0
+        for t in range(4):
+            l[t, t % size] = 2.0 - far if score == "softmax" else -far
+        s = _scores(l.double().numpy(), score)[0]
+        bias = np.zeros(E, np.float32)
+        bias[:size * top] = np.float32(0.5) - s[:size * top].astype(np.float32)
+        bias[1:size * top:2] = np.nextafter(bias[1:size * top:2], np.float32(1))
+        _check(l.cuda(), size * top, score=score, bias=_on_gpu(bias), groups=groups, top_groups=top)
