@@ -126,7 +126,7 @@ struct RouteParams {
   float* weights;         // [T, k]
 };
 
-// The two largest of a group's values, added.
+// Half the sum of the two largest of a group's values (the sum of two fp32 values may be none), or the only one.
 template <class T>
 MX_DEVINL T group_value(const T* c, int size, int first) {
   T a = (T)-INFINITY, b = (T)-INFINITY;
@@ -137,7 +137,7 @@ MX_DEVINL T group_value(const T* c, int size, int first) {
     b = v > a ? a : v > b ? v : b;
     a = v > a ? v : a;
   }
-  return size > 1 ? a + b : a;
+  return size > 1 ? (T)0.5 * a + (T)0.5 * b : a;
 }
 
 // Rank of `value` among the values that lanes 0, step, ... of the warp have; `mine` is its own place there.
@@ -409,7 +409,7 @@ __device__ __noinline__ uint32_t groups_closely(const RouteParams& p, const void
       if (ff_more(v, a)) { b = a; eb = ea; a = v; ea = lane * size + i; }
       else if (i && ff_more(v, b)) { b = v; eb = lane * size + i; }
     }
-  const ff value = size == 1 || isinf(a.hi) ? a : isinf(b.hi) ? b : swiglu_math::ff_add(a, b);
+  const ff value = size == 1 || isinf(a.hi) ? a : isinf(b.hi) ? b : swiglu_math::ff_add(ff{0.5f * a.hi, 0.5f * a.lo}, ff{0.5f * b.hi, 0.5f * b.lo});
   int rank = 0;
 #pragma unroll 1
   for (uint32_t rest = open; rest; rest &= rest - 1) {
@@ -423,11 +423,11 @@ __device__ __noinline__ uint32_t groups_closely(const RouteParams& p, const void
   const int next = __ffs(__ballot_sync(FULL, mine && rank == slots)) - 1;
   if (last >= 0 && next >= 0) {
     const ff va = ff_shfl(value, last), vb = ff_shfl(value, next);
-    if (!(ff_minus(va, vb) > 2 * off) && !(va.hi == vb.hi && isinf(va.hi))) {
+    if (!(ff_minus(va, vb) > off) && !(va.hi == vb.hi && isinf(va.hi))) {
       // Open, unless all that are as near have the same two experts' inputs, which no third comes near to.
       const int a1 = __shfl_sync(FULL, ea, last), a2 = __shfl_sync(FULL, eb, last);
       auto alike = [&](int x, int y) { return logit(row, wide, x) == logit(row, wide, y) && (!p.bias || p.bias[x] == p.bias[y]); };
-      if (mine && !(fabsf(ff_minus(value, va)) > 2 * off)) {
+      if (mine && !(fabsf(ff_minus(value, va)) > off)) {
         ok = ok && alike(ea, a1) && (size == 1 || alike(eb, a2));
 #pragma unroll 1
         for (int i = 0; i < size; ++i) {
@@ -525,9 +525,9 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __gri
       key[i] = first + i >= E ? 0 : key_of(p.bias ? c[i] : l[i]);
     }
     if (p.groups > 1) {
-      // a score is off by 2^-23 (sigmoid), or by (V + 22) 2^-24 of the largest there is (softmax), a sum of two by twice that;
-      // c and the sum are rounded
-      const float off = (sigmoid ? 0x1.1p-21f : (V + 22) * 0x1p-22f * inv) + 0x1p-21f * warp_max(largest);
+      // a score is off by 2^-23 (sigmoid), or by (V + 22) 2^-24 of the largest there is (softmax), and half a sum of two by no
+      // more; c and that are rounded
+      const float off = (sigmoid ? 0x1.1p-22f : (V + 22) * 0x1p-23f * inv) + 0x1p-22f * warp_max(largest);
       const int size = E / p.groups, step = size / V;
       float value;
       int mine, rank, width = 1;  // width: lanes from one group to the next
@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __gri
           d = fmaxf(fmaxf(d, d2), fminf(a, a2));
           a = fmaxf(a, a2);
         }
-        value = size > 1 ? a + d : a;
+        value = size > 1 ? 0.5f * a + 0.5f * d : a;
         mine = lane / step;
         width = step;
         have = mine < p.groups;

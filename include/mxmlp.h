@@ -556,7 +556,8 @@ MX_API int mx_ragged_mm(int mode, const void* a, const void* b, int64_t M_total,
  *   equal ones by number.  ids = the k largest c of the groups taken, larger
  *   ones first, equal ones by number (without a bias: the k largest logits).
  *   weights = scale * s, or with renorm scale * s / (sum of the k s + 1e-20);
- *   fp32, within 2^-18 (scores below 2^-126: within four of fp32's steps of 2^-149).
+ *   fp32, within 2^-18 (scores and quotients below 2^-126: to four of the steps of
+ *   2^-149 that fp32 has there).
  *   logits    [T, E], bf16 (MX_BF16) or fp32 (MX_FP32).
  *   bias      [E] fp32, or NULL.  It decides ids and does not enter weights.
  *   ids, weights  [T, k] int32 and fp32 out.

@@ -145,3 +145,26 @@ def test_doubts_with_logits_beyond_the_range_of_44_bits(score, far):
         bias[:size * top] = np.float32(0.5) - s[:size * top].astype(np.float32)
         bias[1:size * top:2] = np.nextafter(bias[1:size * top:2], np.float32(1))
         _check(l.cuda(), size * top, score=score, bias=_on_gpu(bias), groups=groups, top_groups=top)
+
+
+@pytest.mark.parametrize("score", SCORES)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E,groups", [(8, 4), (12, 4), (32, 4), (64, 8), (30, 5)])
+def test_group_values_past_the_largest_number(score, dtype, E, groups):
+    """Experts put out of reach by the lowest finite bias, or ahead by the largest: a sum of two is none of fp32's numbers, and
+    still ahead of minus infinity or behind plus infinity."""
+    big = float(np.finfo(np.float32).max)
+    for seed in range(20):
+        g = np.random.default_rng(seed)
+        bias = g.choice([-big, -big, -3e38, 0.0, -np.inf] if seed % 2 else [big, 3e38, 0.0, float("inf"), 0.25], E)
+        l = torch.from_numpy(g.normal(size=(6, E)).astype(np.float32))
+        l[1] = 0.5
+        l[2, torch.from_numpy(g.random(E) < 0.3)] = -float("inf")
+        k, top, b = int(g.integers(1, E // groups + 1)), int(g.integers(1, groups)), _on_gpu(bias)
+        # a group of plus and minus infinity is worth a NaN, which spoils its token
+        two = np.sort(np.where(np.isneginf(l.numpy()), -np.inf, bias).reshape(6, groups, -1), 2)[:, :, -2:]
+        spoilt = (np.isposinf(two[:, :, 1]) & np.isneginf(two[:, :, 0])).any(1)
+        l = l.to(dtype).cuda()
+        _check(l[torch.from_numpy(~spoilt).cuda()].contiguous(), k, score=score, bias=b, groups=groups, top_groups=top)
+        w = mx.moe_route(l, k, score=SCORES.index(score), bias=b, groups=groups, top_groups=top)[1]
+        assert torch.equal(torch.isnan(w).all(1).cpu(), torch.from_numpy(spoilt))

@@ -176,3 +176,19 @@ def test_random_doubts(lib, part):
     for seed in range(part * 40, part * 40 + 40):
         l, k, score, bias, groups, top = _random(seed)
         _check(lib, l, k, score, bias, groups, top)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("size", [2, 3, 4, 8])
+def test_group_values_past_the_largest_number(lib, score, size):
+    """Experts put out of reach by the lowest finite bias, or ahead by the largest: a sum of two is none of fp32's numbers, and
+    still ahead of minus infinity or behind plus infinity."""
+    big = float(np.finfo(np.float32).max)
+    for seed in range(40):
+        g = np.random.default_rng(seed)
+        groups = 4
+        bias = g.choice([-big, -big, -3e38, 0.0, -np.inf] if seed % 2 else [big, 3e38, 0.0, np.inf, 0.25], groups * size)
+        l = g.normal(size=(3, groups * size))
+        l[1] = 0.5
+        l[2, g.random(groups * size) < 0.3] = -np.inf
+        _check(lib, l, int(g.integers(1, size + 1)), score, bias, groups, int(g.integers(1, groups)))
