@@ -890,6 +890,9 @@ int launch_cfg(void (*k)(A...), size_t smem, int bt, int ctas, bool whole, const
 // 146 / 144 / 166; 1024 over 64 of 2048 x 2048 45.3 / 43.7 / 54.8; 256 over 8 of it 12.2 / 10.7 / 11.5; 800 over 8 19.7 / 13.5 /
 // 12.4; 2041 over 16 of 1424 x 1008 18.2 / 13.8 / 13.9, of 1008 x 1424 16.7 / 13.8 / 10.9; 1000 over 16 of 5120 x 8192 162 / 123 /
 // 129; 4096 over 16 500 / 288 / 187; 3000 over 64 of 4096 x 2048 111 / 92 / 108; 6000 over 64 183 / 122 / 115.
+//   Groups' sizes are on the device only, so the rule takes their mean, over groups without rows too.  The other way round,
+// 64 / 256: 4096 rows of which one of 64 experts has 4033, of 4096 x 7168 439 / 378, of 2048 x 2048 74 / 67; shared out evenly
+// 305 / 311 of 4096 x 7168.
 struct TokenShape {
   int bt, share;
 };

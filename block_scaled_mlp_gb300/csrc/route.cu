@@ -24,10 +24,11 @@
 //
 // A warp has a token and a lane V neighbouring experts.  What bounds the kernels is a launch's and a few loads' latency
 // and, from some thousand tokens on, instructions: about 20 for each of the k rounds that find the next largest c (eight
-// lanes a token and four tokens a warp take as many, and were slower: 2.8 against 2.0 us for 8 tokens).
-// On a GB300 (back to back in a graph; a launch that does nothing takes 1.5 us): 8 tokens of 64 experts, top 8, 2.3 us, their
-// grouping 2.9, backward 1.9; 16384 tokens 7.6 us, with a bias 10.5, with 8 groups besides 13.4 (256 experts: 29), tokens in
-// doubt 2 to 5 us more; grouping their rows 7.3; backward 4.5 (sigmoid) and 5.6 (softmax).  Their bytes are 2.4 us.
+// lanes a token and four tokens a warp take as many, and the first build of either took 2.8 against 2.0 us for 8 tokens).
+// On a GB300 (back to back in a graph; a launch that does nothing takes 1.5 us): 8 tokens of 64 experts, top 8, 2.4 us, their
+// grouping 3.0, backward 1.9; 16384 tokens 7.7 us (sigmoid) and 8.6 (softmax), with a bias 11.8 and 13.5, with 8 groups besides
+// 13.7 to 16.5 (256 experts: 29 to 36), of which tokens in doubt take 2 to 5; grouping their rows 6.9; backward 4.6 (sigmoid)
+// and 5.7 (softmax).  Their bytes are 2.4 us.
 #include <type_traits>
 
 #include "common.cuh"
@@ -39,7 +40,9 @@ namespace mx {
 namespace {
 
 constexpr uint32_t FULL = 0xFFFFFFFFu;
-constexpr int ROUTE_WARPS = 4;  // eight are as fast, two slower (8.6 against 7.1 us for 16384 tokens)
+// 16384 tokens of 64 experts with two, four and eight: 10.3, 8.6, 9.1 us (softmax), 8.8, 7.7, 7.8 (sigmoid); backward 8.7, 4.6 to
+// 5.7, 4.1 to 4.9.
+constexpr int ROUTE_WARPS = 4;
 
 MX_DEVINL float bf16_value(uint32_t bits) { return __uint_as_float(bits << 16); }
 

@@ -668,7 +668,8 @@ MX_API int mx_fp8_block_quantize_weight(const void* w, int64_t E, int64_t N, int
  *   offs [E] group ends as in mx_ragged_mm (any sizes, rows past the last group
  *        are zeros); NULL: dense, E = 1.
  * A product of two scales has to be in fp32's range (2^-126 to 2^128).
- * Weight gradients contract over tokens and stay in bf16 (mx_ragged_mm).
+ * Weight gradients contract over tokens, of which these operands have no blocks; they
+ * stay in bf16 (mx_ragged_mm).
  * Requirements: N, K multiples of 16; 1 <= E <= 1024; 16-byte aligned a, w
  * and c; M_total may be 0.  err_word as in mx_ragged_mm.
  */
