@@ -16,11 +16,12 @@
 // it among them), those of all groups taken (route_closely), and where 44 bits leave it open too, all in double precision
 // (route_exactly; its fp64 instructions take a warp some 15 us).  Without a bias and groups the logits themselves are the order and there is nothing to bound.
 //
-// Bounds of fp32 scores.  Sigmoid: expf is off by 2^-23 of itself, which moves s by 2^-23 s (1 - s), 1 + t and the
-// reciprocal by 2^-24 s each: 2^-23 s (2 - s) together.  Softmax: l - max is rounded by 2^-24 |l - max| besides, at most
-// 2^-24 (-ln s) of s, and a sum of E terms, with the terms' own errors, is off by (V + 14) 2^-24: that scales all scores
-// of a token alike, so it moves the difference of two by that much of itself.  c is rounded by 2^-24.  Underflow ends at
-// 2^-126.
+// Bounds of fp32 scores.  expf is off by two steps of its last place, as CUDA documents it, 2^-22 of itself at most (over all
+// x from -87 to 88 it is 2.56 2^-24 on a GB300).  Sigmoid: that moves s by 2^-22 s (1 - s), 1 + t and the reciprocal by
+// 2^-24 s each: 2^-23 s (3 - 2 s) together.  Softmax: expf and the product 5 2^-24 of s, and l - max is rounded by 2^-24
+// |l - max|, at most 2^-24 (-ln s) of s; a sum of E terms, with the terms' own errors (4 2^-24, and of the differences 4.5 at
+// most), is off by (V + 14) 2^-24: that scales all scores of a token alike, so it moves the difference of two by that much of
+// itself.  c is rounded by 2^-24.  Underflow ends at 2^-126, and e^-x overflows where s is below 2^-127.
 //
 // A warp has a token and a lane V neighbouring experts.  What bounds the kernels is a launch's and a few loads' latency
 // and, from some thousand tokens on, instructions: about 20 for each of the k rounds that find the next largest c (eight
@@ -528,9 +529,9 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __gri
       key[i] = first + i >= E ? 0 : key_of(p.bias ? c[i] : l[i]);
     }
     if (p.groups > 1) {
-      // a score is off by 2^-23 (sigmoid), or by (V + 22) 2^-24 of the largest there is (softmax), and half a sum of two by no
+      // a score is off by 1.13 2^-23 (sigmoid: s = 3/4), or by (V + 22) 2^-24 of the largest there is (softmax), and half a sum of two by no
       // more; c and that are rounded
-      const float off = (sigmoid ? 0x1.1p-22f : (V + 22) * 0x1p-23f * inv) + 0x1p-22f * warp_max(largest);
+      const float off = (sigmoid ? 0x1.3p-22f : (V + 22) * 0x1p-23f * inv) + 0x1p-22f * warp_max(largest);
       const int size = E / p.groups, step = size / V;
       float value;
       int mine, rank, width = 1;  // width: lanes from one group to the next
@@ -645,18 +646,18 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __gri
     const float b = has ? p.bias[id] : 0.0f, c1 = of_key(mine);
     const float x2 = __shfl_down_sync(FULL, x, 1), s2 = __shfl_down_sync(FULL, s, 1), b2 = __shfl_down_sync(FULL, b, 1);
     const uint32_t next = __shfl_down_sync(FULL, mine, 1);
-    const float u1 = fmaxf(s, 0x1p-126f), own = sigmoid ? 0x1p-23f * u1 * (2.01f - u1) : 0x1.7p-22f * u1 - 0x1p-23f * u1 * __logf(u1);
+    const float u1 = fmaxf(s, 0x1p-126f), own = sigmoid ? 0x1p-22f * u1 * (1.51f - u1) : 0x1.7p-22f * u1 - 0x1p-23f * u1 * __logf(u1);
     const float own2 = __shfl_down_sync(FULL, own, 1);
     // the least of the k may be another than the k-th, and off by more than it
     const float own_most = __uint_as_float(__reduce_max_sync(FULL, has ? __float_as_uint(own) : 0u));
     if (lane < k - 1) {
-      const float c2 = of_key(next), rounding = 0x1.01p-24f * (fabsf(c1) + fabsf(c2));
+      const float c2 = of_key(next), rounding = 0x1.01p-24f * (fabsf(c1) + fabsf(c2)) + 0x1p-125f;
       const bool equal = (x == x2 && b == b2) || (c1 == c2 && isinf(c1));
       const float off = own + own2 + rounding + (sigmoid ? 0.0f : (V + 14) * 0x1p-24f * fabsf(s - s2));
       ordered = equal || c1 - c2 > off || c1 - c2 == INFINITY;  // (off is infinite with either)
     } else if (lane == k - 1 && behind) {  // against any that was not chosen: a score of the largest there is
       const float c2 = of_key(behind);
-      border = own_most + (sigmoid ? 0x1.1p-23f : (V + 22) * 0x1p-24f * inv) + 0x1p-22f * fabsf(c1) + 0x1p-23f * fabsf(c2) + 0x1p-125f;
+      border = own_most + (sigmoid ? 0x1.3p-23f : (V + 22) * 0x1p-24f * inv) + 0x1p-22f * fabsf(c1) + 0x1p-23f * fabsf(c2) + 0x1p-125f;
       sure = c1 - c2 > border || c1 - c2 == INFINITY || (c1 == c2 && isinf(c1));  // else border is finite
     }
   }

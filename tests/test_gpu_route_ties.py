@@ -168,3 +168,29 @@ def test_group_values_past_the_largest_number(score, dtype, E, groups):
         _check(l[torch.from_numpy(~spoilt).cuda()].contiguous(), k, score=score, bias=b, groups=groups, top_groups=top)
         w = mx.moe_route(l, k, score=SCORES.index(score), bias=b, groups=groups, top_groups=top)[1]
         assert torch.equal(torch.isnan(w).all(1).cpu(), torch.from_numpy(spoilt))
+
+
+@pytest.mark.parametrize("binade", [3, 6, 10])
+def test_scores_as_far_off_as_they_are(binade):
+    """Of two experts, one whose fp32 score is too large by as much as there is among four million logits and one whose score
+    is as much too small, with biases that leave the second a little more: fp32 puts the first ahead."""
+    g = torch.Generator().manual_seed(binade)
+    x = (-np.log(2) * binade - torch.rand(1 << 22, generator=g) * 0.3).cuda()
+    got = mx.moe_route(x[:, None].contiguous(), 1, score=SCORES.index("sigmoid"), renorm=False)[1][:, 0].double()
+    exact = 1 / (1 + torch.exp(-x.double()))
+    off = (got - exact) / exact
+    low, high = torch.topk(-off, 100).indices, torch.topk(off, 100).indices
+    xl, el = x[low].cpu().numpy(), exact[low].cpu().numpy()
+    xh, eh = x[high].cpu().numpy(), exact[high].cpu().numpy()
+    bl, bh = (-el).astype(np.float32), (-eh).astype(np.float32)
+    step = np.abs(np.spacing(bl)).max().astype(np.float64)
+    for i in range(100):
+        to_go = eh[i] + bh[i].astype(np.float64) - (el + bl.astype(np.float64))
+        j = np.argmax(to_go % step)
+        b = np.float32(bl[j].astype(np.float64) + np.ceil(to_go[j] / step) * step)
+        for flip in (False, True):
+            l, bias = [xh[i], xl[j]], [bh[i], b]
+            if flip:
+                l.reverse(), bias.reverse()
+            for k in (1, 2):
+                _check(torch.tensor([l + [-50.0]]).cuda(), k, score="sigmoid", bias=_on_gpu(bias + [-9.0]))
